@@ -299,10 +299,9 @@ def _plain_append(s):
     T, dev = s["k_new"].shape[1], table.device
     slots = torch.arange(table.shape[0], device=dev)
     old, new = lengths.long(), (lengths + counts).long()
-    # A last page that several slots hold is copied for all who write to it but the last holder.
+    # A last page that several slots hold is copied for each that writes to it.
     last = torch.where((old % PAGE > 0) & (counts > 0), table[slots, old // PAGE], -1).long()
-    before = ((last[:, None] == last[None, :]) & (slots[None, :] < slots[:, None])).sum(1)
-    copied = (last >= 0) & (refs[last.clamp(min=0)] - before > 1)
+    copied = (last >= 0) & (refs[last.clamp(min=0)] > 1)
     first = torch.where(copied, old // PAGE, (old + PAGE - 1) // PAGE)
     need = (new + PAGE - 1) // PAGE - first
     start = need.cumsum(0) - need
@@ -430,7 +429,7 @@ def work(case):
     counts = _counts(case)
     if case["op"] == "append":
         return dict(bytes=2 * sum(counts) * token + 8 * sum(held), flops=0)
-    shared = sum(n % PAGE for n in lengths)  # rows of shared last pages that are copied
+    shared = 2 * sum(n % PAGE for n in lengths)  # rows of shared last pages that are copied
     return dict(bytes=2 * (2 * sum(counts) + shared) * token + 24 * sum(held), flops=0)
 
 
