@@ -57,12 +57,13 @@ typedef enum {
   GCA_ERR_WORKSPACE = 3,    /* ws is NULL, misaligned or smaller than required          */
   GCA_ERR_CUDA = 4,         /* a CUDA runtime call failed; see gca_last_error_detail()  */
   GCA_ERR_DEVICE_INDEX = 5, /* (gca_check_error) a kernel met idx outside [-1, nC)      */
-  GCA_ERR_TIMEOUT = 6       /* (gca_check_error) a bounded wait inside a kernel ran out  */
+  GCA_ERR_TIMEOUT = 6,      /* (gca_check_error) a bounded wait inside a kernel ran out  */
+  GCA_ERR_CACHE_FULL = 7    /* (gca_check_error) a cache had no room for an append       */
 } gca_status;
 
 typedef enum { GCA_F32 = 0, GCA_BF16 = 1 } gca_dtype;
 
-enum { GCA_CHUNK = 64, GCA_MAX_TOPK = 16 };
+enum { GCA_CHUNK = 64, GCA_MAX_TOPK = 16, GCA_MAX_DRAFT = 256, GCA_MAX_CACHE_ENTRIES = 1024 };
 
 /* Human-readable name of a status. */
 GCA_API const char* gca_status_string(gca_status s);
@@ -407,10 +408,155 @@ GCA_API gca_status gca_scores_backward(const void* q_lmk, int64_t q_row_stride, 
                                void* ws, size_t ws_bytes, gca_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * gca_rotary - rotary positions for queries and keys, and (backward != 0) their gradient.
+ *
+ * For the window attention, or the cached attention below, beside the retrieval.  Pair i of
+ * a head is elements (i, i + rot/2), or (2i, 2i+1) with interleaved != 0, for i < rot/2; at
+ * position p it turns by p w_i:
+ *     y1 = gain (x1 cos - x2 sin),   y2 = gain (x1 sin + x2 cos)
+ * and by -p w_i with backward != 0 (inputs are then the gradients of y, outputs those of
+ * x).  Elements rot .. dh-1 are copied.  Angles keep their precision at any position.
+ *
+ *   q, k    [B][L][H][dh] and [B][L][Hkv][dh] with free strides (views of a fused
+ *           projection; 0 repeats); k may be NULL (Hkv = 0).  dtype of all four tensors.
+ *   q_out, k_out  like them; may be the inputs themselves (same pointer and strides), but
+ *           must not overlap them otherwise.  Their strides may not make elements overlap.
+ *   dh 2..256, rot even in 2..dh.
+ *   freq    [rot/2] device, w_i in units of 2^-64 turns per position, as written by
+ *           gca_rotary_frequencies.
+ *   positions [B][L] int32 device (>= 0 or not), position_batch_stride elements between
+ *           sequences (0: shared by all); NULL: token l is at position l.
+ *
+ * gca_rotary_frequencies writes freq on the HOST: w_i = base^(-2i/rot), then with
+ *   GCA_ROTARY_LINEAR  w_i / factor;
+ *   GCA_ROTARY_NTK     base factor^(rot/(rot-2)) in the place of base (rot > 2);
+ *   GCA_ROTARY_PARTS   (1 - c_i) w_i / factor + c_i w_i, where
+ *                      c_i = clamp((context w_i / 2 pi - low) / (high - low), 0, 1): pairs that
+ *                      turn more than `high` times in `context` tokens keep their speed, those
+ *                      below `low` turns are stretched.
+ * ------------------------------------------------------------------------------- */
+typedef struct {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride; /* elements; unit stride inside a head */
+} gca_heads;
+typedef enum { GCA_ROTARY_PLAIN = 0, GCA_ROTARY_LINEAR = 1, GCA_ROTARY_NTK = 2, GCA_ROTARY_PARTS = 3 } gca_rotary_scaling;
+GCA_API gca_status gca_rotary_frequencies(int rot, double base, gca_rotary_scaling scaling, double factor,
+                                  double context, double low, double high, uint64_t* freq);
+GCA_API gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_heads* q_out, const gca_heads* k_out,
+                      gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot, int interleaved,
+                      int backward, const uint64_t* freq, const int32_t* positions,
+                      int64_t position_batch_stride, float gain, gca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * A paged K/V cache.
+ *
+ * Pages are the method's chunks: 64 tokens of every key head, in the layout of the K/V
+ * store that gca_forward reads (kv_batch_stride = 0, nC = pages, idx = page numbers from
+ * gca_cache_lookup, where heads = H and dh is 32 or 64).  Slot s holds lengths[s] tokens;
+ * tokens 64p .. 64p+63 lie in page table[s][p], -1 where no page is held (behind the length,
+ * or given back by gca_cache_trim).  refs[page] counts the slots that hold a page; 0 is free.
+ * All arrays are device memory of the caller; pools 16-byte aligned, a token's row
+ * (heads * dh elements) a multiple of 16 bytes.
+ *
+ * What the operations have in common: they run on the device without a copy to the host, so
+ * a captured graph follows the cache's state; they change the state in the order of the
+ * stream, and two of them on one cache must not overlap.  `slot_ids` [n] (n <= 1024) names the
+ * slots of the call's entries, NULL: entry i is slot i.  An entry whose slot, count or page
+ * is out of range, or whose slot an earlier entry names, is left out and flagged in the
+ * error word (GCA_ERR_DEVICE_INDEX).  Free pages are taken lowest number first, in the order
+ * of the entries: equal states and calls give equal states.
+ *   ws      >= gca_forward_workspace_size() bytes (error word only).
+ *   scratch >= the matching *_scratch_size() bytes, 256-byte aligned, any contents; one for
+ *           each call that can overlap another.
+ * ------------------------------------------------------------------------------- */
+typedef struct {
+  void* k_pages; void* v_pages; /* [pages][64][heads][dh] */
+  gca_dtype dtype; int heads, dh, pages;
+  int32_t* table; int slots, width; /* [slots][width] */
+  int32_t* lengths;                 /* [slots] */
+  int32_t* refs;                    /* [pages]; may be NULL for attention and lookup */
+} gca_cache;
+
+/* gca_cache_append - counts[i] new tokens for each entry's slot, behind its last.
+ *   k_new, v_new [n][T][heads][dh] (16-byte aligned, head stride dh, other strides multiples
+ *           of 16 bytes); counts [n] int32 in 0..T; path [n][T] int32 (NULL: row t): the
+ *           row of k_new that token t of the entry comes from, e.g. the accepted nodes of a
+ *           draft, in order.  A row outside 0..T-1 is flagged and leaves its token unwritten.
+ * A last page that other slots hold too is first copied to a fresh page (its rows in use;
+ * the others are left as they were) and given back.  Entries are served in order: from the
+ * first that the free pages do not reach, none is, and their slots stay as they were; one
+ * that the table has no room for is left out.  Both are flagged (GCA_ERR_CACHE_FULL). */
+GCA_API size_t gca_cache_append_scratch_size(int n, int T);
+GCA_API gca_status gca_cache_append(const gca_cache* cache, const gca_heads* k_new, const gca_heads* v_new, int n, int T,
+                            const int32_t* slot_ids, const int32_t* counts, const int32_t* path, void* ws,
+                            size_t ws_bytes, void* scratch, size_t scratch_bytes, gca_stream_t stream);
+/* gca_cache_fork - slot dst[i] becomes a copy of slot src[i] that shares its pages.  Left
+ * out and flagged: a destination that is not empty, or that an earlier pair names; a source
+ * that is a destination of the call. */
+GCA_API gca_status gca_cache_fork(const gca_cache* cache, int n, const int32_t* src, const int32_t* dst, void* ws,
+                          size_t ws_bytes, gca_stream_t stream);
+/* gca_cache_trim - keeps the tokens begin[i] .. end[i]-1 of each entry's slot and gives back
+ * the pages that lie wholly outside: end below the length takes the last tokens back, begin
+ * above 0 lets go of those that a window has passed (the length stays; their table entries
+ * become -1).  NULL begin: 0; NULL end: the length; both are clamped to the tokens there
+ * are.  release != 0 frees the slots (begin and end are not used). */
+GCA_API gca_status gca_cache_trim(const gca_cache* cache, int n, const int32_t* slot_ids, const int32_t* begin,
+                          const int32_t* end, int release, void* ws, size_t ws_bytes, gca_stream_t stream);
+/* gca_cache_compact - moves pages so that those in use are numbers 0 .. live-1, with their
+ * counts, and renames them in every table.  With live pages in use, the k-th page in use at
+ * or above `live` moves to the k-th free number below it; the rest stay.  live [1] int32
+ * device out.  Table entries that name a free page become -1 (flagged). */
+GCA_API size_t gca_cache_compact_scratch_size(int pages);
+GCA_API gca_status gca_cache_compact(const gca_cache* cache, int32_t* live, void* ws, size_t ws_bytes, void* scratch,
+                             size_t scratch_bytes, gca_stream_t stream);
+/* gca_cache_lookup - the page of chunk idx[i][e] of each entry's slot: pages_out [n][per].
+ * -1 stays -1; outside [-1, width) or in a bad slot is flagged and gives -1. */
+GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, const int32_t* slot_ids, const int32_t* idx,
+                            int32_t* pages_out, void* ws, size_t ws_bytes, gca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * gca_tree_attention - attention of newly drafted tokens over a paged cache.
+ *
+ * The decoding form of the window attention: T new tokens of each sequence (one token, a
+ * run of tokens, or a tree of drafted candidates) attend with one softmax to the cache's
+ * tokens and to each other.  Query head h reads key head h / (H / heads).
+ *     s = scale <q, k>,   o = sum softmax(s) v,   lse = log sum exp(s)
+ * over the cache's tokens j < lengths[b] of slot b, and the draft's tokens u whose bit is set
+ * in token t's mask; with window > 0 only those with position > position_t - window, where
+ * token j of the cache is at position j.  A token that sees nothing, and padding, gets o = 0
+ * and lse = -inf.  A page number outside [0, pages) is left out (flagged unless it is -1).
+ *
+ *   q [B][T][H][dh], k_new, v_new [B][T][heads][dh]: free strides, 16-byte aligned, strides
+ *           multiples of 16 bytes.  B <= cache->slots: sequence b is slot b.
+ *   mask    [B][T][ceil(T/64)] uint64: bit u % 64 of word u / 64 of row t: t sees u.  NULL: t
+ *           sees the tokens u <= t.  Tokens that no row sees are not used in any way.
+ *   positions [B][T] int32: -1 for padding (seen by none and seeing none), else the token's
+ *           position, taken as lengths[b] where it is lower.  NULL: lengths[b] + t.
+ *   window  0 (everything) or more.   scale > 0.   T 1..256.   dh 32, 64 or 128.
+ *   o       [B][T][H][dh] contiguous, 16-byte aligned.   lse [B][T][H] float32.
+ *   ws      >= gca_forward_workspace_size() bytes (error word only).
+ *   scratch >= gca_tree_attention_scratch_size() bytes, 256-byte aligned, any contents.
+ *
+ * gca_tree_plan - mask and positions of a tree, once for all layers of a step.
+ *   parents [B][T] int32: the earlier token of the draft that token t follows, -1 for the
+ *           cache's last token, -2 for padding.  Any other value is flagged and read as -2;
+ *           what follows padding is padding.  lengths [B].
+ *   mask, positions: as above (a token sees itself and its ancestors; its position is
+ *           lengths[b] plus the number of its ancestors).
+ * ------------------------------------------------------------------------------- */
+GCA_API gca_status gca_tree_plan(const int32_t* parents, const int32_t* lengths, int B, int T, uint64_t* mask,
+                         int32_t* positions, void* ws, size_t ws_bytes, gca_stream_t stream);
+GCA_API size_t gca_tree_attention_scratch_size(int B, int T, int H, int heads, int dh, gca_dtype dtype);
+GCA_API gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_new, const gca_heads* v_new,
+                              const gca_cache* cache, int B, int T, int H, const uint64_t* mask,
+                              const int32_t* positions, int window, float scale, void* o, float* lse, void* ws,
+                              size_t ws_bytes, void* scratch, size_t scratch_bytes, gca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * gca_check_error - synchronise `stream`, read and clear the device error word of `ws`.
  * Returns GCA_OK, GCA_ERR_TIMEOUT (a tensor-core completion wait gave up instead of
  * hanging; the results of that call are not valid), GCA_ERR_DEVICE_INDEX (with the
- * offending index in *bad_value when bad_value != NULL) or GCA_ERR_CUDA.
+ * offending index in *bad_value when bad_value != NULL), GCA_ERR_CACHE_FULL or GCA_ERR_CUDA.
  * ------------------------------------------------------------------------------- */
 GCA_API gca_status gca_check_error(void* ws, gca_stream_t stream, int* bad_value);
 

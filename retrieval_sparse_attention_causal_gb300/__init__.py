@@ -18,11 +18,13 @@ from . import synth  # noqa: F401  (seeded input generators)
 
 CHUNK = 64
 MAX_TOPK = 16
+MAX_DRAFT = 256           # tokens of a draft (tree_attention)
+MAX_CACHE_ENTRIES = 1024  # sequences of one page operation
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libgca.so")
 
 (GCA_OK, GCA_ERR_INVALID_ARG, GCA_ERR_UNSUPPORTED, GCA_ERR_WORKSPACE, GCA_ERR_CUDA, GCA_ERR_DEVICE_INDEX,
- GCA_ERR_TIMEOUT) = range(7)
+ GCA_ERR_TIMEOUT, GCA_ERR_CACHE_FULL) = range(8)
 GCA_F32, GCA_BF16 = 0, 1
 
 
@@ -42,6 +44,20 @@ class EncoderWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ENCODER_WEIGHTS]
 
 
+class Heads(ctypes.Structure):
+    """gca_heads: a [B, L, heads, dh] tensor with its batch, token and head strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    """gca_cache: pools, table, lengths and reference counts of a paged K/V cache."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("heads", ctypes.c_int), ("dh", ctypes.c_int), ("pages", ctypes.c_int), ("table", ctypes.c_void_p),
+                ("slots", ctypes.c_int), ("width", ctypes.c_int), ("lengths", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -49,6 +65,7 @@ def _load():
             "(python retrieval_sparse_attention_causal_gb300/build.py)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, I64, U64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+    HP, CP, F = ctypes.POINTER(Heads), ctypes.POINTER(Cache), ctypes.c_float
     sig = {
         "gca_status_string": (ctypes.c_char_p, [I]),
         "gca_last_error_detail": (ctypes.c_char_p, []),
@@ -76,6 +93,19 @@ def _load():
         "gca_backward": (I, [P, P, P, I, I, I, I, I, I, P, P, I, I, P, P, P, P, P, P, I, P, SZ, P]),
         "gca_scores_backward_workspace_size": (SZ, [I, I, I, I]),
         "gca_scores_backward": (I, [P, I64, I64, P, I64, I, I, I, I, I, P, P, I, P, I, I64, I64, I, P, P, SZ, P]),
+        "gca_rotary_frequencies": (I, [I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                       ctypes.c_double, ctypes.POINTER(U64)]),
+        "gca_rotary": (I, [HP, HP, HP, HP, I, I, I, I, I, I, I, I, I, P, P, I64, F, P]),
+        "gca_cache_append_scratch_size": (SZ, [I, I]),
+        "gca_cache_append": (I, [CP, HP, HP, I, I, P, P, P, P, SZ, P, SZ, P]),
+        "gca_cache_fork": (I, [CP, I, P, P, P, SZ, P]),
+        "gca_cache_trim": (I, [CP, I, P, P, P, I, P, SZ, P]),
+        "gca_cache_compact_scratch_size": (SZ, [I]),
+        "gca_cache_compact": (I, [CP, P, P, SZ, P, SZ, P]),
+        "gca_cache_lookup": (I, [CP, I, I, P, P, P, P, SZ, P]),
+        "gca_tree_plan": (I, [P, P, I, I, P, P, P, SZ, P]),
+        "gca_tree_attention_scratch_size": (SZ, [I, I, I, I, I, I]),
+        "gca_tree_attention": (I, [HP, HP, HP, CP, I, I, I, P, P, I, F, P, P, P, SZ, P, SZ, P]),
         "gca_check_error": (I, [P, P, ctypes.POINTER(I)]),
         "gca_launch_count": (U64, []),
         "gca_profile_begin": (I, []),
@@ -104,6 +134,10 @@ EXPORTS = (
     "gca_backward_workspace_size", "gca_backward",
     "gca_scores_backward_workspace_size", "gca_scores_backward", "gca_check_error", "gca_launch_count",
     "gca_profile_begin", "gca_profile_end", "gca_profile_row",
+    "gca_rotary_frequencies", "gca_rotary",
+    "gca_cache_append_scratch_size", "gca_cache_append", "gca_cache_fork", "gca_cache_trim",
+    "gca_cache_compact_scratch_size", "gca_cache_compact", "gca_cache_lookup",
+    "gca_tree_plan", "gca_tree_attention_scratch_size", "gca_tree_attention",
 )
 
 
@@ -491,6 +525,11 @@ def scores_backward(q_lmk, k_lmk, idx, dscores, ws: Workspace = None, dq_out=Non
                                    _dtype(dq_out), dq_out.stride(1), dq_out.stride(0), int(bool(accumulate)),
                                    _ptr(dk_lmk), _ptr(buf), buf.numel(), _stream()))
     return dq_out, dk_lmk
+
+
+# --------------------------------------------------------------------------- rotary, paged cache, drafted tokens
+from .decoding import (PagedCache, cache_workspace, rotary, rotary_backward, rotary_frequencies,  # noqa: E402,F401
+                       tree_attention, tree_plan)
 
 
 # --------------------------------------------------------------------------- instrumentation

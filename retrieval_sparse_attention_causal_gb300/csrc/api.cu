@@ -1,12 +1,15 @@
 // C ABI entry points of the GCA library: argument validation, workspace carving, kernel
 // launches, the device error word and launch instrumentation.  The operations
 // themselves are documented in include/gca.h.
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/gca.h"
@@ -133,6 +136,7 @@ extern "C" const char* gca_status_string(gca_status s) {
     case GCA_ERR_CUDA: return "GCA_ERR_CUDA";
     case GCA_ERR_DEVICE_INDEX: return "GCA_ERR_DEVICE_INDEX";
     case GCA_ERR_TIMEOUT: return "GCA_ERR_TIMEOUT";
+    case GCA_ERR_CACHE_FULL: return "GCA_ERR_CACHE_FULL";
   }
   return "unknown gca_status";
 }
@@ -577,6 +581,298 @@ extern "C" gca_status gca_scores_backward(const void* q_lmk, int64_t q_row_strid
   return GCA_OK;
 }
 
+// ==================================================================== rotary positions
+extern "C" gca_status gca_rotary_frequencies(int rot, double base, gca_rotary_scaling scaling, double factor,
+                                             double context, double low, double high, uint64_t* freq) {
+  if (rot < 2 || rot > 256 || rot % 2) return fail(GCA_ERR_INVALID_ARG, "rot must be even in 2..256 (got %d)", rot);
+  if (!freq) return fail(GCA_ERR_INVALID_ARG, "freq is NULL");
+  if (!(base >= 1.0) || !std::isfinite(base)) return fail(GCA_ERR_INVALID_ARG, "base must be finite and >= 1");
+  if (scaling < GCA_ROTARY_PLAIN || scaling > GCA_ROTARY_PARTS) return fail(GCA_ERR_INVALID_ARG, "unknown scaling %d", (int)scaling);
+  if (scaling != GCA_ROTARY_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(GCA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  if (scaling == GCA_ROTARY_PARTS && (!(context >= 1.0) || !std::isfinite(context) || !(high > low) || !std::isfinite(high - low)))
+    return fail(GCA_ERR_INVALID_ARG, "parts needs a finite context >= 1 and high > low");
+  const double two_pi = 6.283185307179586476925;
+  double bs = base;
+  if (scaling == GCA_ROTARY_NTK && rot > 2) bs *= std::pow(factor, (double)rot / (rot - 2));
+  for (int i = 0; i < rot / 2; ++i) {
+    double w = std::pow(bs, -2.0 * i / rot);
+    if (scaling == GCA_ROTARY_LINEAR) w /= factor;
+    if (scaling == GCA_ROTARY_PARTS) {
+      const double c = std::min(1.0, std::max(0.0, (context * w / two_pi - low) / (high - low)));
+      w = w * c + w / factor * (1.0 - c);
+    }
+    freq[i] = (uint64_t)std::llrint(w / two_pi * 18446744073709551616.0);  // w <= 1: below 2^62
+  }
+  return GCA_OK;
+}
+
+// A written tensor's elements must not share addresses: with the axes in the order of their
+// strides, each must step over everything the ones before it span.
+static bool strides_overlap(const gca_heads& t, int64_t B, int64_t L, int64_t H, int64_t dh) {
+  std::pair<int64_t, int64_t> ax[3] = {{t.batch_stride, B}, {t.token_stride, L}, {t.head_stride, H}};
+  std::sort(ax, ax + 3);
+  int64_t span = dh;
+  for (auto& x : ax) {
+    if (x.second == 1) continue;
+    if (x.first < span) return true;
+    span += x.first * (x.second - 1);
+  }
+  return false;
+}
+
+extern "C" gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_heads* q_out,
+                                 const gca_heads* k_out, gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot,
+                                 int interleaved, int backward, const uint64_t* freq, const int32_t* positions,
+                                 int64_t position_batch_stride, float gain, gca_stream_t stream) {
+  if (dtype != GCA_F32 && dtype != GCA_BF16) return fail(GCA_ERR_INVALID_ARG, "dtype must be GCA_F32 or GCA_BF16");
+  if (!q || !q_out || !q->data || !q_out->data) return fail(GCA_ERR_INVALID_ARG, "q or q_out is NULL");
+  if (!k != !k_out || (k && (!k->data || !k_out->data))) return fail(GCA_ERR_INVALID_ARG, "k and k_out must both be given");
+  if (B < 1 || L < 1 || H < 1 || Hkv < (k ? 1 : 0) || (!k && Hkv != 0))
+    return fail(GCA_ERR_INVALID_ARG, "B, L, H must be >= 1, and Hkv >= 1 with k, 0 without (got %d, %d, %d, %d)", B, L, H, Hkv);
+  if (H > 65535 || Hkv > 65535) return fail(GCA_ERR_INVALID_ARG, "H and Hkv must be <= 65535");
+  if ((int64_t)B * L > INT32_MAX) return fail(GCA_ERR_INVALID_ARG, "B * L must be below 2^31");
+  if (dh < 2 || dh > 256) return fail(GCA_ERR_UNSUPPORTED, "head dim must be in 2..256 (got %d)", dh);
+  if (rot < 2 || rot > dh || rot % 2) return fail(GCA_ERR_INVALID_ARG, "rot must be even in 2..dh (got %d)", rot);
+  if (!freq || (reinterpret_cast<uintptr_t>(freq) & 7)) return fail(GCA_ERR_INVALID_ARG, "freq must be 8-byte aligned and not NULL");
+  if (position_batch_stride < 0) return fail(GCA_ERR_INVALID_ARG, "position_batch_stride must be >= 0");
+  const int esize = dtype == GCA_BF16 ? 2 : 4;
+  for (const gca_heads* t : {q, k, q_out, k_out}) {
+    if (!t) continue;
+    if (reinterpret_cast<uintptr_t>(t->data) % esize) return fail(GCA_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+    if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0) return fail(GCA_ERR_INVALID_ARG, "strides must be >= 0");
+  }
+  if (strides_overlap(*q_out, B, L, H, dh) || (k && strides_overlap(*k_out, B, L, Hkv, dh)))
+    return fail(GCA_ERR_INVALID_ARG, "output strides make elements overlap");
+  auto same = [](const gca_heads* a, const gca_heads* b) {
+    return a->data == b->data && a->batch_stride == b->batch_stride && a->token_stride == b->token_stride &&
+           a->head_stride == b->head_stride;
+  };
+  auto side = [](const gca_heads* i, const gca_heads* o) {
+    return RotarySide{i->data, i->batch_stride, i->token_stride, i->head_stride,
+                      o->data, o->batch_stride, o->token_stride, o->head_stride};
+  };
+  RotaryArgs a{};
+  a.q = side(q, q_out);
+  if (k) a.k = side(k, k_out);
+  a.bf16 = dtype == GCA_BF16; a.B = B; a.L = L; a.H = H; a.Hkv = Hkv; a.dh = dh; a.rot = rot;
+  a.paired = interleaved ? 1 : 0;
+  a.tail = same(q, q_out) && (!k || same(k, k_out)) ? 0 : dh - rot;
+  a.freq = freq; a.pos = positions; a.pos_bs = position_batch_stride;
+  a.gain = gain; a.sgain = backward ? -gain : gain;
+  cudaError_t e = launch_rotary(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_rotary launch");
+  return GCA_OK;
+}
+
+// ==================================================================== paged cache
+namespace {
+gca_status check_cache(const gca_cache* c, bool need_refs) {
+  if (!c) return fail(GCA_ERR_INVALID_ARG, "cache is NULL");
+  if (c->dtype != GCA_F32 && c->dtype != GCA_BF16) return fail(GCA_ERR_INVALID_ARG, "dtype must be GCA_F32 or GCA_BF16");
+  if (!c->k_pages || !c->v_pages || !c->table || !c->lengths || (need_refs && !c->refs))
+    return fail(GCA_ERR_INVALID_ARG, "a cache pointer is NULL");
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return fail(GCA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
+  if (c->heads < 1 || c->heads > 65535 || c->dh < 1 || c->dh > 65535 || c->pages < 1 || c->slots < 1 || c->width < 1)
+    return fail(GCA_ERR_INVALID_ARG, "heads, dh, pages, slots and width must be >= 1 (heads, dh <= 65535)");
+  if ((int64_t)c->width * 64 > INT32_MAX) return fail(GCA_ERR_INVALID_ARG, "table too wide: 64 * width must be below 2^31");
+  if ((int64_t)c->heads * c->dh * (c->dtype == GCA_BF16 ? 2 : 4) % 16)
+    return fail(GCA_ERR_INVALID_ARG, "a token's row (heads * dh elements) must be a multiple of 16 bytes");
+  return GCA_OK;
+}
+gca_status check_entries(const gca_cache* c, int n, bool listed) {
+  if (n < 1 || n > GCA_MAX_CACHE_ENTRIES) return fail(GCA_ERR_INVALID_ARG, "n must be in 1..%d (got %d)", GCA_MAX_CACHE_ENTRIES, n);
+  if (!listed && n > c->slots) return fail(GCA_ERR_INVALID_ARG, "n must be at most the number of slots where no slots are named");
+  return GCA_OK;
+}
+CacheArgs cache_args(const gca_cache* c, int n, const int32_t* slot, void* ws) {
+  CacheArgs a{};
+  a.kp = static_cast<unsigned char*>(c->k_pages);
+  a.vp = static_cast<unsigned char*>(c->v_pages);
+  a.pages = c->pages;
+  a.token_bytes = (int64_t)c->heads * c->dh * (c->dtype == GCA_BF16 ? 2 : 4);
+  a.table = c->table; a.slots = c->slots; a.width = c->width; a.lengths = c->lengths; a.refs = c->refs;
+  a.n = n; a.slot = slot;
+  a.err = reinterpret_cast<ErrWord*>(ws);
+  return a;
+}
+gca_status check_scratch(const void* p, size_t have, size_t need) {
+  if (p == nullptr) return fail(GCA_ERR_WORKSPACE, "scratch pointer is NULL");
+  if (reinterpret_cast<uintptr_t>(p) & 255) return fail(GCA_ERR_WORKSPACE, "scratch is not 256-byte aligned");
+  if (have < need) return fail(GCA_ERR_WORKSPACE, "scratch has %zu bytes, needs %zu", have, need);
+  return GCA_OK;
+}
+// A tensor whose rows are read in 16-byte units.
+gca_status check_vectors(const gca_heads* t, int esize, const char* what) {
+  if (!t || !t->data) return fail(GCA_ERR_INVALID_ARG, "%s is NULL", what);
+  if (!aligned16(t->data)) return fail(GCA_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+  for (int64_t s : {t->batch_stride, t->token_stride, t->head_stride})
+    if (s < 0 || s * esize % 16) return fail(GCA_ERR_INVALID_ARG, "%s: strides must be >= 0 and multiples of 16 bytes", what);
+  return GCA_OK;
+}
+}  // namespace
+
+extern "C" size_t gca_cache_append_scratch_size(int n, int T) {
+  if (n < 1 || T < 1) return 256;
+  return align256((size_t)n * kAppendRec * 4) + align256((size_t)n * ((size_t)T / 64 + 2) * 4);
+}
+
+extern "C" gca_status gca_cache_append(const gca_cache* cache, const gca_heads* k_new, const gca_heads* v_new, int n,
+                                       int T, const int32_t* slot_ids, const int32_t* counts, const int32_t* path,
+                                       void* ws, size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                       gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
+  if (T < 1 || T > INT32_MAX / 2) return fail(GCA_ERR_INVALID_ARG, "T must be in 1..2^30");
+  if (!counts) return fail(GCA_ERR_INVALID_ARG, "counts is NULL");
+  const int esize = cache->dtype == GCA_BF16 ? 2 : 4;
+  if ((st = check_vectors(k_new, esize, "k_new")) != GCA_OK) return st;
+  if ((st = check_vectors(v_new, esize, "v_new")) != GCA_OK) return st;
+  if (cache->heads > 1 && (k_new->head_stride != cache->dh || v_new->head_stride != cache->dh))
+    return fail(GCA_ERR_INVALID_ARG, "the heads of a new token must be contiguous (head stride dh)");
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  if ((st = check_scratch(scratch, scratch_bytes, gca_cache_append_scratch_size(n, T))) != GCA_OK) return st;
+  AppendArgs a{};
+  a.c = cache_args(cache, n, slot_ids, ws);
+  a.kn = static_cast<const unsigned char*>(k_new->data);
+  a.kn_bs = k_new->batch_stride * esize; a.kn_ts = k_new->token_stride * esize;
+  a.vn = static_cast<const unsigned char*>(v_new->data);
+  a.vn_bs = v_new->batch_stride * esize; a.vn_ts = v_new->token_stride * esize;
+  a.counts = counts; a.path = path; a.T = T;
+  a.rec = static_cast<int32_t*>(scratch);
+  a.fresh = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(scratch) + align256((size_t)n * kAppendRec * 4));
+  cudaError_t e = launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_append launch");
+  return GCA_OK;
+}
+
+extern "C" gca_status gca_cache_fork(const gca_cache* cache, int n, const int32_t* src, const int32_t* dst, void* ws,
+                                     size_t ws_bytes, gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if (!src || !dst) return fail(GCA_ERR_INVALID_ARG, "src or dst is NULL");
+  if ((st = check_entries(cache, n, true)) != GCA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  cudaError_t e = launch_cache_fork(cache_args(cache, n, src, ws), dst, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_fork launch");
+  return GCA_OK;
+}
+
+extern "C" gca_status gca_cache_trim(const gca_cache* cache, int n, const int32_t* slot_ids, const int32_t* begin,
+                                     const int32_t* end, int release, void* ws, size_t ws_bytes, gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  cudaError_t e = launch_cache_trim(cache_args(cache, n, slot_ids, ws), begin, end, release ? 1 : 0,
+                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_trim launch");
+  return GCA_OK;
+}
+
+extern "C" size_t gca_cache_compact_scratch_size(int pages) {
+  if (pages < 1) return 256;
+  return align256((kCompactParts + 1) * 4) + 3 * align256((size_t)pages * 4);
+}
+
+extern "C" gca_status gca_cache_compact(const gca_cache* cache, int32_t* live, void* ws, size_t ws_bytes,
+                                        void* scratch, size_t scratch_bytes, gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if (!live) return fail(GCA_ERR_INVALID_ARG, "live is NULL");
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  if ((st = check_scratch(scratch, scratch_bytes, gca_cache_compact_scratch_size(cache->pages))) != GCA_OK) return st;
+  CompactArgs a{};
+  a.c = cache_args(cache, cache->slots, nullptr, ws);
+  a.live = live;
+  unsigned char* p = static_cast<unsigned char*>(scratch);
+  const size_t list = align256((size_t)cache->pages * 4);
+  a.counts = reinterpret_cast<int32_t*>(p); p += align256((kCompactParts + 1) * 4);
+  a.movers = reinterpret_cast<int32_t*>(p); p += list;
+  a.holes = reinterpret_cast<int32_t*>(p); p += list;
+  a.rank = reinterpret_cast<int32_t*>(p);
+  cudaError_t e = launch_cache_compact(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_compact launch");
+  return GCA_OK;
+}
+
+extern "C" gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, const int32_t* slot_ids,
+                                       const int32_t* idx, int32_t* pages_out, void* ws, size_t ws_bytes,
+                                       gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_cache(cache, false)) != GCA_OK) return st;
+  if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
+  if (per < 1) return fail(GCA_ERR_INVALID_ARG, "per must be >= 1");
+  if (!idx || !pages_out) return fail(GCA_ERR_INVALID_ARG, "idx or pages_out is NULL");
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  cudaError_t e = launch_cache_lookup(cache_args(cache, n, slot_ids, ws), idx, per, pages_out,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_lookup launch");
+  return GCA_OK;
+}
+
+// ==================================================================== attention of drafted tokens
+extern "C" gca_status gca_tree_plan(const int32_t* parents, const int32_t* lengths, int B, int T, uint64_t* mask,
+                                    int32_t* positions, void* ws, size_t ws_bytes, gca_stream_t stream) {
+  if (!parents || !lengths || !mask || !positions) return fail(GCA_ERR_INVALID_ARG, "a pointer is NULL");
+  if (B < 1 || B > 65535) return fail(GCA_ERR_INVALID_ARG, "B must be in 1..65535 (got %d)", B);
+  if (T < 1 || T > GCA_MAX_DRAFT) return fail(GCA_ERR_UNSUPPORTED, "T must be in 1..%d (got %d)", GCA_MAX_DRAFT, T);
+  if (reinterpret_cast<uintptr_t>(mask) & 7) return fail(GCA_ERR_INVALID_ARG, "mask must be 8-byte aligned");
+  gca_status st;
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  TreePlanArgs a{parents, lengths, B, T, (T + 63) / 64, mask, positions, reinterpret_cast<ErrWord*>(ws)};
+  cudaError_t e = launch_tree_plan(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_tree_plan launch");
+  return GCA_OK;
+}
+
+extern "C" size_t gca_tree_attention_scratch_size(int B, int T, int H, int heads, int dh, gca_dtype dtype) {
+  if (B < 1 || T < 1 || T > GCA_MAX_DRAFT || heads < 1 || H < heads || H % heads || dh < 1) return 256;
+  return align256(tree_scratch_bytes(B, T, H, heads, dh, dtype == GCA_BF16));
+}
+
+extern "C" gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_new, const gca_heads* v_new,
+                                         const gca_cache* cache, int B, int T, int H, const uint64_t* mask,
+                                         const int32_t* positions, int window, float scale, void* o, float* lse,
+                                         void* ws, size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                         gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_cache(cache, false)) != GCA_OK) return st;
+  const int esize = cache->dtype == GCA_BF16 ? 2 : 4;
+  if ((st = check_vectors(q, esize, "q")) != GCA_OK) return st;
+  if ((st = check_vectors(k_new, esize, "k_new")) != GCA_OK) return st;
+  if ((st = check_vectors(v_new, esize, "v_new")) != GCA_OK) return st;
+  if (B < 1 || B > cache->slots || B > 65535) return fail(GCA_ERR_INVALID_ARG, "B must be in 1..slots, at most 65535 (got %d)", B);
+  if (T < 1 || T > GCA_MAX_DRAFT) return fail(GCA_ERR_UNSUPPORTED, "T must be in 1..%d (got %d)", GCA_MAX_DRAFT, T);
+  if (H < cache->heads || H % cache->heads || H > 65535)
+    return fail(GCA_ERR_INVALID_ARG, "H must be a multiple of the cache's heads (got %d, %d)", H, cache->heads);
+  if (cache->dh != 32 && cache->dh != 64 && cache->dh != 128)
+    return fail(GCA_ERR_UNSUPPORTED, "head dim must be 32, 64 or 128 (got %d)", cache->dh);
+  if (window < 0) return fail(GCA_ERR_INVALID_ARG, "window must be >= 0");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(GCA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (mask && (reinterpret_cast<uintptr_t>(mask) & 7)) return fail(GCA_ERR_INVALID_ARG, "mask must be 8-byte aligned");
+  if (!o || !lse || !aligned16(o)) return fail(GCA_ERR_INVALID_ARG, "o and lse must not be NULL, o 16-byte aligned");
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  if ((st = check_scratch(scratch, scratch_bytes, gca_tree_attention_scratch_size(B, T, H, cache->heads, cache->dh, cache->dtype))) != GCA_OK)
+    return st;
+  TreeArgs a{};
+  a.q = q->data; a.q_bs = q->batch_stride; a.q_ts = q->token_stride; a.q_hs = q->head_stride;
+  a.kn = k_new->data; a.kn_bs = k_new->batch_stride; a.kn_ts = k_new->token_stride; a.kn_hs = k_new->head_stride;
+  a.vn = v_new->data; a.vn_bs = v_new->batch_stride; a.vn_ts = v_new->token_stride; a.vn_hs = v_new->head_stride;
+  a.kp = cache->k_pages; a.vp = cache->v_pages; a.pages = cache->pages;
+  a.table = cache->table; a.width = cache->width; a.lengths = cache->lengths;
+  a.mask = mask; a.words = (T + 63) / 64; a.positions = positions;
+  a.o = o; a.lse = lse;
+  a.bf16 = cache->dtype == GCA_BF16; a.B = B; a.T = T; a.H = H; a.Hkv = cache->heads; a.g = H / cache->heads;
+  a.dh = cache->dh; a.window = window; a.scale = scale;
+  a.err = reinterpret_cast<ErrWord*>(ws);
+  a.part = static_cast<unsigned char*>(scratch);
+  cudaError_t e = launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_tree_attention launch");
+  return GCA_OK;
+}
+
 // ==================================================================== errors, instrumentation
 extern "C" gca_status gca_check_error(void* ws, gca_stream_t stream, int* bad_value) {
   if (!ws) return fail(GCA_ERR_WORKSPACE, "workspace pointer is NULL");
@@ -594,8 +890,11 @@ extern "C" gca_status gca_check_error(void* ws, gca_stream_t stream, int* bad_va
                 "a bounded wait for tensor-core or copy completion ran out (wait sites 0x%x; first: site %d, "
                 "CTA %d, tile %d, slot %d)",
                 (unsigned)h.wait_sites, h.first[0] - 1, h.first[1], h.first[2], h.first[3]);
+  if (!(h.flags & kErrIndex))
+    return fail(GCA_ERR_CACHE_FULL, "a cache had too few free pages, or too narrow a table, for an append");
   if (bad_value) *bad_value = h.bad_value;
-  return fail(GCA_ERR_DEVICE_INDEX, "a kernel met retrieved index %d outside [-1, nC)", h.bad_value);
+  return fail(GCA_ERR_DEVICE_INDEX, "a kernel met index %d out of range (a retrieved chunk outside [-1, nC), or a page, slot, "
+              "count or token)", h.bad_value);
 }
 
 // ==================================================================== wait self-test

@@ -1,0 +1,408 @@
+// Pages of a K/V cache: appending rows, forking, trimming and compacting.
+//
+// A pool holds pages of 64 tokens (the chunks of the retrieval store); table[slot][p] is the
+// page with the slot's tokens 64 p .. 64 p + 63, or -1; refs[page] counts the slots that
+// hold it, 0 for a free page.  refs is the only record of what is free: a call takes the
+// free pages with the lowest numbers, in the order of its entries, so that equal states and
+// calls give equal states whatever the timing.
+//
+// Bound by memory where rows move (every byte is read and written once), by launch and
+// dependent loads where only the tables change.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gca {
+namespace {
+
+constexpr int kPlanThreads = kCacheEntries;  // one thread an entry
+
+__device__ __forceinline__ void flag_full(ErrWord* e) {
+  if (e) atomicOr(&e->flags, kErrFull);
+}
+
+// The slot of entry i; entries whose slot is out of range, or was named by an earlier
+// entry, are flagged and left out (-1).  `all` holds every entry's slot as given.
+__device__ __forceinline__ int given_slot(const CacheArgs& c, int i) { return c.slot ? c.slot[i] : i; }
+__device__ __forceinline__ int checked_slot(const CacheArgs& c, const int* all, int i) {
+  const int s = all[i];
+  bool bad = s < 0 || s >= c.slots;
+  if (c.slot)
+    for (int j = 0; j < i && !bad; ++j) bad = all[j] == s;
+  if (bad) flag_bad_index(c.err, s);
+  return bad ? -1 : s;
+}
+
+// Inclusive sum over the block's 1024 threads; `red` holds 32 values.
+__device__ __forceinline__ int block_scan(int v, int* red, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  int w = red[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += o;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int base = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  __syncthreads();
+  return v + (warp ? base : 0);
+}
+
+// ------------------------------------------------------------------ append
+// One CTA, one thread an entry: what each entry needs, the free pages in order, the tables.
+__global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a) {
+  const CacheArgs& c = a.c;
+  __shared__ int all[kCacheEntries], start[kCacheEntries], first[kCacheEntries];
+  __shared__ int red[32];
+  const int i = threadIdx.x;
+  all[i] = i < c.n ? given_slot(c, i) : -1;
+  __syncthreads();
+  int slot = -1, old = 0, take = 0, hold = -1;
+  if (i < c.n) {
+    slot = checked_slot(c, all, i);
+    if (slot >= 0) {
+      take = a.counts[i];
+      old = c.lengths[slot];
+      if (take < 0 || take > a.T) {
+        flag_bad_index(c.err, take);
+        take = 0;
+      }
+      if (old < 0 || old > (int64_t)c.width * kChunk) {
+        flag_bad_index(c.err, old);
+        take = 0;
+      } else if ((int64_t)old + take > (int64_t)c.width * kChunk) {
+        flag_full(c.err);
+        take = 0;
+      }
+      if (take > 0 && old % kChunk) {
+        hold = c.table[(int64_t)slot * c.width + old / kChunk];
+        if (hold < 0 || hold >= c.pages) {
+          flag_bad_index(c.err, hold);
+          take = 0;
+          hold = -1;
+        }
+      }
+    }
+  }
+  // A last page that several slots hold is copied for each entry that writes to it (its
+  // readers of this call and those that keep it see the rows as they are).
+  const bool copy = hold >= 0 && c.refs[hold] > 1;
+  const int f = copy ? old / kChunk : (old + kChunk - 1) / kChunk;
+  const int need = take > 0 ? (old + take + kChunk - 1) / kChunk - f : 0;
+  int total;
+  const int incl = block_scan(need, red, total);
+  start[i] = incl - need;
+  first[i] = f;
+  __syncthreads();
+  // The first `total` free pages, in order.
+  int found = 0;
+  for (int64_t p0 = 0; p0 < c.pages && found < total; p0 += 4 * kPlanThreads) {
+    const int64_t p = p0 + 4 * i;
+    int r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = p + k < c.pages ? c.refs[p + k] : 1;
+    const int mine = (r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0);
+    int got;
+    int at = found + block_scan(mine, red, got) - mine;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r[k] == 0) {
+        if (at < total) a.fresh[at] = (int)(p + k);
+        ++at;
+      }
+    found += got;
+  }
+  found = min(found, total);
+  __syncthreads();
+  // Entries are served in order; from the first that the free pages do not reach, none is.
+  const bool served = take > 0 && start[i] + need <= found;
+  if (take > 0 && !served) flag_full(c.err);
+  int hand;
+  block_scan(served ? need : 0, red, hand);  // pages that are handed out: entries are a prefix
+  for (int k = i; k < hand; k += kPlanThreads) {
+    int lo = 0, hi = c.n - 1;  // the last entry whose pages start at k or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start[mid] <= k) lo = mid;
+      else hi = mid - 1;
+    }
+    const int page = a.fresh[k];
+    c.table[(int64_t)all[lo] * c.width + first[lo] + k - start[lo]] = page;
+    c.refs[page] = 1;
+  }
+  if (served) {
+    if (copy) atomicSub(&c.refs[hold], 1);
+    c.lengths[slot] = old + take;
+  }
+  if (i < c.n) {
+    int4* rec = reinterpret_cast<int4*>(a.rec) + i;
+    *rec = make_int4(old, served ? take : 0, served && copy ? hold : -1, slot);
+  }
+}
+
+// CTA (page step, entry): the rows of one page, a quarter of them a CTA.
+constexpr int kRowParts = 4;
+__global__ void __launch_bounds__(256) append_rows_kernel(AppendArgs a) {
+  const CacheArgs& c = a.c;
+  const int i = blockIdx.y, step = blockIdx.x / kRowParts, part = blockIdx.x % kRowParts;
+  const int4 rec = reinterpret_cast<const int4*>(a.rec)[i];
+  const int old = rec.x, now = old + rec.y, slot = rec.w;
+  const int p = old / kChunk + step;
+  if (rec.y == 0 || (int64_t)p * kChunk >= now) return;
+  const int64_t page = c.table[(int64_t)slot * c.width + p];
+  const int units = (int)(c.token_bytes / 16);
+  const int per = kChunk / kRowParts, r0 = part * per;
+  const bool copied = rec.z >= 0 && step == 0;
+  for (int u = threadIdx.x; u < per * units; u += blockDim.x) {
+    const int r = r0 + u / units, x = u % units, j = p * kChunk + r;
+    if (j >= now) break;
+    const int64_t to = (page * kChunk + r) * c.token_bytes + x * 16;
+    const unsigned char *k, *v;
+    if (j >= old) {
+      int t = j - old;
+      if (a.path) {
+        t = a.path[(int64_t)i * a.T + t];
+        if (t < 0 || t >= a.T) {
+          if (x == 0) flag_bad_index(c.err, t);
+          continue;
+        }
+      }
+      k = a.kn + i * a.kn_bs + t * a.kn_ts + x * 16;
+      v = a.vn + i * a.vn_bs + t * a.vn_ts + x * 16;
+    } else if (copied) {
+      const int64_t from = ((int64_t)rec.z * kChunk + r) * c.token_bytes + x * 16;
+      k = c.kp + from;
+      v = c.vp + from;
+    } else {
+      continue;
+    }
+    const uint4 kv = *reinterpret_cast<const uint4*>(k), vv = *reinterpret_cast<const uint4*>(v);
+    *reinterpret_cast<uint4*>(c.kp + to) = kv;
+    *reinterpret_cast<uint4*>(c.vp + to) = vv;
+  }
+}
+
+// ------------------------------------------------------------------ fork
+// One CTA a pair.  A pair whose destination is not empty, is named by an earlier pair, or
+// whose source is a destination of the call, is flagged and left out.
+__global__ void __launch_bounds__(1024) fork_kernel(CacheArgs c, const int32_t* dst) {
+  const int i = blockIdx.x;
+  const int s = c.slot[i], d = dst[i];
+  bool bad = s < 0 || s >= c.slots || d < 0 || d >= c.slots;
+  for (int j = threadIdx.x; j < c.n; j += blockDim.x) bad = bad || dst[j] == s || (j < i && dst[j] == d);
+  if (!bad) bad = c.lengths[d] != 0;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) flag_bad_index(c.err, d);
+    return;
+  }
+  for (int p = threadIdx.x; p < c.width; p += blockDim.x) {
+    int t = c.table[(int64_t)s * c.width + p];
+    if (t < -1 || t >= c.pages) {
+      flag_bad_index(c.err, t);
+      t = -1;
+    }
+    if (t >= 0) atomicAdd(&c.refs[t], 1);
+    c.table[(int64_t)d * c.width + p] = t;
+  }
+  if (threadIdx.x == 0) c.lengths[d] = c.lengths[s];
+}
+
+// ------------------------------------------------------------------ trim
+// One CTA an entry: keeps tokens begin .. end - 1; pages that lie outside are given back.
+__global__ void __launch_bounds__(1024) trim_kernel(CacheArgs c, const int32_t* begin, const int32_t* end, int release) {
+  const int i = blockIdx.x;
+  const int s = given_slot(c, i);
+  bool bad = s < 0 || s >= c.slots;
+  if (c.slot)
+    for (int j = threadIdx.x; j < i; j += blockDim.x) bad = bad || c.slot[j] == s;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) flag_bad_index(c.err, s);
+    return;
+  }
+  const int len = max(c.lengths[s], 0);
+  const int hi = release ? 0 : (end ? min(max(end[i], 0), len) : len);
+  const int lo = begin ? min(max(begin[i], 0), hi) : 0;
+  __syncthreads();  // every thread has read the length
+  for (int p = threadIdx.x; p < c.width; p += blockDim.x) {
+    const int64_t j = (int64_t)p * kChunk;
+    if (j + kChunk > lo && j < hi) continue;
+    int32_t* at = c.table + (int64_t)s * c.width + p;
+    const int t = *at;
+    if (t == -1) continue;
+    *at = -1;
+    if (t < -1 || t >= c.pages) {
+      flag_bad_index(c.err, t);
+    } else if (atomicSub(&c.refs[t], 1) <= 0) {  // not counted for this slot
+      atomicAdd(&c.refs[t], 1);
+      flag_bad_index(c.err, t);
+    }
+  }
+  if (threadIdx.x == 0) c.lengths[s] = hi;
+}
+
+// ------------------------------------------------------------------ compact
+// With n pages in use, those numbered n and above move, in order, to the free numbers
+// below n, in order: no other choice moves fewer.  Three launches: uses per part of the
+// pool; the two lists; the rows and the tables.
+__global__ void __launch_bounds__(256) compact_count_kernel(CompactArgs a) {
+  const int64_t per = (a.c.pages + kCompactParts - 1) / kCompactParts;
+  const int64_t p0 = min(blockIdx.x * per, a.c.pages), p1 = min(p0 + per, a.c.pages);
+  int n = 0;
+  for (int64_t p = p0 + threadIdx.x; p < p1; p += blockDim.x) n += a.c.refs[p] > 0;
+  __shared__ int sum;
+  if (threadIdx.x == 0) sum = 0;
+  __syncthreads();
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&sum, n);
+  __syncthreads();
+  if (threadIdx.x == 0) a.counts[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(1024) compact_lists_kernel(CompactArgs a) {
+  __shared__ int red[32];
+  __shared__ int cnt[kCompactParts];
+  __shared__ int extra;
+  const int64_t per = (a.c.pages + kCompactParts - 1) / kCompactParts;
+  if (threadIdx.x < kCompactParts) cnt[threadIdx.x] = a.counts[threadIdx.x];
+  if (threadIdx.x == 0) extra = 0;
+  __syncthreads();
+  int n = 0, before = 0;  // pages in use: all, before this part
+  for (int k = 0; k < kCompactParts; ++k) {
+    if (k < (int)blockIdx.x) before += cnt[k];
+    n += cnt[k];
+  }
+  // Uses below page n: whole parts, and the part that n lies in.
+  const int whole = (int)(n / per);
+  int below = 0;
+  for (int k = 0; k < whole; ++k) below += cnt[k];
+  int mine = 0;
+  for (int64_t p = whole * per + threadIdx.x; p < n; p += blockDim.x) mine += a.c.refs[p] > 0;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+  if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&extra, mine);
+  __syncthreads();
+  below += extra;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.live[0] = n;
+    a.counts[kCompactParts] = n - below;  // pages that move
+  }
+  const int64_t q0 = min(blockIdx.x * per, a.c.pages), q1 = min(q0 + per, a.c.pages);
+  for (int64_t base = q0; base < q1; base += blockDim.x) {
+    const int64_t p = base + threadIdx.x;
+    const int used = p < q1 && a.c.refs[p] > 0;
+    int got;
+    const int rank = before + block_scan(used, red, got) - used;  // uses before page p
+    before += got;
+    if (p >= q1) continue;
+    if (used && p >= n) {
+      a.movers[rank - below] = (int)p;
+      a.rank[p] = rank - below;
+    } else if (!used) {
+      if (p < n) a.holes[p - rank] = (int)p;
+      else a.rank[p] = -1;
+    }
+  }
+}
+
+constexpr int kMoveParts = 8;
+__global__ void __launch_bounds__(256) compact_move_kernel(CompactArgs a) {
+  const CacheArgs& c = a.c;
+  const int n = a.live[0], moves = a.counts[kCompactParts];
+  const int64_t page16 = kChunk * c.token_bytes / 16, per16 = page16 / kMoveParts;
+  for (int64_t w = blockIdx.x; w < (int64_t)moves * kMoveParts; w += gridDim.x) {
+    const int k = (int)(w / kMoveParts), part = (int)(w % kMoveParts);
+    const int64_t src = a.movers[k] * page16 + part * per16, dst = a.holes[k] * page16 + part * per16;
+    const uint4 *ks = reinterpret_cast<const uint4*>(c.kp) + src, *vs = reinterpret_cast<const uint4*>(c.vp) + src;
+    uint4 *kd = reinterpret_cast<uint4*>(c.kp) + dst, *vd = reinterpret_cast<uint4*>(c.vp) + dst;
+    for (int64_t u = threadIdx.x; u < per16; u += blockDim.x) {
+      const uint4 x = ks[u], y = vs[u];
+      kd[u] = x;
+      vd[u] = y;
+    }
+    if (part == 0 && threadIdx.x == 0) {
+      c.refs[a.holes[k]] = c.refs[a.movers[k]];
+      c.refs[a.movers[k]] = 0;
+    }
+  }
+  const int64_t all = (int64_t)c.slots * c.width;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < all; e += (int64_t)gridDim.x * blockDim.x) {
+    const int t = c.table[e];
+    if (t < -1 || t >= c.pages) {
+      flag_bad_index(c.err, t);
+      c.table[e] = -1;
+    } else if (t >= n) {
+      const int k = a.rank[t];
+      if (k < 0) flag_bad_index(c.err, t);  // a page that nothing counts
+      c.table[e] = k < 0 ? -1 : a.holes[k];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ lookup
+__global__ void __launch_bounds__(256) lookup_kernel(CacheArgs c, const int32_t* idx, int per, int32_t* out) {
+  const int i = blockIdx.y, e = blockIdx.x * blockDim.x + threadIdx.x;
+  if (e >= per) return;
+  const int64_t at = (int64_t)i * per + e;
+  const int s = given_slot(c, i), j = idx[at];
+  int page = -1;
+  if (s < 0 || s >= c.slots) flag_bad_index(c.err, s);
+  else if (j < -1 || j >= c.width) flag_bad_index(c.err, j);
+  else if (j >= 0) page = c.table[(int64_t)s * c.width + j];
+  out[at] = page;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s) {
+  launch_begin("cache_append_plan", s);
+  append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  cudaError_t e = launch_end("cache_append_plan", s);
+  if (e != cudaSuccess || a.T == 0) return e;
+  const int steps = (a.T + kChunk - 1) / kChunk + 1;
+  launch_begin("cache_append_rows", s);
+  append_rows_kernel<<<dim3(steps * kRowParts, a.c.n), 256, 0, s>>>(a);
+  return launch_end("cache_append_rows", s);
+}
+
+cudaError_t launch_cache_fork(const CacheArgs& c, const int32_t* dst, cudaStream_t s) {
+  launch_begin("cache_fork", s);
+  fork_kernel<<<c.n, 1024, 0, s>>>(c, dst);
+  return launch_end("cache_fork", s);
+}
+
+cudaError_t launch_cache_trim(const CacheArgs& c, const int32_t* begin, const int32_t* end, int release, cudaStream_t s) {
+  launch_begin("cache_trim", s);
+  trim_kernel<<<c.n, 1024, 0, s>>>(c, begin, end, release);
+  return launch_end("cache_trim", s);
+}
+
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s) {
+  launch_begin("cache_compact_count", s);
+  compact_count_kernel<<<kCompactParts, 256, 0, s>>>(a);
+  cudaError_t e = launch_end("cache_compact_count", s);
+  if (e != cudaSuccess) return e;
+  launch_begin("cache_compact_lists", s);
+  compact_lists_kernel<<<kCompactParts, 1024, 0, s>>>(a);
+  e = launch_end("cache_compact_lists", s);
+  if (e != cudaSuccess) return e;
+  launch_begin("cache_compact_move", s);
+  compact_move_kernel<<<kSMs * 4, 256, 0, s>>>(a);
+  return launch_end("cache_compact_move", s);
+}
+
+cudaError_t launch_cache_lookup(const CacheArgs& c, const int32_t* idx, int per, int32_t* out, cudaStream_t s) {
+  launch_begin("cache_lookup", s);
+  lookup_kernel<<<dim3((per + 255) / 256, c.n), 256, 0, s>>>(c, idx, per, out);
+  return launch_end("cache_lookup", s);
+}
+
+}  // namespace gca

@@ -13,13 +13,15 @@ constexpr int kMaxTopk = 16;  // largest supported top-k
 
 // Device error word: the first 256 bytes of every workspace.
 struct ErrWord {
-  int flags;      // bit 0: an index outside [-1, nC) was met; bit 1: a bounded wait ran out
+  int flags;      // bit 0: an index outside [-1, nC) was met; bit 1: a bounded wait ran out;
+                  // bit 2: a cache had no room for an append
   int bad_value;  // last offending index
   int wait_sites; // bit s % 32: the wait at site s ran out (sites are numbered per kernel)
   int first[4];   // the first wait that ran out: site + 1, CTA, tile, slot (0 until then)
 };
 constexpr int kErrIndex = 1;
 constexpr int kErrTimeout = 2;
+constexpr int kErrFull = 4;
 constexpr size_t kErrBytes = 256;
 
 __device__ __forceinline__ void flag_bad_index(ErrWord* e, int v) {

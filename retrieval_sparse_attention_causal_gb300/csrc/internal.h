@@ -168,6 +168,79 @@ struct EncoderArgs {
 };
 cudaError_t launch_chunk_encoder(const EncoderArgs& a, cudaStream_t s);
 
+// ---- rotary positions (rotary.cu)
+constexpr int kSMs = 152;  // SMs of a GB300: grids that fill it are multiples of this
+struct RotarySide {
+  const void* in; int64_t in_bs, in_ts, in_hs;  // element strides: batch, token, head
+  void* out; int64_t out_bs, out_ts, out_hs;
+};
+struct RotaryArgs {
+  RotarySide q, k;
+  int bf16, B, L, H, Hkv, dh, rot, paired;
+  int tail;                                // elements behind `rot` that are copied (0 in place)
+  const uint64_t* freq;                    // [rot / 2]
+  const int32_t* pos; int64_t pos_bs;      // null: token l is at position l
+  float gain, sgain;                       // factors of the cosine and of the sine
+  int tokens;                              // per CTA (set by the launcher)
+};
+cudaError_t launch_rotary(RotaryArgs a, cudaStream_t s);
+
+// ---- attention of drafted tokens over a paged cache (tree_attn.cu)
+struct TreeArgs {
+  const void* q; int64_t q_bs, q_ts, q_hs;                 // [B][T][H][dh], element strides
+  const void* kn; int64_t kn_bs, kn_ts, kn_hs;             // the draft's keys [B][T][Hkv][dh]
+  const void* vn; int64_t vn_bs, vn_ts, vn_hs;
+  const void* kp; const void* vp; int64_t pages;           // [pages][64][Hkv][dh]
+  const int32_t* table; int width; const int32_t* lengths;  // [B][width], [B]
+  const uint64_t* mask; int words; const int32_t* positions;  // [B][T][words], [B][T]; may be null
+  void* o; float* lse;                                     // [B][T][H][dh], [B][T][H]
+  int bf16, B, T, H, Hkv, g, dh, window;
+  float scale;
+  ErrWord* err;
+  unsigned char* part;                                     // partial results
+  int rows, nrt, nd;                                       // rows of a tile, tiles of T g rows, blocks of the draft
+  int grid; int64_t min_blocks;                            // CTAs, and the fewest blocks worth a CTA
+};
+size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16);
+cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s);
+struct TreePlanArgs {
+  const int32_t* parents; const int32_t* lengths;
+  int B, T, words;
+  uint64_t* mask; int32_t* positions;
+  ErrWord* err;
+};
+cudaError_t launch_tree_plan(const TreePlanArgs& a, cudaStream_t s);
+
+// ---- page operations of a cache (cache.cu)
+struct CacheArgs {
+  unsigned char* kp; unsigned char* vp; int64_t pages;     // [pages][64] tokens of token_bytes
+  int64_t token_bytes;
+  int32_t* table; int slots, width; int32_t* lengths; int32_t* refs;
+  int n; const int32_t* slot;                              // entries, and their slots (null: entry i is slot i)
+  ErrWord* err;
+};
+struct AppendArgs {
+  CacheArgs c;
+  const unsigned char* kn; int64_t kn_bs, kn_ts;           // byte strides of the new rows
+  const unsigned char* vn; int64_t vn_bs, vn_ts;
+  const int32_t* counts; const int32_t* path; int T;
+  int32_t* rec;                                            // scratch: kAppendRec values an entry
+  int32_t* fresh;                                          // scratch: free pages in order
+};
+constexpr int kAppendRec = 4;      // old length, tokens, source page of a copied last page (or -1), slot
+constexpr int kCacheEntries = 1024;
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheArgs& a, const int32_t* dst, cudaStream_t s);
+cudaError_t launch_cache_trim(const CacheArgs& a, const int32_t* begin, const int32_t* end, int release, cudaStream_t s);
+struct CompactArgs {
+  CacheArgs c;
+  int32_t* live;                                           // out: pages in use
+  int32_t* counts; int32_t* movers; int32_t* holes; int32_t* rank;  // scratch
+};
+constexpr int kCompactParts = 152;
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s);
+cudaError_t launch_cache_lookup(const CacheArgs& a, const int32_t* idx, int per, int32_t* out, cudaStream_t s);
+
 // ---- CSR of consumers per key chunk (gca_bwd.cu), also used by the score backward.
 // Rows r in [0, nrows) of idx [B][ld_rows][topk] are entries e = r*topk + m.
 cudaError_t launch_csr(const int32_t* idx, int B, int ld_rows, int nrows, int topk, int nC,

@@ -1,0 +1,195 @@
+"""CPU tests of the decoding operators: refusals before anything is launched, the rotary
+frequency table, and the page oracle's own rules."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.decode_oracle as orc
+
+FAKE = 0x100000  # 16-byte aligned, never dereferenced: every call below fails validation
+
+
+@pytest.fixture(scope="module")
+def gca():
+    import __graft_entry__
+    __graft_entry__.build()
+    import retrieval_sparse_attention_causal_gb300 as m
+    return m
+
+
+def heads(g, data=FAKE, bs=64 * 12 * 64, ts=12 * 64, hs=64):
+    return ctypes.byref(g.Heads(data, bs, ts, hs))
+
+
+def pool(g, **kw):
+    a = dict(k_pages=FAKE, v_pages=FAKE, dtype=g.GCA_BF16, heads=4, dh=64, pages=100, table=FAKE, slots=8, width=10,
+             lengths=FAKE, refs=FAKE)
+    a.update(kw)
+    return ctypes.byref(g.Cache(**a))
+
+
+def test_rotary_refusals(gca):
+    L = gca.LIB
+
+    def call(q=None, k=None, qo=None, ko=None, dt=gca.GCA_BF16, B=2, n=64, H=12, Hkv=12, dh=64, rot=64, freq=FAKE, pbs=0, nok=False):
+        h = lambda x: x if x is not None else heads(gca)  # noqa: E731
+        return L.gca_rotary(h(q), None if nok else h(k), h(qo), None if nok else h(ko), dt, B, n, H, Hkv, dh, rot, 0, 0,
+                            freq, None, pbs, 1.0, None)
+    assert call(dt=5) == gca.GCA_ERR_INVALID_ARG
+    assert call(q=heads(gca, 0)) == gca.GCA_ERR_INVALID_ARG
+    assert call(ko=heads(gca, 0)) == gca.GCA_ERR_INVALID_ARG
+    assert call(B=0) == gca.GCA_ERR_INVALID_ARG
+    assert call(Hkv=0) == gca.GCA_ERR_INVALID_ARG
+    assert call(nok=True) == gca.GCA_ERR_INVALID_ARG  # Hkv without k
+    assert call(n=1 << 30) == gca.GCA_ERR_INVALID_ARG
+    assert call(dh=300) == gca.GCA_ERR_UNSUPPORTED
+    assert call(rot=63) == gca.GCA_ERR_INVALID_ARG
+    assert call(rot=66) == gca.GCA_ERR_INVALID_ARG
+    assert call(rot=0) == gca.GCA_ERR_INVALID_ARG
+    assert call(freq=0) == gca.GCA_ERR_INVALID_ARG
+    assert call(freq=FAKE + 4) == gca.GCA_ERR_INVALID_ARG
+    assert call(pbs=-1) == gca.GCA_ERR_INVALID_ARG
+    assert call(q=heads(gca, FAKE + 1)) == gca.GCA_ERR_INVALID_ARG
+    assert call(q=heads(gca, ts=-64)) == gca.GCA_ERR_INVALID_ARG
+    assert call(qo=heads(gca, hs=32)) == gca.GCA_ERR_INVALID_ARG  # heads overlap
+    assert call(qo=heads(gca, ts=64, hs=64)) == gca.GCA_ERR_INVALID_ARG
+    assert call(ko=heads(gca, bs=0)) == gca.GCA_ERR_INVALID_ARG
+    assert b"overlap" in L.gca_last_error_detail()
+
+
+def test_rotary_frequencies(gca):
+    for rot, kw in ((64, {}), (2, {}), (40, dict(scaling="linear", factor=16.0)), (64, dict(scaling="ntk", factor=4.0, base=5e5)),
+                    (2, dict(scaling="ntk", factor=4.0)), (128, dict(scaling="parts", factor=8.0, context=2048.0)),
+                    (32, dict(scaling="parts", factor=8.0, context=8192.0, low=1.0, high=4.0))):
+        got = gca.rotary_frequencies(rot, device="cpu", **kw).numpy().view(np.uint64).astype(np.float64) / 2.0 ** 64 * 2 * math.pi
+        want = orc.speeds(rot, **kw)
+        # pow, a few products and the rounding to 2^-64 turns (6.3 2^-65 radians)
+        assert np.all(np.abs(got - want) <= 16 * 2.0 ** -53 * want + 2.0 ** -62)
+    for bad in (dict(rot=3), dict(rot=0), dict(rot=258), dict(rot=8, base=0.5), dict(rot=8, base=float("nan")),
+                dict(rot=8, scaling="linear", factor=0.0), dict(rot=8, scaling="linear", factor=float("inf")),
+                dict(rot=8, scaling="parts", factor=2.0, context=0.0), dict(rot=8, scaling="parts", factor=2.0, context=9.0, low=4.0, high=4.0)):
+        with pytest.raises(gca.GCAError):
+            gca.rotary_frequencies(device="cpu", **bad)
+    with pytest.raises(ValueError):
+        gca.rotary_frequencies(8, scaling="dynamic", device="cpu")
+
+
+def test_cache_refusals(gca):
+    L, E, U, W = gca.LIB, gca.GCA_ERR_INVALID_ARG, gca.GCA_ERR_UNSUPPORTED, gca.GCA_ERR_WORKSPACE
+
+    def append(c=None, k=None, v=None, n=8, T=5, slots=None, counts=FAKE, ws=FAKE, wsb=256, sc=FAKE, scb=1 << 20):
+        h = lambda x: x if x is not None else heads(gca, ts=256, bs=5 * 256)  # noqa: E731
+        return L.gca_cache_append(c if c is not None else pool(gca), h(k), h(v), n, T, slots, counts, None, ws, wsb, sc, scb, None)
+    for kw in (dict(k_pages=0), dict(v_pages=FAKE + 8), dict(dtype=9), dict(heads=0), dict(dh=0), dict(pages=0), dict(table=0),
+               dict(slots=0), dict(width=0), dict(width=1 << 25), dict(lengths=0), dict(refs=0), dict(heads=1, dh=4)):
+        assert append(c=pool(gca, **kw)) == E, kw
+    assert append(n=0) == E and append(n=9) == E and append(n=1025, slots=FAKE) == E
+    assert append(T=0) == E and append(counts=0) == E
+    assert append(k=heads(gca, FAKE + 8)) == E and append(v=heads(gca, ts=257)) == E and append(k=heads(gca, hs=72)) == E
+    assert append(ws=0) == W and append(wsb=8) == W and append(sc=0) == W and append(sc=FAKE + 16) == W
+    assert append(scb=L.gca_cache_append_scratch_size(8, 5) - 1) == W
+    assert L.gca_cache_fork(pool(gca), 2, None, FAKE, FAKE, 256, None) == E
+    assert L.gca_cache_fork(pool(gca), 0, FAKE, FAKE, FAKE, 256, None) == E
+    assert L.gca_cache_fork(pool(gca), 2, FAKE, FAKE, FAKE, 0, None) == W
+    assert L.gca_cache_trim(pool(gca), 9, None, None, None, 0, FAKE, 256, None) == E
+    assert L.gca_cache_trim(pool(gca, refs=0), 8, None, None, None, 0, FAKE, 256, None) == E
+    assert L.gca_cache_compact(pool(gca), None, FAKE, 256, FAKE, 1 << 20, None) == E
+    assert L.gca_cache_compact(pool(gca), FAKE, FAKE, 256, FAKE, 1024, None) == W
+    assert L.gca_cache_lookup(pool(gca), 8, 0, None, FAKE, FAKE, FAKE, 256, None) == E
+    assert L.gca_cache_lookup(pool(gca), 8, 4, None, None, FAKE, FAKE, 256, None) == E
+
+    def attend(c=None, q=None, k=None, v=None, B=2, T=5, H=8, mask=None, window=0, scale=0.125, o=FAKE, lse=FAKE, wsb=256, scb=1 << 30):
+        h = lambda x: x if x is not None else heads(gca)  # noqa: E731
+        return L.gca_tree_attention(h(q), h(k), h(v), c if c is not None else pool(gca), B, T, H, mask, None, window, scale, o,
+                                    lse, FAKE, wsb, FAKE, scb, None)
+    assert attend(c=pool(gca, dh=96)) == U and attend(T=257) == U and attend(T=0) == U
+    assert attend(B=0) == E and attend(B=9) == E and attend(H=6) == E and attend(H=2) == E
+    assert attend(window=-1) == E and attend(scale=0.0) == E and attend(scale=-1.0) == E
+    assert attend(scale=float("inf")) == E and attend(scale=float("nan")) == E
+    assert attend(mask=FAKE + 4) == E and attend(o=0) == E and attend(o=FAKE + 4) == E and attend(lse=0) == E
+    assert attend(q=heads(gca, FAKE + 2)) == E and attend(k=heads(gca, bs=4)) == E and attend(v=heads(gca, 0)) == E
+    assert attend(wsb=0) == W and attend(scb=100) == W
+    assert L.gca_tree_plan(FAKE, FAKE, 2, 257, FAKE, FAKE, FAKE, 256, None) == U
+    assert L.gca_tree_plan(FAKE, FAKE, 0, 5, FAKE, FAKE, FAKE, 256, None) == E
+    assert L.gca_tree_plan(0, FAKE, 2, 5, FAKE, FAKE, FAKE, 256, None) == E
+    assert L.gca_tree_plan(FAKE, FAKE, 2, 5, FAKE + 4, FAKE, FAKE, 256, None) == E
+    assert L.gca_status_string(gca.GCA_ERR_CACHE_FULL) == b"GCA_ERR_CACHE_FULL"
+
+
+def test_binding_refuses_tensors_that_are_not_on_a_gpu(gca):
+    x = torch.zeros(1, 1, 2, 64)
+    with pytest.raises(ValueError):
+        gca.rotary(x, None, torch.zeros(32, dtype=torch.int64))
+    with pytest.raises(TypeError):
+        gca.rotary(x.half(), None, torch.zeros(32, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        gca.rotary(x, None, torch.zeros(32))
+    pages, i = torch.zeros(4, 64, 2, 64), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        gca.PagedCache(pages, pages, torch.zeros(4, 2, dtype=torch.int32), i, i)
+    with pytest.raises(ValueError):
+        gca.PagedCache(pages[:, :32], pages, torch.zeros(4, 2, dtype=torch.int32), i, i)
+    with pytest.raises(ValueError):
+        gca.tree_attention(x, x, x, pages, pages, torch.zeros(4, 2, dtype=torch.int32), i)
+
+
+def test_oracle_pages_keep_their_tokens():
+    """The model's own rule: a slot's tokens are what was appended to it, whatever is forked,
+    trimmed, freed or compacted around it."""
+    rng = np.random.default_rng(0)
+    m = orc.Pages(np.zeros((40, 64, 1, 1)), np.zeros((40, 64, 1, 1)), np.full((4, 6), -1), np.zeros(4, int), np.zeros(40, int))
+    held = [[], [], [], []]
+    for step in range(80):
+        s = int(rng.integers(4))
+        kind = rng.integers(4)
+        if kind < 2:
+            T = int(rng.integers(1, 60))
+            counts = [int(min(rng.integers(0, T + 1), 384 - len(h))) if i == s else 0 for i, h in enumerate(held)]
+            rows = rng.normal(size=(4, T, 1, 1))
+            m.append(rows, rows, counts)
+            if not m.full:
+                held[s] += list(rows[s, :counts[s], 0, 0])
+        elif kind == 2:
+            cut = int(rng.integers(0, len(held[s]) + 1))
+            m.trim(end=[cut], slots=[s])
+            held[s] = held[s][:cut]
+            m.compact()
+        else:
+            d = int(rng.integers(4))
+            if d != s and not held[d]:
+                m.fork([s], [d])
+                held[d] = list(held[s])
+        assert not m.flagged and not m.full
+        for i in range(4):
+            assert list(m.tokens(i).reshape(-1)) == held[i]
+        counted = np.bincount(m.table[m.table >= 0], minlength=40)
+        assert np.array_equal(counted, m.refs)
+
+
+def test_oracle_attention_is_the_softmax_of_what_is_seen():
+    rng = np.random.default_rng(1)
+    see, pos = orc.tree([-1, 0, 0, -2, 2], 70)
+    assert pos.tolist() == [70, 71, 71, -1, 72] and see[4].tolist() == [True, False, True, False, True]
+    assert orc.pack_mask(see[None])[0, :, 0].tolist() == [1, 3, 5, 0, 21]
+    k, v, q = rng.normal(size=(3, 64, 1, 4)), rng.normal(size=(3, 64, 1, 4)), rng.normal(size=(1, 5, 2, 4))
+    kn, vn = rng.normal(size=(1, 5, 1, 4)), rng.normal(size=(1, 5, 1, 4))
+    o, lse, *_ = orc.tree_attention(q, kn, vn, k, v, np.array([[2, 0]]), [70], see[None], pos[None], window=4)
+    keys = np.concatenate([k[0, 5:6, 0], kn[0, [0, 2, 4], 0]])  # token 72 sees positions 69 to 72
+    vals = np.concatenate([v[0, 5:6, 0], vn[0, [0, 2, 4], 0]])
+    e = np.exp(keys @ q[0, 4, 1] / 2)
+    assert np.allclose(o[0, 4, 1], e @ vals / e.sum()) and np.isclose(lse[0, 4, 1], np.log(e.sum()))
+    assert not o[0, 3].any() and np.all(lse[0, 3] == -np.inf)
+
+
+def test_oracle_rotary():
+    x = np.random.default_rng(2).normal(size=(1, 2, 1, 6))
+    w = orc.speeds(4)
+    y = orc.rotary(x, np.array([[0, 7]]), w, gain=2.0)
+    assert np.allclose(y[0, 0, 0, :4], 2 * x[0, 0, 0, :4]) and np.array_equal(y[..., 4:], x[..., 4:])
+    z = (x[0, 1, 0, 1] + 1j * x[0, 1, 0, 3]) * np.exp(7j * w[1]) * 2
+    assert np.allclose([y[0, 1, 0, 1], y[0, 1, 0, 3]], [z.real, z.imag])
+    back = orc.rotary(y, np.array([[0, 7]]), w, gain=0.5, backward=True)
+    assert np.allclose(back, x)
