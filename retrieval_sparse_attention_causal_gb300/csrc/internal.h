@@ -198,9 +198,11 @@ struct TreeArgs {
   float scale;
   ErrWord* err;
   unsigned char* part;                                     // partial results
-  int rows, nrt, nd;                                       // rows of a tile, tiles of T g rows, blocks of the draft
-  int grid; int64_t min_blocks;                            // CTAs, and the fewest blocks worth a CTA
+  int hw, rows, nrt, nd;                                   // key heads and rows of a tile, tiles of T g rows, blocks of the draft
+  int grid, min_blocks;                            // CTAs, and the fewest blocks worth a CTA
+  int wide;                                                // pools on 32-byte boundaries
 };
+cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);  // bf16, T g <= 16 (tree_rows.cu)
 size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16);
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s);
 struct TreePlanArgs {

@@ -18,25 +18,6 @@ namespace gca {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-// ------------------------------------------------------------------ partial results
-// Slot s: [rows] maxima (of log2 e times the scaled logits), [rows] sums, [rows][dh] outputs.
-struct Part {
-  float* m; float* l; float* o;
-};
-__device__ __forceinline__ Part part_of(const TreeArgs& a, int64_t slot) {
-  float* p = reinterpret_cast<float*>(a.part) + slot * a.rows * (a.dh + 2);
-  return Part{p, p + a.rows, p + 2 * a.rows};
-}
-
-// Where row r of a tile goes: token t, query head h.
-__device__ __forceinline__ void row_of(const TreeArgs& a, int r, int m, int& t, int& h) {
-  t = r / a.g;
-  h = m * a.g + (r - t * a.g);
-}
-
 // ------------------------------------------------------------------ CUDA-core kernel
 // 128 threads; thread (ty, tx) owns rows ty RT .. ty RT + RT - 1, of a block's logits the
 // keys tx + 16 j, and of the output DH / 16 columns.  K and V pass through shared memory
@@ -53,27 +34,25 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
   float* Ks = Qs + MT * QS;
   float* Vs = Ks + 64 * QS;
   float* Ps = Vs + 64 * QS;
-  __shared__ int64_t buf[kSimtThreads / 32 + 1];
-  __shared__ Share sh_s;
   __shared__ int row_pos[MT];
   __shared__ unsigned long long used_s;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const Share sh = share_of<kSimtThreads>(a, blockIdx.x, -1, buf, &sh_s);
-  const float sl2 = a.scale * kLog2e;
+  const Share sh = share_of(a, blockIdx.x);
+  const float sl2 = a.scale * kTreeLog2e;
   const int R = a.T * a.g;
   int b = sh.b;
-  int64_t off = sh.off, item = sh.lo;
+  int off = sh.off, item = sh.lo;
   SeqBlocks sb = sh.lo < sh.hi ? seq_blocks(a, b, false) : SeqBlocks{};
   int slot = 0;
   while (item < sh.hi) {
-    const int64_t tile = off / sb.nb;
-    if (tile >= (int64_t)a.Hkv * a.nrt) {
+    const int tile = off / sb.nb;
+    if (tile >= a.Hkv * a.nrt) {
       sb = seq_blocks(a, ++b, false);
       off = 0;
       continue;
     }
-    const int m = (int)(tile / a.nrt), rt = (int)(tile % a.nrt);
-    const int blk0 = (int)(off - tile * sb.nb), blk1 = (int)min((int64_t)sb.nb, blk0 + (sh.hi - item));
+    const int m = tile / a.nrt, rt = tile - m * a.nrt;
+    const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     const int rows = min(MT, R - rt * MT);
     __syncthreads();
     for (int i = tid; i < MT * DH; i += kSimtThreads) {
@@ -222,7 +201,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
         row_of(a, rt * MT + r, m, t, h);
         const int64_t at = ((int64_t)b * a.T + t) * a.H + h;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;  // sum is 0 where the row saw nothing
-        if (tx == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : mx[i] * kLn2 + logf(sum);
+        if (tx == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : mx[i] * kTreeLn2 + logf(sum);
 #pragma unroll
         for (int c = 0; c < NC * CV; ++c)
           Elem<T>::st(reinterpret_cast<T*>(a.o) + at * DH + (c / CV) * 16 * CV + tx * CV + c % CV, o[i][c] * inv);
@@ -242,68 +221,103 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
 }
 
 // ------------------------------------------------------------------ joining the partials
-// CTA (tile, sequence, row group): up to 8 rows, each by 16 threads over the columns and
-// 256 / (16 rows) threads over the partials.
+// CTA (tile, sequence, row group): rg rows, each by 16 threads over the columns and 16 / rg
+// sets of threads over the partials.  A thread walks its partials once, with a running
+// maximum; the sets are joined in shared memory.
 constexpr int kJoinThreads = 256;
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, int rg) {
-  constexpr int NC = DH / 16;
-  __shared__ int64_t buf[kJoinThreads / 32 + 1];
-  __shared__ Share sh_s;
-  __shared__ float red_m[16][17], red_l[16];
-  __shared__ float red_o[16][DH + 1];
-  const int b = blockIdx.y, tile = blockIdx.x, m = tile / a.nrt, rt = tile % a.nrt;
-  const Share sh = share_of<kJoinThreads>(a, 1, b, buf, &sh_s);
+  constexpr int NC = DH / 16, CV = NC < 4 ? NC : 4, NQ = NC / CV;  // a thread's columns: NQ runs of CV
+  __shared__ float red_m[16], red_l[16];
+  __shared__ __align__(16) float red_o[16][DH + 4];
+  const int b = blockIdx.y, tile = blockIdx.x, hg = tile / a.nrt, rt = tile % a.nrt;
+  const Share sh = shares(a, items_before(a, a.B, false));
   const SeqBlocks sb = seq_blocks(a, b, false);
-  const int64_t s0 = sh.lo + (int64_t)tile * sb.nb, s1 = s0 + sb.nb;
-  const int64_t c0 = ((s0 + 1) * sh.G - 1) / sh.W, c1 = (s1 * sh.G - 1) / sh.W;  // CTAs of its first and last block
+  const int s0 = items_before(a, b, false) + tile * sb.nb;
+  const int c0 = owner_of(sh, s0), c1 = owner_of(sh, s0 + sb.nb - 1);  // CTAs of its first and last block
   if (c0 == c1) return;  // finished there
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, ps = 16 / rg;
-  const int ri = y % rg, pi = y / rg;
-  const int r = blockIdx.z * rg + ri, rows = min(a.rows, a.T * a.g - rt * a.rows);
-  const bool on = r < rows;
-  float mx = -CUDART_INF_F;
-  auto slot_of = [&](int64_t c) { return 2 * c + (sh.W * c / sh.G < s0 ? 1 : 0); };
-  if (on)
-    for (int64_t c = c0 + pi * 16 + x; c <= c1; c += 16 * ps) mx = fmaxf(mx, part_of(a, slot_of(c)).m[r]);
-  red_m[y][x] = mx;
-  __syncthreads();
-  mx = -CUDART_INF_F;
-  for (int p = 0; p < ps; ++p)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, red_m[p * rg + ri][i]);
-  const float base = mx == -CUDART_INF_F ? 0.f : mx;
-  float l = 0.f, o[NC];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, ps = 16 / rg, ri = y % rg, pi = y / rg;
+  const int most = min(a.rows, a.T * a.g - rt * a.rows), v = blockIdx.z * rg + ri;
+  const int hi = v / most, r = v - hi * most, at = hi * a.rows + r;  // key head of the tile, row, place in the slot
+  const bool on = hi < a.hw;
+  float mx = -CUDART_INF_F, l = 0.f, o[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) o[i] = 0.f;
+  const bool late = first_item(sh, c0) < s0;  // the first of them began in another tile
   if (on) {
-#pragma unroll 4
-    for (int64_t c = c0 + pi; c <= c1; c += ps) {
-      const Part p = part_of(a, slot_of(c));
-      const float w = exp2f(p.m[r] - base);
-      l = fmaf(p.l[r], w, l);
+    constexpr int U = 4;
+    for (int c = c0 + pi; c <= c1; c += U * ps) {
+      float m[U], w[U], y4[U][NC];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) o[i] = fmaf(p.o[(int64_t)r * DH + x + 16 * i], w, o[i]);
+      for (int k = 0; k < U; ++k) {
+        const int cc = c + k * ps;
+        m[k] = -CUDART_INF_F;
+        w[k] = 0.f;
+        if (cc <= c1) {
+          const Part p = part_of(a, 2 * (int64_t)cc + (cc == c0 && late ? 1 : 0));
+          m[k] = p.m[at];
+          w[k] = p.l[at];
+          const float* src = p.o + (int64_t)at * DH + x * CV;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if constexpr (CV == 4) {
+              const float4 f = *reinterpret_cast<const float4*>(src + 64 * q);
+              y4[k][4 * q] = f.x, y4[k][4 * q + 1] = f.y, y4[k][4 * q + 2] = f.z, y4[k][4 * q + 3] = f.w;
+            } else {
+              const float2 f = *reinterpret_cast<const float2*>(src);
+              y4[k][0] = f.x, y4[k][1] = f.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NC; ++i) y4[k][i] = 0.f;
+        }
+      }
+      float now = mx;
+#pragma unroll
+      for (int k = 0; k < U; ++k) now = fmaxf(now, m[k]);
+      const float base = now == -CUDART_INF_F ? 0.f : now, f0 = exp2f(mx - base);
+      mx = now;
+      l *= f0;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) o[i] *= f0;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float f = exp2f(m[k] - base);
+        l = fmaf(w[k], f, l);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) o[i] = fmaf(y4[k][i], f, o[i]);
+      }
     }
   }
-  if (x == 0) red_l[y] = l;
+  if (x == 0) {
+    red_m[y] = mx;
+    red_l[y] = l;
+  }
 #pragma unroll
-  for (int i = 0; i < NC; ++i) red_o[y][x + 16 * i] = o[i];
+  for (int i = 0; i < NC; ++i) red_o[y][(i / CV) * 64 + x * CV + i % CV] = o[i];
   __syncthreads();
   if (pi != 0 || !on) return;
-  for (int p = 1; p < ps; ++p) {
-    l += red_l[p * rg + ri];
+  float top = mx;
+  for (int p = 1; p < ps; ++p) top = fmaxf(top, red_m[p * rg + ri]);
+  const float base = top == -CUDART_INF_F ? 0.f : top, f0 = exp2f(mx - base);
+  l *= f0;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) o[i] += red_o[p * rg + ri][x + 16 * i];
+  for (int i = 0; i < NC; ++i) o[i] *= f0;
+  for (int p = 1; p < ps; ++p) {
+    const float f = exp2f(red_m[p * rg + ri] - base);
+    l = fmaf(red_l[p * rg + ri], f, l);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) o[i] = fmaf(red_o[p * rg + ri][(i / CV) * 64 + x * CV + i % CV], f, o[i]);
   }
   int t, h;
-  row_of(a, rt * a.rows + r, m, t, h);
-  const int64_t at = ((int64_t)b * a.T + t) * a.H + h;
+  row_of(a, rt * a.rows + r, hg * a.hw + hi, t, h);
+  const int64_t to = ((int64_t)b * a.T + t) * a.H + h;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (x == 0) a.lse[at] = l == 0.f ? -CUDART_INF_F : mx * kLn2 + logf(l);
+  if (x == 0) a.lse[to] = l == 0.f ? -CUDART_INF_F : top * kTreeLn2 + logf(l);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) Elem<T>::st(reinterpret_cast<T*>(a.o) + at * DH + x + 16 * i, o[i] * inv);
+  for (int i = 0; i < NC; ++i) Elem<T>::st(reinterpret_cast<T*>(a.o) + to * DH + (i / CV) * 64 + x * CV + i % CV, o[i] * inv);
 }
 
 // ------------------------------------------------------------------ plan of a tree
@@ -361,56 +375,67 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 }
 
 // ------------------------------------------------------------------ launching
+enum Kind { kRows, kSimt };
 struct Shape {
-  int rows, grid, min_blocks;
+  Kind kind;
+  int hw, rows;    // key heads and rows of a tile
+  int grid;        // CTAs
+  int min_blocks;  // the fewest blocks worth a CTA of their own
 };
-// Rows of a tile, CTAs, and the fewest blocks worth a CTA of their own.
-Shape shape_of(int T, int g) {
+Shape shape_of(int T, int g, int Hkv, int dh, int bf16) {
   const int R = T * g;
-  const int rows = R <= 8 ? 8 : (R <= 16 ? 16 : 32);
-  return Shape{rows, kSMs * 2, 1};
+  if (bf16 && R <= 16) return Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, kSMs * (dh == 32 ? 3 : 2), 1};
+  return Shape{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), kSMs * 2, 1};
 }
 
 template <typename T, int DH, int RT>
 cudaError_t run_simt(const TreeArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem((const void*)tree_simt_kernel<T, DH, RT>, simt_smem<DH, RT>());
   if (e != cudaSuccess) return e;
-  launch_begin("tree_attn", s);
+  launch_begin("tree_simt", s);
   tree_simt_kernel<T, DH, RT><<<a.grid, kSimtThreads, simt_smem<DH, RT>(), s>>>(a);
-  return launch_end("tree_attn", s);
+  return launch_end("tree_simt", s);
 }
 template <typename T, int DH>
-cudaError_t run_dh(const TreeArgs& a, cudaStream_t s) {
-  cudaError_t e = a.rows == 8 ? run_simt<T, DH, 1>(a, s) : (a.rows == 16 ? run_simt<T, DH, 2>(a, s) : run_simt<T, DH, 4>(a, s));
+cudaError_t run_dh(const TreeArgs& a, Kind kind, cudaStream_t s) {
+  cudaError_t e;
+  if (kind == kRows) e = launch_tree_rows(a, s);
+  else e = a.rows == 8 ? run_simt<T, DH, 1>(a, s) : (a.rows == 16 ? run_simt<T, DH, 2>(a, s) : run_simt<T, DH, 4>(a, s));
   if (e != cudaSuccess) return e;
-  const int most = std::min(a.rows, a.T * a.g);
-  const int rg = most >= 8 ? 8 : (most >= 4 ? 4 : (most >= 2 ? 2 : 1));
+  // Rows of a CTA: as many as leave a thread about four partials to walk (a tile has about
+  // grid / tiles of them), and no more than there are.
+  const int rows = a.hw * std::min(a.rows, a.T * a.g), tiles = a.Hkv / a.hw * a.nrt;
+  const int64_t parts = a.grid / ((int64_t)tiles * a.B) + 1;
+  int rg = 8;
+  while (rg > 1 && (rg > rows || parts * rg > 64)) rg >>= 1;
   launch_begin("tree_join", s);
-  tree_join_kernel<T, DH><<<dim3(a.Hkv * a.nrt, a.B, (most + rg - 1) / rg), kJoinThreads, 0, s>>>(a, rg);
+  tree_join_kernel<T, DH><<<dim3(tiles, a.B, (rows + rg - 1) / rg), kJoinThreads, 0, s>>>(a, rg);
   return launch_end("tree_join", s);
 }
 template <typename T>
-cudaError_t run(const TreeArgs& a, cudaStream_t s) {
-  if (a.dh == 32) return run_dh<T, 32>(a, s);
-  if (a.dh == 64) return run_dh<T, 64>(a, s);
-  return run_dh<T, 128>(a, s);
+cudaError_t run(const TreeArgs& a, Kind kind, cudaStream_t s) {
+  if (a.dh == 32) return run_dh<T, 32>(a, kind, s);
+  if (a.dh == 64) return run_dh<T, 64>(a, kind, s);
+  return run_dh<T, 128>(a, kind, s);
 }
 
 }  // namespace
 
 size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16) {
-  const Shape sh = shape_of(T, H / Hkv);
-  return (size_t)2 * sh.grid * sh.rows * (dh + 2) * 4;
+  const Shape sh = shape_of(T, H / Hkv, Hkv, dh, bf16);
+  return (size_t)2 * sh.grid * sh.hw * sh.rows * (dh + 2) * 4;
 }
 
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
-  const Shape sh = shape_of(a.T, a.g);
+  const Shape sh = shape_of(a.T, a.g, a.Hkv, a.dh, a.bf16);
+  a.hw = sh.hw;
   a.rows = sh.rows;
   a.grid = sh.grid;
   a.min_blocks = sh.min_blocks;
   a.nrt = (a.T * a.g + a.rows - 1) / a.rows;
   a.nd = (a.T + kChunk - 1) / kChunk;
-  return a.bf16 ? run<bf16>(a, s) : run<float>(a, s);
+  a.wide = (reinterpret_cast<uintptr_t>(a.kp) | reinterpret_cast<uintptr_t>(a.vp)) % 32 == 0;
+  return a.bf16 ? run<bf16>(a, sh.kind, s) : run<float>(a, sh.kind, s);
 }
 
 cudaError_t launch_tree_plan(const TreePlanArgs& a, cudaStream_t s) {

@@ -1,10 +1,10 @@
 // How the attention of drafted tokens over a paged cache is divided among its CTAs.
 //
-// A tile is (sequence b, key head m, row group): up to `rows` of the T * g query rows that
-// share key head m (row r = token r / g, query head m g + r % g).  Its keys are blocks of
-// 64: the pages of the context that some row can see, then the draft's own tokens.  All
-// tiles' blocks, laid end to end, are one list of W items; CTA c of G takes the items
-// [c W / G, (c + 1) W / G), whatever sequences they belong to, so a batch of one long and
+// A tile is (sequence b, `hw` key heads side by side, row group): of each key head m up to
+// `rows` of the T * g query rows that share it (row r = token r / g, query head m g + r % g).
+// Its keys are blocks of 64: the pages of the context that some row can see, then the draft's own tokens.  All
+// tiles' blocks, laid end to end, are one list of W items, of which each of G CTAs takes W / G
+// in a row (one more or less), whatever sequences they belong to, so a batch of one long and
 // many short sequences divides as evenly as a single sequence.  The lengths are read on
 // the device: a captured graph follows them.
 //
@@ -41,53 +41,79 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const TreeArgs& a, int b, bool f
 }
 
 struct Share {
-  int b;          // sequence that item `lo` lies in
-  int64_t off;    // its offset among that sequence's items
-  int64_t lo, hi; // this CTA's items
-  int64_t W;      // all items
-  int64_t G;      // CTAs that have work
+  int W, G;      // all items, CTAs that have work
+  int q, rem;    // W = q G + rem: the first rem CTAs take q + 1 items, the others q
+  int lo, hi;    // this CTA's items
+  int b, off;    // the sequence that item lo lies in, and its offset among that sequence's items
 };
+__device__ __forceinline__ int first_item(const Share& s, int cta) { return s.q * cta + min(cta, s.rem); }
+__device__ __forceinline__ int owner_of(const Share& s, int item) {
+  const int t = s.rem * (s.q + 1);
+  return item < t ? item / (s.q + 1) : s.rem + (item - t) / s.q;
+}
 
-// Called by all `NT` threads of a CTA; `buf` holds NT / 32 + 1 values.  With `find` >= 0 the
-// item of a given sequence's start is returned in `lo` instead of this CTA's share.
-template <int NT>
-__device__ __forceinline__ Share share_of(const TreeArgs& a, int cta, int find, int64_t* buf, Share* out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.B + NT - 1) / NT, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  const int64_t tiles = (int64_t)a.Hkv * a.nrt;
-  int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_blocks(a, b, cta == 0).nb * tiles;
-  int64_t incl = sum;
+// Items of the sequences before b (or of all of them), summed by one warp.  (The host sees to
+// it that all items together stay below 2^31.)
+__device__ __forceinline__ int items_before(const TreeArgs& a, int b, bool flag) {
+  int sum = 0;
+  for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_blocks(a, i, flag).nb;
+  return __reduce_add_sync(0xffffffffu, sum) * (a.Hkv / a.hw * a.nrt);
+}
+__device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
+  Share s;
+  s.W = W;
+  s.G = min(a.grid, max(1, W / a.min_blocks));
+  s.q = W / s.G;
+  s.rem = W - s.q * s.G;
+  return s;
+}
+
+// The share of a CTA; called by whole warps, each for itself.
+__device__ __forceinline__ Share share_of(const TreeArgs& a, int cta) {
+  const int lane = threadIdx.x & 31, tiles = a.Hkv / a.hw * a.nrt;
+  Share s = shares(a, items_before(a, a.B, cta == 0 && threadIdx.x < 32));
+  s.lo = cta < s.G ? first_item(s, cta) : s.W;
+  s.hi = cta < s.G ? first_item(s, cta + 1) : s.W;
+  s.b = s.off = 0;
+  if (s.lo >= s.hi) return s;
+  for (int b0 = 0, at = 0;; b0 += 32) {
+    const int n = b0 + lane < a.B ? seq_blocks(a, b0 + lane, false).nb * tiles : 0;
+    int incl = n;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) buf[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, W = 0;
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w == warp) before = W;
-    W += buf[w];
-  }
-  const int64_t excl = before + incl - sum;
-  const int64_t G = min((int64_t)a.grid, max((int64_t)1, (W + a.min_blocks - 1) / a.min_blocks));
-  const int64_t lo = find >= 0 ? 0 : (cta < G ? W * cta / G : W);
-  const int64_t hi = find >= 0 ? 0 : (cta < G ? W * (cta + 1) / G : W);
-  if (find >= 0 ? (find >= b0 && find < b1) : (lo >= excl && lo < excl + sum)) {
-    int64_t at = excl;
-    int b = b0;
-    for (;; ++b) {
-      const int64_t n = seq_blocks(a, b, false).nb * tiles;
-      if (find >= 0 ? b == find : lo < at + n) break;
-      at += n;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
     }
-    *out = find >= 0 ? Share{b, 0, at, 0, W, G} : Share{b, lo - at, lo, hi, W, G};
-  } else if (find < 0 && lo >= W && tid == 0) {
-    *out = Share{0, 0, lo, hi, W, G};
+    const uint32_t in = __ballot_sync(0xffffffffu, n > 0 && s.lo < at + incl);
+    if (in) {
+      const int l = __ffs(in) - 1;
+      s.b = b0 + l;
+      s.off = s.lo - at - __shfl_sync(0xffffffffu, incl - n, l);
+      return s;
+    }
+    at += __shfl_sync(0xffffffffu, incl, 31);
+    if (b0 + 32 >= a.B) return s;
   }
-  __syncthreads();
-  return *out;
+}
+
+constexpr float kTreeLog2e = 1.4426950408889634f;
+constexpr float kTreeLn2 = 0.6931471805599453f;
+
+// Partial results.
+// Slot s: [hw rows] maxima (of log2 e times the scaled logits), as many sums, [hw rows][dh] outputs.
+struct Part {
+  float* m; float* l; float* o;
+};
+__device__ __forceinline__ Part part_of(const TreeArgs& a, int64_t slot) {
+  const int n = a.hw * a.rows;
+  float* p = reinterpret_cast<float*>(a.part) + slot * n * (a.dh + 2);
+  return Part{p, p + n, p + 2 * n};
+}
+
+// Where row r of a tile goes: token t, query head h.
+__device__ __forceinline__ void row_of(const TreeArgs& a, int r, int m, int& t, int& h) {
+  t = r / a.g;
+  h = m * a.g + (r - t * a.g);
 }
 
 // Whether key u of the draft is seen by row t (mask words, or the causal chain), before the window.

@@ -10,7 +10,6 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (runs the kernels)")
-    config.addinivalue_line("markers", "flags: leaves the error word to the test")
 
 
 def pytest_collection_modifyitems(config, items):

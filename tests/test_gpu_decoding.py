@@ -28,8 +28,14 @@ def _g():
 @pytest.fixture(autouse=True)
 def _clean_error_word(request):
     yield
-    if request.node.get_closest_marker("flags") is None:
+    if not getattr(request.function, "flags", False):
         _g().cache_workspace("cuda").check()
+
+
+def flags(test):
+    """A test that sets the error word and reads it itself."""
+    test.flags = True
+    return test
 
 
 def ints(x):
@@ -162,7 +168,7 @@ def test_tree_plan_against_oracle(T):
     assert np.array_equal(mask.cpu().numpy(), orc.pack_mask(np.stack([w[0] for w in want])))
 
 
-@pytest.mark.flags
+@flags
 def test_tree_plan_flags_bad_parents():
     g = _g()
     mask, pos = g.tree_plan(ints([[-1, 0, 2, 1, -5, 3]]), ints([7]))  # tokens 2 and 4 are not trees
@@ -318,7 +324,7 @@ def test_tree_attention_large_logits():
         within(host(o), ro, (np.expm1(2 * dw) + HALF["bf16"])[..., None] * mean_abs * 1.01 + 2 * HALF["bf16"] * np.abs(ro), "o")
 
 
-@pytest.mark.flags
+@flags
 def test_tree_attention_flags_bad_pages_and_lengths():
     """A page number outside the pool is left out like a page that is not held, and flagged;
     so is a length that the table has no room for, which is read as the table's width."""
@@ -511,7 +517,7 @@ def test_append_copies_a_shared_last_page():
         same_state(cache, model)
 
 
-@pytest.mark.flags
+@flags
 @pytest.mark.parametrize("pages", [10, 11, 12, 13, 14, 20])
 def test_append_without_room(pages):
     """Entries are served in order until the free pages run out; one that the table has no room
@@ -529,7 +535,7 @@ def test_append_without_room(pages):
     assert e.value.status == g.GCA_ERR_CACHE_FULL
 
 
-@pytest.mark.flags
+@flags
 def test_append_flags_bad_entries():
     g = _g()
     cache, model = cache_pair(np.random.default_rng(3), [10, 20, 30, 64], 4, 20)
@@ -565,7 +571,7 @@ def test_fork_trim_free():
     assert not model.refs.any()
 
 
-@pytest.mark.flags
+@flags
 def test_fork_and_trim_flag_bad_entries():
     g = _g()
     cache, model = cache_pair(np.random.default_rng(5), [100, 0, 0, 70, 0], 4, 30)
@@ -657,7 +663,7 @@ def test_lookup_feeds_gca():
     assert torch.equal(got, want)
 
 
-@pytest.mark.flags
+@flags
 def test_lookup_flags():
     g = _g()
     cache, _ = cache_pair(np.random.default_rng(0), [100, 70], 4, 8)
