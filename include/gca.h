@@ -527,7 +527,7 @@ GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, cons
  * and lse = -inf.  A page number outside [0, pages) is left out (flagged unless it is -1).
  *
  *   q [B][T][H][dh], k_new, v_new [B][T][heads][dh]: free strides, 16-byte aligned, strides
- *           multiples of 16 bytes.  B <= cache->slots: sequence b is slot b.
+ *           multiples of 16 bytes (0 repeats a sequence or a head; in k_new, v_new not a token).  B <= cache->slots: sequence b is slot b.
  *   mask    [B][T][ceil(T/64)] uint64: bit u % 64 of word u / 64 of row t: t sees u.  NULL: t
  *           sees the tokens u <= t.  Tokens that no row sees are not used in any way.
  *   positions [B][T] int32: -1 for padding (seen by none and seeing none), else the token's

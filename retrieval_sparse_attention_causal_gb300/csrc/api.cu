@@ -852,8 +852,10 @@ extern "C" gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_
   if (window < 0) return fail(GCA_ERR_INVALID_ARG, "window must be >= 0");
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(GCA_ERR_INVALID_ARG, "scale must be finite and > 0");
   if (mask && (reinterpret_cast<uintptr_t>(mask) & 7)) return fail(GCA_ERR_INVALID_ARG, "mask must be 8-byte aligned");
-  // Blocks of 64 keys, times the tiles of at least 8 rows that walk them.
-  if ((double)B * H * ((T + 7) / 8) * ((double)cache->width + 4) > INT32_MAX)
+  if ((T > 1 && k_new->token_stride == 0) || (T > 1 && v_new->token_stride == 0))
+    return fail(GCA_ERR_UNSUPPORTED, "k_new and v_new may not repeat one token (token stride 0)");
+  // All blocks of 64 keys are numbered in 32 bits.
+  if ((double)B * cache->heads * ((double)cache->width + 4) > INT32_MAX)
     return fail(GCA_ERR_UNSUPPORTED, "B, H, T and the table's width are too large together");
   if (!o || !lse || !aligned16(o)) return fail(GCA_ERR_INVALID_ARG, "o and lse must not be NULL, o 16-byte aligned");
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;

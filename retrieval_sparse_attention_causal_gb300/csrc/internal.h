@@ -39,6 +39,11 @@ cudaError_t make_chunk_token_tmap(CUtensorMap* out, const void* base, int64_t co
 // batch stride 0 = one table for every sequence) as boxes of 64 dims x box_rows rows.
 cudaError_t make_lmk_tmap(CUtensorMap* out, const void* base, int64_t D, int64_t rows, int64_t batches,
                           int64_t row_stride, int64_t batch_stride, int box_rows);
+// Pages [pages][64][heads][dh] bf16 as boxes of 64 elements of one head of a page's 64 tokens, and
+// rows [batches][tokens][heads][dh] with free strides as boxes of 64 tokens, 128-byte swizzled (tmap.cu).
+cudaError_t make_pages_tmap(CUtensorMap* out, const void* base, int dh, int heads, int64_t pages);
+cudaError_t make_draft_tmap(CUtensorMap* out, const void* base, int dh, int heads, int tokens, int batches,
+                            int64_t head_stride, int64_t token_stride, int64_t batch_stride);
 // The same matrix as a TMA store target: 32 x 32 boxes, 64-byte swizzle (tmap.cu).
 cudaError_t make_store_tmap(CUtensorMap* out, const void* base, int64_t cols, int64_t rows);
 
@@ -198,11 +203,12 @@ struct TreeArgs {
   float scale;
   ErrWord* err;
   unsigned char* part;                                     // partial results
-  int hw, rows, nrt, nd;                                   // key heads and rows of a tile, tiles of T g rows, blocks of the draft
-  int grid, min_blocks;                            // CTAs, and the fewest blocks worth a CTA
+  int hw, rows, nrt, nd;                                   // key heads of a tile, rows of a CTA, groups of rows, blocks of the draft
+  int grid;                                                // shares of the work, at most
   int wide;                                                // pools on 32-byte boundaries
 };
-cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);  // bf16, T g <= 16 (tree_rows.cu)
+cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);  // bf16, 16 rows a CTA (tree_rows.cu)
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t s);    // bf16, dh 64 or 128 (tree_tc.cu)
 size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16);
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s);
 struct TreePlanArgs {

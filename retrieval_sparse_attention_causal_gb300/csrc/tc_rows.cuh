@@ -56,6 +56,13 @@ __device__ __forceinline__ void st32x32b_x8(uint32_t taddr, const uint32_t (&v)[
                : "memory");
 }
 
+// 4 consecutive 32-bit columns of the thread's lane.
+__device__ __forceinline__ void st32x32b_x4(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
+
 // TMA tile load of a 2-D tensor map (x innermost; x times the element size must be a
 // multiple of 16 bytes), completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {

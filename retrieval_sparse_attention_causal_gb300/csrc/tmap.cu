@@ -93,6 +93,41 @@ cudaError_t make_lmk_tmap(CUtensorMap* out, const void* base, int64_t D, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_pages_tmap(CUtensorMap* out, const void* base, int dh, int heads, int64_t pages) {
+  std::call_once(g_once, load_encode);
+  if (g_encode_err != cudaSuccess) return g_encode_err;
+  // dims innermost first: element, head, token of the page, page.  The box is 64 elements (one
+  // swizzle span) of one head of a page's 64 tokens; a page number behind the pool reads zeros.
+  cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)heads, 64, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {(cuuint64_t)dh * 2, (cuuint64_t)heads * dh * 2, (cuuint64_t)heads * dh * 2 * 64};
+  cuuint32_t box[4] = {64, 1, 64, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_draft_tmap(CUtensorMap* out, const void* base, int dh, int heads, int tokens, int batches,
+                            int64_t head_stride, int64_t token_stride, int64_t batch_stride) {
+  std::call_once(g_once, load_encode);
+  if (g_encode_err != cudaSuccess) return g_encode_err;
+  // dims innermost first: element, head, token, sequence, with free strides (in elements).  An
+  // axis of stride 0 repeats one entry: it becomes an axis of one, read at coordinate 0 (its
+  // stride in the map is then any valid one).  Tokens past the end read zeros.
+  const int64_t any = (int64_t)heads * dh;
+  cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)(head_stride ? heads : 1), (cuuint64_t)(token_stride ? tokens : 1),
+                        (cuuint64_t)(batch_stride ? batches : 1)};
+  cuuint64_t strides[3] = {(cuuint64_t)(head_stride ? head_stride : any) * 2, (cuuint64_t)(token_stride ? token_stride : any) * 2,
+                           (cuuint64_t)(batch_stride ? batch_stride : any) * 2};
+  cuuint32_t box[4] = {64, 1, 64, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_store_tmap(CUtensorMap* out, const void* base, int64_t cols, int64_t rows) {
   std::call_once(g_once, load_encode);
   if (g_encode_err != cudaSuccess) return g_encode_err;

@@ -18,16 +18,16 @@ namespace gca {
 namespace {
 
 using bf16 = __nv_bfloat16;
-// ------------------------------------------------------------------ CUDA-core kernel
+// ------------------------------------------------------------------ CUDA-core kernel (float32)
 // 128 threads; thread (ty, tx) owns rows ty RT .. ty RT + RT - 1, of a block's logits the
-// keys tx + 16 j, and of the output DH / 16 columns.  K and V pass through shared memory
-// in 32 bits.
+// keys tx + 16 j, and of the output DH / 16 columns.  K and V pass through shared memory.
 constexpr int kSimtThreads = 128;
 template <int DH, int RT>
 constexpr int simt_smem() { return (8 * RT * (DH + 4) + 2 * 64 * (DH + 4) + 8 * RT * 68) * 4; }
 
-template <typename T, int DH, int RT>
+template <int DH, int RT>
 __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
+  using T = float;
   constexpr int MT = 8 * RT, QS = DH + 4, CV = DH >= 64 ? 4 : 2, NC = DH / 16 / CV;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -37,21 +37,21 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
   __shared__ int row_pos[MT];
   __shared__ unsigned long long used_s;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const Share sh = share_of(a, blockIdx.x);
+  const Share sh = my_share(a);
   const float sl2 = a.scale * kTreeLog2e;
-  const int R = a.T * a.g;
+  const int R = a.T * a.g, rt = blockIdx.x % a.nrt;
   int b = sh.b;
   int off = sh.off, item = sh.lo;
   SeqBlocks sb = sh.lo < sh.hi ? seq_blocks(a, b, false) : SeqBlocks{};
   int slot = 0;
   while (item < sh.hi) {
     const int tile = off / sb.nb;
-    if (tile >= a.Hkv * a.nrt) {
+    if (tile >= a.Hkv) {
       sb = seq_blocks(a, ++b, false);
       off = 0;
       continue;
     }
-    const int m = tile / a.nrt, rt = tile - m * a.nrt;
+    const int m = tile;
     const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     const int rows = min(MT, R - rt * MT);
     __syncthreads();
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
       }
     }
     const bool whole = blk0 == 0 && blk1 == sb.nb;
-    const Part part = part_of(a, 2 * (int64_t)blockIdx.x + slot);
+    const Part part = part_of(a, blockIdx.x / a.nrt, rt, slot);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int r = ty * RT + i;
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, int
   const int b = blockIdx.y, tile = blockIdx.x, hg = tile / a.nrt, rt = tile % a.nrt;
   const Share sh = shares(a, items_before(a, a.B, false));
   const SeqBlocks sb = seq_blocks(a, b, false);
-  const int s0 = items_before(a, b, false) + tile * sb.nb;
-  const int c0 = owner_of(sh, s0), c1 = owner_of(sh, s0 + sb.nb - 1);  // CTAs of its first and last block
+  const int s0 = items_before(a, b, false) + hg * sb.nb;
+  const int c0 = owner_of(sh, s0), c1 = owner_of(sh, s0 + sb.nb - 1);  // shares of its first and last block
   if (c0 == c1) return;  // finished there
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4, ps = 16 / rg, ri = y % rg, pi = y / rg;
   const int most = min(a.rows, a.T * a.g - rt * a.rows), v = blockIdx.z * rg + ri;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, int
         m[k] = -CUDART_INF_F;
         w[k] = 0.f;
         if (cc <= c1) {
-          const Part p = part_of(a, 2 * (int64_t)cc + (cc == c0 && late ? 1 : 0));
+          const Part p = part_of(a, cc, rt, cc == c0 && late ? 1 : 0);
           m[k] = p.m[at];
           w[k] = p.l[at];
           const float* src = p.o + (int64_t)at * DH + x * CV;
@@ -375,32 +375,35 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 }
 
 // ------------------------------------------------------------------ launching
-enum Kind { kRows, kSimt };
+enum Kind { kRows, kTensor, kSimt };
 struct Shape {
   Kind kind;
-  int hw, rows;    // key heads and rows of a tile
-  int grid;        // CTAs
-  int min_blocks;  // the fewest blocks worth a CTA of their own
+  int hw, rows, nrt;  // key heads of a tile, rows of a CTA, groups of rows
+  int ctas;           // on the GPU at once
 };
 Shape shape_of(int T, int g, int Hkv, int dh, int bf16) {
   const int R = T * g;
-  if (bf16 && R <= 16) return Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, kSMs * (dh == 32 ? 3 : 2), 1};
-  return Shape{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), kSMs * 2, 1};
+  Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, 2 * kSMs};
+  if (bf16 && (R <= 16 || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
+  else if (bf16) s = Shape{kTensor, 1, 128, 1, 2 * kSMs};
+  s.nrt = (R + s.rows - 1) / s.rows;
+  return s;
 }
+int shares_of(const Shape& s) { return std::max(1, s.ctas / s.nrt); }
 
-template <typename T, int DH, int RT>
+template <int DH, int RT>
 cudaError_t run_simt(const TreeArgs& a, cudaStream_t s) {
-  cudaError_t e = allow_smem((const void*)tree_simt_kernel<T, DH, RT>, simt_smem<DH, RT>());
+  cudaError_t e = allow_smem((const void*)tree_simt_kernel<DH, RT>, simt_smem<DH, RT>());
   if (e != cudaSuccess) return e;
   launch_begin("tree_simt", s);
-  tree_simt_kernel<T, DH, RT><<<a.grid, kSimtThreads, simt_smem<DH, RT>(), s>>>(a);
+  tree_simt_kernel<DH, RT><<<a.grid * a.nrt, kSimtThreads, simt_smem<DH, RT>(), s>>>(a);
   return launch_end("tree_simt", s);
 }
 template <typename T, int DH>
 cudaError_t run_dh(const TreeArgs& a, Kind kind, cudaStream_t s) {
   cudaError_t e;
-  if (kind == kRows) e = launch_tree_rows(a, s);
-  else e = a.rows == 8 ? run_simt<T, DH, 1>(a, s) : (a.rows == 16 ? run_simt<T, DH, 2>(a, s) : run_simt<T, DH, 4>(a, s));
+  if constexpr (sizeof(T) == 2) e = kind == kRows ? launch_tree_rows(a, s) : launch_tree_tc(a, s);
+  else e = a.rows == 8 ? run_simt<DH, 1>(a, s) : (a.rows == 16 ? run_simt<DH, 2>(a, s) : run_simt<DH, 4>(a, s));
   if (e != cudaSuccess) return e;
   // Rows of a CTA: as many as leave a thread about four partials to walk (a tile has about
   // grid / tiles of them), and no more than there are.
@@ -423,16 +426,15 @@ cudaError_t run(const TreeArgs& a, Kind kind, cudaStream_t s) {
 
 size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16) {
   const Shape sh = shape_of(T, H / Hkv, Hkv, dh, bf16);
-  return (size_t)2 * sh.grid * sh.hw * sh.rows * (dh + 2) * 4;
+  return (size_t)2 * shares_of(sh) * sh.nrt * sh.hw * sh.rows * (dh + 2) * 4;
 }
 
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
   const Shape sh = shape_of(a.T, a.g, a.Hkv, a.dh, a.bf16);
   a.hw = sh.hw;
   a.rows = sh.rows;
-  a.grid = sh.grid;
-  a.min_blocks = sh.min_blocks;
-  a.nrt = (a.T * a.g + a.rows - 1) / a.rows;
+  a.grid = shares_of(sh);
+  a.nrt = sh.nrt;
   a.nd = (a.T + kChunk - 1) / kChunk;
   a.wide = (reinterpret_cast<uintptr_t>(a.kp) | reinterpret_cast<uintptr_t>(a.vp)) % 32 == 0;
   return a.bf16 ? run<bf16>(a, sh.kind, s) : run<float>(a, sh.kind, s);

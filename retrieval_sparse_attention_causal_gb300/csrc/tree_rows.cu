@@ -1,5 +1,5 @@
 // Attention of drafted tokens over a paged cache where few query rows share a key head
-// (T g <= 16: single tokens, short drafts), bf16, without shared memory on the way.
+// (T g <= 16: single tokens, short drafts; and all drafts of heads of 32), bf16, without shared memory on the way.
 //
 // Bound by memory: 16 rows ask 16 operations of each byte of K and V, a twentieth of what
 // the tensor pipes of mma.sync give.  So the keys and values go straight from global memory
@@ -119,10 +119,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
   static_assert(kWarps * G::KS * 32 * sizeof(uint4) <= sizeof both, "");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, c = lane & 3;
-  const Share sh = share_of(a, blockIdx.x);
+  const Share sh = my_share(a);
   if (sh.lo >= sh.hi) return;
   const float sl2 = a.scale * kTreeLog2e;
-  const int R = a.T * a.g;
+  const int rt = blockIdx.x % a.nrt, R = a.T * a.g - 16 * rt;  // rows from this CTA's first on
   int b = sh.b;
   int off = sh.off, item = sh.lo;
   SeqBlocks sb = seq_blocks(a, b, false);
@@ -138,21 +138,19 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
     const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     // Q fragments, and the two rows' positions and masks.
     uint32_t qf[G::KS][4];
-    int pos[2];
-    uint64_t see[2];
+    int pos[2], tok[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = n + 8 * i;
       uint32_t w[DH / 8] = {};
       pos[i] = -1;
-      see[i] = 0;
+      tok[i] = 0;
       if (r < R) {
         int t, h;
-        row_of(a, r, m, t, h);
+        row_of(a, 16 * rt + r, m, t, h);
         load_key_row<DH>(w, reinterpret_cast<const bf16*>(a.q) + b * a.q_bs + t * a.q_ts + h * a.q_hs, c, false);
         pos[i] = (int)token_position(a, b, t, sb.len);
-        see[i] = a.mask ? a.mask[((int64_t)b * a.T + t) * a.words] : (2ull << t) - 1;
-        if (pos[i] < 0) see[i] = 0;
+        tok[i] = t;
       }
 #pragma unroll
       for (int ks = 0; ks < G::KS; ++ks) {
@@ -165,15 +163,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
       for (int ks = 0; ks < G::KS; ++ks) q_s[warp][ks][lane] = make_uint4(qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3]);
     __syncthreads();
     int far = max(pos[0], pos[1]);
-    unsigned long long used = see[0] | see[1];  // draft tokens that some row sees (T <= 16 here)
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-      far = max(far, __shfl_xor_sync(kAll, far, d));
-      used |= __shfl_xor_sync(kAll, used, d);
-    }
-    if (a.positions)
-      for (int u = 0; u < a.T; ++u)
-        if (a.positions[(int64_t)b * a.T + u] < 0) used &= ~(1ull << u);
+    for (int d = 4; d < 32; d <<= 1) far = max(far, __shfl_xor_sync(kAll, far, d));
 
     float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f}, o[NV][4];
 #pragma unroll
@@ -241,31 +232,55 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
     };
     auto weigh = [&](UnitData<DH>& d, float (&s)[G::NB][4], const UnitAt& u) {
       if (!u.ctx || u.lo > 0 || u.hi < G::KB || (a.window > 0 && u.j0 <= far - a.window)) {
+        // Bit k of see[i]: row i of this thread sees key k; of used: some row of the CTA may.
+        uint64_t see[2], used;
+        const uint64_t there = (u.hi >= 64 ? ~0ull : (1ull << max(u.hi, 0)) - 1) & ~((u.lo >= 64 ? 0ull : 1ull << u.lo) - 1);
+        if (u.ctx) {
+          used = u.lo >= 64 ? 0ull : there;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int gone = a.window > 0 ? pos[i] - a.window + 1 - u.j0 : 0;  // keys that the window has passed
+            see[i] = gone >= 64 ? 0ull : used & ~((1ull << max(gone, 0)) - 1);
+          }
+        } else {
+          uint64_t real = ~0ull;  // tokens that are not padding
+          if (a.positions) {
+            const int32_t* p = a.positions + (int64_t)b * a.T;
+            const uint32_t p0 = __ballot_sync(kAll, p[min(u.j0 + lane, a.T - 1)] >= 0);
+            const uint32_t p1 = G::KB > 32 ? __ballot_sync(kAll, p[min(u.j0 + 32 + lane, a.T - 1)] >= 0) : 0;
+            real = ((uint64_t)p1 << 32) | p0;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            see[i] = 0;
+            if (pos[i] < 0) continue;
+            const int past = tok[i] - u.j0;  // tokens of the unit before this row's own
+            see[i] = a.mask ? a.mask[((int64_t)b * a.T + tok[i]) * a.words + (u.j0 >> 6)] >> (u.j0 & 63)
+                            : (past >= 63 ? ~0ull : (past < 0 ? 0ull : (2ull << past) - 1));
+            see[i] &= there & real;
+          }
+          used = see[0] | see[1];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) used |= __shfl_xor_sync(kAll, used, d);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (a.window > 0 && pos[i] - a.window >= sb.len)  // the window ends inside the draft
+              for (int k = 0; k < G::KB; ++k)
+                if ((see[i] >> k) & 1 && token_position(a, b, u.j0 + k, sb.len) <= (int64_t)pos[i] - a.window) see[i] &= ~(1ull << k);
+        }
 #pragma unroll
         for (int j = 0; j < G::NB; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = 8 * j + 2 * c + (e & 1), i = e >> 1;
-            bool on = key >= u.lo && key < u.hi;
-            if (u.ctx) {
-              on = on && (a.window <= 0 || u.j0 + key > pos[i] - a.window);
-            } else if (on) {
-              const int t = u.j0 + key;
-              on = ((see[i] & used) >> t) & 1;
-              if (on && a.window > 0) on = token_position(a, b, t, sb.len) > (int64_t)pos[i] - a.window;
-            }
-            if (!on) s[j][e] = -CUDART_INF_F;
-          }
+          for (int e = 0; e < 4; ++e)
+            if (!((see[e >> 1] >> (8 * j + 2 * c + (e & 1))) & 1)) s[j][e] = -CUDART_INF_F;
         // What nobody sees is zeros: a weight of 0 times what lies there must stay 0.
 #pragma unroll
         for (int t = 0; t < G::ST; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = 16 * t + 2 * c + (e & 1) + 8 * (e >> 1);
-            if (key < u.lo || key >= u.hi || (!u.ctx && !((used >> (u.j0 + key)) & 1)))
+          for (int e = 0; e < 4; ++e)
+            if (!((used >> (16 * t + 2 * c + (e & 1) + 8 * (e >> 1))) & 1))
 #pragma unroll
               for (int w = 0; w < G::VW; ++w) d.v[t][e][w] = 0;
-          }
       }
       float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -378,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
       if (r >= R) continue;
       if (blk0 == 0 && blk1 == sb.nb) {
         int t, h;
-        row_of(a, r, m, t, h);
+        row_of(a, 16 * rt + r, m, t, h);
         const int64_t at = ((int64_t)b * a.T + t) * a.H + h;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (d0 == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : top * kTreeLn2 + logf(sum);
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
 #pragma unroll
         for (int e = 0; e < NV / 2; e += 2) *reinterpret_cast<uint2*>(to + e) = make_uint2(w[e], w[e + 1]);
       } else {
-        const Part part = part_of(a, 2 * (int64_t)blockIdx.x + slot);
+        const Part part = part_of(a, blockIdx.x / a.nrt, rt, slot);
         const int at = i * a.rows + r;
         if (d0 == 0) {
           part.m[at] = top;
@@ -411,9 +426,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
 
 cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s) {
   launch_begin("tree_rows", s);
-  if (a.dh == 32) tree_rows_kernel<32><<<a.grid, kThreads, 0, s>>>(a);
-  else if (a.dh == 64) tree_rows_kernel<64><<<a.grid, kThreads, 0, s>>>(a);
-  else tree_rows_kernel<128><<<a.grid, kThreads, 0, s>>>(a);
+  if (a.dh == 32) tree_rows_kernel<32><<<a.grid * a.nrt, kThreads, 0, s>>>(a);
+  else if (a.dh == 64) tree_rows_kernel<64><<<a.grid * a.nrt, kThreads, 0, s>>>(a);
+  else tree_rows_kernel<128><<<a.grid * a.nrt, kThreads, 0, s>>>(a);
   return launch_end("tree_rows", s);
 }
 

@@ -1,17 +1,20 @@
 // How the attention of drafted tokens over a paged cache is divided among its CTAs.
 //
-// A tile is (sequence b, `hw` key heads side by side, row group): of each key head m up to
-// `rows` of the T * g query rows that share it (row r = token r / g, query head m g + r % g).
-// Its keys are blocks of 64: the pages of the context that some row can see, then the draft's own tokens.  All
-// tiles' blocks, laid end to end, are one list of W items, of which each of G CTAs takes W / G
-// in a row (one more or less), whatever sequences they belong to, so a batch of one long and
-// many short sequences divides as evenly as a single sequence.  The lengths are read on
-// the device: a captured graph follows them.
+// A tile is (sequence b, `hw` key heads side by side).  Its keys are blocks of 64: the pages of
+// the context that some row can see, then the draft's own tokens.  All tiles' blocks, laid
+// end to end, are one list of W items, cut into G shares of W / G in a row (one more or
+// less), whatever sequences they belong to, so a batch of one long and many short sequences
+// divides as evenly as a single sequence.  The lengths are read on the device: a captured
+// graph follows them.
 //
-// A tile that lies in one CTA's items is finished there.  Of the others each CTA writes a
-// partial result (row maximum, row sum, unnormalised output): the tile that it begins in
-// to slot 2c, the one that it ends in to slot 2c + 1; the joining kernel finds a tile's
-// partials by the same arithmetic.
+// Of each key head m, T * g query rows share the keys (row r = token r / g, query head
+// m g + r % g), in `nrt` groups of `rows`.  Share c has a CTA for each group: they walk the same
+// pages at the same time, and all but the first find them in L2.
+//
+// A tile that lies in one share is finished there.  Of the others each CTA writes a partial
+// result (row maximum, row sum, unnormalised output): the tile that its share begins in to
+// the first of its two slots, the one that it ends in to the second; the joining kernel finds
+// a tile's partials by the same arithmetic.
 #pragma once
 
 #include "common.cuh"
@@ -41,12 +44,12 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const TreeArgs& a, int b, bool f
 }
 
 struct Share {
-  int W, G;      // all items, CTAs that have work
-  int q, rem;    // W = q G + rem: the first rem CTAs take q + 1 items, the others q
-  int lo, hi;    // this CTA's items
+  int W, G;      // all items, shares
+  int q, rem;    // W = q G + rem: the first rem shares have q + 1 items, the others q
+  int lo, hi;    // items of this share
   int b, off;    // the sequence that item lo lies in, and its offset among that sequence's items
 };
-__device__ __forceinline__ int first_item(const Share& s, int cta) { return s.q * cta + min(cta, s.rem); }
+__device__ __forceinline__ int first_item(const Share& s, int share) { return s.q * share + min(share, s.rem); }
 __device__ __forceinline__ int owner_of(const Share& s, int item) {
   const int t = s.rem * (s.q + 1);
   return item < t ? item / (s.q + 1) : s.rem + (item - t) / s.q;
@@ -57,23 +60,23 @@ __device__ __forceinline__ int owner_of(const Share& s, int item) {
 __device__ __forceinline__ int items_before(const TreeArgs& a, int b, bool flag) {
   int sum = 0;
   for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_blocks(a, i, flag).nb;
-  return __reduce_add_sync(0xffffffffu, sum) * (a.Hkv / a.hw * a.nrt);
+  return __reduce_add_sync(0xffffffffu, sum) * (a.Hkv / a.hw);
 }
 __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
   Share s;
   s.W = W;
-  s.G = min(a.grid, max(1, W / a.min_blocks));
+  s.G = min(a.grid, W);
   s.q = W / s.G;
   s.rem = W - s.q * s.G;
   return s;
 }
 
-// The share of a CTA; called by whole warps, each for itself.
-__device__ __forceinline__ Share share_of(const TreeArgs& a, int cta) {
-  const int lane = threadIdx.x & 31, tiles = a.Hkv / a.hw * a.nrt;
-  Share s = shares(a, items_before(a, a.B, cta == 0 && threadIdx.x < 32));
-  s.lo = cta < s.G ? first_item(s, cta) : s.W;
-  s.hi = cta < s.G ? first_item(s, cta + 1) : s.W;
+// This CTA's share; called by whole warps, each for itself.
+__device__ __forceinline__ Share my_share(const TreeArgs& a) {
+  const int lane = threadIdx.x & 31, tiles = a.Hkv / a.hw, share = blockIdx.x / a.nrt;
+  Share s = shares(a, items_before(a, a.B, blockIdx.x == 0 && threadIdx.x < 32));
+  s.lo = share < s.G ? first_item(s, share) : s.W;
+  s.hi = share < s.G ? first_item(s, share + 1) : s.W;
   s.b = s.off = 0;
   if (s.lo >= s.hi) return s;
   for (int b0 = 0, at = 0;; b0 += 32) {
@@ -100,13 +103,13 @@ constexpr float kTreeLog2e = 1.4426950408889634f;
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
 // Partial results.
-// Slot s: [hw rows] maxima (of log2 e times the scaled logits), as many sums, [hw rows][dh] outputs.
+// A slot: [hw rows] maxima (of log2 e times the scaled logits), as many sums, [hw rows][dh] outputs.
 struct Part {
   float* m; float* l; float* o;
 };
-__device__ __forceinline__ Part part_of(const TreeArgs& a, int64_t slot) {
+__device__ __forceinline__ Part part_of(const TreeArgs& a, int share, int rt, int which) {
   const int n = a.hw * a.rows;
-  float* p = reinterpret_cast<float*>(a.part) + slot * n * (a.dh + 2);
+  float* p = reinterpret_cast<float*>(a.part) + (((int64_t)share * a.nrt + rt) * 2 + which) * n * (a.dh + 2);
   return Part{p, p + n, p + 2 * n};
 }
 
