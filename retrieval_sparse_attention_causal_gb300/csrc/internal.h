@@ -203,7 +203,8 @@ struct TreeArgs {
   float scale;
   ErrWord* err;
   unsigned char* part;                                     // partial results
-  int hw, rows, nrt, nd;                                   // key heads of a tile, rows of a CTA, groups of rows, blocks of the draft
+  int hw, hl, rows, nrt, nd;                               // key heads of a CTA, such CTAs of a share, rows of a CTA, groups of rows,
+                                                           // blocks of the draft
   int grid;                                                // shares of the work, at most
   int wide;                                                // pools on 32-byte boundaries
 };

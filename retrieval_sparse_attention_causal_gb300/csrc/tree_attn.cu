@@ -39,19 +39,19 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const Share sh = my_share(a);
   const float sl2 = a.scale * kTreeLog2e;
-  const int R = a.T * a.g, rt = blockIdx.x % a.nrt;
+  const int R = a.T * a.g, rt = my_rows(a);
   int b = sh.b;
   int off = sh.off, item = sh.lo;
   SeqBlocks sb = sh.lo < sh.hi ? seq_blocks(a, b, false) : SeqBlocks{};
   int slot = 0;
   while (item < sh.hi) {
     const int tile = off / sb.nb;
-    if (tile >= a.Hkv) {
+    if (tile >= a.Hkv / a.hl) {
       sb = seq_blocks(a, ++b, false);
       off = 0;
       continue;
     }
-    const int m = tile;
+    const int m = my_heads(a, tile);
     const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     const int rows = min(MT, R - rt * MT);
     __syncthreads();
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
       }
     }
     const bool whole = blk0 == 0 && blk1 == sb.nb;
-    const Part part = part_of(a, blockIdx.x / a.nrt, rt, slot);
+    const Part part = part_of(a, blockIdx.x, slot);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int r = ty * RT + i;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, int
   const int b = blockIdx.y, tile = blockIdx.x, hg = tile / a.nrt, rt = tile % a.nrt;
   const Share sh = shares(a, items_before(a, a.B, false));
   const SeqBlocks sb = seq_blocks(a, b, false);
-  const int s0 = items_before(a, b, false) + hg * sb.nb;
+  const int s0 = items_before(a, b, false) + hg / a.hl * sb.nb;
   const int c0 = owner_of(sh, s0), c1 = owner_of(sh, s0 + sb.nb - 1);  // shares of its first and last block
   if (c0 == c1) return;  // finished there
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4, ps = 16 / rg, ri = y % rg, pi = y / rg;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, int
         m[k] = -CUDART_INF_F;
         w[k] = 0.f;
         if (cc <= c1) {
-          const Part p = part_of(a, cc, rt, cc == c0 && late ? 1 : 0);
+          const Part p = part_of(a, ((int64_t)cc * a.hl + hg % a.hl) * a.nrt + rt, cc == c0 && late ? 1 : 0);
           m[k] = p.m[at];
           w[k] = p.l[at];
           const float* src = p.o + (int64_t)at * DH + x * CV;
@@ -378,8 +378,9 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 enum Kind { kRows, kTensor, kSimt };
 struct Shape {
   Kind kind;
-  int hw, rows, nrt;  // key heads of a tile, rows of a CTA, groups of rows
+  int hw, rows, nrt;  // key heads and rows of a CTA, groups of rows
   int ctas;           // on the GPU at once
+  int hl;             // CTAs of a share side by side over the key heads
 };
 Shape shape_of(int T, int g, int Hkv, int dh, int bf16) {
   const int R = T * g;
@@ -387,16 +388,21 @@ Shape shape_of(int T, int g, int Hkv, int dh, int bf16) {
   if (bf16 && (R <= 16 || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
   else if (bf16) s = Shape{kTensor, 1, 128, 1, 2 * kSMs};
   s.nrt = (R + s.rows - 1) / s.rows;
+  // As many heads walk together as leave nine shares or more (what does not divide the GPU's
+  // CTAs stays idle: at most a tenth).
+  s.hl = 1;
+  for (int h = 1; h * s.hw <= Hkv; ++h)
+    if (Hkv % (h * s.hw) == 0 && h * s.nrt <= 32) s.hl = h;
   return s;
 }
-int shares_of(const Shape& s) { return std::max(1, s.ctas / s.nrt); }
+int shares_of(const Shape& s) { return std::max(1, s.ctas / (s.nrt * s.hl)); }
 
 template <int DH, int RT>
 cudaError_t run_simt(const TreeArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem((const void*)tree_simt_kernel<DH, RT>, simt_smem<DH, RT>());
   if (e != cudaSuccess) return e;
   launch_begin("tree_simt", s);
-  tree_simt_kernel<DH, RT><<<a.grid * a.nrt, kSimtThreads, simt_smem<DH, RT>(), s>>>(a);
+  tree_simt_kernel<DH, RT><<<a.grid * a.hl * a.nrt, kSimtThreads, simt_smem<DH, RT>(), s>>>(a);
   return launch_end("tree_simt", s);
 }
 template <typename T, int DH>
@@ -408,7 +414,7 @@ cudaError_t run_dh(const TreeArgs& a, Kind kind, cudaStream_t s) {
   // Rows of a CTA: as many as leave a thread about four partials to walk (a tile has about
   // grid / tiles of them), and no more than there are.
   const int rows = a.hw * std::min(a.rows, a.T * a.g), tiles = a.Hkv / a.hw * a.nrt;
-  const int64_t parts = a.grid / ((int64_t)tiles * a.B) + 1;
+  const int64_t parts = (int64_t)a.grid * a.hl / ((int64_t)(a.Hkv / a.hw) * a.B) + 1;
   int rg = 8;
   while (rg > 1 && (rg > rows || parts * rg > 64)) rg >>= 1;
   launch_begin("tree_join", s);
@@ -426,7 +432,7 @@ cudaError_t run(const TreeArgs& a, Kind kind, cudaStream_t s) {
 
 size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16) {
   const Shape sh = shape_of(T, H / Hkv, Hkv, dh, bf16);
-  return (size_t)2 * shares_of(sh) * sh.nrt * sh.hw * sh.rows * (dh + 2) * 4;
+  return (size_t)2 * shares_of(sh) * sh.nrt * sh.hl * sh.hw * sh.rows * (dh + 2) * 4;
 }
 
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
@@ -435,6 +441,7 @@ cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
   a.rows = sh.rows;
   a.grid = shares_of(sh);
   a.nrt = sh.nrt;
+  a.hl = sh.hl;
   a.nd = (a.T + kChunk - 1) / kChunk;
   a.wide = (reinterpret_cast<uintptr_t>(a.kp) | reinterpret_cast<uintptr_t>(a.vp)) % 32 == 0;
   return a.bf16 ? run<bf16>(a, sh.kind, s) : run<float>(a, sh.kind, s);

@@ -122,19 +122,19 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
   const Share sh = my_share(a);
   if (sh.lo >= sh.hi) return;
   const float sl2 = a.scale * kTreeLog2e;
-  const int rt = blockIdx.x % a.nrt, R = a.T * a.g - 16 * rt;  // rows from this CTA's first on
+  const int rt = my_rows(a), R = a.T * a.g - 16 * rt;  // rows from this CTA's first on
   int b = sh.b;
   int off = sh.off, item = sh.lo;
   SeqBlocks sb = seq_blocks(a, b, false);
   int slot = 0;
   while (item < sh.hi) {
     const int tile = off / sb.nb;
-    if (tile >= a.Hkv / a.hw) {
+    if (tile >= a.Hkv / (a.hw * a.hl)) {
       sb = seq_blocks(a, ++b, false);
       off = 0;
       continue;
     }
-    const int m = tile * a.hw + warp % a.hw;  // this warp's key head
+    const int m = my_heads(a, tile) + warp % a.hw;  // this warp's key head
     const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     // Q fragments, and the two rows' positions and masks.
     uint32_t qf[G::KS][4];
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
     }
     __syncthreads();
     for (int i = 0; i < a.hw; ++i) {
-      const int r = tid >> 3, d0 = (tid & 7) * NV, m = tile * a.hw + i;
+      const int r = tid >> 3, d0 = (tid & 7) * NV, m = my_heads(a, tile) + i;
       float top = -CUDART_INF_F;
       for (int w = i; w < kWarps; w += a.hw) top = fmaxf(top, join_m[w][r]);
       float sum = 0.f, out[NV];
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
 #pragma unroll
         for (int e = 0; e < NV / 2; e += 2) *reinterpret_cast<uint2*>(to + e) = make_uint2(w[e], w[e + 1]);
       } else {
-        const Part part = part_of(a, blockIdx.x / a.nrt, rt, slot);
+        const Part part = part_of(a, blockIdx.x, slot);
         const int at = i * a.rows + r;
         if (d0 == 0) {
           part.m[at] = top;
@@ -426,9 +426,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
 
 cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s) {
   launch_begin("tree_rows", s);
-  if (a.dh == 32) tree_rows_kernel<32><<<a.grid * a.nrt, kThreads, 0, s>>>(a);
-  else if (a.dh == 64) tree_rows_kernel<64><<<a.grid * a.nrt, kThreads, 0, s>>>(a);
-  else tree_rows_kernel<128><<<a.grid * a.nrt, kThreads, 0, s>>>(a);
+  if (a.dh == 32) tree_rows_kernel<32><<<a.grid * a.hl * a.nrt, kThreads, 0, s>>>(a);
+  else if (a.dh == 64) tree_rows_kernel<64><<<a.grid * a.hl * a.nrt, kThreads, 0, s>>>(a);
+  else tree_rows_kernel<128><<<a.grid * a.hl * a.nrt, kThreads, 0, s>>>(a);
   return launch_end("tree_rows", s);
 }
 

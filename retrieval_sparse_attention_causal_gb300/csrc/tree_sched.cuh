@@ -1,20 +1,23 @@
 // How the attention of drafted tokens over a paged cache is divided among its CTAs.
 //
-// A tile is (sequence b, `hw` key heads side by side).  Its keys are blocks of 64: the pages of
-// the context that some row can see, then the draft's own tokens.  All tiles' blocks, laid
-// end to end, are one list of W items, cut into G shares of W / G in a row (one more or
+// The work is a list of W items: for each sequence b, for each set of `hl * hw` key heads side by
+// side, its blocks of 64 keys (the pages of the context that some row can see, then the
+// draft's own tokens).  The list is cut into G shares of W / G items in a row (one more or
 // less), whatever sequences they belong to, so a batch of one long and many short sequences
 // divides as evenly as a single sequence.  The lengths are read on the device: a captured
 // graph follows them.
 //
-// Of each key head m, T * g query rows share the keys (row r = token r / g, query head
-// m g + r % g), in `nrt` groups of `rows`.  Share c has a CTA for each group: they walk the same
-// pages at the same time, and all but the first find them in L2.
+// A share has hl * nrt CTAs, which walk its items together: one for each `hw` of the set's key
+// heads, and of each key head m one for each `rows` of the T * g query rows that share it (row
+// r = token r / g, query head m g + r % g).  The heads of a token lie side by side in memory:
+// read at the same time they make long runs for DRAM, read at different times pieces of a
+// few bytes (measured: 12 heads of 64 over 128K tokens, 64 rows a head: LONG us together, 203 us
+// apart); and the row groups after the first find their pages in L2.
 //
-// A tile that lies in one share is finished there.  Of the others each CTA writes a partial
-// result (row maximum, row sum, unnormalised output): the tile that its share begins in to
-// the first of its two slots, the one that it ends in to the second; the joining kernel finds
-// a tile's partials by the same arithmetic.
+// A tile (sequence, hw heads, row group) whose blocks lie in one share is finished there.  Of
+// the others each CTA writes a partial result (row maximum, row sum, unnormalised output): the
+// one that its share begins in to the first of its two slots, the one that it ends in to the
+// second; the joining kernel finds a tile's partials by the same arithmetic.
 #pragma once
 
 #include "common.cuh"
@@ -60,7 +63,7 @@ __device__ __forceinline__ int owner_of(const Share& s, int item) {
 __device__ __forceinline__ int items_before(const TreeArgs& a, int b, bool flag) {
   int sum = 0;
   for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_blocks(a, i, flag).nb;
-  return __reduce_add_sync(0xffffffffu, sum) * (a.Hkv / a.hw);
+  return __reduce_add_sync(0xffffffffu, sum) * (a.Hkv / (a.hw * a.hl));
 }
 __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
   Share s;
@@ -73,7 +76,7 @@ __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
 
 // This CTA's share; called by whole warps, each for itself.
 __device__ __forceinline__ Share my_share(const TreeArgs& a) {
-  const int lane = threadIdx.x & 31, tiles = a.Hkv / a.hw, share = blockIdx.x / a.nrt;
+  const int lane = threadIdx.x & 31, tiles = a.Hkv / (a.hw * a.hl), share = blockIdx.x / (a.hl * a.nrt);
   Share s = shares(a, items_before(a, a.B, blockIdx.x == 0 && threadIdx.x < 32));
   s.lo = share < s.G ? first_item(s, share) : s.W;
   s.hi = share < s.G ? first_item(s, share + 1) : s.W;
@@ -99,6 +102,12 @@ __device__ __forceinline__ Share my_share(const TreeArgs& a) {
   }
 }
 
+// This CTA's row group, and the first key head of tile t of its sequence.
+__device__ __forceinline__ int my_rows(const TreeArgs& a) { return blockIdx.x % a.nrt; }
+__device__ __forceinline__ int my_heads(const TreeArgs& a, int t) {
+  return (t * a.hl + (int)(blockIdx.x / a.nrt) % a.hl) * a.hw;
+}
+
 constexpr float kTreeLog2e = 1.4426950408889634f;
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
@@ -107,9 +116,9 @@ constexpr float kTreeLn2 = 0.6931471805599453f;
 struct Part {
   float* m; float* l; float* o;
 };
-__device__ __forceinline__ Part part_of(const TreeArgs& a, int share, int rt, int which) {
+__device__ __forceinline__ Part part_of(const TreeArgs& a, int64_t cta, int which) {
   const int n = a.hw * a.rows;
-  float* p = reinterpret_cast<float*>(a.part) + (((int64_t)share * a.nrt + rt) * 2 + which) * n * (a.dh + 2);
+  float* p = reinterpret_cast<float*>(a.part) + (cta * 2 + which) * n * (a.dh + 2);
   return Part{p, p + n, p + 2 * n};
 }
 

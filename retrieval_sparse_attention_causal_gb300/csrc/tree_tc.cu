@@ -8,6 +8,9 @@
 //     of K and V into a ring, in the order the products read them: K(0), K(1), V(0), K(2), ...
 //   * warp 4 (products): S(n) = Q K(n)^T into one of two TMEM buffers, one block ahead of the
 //     softmax; O += P(n) V(n) with P in the buffer that S(n) lay in.
+//     Barriers of blocks (S ready, P ready, O done) come in pairs, one for even and one for odd
+//     blocks: S(n) is issued before P V (n - 1), so a thread that has seen S(n) knows that
+//     P V (n - 2) is done, not that P V (n - 1) is, and one barrier's parity would not tell.
 //   * warps 0-3 (softmax): a thread owns a row.  Running maximum and sum; the output is only
 //     rescaled when a row's maximum has grown by more than 2^8 over the one in use, which
 //     keeps the weights below 2^8 (their sum stays in 32 bits, and bf16 rounds relative to
@@ -63,7 +66,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   extern __shared__ __align__(1024) unsigned char dsm[];
   unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = Qs + C::QB;
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -78,8 +81,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar_s[i], 1);
       tc::mbar_init(&bar_p[i], 4);
+      tc::mbar_init(&bar_o[i], 1);
     }
-    tc::mbar_init(&bar_o, 1);
     abort_s = 0;
     tc::fence_mbar_init();
   }
@@ -88,15 +91,15 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   __syncthreads();
   tc::fence_after();
   const uint32_t tS = tmem_slot, tO = tmem_slot + 128;
-  const int rt = blockIdx.x % a.nrt;
+  const int rt = my_rows(a);
 
-  // The segments of this CTA, walked by every role: blocks blk0 .. blk1 - 1 of key head `tile`.
+  // The segments of this CTA, walked by every role: blocks blk0 .. blk1 - 1 of tile `tile`.
   int b = sh.b, off = sh.off, item = sh.lo;
   SeqBlocks sb = seq_blocks(a, b, false);
   int tile = 0, blk0 = 0, blk1 = 0;
   auto segment = [&]() -> bool {
     if (item >= sh.hi) return false;
-    while ((tile = off / sb.nb) >= a.Hkv) {
+    while ((tile = off / sb.nb) >= a.Hkv / a.hl) {
       sb = seq_blocks(a, ++b, false);
       off = 0;
     }
@@ -107,8 +110,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     return true;
   };
   // Waits of a warp: it goes on or gives up as a whole.
-  auto parked = [&](uint64_t* bar, uint32_t parity, int site, int at) {
-    return __all_sync(kAll, park_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
+  auto spun = [&](uint64_t* bar, uint32_t parity, int site, int at) {
+    return __all_sync(kAll, spin_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
   };
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     return __all_sync(kAll, wait_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
@@ -126,7 +129,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     Ring r;
     int issued = 0;
     while (ok && segment()) {
-      const int m = tile, n = blk1 - blk0;
+      const int m = my_heads(a, tile), n = blk1 - blk0;
       int kfirst = -64, kpages = -1, vfirst = -64, vpages = -1;  // 32 page numbers, one a lane, for K and for V
       auto load = [&](int blk, bool value) {
         int& first = value ? vfirst : kfirst;
@@ -144,7 +147,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             page = (int)a.pages;  // behind the pool: reads zeros
           }
         }
-        if (issued >= NS) ok = parked(&bar_empty[r.stage], r.phase ^ 1, kSiteEmpty, blk);
+        if (issued >= NS) ok = spun(&bar_empty[r.stage], r.phase ^ 1, kSiteEmpty, blk);
         if (!ok) return;
         if (lane == 0) {
           unsigned char* to = ring + r.stage * C::STAGE;
@@ -180,7 +183,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     int seg = 0, nth = 0;  // segments, and blocks, so far
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
     auto wait_full = [&](int blk) {
-      ok = ok && parked(&bar_full[r.stage], r.phase, kSiteFull, blk);
+      ok = ok && spun(&bar_full[r.stage], r.phase, kSiteFull, blk);
       tc::fence_after();
     };
     auto logits = [&](int blk, int i) {
@@ -196,14 +199,14 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       r.next(NS);
     };
     while (ok && segment()) {
-      ok = parked(&bar_q, seg & 1, kSiteQ, seg);
+      ok = spun(&bar_q, seg & 1, kSiteQ, seg);
       tc::fence_after();
       ++seg;
       if (ok) logits(blk0, nth);
       for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
         if (blk + 1 < blk1) logits(blk + 1, nth + 1);
         if (!ok) break;
-        ok = parked(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, blk);
+        ok = spun(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, blk);
         if (ok) wait_full(blk);
         if (!ok) break;
         const uint32_t v = tc::su32(ring + r.stage * C::STAGE);
@@ -212,7 +215,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
           tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tS + 64 * (nth & 1), tc::desc_mn(v + s * kTile), kIdPV,
                                                blk > blk0 ? 1u : 0u);
         tc::commit_warp(&bar_empty[r.stage]);
-        tc::commit_warp(&bar_o);
+        tc::commit_warp(&bar_o[nth & 1]);
         r.next(NS);
       }
     }
@@ -224,8 +227,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     int nth = 0, tiles_read = 0;  // blocks, and ring tiles, so far
     int slot = 0;
     while (ok && segment()) {
-      const int m = tile, r = rt * kRows + tid, n = blk1 - blk0;
-      const bool on = r < R;
+      const int m = my_heads(a, tile), r = rt * kRows + tid, n = blk1 - blk0;
+      const bool on = r < R, idle = rt * kRows + 32 * warp >= R;
       int t = 0, h = 0, pos = -1;
       {
         uint4 w[DH / 8];
@@ -314,6 +317,11 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         }
         ok = ok && waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
         if (!ok) break;
+        page = next_page;
+        if (idle) {  // no row of this warp exists: what P holds for them goes nowhere
+          if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
+          continue;
+        }
         tc::fence_after();
         const uint32_t tP = tS + 64 * (nth & 1) + lanes;
         float s[2][32];
@@ -329,11 +337,12 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             for (int i = 0; i < 32; ++i)
               if (!((w[q] >> i) & 1)) s[q][i] = -CUDART_INF_F;
         }
-        float top = -CUDART_INF_F;
+        float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) top = tc::max3(top, s[q][i], s[q][i + 1]);
+          for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 3] = tc::max3(tops[(i >> 1) & 3], s[q][i], s[q][i + 1]);
+        const float top = fmaxf(tc::max3(tops[0], tops[1], tops[2]), tops[3]);
         const bool grow = (top - mx) * sl2 > kGrow || (mx == -CUDART_INF_F && top > mx);
         if (__any_sync(kAll, grow)) {
           const float now = grow ? top : mx;
@@ -341,7 +350,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
           mx = now;
           l *= f;
           if (blk > blk0) {
-            ok = waited(&bar_o, (nth - 1) & 1, kSiteO, blk);
+            ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
             tc::fence_after();
 #pragma unroll
             for (int q = 0; q < DH / 32; ++q) {
@@ -385,18 +394,17 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
-        page = next_page;
       }
       tiles_read += 2 * n;
       if (!ok) break;
-      ok = waited(&bar_o, (nth - 1) & 1, kSiteO, -1);
+      ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, -1);
       if (!ok) break;
       tc::fence_after();
       if (pos < 0) l = 0.f;
       const bool whole = blk0 == 0 && blk1 == sb.nb;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t at = ((int64_t)b * a.T + t) * a.H + h;
-      const Part part = part_of(a, blockIdx.x / a.nrt, rt, slot);
+      const Part part = part_of(a, blockIdx.x, slot);
 #pragma unroll
       for (int q = 0; q < DH / 32; ++q) {
         float o[32];
@@ -450,7 +458,7 @@ cudaError_t run_tc(const TreeArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = allow_smem((const void*)tree_tc_kernel<DH>, Tc<DH>::SMEM);
   if (e != cudaSuccess) return e;
   launch_begin("tree_tc", s);
-  tree_tc_kernel<DH><<<a.grid * a.nrt, kThreads, Tc<DH>::SMEM, s>>>(a, tk, tv, tkn, tvn);
+  tree_tc_kernel<DH><<<a.grid * a.hl * a.nrt, kThreads, Tc<DH>::SMEM, s>>>(a, tk, tv, tkn, tvn);
   return launch_end("tree_tc", s);
 }
 
