@@ -10,6 +10,8 @@ or `python retrieval_sparse_attention_causal_gb300/build.py`).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -104,7 +106,7 @@ def _load():
         "gca_cache_compact": (I, [CP, P, P, SZ, P, SZ, P]),
         "gca_cache_lookup": (I, [CP, I, I, P, P, P, P, SZ, P]),
         "gca_tree_plan": (I, [P, P, I, I, P, P, P, SZ, P]),
-        "gca_tree_attention_scratch_size": (SZ, [I, I, I, I, I, I]),
+        "gca_tree_attention_scratch_size": (SZ, [I, I, I, I, I, I, I]),
         "gca_tree_attention": (I, [HP, HP, HP, CP, I, I, I, P, P, I, F, P, P, P, SZ, P, SZ, P]),
         "gca_check_error": (I, [P, P, ctypes.POINTER(I)]),
         "gca_launch_count": (U64, []),
@@ -120,7 +122,20 @@ def _load():
     return lib
 
 
+def _load_decoding():
+    """The extension that binds the decoding operators (csrc/binding.cpp)."""
+    path = os.path.join(_HERE, "_build", "_gca_decoding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} not found; build it first (python retrieval_sparse_attention_causal_gb300/build.py)")
+    loader = importlib.machinery.ExtensionFileLoader("_gca_decoding", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_gca_decoding", path, loader=loader))
+    loader.exec_module(mod)
+    mod.set_error(GCAError)
+    return mod
+
+
 LIB = _load()
+EXT = _load_decoding()
 EXPORTS = (
     "gca_status_string", "gca_last_error_detail", "gca_retrieve_workspace_size", "gca_retrieve_topk",
     "gca_retrieve_topk_dseed",

@@ -1,21 +1,25 @@
-"""Builds libgca.so (the CUDA library behind include/gca.h) for sm_103a, in-tree.
+"""Builds libgca.so (the CUDA library behind include/gca.h) for sm_103a, in-tree, and the
+Python extension that binds its decoding operators to PyTorch tensors.
 
-Each translation unit is compiled by its own nvcc process (in parallel), then linked
-into one shared library under retrieval_sparse_attention_causal_gb300/_build/.
+Each translation unit is compiled by its own process (in parallel), then linked into the
+two shared libraries under retrieval_sparse_attention_causal_gb300/_build/.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgca.so")
+EXT = os.path.join(BUILD, "_gca_decoding.so")
 SOURCES = ["api.cu", "retrieve.cu", "gca_fwd.cu", "gca_bwd.cu", "scores_bwd.cu", "noalloc.cu", "tmap.cu", "gca_bwd_tc.cu",
            "gather.cu", "block_attn.cu", "window_bwd.cu", "encoder.cu", "retrieve_tc.cu", "rotary.cu", "tree_attn.cu",
            "tree_rows.cu", "tree_tc.cu", "cache.cu"]
@@ -40,6 +44,22 @@ def _stale(obj, src):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding(obj):
+    """Compile command of the Python extension, and its link command (torch's headers and
+    libraries, found without importing it)."""
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    cxx = os.environ.get("CXX", "g++")
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{d}" for d in inc), "-c",
+                os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    link = [cxx, "-shared", "-o", EXT, obj, f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", f"-L{BUILD}", "-lgca", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -50,20 +70,28 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         obj = os.path.join(BUILD, s.replace(".cu", ".o"))
         if _stale(obj, src) or extra_flags:
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
+    cuda_jobs = bool(jobs)
+    bind_obj = os.path.join(BUILD, "binding.o")
+    compile_binding, link_binding = _binding(bind_obj)
+    bind_job = _stale(bind_obj, os.path.join(CSRC, "binding.cpp"))
+    if bind_job:
+        jobs.append(compile_binding)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
+            raise RuntimeError(f"compiler failed: {' '.join(cmd)}")
         return r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         list(ex.map(run, jobs))
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
-    if jobs or not os.path.exists(LIB):
+    if cuda_jobs or not os.path.exists(LIB):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs])
+    if bind_job or not os.path.exists(EXT):
+        run(link_binding)
     return LIB
 
 

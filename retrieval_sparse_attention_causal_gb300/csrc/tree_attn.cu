@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 }
 
 // ------------------------------------------------------------------ launching
+constexpr int kFewBlocks = 16 * 2 * kSMs;
 enum Kind { kRows, kTensor, kSimt };
 struct Shape {
   Kind kind;
@@ -382,17 +383,18 @@ struct Shape {
   int ctas;           // on the GPU at once
   int hl;             // CTAs of a share side by side over the key heads
 };
-Shape shape_of(int T, int g, int Hkv, int dh, int bf16) {
+Shape shape_of(int B, int T, int g, int Hkv, int dh, int bf16, int width) {
   const int R = T * g;
   Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, 2 * kSMs};
-  if (bf16 && (R <= 16 || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
+  const int64_t blocks = (int64_t)B * Hkv * (width + 1);  // at most
+  if (bf16 && ((R <= 16 && blocks < kFewBlocks) || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
   else if (bf16) s = Shape{kTensor, 1, 128, 1, 2 * kSMs};
   s.nrt = (R + s.rows - 1) / s.rows;
   // As many heads walk together as leave nine shares or more (what does not divide the GPU's
   // CTAs stays idle: at most a tenth).
   s.hl = 1;
   for (int h = 1; h * s.hw <= Hkv; ++h)
-    if (Hkv % (h * s.hw) == 0 && h * s.nrt <= 32) s.hl = h;
+    if (Hkv % (h * s.hw) == 0 && h * s.nrt * 9 <= s.ctas) s.hl = h;
   return s;
 }
 int shares_of(const Shape& s) { return std::max(1, s.ctas / (s.nrt * s.hl)); }
@@ -430,13 +432,13 @@ cudaError_t run(const TreeArgs& a, Kind kind, cudaStream_t s) {
 
 }  // namespace
 
-size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16) {
-  const Shape sh = shape_of(T, H / Hkv, Hkv, dh, bf16);
+size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16, int width) {
+  const Shape sh = shape_of(B, T, H / Hkv, Hkv, dh, bf16, width);
   return (size_t)2 * shares_of(sh) * sh.nrt * sh.hl * sh.hw * sh.rows * (dh + 2) * 4;
 }
 
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
-  const Shape sh = shape_of(a.T, a.g, a.Hkv, a.dh, a.bf16);
+  const Shape sh = shape_of(a.B, a.T, a.g, a.Hkv, a.dh, a.bf16, a.width);
   a.hw = sh.hw;
   a.rows = sh.rows;
   a.grid = shares_of(sh);

@@ -4,17 +4,20 @@
 // With 128 rows a byte of K or V asks 128 operations: still below the balance of memory and
 // tensor pipes (about 290), so the aim is a stream of pages that never waits.  One CTA walks
 // its share of the blocks for 128 rows (padded) of one key head; two CTAs share an SM.
-//   * warp 5 (loads): page numbers of 32 blocks at a time, and one TMA load per 64 x 64 tile
-//     of K and V into a ring, in the order the products read them: K(0), K(1), V(0), K(2), ...
-//   * warp 4 (products): S(n) = Q K(n)^T into one of two TMEM buffers, one block ahead of the
+//   * one warp loads: page numbers of 32 blocks at a time, and TMA tiles of 64 x 64 into a ring of
+//     16 KB slots, K and V in turn (two tiles a barrier: waiting for one and announcing a load
+//     take about 200 cycles, which at 8 KB a slot held a CTA to 14 bytes a cycle, less than its
+//     share of DRAM).
+//   * one warp issues the products: S(n) = Q K(n)^T into one of two TMEM buffers, one block ahead of the
 //     softmax; O += P(n) V(n) with P in the buffer that S(n) lay in.
 //     Barriers of blocks (S ready, P ready, O done) come in pairs, one for even and one for odd
 //     blocks: S(n) is issued before P V (n - 1), so a thread that has seen S(n) knows that
 //     P V (n - 2) is done, not that P V (n - 1) is, and one barrier's parity would not tell.
-//   * warps 0-3 (softmax): a thread owns a row.  Running maximum and sum; the output is only
-//     rescaled when a row's maximum has grown by more than 2^8 over the one in use, which
-//     keeps the weights below 2^8 (their sum stays in 32 bits, and bf16 rounds relative to
-//     the weight, so nothing is lost); after a few blocks that no longer happens.
+//   * four warps a row tile do the softmax: a thread owns a row.  The weights are exp(s - r) with a reference r
+//     that is the row's maximum when it is taken.  It need not stay that: a larger logit only
+//     makes larger weights, and bf16 and float32 round relative to the value.  So a block's
+//     maximum is not computed; when the sum of a row's 64 weights passes 2^14, the block is
+//     weighed again by the new maximum, and the output and the sum so far are scaled to it.
 // The last page, the window's edge and the draft's own block are masked by a 64-bit word a
 // row; there the rows of V that nobody sees are set to zeros in shared memory, for a weight
 // of 0 times what lies in them must stay 0.
@@ -30,30 +33,21 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 192;
-constexpr int kRows = 128;
+constexpr int kRows = 128;       // the lanes of TMEM
+constexpr int kCols = 256;       // of TMEM: two logit buffers of 64, the output
 constexpr int kTile = 8192;     // 64 tokens x 64 elements
-constexpr float kGrow = 8.f;    // log2 of how far a row's maximum may outgrow the one in use
+constexpr int kSlot = 2 * kTile;
+constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
 constexpr uint32_t kAll = 0xffffffffu;
 enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteS, kSiteP, kSiteO, kSiteV };
 
 template <int DH>
 struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
-  static constexpr int STAGE = kTile * SUB;         // K or V of a block
-  static constexpr int QB = 2 * kTile * SUB;        // 128 rows
-  static constexpr int NS = DH == 64 ? 11 : 4;      // ring stages
-  static constexpr int SMEM = QB + NS * STAGE + 1024;
-};
-
-struct Ring {
-  int stage = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++stage == n) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
+  static constexpr int PB = 2 / SUB;                // blocks of 64 keys of a ring slot: 16 KB of K or of V
+  static constexpr int QB = 2 * kTile * SUB;        // a row tile of Q
+  static constexpr int NS = DH == 64 ? 5 : 4;       // ring slots
+  static constexpr int SMEM = QB + NS * kSlot + 1024;
 };
 
 template <int DH>
@@ -61,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmKn, const __grid_constant__ CUtensorMap tmVn) {
   using C = Tc<DH>;
-  constexpr int SUB = C::SUB, NS = C::NS;
+  constexpr int SUB = C::SUB, NS = C::NS, PB = C::PB;
   constexpr uint32_t kIdS = tc::idesc_bf16(kRows, 64, false), kIdPV = tc::idesc_bf16(kRows, 64, true);
   extern __shared__ __align__(1024) unsigned char dsm[];
   unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
@@ -86,11 +80,11 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     abort_s = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 4) tc::tmem_alloc(&tmem_slot, 256);
+  if (warp == 4) tc::tmem_alloc(&tmem_slot, kCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tS = tmem_slot, tO = tmem_slot + 128;
+  const uint32_t tmem = tmem_slot;
   const int rt = my_rows(a);
 
   // The segments of this CTA, walked by every role: blocks blk0 .. blk1 - 1 of tile `tile`.
@@ -110,9 +104,6 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     return true;
   };
   // Waits of a warp: it goes on or gives up as a whole.
-  auto spun = [&](uint64_t* bar, uint32_t parity, int site, int at) {
-    return __all_sync(kAll, spin_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
-  };
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     return __all_sync(kAll, wait_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
   };
@@ -126,105 +117,107 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       prefetch_tmap(&tmKn);
       prefetch_tmap(&tmVn);
     }
-    Ring r;
-    int issued = 0;
+    int id = 0;  // slots so far
     while (ok && segment()) {
       const int m = my_heads(a, tile), n = blk1 - blk0;
-      int kfirst = -64, kpages = -1, vfirst = -64, vpages = -1;  // 32 page numbers, one a lane, for K and for V
-      auto load = [&](int blk, bool value) {
-        int& first = value ? vfirst : kfirst;
-        int& pages = value ? vpages : kpages;
-        int page = -1;
-        const bool ctx = blk < sb.np;
-        if (ctx) {
-          if (blk - first >= 32) {
-            first = blk;
-            pages = blk + lane < sb.np ? a.table[(int64_t)b * a.width + sb.p0 + blk + lane] : -1;
-          }
-          page = __shfl_sync(kAll, pages, blk - first);
-          if (page < 0 || page >= a.pages) {
-            if (page != -1 && !value && lane == 0) flag_bad_index(a.err, page);
-            page = (int)a.pages;  // behind the pool: reads zeros
-          }
-        }
-        if (issued >= NS) ok = spun(&bar_empty[r.stage], r.phase ^ 1, kSiteEmpty, blk);
-        if (!ok) return;
-        if (lane == 0) {
-          unsigned char* to = ring + r.stage * C::STAGE;
-          tc::mbar_expect_tx(&bar_full[r.stage], C::STAGE);
+      int first = -64, pages = -1;  // 32 page numbers, one a lane
+      for (int x = 0; x < n && ok; x += PB) {
+        const int count = min(PB, n - x);
+        int page[PB];
 #pragma unroll
-          for (int s = 0; s < SUB; ++s) {
-            if (ctx) tc::tma_load_4d(to + s * kTile, value ? &tmV : &tmK, 64 * s, m, 0, page, &bar_full[r.stage]);
-            else
-              tc::tma_load_4d(to + s * kTile, value ? &tmVn : &tmKn, 64 * s, value ? (a.vn_hs ? m : 0) : (a.kn_hs ? m : 0),
-                              (value ? a.vn_ts : a.kn_ts) ? (blk - sb.np) * kChunk : 0,
-                              (value ? a.vn_bs : a.kn_bs) ? b : 0, &bar_full[r.stage]);
+        for (int i = 0; i < PB; ++i) {
+          const int blk = blk0 + x + i;
+          if (blk < sb.np && i < count) {
+            if (blk - first >= 32) {
+              first = blk;
+              pages = blk + lane < sb.np ? a.table[(int64_t)b * a.width + sb.p0 + blk + lane] : -1;
+            }
+            page[i] = __shfl_sync(kAll, pages, blk - first);
+            if (page[i] < 0 || page[i] >= a.pages) {
+              if (page[i] != -1 && lane == 0) flag_bad_index(a.err, page[i]);
+              page[i] = (int)a.pages;  // behind the pool: reads zeros
+            }
           }
         }
-        __syncwarp();
-        ++issued;
-        r.next(NS);
-      };
-      load(blk0, false);
-      for (int i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) load(blk0 + i + 1, false);
-        if (ok) load(blk0 + i, true);
+#pragma unroll
+        for (int v = 0; v < 2; ++v, ++id) {  // K, then V
+          const int st = id % NS;
+          if (id >= NS) ok = ok && waited(&bar_empty[st], (id / NS - 1) & 1, kSiteEmpty, x);
+          if (!ok) break;
+          unsigned char* to = ring + st * kSlot;
+          tc::mbar_expect_tx_warp(&bar_full[st], count * SUB * kTile);
+#pragma unroll
+          for (int i = 0; i < PB; ++i) {
+            if (i >= count) break;
+            const int blk = blk0 + x + i;
+#pragma unroll
+            for (int s = 0; s < SUB; ++s, to += kTile) {
+              if (blk < sb.np) {
+                tc::tma_load_4d_warp(to, v ? &tmV : &tmK, 64 * s, m, 0, page[i], &bar_full[st]);
+              } else {  // the draft's (an axis of stride 0 has one entry in the map)
+                const int64_t hs = v ? a.vn_hs : a.kn_hs, ts = v ? a.vn_ts : a.kn_ts, bs = v ? a.vn_bs : a.kn_bs;
+                tc::tma_load_4d_warp(to, v ? &tmVn : &tmKn, 64 * s, hs ? m : 0, ts ? (blk - sb.np) * kChunk : 0, bs ? b : 0,
+                                     &bar_full[st]);
+              }
+            }
+          }
+        }
       }
     }
     if (!ok)  // let the copies in flight land before the CTA ends
-      for (int i = 0; i < min(issued, NS); ++i) {
-        r.stage = (r.stage + NS - 1) % NS;
-        if (r.stage == NS - 1) r.phase ^= 1;
-        tc::mbar_wait(&bar_full[r.stage], r.phase, 1u << 16);
-      }
+      for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&bar_full[i % NS], (i / NS) & 1, 1u << 16);
   } else if (warp == 4) {
     // ---------------------------------------------------------------- products
-    Ring r;
-    int seg = 0, nth = 0;  // segments, and blocks, so far
+    int seg = 0, nth = 0, id = 0;  // segments, blocks and slots so far
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
-    auto wait_full = [&](int blk) {
-      ok = ok && spun(&bar_full[r.stage], r.phase, kSiteFull, blk);
-      tc::fence_after();
+    // K (v = 0) or V of the segment's block x: its address, once its slot is full.
+    auto slot_of = [&](int x, int v) { return id + 2 * (x / PB) + v; };
+    auto operand = [&](int x, int v) {
+      const int i = slot_of(x, v);
+      if (x % PB == 0) ok = ok && waited(&bar_full[i % NS], (i / NS) & 1, kSiteFull, x);
+      return tc::su32(ring + (i % NS) * kSlot + (x % PB) * kTile);
     };
-    auto logits = [&](int blk, int i) {
-      wait_full(blk);
+    auto release = [&](int x, int v, int n) {
+      if (x % PB == PB - 1 || x == n - 1) tc::commit_warp(&bar_empty[slot_of(x, v) % NS]);
+    };
+    auto logits = [&](int x, int i, int n) {
+      const uint32_t k = operand(x, 0);
       if (!ok) return;
-      const uint32_t k = tc::su32(ring + r.stage * C::STAGE);
+      tc::fence_after();
 #pragma unroll
       for (int s = 0; s < SUB; ++s)
-        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tS + 64 * (i & 1), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
+        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (i & 1), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
                                                 s ? 1u : 0u);
-      tc::commit_warp(&bar_empty[r.stage]);
       tc::commit_warp(&bar_s[i & 1]);
-      r.next(NS);
+      release(x, 0, n);
     };
     while (ok && segment()) {
-      ok = spun(&bar_q, seg & 1, kSiteQ, seg);
+      const int n = blk1 - blk0;
+      ok = waited(&bar_q, seg & 1, kSiteQ, seg);
       tc::fence_after();
       ++seg;
-      if (ok) logits(blk0, nth);
-      for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
-        if (blk + 1 < blk1) logits(blk + 1, nth + 1);
+      if (ok) logits(0, nth, n);
+      for (int x = 0; x < n && ok; ++x, ++nth) {
+        if (x + 1 < n) logits(x + 1, nth + 1, n);
+        const uint32_t v = operand(x, 1);
+        ok = ok && waited(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, x);
         if (!ok) break;
-        ok = spun(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, blk);
-        if (ok) wait_full(blk);
-        if (!ok) break;
-        const uint32_t v = tc::su32(ring + r.stage * C::STAGE);
+        tc::fence_after();
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
-          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tS + 64 * (nth & 1), tc::desc_mn(v + s * kTile), kIdPV,
-                                               blk > blk0 ? 1u : 0u);
-        tc::commit_warp(&bar_empty[r.stage]);
+          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 128 + 64 * s, tmem + 64 * (nth & 1), tc::desc_mn(v + s * kTile), kIdPV,
+                                               x > 0 ? 1u : 0u);
         tc::commit_warp(&bar_o[nth & 1]);
-        r.next(NS);
+        release(x, 1, n);
       }
+      id += 2 * ((n + PB - 1) / PB);
     }
   } else {
     // ---------------------------------------------------------------- softmax
     const float sl2 = a.scale * kTreeLog2e;
     const int R = a.T * a.g;
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    int nth = 0, tiles_read = 0;  // blocks, and ring tiles, so far
+    const uint32_t tS = tmem + ((uint32_t)(32 * warp) << 16), tO = tS + 128;
+    int nth = 0, id = 0;  // blocks and ring slots so far
     int slot = 0;
     while (ok && segment()) {
       const int m = my_heads(a, tile), r = rt * kRows + tid, n = blk1 - blk0;
@@ -250,25 +243,36 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar_q);
-      const int far = __reduce_max_sync(kAll, pos);  // of this warp's rows
       float mx = -CUDART_INF_F, l = 0.f;
-      auto page_at = [&](int blk) { return blk < sb.np ? a.table[(int64_t)b * a.width + sb.p0 + blk] : 0; };
-      int page = page_at(blk0);
+      // Blocks in0 .. in1 - 1 are seen whole by every row of this warp, unless there are holes.
+      const int far = max(__reduce_max_sync(kAll, pos), sb.len);
+      const int in0 = a.window > 0 && far >= a.window ? (far - a.window) / kChunk + 1 - sb.p0 : 0, in1 = sb.len / kChunk - sb.p0;
+      auto page_at = [&](int blk) { return a.table[(int64_t)b * a.width + sb.p0 + blk]; };
+      bool hole = false;  // a page that is not held
+      for (int blk = blk0 + lane; blk < min(blk1, sb.np); blk += 32) {
+        const int page = page_at(blk);
+        hole = hole || page < 0 || page >= a.pages;
+      }
+      const bool holes = __any_sync(kAll, hole);
+      bool settled = false;  // every row that sees something has a reference
       for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
-        const bool ctx = blk < sb.np;
-        const int j0 = ctx ? (sb.p0 + blk) * kChunk : (blk - sb.np) * kChunk;
-        // Keys lo .. hi - 1 of the block exist.
-        int lo = 0, hi = min(kChunk, (ctx ? sb.len : a.T) - j0);
-        if (ctx && a.window > 0) lo = max(0, sb.len - a.window + 1 - j0);
-        if (ctx && (page < 0 || page >= a.pages)) hi = 0;
-        const int next_page = blk + 1 < blk1 ? page_at(blk + 1) : 0;
-        const bool edge = !ctx || lo > 0 || hi < kChunk;
-        uint64_t see = ~0ull, real = ~0ull;  // keys that this row sees; draft tokens that are not padding
-        auto draft_word = [&](int x) {       // of the draft's tokens in this block, those in row x's mask
-          if (a.mask) return a.mask[((int64_t)b * a.T + x) * a.words + blk - sb.np];
-          return (uint64_t)(x - j0 >= 63 ? ~0ull : (x < j0 ? 0ull : (2ull << (x - j0)) - 1));
-        };
-        if (edge || (a.window > 0 && j0 <= far - a.window)) {
+        const bool inner = blk >= in0 && blk < in1 && !holes;
+        uint64_t see = ~0ull;  // keys that this row sees
+        if (__builtin_expect(!inner, 0)) {
+          const bool ctx = blk < sb.np;
+          const int j0 = ctx ? (sb.p0 + blk) * kChunk : (blk - sb.np) * kChunk;
+          // Keys lo .. hi - 1 of the block exist.
+          int lo = 0, hi = min(kChunk, (ctx ? sb.len : a.T) - j0);
+          if (ctx && a.window > 0) lo = max(0, sb.len - a.window + 1 - j0);
+          if (ctx && holes) {
+            const int page = page_at(blk);
+            if (page < 0 || page >= a.pages) hi = 0;
+          }
+          uint64_t real = ~0ull;          // draft tokens that are not padding
+          auto draft_word = [&](int x) {  // of the draft's tokens in this block, those in row x's mask
+            if (a.mask) return a.mask[((int64_t)b * a.T + x) * a.words + blk - sb.np];
+            return (uint64_t)(x - j0 >= 63 ? ~0ull : (x < j0 ? 0ull : (2ull << (x - j0)) - 1));
+          };
           int c0 = lo;
           if (ctx && a.window > 0) c0 = max(c0, pos - a.window + 1 - j0);
           c0 = min(c0, kChunk);
@@ -290,112 +294,116 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             }
             see = word;
           }
-        }
-        if (edge) {
-          // V's rows that no row of the tile sees become zeros.
-          uint64_t used = hi == 64 ? ~0ull : (1ull << max(hi, 0)) - 1;
-          used &= lo >= 64 ? 0ull : ~((1ull << lo) - 1);
-          if (!ctx) {
-            uint64_t any = 0;
-            for (int x = rt * kRows / a.g + lane; x < min(a.T, (rt * kRows + kRows - 1) / a.g + 1); x += 32)
-              if (token_position(a, b, x, sb.len) >= 0) any |= draft_word(x);
-            any &= real;
-            used &= ((uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32) | __reduce_or_sync(kAll, (uint32_t)any);
-          }
-          const int at = tiles_read + (blk + 1 < blk1 ? 2 + 2 * (blk - blk0) : 2 * n - 1);
-          ok = waited(&bar_full[at % NS], (at / NS) & 1, kSiteV, blk);
-          const int row = tid >> 1;
-          if (ok && !((used >> row) & 1)) {
+          if (!ctx || lo > 0 || hi < kChunk) {
+            // V's rows that no row of the CTA sees become zeros.
+            uint64_t used = hi == 64 ? ~0ull : (1ull << max(hi, 0)) - 1;
+            used &= lo >= 64 ? 0ull : ~((1ull << lo) - 1);
+            if (!ctx) {
+              uint64_t any = 0;
+              for (int x = rt * kRows / a.g + lane; x < min(a.T, ((rt + 1) * kRows - 1) / a.g + 1); x += 32)
+                if (token_position(a, b, x, sb.len) >= 0) any |= draft_word(x);
+              any &= real;
+              used &= ((uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32) | __reduce_or_sync(kAll, (uint32_t)any);
+            }
+            const int at = id + 2 * ((blk - blk0) / PB) + 1, part = (blk - blk0) % PB;
+            ok = waited(&bar_full[at % NS], (at / NS) & 1, kSiteV, blk);
+            if (ok && !((used >> (tid >> 1)) & 1)) {
 #pragma unroll
-            for (int s = 0; s < SUB; ++s)
+              for (int s = 0; s < SUB; ++s)
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint4*>(ring + (at % NS) * C::STAGE + s * kTile + row * 128 + (tid & 1) * 64 + u * 16) =
-                    make_uint4(0, 0, 0, 0);
+                for (int u = 0; u < 4; ++u)
+                  *reinterpret_cast<uint4*>(ring + (at % NS) * kSlot + (part + s) * kTile + (tid >> 1) * 128 + (tid & 1) * 64 + u * 16) =
+                      make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();
           }
-          tc::fence_async_smem();
         }
         ok = ok && waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
         if (!ok) break;
-        page = next_page;
         if (idle) {  // no row of this warp exists: what P holds for them goes nowhere
+          __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
           continue;
         }
         tc::fence_after();
-        const uint32_t tP = tS + 64 * (nth & 1) + lanes;
-        float s[2][32];
-        tc::ld32x32b_x32(tP, s[0]);
-        tc::ld32x32b_x32(tP + 32, s[1]);
-        tc::ld_wait_row(s[0]);
-        tc::ld_wait_row(s[1]);
-        if (see != ~0ull) {
-          const uint32_t w[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
+        const uint32_t tP = tS + 64 * (nth & 1);
+        // The weights by the reference in use; where a row's sum shows that it is outgrown (or
+        // there is none yet), once more by the new one.
+        bool exact = !settled;
+        uint32_t p[4][8];
+        float sum;
+        for (;;) {
+          float s[2][32];
+          tc::ld32x32b_x32(tP, s[0]);
+          tc::ld32x32b_x32(tP + 32, s[1]);
+          tc::ld_wait_row(s[0]);
+          tc::ld_wait_row(s[1]);
+          if (__builtin_expect(!inner, 0)) {
+            const uint32_t w[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((w[q] >> i) & 1)) s[q][i] = -CUDART_INF_F;
-        }
-        float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+              for (int i = 0; i < 32; ++i)
+                if (!((w[q] >> i) & 1)) s[q][i] = -CUDART_INF_F;
+          }
+          if (__builtin_expect(exact, 0)) {
+            float tops[4] = {mx, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 3] = tc::max3(tops[(i >> 1) & 3], s[q][i], s[q][i + 1]);
-        const float top = fmaxf(tc::max3(tops[0], tops[1], tops[2]), tops[3]);
-        const bool grow = (top - mx) * sl2 > kGrow || (mx == -CUDART_INF_F && top > mx);
-        if (__any_sync(kAll, grow)) {
-          const float now = grow ? top : mx;
-          const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
-          mx = now;
-          l *= f;
-          if (blk > blk0) {
-            ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
-            tc::fence_after();
+              for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 3] = tc::max3(tops[(i >> 1) & 3], s[q][i], s[q][i + 1]);
+            const float now = fmaxf(tc::max3(tops[0], tops[1], tops[2]), tops[3]);
+            const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
+            mx = now;
+            l *= f;
+            settled = __all_sync(kAll, mx != -CUDART_INF_F || pos < 0);
+            if (blk > blk0) {
+              ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
+              tc::fence_after();
 #pragma unroll
-            for (int q = 0; q < DH / 32; ++q) {
-              float o[32];
-              tc::ld32x32b_x32(tO + lanes + 32 * q, o);
-              tc::ld_wait_row(o);
+              for (int q = 0; q < DH / 32; ++q) {
+                float o[32];
+                tc::ld32x32b_x32(tO + 32 * q, o);
+                tc::ld_wait_row(o);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[8];
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 * i + e] * f);
-                tc::st32x32b_x8(tO + lanes + 32 * q + 8 * i, w);
+                  for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 * i + e] * f);
+                  tc::st32x32b_x8(tO + 32 * q + 8 * i, w);
+                }
               }
             }
           }
-        }
-        const float base = mx == -CUDART_INF_F ? 0.f : -mx * sl2;
-        const uint64_t k2 = tc::f2(sl2, sl2), b2 = tc::f2(base, base);
-        uint64_t sum[2] = {0, 0};
+          const float base = mx == -CUDART_INF_F ? 0.f : -mx * sl2;
+          const uint64_t k2 = tc::f2(sl2, sl2), b2 = tc::f2(base, base);
+          uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int i = 0; i < 16; ++i) {
               float x, y;
-              tc::uf2(tc::fma2(tc::f2(s[q][8 * i + 2 * e], s[q][8 * i + 2 * e + 1]), k2, b2), x, y);
+              tc::uf2(tc::fma2(tc::f2(s[q][2 * i], s[q][2 * i + 1]), k2, b2), x, y);
               x = tc::ex2(x);
               y = tc::ex2(y);
-              sum[e & 1] = tc::add2(sum[e & 1], tc::f2(x, y));
-              w[e] = pack_bf16(x, y);
+              sums[i & 3] = tc::add2(sums[i & 3], tc::f2(x, y));
+              p[2 * q + i / 8][i % 8] = pack_bf16(x, y);
             }
-            tc::st32x32b_x4(tP + 16 * q + 4 * i, w);
-          }
-        float x0, x1, x2, x3;
-        tc::uf2(sum[0], x0, x1);
-        tc::uf2(sum[1], x2, x3);
-        l += (x0 + x1) + (x2 + x3);
+          float x, y;
+          tc::uf2(tc::add2(tc::add2(sums[0], sums[1]), tc::add2(sums[2], sums[3])), x, y);
+          sum = x + y;
+          if (exact || !__any_sync(kAll, sum > kMost)) break;
+          exact = true;
+        }
+        l += sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
       }
-      tiles_read += 2 * n;
+      id += 2 * ((n + PB - 1) / PB);
       if (!ok) break;
       ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, -1);
       if (!ok) break;
@@ -408,7 +416,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
 #pragma unroll
       for (int q = 0; q < DH / 32; ++q) {
         float o[32];
-        tc::ld32x32b_x32(tO + lanes + 32 * q, o);
+        tc::ld32x32b_x32(tO + 32 * q, o);
         tc::ld_wait_row(o);
         if (!on) continue;
         if (whole) {
@@ -444,21 +452,22 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   __syncthreads();
   if (warp == 4) {
     tc::fence_after();
-    tc::tmem_dealloc(tmem_slot, 256);
+    tc::tmem_dealloc(tmem_slot, kCols);
   }
 }
 
 template <int DH>
 cudaError_t run_tc(const TreeArgs& a, cudaStream_t s) {
+  using C = Tc<DH>;
   CUtensorMap tk, tv, tkn, tvn;
   cudaError_t e = make_pages_tmap(&tk, a.kp, DH, a.Hkv, a.pages);
   if (e == cudaSuccess) e = make_pages_tmap(&tv, a.vp, DH, a.Hkv, a.pages);
   if (e == cudaSuccess) e = make_draft_tmap(&tkn, a.kn, DH, a.Hkv, a.T, a.B, a.kn_hs, a.kn_ts, a.kn_bs);
   if (e == cudaSuccess) e = make_draft_tmap(&tvn, a.vn, DH, a.Hkv, a.T, a.B, a.vn_hs, a.vn_ts, a.vn_bs);
-  if (e == cudaSuccess) e = allow_smem((const void*)tree_tc_kernel<DH>, Tc<DH>::SMEM);
+  if (e == cudaSuccess) e = allow_smem((const void*)tree_tc_kernel<DH>, C::SMEM);
   if (e != cudaSuccess) return e;
   launch_begin("tree_tc", s);
-  tree_tc_kernel<DH><<<a.grid * a.hl * a.nrt, kThreads, Tc<DH>::SMEM, s>>>(a, tk, tv, tkn, tvn);
+  tree_tc_kernel<DH><<<a.grid * a.hl * a.nrt, kThreads, C::SMEM, s>>>(a, tk, tv, tkn, tvn);
   return launch_end("tree_tc", s);
 }
 
