@@ -631,7 +631,7 @@ extern "C" gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const g
   if (B < 1 || L < 1 || H < 1 || Hkv < (k ? 1 : 0) || (!k && Hkv != 0))
     return fail(GCA_ERR_INVALID_ARG, "B, L, H must be >= 1, and Hkv >= 1 with k, 0 without (got %d, %d, %d, %d)", B, L, H, Hkv);
   if (H > 65535 || Hkv > 65535) return fail(GCA_ERR_INVALID_ARG, "H and Hkv must be <= 65535");
-  if ((int64_t)B * L > INT32_MAX) return fail(GCA_ERR_INVALID_ARG, "B * L must be below 2^31");
+  if ((int64_t)B * L > INT32_MAX || B > 65535) return fail(GCA_ERR_INVALID_ARG, "B * L must be below 2^31, B at most 65535");
   if (dh < 2 || dh > 256) return fail(GCA_ERR_UNSUPPORTED, "head dim must be in 2..256 (got %d)", dh);
   if (rot < 2 || rot > dh || rot % 2) return fail(GCA_ERR_INVALID_ARG, "rot must be even in 2..dh (got %d)", rot);
   if (!freq || (reinterpret_cast<uintptr_t>(freq) & 7)) return fail(GCA_ERR_INVALID_ARG, "freq must be 8-byte aligned and not NULL");
