@@ -60,6 +60,7 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& total) {
 // One CTA, one thread an entry: what each entry needs, the free pages in order, the tables.
 __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a) {
   const CacheArgs& c = a.c;
+  let_next();
   __shared__ int all[kCacheEntries], start[kCacheEntries], first[kCacheEntries];
   __shared__ int red[32];
   const int i = threadIdx.x;
@@ -148,45 +149,60 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a)
   }
 }
 
-// CTA (page step, entry): the rows of one page, a quarter of them a CTA.
+// CTA (page step, entry): the rows of one page, a quarter of them a CTA.  A thread has the
+// loads of kFly units of K and of V on their way before it stores the first.
 constexpr int kRowParts = 4;
+constexpr int kFly = 3;
 __global__ void __launch_bounds__(256) append_rows_kernel(AppendArgs a) {
   const CacheArgs& c = a.c;
+  after_previous();
   const int i = blockIdx.y, step = blockIdx.x / kRowParts, part = blockIdx.x % kRowParts;
   const int4 rec = reinterpret_cast<const int4*>(a.rec)[i];
   const int old = rec.x, now = old + rec.y, slot = rec.w;
   const int p = old / kChunk + step;
   if (rec.y == 0 || (int64_t)p * kChunk >= now) return;
   const int64_t page = c.table[(int64_t)slot * c.width + p];
-  const int units = (int)(c.token_bytes / 16);
-  const int per = kChunk / kRowParts, r0 = part * per;
+  const int units = (int)(c.token_bytes / 16), per = kChunk / kRowParts, r0 = part * per;
   const bool copied = rec.z >= 0 && step == 0;
-  for (int u = threadIdx.x; u < per * units; u += blockDim.x) {
-    const int r = r0 + u / units, x = u % units, j = p * kChunk + r;
-    if (j >= now) break;
-    const int64_t to = (page * kChunk + r) * c.token_bytes + x * 16;
-    const unsigned char *k, *v;
-    if (j >= old) {
-      int t = j - old;
-      if (a.path) {
-        t = a.path[(int64_t)i * a.T + t];
-        if (t < 0 || t >= a.T) {
-          if (x == 0) flag_bad_index(c.err, t);
-          continue;
+  // Rows first .. end - 1 of this part are written.
+  const int first = copied ? r0 : max(r0, old - p * kChunk), end = min(r0 + per, now - p * kChunk);
+  for (int u0 = first * units + threadIdx.x; u0 < end * units; u0 += kFly * blockDim.x) {
+    uint4 kv[kFly], vv[kFly];
+    bool on[kFly];
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      const int u = u0 + f * blockDim.x;
+      on[f] = u < end * units;
+      if (!on[f]) continue;
+      const int r = u / units, x = u - r * units, t = p * kChunk + r - old;  // row of the page; token of the entry
+      const unsigned char *k, *v;
+      if (t >= 0) {
+        int row = t;
+        if (a.path) {
+          row = a.path[(int64_t)i * a.T + t];
+          if (row < 0 || row >= a.T) {
+            if (x == 0) flag_bad_index(c.err, row);
+            on[f] = false;
+            continue;
+          }
         }
+        k = a.kn + i * a.kn_bs + row * a.kn_ts + x * 16;
+        v = a.vn + i * a.vn_bs + row * a.vn_ts + x * 16;
+      } else {
+        const int64_t from = ((int64_t)rec.z * kChunk + r) * c.token_bytes + x * 16;
+        k = c.kp + from;
+        v = c.vp + from;
       }
-      k = a.kn + i * a.kn_bs + t * a.kn_ts + x * 16;
-      v = a.vn + i * a.vn_bs + t * a.vn_ts + x * 16;
-    } else if (copied) {
-      const int64_t from = ((int64_t)rec.z * kChunk + r) * c.token_bytes + x * 16;
-      k = c.kp + from;
-      v = c.vp + from;
-    } else {
-      continue;
+      kv[f] = *reinterpret_cast<const uint4*>(k);
+      vv[f] = *reinterpret_cast<const uint4*>(v);
     }
-    const uint4 kv = *reinterpret_cast<const uint4*>(k), vv = *reinterpret_cast<const uint4*>(v);
-    *reinterpret_cast<uint4*>(c.kp + to) = kv;
-    *reinterpret_cast<uint4*>(c.vp + to) = vv;
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      if (!on[f]) continue;
+      const int64_t to = page * kChunk * c.token_bytes + (int64_t)(u0 + f * blockDim.x) * 16;
+      *reinterpret_cast<uint4*>(c.kp + to) = kv[f];
+      *reinterpret_cast<uint4*>(c.vp + to) = vv[f];
+    }
   }
 }
 
@@ -253,6 +269,7 @@ __global__ void __launch_bounds__(1024) trim_kernel(CacheArgs c, const int32_t* 
 // below n, in order: no other choice moves fewer.  Three launches: uses per part of the
 // pool; the two lists; the rows and the tables.
 __global__ void __launch_bounds__(256) compact_count_kernel(CompactArgs a) {
+  let_next();
   const int64_t per = (a.c.pages + kCompactParts - 1) / kCompactParts;
   const int64_t p0 = min(blockIdx.x * per, a.c.pages), p1 = min(p0 + per, a.c.pages);
   int n = 0;
@@ -271,6 +288,8 @@ __global__ void __launch_bounds__(1024) compact_lists_kernel(CompactArgs a) {
   __shared__ int red[32];
   __shared__ int cnt[kCompactParts];
   __shared__ int extra;
+  after_previous();
+  let_next();
   const int64_t per = (a.c.pages + kCompactParts - 1) / kCompactParts;
   if (threadIdx.x < kCompactParts) cnt[threadIdx.x] = a.counts[threadIdx.x];
   if (threadIdx.x == 0) extra = 0;
@@ -316,6 +335,7 @@ __global__ void __launch_bounds__(1024) compact_lists_kernel(CompactArgs a) {
 constexpr int kMoveParts = 8;
 __global__ void __launch_bounds__(256) compact_move_kernel(CompactArgs a) {
   const CacheArgs& c = a.c;
+  after_previous();
   const int n = a.live[0], moves = a.counts[kCompactParts];
   const int64_t page16 = kChunk * c.token_bytes / 16, per16 = page16 / kMoveParts;
   for (int64_t w = blockIdx.x; w < (int64_t)moves * kMoveParts; w += gridDim.x) {
@@ -323,10 +343,20 @@ __global__ void __launch_bounds__(256) compact_move_kernel(CompactArgs a) {
     const int64_t src = a.movers[k] * page16 + part * per16, dst = a.holes[k] * page16 + part * per16;
     const uint4 *ks = reinterpret_cast<const uint4*>(c.kp) + src, *vs = reinterpret_cast<const uint4*>(c.vp) + src;
     uint4 *kd = reinterpret_cast<uint4*>(c.kp) + dst, *vd = reinterpret_cast<uint4*>(c.vp) + dst;
-    for (int64_t u = threadIdx.x; u < per16; u += blockDim.x) {
-      const uint4 x = ks[u], y = vs[u];
-      kd[u] = x;
-      vd[u] = y;
+    for (int64_t u = threadIdx.x; u < per16; u += kFly * blockDim.x) {
+      uint4 x[kFly], y[kFly];
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+        if (u + f * blockDim.x >= per16) continue;
+        x[f] = ks[u + f * blockDim.x];
+        y[f] = vs[u + f * blockDim.x];
+      }
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+        if (u + f * blockDim.x >= per16) continue;
+        kd[u + f * blockDim.x] = x[f];
+        vd[u + f * blockDim.x] = y[f];
+      }
     }
     if (part == 0 && threadIdx.x == 0) {
       c.refs[a.holes[k]] = c.refs[a.movers[k]];
@@ -366,11 +396,12 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s) {
   launch_begin("cache_append_plan", s);
   append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
   cudaError_t e = launch_end("cache_append_plan", s);
-  if (e != cudaSuccess || a.T == 0) return e;
+  if (e != cudaSuccess) return e;
   const int steps = (a.T + kChunk - 1) / kChunk + 1;
   launch_begin("cache_append_rows", s);
-  append_rows_kernel<<<dim3(steps * kRowParts, a.c.n), 256, 0, s>>>(a);
-  return launch_end("cache_append_rows", s);
+  e = launch_after(append_rows_kernel, dim3(steps * kRowParts, a.c.n), dim3(256), s, a);
+  const cudaError_t last = launch_end("cache_append_rows", s);
+  return e != cudaSuccess ? e : last;
 }
 
 cudaError_t launch_cache_fork(const CacheArgs& c, const int32_t* dst, cudaStream_t s) {
@@ -391,12 +422,13 @@ cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s) {
   cudaError_t e = launch_end("cache_compact_count", s);
   if (e != cudaSuccess) return e;
   launch_begin("cache_compact_lists", s);
-  compact_lists_kernel<<<kCompactParts, 1024, 0, s>>>(a);
-  e = launch_end("cache_compact_lists", s);
-  if (e != cudaSuccess) return e;
+  e = launch_after(compact_lists_kernel, dim3(kCompactParts), dim3(1024), s, a);
+  cudaError_t last = launch_end("cache_compact_lists", s);
+  if (e != cudaSuccess || last != cudaSuccess) return e != cudaSuccess ? e : last;
   launch_begin("cache_compact_move", s);
-  compact_move_kernel<<<kSMs * 4, 256, 0, s>>>(a);
-  return launch_end("cache_compact_move", s);
+  e = launch_after(compact_move_kernel, dim3(kSMs * 6), dim3(256), s, a);
+  last = launch_end("cache_compact_move", s);
+  return e != cudaSuccess ? e : last;
 }
 
 cudaError_t launch_cache_lookup(const CacheArgs& c, const int32_t* idx, int per, int32_t* out, cudaStream_t s) {

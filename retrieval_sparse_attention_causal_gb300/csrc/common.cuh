@@ -44,6 +44,13 @@ __device__ __forceinline__ void flag_timeout(ErrWord* e, int site = 0, int cta =
   }
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel launched by launch_after() may start before the one ahead of it in the stream has
+// ended: what that one writes is there after after_previous().  What was there before that
+// one began may be read at once.  The one ahead lets it start with let_next().
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- element access
 template <typename T> struct Elem;
 template <> struct Elem<float> {

@@ -17,6 +17,22 @@ struct ErrWord;
 void launch_begin(const char* name, cudaStream_t s);
 cudaError_t launch_end(const char* name, cudaStream_t s);
 
+// Launches a kernel that may start before the previous one of the stream has ended (it waits
+// for it with after_previous()): its launch and its first steps overlap that one's end.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // Records `msg` as the calling thread's error detail and returns `s`.
 int set_error_detail(const char* msg);
 

@@ -35,8 +35,10 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
   float* Vs = Ks + 64 * QS;
   float* Ps = Vs + 64 * QS;
   __shared__ int row_pos[MT];
-  __shared__ unsigned long long used_s;
+  __shared__ unsigned long long used_s, row_see[MT];
+  __shared__ uint32_t real_s[2];
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  let_next();
   const Share sh = my_share(a);
   const float sl2 = a.scale * kTreeLog2e;
   const int R = a.T * a.g, rt = my_rows(a);
@@ -55,15 +57,15 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
     const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     const int rows = min(MT, R - rt * MT);
     __syncthreads();
-    for (int i = tid; i < MT * DH; i += kSimtThreads) {
-      const int r = i / DH, d = i - r * DH;
-      float v = 0.f;
+    for (int i = tid; i < MT * DH / 4; i += kSimtThreads) {
+      const int r = i / (DH / 4), d = i % (DH / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
         int t, h;
         row_of(a, rt * MT + r, m, t, h);
-        v = Elem<T>::ld(reinterpret_cast<const T*>(a.q) + b * a.q_bs + t * a.q_ts + h * a.q_hs + d);
+        v = *reinterpret_cast<const float4*>(reinterpret_cast<const T*>(a.q) + b * a.q_bs + t * a.q_ts + h * a.q_hs + d);
       }
-      Qs[r * QS + d] = v;
+      *reinterpret_cast<float4*>(Qs + r * QS + d) = v;
     }
     if (tid < MT) row_pos[tid] = tid < rows ? (int)token_position(a, b, (rt * MT + tid) / a.g, sb.len) : -1;
     float mx[RT], l[RT], o[RT][NC * CV];
@@ -100,24 +102,49 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
         vts = a.vn_ts;
       }
       __syncthreads();  // the last block's readers are done; row_pos is written
-      if (tid == 0) used_s = ctx ? ~0ull : 0ull;
-      __syncthreads();
-      if (!ctx) {  // draft tokens that some row of the tile sees
-        for (int k = tid; k < kChunk; k += kSimtThreads) {
-          bool any = false;
-          if (k < hi && token_position(a, b, j0 + k, sb.len) >= 0)
-            for (int r = 0; r < rows && !any; r += 1) any = row_pos[r] >= 0 && sees_draft(a, b, (rt * MT + r) / a.g, j0 + k);
-          if (any) atomicOr(&used_s, 1ull << k);
+      // Which keys each row sees, one bit a key; of the draft's, those that any row sees.
+      if (!ctx) {
+        if (tid < 64) {
+          const bool real = j0 + tid < a.T && token_position(a, b, j0 + tid, sb.len) >= 0;
+          const uint32_t w = __ballot_sync(0xffffffffu, real);
+          if ((tid & 31) == 0) real_s[tid >> 5] = w;
         }
+        if (tid == 0) used_s = 0;
         __syncthreads();
       }
-      const unsigned long long used = used_s;
+      if (tid < MT) {
+        const int pos = row_pos[tid];
+        unsigned long long see = 0;
+        if (pos >= 0) {
+          int c0 = lo;
+          if (ctx && a.window > 0) c0 = min(max(c0, pos - a.window + 1 - j0), kChunk);
+          see = c0 >= hi ? 0ull : (hi == 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << c0) - 1);
+          if (!ctx) {
+            const int t = (rt * MT + tid) / a.g;
+            see &= ((unsigned long long)real_s[1] << 32) | real_s[0];
+            see &= a.mask ? a.mask[((int64_t)b * a.T + t) * a.words + (j0 >> 6)]
+                          : (t - j0 >= 63 ? ~0ull : (t < j0 ? 0ull : (2ull << (t - j0)) - 1));
+            if (a.window > 0 && pos - a.window >= sb.len)  // the window ends inside the draft
+              for (int u = 0; u < kChunk; ++u)
+                if ((see >> u) & 1 && token_position(a, b, j0 + u, sb.len) <= (int64_t)pos - a.window) see &= ~(1ull << u);
+            atomicOr(&used_s, see);
+          }
+        }
+        row_see[tid] = see;
+      }
+      __syncthreads();
+      const unsigned long long used = ctx ? ~0ull : used_s;
       // Rows that nobody sees are zeros: a weight of 0 times what lies there must stay 0.
-      for (int i = tid; i < kChunk * DH; i += kSimtThreads) {
-        const int r = i / DH, d = i - r * DH;
-        const bool on = r >= lo && r < hi && ((used >> r) & 1);
-        Ks[r * QS + d] = on ? Elem<T>::ld(kb + r * kts + d) : 0.f;
-        Vs[r * QS + d] = on ? Elem<T>::ld(vb + r * vts + d) : 0.f;
+#pragma unroll 4
+      for (int i = tid; i < kChunk * DH / 4; i += kSimtThreads) {
+        const int r = i / (DH / 4), d = i % (DH / 4) * 4;
+        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+        if (r >= lo && r < hi && ((used >> r) & 1)) {
+          kv = *reinterpret_cast<const float4*>(kb + r * kts + d);
+          vv = *reinterpret_cast<const float4*>(vb + r * vts + d);
+        }
+        *reinterpret_cast<float4*>(Ks + r * QS + d) = kv;
+        *reinterpret_cast<float4*>(Vs + r * QS + d) = vv;
       }
       __syncthreads();
       float s[RT][4];
@@ -140,18 +167,12 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const int r = ty * RT + i, pos = row_pos[r];
+        const int r = ty * RT + i;
+        const unsigned long long see = row_see[r];
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int k = tx + 16 * j;
-          bool on = pos >= 0 && k >= lo && k < hi;
-          if (ctx) {
-            on = on && (a.window <= 0 || j0 + k > pos - a.window);
-          } else if (on) {
-            const int64_t up = token_position(a, b, j0 + k, sb.len);
-            on = up >= 0 && sees_draft(a, b, (rt * MT + r) / a.g, j0 + k) && (a.window <= 0 || up > (int64_t)pos - a.window);
-          }
+          const bool on = (see >> (tx + 16 * j)) & 1;
           s[i][j] = on ? s[i][j] * sl2 : -CUDART_INF_F;
           top = fmaxf(top, s[i][j]);
         }
@@ -236,6 +257,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeArgs a, int
   const SeqBlocks sb = seq_blocks(a, b, false);
   const int s0 = items_before(a, b, false) + hg / a.hl * sb.nb;
   const int c0 = owner_of(sh, s0), c1 = owner_of(sh, s0 + sb.nb - 1);  // shares of its first and last block
+  after_previous();      // (by every CTA: the grid must not end before the one ahead of it)
   if (c0 == c1) return;  // finished there
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4, ps = 16 / rg, ri = y % rg, pi = y / rg;
   const int most = min(a.rows, a.T * a.g - rt * a.rows), v = blockIdx.z * rg + ri;
@@ -420,8 +442,9 @@ cudaError_t run_dh(const TreeArgs& a, Kind kind, cudaStream_t s) {
   int rg = 8;
   while (rg > 1 && (rg > rows || parts * rg > 64)) rg >>= 1;
   launch_begin("tree_join", s);
-  tree_join_kernel<T, DH><<<dim3(tiles, a.B, (rows + rg - 1) / rg), kJoinThreads, 0, s>>>(a, rg);
-  return launch_end("tree_join", s);
+  e = launch_after(tree_join_kernel<T, DH>, dim3(tiles, a.B, (rows + rg - 1) / rg), dim3(kJoinThreads), s, a, rg);
+  const cudaError_t last = launch_end("tree_join", s);
+  return e != cudaSuccess ? e : last;
 }
 template <typename T>
 cudaError_t run(const TreeArgs& a, Kind kind, cudaStream_t s) {

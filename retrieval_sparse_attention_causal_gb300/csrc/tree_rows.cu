@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
   static_assert(kWarps * G::KS * 32 * sizeof(uint4) <= sizeof both, "");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, c = lane & 3;
+  let_next();
   const Share sh = my_share(a);
   if (sh.lo >= sh.hi) return;
   const float sl2 = a.scale * kTreeLog2e;

@@ -128,12 +128,6 @@ __device__ __forceinline__ void row_of(const TreeArgs& a, int r, int m, int& t, 
   h = m * a.g + (r - t * a.g);
 }
 
-// Whether key u of the draft is seen by row t (mask words, or the causal chain), before the window.
-__device__ __forceinline__ bool sees_draft(const TreeArgs& a, int b, int t, int u) {
-  if (!a.mask) return u <= t;
-  return (a.mask[((int64_t)b * a.T + t) * a.words + (u >> 6)] >> (u & 63)) & 1;
-}
-
 // Position of token t (never below the context's length), or -1 for padding.
 __device__ __forceinline__ int64_t token_position(const TreeArgs& a, int b, int t, int len) {
   if (!a.positions) return (int64_t)len + t;

@@ -64,6 +64,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next();
   const Share sh = my_share(a);
   if (sh.lo >= sh.hi) return;
   if (tid == 0) {
