@@ -546,7 +546,7 @@ GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, cons
  * ------------------------------------------------------------------------------- */
 GCA_API gca_status gca_tree_plan(const int32_t* parents, const int32_t* lengths, int B, int T, uint64_t* mask,
                          int32_t* positions, void* ws, size_t ws_bytes, gca_stream_t stream);
-GCA_API size_t gca_tree_attention_scratch_size(int B, int T, int H, int heads, int dh, int width, gca_dtype dtype);
+GCA_API size_t gca_tree_attention_scratch_size(int B, int T, int H, int heads, int dh, int width, int window, gca_dtype dtype);
 GCA_API gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_new, const gca_heads* v_new,
                               const gca_cache* cache, int B, int T, int H, const uint64_t* mask,
                               const int32_t* positions, int window, float scale, void* o, float* lse, void* ws,

@@ -106,7 +106,7 @@ def _load():
         "gca_cache_compact": (I, [CP, P, P, SZ, P, SZ, P]),
         "gca_cache_lookup": (I, [CP, I, I, P, P, P, P, SZ, P]),
         "gca_tree_plan": (I, [P, P, I, I, P, P, P, SZ, P]),
-        "gca_tree_attention_scratch_size": (SZ, [I, I, I, I, I, I, I]),
+        "gca_tree_attention_scratch_size": (SZ, [I, I, I, I, I, I, I, I]),
         "gca_tree_attention": (I, [HP, HP, HP, CP, I, I, I, P, P, I, F, P, P, P, SZ, P, SZ, P]),
         "gca_check_error": (I, [P, P, ctypes.POINTER(I)]),
         "gca_launch_count": (U64, []),

@@ -827,9 +827,9 @@ extern "C" gca_status gca_tree_plan(const int32_t* parents, const int32_t* lengt
   return GCA_OK;
 }
 
-extern "C" size_t gca_tree_attention_scratch_size(int B, int T, int H, int heads, int dh, int width, gca_dtype dtype) {
-  if (B < 1 || T < 1 || T > GCA_MAX_DRAFT || heads < 1 || H < heads || H % heads || dh < 1 || width < 1) return 256;
-  return align256(tree_scratch_bytes(B, T, H, heads, dh, dtype == GCA_BF16, width));
+extern "C" size_t gca_tree_attention_scratch_size(int B, int T, int H, int heads, int dh, int width, int window, gca_dtype dtype) {
+  if (B < 1 || T < 1 || T > GCA_MAX_DRAFT || heads < 1 || H < heads || H % heads || dh < 1 || width < 1 || window < 0) return 256;
+  return align256(tree_scratch_bytes(B, T, H, heads, dh, dtype == GCA_BF16, width, window));
 }
 
 extern "C" gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_new, const gca_heads* v_new,
@@ -859,7 +859,7 @@ extern "C" gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_
     return fail(GCA_ERR_UNSUPPORTED, "B, H, T and the table's width are too large together");
   if (!o || !lse || !aligned16(o)) return fail(GCA_ERR_INVALID_ARG, "o and lse must not be NULL, o 16-byte aligned");
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
-  if ((st = check_scratch(scratch, scratch_bytes, gca_tree_attention_scratch_size(B, T, H, cache->heads, cache->dh, cache->width, cache->dtype))) != GCA_OK)
+  if ((st = check_scratch(scratch, scratch_bytes, gca_tree_attention_scratch_size(B, T, H, cache->heads, cache->dh, cache->width, window, cache->dtype))) != GCA_OK)
     return st;
   TreeArgs a{};
   a.q = q->data; a.q_bs = q->batch_stride; a.q_ts = q->token_stride; a.q_hs = q->head_stride;

@@ -263,7 +263,7 @@ PyObject* attend(const gca_cache& c, On& on, Args x, Args y) {
   if (!out) o_new = at::empty({B, T, H, dh}, on.options(q.scalar_type()));
   if (!lse) l_new = at::empty({B, T, H}, on.options(at::kFloat));
   const Word w(ws, on);
-  const Scratch s(gca_tree_attention_scratch_size((int)B, (int)T, (int)H, c.heads, c.dh, c.width, c.dtype), on);
+  const Scratch s(gca_tree_attention_scratch_size((int)B, (int)T, (int)H, c.heads, c.dh, c.width, window, c.dtype), on);
   const gca_heads hq = heads(q), hk = heads(kn), hv = heads(vn);
   check(gca_tree_attention(&hq, &hk, &hv, &c, (int)B, (int)T, (int)H, mask ? static_cast<const uint64_t*>(mask->data_ptr()) : nullptr,
                            pos ? static_cast<const int32_t*>(pos->data_ptr()) : nullptr, window, scale, out ? out->data_ptr() : o_new.data_ptr(),

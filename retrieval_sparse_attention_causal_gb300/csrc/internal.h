@@ -226,7 +226,7 @@ struct TreeArgs {
 };
 cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);  // bf16, 16 rows a CTA (tree_rows.cu)
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t s);    // bf16, dh 64 or 128 (tree_tc.cu)
-size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16, int width);
+size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16, int width, int window);
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s);
 struct TreePlanArgs {
   const int32_t* parents; const int32_t* lengths;

@@ -58,12 +58,18 @@ __device__ __forceinline__ int owner_of(const Share& s, int item) {
   return item < t ? item / (s.q + 1) : s.rem + (item - t) / s.q;
 }
 
-// Items of the sequences before b (or of all of them), summed by one warp.  (The host sees to
-// it that all items together stay below 2^31.)
-__device__ __forceinline__ int items_before(const TreeArgs& a, int b, bool flag) {
-  int sum = 0;
-  for (int i = threadIdx.x & 31; i < b; i += 32) sum += seq_blocks(a, i, flag).nb;
-  return __reduce_add_sync(0xffffffffu, sum) * (a.Hkv / (a.hw * a.hl));
+// Items of all sequences, and of those before b, summed by one warp.  (The host sees to it that
+// all items together stay below 2^31.)
+__device__ __forceinline__ int all_items(const TreeArgs& a, int b, int& before, bool flag) {
+  int sum = 0, part = 0;
+  for (int i = threadIdx.x & 31; i < a.B; i += 32) {
+    const int n = seq_blocks(a, i, flag).nb;
+    sum += n;
+    if (i < b) part += n;
+  }
+  const int sets = a.Hkv / (a.hw * a.hl);
+  before = __reduce_add_sync(0xffffffffu, part) * sets;
+  return __reduce_add_sync(0xffffffffu, sum) * sets;
 }
 __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
   Share s;
@@ -77,7 +83,8 @@ __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
 // This CTA's share; called by whole warps, each for itself.
 __device__ __forceinline__ Share my_share(const TreeArgs& a) {
   const int lane = threadIdx.x & 31, tiles = a.Hkv / (a.hw * a.hl), share = blockIdx.x / (a.hl * a.nrt);
-  Share s = shares(a, items_before(a, a.B, blockIdx.x == 0 && threadIdx.x < 32));
+  int before;
+  Share s = shares(a, all_items(a, 0, before, blockIdx.x == 0 && threadIdx.x < 32));
   s.lo = share < s.G ? first_item(s, share) : s.W;
   s.hi = share < s.G ? first_item(s, share + 1) : s.W;
   s.b = s.off = 0;

@@ -34,7 +34,6 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 192;
 constexpr int kRows = 128;       // the lanes of TMEM
-constexpr int kCols = 256;       // of TMEM: two logit buffers of 64, the output
 constexpr int kTile = 8192;     // 64 tokens x 64 elements
 constexpr int kSlot = 2 * kTile;
 constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
@@ -46,21 +45,24 @@ struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
   static constexpr int PB = 2 / SUB;                // blocks of 64 keys of a ring slot: 16 KB of K or of V
   static constexpr int QB = 2 * kTile * SUB;        // a row tile of Q
+  static constexpr int CTAS = 2;                    // on an SM
+  static constexpr int SB = 2;                      // logit buffers
+  static constexpr int COLS = 256;                  // of TMEM: the logit buffers, the output behind them
   static constexpr int NS = DH == 64 ? 5 : 4;       // ring slots
   static constexpr int SMEM = QB + NS * kSlot + 1024;
 };
 
 template <int DH>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Tc<DH>::CTAS)
 tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmKn, const __grid_constant__ CUtensorMap tmVn) {
   using C = Tc<DH>;
-  constexpr int SUB = C::SUB, NS = C::NS, PB = C::PB;
+  constexpr int SUB = C::SUB, NS = C::NS, PB = C::PB, SB = C::SB;
   constexpr uint32_t kIdS = tc::idesc_bf16(kRows, 64, false), kIdPV = tc::idesc_bf16(kRows, 64, true);
   extern __shared__ __align__(1024) unsigned char dsm[];
   unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = Qs + C::QB;
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o[2];
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[SB], bar_p[SB], bar_o[SB];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -73,7 +75,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       tc::mbar_init(&bar_empty[i], 1);
     }
     tc::mbar_init(&bar_q, 4);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SB; ++i) {
       tc::mbar_init(&bar_s[i], 1);
       tc::mbar_init(&bar_p[i], 4);
       tc::mbar_init(&bar_o[i], 1);
@@ -81,7 +83,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     abort_s = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 4) tc::tmem_alloc(&tmem_slot, kCols);
+  if (warp == 4) tc::tmem_alloc(&tmem_slot, C::COLS);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -187,9 +189,9 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       tc::fence_after();
 #pragma unroll
       for (int s = 0; s < SUB; ++s)
-        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (i & 1), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
+        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (i % SB), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
                                                 s ? 1u : 0u);
-      tc::commit_warp(&bar_s[i & 1]);
+      tc::commit_warp(&bar_s[i % SB]);
       release(x, 0, n);
     };
     while (ok && segment()) {
@@ -199,17 +201,18 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       ++seg;
       if (ok) logits(0, nth, n);
       for (int x = 0; x < n && ok; ++x, ++nth) {
-        if (x + 1 < n) logits(x + 1, nth + 1, n);
+        if (SB > 1 && x + 1 < n) logits(x + 1, nth + 1, n);
         const uint32_t v = operand(x, 1);
-        ok = ok && waited(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, x);
+        ok = ok && waited(&bar_p[nth % SB], (nth / SB) & 1, kSiteP, x);
         if (!ok) break;
         tc::fence_after();
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
-          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 128 + 64 * s, tmem + 64 * (nth & 1), tc::desc_mn(v + s * kTile), kIdPV,
+          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 64 * (SB + s), tmem + 64 * (nth % SB), tc::desc_mn(v + s * kTile), kIdPV,
                                                x > 0 ? 1u : 0u);
-        tc::commit_warp(&bar_o[nth & 1]);
+        tc::commit_warp(&bar_o[nth % SB]);
         release(x, 1, n);
+        if (SB == 1 && x + 1 < n) logits(x + 1, nth + 1, n);
       }
       id += 2 * ((n + PB - 1) / PB);
     }
@@ -217,29 +220,47 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     // ---------------------------------------------------------------- softmax
     const float sl2 = a.scale * kTreeLog2e;
     const int R = a.T * a.g;
-    const uint32_t tS = tmem + ((uint32_t)(32 * warp) << 16), tO = tS + 128;
+    const uint32_t tS = tmem + ((uint32_t)(32 * warp) << 16), tO = tS + 64 * SB;
     int nth = 0, id = 0;  // blocks and ring slots so far
     int slot = 0;
     while (ok && segment()) {
       const int m = my_heads(a, tile), r = rt * kRows + tid, n = blk1 - blk0;
       const bool on = r < R, idle = rt * kRows + 32 * warp >= R;
       int t = 0, h = 0, pos = -1;
-      {
-        uint4 w[DH / 8];
-        if (on) {
-          row_of(a, r, m, t, h);
-          pos = (int)token_position(a, b, t, sb.len);
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.q) + b * a.q_bs + t * a.q_ts + h * a.q_hs);
+      // What the segment asks of memory, all of it before the first use: Q, the row's position, the
+      // page numbers, and of the draft's first block the mask and the positions.
+      auto page_at = [&](int blk) { return a.table[(int64_t)b * a.width + sb.p0 + blk]; };
+      auto draft_word = [&](int x, int w) {  // of the draft's tokens 64 w .. 64 w + 63, those in token x's mask
+        if (a.mask) return a.mask[((int64_t)b * a.T + x) * a.words + w];
+        return (uint64_t)(x - 64 * w >= 63 ? ~0ull : (x < 64 * w ? 0ull : (2ull << (x - 64 * w)) - 1));
+      };
+      const int32_t* where = a.positions ? a.positions + (int64_t)b * a.T : nullptr;
+      if (on) row_of(a, r, m, t, h);
+      uint4 w[DH / 8];
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.q) + b * a.q_bs + t * a.q_ts + h * a.q_hs);
 #pragma unroll
-          for (int u = 0; u < DH / 8; ++u) w[u] = src[u];
-        } else {
-#pragma unroll
-          for (int u = 0; u < DH / 8; ++u) w[u] = make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < DH / 8; ++u) w[u] = on ? src[u] : make_uint4(0, 0, 0, 0);
+      if (on) pos = (int)token_position(a, b, t, sb.len);
+      const int held = min(blk1, sb.np);
+      int page = blk0 + lane < held ? page_at(blk0 + lane) : 0;
+      const bool draft = blk1 > sb.np;
+      const int x0 = rt * kRows / a.g + lane, x1 = min(a.T, ((rt + 1) * kRows - 1) / a.g + 1);  // tokens of the CTA's rows
+      uint64_t own = 0, any = 0;  // of the first draft block: this row's mask, all rows' masks
+      int real0 = 0, real1 = 0;   // positions of its tokens
+      if (draft) {
+        if (on) own = draft_word(t, 0);
+        for (int x = x0; x < x1; x += 32) {
+          const int p = where ? where[x] : 0;
+          const uint64_t d = draft_word(x, 0);
+          any |= p >= 0 ? d : 0;
         }
-#pragma unroll
-        for (int u = 0; u < DH / 8; ++u)
-          *reinterpret_cast<uint4*>(Qs + (u / 8) * 2 * kTile + swz<128>(tid, u % 8)) = w[u];
+        if (where) {
+          real0 = where[min(lane, a.T - 1)];
+          real1 = where[min(32 + lane, a.T - 1)];
+        }
       }
+#pragma unroll
+      for (int u = 0; u < DH / 8; ++u) *reinterpret_cast<uint4*>(Qs + (u / 8) * 2 * kTile + swz<128>(tid, u % 8)) = w[u];
       tc::fence_async_smem();
       tc::fence_before();
       __syncwarp();
@@ -248,10 +269,9 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       // Blocks in0 .. in1 - 1 are seen whole by every row of this warp, unless there are holes.
       const int far = max(__reduce_max_sync(kAll, pos), sb.len);
       const int in0 = a.window > 0 && far >= a.window ? (far - a.window) / kChunk + 1 - sb.p0 : 0, in1 = sb.len / kChunk - sb.p0;
-      auto page_at = [&](int blk) { return a.table[(int64_t)b * a.width + sb.p0 + blk]; };
-      bool hole = false;  // a page that is not held
-      for (int blk = blk0 + lane; blk < min(blk1, sb.np); blk += 32) {
-        const int page = page_at(blk);
+      bool hole = page < 0 || page >= a.pages;  // a page that is not held
+      for (int blk = blk0 + 32 + lane; blk < held; blk += 32) {
+        page = page_at(blk);
         hole = hole || page < 0 || page >= a.pages;
       }
       const bool holes = __any_sync(kAll, hole);
@@ -269,26 +289,29 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             const int page = page_at(blk);
             if (page < 0 || page >= a.pages) hi = 0;
           }
-          uint64_t real = ~0ull;          // draft tokens that are not padding
-          auto draft_word = [&](int x) {  // of the draft's tokens in this block, those in row x's mask
-            if (a.mask) return a.mask[((int64_t)b * a.T + x) * a.words + blk - sb.np];
-            return (uint64_t)(x - j0 >= 63 ? ~0ull : (x < j0 ? 0ull : (2ull << (x - j0)) - 1));
-          };
           int c0 = lo;
           if (ctx && a.window > 0) c0 = max(c0, pos - a.window + 1 - j0);
           c0 = min(c0, kChunk);
           see = c0 >= hi ? 0ull : ((hi == 64 ? ~0ull : (1ull << hi) - 1) & ~((c0 == 64 ? 0ull : 1ull << c0) - 1));
           if (c0 == 64) see = 0;
+          uint64_t seen = 0;  // by some row of the CTA
           if (!ctx) {
-            if (a.positions) {
-              const int32_t* p = a.positions + (int64_t)b * a.T;
-              const uint32_t p0 = __ballot_sync(kAll, j0 + lane < a.T && p[min(j0 + lane, a.T - 1)] >= 0);
-              const uint32_t p1 = __ballot_sync(kAll, j0 + 32 + lane < a.T && p[min(j0 + 32 + lane, a.T - 1)] >= 0);
-              real = ((uint64_t)p1 << 32) | p0;
+            uint64_t real = ~0ull;  // tokens that are not padding
+            if (j0 > 0) {
+              own = on ? draft_word(t, j0 / kChunk) : 0;
+              any = 0;
+              for (int x = x0; x < x1; x += 32)
+                if (!where || where[x] >= 0) any |= draft_word(x, j0 / kChunk);
+              if (where) {
+                real0 = where[min(j0 + lane, a.T - 1)];
+                real1 = where[min(j0 + 32 + lane, a.T - 1)];
+              }
             }
+            if (where) real = ((uint64_t)__ballot_sync(kAll, real1 >= 0) << 32) | __ballot_sync(kAll, real0 >= 0);
+            seen = real & (((uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32) | __reduce_or_sync(kAll, (uint32_t)any));
             uint64_t word = 0;
             if (pos >= 0) {
-              word = draft_word(t) & see & real;
+              word = own & see & real;
               if (a.window > 0 && pos - a.window >= sb.len)  // the window ends inside the draft
                 for (int u = 0; u < kChunk; ++u)
                   if ((word >> u) & 1 && token_position(a, b, j0 + u, sb.len) <= (int64_t)pos - a.window) word &= ~(1ull << u);
@@ -299,13 +322,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             // V's rows that no row of the CTA sees become zeros.
             uint64_t used = hi == 64 ? ~0ull : (1ull << max(hi, 0)) - 1;
             used &= lo >= 64 ? 0ull : ~((1ull << lo) - 1);
-            if (!ctx) {
-              uint64_t any = 0;
-              for (int x = rt * kRows / a.g + lane; x < min(a.T, ((rt + 1) * kRows - 1) / a.g + 1); x += 32)
-                if (token_position(a, b, x, sb.len) >= 0) any |= draft_word(x);
-              any &= real;
-              used &= ((uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32) | __reduce_or_sync(kAll, (uint32_t)any);
-            }
+            if (!ctx) used &= seen;
             const int at = id + 2 * ((blk - blk0) / PB) + 1, part = (blk - blk0) % PB;
             ok = waited(&bar_full[at % NS], (at / NS) & 1, kSiteV, blk);
             if (ok && !((used >> (tid >> 1)) & 1)) {
@@ -319,47 +336,47 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             tc::fence_async_smem();
           }
         }
-        ok = ok && waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
+        ok = ok && waited(&bar_s[nth % SB], (nth / SB) & 1, kSiteS, blk);
         if (!ok) break;
         if (idle) {  // no row of this warp exists: what P holds for them goes nowhere
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
+          if (lane == 0) tc::mbar_arrive(&bar_p[nth % SB]);
           continue;
         }
         tc::fence_after();
-        const uint32_t tP = tS + 64 * (nth & 1);
+        const uint32_t tP = tS + 64 * (nth % SB);
         // The weights by the reference in use; where a row's sum shows that it is outgrown (or
         // there is none yet), once more by the new one.
         bool exact = !settled;
         uint32_t p[4][8];
         float sum;
-        for (;;) {
-          float s[2][32];
-          tc::ld32x32b_x32(tP, s[0]);
-          tc::ld32x32b_x32(tP + 32, s[1]);
-          tc::ld_wait_row(s[0]);
-          tc::ld_wait_row(s[1]);
+        // 32 logits of the row, with what it does not see at -inf.
+        auto half = [&](float (&s)[32], int q) {
+          tc::ld32x32b_x32(tP + 32 * q, s);
+          tc::ld_wait_row(s);
           if (__builtin_expect(!inner, 0)) {
-            const uint32_t w[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
+            const uint32_t w = (uint32_t)(see >> (32 * q));
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((w[q] >> i) & 1)) s[q][i] = -CUDART_INF_F;
+            for (int i = 0; i < 32; ++i)
+              if (!((w >> i) & 1)) s[i] = -CUDART_INF_F;
           }
+        };
+        for (;;) {
           if (__builtin_expect(exact, 0)) {
-            float tops[4] = {mx, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+            float now = mx;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q) {
+              float s[32];
+              half(s, q);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 3] = tc::max3(tops[(i >> 1) & 3], s[q][i], s[q][i + 1]);
-            const float now = fmaxf(tc::max3(tops[0], tops[1], tops[2]), tops[3]);
+              for (int i = 0; i < 32; i += 2) now = tc::max3(now, s[i], s[i + 1]);
+            }
             const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
             mx = now;
             l *= f;
             settled = __all_sync(kAll, mx != -CUDART_INF_F || pos < 0);
             if (blk > blk0) {
-              ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
+              ok = waited(&bar_o[(nth - 1) % SB], ((nth - 1) / SB) & 1, kSiteO, blk);
               tc::fence_after();
 #pragma unroll
               for (int q = 0; q < DH / 32; ++q) {
@@ -380,16 +397,19 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
           const uint64_t k2 = tc::f2(sl2, sl2), b2 = tc::f2(base, base);
           uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 2; ++q) {
+            float s[32];
+            half(s, q);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float x, y;
-              tc::uf2(tc::fma2(tc::f2(s[q][2 * i], s[q][2 * i + 1]), k2, b2), x, y);
+              tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, b2), x, y);
               x = tc::ex2(x);
               y = tc::ex2(y);
               sums[i & 3] = tc::add2(sums[i & 3], tc::f2(x, y));
               p[2 * q + i / 8][i % 8] = pack_bf16(x, y);
             }
+          }
           float x, y;
           tc::uf2(tc::add2(tc::add2(sums[0], sums[1]), tc::add2(sums[2], sums[3])), x, y);
           sum = x + y;
@@ -402,11 +422,11 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
+        if (lane == 0) tc::mbar_arrive(&bar_p[nth % SB]);
       }
       id += 2 * ((n + PB - 1) / PB);
       if (!ok) break;
-      ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, -1);
+      ok = waited(&bar_o[(nth - 1) % SB], ((nth - 1) / SB) & 1, kSiteO, -1);
       if (!ok) break;
       tc::fence_after();
       if (pos < 0) l = 0.f;
@@ -453,7 +473,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   __syncthreads();
   if (warp == 4) {
     tc::fence_after();
-    tc::tmem_dealloc(tmem_slot, kCols);
+    tc::tmem_dealloc(tmem_slot, C::COLS);
   }
 }
 
