@@ -286,23 +286,22 @@ __global__ void __launch_bounds__(256) compact_count_kernel(CompactArgs a) {
 
 __global__ void __launch_bounds__(1024) compact_lists_kernel(CompactArgs a) {
   __shared__ int red[32];
-  __shared__ int cnt[kCompactParts];
   __shared__ int extra;
   after_previous();
   let_next();
   const int64_t per = (a.c.pages + kCompactParts - 1) / kCompactParts;
-  if (threadIdx.x < kCompactParts) cnt[threadIdx.x] = a.counts[threadIdx.x];
   if (threadIdx.x == 0) extra = 0;
   __syncthreads();
-  int n = 0, before = 0;  // pages in use: all, before this part
-  for (int k = 0; k < kCompactParts; ++k) {
-    if (k < (int)blockIdx.x) before += cnt[k];
-    n += cnt[k];
-  }
-  // Uses below page n: whole parts, and the part that n lies in.
+  // Pages in use: all, before this part, and below page n in whole parts (each warp for itself).
+  auto uses = [&](int parts) {
+    int sum = 0;
+    for (int k = threadIdx.x & 31; k < parts; k += 32) sum += a.counts[k];
+    return __reduce_add_sync(0xffffffffu, sum);
+  };
+  const int n = uses(kCompactParts);
+  int before = uses(blockIdx.x);
   const int whole = (int)(n / per);
-  int below = 0;
-  for (int k = 0; k < whole; ++k) below += cnt[k];
+  int below = uses(whole);
   int mine = 0;
   for (int64_t p = whole * per + threadIdx.x; p < n; p += blockDim.x) mine += a.c.refs[p] > 0;
 #pragma unroll

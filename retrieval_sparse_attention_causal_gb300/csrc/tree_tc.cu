@@ -275,6 +275,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         hole = hole || page < 0 || page >= a.pages;
       }
       const bool holes = __any_sync(kAll, hole);
+      bool ready = false;    // the block's logits were seen to be complete
       bool settled = false;  // every row that sees something has a reference
       for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
         const bool inner = blk >= in0 && blk < in1 && !holes;
@@ -336,7 +337,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             tc::fence_async_smem();
           }
         }
-        ok = ok && waited(&bar_s[nth % SB], (nth / SB) & 1, kSiteS, blk);
+        if (!ready) ok = ok && waited(&bar_s[nth % SB], (nth / SB) & 1, kSiteS, blk);
+        ready = false;
         if (!ok) break;
         if (idle) {  // no row of this warp exists: what P holds for them goes nowhere
           __syncwarp();
@@ -350,10 +352,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         bool exact = !settled;
         uint32_t p[4][8];
         float sum;
-        // 32 logits of the row, with what it does not see at -inf.
-        auto half = [&](float (&s)[32], int q) {
-          tc::ld32x32b_x32(tP + 32 * q, s);
-          tc::ld_wait_row(s);
+        // Of 32 logits of the row, what it does not see becomes -inf.
+        auto hide = [&](float (&s)[32], int q) {
           if (__builtin_expect(!inner, 0)) {
             const uint32_t w = (uint32_t)(see >> (32 * q));
 #pragma unroll
@@ -367,7 +367,9 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               float s[32];
-              half(s, q);
+              tc::ld32x32b_x32(tP + 32 * q, s);
+              tc::ld_wait_row(s);
+              hide(s, q);
 #pragma unroll
               for (int i = 0; i < 32; i += 2) now = tc::max3(now, s[i], s[i + 1]);
             }
@@ -396,10 +398,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
           const float base = mx == -CUDART_INF_F ? 0.f : -mx * sl2;
           const uint64_t k2 = tc::f2(sl2, sl2), b2 = tc::f2(base, base);
           uint64_t sums[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float s[32];
-            half(s, q);
+          auto weigh = [&](float (&s)[32], int q) {
+            hide(s, q);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float x, y;
@@ -409,7 +409,14 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
               sums[i & 3] = tc::add2(sums[i & 3], tc::f2(x, y));
               p[2 * q + i / 8][i % 8] = pack_bf16(x, y);
             }
-          }
+          };
+          float s0[32], s1[32];
+          tc::ld32x32b_x32(tP, s0);
+          tc::ld_wait_row(s0);
+          tc::ld32x32b_x32(tP + 32, s1);  // on its way while the first half is weighed
+          weigh(s0, 0);
+          tc::ld_wait_row(s1);
+          weigh(s1, 1);
           float x, y;
           tc::uf2(tc::add2(tc::add2(sums[0], sums[1]), tc::add2(sums[2], sums[3])), x, y);
           sum = x + y;
@@ -419,6 +426,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         l += sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
+        if (blk + 1 < blk1) ready = __all_sync(kAll, tc::mbar_try(&bar_s[(nth + 1) % SB], ((nth + 1) / SB) & 1)) != 0;
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
