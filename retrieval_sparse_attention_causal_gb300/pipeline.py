@@ -9,6 +9,11 @@
   prefill:                              retrieval (no noise) -> GCA forward
   decode:                               retrieval of one new chunk over all past chunks
                                         -> GCA forward over the retrieved chunks
+  window sublayer, training:            rotary -> window attention -> its backward -> the
+                                        gradient of rotary
+  window sublayer, decoding a draft:    plan of the tree -> rotary at its positions ->
+                                        attention over a paged cache; then the accepted
+                                        path goes into the cache
 
 Source: Paper-Notes page on "Efficient Length-Generalizable Attention via Causal
 Retrieval for Long-Context Language Modeling", sections 整体框架 (framework: chunks of
@@ -19,8 +24,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (CHUNK, Workspace, default_workspace, gather_chunks, gca_backward, gca_forward, launch_count,
-               retrieve_topk, scores_backward)
+from . import (CHUNK, PagedCache, Workspace, default_workspace, gather_chunks, gca_backward, gca_forward, launch_count,
+               retrieve_topk, rotary, rotary_backward, scores_backward, tree_plan, window_backward, window_forward)
 
 
 def landmark_view(o: torch.Tensor) -> torch.Tensor:
@@ -96,6 +101,51 @@ def decode_offload(q_new, k_host, v_host, q_lmk_new, k_lmk_store, topk=8, kv_sha
     kd, vd, il = gather_chunks(k_host, v_host, idx, kv_shared=kv_shared, ws=ws, k_dst=kd, v_dst=vd, idx_local=il)
     o, lse = gca_forward(q_new, kd, vd, il, scores, shift=0, ws=ws)
     return dict(idx=idx, scores=scores, o=o, lse=lse, idx_local=il)
+
+
+def decode_paged(q_new, cache: PagedCache, q_lmk_new, k_lmk_store, topk=8, ws=None):
+    """Decode with the K/V store in the pages of a cache (slot b holds sequence b's chunks):
+    retrieval, the retrieved chunks' page numbers, then the GCA forward on the pool, nothing
+    copied.  q_new [B, 64, H, dh], q_lmk_new [B, 1, D], k_lmk_store [B, nC, D]; topk <= nC full
+    chunks per slot."""
+    ws = ws or default_workspace(q_new.device)
+    nC = k_lmk_store.shape[1]
+    idx, scores = retrieve_topk(q_lmk_new, k_lmk_store, topk, nC, False, ws=ws)
+    k, v = cache.store()
+    o, lse = gca_forward(q_new, k, v, cache.lookup(idx), scores, shift=0, kv_shared=True, ws=ws)
+    return dict(idx=idx, scores=scores, o=o, lse=lse)
+
+
+def window_step(q, k, v, dout, freq, window=512, positions=None, interleaved=False, gain=1.0, ws=None):
+    """The attention block's window sublayer with rotary positions, forward and backward.
+    q, k, v, dout [B, L, H, dh]; freq from rotary_frequencies.  Returns o, lse and the gradients
+    dq, dk, dv of q, k, v."""
+    ws = ws or default_workspace(q.device)
+    qr, kr = rotary(q, k, freq, positions, interleaved, gain)
+    o, lse = window_forward(qr, kr, v, window=window, ws=ws)
+    dq, dk, dv = window_backward(qr, kr, v, o, dout, lse, window=window, ws=ws)
+    rotary_backward(dq, dk, freq, positions, interleaved, gain, q_out=dq, k_out=dk)
+    return dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv)
+
+
+def draft_step(q, k, v, parents, cache: PagedCache, freq, window=512, interleaved=False, gain=1.0, plan=None):
+    """The window sublayer of a decoding step over a tree of drafted tokens: q [B, T, H, dh],
+    k, v [B, T, heads, dh] before rotary; parents int32 [B, T] (see tree_plan; T = 1 with parents
+    -1: ordinary decoding), or `plan` = (mask, positions) of the step's first layer.  Returns o,
+    lse, the plan, and the turned k with v for accept_draft."""
+    mask, positions = plan if plan is not None else tree_plan(parents, cache.lengths, ws=cache.ws)
+    q, k = rotary(q, k, freq, positions, interleaved, gain)
+    o, lse = cache.attention(q, k, v, mask, positions, window=window)
+    return dict(o=o, lse=lse, plan=(mask, positions), k=k, v=v)
+
+
+def accept_draft(step: dict, cache: PagedCache, counts, path, begin=None):
+    """The accepted tokens of a draft_step go into the cache: counts[b] of them, the nodes
+    path[b, :counts[b]] of sequence b's tree from the root on (int32 [B], [B, T]).  begin
+    (int32 [B]) gives back the pages that the window has passed."""
+    cache.append(step["k"], step["v"], counts, path=path)
+    if begin is not None:
+        cache.trim(begin=begin)
 
 
 class TrainGraph:

@@ -421,7 +421,6 @@ def test_offsets_beyond_32_bits():
     pages = 2 ** 31 // (64 * Hkv * dh) + 40
     kp = torch.empty((pages, 64, Hkv, dh), dtype=torch.bfloat16, device="cuda")
     vp = torch.empty_like(kp)
-    rng = np.random.default_rng(0)
     table = np.full((1, 4), -1)
     table[0, :3] = pages - 1 - np.arange(3) * 7
     refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
@@ -445,7 +444,6 @@ def test_offsets_beyond_32_bits():
     assert int(cache.compact()) == 8
     assert cache.table.tolist() == [[7, 6, 5, 4]]
     assert np.array_equal(host(vp[7]), v[0]) and np.array_equal(host(kp[6]), k[1])
-    del rng
 
 
 # ------------------------------------------------------------------ pages
@@ -661,6 +659,106 @@ def test_lookup_feeds_gca():
     want, _ = g.gca_forward(q, dev(k, "bf16"), dev(v, "bf16"), ints(idx), sc, shift=0)
     got, _ = g.gca_forward(q, *cache.store(), cache.lookup(ints(idx)), sc, shift=0, kv_shared=True)
     assert torch.equal(got, want)
+
+
+def test_decode_paged_equals_decode():
+    g = _g()
+    from retrieval_sparse_attention_causal_gb300 import pipeline
+    B, nC, H, dh, D = 3, 12, 4, 64, 256
+    k, v = (synth.normal(1, s, (B, nC * 64, H, dh), 1.0, "bf16") for s in (20, 21))
+    lm = synth.landmark_inputs(1, B, 1, nC, D, "bf16")
+    q = torch.randn((B, 64, H, dh), device="cuda").bfloat16()
+    cache = g.PagedCache.empty(B * nC + 5, B, nC, H, dh)
+    cache.append(dev(k, "bf16"), dev(v, "bf16"), ints([nC * 64] * B))
+    want = pipeline.decode(q, dev(k, "bf16"), dev(v, "bf16"), dev(lm["q_lmk"], "bf16"), dev(lm["k_lmk"], "bf16"), topk=4)
+    got = pipeline.decode_paged(q, cache, dev(lm["q_lmk"], "bf16"), dev(lm["k_lmk"], "bf16"), topk=4)
+    for n in ("idx", "scores", "o", "lse"):
+        assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype,H,dh,L,W", [("f32", 2, 32, 192, 64), ("bf16", 3, 64, 320, 128)])
+def test_window_step_against_oracle(dtype, H, dh, L, W):
+    """Rotary, window attention, its gradients and rotary's, as one training step.  Tolerances of
+    the window tests (tests/gpu_helpers.py), with the rounding of the turned queries and keys:
+    one more half step of values up to 5 in a sum of dh terms of size 1/sqrt(dh), so twice them."""
+    import oracle.gca_oracle as gorc
+    from retrieval_sparse_attention_causal_gb300 import pipeline
+    from tests.gpu_helpers import TOL, assert_close
+    B, rot = 2, dh // 2
+    q, k, v, do = (synth.normal(2, s, (B, L, H, dh), 1.0, dtype) for s in (synth.S_Q, synth.S_K, synth.S_V, synth.S_DO))
+    pos = np.arange(L)[None].repeat(B, 0) + np.array([[0], [70000]])
+    w = orc.speeds(rot)
+    r = pipeline.window_step(*(dev(x, dtype) for x in (q, k, v, do)), _g().rotary_frequencies(rot), window=W, positions=ints(pos))
+    qr, kr = orc.rotary(q, pos, w), orc.rotary(k, pos, w)
+    o, lse = gorc.swa_forward(qr, kr, v, W)
+    dq, dk, dv = gorc.swa_backward(qr, kr, v, do, W)
+    dq, dk = orc.rotary(dq, pos, w, backward=True), orc.rotary(dk, pos, w, backward=True)
+    for got, ref, n in ((r["o"], o, "o"), (r["dq"], dq, "dq"), (r["dk"], dk, "dk"), (r["dv"], dv, "dv")):
+        assert_close(host(got), ref, 2 * TOL[dtype], n)
+
+
+@pytest.mark.parametrize("dtype,T,H,Hkv,dh,window", [("bf16", 6, 4, 2, 64, 0), ("bf16", 40, 4, 4, 64, 96), ("f32", 5, 2, 1, 32, 70),
+                                                     ("bf16", 1, 8, 2, 64, 128)])
+def test_drafts_accepted_step_by_step(dtype, T, H, Hkv, dh, window):
+    """A run of decoding steps: every step drafts a tree, attends, and accepts a random path of it;
+    pages behind the window are given back.  The output of each accepted token equals dense causal
+    attention (float64) over the tokens accepted before it, at their positions."""
+    g = _g()
+    from retrieval_sparse_attention_causal_gb300 import pipeline
+    rng = np.random.default_rng(T + dh)
+    B, rot = 3, dh
+    w, freq = orc.speeds(rot), g.rotary_frequencies(rot)
+    cache = g.PagedCache.empty(60, B, 24, Hkv, dh, dtype=TORCH[dtype])
+    prompt = [0, 70, 130]
+    kp, vp = (synth.normal(0, s, (B, 130, Hkv, dh), 1.0, dtype) for s in (20, 21))
+    kept = [[(kp[b, j], vp[b, j]) for j in range(prompt[b])] for b in range(B)]  # before rotary
+    kr, _ = g.rotary(dev(kp, dtype), None, freq)
+    cache.append(kr, dev(vp, dtype), ints(prompt))
+    graph = 0
+    for step in range(8):
+        q, k, v = (synth.normal(10 + step, s, (B, T, n, dh), 1.0, dtype) for s, n in ((22, H), (23, Hkv), (24, Hkv)))
+        parents = np.array([[int(rng.integers(-1, t)) if t else -1 for t in range(T)] for _ in range(B)])
+        out = pipeline.draft_step(dev(q, dtype), dev(k, dtype), dev(v, dtype), ints(parents), cache, freq, window=window)
+        paths = []
+        for b in range(B):
+            node, path = int(rng.integers(0, T)), []
+            while node >= 0:
+                path.insert(0, node)
+                node = parents[b, node]
+            paths.append(path if rng.random() < 0.9 else [])
+        got = host(out["o"])
+        for b, path in enumerate(paths):
+            seq = kept[b] + [(k[b, t], v[b, t]) for t in path]
+            for i, t in enumerate(path):
+                n = len(kept[b]) + i + 1
+                lo = max(0, n - window) if window else 0
+                at = np.arange(lo, n)[None]
+                ks = orc.rotary(np.stack([x[0] for x in seq[lo:n]])[None], at, w)[0]
+                vs = np.stack([x[1] for x in seq[lo:n]])
+                qr = orc.rotary(q[b:b + 1, t:t + 1], np.array([[n - 1]]), w)[0, 0]
+                for h in range(H):
+                    m = h // (H // Hkv)
+                    s = ks[:, m] @ qr[h] / np.sqrt(dh)
+                    e = np.exp(s - s.max())
+                    ref = e @ vs[:, m] / e.sum()
+                    # The turned q and k are rounded: ds <= 2 half steps of sum |q k| / sqrt(dh); the
+                    # weights' own rounding and the output's: two more.
+                    ds = 2.2 * HALF[dtype] * (np.abs(ks[:, m]) @ np.abs(qr[h])).max() / np.sqrt(dh) + 1e-5
+                    lim = (np.expm1(2 * ds) + 2 * HALF[dtype] + 1e-5) * (e @ np.abs(vs[:, m]) / e.sum()) + HALF[dtype] * np.abs(ref)
+                    assert np.all(np.abs(got[b, t, h] - ref) <= lim), (step, b, t, h)
+                    graph += 1
+        counts = [len(p) for p in paths]
+        begin = [max(0, len(kept[b]) + counts[b] - window + 1) if window else 0 for b in range(B)]
+        pipeline.accept_draft(out, cache, ints(counts), ints([p + [0] * (T - len(p)) for p in paths]), begin=ints(begin))
+        for b, path in enumerate(paths):
+            kept[b] += [(k[b, t], v[b, t]) for t in path]
+    assert cache.lengths.tolist() == [len(x) for x in kept] and graph > 40
+    held = (cache.table >= 0).sum().item()
+    assert held == (cache.refs > 0).sum().item()
+    if window:
+        assert held <= B * (window // 64 + 2)
+    cache.free()
+    assert not cache.refs.any()
 
 
 @flags
