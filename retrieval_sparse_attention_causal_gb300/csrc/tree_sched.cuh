@@ -11,8 +11,8 @@
 // heads, and of each key head m one for each `rows` of the T * g query rows that share it (row
 // r = token r / g, query head m g + r % g).  The heads of a token lie side by side in memory:
 // read at the same time they make long runs for DRAM, read at different times pieces of a
-// few bytes (measured: 12 heads of 64 over 128K tokens, 64 rows a head: LONG us together, 203 us
-// apart); and the row groups after the first find their pages in L2.
+// 128 bytes (measured: 12 heads of 64 over 4 x 64K tokens, 32 rows a head: 142 us together, 203
+// us apart); and the row groups after the first find their pages in L2.
 //
 // A tile (sequence, hw heads, row group) whose blocks lie in one share is finished there.  Of
 // the others each CTA writes a partial result (row maximum, row sum, unnormalised output): the

@@ -280,6 +280,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
         const bool inner = blk >= in0 && blk < in1 && !holes;
         uint64_t see = ~0ull;  // keys that this row sees
+        uint64_t used = 0;     // where `blank`: keys that some row of the CTA sees
+        bool blank = false;
         if (__builtin_expect(!inner, 0)) {
           const bool ctx = blk < sb.np;
           const int j0 = ctx ? (sb.p0 + blk) * kChunk : (blk - sb.np) * kChunk;
@@ -320,25 +322,29 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             see = word;
           }
           if (!ctx || lo > 0 || hi < kChunk) {
-            // V's rows that no row of the CTA sees become zeros.
-            uint64_t used = hi == 64 ? ~0ull : (1ull << max(hi, 0)) - 1;
+            blank = true;
+            used = hi == 64 ? ~0ull : (1ull << max(hi, 0)) - 1;
             used &= lo >= 64 ? 0ull : ~((1ull << lo) - 1);
             if (!ctx) used &= seen;
-            const int at = id + 2 * ((blk - blk0) / PB) + 1, part = (blk - blk0) % PB;
-            ok = waited(&bar_full[at % NS], (at / NS) & 1, kSiteV, blk);
-            if (ok && !((used >> (tid >> 1)) & 1)) {
-#pragma unroll
-              for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  *reinterpret_cast<uint4*>(ring + (at % NS) * kSlot + (part + s) * kTile + (tid >> 1) * 128 + (tid & 1) * 64 + u * 16) =
-                      make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_async_smem();
           }
         }
         if (!ready) ok = ok && waited(&bar_s[nth % SB], (nth / SB) & 1, kSiteS, blk);
         ready = false;
+        if (blank) {
+          // V's rows that no row of the CTA sees become zeros.  S(n) has been seen, so the slot's last
+          // tile (V(n - 2) at the nearest) has been read, and the parity below is that of this one.
+          const int at = id + 2 * ((blk - blk0) / PB) + 1, part = (blk - blk0) % PB;
+          ok = ok && waited(&bar_full[at % NS], (at / NS) & 1, kSiteV, blk);
+          if (ok && !((used >> (tid >> 1)) & 1)) {
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(ring + (at % NS) * kSlot + (part + s) * kTile + (tid >> 1) * 128 + (tid & 1) * 64 + u * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_async_smem();
+        }
         if (!ok) break;
         if (idle) {  // no row of this warp exists: what P holds for them goes nowhere
           __syncwarp();

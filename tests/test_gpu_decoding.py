@@ -367,6 +367,26 @@ def test_tree_attention_is_deterministic_and_keeps_to_its_stream():
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("T,H,Hkv,dh,top", [(1, 16, 4, 128, 32768), (8, 16, 4, 128, 20000), (40, 8, 4, 128, 9000), (24, 12, 12, 64, 9000),
+                                            (64, 16, 4, 64, 9000), (1, 12, 12, 64, 40000)])
+def test_tree_attention_repeats_bit_for_bit(T, H, Hkv, dh, top):
+    """Many ends of sequences among long ones, thirty times: the handing over of blanked, masked
+    and streamed pages must not depend on timing."""
+    g = _g()
+    rng = np.random.default_rng(dh + T)
+    lengths = [int(x) for x in rng.integers(1, top, 16)]
+    held = [-(-n // 64) for n in lengths]
+    table = np.full((16, max(held) + 1), -1)
+    order = rng.permutation(sum(held))
+    for b, n in enumerate(held):
+        table[b, :n] = order[sum(held[:b]):sum(held[:b + 1])]
+    kp, vp = (synth.device_normal(0, s, (sum(held), 64, Hkv, dh), 1.0, torch.bfloat16) for s in (20, 21))
+    q, kn, vn = (synth.device_normal(0, s, (16, T, n, dh), 1.0, torch.bfloat16) for s, n in ((22, H), (23, Hkv), (24, Hkv)))
+    outs = [g.tree_attention(q, kn, vn, kp, vp, ints(table), ints(lengths)) for _ in range(30)]
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
 def test_captured_steps_follow_the_cache():
     """Two captured steps (plan, attention, append) on two caches, replayed in turn and at once
     on two streams: each follows its own lengths and tables, and equals eager calls."""
