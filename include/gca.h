@@ -421,7 +421,7 @@ GCA_API gca_status gca_scores_backward(const void* q_lmk, int64_t q_row_stride, 
  *           projection; 0 repeats); k may be NULL (Hkv = 0).  dtype of all four tensors.
  *   q_out, k_out  like them; may be the inputs themselves (same pointer and strides), but
  *           must not overlap them otherwise.  Their strides may not make elements overlap.
- *   dh 2..256, rot even in 2..dh.
+ *   dh 2..256, rot even in 2..dh.   B <= 65535, B * L < 2^31.
  *   freq    [rot/2] device, w_i in units of 2^-64 turns per position, as written by
  *           gca_rotary_frequencies.
  *   positions [B][L] int32 device (>= 0 or not), position_batch_stride elements between
@@ -535,7 +535,10 @@ GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, cons
  *   window  0 (everything) or more.   scale > 0.   T 1..256.   dh 32, 64 or 128.
  *   o       [B][T][H][dh] contiguous, 16-byte aligned.   lse [B][T][H] float32.
  *   ws      >= gca_forward_workspace_size() bytes (error word only).
- *   scratch >= gca_tree_attention_scratch_size() bytes, 256-byte aligned, any contents.
+ *   scratch >= gca_tree_attention_scratch_size() bytes, 256-byte aligned, any contents; one for
+ *           each call that can overlap another.
+ * bf16 products accumulate in float32; their softmax weights are rounded to bf16 for the product
+ * with v (relative to each weight, 2^-8 at most), as in gca_window_forward.
  *
  * gca_tree_plan - mask and positions of a tree, once for all layers of a step.
  *   parents [B][T] int32: the earlier token of the draft that token t follows, -1 for the

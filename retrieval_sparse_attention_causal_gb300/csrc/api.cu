@@ -725,6 +725,7 @@ extern "C" gca_status gca_cache_append(const gca_cache* cache, const gca_heads* 
   if ((st = check_cache(cache, true)) != GCA_OK) return st;
   if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
   if (T < 1 || T > INT32_MAX / 2) return fail(GCA_ERR_INVALID_ARG, "T must be in 1..2^30");
+  if ((int64_t)n * (T / 64 + 2) > INT32_MAX) return fail(GCA_ERR_INVALID_ARG, "n and T are too large together");
   if (!counts) return fail(GCA_ERR_INVALID_ARG, "counts is NULL");
   const int esize = cache->dtype == GCA_BF16 ? 2 : 4;
   if ((st = check_vectors(k_new, esize, "k_new")) != GCA_OK) return st;

@@ -18,14 +18,23 @@ from . import CHUNK, EXT, LIB, Workspace, _check, _need
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 
+class _ErrorWord(Workspace):
+    """The default error word of a device: a workspace that never grows."""
+
+    def __init__(self, index: int):
+        self.device = torch.device("cuda", index)
+        self.buf = EXT.error_word(index)
+
+    def check(self):
+        with torch.cuda.device(self.device):
+            super().check()
+
+
 def cache_workspace(device) -> Workspace:
-    """The workspace whose error word the calls of this module use by default (it never
-    grows; `cache_workspace(device).check()` raises what a kernel flagged)."""
+    """The workspace whose error word the calls of this module use by default;
+    `cache_workspace(device).check()` raises what a kernel flagged."""
     d = torch.device(device)
-    ws = Workspace.__new__(Workspace)
-    ws.device = torch.device("cuda", d.index if d.index is not None else torch.cuda.current_device())
-    ws.buf = EXT.error_word(ws.device.index)
-    return ws
+    return _ErrorWord(d.index if d.index is not None else torch.cuda.current_device())
 
 
 def _word(ws):

@@ -45,6 +45,7 @@ def test_rotary_refusals(gca):
     assert call(Hkv=0) == gca.GCA_ERR_INVALID_ARG
     assert call(nok=True) == gca.GCA_ERR_INVALID_ARG  # Hkv without k
     assert call(n=1 << 30) == gca.GCA_ERR_INVALID_ARG
+    assert call(B=65536, n=1) == gca.GCA_ERR_INVALID_ARG
     assert call(dh=300) == gca.GCA_ERR_UNSUPPORTED
     assert call(rot=63) == gca.GCA_ERR_INVALID_ARG
     assert call(rot=66) == gca.GCA_ERR_INVALID_ARG
@@ -87,7 +88,7 @@ def test_cache_refusals(gca):
                dict(slots=0), dict(width=0), dict(width=1 << 25), dict(lengths=0), dict(refs=0), dict(heads=1, dh=4)):
         assert append(c=pool(gca, **kw)) == E, kw
     assert append(n=0) == E and append(n=9) == E and append(n=1025, slots=FAKE) == E
-    assert append(T=0) == E and append(counts=0) == E
+    assert append(T=0) == E and append(counts=0) == E and append(n=1024, slots=FAKE, T=1 << 28) == E
     assert append(k=heads(gca, FAKE + 8)) == E and append(v=heads(gca, ts=257)) == E and append(k=heads(gca, hs=72)) == E
     assert append(ws=0) == W and append(wsb=8) == W and append(sc=0) == W and append(sc=FAKE + 16) == W
     assert append(scb=L.gca_cache_append_scratch_size(8, 5) - 1) == W
@@ -111,6 +112,8 @@ def test_cache_refusals(gca):
     assert attend(scale=float("inf")) == E and attend(scale=float("nan")) == E
     assert attend(mask=FAKE + 4) == E and attend(o=0) == E and attend(o=FAKE + 4) == E and attend(lse=0) == E
     assert attend(q=heads(gca, FAKE + 2)) == E and attend(k=heads(gca, bs=4)) == E and attend(v=heads(gca, 0)) == E
+    assert attend(k=heads(gca, ts=0)) == U and attend(v=heads(gca, ts=0)) == U  # one token repeated
+    assert attend(c=pool(gca, heads=65535, width=1 << 24), H=65535) == U
     assert attend(wsb=0) == W and attend(scb=100) == W
     assert L.gca_tree_plan(FAKE, FAKE, 2, 257, FAKE, FAKE, FAKE, 256, None) == U
     assert L.gca_tree_plan(FAKE, FAKE, 0, 5, FAKE, FAKE, FAKE, 256, None) == E

@@ -201,9 +201,12 @@ def random_cache(rng, lengths, Hkv, dh, dtype, spare=2, width_spare=1, seed=0):
 
 
 def random_draft(rng, B, T, lengths, kind):
-    """(see, pos): 'chain' (None, None), 'tree' with padding, 'wild': any mask, rows that see nothing."""
+    """(see, pos): 'chain' (None, None), 'padded chain' (None, pos), 'tree' with padding, 'wild': any
+    mask, rows that see nothing."""
     if kind == "chain":
         return None, None
+    if kind == "padded chain":
+        return None, np.array([[lengths[b] + t if t < max(1, T - 2 * b) else -1 for t in range(T)] for b in range(B)])
     see, pos = np.zeros((B, T, T), dtype=bool), np.full((B, T), -1)
     for b in range(B):
         if kind == "tree":
@@ -232,8 +235,8 @@ def attend_and_check(rng, lengths, T, H, Hkv, dh, dtype, kind, window=0, scale=N
     see, pos = random_draft(rng, B, T, lengths, kind)
     rsee = np.tril(np.ones((B, T, T), dtype=bool)) if see is None else see
     rpos = np.array(lengths)[:, None] + np.arange(T) if pos is None else pos
-    if kind == "tree":  # padding holds anything
-        kn[rpos < 0], vn[rpos < 0] = np.nan, np.inf
+    if kind in ("tree", "padded chain"):  # padding holds anything
+        kn[rpos < 0], vn[rpos < 0], q[rpos < 0] = np.nan, np.inf, np.nan
     if views:
         fused = torch.full((B, T, H + 2 * Hkv + 1, dh), float("nan"), dtype=TORCH[dtype], device="cuda")
         qd, kd, vd = fused[:, :, :H], fused[:, :, H:H + Hkv], fused[:, :, H + Hkv:H + 2 * Hkv]
@@ -275,6 +278,12 @@ ATTENTION = [  # lengths, T, H, Hkv, dh, dtype, kind, window
     ([200, 65], 100, 6, 2, 32, "bf16", "wild", 0),
     ([200, 65], 33, 8, 1, 64, "bf16", "wild", 5),
     ([100, 65], 9, 8, 2, 128, "bf16", "wild", 40),
+    ([90, 0], 100, 32, 1, 64, "bf16", "tree", 0),
+    ([70, 3], 130, 24, 1, 128, "bf16", "tree", 50),
+    ([300, 65, 7], 12, 4, 4, 64, "bf16", "padded chain", 0),
+    ([300, 65, 7], 70, 6, 3, 64, "bf16", "padded chain", 20),
+    ([80, 65, 7], 9, 4, 2, 32, "f32", "padded chain", 3),
+    ([64, 30], 40, 40, 2, 32, "f32", "tree", 0),
     ([0, 1, 200], 1, 4, 4, 32, "f32", "chain", 0),
     ([200, 31], 13, 6, 2, 32, "f32", "tree", 0),
     ([130, 64], 70, 4, 1, 64, "f32", "tree", 33),
