@@ -33,8 +33,10 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 192;
+constexpr int kCtas = 2;         // on an SM
+constexpr int kCols = 256;       // of TMEM: two buffers of logits, the output behind them
 constexpr int kRows = 128;       // the lanes of TMEM
-constexpr int kTile = 8192;     // 64 tokens x 64 elements
+constexpr int kTile = 8192;      // 64 tokens x 64 elements
 constexpr int kSlot = 2 * kTile;
 constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
 constexpr uint32_t kAll = 0xffffffffu;
@@ -45,24 +47,21 @@ struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
   static constexpr int PB = 2 / SUB;                // blocks of 64 keys of a ring slot: 16 KB of K or of V
   static constexpr int QB = 2 * kTile * SUB;        // a row tile of Q
-  static constexpr int CTAS = 2;                    // on an SM
-  static constexpr int SB = 2;                      // logit buffers
-  static constexpr int COLS = 256;                  // of TMEM: the logit buffers, the output behind them
   static constexpr int NS = DH == 64 ? 5 : 4;       // ring slots
   static constexpr int SMEM = QB + NS * kSlot + 1024;
 };
 
 template <int DH>
-__global__ void __launch_bounds__(kThreads, Tc<DH>::CTAS)
+__global__ void __launch_bounds__(kThreads, kCtas)
 tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmKn, const __grid_constant__ CUtensorMap tmVn) {
   using C = Tc<DH>;
-  constexpr int SUB = C::SUB, NS = C::NS, PB = C::PB, SB = C::SB;
+  constexpr int SUB = C::SUB, NS = C::NS, PB = C::PB;
   constexpr uint32_t kIdS = tc::idesc_bf16(kRows, 64, false), kIdPV = tc::idesc_bf16(kRows, 64, true);
   extern __shared__ __align__(1024) unsigned char dsm[];
   unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = Qs + C::QB;
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[SB], bar_p[SB], bar_o[SB];
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -75,7 +74,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       tc::mbar_init(&bar_empty[i], 1);
     }
     tc::mbar_init(&bar_q, 4);
-    for (int i = 0; i < SB; ++i) {
+    for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar_s[i], 1);
       tc::mbar_init(&bar_p[i], 4);
       tc::mbar_init(&bar_o[i], 1);
@@ -83,7 +82,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     abort_s = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 4) tc::tmem_alloc(&tmem_slot, C::COLS);
+  if (warp == 4) tc::tmem_alloc(&tmem_slot, kCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -189,9 +188,9 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       tc::fence_after();
 #pragma unroll
       for (int s = 0; s < SUB; ++s)
-        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (i % SB), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
+        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (i & 1), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
                                                 s ? 1u : 0u);
-      tc::commit_warp(&bar_s[i % SB]);
+      tc::commit_warp(&bar_s[i & 1]);
       release(x, 0, n);
     };
     while (ok && segment()) {
@@ -201,18 +200,17 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       ++seg;
       if (ok) logits(0, nth, n);
       for (int x = 0; x < n && ok; ++x, ++nth) {
-        if (SB > 1 && x + 1 < n) logits(x + 1, nth + 1, n);
+        if (x + 1 < n) logits(x + 1, nth + 1, n);
         const uint32_t v = operand(x, 1);
-        ok = ok && waited(&bar_p[nth % SB], (nth / SB) & 1, kSiteP, x);
+        ok = ok && waited(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, x);
         if (!ok) break;
         tc::fence_after();
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
-          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 64 * (SB + s), tmem + 64 * (nth % SB), tc::desc_mn(v + s * kTile), kIdPV,
+          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 64 * (2 + s), tmem + 64 * (nth & 1), tc::desc_mn(v + s * kTile), kIdPV,
                                                x > 0 ? 1u : 0u);
-        tc::commit_warp(&bar_o[nth % SB]);
+        tc::commit_warp(&bar_o[nth & 1]);
         release(x, 1, n);
-        if (SB == 1 && x + 1 < n) logits(x + 1, nth + 1, n);
       }
       id += 2 * ((n + PB - 1) / PB);
     }
@@ -220,7 +218,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     // ---------------------------------------------------------------- softmax
     const float sl2 = a.scale * kTreeLog2e;
     const int R = a.T * a.g;
-    const uint32_t tS = tmem + ((uint32_t)(32 * warp) << 16), tO = tS + 64 * SB;
+    const uint32_t tS = tmem + ((uint32_t)(32 * warp) << 16), tO = tS + 128;
     int nth = 0, id = 0;  // blocks and ring slots so far
     int slot = 0;
     while (ok && segment()) {
@@ -328,7 +326,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             if (!ctx) used &= seen;
           }
         }
-        if (!ready) ok = ok && waited(&bar_s[nth % SB], (nth / SB) & 1, kSiteS, blk);
+        if (!ready) ok = ok && waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
         ready = false;
         if (blank) {
           // V's rows that no row of the CTA sees become zeros.  S(n) has been seen, so the slot's last
@@ -348,11 +346,11 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         if (!ok) break;
         if (idle) {  // no row of this warp exists: what P holds for them goes nowhere
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar_p[nth % SB]);
+          if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
           continue;
         }
         tc::fence_after();
-        const uint32_t tP = tS + 64 * (nth % SB);
+        const uint32_t tP = tS + 64 * (nth & 1);
         // The weights by the reference in use; where a row's sum shows that it is outgrown (or
         // there is none yet), once more by the new one.
         bool exact = !settled;
@@ -384,7 +382,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             l *= f;
             settled = __all_sync(kAll, mx != -CUDART_INF_F || pos < 0);
             if (blk > blk0) {
-              ok = waited(&bar_o[(nth - 1) % SB], ((nth - 1) / SB) & 1, kSiteO, blk);
+              ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
               tc::fence_after();
 #pragma unroll
               for (int q = 0; q < DH / 32; ++q) {
@@ -432,15 +430,15 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         l += sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
-        if (blk + 1 < blk1) ready = __all_sync(kAll, tc::mbar_try(&bar_s[(nth + 1) % SB], ((nth + 1) / SB) & 1)) != 0;
+        if (blk + 1 < blk1) ready = __all_sync(kAll, tc::mbar_try(&bar_s[(nth + 1) & 1], ((nth + 1) >> 1) & 1)) != 0;
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar_p[nth % SB]);
+        if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
       }
       id += 2 * ((n + PB - 1) / PB);
       if (!ok) break;
-      ok = waited(&bar_o[(nth - 1) % SB], ((nth - 1) / SB) & 1, kSiteO, -1);
+      ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, -1);
       if (!ok) break;
       tc::fence_after();
       if (pos < 0) l = 0.f;
@@ -487,7 +485,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   __syncthreads();
   if (warp == 4) {
     tc::fence_after();
-    tc::tmem_dealloc(tmem_slot, C::COLS);
+    tc::tmem_dealloc(tmem_slot, kCols);
   }
 }
 
