@@ -856,7 +856,7 @@ extern "C" gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_
   if ((T > 1 && k_new->token_stride == 0) || (T > 1 && v_new->token_stride == 0))
     return fail(GCA_ERR_UNSUPPORTED, "k_new and v_new may not repeat one token (token stride 0)");
   // All blocks of 64 keys are numbered in 32 bits.
-  if ((double)B * cache->heads * ((double)cache->width + 4) > INT32_MAX)
+  if ((double)B * cache->heads * ((double)cache->width + 16) > INT32_MAX)
     return fail(GCA_ERR_UNSUPPORTED, "B, H, T and the table's width are too large together");
   if (!o || !lse || !aligned16(o)) return fail(GCA_ERR_INVALID_ARG, "o and lse must not be NULL, o 16-byte aligned");
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;

@@ -219,9 +219,11 @@ struct TreeArgs {
   float scale;
   ErrWord* err;
   unsigned char* part;                                     // partial results
+  int lead;                                                // items without work before a tile's blocks
   int hw, hl, rows, nrt, nd;                               // key heads of a CTA, such CTAs of a share, rows of a CTA, groups of rows,
                                                            // blocks of the draft
   int grid;                                                // shares of the work, at most
+  int pieces;                                              // how partial outputs lie
   int wide;                                                // pools on 32-byte boundaries
 };
 cudaError_t launch_tree_rows(const TreeArgs& a, cudaStream_t s);  // bf16, 16 rows a CTA (tree_rows.cu)

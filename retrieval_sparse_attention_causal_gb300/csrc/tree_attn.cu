@@ -42,19 +42,12 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
   const Share sh = my_share(a);
   const float sl2 = a.scale * kTreeLog2e;
   const int R = a.T * a.g, rt = my_rows(a);
-  int b = sh.b;
-  int off = sh.off, item = sh.lo;
-  SeqBlocks sb = sh.lo < sh.hi ? seq_blocks(a, b, false) : SeqBlocks{};
+  Walk walk(a, sh);
+  const SeqBlocks& sb = walk.sb;
+  const int &b = walk.b, &tile = walk.tile, &blk0 = walk.blk0, &blk1 = walk.blk1;
   int slot = 0;
-  while (item < sh.hi) {
-    const int tile = off / sb.nb;
-    if (tile >= a.Hkv / a.hl) {
-      sb = seq_blocks(a, ++b, false);
-      off = 0;
-      continue;
-    }
+  while (walk.next(a)) {
     const int m = my_heads(a, tile);
-    const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     const int rows = min(MT, R - rt * MT);
     __syncthreads();
     for (int i = tid; i < MT * DH / 4; i += kSimtThreads) {
@@ -232,12 +225,10 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
           part.l[r] = sum;
         }
 #pragma unroll
-        for (int c = 0; c < NC * CV; ++c) part.o[r * DH + (c / CV) * 16 * CV + tx * CV + c % CV] = o[i][c];
+        for (int c = 0; c < NC * CV; ++c) *part.at(r, (c / CV) * 16 * CV + tx * CV + c % CV) = o[i][c];
       }
     }
     slot = 1;
-    off += blk1 - blk0;
-    item += blk1 - blk0;
   }
 }
 
@@ -246,6 +237,8 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
 // sets of threads over the partials.  A thread walks its partials once, with a running
 // maximum; the sets are joined in shared memory.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCtas = 4 * kSMs;
+constexpr int kJoinFly = 4;  // partials that a thread has on their way
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_kernel(TreeArgs a, int rg) {
@@ -256,11 +249,13 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_ker
   int before;
   const Share sh = shares(a, all_items(a, b, before, false));
   const SeqBlocks sb = seq_blocks(a, b, false);
-  const int s0 = before + hg / a.hl * sb.nb;
-  const int c0 = owner_of(sh, s0), c1 = owner_of(sh, s0 + sb.nb - 1);  // shares of its first and last block
+  const int s0 = before + hg / a.hl * sb.items;
+  const int c0 = owner_of(sh, s0 + a.lead), c1 = owner_of(sh, s0 + sb.items - 1);  // shares of its first and last block
   after_previous();      // (by every CTA: the grid must not end before the one ahead of it)
   if (c0 == c1) return;  // finished there
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, ps = 16 / rg, ri = y % rg, pi = y / rg;
+  // Threads of a row, or of a column's rows, side by side: as the partials lie.
+  const int ps = 16 / rg, ri = a.pieces ? threadIdx.x % rg : threadIdx.x / 16 % rg,
+            x = a.pieces ? threadIdx.x / rg % 16 : threadIdx.x % 16, pi = threadIdx.x / (16 * rg), y = pi * rg + ri;
   const int most = min(a.rows, a.T * a.g - rt * a.rows), v = blockIdx.z * rg + ri;
   const int hi = v / most, r = v - hi * most, at = hi * a.rows + r;  // key head of the tile, row, place in the slot
   const bool on = hi < a.hw;
@@ -269,7 +264,7 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_ker
   for (int i = 0; i < NC; ++i) o[i] = 0.f;
   const bool late = first_item(sh, c0) < s0;  // the first of them began in another tile
   if (on) {
-    constexpr int U = 4;
+    constexpr int U = kJoinFly;
     for (int c = c0 + pi; c <= c1; c += U * ps) {
       float m[U], w[U], y4[U][NC];
 #pragma unroll
@@ -281,14 +276,13 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_ker
           const Part p = part_of(a, ((int64_t)cc * a.hl + hg % a.hl) * a.nrt + rt, cc == c0 && late ? 1 : 0);
           m[k] = p.m[at];
           w[k] = p.l[at];
-          const float* src = p.o + (int64_t)at * DH + x * CV;
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if constexpr (CV == 4) {
-              const float4 f = *reinterpret_cast<const float4*>(src + 64 * q);
+              const float4 f = *reinterpret_cast<const float4*>(p.at(at, 64 * q + 4 * x));
               y4[k][4 * q] = f.x, y4[k][4 * q + 1] = f.y, y4[k][4 * q + 2] = f.z, y4[k][4 * q + 3] = f.w;
             } else {
-              const float2 f = *reinterpret_cast<const float2*>(src);
+              const float2 f = *reinterpret_cast<const float2*>(p.at(at, 2 * x));
               y4[k][0] = f.x, y4[k][1] = f.y;
             }
           }
@@ -340,7 +334,18 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_ker
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if (x == 0) a.lse[to] = l == 0.f ? -CUDART_INF_F : top * kTreeLn2 + logf(l);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) Elem<T>::st(reinterpret_cast<T*>(a.o) + to * DH + (i / CV) * 64 + x * CV + i % CV, o[i] * inv);
+  for (int q = 0; q < NQ; ++q) {
+    T* row = reinterpret_cast<T*>(a.o) + to * DH + 64 * q + x * CV;
+    const float* f = o + CV * q;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < CV; i += 2) reinterpret_cast<float2*>(row)[i / 2] = make_float2(f[i] * inv, f[i + 1] * inv);
+    } else if constexpr (CV == 4) {
+      *reinterpret_cast<uint2*>(row) = make_uint2(pack_bf16(f[0] * inv, f[1] * inv), pack_bf16(f[2] * inv, f[3] * inv));
+    } else {
+      *reinterpret_cast<uint32_t*>(row) = pack_bf16(f[0] * inv, f[1] * inv);
+    }
+  }
 }
 
 // ------------------------------------------------------------------ plan of a tree
@@ -398,6 +403,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 }
 
 // ------------------------------------------------------------------ launching
+constexpr int kLeadTc = 4, kLeadRows = 1;
 enum Kind { kRows, kTensor, kSimt };
 struct Shape {
   Kind kind;
@@ -405,6 +411,8 @@ struct Shape {
   int ctas;           // on the GPU at once
   int hl;             // CTAs of a share side by side over the key heads
 };
+// Pages of a sequence that some row can see, at most.
+int seen_pages(int width, int window) { return window > 0 ? std::min(width, window / kChunk + 2) : width; }
 Shape shape_of(int B, int T, int g, int Hkv, int dh, int bf16, int width, int window) {
   const int R = T * g;
   Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, 2 * kSMs};
@@ -413,7 +421,7 @@ Shape shape_of(int B, int T, int g, int Hkv, int dh, int bf16, int width, int wi
   // better.  Measured: 12 heads over 4000 tokens, one token: 10.3 against 13.1 us; 64 sequences
   // with a window of 512: 29 against 49; 32 sequences over 32K, dh 128: 352 against 323; 48
   // rows over 10 blocks of 192 sequence-heads: 28 against 23.
-  const int seen = window > 0 ? std::min(width, window / kChunk + 2) : width;       // pages of a sequence, at most
+  const int seen = seen_pages(width, window);
   const int64_t work = (int64_t)B * Hkv * (seen + (T + 63) / 64) * ((R + 15) / 16);  // blocks, once for each 16 rows
   const bool few = R <= 16 ? work <= 32 * kSMs || seen < 32 : work <= 12 * kSMs;
   if (bf16 && (few || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
@@ -448,6 +456,7 @@ cudaError_t run_dh(const TreeArgs& a, Kind kind, cudaStream_t s) {
   const int64_t parts = (int64_t)a.grid * a.hl / ((int64_t)(a.Hkv / a.hw) * a.B) + 1;
   int rg = 16;
   while (rg > 1 && (rg / 2 >= rows || parts * rg > 64)) rg >>= 1;
+  while (rg < 16 && (int64_t)tiles * a.B * ((rows + rg - 1) / rg) > kJoinCtas) rg <<= 1;
   launch_begin("tree_join", s);
   e = launch_after(tree_join_kernel<T, DH>, dim3(tiles, a.B, (rows + rg - 1) / rg), dim3(kJoinThreads), s, a, rg);
   const cudaError_t last = launch_end("tree_join", s);
@@ -475,6 +484,9 @@ cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
   a.nrt = sh.nrt;
   a.hl = sh.hl;
   a.nd = (a.T + kChunk - 1) / kChunk;
+  a.pieces = sh.kind == kTensor;
+  const int64_t items = (int64_t)a.B * (a.Hkv / (a.hw * a.hl)) * (seen_pages(a.width, a.window) + a.nd);
+  a.lead = sh.kind == kTensor ? kLeadTc : (items > 2 * a.grid ? kLeadRows : 0);
   a.wide = (reinterpret_cast<uintptr_t>(a.kp) | reinterpret_cast<uintptr_t>(a.vp)) % 32 == 0;
   return a.bf16 ? run<bf16>(a, sh.kind, s) : run<float>(a, sh.kind, s);
 }

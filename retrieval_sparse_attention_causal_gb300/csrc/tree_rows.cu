@@ -124,19 +124,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
   if (sh.lo >= sh.hi) return;
   const float sl2 = a.scale * kTreeLog2e;
   const int rt = my_rows(a), R = a.T * a.g - 16 * rt;  // rows from this CTA's first on
-  int b = sh.b;
-  int off = sh.off, item = sh.lo;
-  SeqBlocks sb = seq_blocks(a, b, false);
+  Walk walk(a, sh);
+  const SeqBlocks& sb = walk.sb;
+  const int &b = walk.b, &tile = walk.tile, &blk0 = walk.blk0, &blk1 = walk.blk1;
   int slot = 0;
-  while (item < sh.hi) {
-    const int tile = off / sb.nb;
-    if (tile >= a.Hkv / (a.hw * a.hl)) {
-      sb = seq_blocks(a, ++b, false);
-      off = 0;
-      continue;
-    }
+  while (walk.next(a)) {
     const int m = my_heads(a, tile) + warp % a.hw;  // this warp's key head
-    const int blk0 = off - tile * sb.nb, blk1 = min(sb.nb, blk0 + sh.hi - item);
     // Q fragments, and the two rows' positions and masks.
     uint32_t qf[G::KS][4];
     int pos[2], tok[2];
@@ -413,13 +406,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
         }
 #pragma unroll
         for (int e = 0; e < NV; e += 4)
-          *reinterpret_cast<float4*>(part.o + at * DH + d0 + e) = make_float4(out[e], out[e + 1], out[e + 2], out[e + 3]);
+          *reinterpret_cast<float4*>(part.at(at, d0 + e)) = make_float4(out[e], out[e + 1], out[e + 2], out[e + 3]);
       }
     }
     __syncthreads();  // join_* are free again
     slot = 1;
-    off += blk1 - blk0;
-    item += blk1 - blk0;
   }
 }
 

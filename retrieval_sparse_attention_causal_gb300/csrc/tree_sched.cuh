@@ -10,7 +10,7 @@
 // A share has hl * nrt CTAs, which walk its items together: one for each `hw` of the set's key
 // heads, and of each key head m one for each `rows` of the T * g query rows that share it (row
 // r = token r / g, query head m g + r % g).  The heads of a token lie side by side in memory:
-// read at the same time they make long runs for DRAM, read at different times pieces of a
+// read at the same time they make long runs for DRAM, read at different times pieces of
 // 128 bytes (measured: 12 heads of 64 over 4 x 64K tokens, 32 rows a head: 142 us together, 203
 // us apart); and the row groups after the first find their pages in L2.
 //
@@ -18,6 +18,10 @@
 // the others each CTA writes a partial result (row maximum, row sum, unnormalised output): the
 // one that its share begins in to the first of its two slots, the one that it ends in to the
 // second; the joining kernel finds a tile's partials by the same arithmetic.
+//
+// Going on to another tile costs a CTA the queries' load, a pipeline that fills again and a
+// second result.  So each tile has `lead` items without work before its first block, about
+// what that costs in blocks: a share that holds them has fewer blocks.
 #pragma once
 
 #include "common.cuh"
@@ -30,6 +34,7 @@ struct SeqBlocks {
   int p0;     // first page that some row can see
   int np;     // pages from there
   int nb;     // blocks: pages, then the draft's
+  int items;  // the blocks and the lead
 };
 
 __device__ __forceinline__ SeqBlocks seq_blocks(const TreeArgs& a, int b, bool flag) {
@@ -43,6 +48,7 @@ __device__ __forceinline__ SeqBlocks seq_blocks(const TreeArgs& a, int b, bool f
   s.np = (int)(((int64_t)s.len + kChunk - 1) / kChunk) - s.p0;
   if (s.np < 0) s.np = 0;
   s.nb = s.np + a.nd;
+  s.items = a.lead + s.nb;
   return s;
 }
 
@@ -63,7 +69,7 @@ __device__ __forceinline__ int owner_of(const Share& s, int item) {
 __device__ __forceinline__ int all_items(const TreeArgs& a, int b, int& before, bool flag) {
   int sum = 0, part = 0;
   for (int i = threadIdx.x & 31; i < a.B; i += 32) {
-    const int n = seq_blocks(a, i, flag).nb;
+    const int n = seq_blocks(a, i, flag).items;
     sum += n;
     if (i < b) part += n;
   }
@@ -90,7 +96,7 @@ __device__ __forceinline__ Share my_share(const TreeArgs& a) {
   s.b = s.off = 0;
   if (s.lo >= s.hi) return s;
   for (int b0 = 0, at = 0;; b0 += 32) {
-    const int n = b0 + lane < a.B ? seq_blocks(a, b0 + lane, false).nb * tiles : 0;
+    const int n = b0 + lane < a.B ? seq_blocks(a, b0 + lane, false).items * tiles : 0;
     int incl = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -109,6 +115,33 @@ __device__ __forceinline__ Share my_share(const TreeArgs& a) {
   }
 }
 
+// The segments of a share, one after the other: blocks blk0 .. blk1 - 1 of tile `tile` of
+// sequence b.
+struct Walk {
+  int b, off, item, hi;
+  SeqBlocks sb;
+  int tile, blk0, blk1;
+  __device__ __forceinline__ Walk(const TreeArgs& a, const Share& s) : b(s.b), off(s.off), item(s.lo), hi(s.hi), tile(0), blk0(0), blk1(0) {
+    if (item < hi) sb = seq_blocks(a, b, false);
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a) {
+    const int tiles = a.Hkv / (a.hw * a.hl);
+    while (item < hi) {
+      while ((tile = off / sb.items) >= tiles) {
+        sb = seq_blocks(a, ++b, false);
+        off = 0;
+      }
+      const int from = off - tile * sb.items - a.lead;  // below 0: in the lead
+      blk0 = max(from, 0);
+      blk1 = min(sb.nb, from + hi - item);
+      off += blk1 - from;
+      item += blk1 - from;
+      if (blk0 < blk1) return true;
+    }
+    return false;
+  }
+};
+
 // This CTA's row group, and the first key head of tile t of its sequence.
 __device__ __forceinline__ int my_rows(const TreeArgs& a) { return blockIdx.x % a.nrt; }
 __device__ __forceinline__ int my_heads(const TreeArgs& a, int t) {
@@ -119,14 +152,17 @@ constexpr float kTreeLog2e = 1.4426950408889634f;
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
 // Partial results.
-// A slot: [hw rows] maxima (of log2 e times the scaled logits), as many sums, [hw rows][dh] outputs.
+// A slot: n = hw rows maxima (of log2 e times the scaled logits), as many sums, and the outputs:
+// [n][dh], or, where a thread holds a row (`a.pieces`), [dh / 4][n][4], so that a warp writes runs.
 struct Part {
   float* m; float* l; float* o;
+  int row, piece;  // from a row to the next, from four columns to the next
+  __device__ __forceinline__ float* at(int r, int col) const { return o + r * row + (col >> 2) * piece + (col & 3); }
 };
 __device__ __forceinline__ Part part_of(const TreeArgs& a, int64_t cta, int which) {
   const int n = a.hw * a.rows;
   float* p = reinterpret_cast<float*>(a.part) + (cta * 2 + which) * n * (a.dh + 2);
-  return Part{p, p + n, p + 2 * n};
+  return a.pieces ? Part{p, p + n, p + 2 * n, 4, 4 * n} : Part{p, p + n, p + 2 * n, a.dh, 4};
 }
 
 // Where row r of a tile goes: token t, query head h.

@@ -66,6 +66,12 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next();
+  if (tid == 160) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmKn);
+    prefetch_tmap(&tmVn);
+  }
   const Share sh = my_share(a);
   if (sh.lo >= sh.hi) return;
   if (tid == 0) {
@@ -89,22 +95,10 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   const uint32_t tmem = tmem_slot;
   const int rt = my_rows(a);
 
-  // The segments of this CTA, walked by every role: blocks blk0 .. blk1 - 1 of tile `tile`.
-  int b = sh.b, off = sh.off, item = sh.lo;
-  SeqBlocks sb = seq_blocks(a, b, false);
-  int tile = 0, blk0 = 0, blk1 = 0;
-  auto segment = [&]() -> bool {
-    if (item >= sh.hi) return false;
-    while ((tile = off / sb.nb) >= a.Hkv / a.hl) {
-      sb = seq_blocks(a, ++b, false);
-      off = 0;
-    }
-    blk0 = off - tile * sb.nb;
-    blk1 = min(sb.nb, blk0 + sh.hi - item);
-    off += blk1 - blk0;
-    item += blk1 - blk0;
-    return true;
-  };
+  // The segments of this CTA, walked by every role.
+  Walk at(a, sh);
+  const SeqBlocks& sb = at.sb;
+  const int &b = at.b, &tile = at.tile, &blk0 = at.blk0, &blk1 = at.blk1;
   // Waits of a warp: it goes on or gives up as a whole.
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     return __all_sync(kAll, wait_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
@@ -113,14 +107,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
 
   if (warp == 5) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
-      prefetch_tmap(&tmKn);
-      prefetch_tmap(&tmVn);
-    }
     int id = 0;  // slots so far
-    while (ok && segment()) {
+    while (ok && at.next(a)) {
       const int m = my_heads(a, tile), n = blk1 - blk0;
       int first = -64, pages = -1;  // 32 page numbers, one a lane
       for (int x = 0; x < n && ok; x += PB) {
@@ -193,7 +181,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       tc::commit_warp(&bar_s[i & 1]);
       release(x, 0, n);
     };
-    while (ok && segment()) {
+    while (ok && at.next(a)) {
       const int n = blk1 - blk0;
       ok = waited(&bar_q, seg & 1, kSiteQ, seg);
       tc::fence_after();
@@ -221,7 +209,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
     const uint32_t tS = tmem + ((uint32_t)(32 * warp) << 16), tO = tS + 128;
     int nth = 0, id = 0;  // blocks and ring slots so far
     int slot = 0;
-    while (ok && segment()) {
+    while (ok && at.next(a)) {
       const int m = my_heads(a, tile), r = rt * kRows + tid, n = blk1 - blk0;
       const bool on = r < R, idle = rt * kRows + 32 * warp >= R;
       int t = 0, h = 0, pos = -1;
@@ -331,14 +319,14 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         if (blank) {
           // V's rows that no row of the CTA sees become zeros.  S(n) has been seen, so the slot's last
           // tile (V(n - 2) at the nearest) has been read, and the parity below is that of this one.
-          const int at = id + 2 * ((blk - blk0) / PB) + 1, part = (blk - blk0) % PB;
-          ok = ok && waited(&bar_full[at % NS], (at / NS) & 1, kSiteV, blk);
+          const int i = id + 2 * ((blk - blk0) / PB) + 1, part = (blk - blk0) % PB;
+          ok = ok && waited(&bar_full[i % NS], (i / NS) & 1, kSiteV, blk);
           if (ok && !((used >> (tid >> 1)) & 1)) {
 #pragma unroll
             for (int s = 0; s < SUB; ++s)
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint4*>(ring + (at % NS) * kSlot + (part + s) * kTile + (tid >> 1) * 128 + (tid & 1) * 64 + u * 16) =
+                *reinterpret_cast<uint4*>(ring + (i % NS) * kSlot + (part + s) * kTile + (tid >> 1) * 128 + (tid & 1) * 64 + u * 16) =
                     make_uint4(0, 0, 0, 0);
           }
           tc::fence_async_smem();
@@ -444,7 +432,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       if (pos < 0) l = 0.f;
       const bool whole = blk0 == 0 && blk1 == sb.nb;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t at = ((int64_t)b * a.T + t) * a.H + h;
+      const int64_t to = ((int64_t)b * a.T + t) * a.H + h;
       const Part part = part_of(a, blockIdx.x, slot);
 #pragma unroll
       for (int q = 0; q < DH / 32; ++q) {
@@ -453,25 +441,25 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         tc::ld_wait_row(o);
         if (!on) continue;
         if (whole) {
-          uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + at * DH + 32 * q);
+          uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + to * DH + 32 * q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               w[e] = l == 0.f ? 0u : pack_bf16(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
-            to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            row[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          float4* to = reinterpret_cast<float4*>(part.o + (int64_t)tid * DH + 32 * q);
-#pragma unroll
+          #pragma unroll
           for (int i = 0; i < 8; ++i)
-            to[i] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            *reinterpret_cast<float4*>(part.at(tid, 32 * q + 4 * i)) =
+                l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (on) {
         if (whole) {
-          a.lse[at] = l == 0.f ? -CUDART_INF_F : mx * a.scale + logf(l);
+          a.lse[to] = l == 0.f ? -CUDART_INF_F : mx * a.scale + logf(l);
         } else {
           part.m[tid] = l == 0.f ? -CUDART_INF_F : mx * sl2;
           part.l[tid] = l;
