@@ -101,6 +101,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   const int &b = at.b, &tile = at.tile, &blk0 = at.blk0, &blk1 = at.blk1;
   // Waits of a warp: it goes on or gives up as a whole.
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
+    if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
     return __all_sync(kAll, wait_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
   };
   bool ok = true;
@@ -261,9 +262,65 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         hole = hole || page < 0 || page >= a.pages;
       }
       const bool holes = __any_sync(kAll, hole);
-      bool ready = false;    // the block's logits were seen to be complete
       bool settled = false;  // every row that sees something has a reference
+      const int run1 = holes || idle ? blk0 : min(in1, blk1);
+      uint32_t p[4][8];
+      uint64_t sums[4], k2 = tc::f2(sl2, sl2), b2 = 0;
+      auto weigh = [&](const float (&s)[32], int q) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x, y;
+          tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, b2), x, y);
+          x = tc::ex2(x);
+          y = tc::ex2(y);
+          sums[i & 3] = q == 0 && i < 4 ? tc::f2(x, y) : tc::add2(sums[i & 3], tc::f2(x, y));
+          p[2 * q + i / 8][i % 8] = pack_bf16(x, y);
+        }
+      };
+      auto total = [&]() {
+        float x, y;
+        tc::uf2(tc::add2(tc::add2(sums[0], sums[1]), tc::add2(sums[2], sums[3])), x, y);
+        return x + y;
+      };
+      auto set_base = [&]() {
+        const float base = mx == -CUDART_INF_F ? 0.f : -mx * sl2;
+        b2 = tc::f2(base, base);
+      };
       for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
+        // Blocks that are seen whole, by references that hold: one straight run of instructions (a taken
+        // branch costs a warp some 50 to 200 cycles of fetching; the block's arithmetic takes 700).
+        if (settled && blk >= in0 && blk < run1) {
+          set_base();
+          uint32_t there = 0;  // the block's logits were seen to be complete
+          for (;;) {
+            if (__builtin_expect(!__all_sync(kAll, there), 0)) {
+              ok = waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
+              if (!ok) break;
+            }
+            tc::fence_after();
+            const uint32_t tP = tS + 64 * (nth & 1);
+            float s0[32], s1[32];
+            tc::ld32x32b_x32(tP, s0);
+            tc::ld_wait_row(s0);
+            tc::ld32x32b_x32(tP + 32, s1);  // on its way while the first half is weighed
+            weigh(s0, 0);
+            tc::ld_wait_row(s1);
+            weigh(s1, 1);
+            const float sum = total();
+            if (__builtin_expect(__any_sync(kAll, sum > kMost), 0)) break;  // weighed again below
+            l += sum;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
+            there = tc::mbar_test(&bar_s[(nth + 1) & 1], ((nth + 1) >> 1) & 1);  // used at the next block
+            tc::st_wait();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar_p[nth & 1]);
+            ++nth;
+            if (++blk >= run1) break;
+          }
+          if (!ok || blk >= blk1) break;
+        }
         const bool inner = blk >= in0 && blk < in1 && !holes;
         uint64_t see = ~0ull;  // keys that this row sees
         uint64_t used = 0;     // where `blank`: keys that some row of the CTA sees
@@ -314,8 +371,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             if (!ctx) used &= seen;
           }
         }
-        if (!ready) ok = ok && waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
-        ready = false;
+        ok = ok && waited(&bar_s[nth & 1], (nth >> 1) & 1, kSiteS, blk);
         if (blank) {
           // V's rows that no row of the CTA sees become zeros.  S(n) has been seen, so the slot's last
           // tile (V(n - 2) at the nearest) has been read, and the parity below is that of this one.
@@ -342,7 +398,6 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         // The weights by the reference in use; where a row's sum shows that it is outgrown (or
         // there is none yet), once more by the new one.
         bool exact = !settled;
-        uint32_t p[4][8];
         float sum;
         // Of 32 logits of the row, what it does not see becomes -inf.
         auto hide = [&](float (&s)[32], int q) {
@@ -387,38 +442,23 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
               }
             }
           }
-          const float base = mx == -CUDART_INF_F ? 0.f : -mx * sl2;
-          const uint64_t k2 = tc::f2(sl2, sl2), b2 = tc::f2(base, base);
-          uint64_t sums[4] = {0, 0, 0, 0};
-          auto weigh = [&](float (&s)[32], int q) {
-            hide(s, q);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x, y;
-              tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, b2), x, y);
-              x = tc::ex2(x);
-              y = tc::ex2(y);
-              sums[i & 3] = tc::add2(sums[i & 3], tc::f2(x, y));
-              p[2 * q + i / 8][i % 8] = pack_bf16(x, y);
-            }
-          };
+          set_base();
           float s0[32], s1[32];
           tc::ld32x32b_x32(tP, s0);
           tc::ld_wait_row(s0);
-          tc::ld32x32b_x32(tP + 32, s1);  // on its way while the first half is weighed
+          tc::ld32x32b_x32(tP + 32, s1);
+          hide(s0, 0);
           weigh(s0, 0);
           tc::ld_wait_row(s1);
+          hide(s1, 1);
           weigh(s1, 1);
-          float x, y;
-          tc::uf2(tc::add2(tc::add2(sums[0], sums[1]), tc::add2(sums[2], sums[3])), x, y);
-          sum = x + y;
+          sum = total();
           if (exact || !__any_sync(kAll, sum > kMost)) break;
           exact = true;
         }
         l += sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
-        if (blk + 1 < blk1) ready = __all_sync(kAll, tc::mbar_try(&bar_s[(nth + 1) & 1], ((nth + 1) >> 1) & 1)) != 0;
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
