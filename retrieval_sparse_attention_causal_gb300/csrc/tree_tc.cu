@@ -42,6 +42,11 @@ constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a b
 constexpr uint32_t kAll = 0xffffffffu;
 enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteS, kSiteP, kSiteO, kSiteV };
 
+// The rest of a wait that its first probe did not end: off the straight path, and one copy of it.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
+  return __all_sync(kAll, wait_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
+}
+
 template <int DH>
 struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
@@ -102,55 +107,70 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   // Waits of a warp: it goes on or gives up as a whole.
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
-    return __all_sync(kAll, wait_or_abort(bar, parity, &abort_s, a.err, site, tile, at)) != 0;
+    return wait_on(bar, parity, &abort_s, a.err, site, tile, at);
   };
   bool ok = true;
 
   if (warp == 5) {
     // ---------------------------------------------------------------- loads
-    int id = 0;  // slots so far
+    int id = 0, st = 0;     // slots so far, the next
+    uint32_t parity = 0;    // of its filling
     while (ok && at.next(a)) {
       const int m = my_heads(a, tile), n = blk1 - blk0;
-      int first = -64, pages = -1;  // 32 page numbers, one a lane
+      // 32 page numbers at a time, one a lane, and the next 32; behind the pool, which reads zeros,
+      // where there is no page.
+      int pages = 0, next = 0;
+      auto pages_at = [&](int blk) {
+        int page = -1;
+        if (blk + lane < sb.np) page = a.table[(int64_t)b * a.width + sb.p0 + blk + lane];
+        if (page >= 0 && page < a.pages) return page;
+        if (page != -1) flag_bad_index(a.err, page);
+        return (int)a.pages;
+      };
       for (int x = 0; x < n && ok; x += PB) {
-        const int count = min(PB, n - x);
+        if (x % 32 == 0) {
+          pages = x == 0 ? pages_at(blk0) : next;
+          if (x + 32 < n) next = pages_at(blk0 + x + 32);
+        }
         int page[PB];
 #pragma unroll
-        for (int i = 0; i < PB; ++i) {
-          const int blk = blk0 + x + i;
-          if (blk < sb.np && i < count) {
-            if (blk - first >= 32) {
-              first = blk;
-              pages = blk + lane < sb.np ? a.table[(int64_t)b * a.width + sb.p0 + blk + lane] : -1;
-            }
-            page[i] = __shfl_sync(kAll, pages, blk - first);
-            if (page[i] < 0 || page[i] >= a.pages) {
-              if (page[i] != -1 && lane == 0) flag_bad_index(a.err, page[i]);
-              page[i] = (int)a.pages;  // behind the pool: reads zeros
-            }
-          }
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v, ++id) {  // K, then V
-          const int st = id % NS;
-          if (id >= NS) ok = ok && waited(&bar_empty[st], (id / NS - 1) & 1, kSiteEmpty, x);
+        for (int i = 0; i < PB; ++i) page[i] = __shfl_sync(kAll, pages, (x + i) % 32);
+        const int count = min(PB, n - x);
+        const bool full = x + PB <= min(n, sb.np - blk0);  // blocks of the context
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {  // K, then V
+          ok = ok && waited(&bar_empty[st], parity ^ 1, kSiteEmpty, x);
           if (!ok) break;
           unsigned char* to = ring + st * kSlot;
-          tc::mbar_expect_tx_warp(&bar_full[st], count * SUB * kTile);
+          uint64_t* bar = &bar_full[st];
+          if (__builtin_expect(full, 1)) {
+            tc::mbar_expect_tx_warp(bar, kSlot);
 #pragma unroll
-          for (int i = 0; i < PB; ++i) {
-            if (i >= count) break;
-            const int blk = blk0 + x + i;
+            for (int i = 0; i < PB; ++i)
 #pragma unroll
-            for (int s = 0; s < SUB; ++s, to += kTile) {
-              if (blk < sb.np) {
-                tc::tma_load_4d_warp(to, v ? &tmV : &tmK, 64 * s, m, 0, page[i], &bar_full[st]);
-              } else {  // the draft's (an axis of stride 0 has one entry in the map)
-                const int64_t hs = v ? a.vn_hs : a.kn_hs, ts = v ? a.vn_ts : a.kn_ts, bs = v ? a.vn_bs : a.kn_bs;
-                tc::tma_load_4d_warp(to, v ? &tmVn : &tmKn, 64 * s, hs ? m : 0, ts ? (blk - sb.np) * kChunk : 0, bs ? b : 0,
-                                     &bar_full[st]);
+              for (int s = 0; s < SUB; ++s)
+                tc::tma_load_4d_warp(to + (i * SUB + s) * kTile, v ? &tmV : &tmK, 64 * s, m, 0, page[i], bar);
+          } else {
+            tc::mbar_expect_tx_warp(bar, count * SUB * kTile);
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+              if (i >= count) break;
+              const int blk = blk0 + x + i;
+#pragma unroll
+              for (int s = 0; s < SUB; ++s, to += kTile) {
+                if (blk < sb.np) {
+                  tc::tma_load_4d_warp(to, v ? &tmV : &tmK, 64 * s, m, 0, page[i], bar);
+                } else {  // the draft's (an axis of stride 0 has one entry in the map)
+                  const int64_t hs = v ? a.vn_hs : a.kn_hs, ts = v ? a.vn_ts : a.kn_ts, bs = v ? a.vn_bs : a.kn_bs;
+                  tc::tma_load_4d_warp(to, v ? &tmVn : &tmKn, 64 * s, hs ? m : 0, ts ? (blk - sb.np) * kChunk : 0, bs ? b : 0, bar);
+                }
               }
             }
+          }
+          ++id;
+          if (++st == NS) {
+            st = 0;
+            parity ^= 1;
           }
         }
       }
@@ -159,49 +179,61 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&bar_full[i % NS], (i / NS) & 1, 1u << 16);
   } else if (warp == 4) {
     // ---------------------------------------------------------------- products
-    int seg = 0, nth = 0, id = 0;  // segments, blocks and slots so far
+    int seg = 0, nth = 0;  // segments and blocks so far
+    int ks = 0, vs = 1;    // the slots that K and V come from, and the parities they are filled at
+    uint32_t kp = 0, vp = 0;
+    auto pass = [](int& slot, uint32_t& parity) {
+      slot += 2;
+      if (slot >= NS) {
+        slot -= NS;
+        parity ^= 1;
+      }
+    };
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
-    // K (v = 0) or V of the segment's block x: its address, once its slot is full.
-    auto slot_of = [&](int x, int v) { return id + 2 * (x / PB) + v; };
-    auto operand = [&](int x, int v) {
-      const int i = slot_of(x, v);
-      if (x % PB == 0) ok = ok && waited(&bar_full[i % NS], (i / NS) & 1, kSiteFull, x);
-      return tc::su32(ring + (i % NS) * kSlot + (x % PB) * kTile);
-    };
-    auto release = [&](int x, int v, int n) {
-      if (x % PB == PB - 1 || x == n - 1) tc::commit_warp(&bar_empty[slot_of(x, v) % NS]);
-    };
-    auto logits = [&](int x, int i, int n) {
-      const uint32_t k = operand(x, 0);
-      if (!ok) return;
-      tc::fence_after();
-#pragma unroll
-      for (int s = 0; s < SUB; ++s)
-        tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (i & 1), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile), kIdS,
-                                                s ? 1u : 0u);
-      tc::commit_warp(&bar_s[i & 1]);
-      release(x, 0, n);
-    };
     while (ok && at.next(a)) {
       const int n = blk1 - blk0;
       ok = waited(&bar_q, seg & 1, kSiteQ, seg);
-      tc::fence_after();
       ++seg;
-      if (ok) logits(0, nth, n);
-      for (int x = 0; x < n && ok; ++x, ++nth) {
-        if (x + 1 < n) logits(x + 1, nth + 1, n);
-        const uint32_t v = operand(x, 1);
-        ok = ok && waited(&bar_p[nth & 1], (nth >> 1) & 1, kSiteP, x);
-        if (!ok) break;
-        tc::fence_after();
+      // Step x: P V of block x, and the logits of block x + 2 in the buffer that P lay in.
+      for (int x0 = -2; x0 < n && ok; x0 += PB) {
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
-          tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 64 * (2 + s), tmem + 64 * (nth & 1), tc::desc_mn(v + s * kTile), kIdPV,
-                                               x > 0 ? 1u : 0u);
-        tc::commit_warp(&bar_o[nth & 1]);
-        release(x, 1, n);
+        for (int i = 0; i < PB; ++i) {
+          const int x = x0 + i, j = nth + x;
+          if (x >= n) break;
+          if (x >= 0) {
+            if (i == 0) ok = waited(&bar_full[vs], vp, kSiteFull, x);
+            ok = ok && waited(&bar_p[j & 1], (j >> 1) & 1, kSiteP, x);
+            if (!ok) break;
+            const uint32_t v = tc::su32(ring + vs * kSlot + i * kTile);
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+              tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tmem + 64 * (2 + s), tmem + 64 * (j & 1), tc::desc_mn(v + s * kTile), kIdPV,
+                                                   x > 0 ? 1u : 0u);
+            tc::commit_warp(&bar_o[j & 1]);
+            if (i == PB - 1 || x == n - 1) {
+              tc::commit_warp(&bar_empty[vs]);
+              pass(vs, vp);
+            }
+          }
+          if (x + 2 < n) {
+            if (i == 0) ok = waited(&bar_full[ks], kp, kSiteFull, x + 2);
+            if (!ok) break;
+            const uint32_t k = tc::su32(ring + ks * kSlot + i * kTile);
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+              tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + 64 * (j & 1), dQ + s * (2 * kTile >> 4), tc::desc_km(k + s * kTile),
+                                                      kIdS, s ? 1u : 0u);
+            tc::commit_warp(&bar_s[j & 1]);
+            if (i == PB - 1 || x + 2 == n - 1) {
+              tc::commit_warp(&bar_empty[ks]);
+              pass(ks, kp);
+            }
+          }
+        }
       }
-      id += 2 * ((n + PB - 1) / PB);
+      nth += n;
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -264,17 +296,17 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       const bool holes = __any_sync(kAll, hole);
       bool settled = false;  // every row that sees something has a reference
       const int run1 = holes || idle ? blk0 : min(in1, blk1);
-      uint32_t p[4][8];
-      uint64_t sums[4], k2 = tc::f2(sl2, sl2), b2 = 0;
-      auto weigh = [&](const float (&s)[32], int q) {
+      uint64_t sums[4], b2 = 0;
+      const uint64_t k2 = tc::f2(sl2, sl2);
+      auto weigh = [&](const float (&s)[32], uint32_t (&p)[2][8]) {  // by the row's reference
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float x, y;
           tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, b2), x, y);
           x = tc::ex2(x);
           y = tc::ex2(y);
-          sums[i & 3] = q == 0 && i < 4 ? tc::f2(x, y) : tc::add2(sums[i & 3], tc::f2(x, y));
-          p[2 * q + i / 8][i % 8] = pack_bf16(x, y);
+          sums[i & 3] = tc::add2(sums[i & 3], tc::f2(x, y));
+          p[i / 8][i % 8] = pack_bf16(x, y);
         }
       };
       auto total = [&]() {
@@ -303,14 +335,19 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
             tc::ld32x32b_x32(tP, s0);
             tc::ld_wait_row(s0);
             tc::ld32x32b_x32(tP + 32, s1);  // on its way while the first half is weighed
-            weigh(s0, 0);
+            uint32_t p0[2][8], p1[2][8];
+            sums[0] = sums[1] = sums[2] = sums[3] = 0;
+            weigh(s0, p0);
             tc::ld_wait_row(s1);
-            weigh(s1, 1);
+            weigh(s1, p1);
             const float sum = total();
             if (__builtin_expect(__any_sync(kAll, sum > kMost), 0)) break;  // weighed again below
             l += sum;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
+            for (int i = 0; i < 2; ++i) {
+              tc::st32x32b_x8(tP + 8 * i, p0[i]);
+              tc::st32x32b_x8(tP + 16 + 8 * i, p1[i]);
+            }
             there = tc::mbar_test(&bar_s[(nth + 1) & 1], ((nth + 1) >> 1) & 1);  // used at the next block
             tc::st_wait();
             tc::fence_before();
@@ -395,70 +432,60 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         }
         tc::fence_after();
         const uint32_t tP = tS + 64 * (nth & 1);
-        // The weights by the reference in use; where a row's sum shows that it is outgrown (or
-        // there is none yet), once more by the new one.
-        bool exact = !settled;
-        float sum;
         // Of 32 logits of the row, what it does not see becomes -inf.
         auto hide = [&](float (&s)[32], int q) {
-          if (__builtin_expect(!inner, 0)) {
-            const uint32_t w = (uint32_t)(see >> (32 * q));
+          const uint32_t w = (uint32_t)(see >> (32 * q));
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((w >> i) & 1)) s[i] = -CUDART_INF_F;
-          }
+          for (int i = 0; i < 32; ++i)
+            if (!((w >> i) & 1)) s[i] = -CUDART_INF_F;
         };
-        for (;;) {
-          if (__builtin_expect(exact, 0)) {
-            float now = mx;
+        // The maximum with this block, and the weights by it.  Loops that are not unrolled: few blocks
+        // come here, and code that is short leaves the caches of instructions to the straight run.
+        float now = mx;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float s[32];
+          tc::ld32x32b_x32(tP + 32 * q, s);
+          tc::ld_wait_row(s);
+          hide(s, q);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float s[32];
-              tc::ld32x32b_x32(tP + 32 * q, s);
-              tc::ld_wait_row(s);
-              hide(s, q);
+          for (int i = 0; i < 32; i += 2) now = tc::max3(now, s[i], s[i + 1]);
+        }
+        const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
+        mx = now;
+        l *= f;
+        settled = __all_sync(kAll, mx != -CUDART_INF_F || pos < 0);
+        if (blk > blk0 && __any_sync(kAll, f != 1.f)) {
+          ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
+          tc::fence_after();
+#pragma unroll 1
+          for (int q = 0; q < DH / 32; ++q) {
+            float o[32];
+            tc::ld32x32b_x32(tO + 32 * q, o);
+            tc::ld_wait_row(o);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) now = tc::max3(now, s[i], s[i + 1]);
-            }
-            const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
-            mx = now;
-            l *= f;
-            settled = __all_sync(kAll, mx != -CUDART_INF_F || pos < 0);
-            if (blk > blk0) {
-              ok = waited(&bar_o[(nth - 1) & 1], ((nth - 1) >> 1) & 1, kSiteO, blk);
-              tc::fence_after();
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[8];
 #pragma unroll
-              for (int q = 0; q < DH / 32; ++q) {
-                float o[32];
-                tc::ld32x32b_x32(tO + 32 * q, o);
-                tc::ld_wait_row(o);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t w[8];
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 * i + e] * f);
-                  tc::st32x32b_x8(tO + 32 * q + 8 * i, w);
-                }
-              }
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[8 * i + e] * f);
+              tc::st32x32b_x8(tO + 32 * q + 8 * i, w);
             }
           }
-          set_base();
-          float s0[32], s1[32];
-          tc::ld32x32b_x32(tP, s0);
-          tc::ld_wait_row(s0);
-          tc::ld32x32b_x32(tP + 32, s1);
-          hide(s0, 0);
-          weigh(s0, 0);
-          tc::ld_wait_row(s1);
-          hide(s1, 1);
-          weigh(s1, 1);
-          sum = total();
-          if (exact || !__any_sync(kAll, sum > kMost)) break;
-          exact = true;
         }
-        l += sum;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc::st32x32b_x8(tP + 8 * i, p[i]);
+        set_base();
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float s[32];
+          tc::ld32x32b_x32(tP + 32 * q, s);
+          tc::ld_wait_row(s);
+          hide(s, q);
+          uint32_t w[2][8];
+          sums[0] = sums[1] = sums[2] = sums[3] = 0;
+          weigh(s, w);
+          l += total();
+          tc::st32x32b_x8(tP + 16 * q, w[0]);  // over logits that have been read
+          tc::st32x32b_x8(tP + 16 * q + 8, w[1]);
+        }
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
@@ -474,7 +501,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t to = ((int64_t)b * a.T + t) * a.H + h;
       const Part part = part_of(a, blockIdx.x, slot);
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < DH / 32; ++q) {
         float o[32];
         tc::ld32x32b_x32(tO + 32 * q, o);
