@@ -40,7 +40,7 @@ constexpr int kTile = 8192;      // 64 tokens x 64 elements
 constexpr int kSlot = 2 * kTile;
 constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
 constexpr uint32_t kAll = 0xffffffffu;
-enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteS, kSiteP, kSiteO, kSiteV };
+enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteS, kSiteP, kSiteO, kSiteV, kSiteRing };
 
 // The rest of a wait that its first probe did not end: off the straight path, and one copy of it.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
@@ -52,8 +52,8 @@ struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
   static constexpr int PB = 2 / SUB;                // blocks of 64 keys of a ring slot: 16 KB of K or of V
   static constexpr int QB = 2 * kTile * SUB;        // a row tile of Q
-  static constexpr int NS = DH == 64 ? 5 : 4;       // ring slots
-  static constexpr int SMEM = QB + NS * kSlot + 1024;
+  static constexpr int NS = DH == 64 ? 6 : 5;       // ring slots: with the barriers' 1 KB, half of an SM's shared memory
+  static constexpr int SMEM = QB + NS * kSlot;
 };
 
 template <int DH>
@@ -64,13 +64,17 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
   constexpr int SUB = C::SUB, NS = C::NS, PB = C::PB;
   constexpr uint32_t kIdS = tc::idesc_bf16(kRows, 64, false), kIdPV = tc::idesc_bf16(kRows, 64, true);
   extern __shared__ __align__(1024) unsigned char dsm[];
-  unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  unsigned char* Qs = dsm;
   unsigned char* ring = Qs + C::QB;
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q, bar_s[2], bar_p[2], bar_o[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next();
+  if (tc::su32(dsm) & 1023) {  // the tiles' swizzle counts on it
+    if (tid == 0) flag_timeout(a.err, kSiteRing, blockIdx.x, 0, 0);
+    return;
+  }
   if (tid == 160) {
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
