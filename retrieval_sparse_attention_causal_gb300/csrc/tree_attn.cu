@@ -418,12 +418,13 @@ Shape shape_of(int B, int T, int g, int Hkv, int dh, int bf16, int width, int wi
   Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, 2 * kSMs};
   // bf16: 16 rows a warp without shared memory, or 128 rows a CTA on the tensor cores?  The
   // first starts and ends faster and re-reads the keys for each 16 rows; the second streams
-  // better.  Measured: 12 heads over 4000 tokens, one token: 10.3 against 13.1 us; 64 sequences
-  // with a window of 512: 29 against 49; 32 sequences over 32K, dh 128: 352 against 323; 48
-  // rows over 10 blocks of 192 sequence-heads: 28 against 23.
+  // better and pays more for going on to another tile.  Measured, first against second, in us:
+  // 12 heads over 4000 tokens, one token: 10.4, 13.5; four sequences over 2K: 15.2, 14.6; 4 heads
+  // of 128, 32 sequences over 2K: 36.9, 31.1; 64 sequences with a window of 512: 28.5, 34.8; drafts
+  // of 64 over 1K tokens, one sequence: 13.1, 13.5; four: 17.6, 15.5.
   const int seen = seen_pages(width, window);
-  const int64_t work = (int64_t)B * Hkv * (seen + (T + 63) / 64) * ((R + 15) / 16);  // blocks, once for each 16 rows
-  const bool few = R <= 16 ? work <= 32 * kSMs || seen < 32 : work <= 12 * kSMs;
+  const int64_t work = (int64_t)B * Hkv * (seen + (T + 63) / 64) * ((R + 15) / 16) * dh / 64;  // 8 KB blocks, once for each 16 rows
+  const bool few = (R <= 16 && seen < 32) || work <= 6 * kSMs;
   if (bf16 && (few || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
   else if (bf16) s = Shape{kTensor, 1, 128, 1, 2 * kSMs};
   s.nrt = (R + s.rows - 1) / s.rows;
