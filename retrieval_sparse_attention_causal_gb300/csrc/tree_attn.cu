@@ -308,25 +308,28 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_ker
       }
     }
   }
-  if (x == 0) {
-    red_m[y] = mx;
-    red_l[y] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < NC; ++i) red_o[y][(i / CV) * 64 + x * CV + i % CV] = o[i];
+  // Each set by the maximum of all; then their sum.
+  if (x == 0) red_m[y] = mx;
   __syncthreads();
-  if (pi != 0 || !on) return;
-  float top = mx;
-  for (int p = 1; p < ps; ++p) top = fmaxf(top, red_m[p * rg + ri]);
-  const float base = top == -CUDART_INF_F ? 0.f : top, f0 = exp2f(mx - base);
+  float top = -CUDART_INF_F;
+#pragma unroll 4
+  for (int p = 0; p < ps; ++p) top = fmaxf(top, red_m[p * rg + ri]);
+  const float f0 = exp2f(mx - (top == -CUDART_INF_F ? 0.f : top));
   l *= f0;
 #pragma unroll
   for (int i = 0; i < NC; ++i) o[i] *= f0;
-  for (int p = 1; p < ps; ++p) {
-    const float f = exp2f(red_m[p * rg + ri] - base);
-    l = fmaf(red_l[p * rg + ri], f, l);
+  if (pi > 0) {
+    if (x == 0) red_l[y] = l;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) o[i] = fmaf(red_o[p * rg + ri][(i / CV) * 64 + x * CV + i % CV], f, o[i]);
+    for (int i = 0; i < NC; ++i) red_o[y][(i / CV) * 64 + x * CV + i % CV] = o[i];
+  }
+  __syncthreads();
+  if (pi != 0 || !on) return;
+#pragma unroll 4
+  for (int p = 1; p < ps; ++p) {
+    l += red_l[p * rg + ri];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) o[i] += red_o[p * rg + ri][(i / CV) * 64 + x * CV + i % CV];
   }
   int t, h;
   row_of(a, rt * a.rows + r, hg * a.hw + hi, t, h);

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
       l[i] += __shfl_xor_sync(kAll, l[i], 1);
       l[i] += __shfl_xor_sync(kAll, l[i], 2);
       const int r = n + 8 * i;
+      if (r >= R) continue;
       if (c == 0) {
         join_m[warp][r] = pos[i] < 0 ? -CUDART_INF_F : mx[i] * sl2;
         join_l[warp][r] = pos[i] < 0 ? 0.f : l[i];
@@ -370,8 +371,9 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
               make_float4(o[e][2 * i + q], o[e + 1][2 * i + q], o[e + 2][2 * i + q], o[e + 3][2 * i + q]);
     }
     __syncthreads();
-    for (int i = 0; i < a.hw; ++i) {
-      const int r = tid >> 3, d0 = (tid & 7) * NV, m = my_heads(a, tile) + i;
+    const int there = min(R, 16);  // rows
+    for (int task = tid; task < a.hw * there * 8; task += kThreads) {
+      const int row = task >> 3, i = row / there, r = row - i * there, d0 = (task & 7) * NV, m = my_heads(a, tile) + i;
       float top = -CUDART_INF_F;
       for (int w = i; w < kWarps; w += a.hw) top = fmaxf(top, join_m[w][r]);
       float sum = 0.f, out[NV];
@@ -384,7 +386,6 @@ __global__ void __launch_bounds__(kThreads, kCtas<DH>) tree_rows_kernel(TreeArgs
 #pragma unroll
         for (int e = 0; e < NV; ++e) out[e] = fmaf(join_o[w][r][d0 + e], f, out[e]);
       }
-      if (r >= R) continue;
       if (blk0 == 0 && blk1 == sb.nb) {
         int t, h;
         row_of(a, 16 * rt + r, m, t, h);
