@@ -219,6 +219,7 @@ struct TreeArgs {
   float scale;
   ErrWord* err;
   unsigned char* part;                                     // partial results
+  int least, far;                                          // log2 of a share's least blocks; one more with more items than `far`
   int lead;                                                // items without work before a tile's blocks
   int hw, hl, rows, nrt, nd;                               // key heads of a CTA, such CTAs of a share, rows of a CTA, groups of rows,
                                                            // blocks of the draft

@@ -406,6 +406,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 }
 
 // ------------------------------------------------------------------ launching
+// Lead and least blocks of a share (see tree_sched.cuh).  Measured without and with the lead: 2 x 64K
+// tokens, 128 rows, 47.8 and 41.3 us; 32 single tokens over 2K, dh 128, 38.5 and 36.9; where a share
+// has a block or two the small kernel is better without (11.9 and 13.3 us).  Shares of one block
+// and of four, 128 rows over 2K and 4K tokens: 15.6 and 13.7, 16.0 and 14.3 us.
 constexpr int kLeadTc = 4, kLeadRows = 1;
 enum Kind { kRows, kTensor, kSimt };
 struct Shape {
@@ -489,6 +493,12 @@ cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
   a.hl = sh.hl;
   a.nd = (a.T + kChunk - 1) / kChunk;
   a.pieces = sh.kind == kTensor;
+  // Each partial of a tile costs the join about 0.04 us and each block a share about 0.4: the best
+  // number of blocks grows with the root of the tile's.  One key head, 64K tokens, 8 rows: shares of
+  // four blocks 19.0 us, of eight 13.7; where 76 shares of each head walk, eight are no better.
+  const int64_t many = (int64_t)400 * a.B * (a.Hkv / (a.hw * a.hl));
+  a.least = sh.kind == kTensor ? 2 : 0;
+  a.far = sh.kind == kTensor && a.grid >= kSMs ? (int)std::min<int64_t>(many, INT32_MAX) : INT32_MAX;
   const int64_t items = (int64_t)a.B * (a.Hkv / (a.hw * a.hl)) * (seen_pages(a.width, a.window) + a.nd);
   a.lead = sh.kind == kTensor ? kLeadTc : (items > 2 * a.grid ? kLeadRows : 0);
   a.wide = (reinterpret_cast<uintptr_t>(a.kp) | reinterpret_cast<uintptr_t>(a.vp)) % 32 == 0;

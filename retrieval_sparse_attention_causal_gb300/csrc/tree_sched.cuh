@@ -80,7 +80,7 @@ __device__ __forceinline__ int all_items(const TreeArgs& a, int b, int& before, 
 __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
   Share s;
   s.W = W;
-  s.G = min(a.grid, W);
+  s.G = max(1, min(a.grid, W >> (W > a.far ? a.least + 1 : a.least)));
   s.q = W / s.G;
   s.rem = W - s.q * s.G;
   return s;

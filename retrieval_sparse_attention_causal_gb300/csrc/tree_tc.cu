@@ -1,26 +1,40 @@
-// Attention of drafted tokens over a paged cache where many query rows share a key head
-// (T g > 16), bf16, dh 64 or 128, on the 5th-generation tensor cores.
+// Attention of drafted tokens over a paged cache where there is much to read, bf16, dh 64 or
+// 128, on the 5th-generation tensor cores.
 //
 // With 128 rows a byte of K or V asks 128 operations: still below the balance of memory and
 // tensor pipes (about 290), so the aim is a stream of pages that never waits.  One CTA walks
 // its share of the blocks for 128 rows (padded) of one key head; two CTAs share an SM.
-//   * one warp loads: page numbers of 32 blocks at a time, and TMA tiles of 64 x 64 into a ring of
-//     16 KB slots, K and V in turn (two tiles a barrier: waiting for one and announcing a load
-//     take about 200 cycles, which at 8 KB a slot held a CTA to 14 bytes a cycle, less than its
-//     share of DRAM).
-//   * one warp issues the products: S(n) = Q K(n)^T into one of two TMEM buffers, one block ahead of the
-//     softmax; O += P(n) V(n) with P in the buffer that S(n) lay in.
+//   * one warp loads: page numbers of 32 blocks at a time (and the next 32 on their way), and TMA
+//     tiles of 64 x 64 into a ring of 16 KB slots, K and V in turn (two tiles a barrier: waiting
+//     for one and announcing a load take about 200 cycles, which at 8 KB a slot held a CTA to 14
+//     bytes a cycle, less than its share of DRAM).  Ring and Q take all of an SM's shared memory:
+//     a slot more was 3 % at dh 64, 7 % at dh 128.
+//   * one warp issues the products: S(n) = Q K(n)^T into one of two TMEM buffers; O += P(n) V(n)
+//     with P in the buffer that S(n) lay in; behind that S(n + 2), which takes the buffer over, so
+//     that the softmax always has a block to go on with.
 //     Barriers of blocks (S ready, P ready, O done) come in pairs, one for even and one for odd
 //     blocks: S(n) is issued before P V (n - 1), so a thread that has seen S(n) knows that
 //     P V (n - 2) is done, not that P V (n - 1) is, and one barrier's parity would not tell.
-//   * four warps a row tile do the softmax: a thread owns a row.  The weights are exp(s - r) with a reference r
+//   * four warps do the softmax: a thread owns a row.  The weights are exp(s - r) with a reference r
 //     that is the row's maximum when it is taken.  It need not stay that: a larger logit only
 //     makes larger weights, and bf16 and float32 round relative to the value.  So a block's
 //     maximum is not computed; when the sum of a row's 64 weights passes 2^14, the block is
 //     weighed again by the new maximum, and the output and the sum so far are scaled to it.
+//     P is rounded to bf16, the type of the product's other operand, so each weight is off by half a
+//     step (2^-8 of it) at most, like the output itself; the sum is of the float32 weights.
 // The last page, the window's edge and the draft's own block are masked by a 64-bit word a
 // row; there the rows of V that nobody sees are set to zeros in shared memory, for a weight
 // of 0 times what lies in them must stay 0.
+//
+// What costs beside the memory is the way of the code to the warps: six warps of three kinds
+// share the instruction caches, and a CTA walks a few blocks to a few hundred.  So blocks that
+// are seen whole run through one straight loop, everything else is rolled up and there once,
+// and a wait whose first probe fails goes on in a function of its own.  Against code that was
+// inlined and unrolled throughout: 2 x 256K tokens, 64 drafted, 16 query and 4 key heads of 64,
+// 200 -> 130 us (1074 MB from L2, half of that from DRAM; issue slots 51 %, tensor pipe 44 %, the
+// exponentials' pipe 44 %, DRAM 52 %: none alone bounds it); 64 of 12 heads over 2 x 128K, 137
+// -> 127 us (6.3 TB/s); 16 sequences of trees in a window of 512, 22.5 -> 18.9 us (launches and
+// the chain of a first block: lengths, page numbers, tiles, products, about 6 us).
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -52,7 +66,7 @@ struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
   static constexpr int PB = 2 / SUB;                // blocks of 64 keys of a ring slot: 16 KB of K or of V
   static constexpr int QB = 2 * kTile * SUB;        // a row tile of Q
-  static constexpr int NS = DH == 64 ? 6 : 5;       // ring slots: with the barriers' 1 KB, half of an SM's shared memory
+  static constexpr int NS = DH == 64 ? 6 : 5;       // ring slots: with 1 KB of barriers and 1 KB of the system's, half of an SM's 228 KB
   static constexpr int SMEM = QB + NS * kSlot;
 };
 
@@ -323,8 +337,8 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
         b2 = tc::f2(base, base);
       };
       for (int blk = blk0; blk < blk1 && ok; ++blk, ++nth) {
-        // Blocks that are seen whole, by references that hold: one straight run of instructions (a taken
-        // branch costs a warp some 50 to 200 cycles of fetching; the block's arithmetic takes 700).
+        // Blocks that are seen whole, by references that hold: one straight run of instructions.  (Each branch
+        // that was taken cost a warp 50 to 200 cycles; a block's arithmetic takes 700.)
         if (settled && blk >= in0 && blk < run1) {
           set_base();
           uint32_t there = 0;  // the block's logits were seen to be complete
