@@ -21,6 +21,12 @@ using bf16 = __nv_bfloat16;
 // ------------------------------------------------------------------ CUDA-core kernel (float32)
 // 128 threads; thread (ty, tx) owns rows ty RT .. ty RT + RT - 1, of a block's logits the
 // keys tx + 16 j, and of the output DH / 16 columns.  K and V pass through shared memory.
+// The path of exact results: products, sums and weights in float32 (a tensor core would round
+// its operands).  Bound by the reads of shared memory: five of 16 bytes for 16 products a thread
+// where a thread has one row, eight for 64 where it has four; nothing hides a block's load but
+// the other CTAs of the SM (four; with two, 12 heads over 64K tokens take 320 us, not 207).
+// Measured: one token of 12 heads over 64K, 207 us (1.9 TB/s); 8 drafts of 16 over 4K, 128 us (10
+// TFLOP/s); 64 drafted tokens of 16 and 4 heads over 16K, 143 us (30 TFLOP/s).
 constexpr int kSimtThreads = 128;
 template <int DH, int RT>
 constexpr int simt_smem() { return (8 * RT * (DH + 4) + 2 * 64 * (DH + 4) + 8 * RT * 68) * 4; }
@@ -235,7 +241,11 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
 // ------------------------------------------------------------------ joining the partials
 // CTA (tile, sequence, row group): rg rows, each by 16 threads over the columns and 16 / rg
 // sets of threads over the partials.  A thread walks its partials once, with a running
-// maximum; the sets are joined in shared memory.
+// maximum; the sets are joined in shared memory.  It finds its partials while the kernel before it
+// still runs, and waits for that one's end.  Bound by latency and by how fast lines that other SMs
+// have just written come back: 1024 rows of 38 partials (10 MB), 6 us from the last partial to the
+// end; 12 rows of 64, 2.6 us.  More CTAs than run at once were slower (9 us there with 1024), a
+// column's rows read a line at a time no faster.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 4 * kSMs;
 constexpr int kJoinFly = 4;  // partials that a thread has on their way
@@ -353,7 +363,8 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 128 ? 3 : 4) tree_join_ker
 
 // ------------------------------------------------------------------ plan of a tree
 // One CTA a sequence, one thread a token.  Ancestors by doubling: after step i a token knows
-// its 2^i nearest ancestors and the one beyond them.
+// its 2^i nearest ancestors and the one beyond them.  Bound by its launch and eight rounds of
+// barriers: 2.4 us for 16 trees of 64, 3.1 for 64 of 256.
 constexpr int kPlanThreads = GCA_MAX_DRAFT;
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a) {
   constexpr int W = GCA_MAX_DRAFT / 64;
@@ -422,7 +433,7 @@ struct Shape {
 int seen_pages(int width, int window) { return window > 0 ? std::min(width, window / kChunk + 2) : width; }
 Shape shape_of(int B, int T, int g, int Hkv, int dh, int bf16, int width, int window) {
   const int R = T * g;
-  Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, 2 * kSMs};
+  Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, (dh == 128 ? 2 : 4) * kSMs};
   // bf16: 16 rows a warp without shared memory, or 128 rows a CTA on the tensor cores?  The
   // first starts and ends faster and re-reads the keys for each 16 rows; the second streams
   // better and pays more for going on to another tile.  Measured, first against second, in us:
