@@ -223,10 +223,16 @@ def random_draft(rng, B, T, lengths, kind):
     return see, pos
 
 
-def attend_and_check(rng, lengths, T, H, Hkv, dh, dtype, kind, window=0, scale=None, holes=False, views=False, seed=0):
+def attend_and_check(rng, lengths, T, H, Hkv, dh, dtype, kind, window=0, scale=None, holes=False, views=False, seed=0, width_spare=1,
+                     rise=0.0):
     g = _g()
     B = len(lengths)
-    k, v, table, _ = random_cache(rng, lengths, Hkv, dh, dtype, seed=seed)
+    k, v, table, _ = random_cache(rng, lengths, Hkv, dh, dtype, seed=seed, width_spare=width_spare)
+    if rise:  # keys that grow along the context, rounded to the type once more
+        for b, n in enumerate(lengths):
+            for j in range(n):
+                k[table[b, j // 64], j % 64] *= 1 + rise * j / n
+        k = host(dev(k, dtype))
     if holes:  # pages that are not held
         for b in range(B):
             table[b, rng.random(table.shape[1]) < 0.3] = -1
@@ -255,7 +261,7 @@ def attend_and_check(rng, lengths, T, H, Hkv, dh, dtype, kind, window=0, scale=N
     dw = 2 * ds + 4 * U * dot_abs + 8 * U + 1.2 * keys * U
     within(host(lse), rl, ds + dw + np.where(np.isfinite(rl), 4 * U * (1 + np.abs(rl)), 0), "lse")
     weight = HALF["bf16"] if dtype == "bf16" else 0.0
-    lim = (2 * dw + weight)[..., None] * mean_abs * (1 + 2 * HALF[dtype]) + 2 * HALF[dtype] * np.abs(ro) + 1e-38
+    lim = ((np.expm1(2 * dw) if rise else 2 * dw) + weight)[..., None] * mean_abs * (1 + 2 * HALF[dtype]) + 2 * HALF[dtype] * np.abs(ro) + 1e-38
     within(host(o), ro, lim, "o")
     return o, lse
 
@@ -307,6 +313,37 @@ def test_tree_attention_strides_holes_and_scale(dtype, T, H, dh):
 def test_tree_attention_long_ragged(T, H, Hkv, dh, dtype):
     """Work split over many CTAs, a long sequence between short ones."""
     attend_and_check(np.random.default_rng(4), [0, 20000, 5, 64, 1], T, H, Hkv, dh, dtype, "tree", seed=3)
+
+
+TENSOR = [  # lengths, T, H, Hkv, dh, kind, window, rise: of the tensor-core kernel
+    ([0], 1, 1, 1, 64, "chain", 0, 0),
+    ([64, 0, 63, 65], 1, 12, 12, 64, "chain", 0, 0),
+    ([700, 3, 129], 1, 16, 4, 128, "chain", 0, 0),
+    ([333, 64, 1, 0], 16, 12, 12, 64, "tree", 0, 0),
+    ([500, 20], 64, 4, 1, 64, "tree", 0, 0),
+    ([150, 70], 65, 4, 2, 128, "tree", 0, 0),
+    ([129, 0], 200, 2, 1, 64, "tree", 0, 0),
+    ([200, 65], 33, 8, 1, 64, "wild", 0, 0),
+    ([100, 65], 9, 8, 2, 128, "wild", 0, 0),
+    ([300, 65, 7], 70, 6, 3, 64, "padded chain", 0, 0),
+    ([260, 64, 0, 1, 130, 99] * 2, 48, 12, 12, 64, "tree", 100, 0),
+    ([200, 65, 130, 64, 1, 0] * 2, 33, 24, 6, 64, "wild", 40, 0),
+    ([100, 65, 300] * 2, 20, 16, 4, 128, "padded chain", 70, 0),
+    ([2000, 700], 3, 4, 1, 64, "chain", 0, 12.0),
+    ([1500, 64], 64, 4, 2, 64, "tree", 0, 8.0),
+    ([900], 40, 4, 1, 128, "wild", 0, 10.0),
+]
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,kind,window,rise", TENSOR)
+def test_tree_attention_on_the_tensor_cores(lengths, T, H, Hkv, dh, kind, window, rise):
+    """Odd sizes, masks and windows where a wide table (or many heads) makes it the kernel that is taken;
+    logits that outgrow the reference of a row's weights again and again."""
+    g = _g()
+    g.profile_begin()
+    attend_and_check(np.random.default_rng(T * 5 + dh), lengths, T, H, Hkv, dh, "bf16", kind, window, width_spare=1 if window else 1000,
+                     rise=rise)
+    assert "tree_tc" in g.profile_end()
 
 
 def test_tree_attention_many_sequences():
