@@ -56,13 +56,6 @@ __device__ __forceinline__ void st32x32b_x8(uint32_t taddr, const uint32_t (&v)[
                : "memory");
 }
 
-// 4 consecutive 32-bit columns of the thread's lane.
-__device__ __forceinline__ void st32x32b_x4(uint32_t taddr, const uint32_t (&v)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
-               : "memory");
-}
-
 // Announcement of `bytes`, and a 4-D TMA tile load, by one elected lane of a converged warp that
 // calls with the same operands (a one-lane branch around them costs about twice the issue time).
 __device__ __forceinline__ void mbar_expect_tx_warp(uint64_t* bar, uint32_t bytes) {
