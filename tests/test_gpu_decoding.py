@@ -653,7 +653,7 @@ def test_fork_and_trim_flag_bad_entries():
         cache.check()
 
 
-@pytest.mark.parametrize("pages,seed", [(1, 0), (9, 1), (200, 2), (1000, 3)])
+@pytest.mark.parametrize("pages,seed", [(1, 0), (9, 1), (200, 2), (1000, 3), (8191, 4), (8192, 5), (8193, 6), (11000, 7)])
 def test_compact(pages, seed):
     rng = np.random.default_rng(seed)
     lengths = []
@@ -663,12 +663,23 @@ def test_compact(pages, seed):
     if lengths:
         cache.fork(ints([0]), ints([len(lengths)]))
         model.fork([0], [len(lengths)])
-    gone = [s for s in range(1, len(lengths)) if rng.random() < 0.4]
+    gone = [s for s in range(1, len(lengths)) if rng.random() < 0.4][:1024]
     if gone:
         cache.free(ints(gone))
         model.trim(slots=gone, release=True)
     live = cache.compact()
     assert int(live) == model.compact()
+    same_state(cache, model)
+
+
+@pytest.mark.parametrize("pages", [64, 8192, 8256])
+def test_compact_of_a_full_and_of_an_empty_pool(pages):
+    cache, model = cache_pair(np.random.default_rng(0), [4096] * (pages // 64), 64, pages, Hkv=1, dh=32)
+    assert int(cache.compact()) == model.compact() == pages
+    same_state(cache, model)
+    cache.free()
+    model.trim(slots=list(range(pages // 64)), release=True)
+    assert int(cache.compact()) == model.compact() == 0
     same_state(cache, model)
 
 
