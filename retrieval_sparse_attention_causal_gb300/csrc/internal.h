@@ -224,6 +224,7 @@ struct TreeArgs {
   int hw, hl, rows, nrt, nd;                               // key heads of a CTA, such CTAs of a share, rows of a CTA, groups of rows,
                                                            // blocks of the draft
   int grid;                                                // shares of the work, at most
+  int whole;                                               // a share is a sequence: nothing to join
   int pieces;                                              // how partial outputs lie
   int wide;                                                // pools on 32-byte boundaries
 };

@@ -422,38 +422,55 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(TreePlanArgs a)
 // has a block or two the small kernel is better without (11.9 and 13.3 us).  Shares of one block
 // and of four, 128 rows over 2K and 4K tokens: 15.6 and 13.7, 16.0 and 14.3 us.
 constexpr int kLeadTc = 4, kLeadRows = 1;
+constexpr int kJoinTc = 16, kJoinRows = 2;  // what partial results and their join cost, in blocks of a CTA
 enum Kind { kRows, kTensor, kSimt };
 struct Shape {
   Kind kind;
   int hw, rows, nrt;  // key heads and rows of a CTA, groups of rows
   int ctas;           // on the GPU at once
   int hl;             // CTAs of a share side by side over the key heads
+  bool whole;         // a CTA finishes its tile
 };
 // Pages of a sequence that some row can see, at most.
 int seen_pages(int width, int window) { return window > 0 ? std::min(width, window / kChunk + 2) : width; }
 Shape shape_of(int B, int T, int g, int Hkv, int dh, int bf16, int width, int window) {
   const int R = T * g;
   Shape s{kSimt, 1, R <= 8 ? 8 : (R <= 16 ? 16 : 32), 1, (dh == 128 ? 2 : 4) * kSMs};
+  const int seen = seen_pages(width, window), most = seen + (T + kChunk - 1) / kChunk;  // blocks of a tile, at most
+  // Whole tiles: a CTA walks more blocks than a share would have, which must cost less than partial
+  // results and their join.  Measured, joined against whole, in us: 16 trees of 48 tokens in a window
+  // of 512, 12 heads, 19.4, 13.0; 4 of 32 over 1000 tokens 16.6, 14.1; with the small kernel 100 single
+  // tokens over 300 25.9, 21.5, but 64 over 600 30.7, 35.6.  In float32 a block costs too much.
+  auto whole = [&](int64_t tiles, int ctas, int join) { return tiles <= ctas && most * (ctas - tiles) <= (int64_t)join * ctas; };
   // bf16: 16 rows a warp without shared memory, or 128 rows a CTA on the tensor cores?  The
   // first starts and ends faster and re-reads the keys for each 16 rows; the second streams
-  // better and pays more for going on to another tile.  Measured, first against second, in us:
-  // 12 heads over 4000 tokens, one token: 10.4, 13.5; four sequences over 2K: 15.2, 14.6; 4 heads
-  // of 128, 32 sequences over 2K: 36.9, 31.1; 64 sequences with a window of 512: 28.5, 34.8; drafts
-  // of 64 over 1K tokens, one sequence: 13.1, 13.5; four: 17.6, 15.5.
-  const int seen = seen_pages(width, window);
-  const int64_t work = (int64_t)B * Hkv * (seen + (T + 63) / 64) * ((R + 15) / 16) * dh / 64;  // 8 KB blocks, once for each 16 rows
-  const bool few = (R <= 16 && seen < 32) || work <= 6 * kSMs;
-  if (bf16 && (few || dh == 32)) s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
-  else if (bf16) s = Shape{kTensor, 1, 128, 1, 2 * kSMs};
+  // better, has no join where its tiles are whole, and pays more for going on to another.
+  // Measured, first against second, in us: 12 heads over 4000 tokens, one token: 10.1, 14.2; four
+  // sequences over 2K: 15.2, 14.6; 4 heads of 128, 32 sequences over 2K: 36.0, 31.1; 64 sequences with a
+  // window of 512: 27.7, 35.5; 16 of them (whole tiles) 14.2, 10.9; one over 600 tokens 8.6, 11.1, over
+  // 130 8.4, 8.0 (4 heads of 128 10.5, 8.8); drafts of 64 over 1K tokens, four sequences: 18.1, 13.5.
+  const int64_t work = (int64_t)B * Hkv * most * ((R + 15) / 16) * dh / 64;  // 8 KB blocks, once for each 16 rows
+  bool few = (R <= 16 && seen < 32) || work <= 6 * kSMs;
+  const int groups = (R + 127) / 128;
+  if (whole((int64_t)B * Hkv * groups, 2 * kSMs, kJoinTc) && most <= 3 + dh / 32 + work / 190) few = false;
+  int join = 0;
+  if (bf16 && (few || dh == 32)) {
+    s = Shape{kRows, Hkv % 4 == 0 ? 4 : (Hkv % 2 == 0 ? 2 : 1), 16, 1, kSMs * (dh == 32 ? 3 : 2)};
+    join = kJoinRows;
+  } else if (bf16) {
+    s = Shape{kTensor, 1, 128, 1, 2 * kSMs};
+    join = kJoinTc;
+  }
   s.nrt = (R + s.rows - 1) / s.rows;
+  s.whole = join > 0 && whole((int64_t)B * (Hkv / s.hw) * s.nrt, s.ctas, join);
   // As many heads walk together as leave nine shares or more (what does not divide the GPU's
-  // CTAs stays idle: at most a tenth).
-  s.hl = 1;
-  for (int h = 1; h * s.hw <= Hkv; ++h)
+  // CTAs stays idle: at most a tenth); where tiles are whole, all.
+  s.hl = s.whole ? Hkv / s.hw : 1;
+  for (int h = 1; h * s.hw <= Hkv && !s.whole; ++h)
     if (Hkv % (h * s.hw) == 0 && h * s.nrt * 9 <= s.ctas) s.hl = h;
   return s;
 }
-int shares_of(const Shape& s) { return std::max(1, s.ctas / (s.nrt * s.hl)); }
+int shares_of(const Shape& s, int B) { return s.whole ? B : std::max(1, s.ctas / (s.nrt * s.hl)); }
 
 template <int DH, int RT>
 cudaError_t run_simt(const TreeArgs& a, cudaStream_t s) {
@@ -468,7 +485,7 @@ cudaError_t run_dh(const TreeArgs& a, Kind kind, cudaStream_t s) {
   cudaError_t e;
   if constexpr (sizeof(T) == 2) e = kind == kRows ? launch_tree_rows(a, s) : launch_tree_tc(a, s);
   else e = a.rows == 8 ? run_simt<DH, 1>(a, s) : (a.rows == 16 ? run_simt<DH, 2>(a, s) : run_simt<DH, 4>(a, s));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole) return e;
   // Rows of a CTA: as many as leave a thread about four partials to walk (a tile has about
   // grid / tiles of them), and no more than there are.
   const int rows = a.hw * std::min(a.rows, a.T * a.g), tiles = a.Hkv / a.hw * a.nrt;
@@ -492,14 +509,16 @@ cudaError_t run(const TreeArgs& a, Kind kind, cudaStream_t s) {
 
 size_t tree_scratch_bytes(int B, int T, int H, int Hkv, int dh, int bf16, int width, int window) {
   const Shape sh = shape_of(B, T, H / Hkv, Hkv, dh, bf16, width, window);
-  return (size_t)2 * shares_of(sh) * sh.nrt * sh.hl * sh.hw * sh.rows * (dh + 2) * 4;
+  if (sh.whole) return 256;  // nothing is kept there
+  return (size_t)2 * shares_of(sh, B) * sh.nrt * sh.hl * sh.hw * sh.rows * (dh + 2) * 4;
 }
 
 cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
   const Shape sh = shape_of(a.B, a.T, a.g, a.Hkv, a.dh, a.bf16, a.width, a.window);
   a.hw = sh.hw;
   a.rows = sh.rows;
-  a.grid = shares_of(sh);
+  a.grid = shares_of(sh, a.B);
+  a.whole = sh.whole;
   a.nrt = sh.nrt;
   a.hl = sh.hl;
   a.nd = (a.T + kChunk - 1) / kChunk;
@@ -511,7 +530,7 @@ cudaError_t launch_tree_attention(TreeArgs a, cudaStream_t s) {
   a.least = sh.kind == kTensor ? 2 : 0;
   a.far = sh.kind == kTensor && a.grid >= kSMs ? (int)std::min<int64_t>(many, INT32_MAX) : INT32_MAX;
   const int64_t items = (int64_t)a.B * (a.Hkv / (a.hw * a.hl)) * (seen_pages(a.width, a.window) + a.nd);
-  a.lead = sh.kind == kTensor ? kLeadTc : (items > 2 * a.grid ? kLeadRows : 0);
+  a.lead = sh.whole ? 0 : sh.kind == kTensor ? kLeadTc : (items > 2 * a.grid ? kLeadRows : 0);
   a.wide = (reinterpret_cast<uintptr_t>(a.kp) | reinterpret_cast<uintptr_t>(a.vp)) % 32 == 0;
   return a.bf16 ? run<bf16>(a, sh.kind, s) : run<float>(a, sh.kind, s);
 }

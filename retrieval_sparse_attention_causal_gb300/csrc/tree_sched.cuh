@@ -19,6 +19,9 @@
 // one that its share begins in to the first of its two slots, the one that it ends in to the
 // second; the joining kernel finds a tile's partials by the same arithmetic.
 //
+// Where the tiles are short and all of them find a CTA at once, a share is a sequence, its CTAs
+// finish a tile each, and there is nothing to join.
+//
 // Going on to another tile costs a CTA the queries' load, a pipeline that fills again and a
 // second result.  So each tile has `lead` items without work before its first block, about
 // what that costs in blocks: a share that holds them has fewer blocks.
@@ -89,6 +92,12 @@ __device__ __forceinline__ Share shares(const TreeArgs& a, int W) {
 // This CTA's share; called by whole warps, each for itself.
 __device__ __forceinline__ Share my_share(const TreeArgs& a) {
   const int lane = threadIdx.x & 31, tiles = a.Hkv / (a.hw * a.hl), share = blockIdx.x / (a.hl * a.nrt);
+  if (a.whole) {
+    Share s{};
+    s.b = share;
+    s.hi = seq_blocks(a, share, blockIdx.x % (a.hl * a.nrt) == 0 && threadIdx.x == 0).items;
+    return s;
+  }
   int before;
   Share s = shares(a, all_items(a, 0, before, blockIdx.x == 0 && threadIdx.x < 32));
   s.lo = share < s.G ? first_item(s, share) : s.W;

@@ -346,6 +346,52 @@ def test_tree_attention_on_the_tensor_cores(lengths, T, H, Hkv, dh, kind, window
     assert "tree_tc" in g.profile_end()
 
 
+ROWS = [  # lengths, T, H, Hkv, dh, kind, window, pages of the table behind the longest: of the kernel of 16 rows
+    ([64, 0, 63, 65], 1, 12, 12, 64, "chain", 0, 24),
+    ([700, 3, 129], 1, 16, 4, 128, "chain", 0, 15),
+    ([130, 64], 2, 6, 2, 64, "chain", 0, 24),
+    ([200, 0, 64], 5, 4, 4, 64, "tree", 0, 24),
+    ([333, 64, 1, 0], 16, 12, 12, 64, "tree", 0, 24),
+    ([500, 20], 64, 4, 1, 64, "tree", 0, 14),
+    ([150, 70], 65, 4, 2, 128, "tree", 0, 7),
+    ([200, 65], 33, 8, 1, 64, "wild", 0, 18),
+    ([100, 65], 9, 8, 2, 128, "wild", 0, 24),
+    ([300, 65, 7], 12, 4, 4, 64, "padded chain", 0, 24),
+    ([260, 64, 0, 1, 130, 99] * 6, 5, 12, 12, 64, "tree", 70, 1),
+    ([260, 64, 0, 1, 130, 99] * 7, 3, 48, 12, 128, "wild", 40, 1),
+    ([260, 64, 0, 1, 130, 99] * 7, 16, 16, 16, 64, "padded chain", 9, 1),
+]
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,kind,window,spare", ROWS)
+def test_tree_attention_of_sixteen_rows(lengths, T, H, Hkv, dh, kind, window, spare):
+    """The same where there is little to read, but too much for whole tiles of the other kernel."""
+    g = _g()
+    g.profile_begin()
+    attend_and_check(np.random.default_rng(T * 3 + dh), lengths, T, H, Hkv, dh, "bf16", kind, window, width_spare=spare)
+    assert "tree_rows" in g.profile_end()
+
+
+WHOLE = [  # lengths, T, H, Hkv, dh, dtype, kind, window: a tile a CTA, nothing to join
+    ([0], 1, 1, 1, 64, "bf16", "chain", 0),
+    ([64, 0, 63, 65], 1, 12, 12, 64, "bf16", "chain", 0),
+    ([500, 20, 800], 64, 16, 4, 64, "bf16", "tree", 0),
+    ([700, 3, 129] * 5, 48, 12, 12, 64, "bf16", "tree", 512),
+    ([700, 3, 129] * 2, 150, 8, 4, 128, "bf16", "wild", 300),
+    ([100, 0, 65] * 84, 2, 4, 4, 32, "bf16", "tree", 0),
+    ([100, 0, 300] * 32, 1, 12, 12, 64, "bf16", "chain", 0),
+]
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,dtype,kind,window", WHOLE)
+def test_tree_attention_of_whole_tiles(lengths, T, H, Hkv, dh, dtype, kind, window):
+    g = _g()
+    g.profile_begin()
+    attend_and_check(np.random.default_rng(T * 2 + dh), lengths, T, H, Hkv, dh, dtype, kind, window)
+    names = g.profile_end()
+    assert "tree_join" not in names and ("tree_rows" in names or "tree_tc" in names)
+
+
 def test_tree_attention_many_sequences():
     attend_and_check(np.random.default_rng(8), [int(x) for x in np.random.default_rng(1).integers(0, 90, 300)], 1, 2, 1, 32,
                      "bf16", "chain")
