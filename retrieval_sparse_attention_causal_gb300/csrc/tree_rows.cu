@@ -20,8 +20,8 @@
 // the units of a head; the warps of one head join their results in shared memory once per
 // tile.
 //
-// Such calls are bound by latency.  One token of 12 heads over 4000 tokens: 9.7 us, of which 1.8 are
-// the bytes' at DRAM's rate: 2 us of launches, 1.1 to the share, 0.8 to the queries, 2.5 for one
+// Such calls are bound by latency.  One token of 12 heads over 4000 tokens: 10.0 us, of which 1.8 are
+// the bytes' at DRAM's rate: about 2 us of launches, 1.1 to the share, 0.8 to the queries, 2.5 for one
 // block, 0.7 for the results, 2.6 for the join.  64 single tokens with a window of 512: 27.7 us (3.6
 // TB/s).  Tried and slower or equal: one copy of the loop's code (28.8 us there), the partial
 // results written by all rows' threads (28.6).
