@@ -16,7 +16,6 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
-#include <cstring>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -200,7 +199,8 @@ PyObject* rotary(Args a) {
 }
 
 // ---------------------------------------------------------------- pools
-// k_pages, v_pages, table, lengths, refs (or None)
+// k_pages, v_pages, table, lengths, refs (or None): the state as the tensors have it at this call.  Nothing
+// of it is kept: a tensor that was replaced or resized since the last call is seen as it is.
 gca_cache pool_of(Args a, On& on) {
   const Tensor &k = tensor(a[0], "k_pages"), &v = tensor(a[1], "v_pages"), &table = tensor(a[2], "table"), &len = tensor(a[3], "lengths");
   const Tensor* refs = optional(a[4], "refs");
@@ -216,25 +216,11 @@ gca_cache pool_of(Args a, On& on) {
                    static_cast<int32_t*>(table.data_ptr()), (int)table.size(0), (int)table.size(1),
                    static_cast<int32_t*>(len.data_ptr()), refs ? static_cast<int32_t*>(refs->data_ptr()) : nullptr};
 }
-// What PagedCache keeps of its tensors: the struct and the device.
-struct Pool {
-  gca_cache c;
-  int dev;
-};
-PyObject* pool(Args a) {
+// k_pages, v_pages, table, lengths, refs: refused where a call on them would be.
+PyObject* check_pool(Args a) {
   On on;
-  Pool p{};
-  p.c = pool_of(a, on);
-  p.dev = on.device();
-  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&p), sizeof p);
-}
-Pool unpack(PyObject* o, On& on, std::initializer_list<const Tensor*> ts) {
-  if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != sizeof(Pool)) throw Refused{PyExc_TypeError, "not a pool"};
-  Pool p;
-  memcpy(&p, PyBytes_AS_STRING(o), sizeof p);
-  for (const Tensor* t : ts) on.add(t);
-  need(on.device() < 0 || on.device() == p.dev, "tensors must live on the cache's device");
-  return p;
+  pool_of(a, on);
+  Py_RETURN_NONE;
 }
 
 // ---------------------------------------------------------------- attention
@@ -270,17 +256,11 @@ PyObject* attend(const gca_cache& c, On& on, Args x, Args y) {
                            static_cast<float*>(lse ? lse->data_ptr() : l_new.data_ptr()), w.p, w.n, s.p, s.n, on.stream()));
   return pair(out ? same(y[4]) : wrap(o_new), lse ? same(y[5]) : wrap(l_new));
 }
-// q, k_new, v_new, k_pages, v_pages, table, lengths, None, mask, positions, window, scale, out, lse, ws
+// q, k_new, v_new, the cache's five, mask, positions, window, scale, out, lse, ws
 PyObject* tree_attention(Args a) {
   On on;
   const gca_cache c = pool_of(a + 3, on);
   return attend(c, on, a, a + 8);
-}
-// pool, q, k_new, v_new, mask, positions, window, scale, out, lse, ws
-PyObject* pool_attention(Args a) {
-  On on;
-  const Pool p = unpack(a[0], on, {&tensor(a[1], "q")});
-  return attend(p.c, on, a + 1, a + 4);
 }
 // parents, lengths, ws
 PyObject* tree_plan(Args a) {
@@ -309,78 +289,81 @@ const int32_t* entries(const Tensor* slots, int64_t n, const gca_cache& c) {
   else need(n == c.slots, "without `slots` the call has one entry for each slot");
   return ints(slots);
 }
-// pool, k_new, v_new, counts, path, slots, ws
+// The cache's five, then: k_new, v_new, counts, path, slots, ws
 PyObject* append(Args a) {
-  const Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new"), &counts = tensor(a[3], "counts");
-  const Tensor *path = optional(a[4], "path"), *slots = optional(a[5], "slots"), *ws = optional(a[6], "ws");
+  const Tensor &k = tensor(a[5], "k_new"), &v = tensor(a[6], "v_new"), &counts = tensor(a[7], "counts");
+  const Tensor *path = optional(a[8], "path"), *slots = optional(a[9], "slots"), *ws = optional(a[10], "ws");
   On on;
-  const Pool p = unpack(a[0], on, {&k, &v, &counts, path, slots, ws});
+  const gca_cache c = pool_of(a, on);
+  for (const Tensor* t : {&k, &v, &counts, path, slots, ws}) on.add(t);
   need(k.dim() == 4, "k_new, v_new must be [n, T, heads, dh]");
   const int64_t n = k.size(0), T = k.size(1);
   for (const Tensor* t : {&k, &v})
-    need(t->dim() == 4 && t->size(0) == n && t->size(1) == T && t->size(2) == p.c.heads && t->size(3) == p.c.dh && dtype_of(*t) == p.c.dtype && unit(*t),
+    need(t->dim() == 4 && t->size(0) == n && t->size(1) == T && t->size(2) == c.heads && t->size(3) == c.dh && dtype_of(*t) == c.dtype && unit(*t),
          "k_new, v_new must be [n, T, heads, dh] of the pages' type, with unit stride in the last dim");
   need_int32(counts, {n}, "counts");
   if (path) need_int32(*path, {n, T}, "path");
-  const int32_t* ids = entries(slots, n, p.c);
+  const int32_t* ids = entries(slots, n, c);
   need(T <= INT32_MAX, "a size is out of range");
   on.enter();
   const Word w(ws, on);
   const Scratch s(gca_cache_append_scratch_size((int)n, (int)T), on);
   const gca_heads hk = heads(k), hv = heads(v);
-  check(gca_cache_append(&p.c, &hk, &hv, (int)n, (int)T, ids, ints(&counts), ints(path), w.p, w.n, s.p, s.n, on.stream()));
+  check(gca_cache_append(&c, &hk, &hv, (int)n, (int)T, ids, ints(&counts), ints(path), w.p, w.n, s.p, s.n, on.stream()));
   Py_RETURN_NONE;
 }
-// pool, src, dst, ws
+// src, dst, ws
 PyObject* fork(Args a) {
-  const Tensor &src = tensor(a[1], "src"), &dst = tensor(a[2], "dst");
-  const Tensor* ws = optional(a[3], "ws");
+  const Tensor &src = tensor(a[5], "src"), &dst = tensor(a[6], "dst");
+  const Tensor* ws = optional(a[7], "ws");
   On on;
-  const Pool p = unpack(a[0], on, {&src, &dst, ws});
+  const gca_cache c = pool_of(a, on);
+  for (const Tensor* t : {&src, &dst, ws}) on.add(t);
   need(src.dim() == 1 && src.size(0) >= 1 && src.size(0) <= INT32_MAX, "src and dst must be int32 [n]");
   need_int32(src, {src.size(0)}, "src");
   need_int32(dst, {src.size(0)}, "dst");
   on.enter();
   const Word w(ws, on);
-  check(gca_cache_fork(&p.c, (int)src.size(0), ints(&src), ints(&dst), w.p, w.n, on.stream()));
+  check(gca_cache_fork(&c, (int)src.size(0), ints(&src), ints(&dst), w.p, w.n, on.stream()));
   Py_RETURN_NONE;
 }
-// pool, table, begin, end, slots, release, ws
+// begin, end, slots, release, ws
 PyObject* trim(Args a) {
-  const Tensor& table = tensor(a[1], "table");  // a tensor of the cache, for its device
-  const Tensor *begin = optional(a[2], "begin"), *end = optional(a[3], "end"), *slots = optional(a[4], "slots"), *ws = optional(a[6], "ws");
+  const Tensor *begin = optional(a[5], "begin"), *end = optional(a[6], "end"), *slots = optional(a[7], "slots"), *ws = optional(a[9], "ws");
   On on;
-  const Pool p = unpack(a[0], on, {&table, begin, end, slots, ws});
+  const gca_cache c = pool_of(a, on);
+  for (const Tensor* t : {begin, end, slots, ws}) on.add(t);
   const Tensor* first = begin ? begin : end ? end : slots;
   need(!first || first->dim() == 1, "begin, end and slots must be int32 [n]");
-  const int64_t n = first ? first->size(0) : p.c.slots;
+  const int64_t n = first ? first->size(0) : c.slots;
   if (begin) need_int32(*begin, {n}, "begin");
   if (end) need_int32(*end, {n}, "end");
-  const int32_t* ids = entries(slots, n, p.c);
+  const int32_t* ids = entries(slots, n, c);
   on.enter();
   const Word w(ws, on);
-  check(gca_cache_trim(&p.c, (int)n, ids, ints(begin), ints(end), (int)integer(a[5]), w.p, w.n, on.stream()));
+  check(gca_cache_trim(&c, (int)n, ids, ints(begin), ints(end), (int)integer(a[8]), w.p, w.n, on.stream()));
   Py_RETURN_NONE;
 }
-// pool, table, ws
+// ws
 PyObject* compact(Args a) {
-  const Tensor& table = tensor(a[1], "table");
-  const Tensor* ws = optional(a[2], "ws");
+  const Tensor* ws = optional(a[5], "ws");
   On on;
-  const Pool p = unpack(a[0], on, {&table, ws});
+  const gca_cache c = pool_of(a, on);
+  on.add(ws);
   on.enter();
   Tensor live = at::empty({1}, on.options(at::kInt));
   const Word w(ws, on);
-  const Scratch s(gca_cache_compact_scratch_size(p.c.pages), on);
-  check(gca_cache_compact(&p.c, static_cast<int32_t*>(live.data_ptr()), w.p, w.n, s.p, s.n, on.stream()));
+  const Scratch s(gca_cache_compact_scratch_size(c.pages), on);
+  check(gca_cache_compact(&c, static_cast<int32_t*>(live.data_ptr()), w.p, w.n, s.p, s.n, on.stream()));
   return wrap(live);
 }
-// pool, idx, slots, ws
+// idx, slots, ws
 PyObject* lookup(Args a) {
-  const Tensor& idx = tensor(a[1], "idx");
-  const Tensor *slots = optional(a[2], "slots"), *ws = optional(a[3], "ws");
+  const Tensor& idx = tensor(a[5], "idx");
+  const Tensor *slots = optional(a[6], "slots"), *ws = optional(a[7], "ws");
   On on;
-  const Pool p = unpack(a[0], on, {&idx, slots, ws});
+  const gca_cache c = pool_of(a, on);
+  for (const Tensor* t : {&idx, slots, ws}) on.add(t);
   need(idx.scalar_type() == at::kInt && idx.dim() >= 2 && idx.is_contiguous() && idx.numel() >= 1 && idx.numel() <= INT32_MAX,
        "idx must be a contiguous int32 [n, ...] tensor");
   const int64_t n = idx.size(0);
@@ -388,7 +371,7 @@ PyObject* lookup(Args a) {
   on.enter();
   Tensor out = at::empty_like(idx);
   const Word w(ws, on);
-  check(gca_cache_lookup(&p.c, (int)n, (int)(idx.numel() / n), ints(slots), ints(&idx), static_cast<int32_t*>(out.data_ptr()), w.p, w.n, on.stream()));
+  check(gca_cache_lookup(&c, (int)n, (int)(idx.numel() / n), ints(slots), ints(&idx), static_cast<int32_t*>(out.data_ptr()), w.p, w.n, on.stream()));
   return wrap(out);
 }
 PyObject* error_word_of(Args a) { return wrap(error_word(as_int(a[0], "device"))); }
@@ -427,9 +410,9 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
 }
 PyMethodDef g_methods[] = {
-    method<rotary, 9>("rotary"), method<pool, 5>("pool"), method<tree_attention, 15>("tree_attention"),
-    method<pool_attention, 11>("pool_attention"), method<tree_plan, 3>("tree_plan"), method<append, 7>("append"),
-    method<fork, 4>("fork"), method<trim, 7>("trim"), method<compact, 3>("compact"), method<lookup, 4>("lookup"),
+    method<rotary, 9>("rotary"), method<check_pool, 5>("check_pool"), method<tree_attention, 15>("tree_attention"),
+    method<tree_plan, 3>("tree_plan"), method<append, 11>("append"), method<fork, 8>("fork"), method<trim, 10>("trim"),
+    method<compact, 6>("compact"), method<lookup, 8>("lookup"),
     method<error_word_of, 1>("error_word"), method<set_error, 1>("set_error"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_gca_decoding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -107,12 +107,15 @@ class PagedCache:
     The pool is also a K/V store for gca_forward: gca_forward(q, *cache.store(),
     cache.lookup(idx), scores, shift=0, kv_shared=True) attends to retrieved chunks where
     they lie.  Calls change the state in place, in stream order; no call waits for the
-    device.  What a call could not do is flagged in the error word (see check())."""
+    device.  What a call could not do is flagged in the error word (see check()).
 
-    __slots__ = ("k_pages", "v_pages", "table", "lengths", "refs", "ws", "_pool")
+    The five tensors are all there is: each call takes them as they are then, so that one of
+    them may be replaced (a larger pool, a wider table) and a copy is a cache of its own."""
+
+    __slots__ = ("k_pages", "v_pages", "table", "lengths", "refs", "ws")
 
     def __init__(self, k_pages, v_pages, table, lengths, refs, ws: Workspace = None):
-        self._pool = EXT.pool(k_pages, v_pages, table, lengths, refs)
+        EXT.check_pool(k_pages, v_pages, table, lengths, refs)
         self.k_pages, self.v_pages, self.table, self.lengths, self.refs = k_pages, v_pages, table, lengths, refs
         self.ws = ws
 
@@ -131,32 +134,33 @@ class PagedCache:
         """Adds counts[i] tokens (int32 [n], 0 .. T) behind the last of slots[i] (default:
         entry i is slot i): rows 0 .. of k_new, v_new [n, T, heads, dh], or the rows that
         path int32 [n, T] names (an accepted path of a draft).  See gca_cache_append."""
-        EXT.append(self._pool, k_new, v_new, counts, path, slots, _word(self.ws))
+        EXT.append(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, k_new, v_new, counts, path, slots,
+                   _word(self.ws))
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor):
         """Slots dst[i] (int32 [n], empty) become copies of slots src[i] that share their
         pages; a shared last page is copied when one of them appends (gca_cache_fork)."""
-        EXT.fork(self._pool, src, dst, _word(self.ws))
+        EXT.fork(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, src, dst, _word(self.ws))
 
     def trim(self, begin: torch.Tensor = None, end: torch.Tensor = None, slots: torch.Tensor = None):
         """Keeps tokens begin[i] .. end[i]-1 (int32 [n]) of the slots and gives back the pages
         outside: `end` takes back the last tokens, `begin` lets go of pages that a window has
         passed (gca_cache_trim)."""
-        EXT.trim(self._pool, self.table, begin, end, slots, 0, _word(self.ws))
+        EXT.trim(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, begin, end, slots, 0, _word(self.ws))
 
     def free(self, slots: torch.Tensor = None):
         """Empties the slots (int32 [n]; default: all) and gives back their pages."""
-        EXT.trim(self._pool, self.table, None, None, slots, 1, _word(self.ws))
+        EXT.trim(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, None, None, slots, 1, _word(self.ws))
 
     def compact(self) -> torch.Tensor:
         """Moves the pages in use to the lowest numbers (gca_cache_compact); returns their
         count, an int32 [1] device tensor: the pages from there on are free."""
-        return EXT.compact(self._pool, self.table, _word(self.ws))
+        return EXT.compact(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, _word(self.ws))
 
     def lookup(self, idx: torch.Tensor, slots: torch.Tensor = None) -> torch.Tensor:
         """Page numbers of retrieved chunks (gca_cache_lookup): idx int32 [n, ...], chunk j of
         slot slots[i] (default: entry i is slot i) or -1; returns int32 like idx."""
-        return EXT.lookup(self._pool, idx, slots, _word(self.ws))
+        return EXT.lookup(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, idx, slots, _word(self.ws))
 
     def store(self):
         """The pools as a K/V store shared by all sequences, for gca_forward and gather_chunks:
@@ -166,7 +170,8 @@ class PagedCache:
     def attention(self, q, k_new, v_new, mask=None, positions=None, window: int = 0, scale: float = None, out=None,
                   lse=None):
         """tree_attention over this cache: sequence b is slot b."""
-        return EXT.pool_attention(self._pool, q, k_new, v_new, mask, positions, window, scale, out, lse, _word(self.ws))
+        return EXT.tree_attention(q, k_new, v_new, self.k_pages, self.v_pages, self.table, self.lengths, self.refs, mask,
+                                  positions, window, scale, out, lse, _word(self.ws))
 
     def check(self):
         """Synchronise the current stream and raise GCAError if a call flagged an entry since

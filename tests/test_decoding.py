@@ -196,3 +196,43 @@ def test_oracle_rotary():
     assert np.allclose([y[0, 1, 0, 1], y[0, 1, 0, 3]], [z.real, z.imag])
     back = orc.rotary(y, np.array([[0, 7]]), w, gain=0.5, backward=True)
     assert np.allclose(back, x)
+
+
+class Recorder:
+    """Stands in for the native binding: keeps the arguments of the last call."""
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.__dict__["last"] = args
+            return b"kept"
+        return call
+
+
+def test_paged_cache_hands_over_the_tensors_that_it_shows(gca, monkeypatch):
+    """Every call gets the cache's tensors as they are at that call: of a deep copy or an unpickled
+    cache its own, after an assignment the new one.  (Addresses kept from an earlier time would be
+    those of another cache, or of memory that was given back.)"""
+    import copy
+    import pickle
+    from retrieval_sparse_attention_causal_gb300 import decoding
+    rec = Recorder()
+    monkeypatch.setattr(decoding, "EXT", rec)
+    names = ("k_pages", "v_pages", "table", "lengths", "refs")
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    pages = torch.zeros(4, 64, 2, 64)
+    cache = gca.PagedCache(pages, pages.clone(), i(3, 2), i(3), i(4))
+    x = torch.zeros(3, 1, 2, 64)
+
+    def handed_over(c):
+        for call, at in ((lambda: c.append(x, x, i(3)), 0), (lambda: c.fork(i(1), i(1)), 0), (lambda: c.trim(end=i(3)), 0),
+                         (c.free, 0), (c.compact, 0), (lambda: c.lookup(i(3, 1)), 0), (lambda: c.attention(x, x, x), 3)):
+            call()
+            for n, t in zip(names, rec.last[at:at + 5]):
+                assert t is getattr(c, n), n
+
+    handed_over(cache)
+    for twin in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        assert all(getattr(twin, n).data_ptr() != getattr(cache, n).data_ptr() for n in names)
+        handed_over(twin)
+    cache.table, cache.k_pages, cache.v_pages, cache.refs = i(3, 9), torch.zeros(8, 64, 2, 64), torch.zeros(8, 64, 2, 64), i(8)
+    handed_over(cache)

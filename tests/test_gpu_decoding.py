@@ -893,3 +893,43 @@ def test_lookup_flags():
     assert got.tolist() == [[[t[1, 0], t[1, 1], -1, -1]], [[-1, t[0, 1], t[0, 0], -1]], [[-1] * 4]]
     with pytest.raises(g.GCAError):
         cache.check()
+
+
+def test_copies_and_replaced_tensors_of_a_cache():
+    """A deep copy (and an unpickled cache) is a cache of its own; a larger pool, a wider table and
+    more slots take effect at the next call; tensors that do not fit together are refused."""
+    import copy
+    import pickle
+    g = _g()
+    cache, model = cache_pair(np.random.default_rng(7), [100, 0, 64], 3, 12)
+    kn, vn = new_rows(8, 3, 40)
+    before = copy.deepcopy(model)
+    for twin in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        other = copy.deepcopy(before)
+        twin.append(dev(kn, "bf16"), dev(vn, "bf16"), ints([3, 40, 1]))
+        other.append(kn, vn, [3, 40, 1])
+        same_state(twin, other)
+        same_state(cache, model)
+        del twin
+    cache.append(dev(kn, "bf16"), dev(vn, "bf16"), ints([1, 2, 3]))
+    model.append(kn, vn, [1, 2, 3])
+    same_state(cache, model)
+    more = synth.normal(3, 20, (5, 64, 2, 32), 1.0, "bf16")
+    cache.k_pages, cache.v_pages = (torch.cat([p, dev(more, "bf16")]) for p in (cache.k_pages, cache.v_pages))
+    with pytest.raises(ValueError):
+        cache.compact()  # the counts are those of the smaller pool
+    cache.refs = torch.cat([cache.refs, ints([0] * 5)])
+    cache.table = torch.cat([cache.table, ints([[-1] * 2] * 3)], 1)
+    model.k, model.v = (np.concatenate([p, more]) for p in (model.k, model.v))
+    model.refs = np.concatenate([model.refs, np.zeros(5, dtype=np.int64)])
+    model.table = np.concatenate([model.table, np.full((3, 2), -1)], 1)
+    kn, vn = new_rows(9, 3, 200)
+    cache.append(dev(kn, "bf16"), dev(vn, "bf16"), ints([200, 150, 140]))
+    model.append(kn, vn, [200, 150, 140])
+    assert not model.full
+    same_state(cache, model)
+    cache.check()
+    q, k1, v1 = (dev(synth.normal(4, s, (3, 1, n, 32), 1.0, "bf16"), "bf16") for s, n in ((22, 4), (23, 2), (24, 2)))
+    o, _ = cache.attention(q, k1, v1)
+    want, _ = g.tree_attention(q, k1, v1, cache.k_pages, cache.v_pages, cache.table, cache.lengths)
+    assert torch.equal(o, want)
