@@ -220,12 +220,19 @@ class Pages:
         live = int((self.refs > 0).sum())
         moved = [p for p in range(live, len(self.refs)) if self.refs[p] > 0]
         holes = [p for p in range(live) if self.refs[p] == 0]
+        held = self.refs > 0
         to = {a: b for a, b in zip(moved, holes)}
         for a, b in to.items():
             self.k[b], self.v[b] = self.k[a], self.v[a]
             self.refs[b], self.refs[a] = self.refs[a], 0
         for e, page in np.ndenumerate(self.table):
-            self.table[e] = to.get(int(page), page)
+            if page == -1:
+                continue
+            if not 0 <= page < len(held) or not held[page]:  # no page, or a free one
+                self.flagged = True
+                self.table[e] = -1
+            else:
+                self.table[e] = to.get(int(page), page)
         return live
 
     def tokens(self, s):

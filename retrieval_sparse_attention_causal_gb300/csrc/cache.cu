@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(1024) trim_kernel(CacheArgs c, const int32_t* 
 // ------------------------------------------------------------------ compact
 // With n pages in use, those numbered n and above move, in order, to the free numbers
 // below n, in order: no other choice moves fewer.  Three launches: uses per part of the
-// pool; the two lists; the rows and the tables.  A pool of up to kSmallPool pages takes two: one
+// pool; the two lists, and for every page its rank (-1: free; n and above: its place among those
+// that move); the rows and the tables.  A pool of up to kSmallPool pages takes two: one
 // CTA makes the lists.
 __global__ void __launch_bounds__(256) compact_count_kernel(CompactArgs a) {
   let_next();
@@ -328,13 +329,9 @@ __global__ void __launch_bounds__(1024) compact_lists_kernel(CompactArgs a) {
     const int rank = before + block_scan(used, red, got) - used;  // uses before page p
     before += got;
     if (p >= q1) continue;
-    if (used && p >= n) {
-      a.movers[rank - below] = (int)p;
-      a.rank[p] = rank - below;
-    } else if (!used) {
-      if (p < n) a.holes[p - rank] = (int)p;
-      else a.rank[p] = -1;
-    }
+    if (used && p >= n) a.movers[rank - below] = (int)p;
+    if (!used && p < n) a.holes[p - rank] = (int)p;
+    a.rank[p] = used ? max(rank - below, 0) : -1;
   }
 }
 
@@ -364,16 +361,10 @@ __global__ void __launch_bounds__(1024) compact_small_kernel(CompactArgs a) {
   for (int k = 0; k < kSmallPages; ++k) {
     const int p = p0 + k;
     if (p >= pages) break;
-    if ((used >> k) & 1) {
-      if (p >= n) {
-        a.movers[rank(k) - below] = p;
-        a.rank[p] = rank(k) - below;
-      }
-    } else if (p < n) {
-      a.holes[p - rank(k)] = p;
-    } else {
-      a.rank[p] = -1;
-    }
+    const bool on = (used >> k) & 1;
+    if (on && p >= n) a.movers[rank(k) - below] = p;
+    if (!on && p < n) a.holes[p - rank(k)] = p;
+    a.rank[p] = on ? max(rank(k) - below, 0) : -1;
   }
 }
 
@@ -411,13 +402,15 @@ __global__ void __launch_bounds__(256) compact_move_kernel(CompactArgs a) {
   const int64_t all = (int64_t)c.slots * c.width;
   for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < all; e += (int64_t)gridDim.x * blockDim.x) {
     const int t = c.table[e];
-    if (t < -1 || t >= c.pages) {
+    if (t == -1) continue;
+    // A free page's number is no one's: it may be the new place of a page that moves.  (Its rank tells; the
+    // counts change while this runs.)
+    const int k = t >= 0 && t < c.pages ? a.rank[t] : -1;
+    if (k < 0) {
       flag_bad_index(c.err, t);
       c.table[e] = -1;
     } else if (t >= n) {
-      const int k = a.rank[t];
-      if (k < 0) flag_bad_index(c.err, t);  // a page that nothing counts
-      c.table[e] = k < 0 ? -1 : a.holes[k];
+      c.table[e] = a.holes[k];
     }
   }
 }

@@ -264,7 +264,7 @@ cudaError_t launch_cache_trim(const CacheArgs& a, const int32_t* begin, const in
 struct CompactArgs {
   CacheArgs c;
   int32_t* live;                                           // out: pages in use
-  int32_t* counts; int32_t* movers; int32_t* holes; int32_t* rank;  // scratch
+  int32_t* counts; int32_t* movers; int32_t* holes; int32_t* rank;  // scratch; rank [pages]: -1 where a page is free
 };
 constexpr int kCompactParts = 152;
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s);

@@ -236,3 +236,11 @@ def test_paged_cache_hands_over_the_tensors_that_it_shows(gca, monkeypatch):
         handed_over(twin)
     cache.table, cache.k_pages, cache.v_pages, cache.refs = i(3, 9), torch.zeros(8, 64, 2, 64), torch.zeros(8, 64, 2, 64), i(8)
     handed_over(cache)
+
+
+def test_oracle_compact_clears_entries_that_name_free_pages():
+    m = orc.Pages(np.arange(6.0).reshape(6, 1, 1, 1) * np.ones((6, 64, 1, 1)), np.zeros((6, 64, 1, 1)),
+                  np.array([[5, 1, -1], [3, 0, 9]]), np.array([128, 64]), np.array([0, 1, 0, 1, 0, 1]))
+    assert m.compact() == 3  # pages 3 and 5 move to 0 and 2; the entry with 0 named a free page, 9 no page
+    assert m.flagged and m.table.tolist() == [[2, 1, -1], [0, -1, -1]] and m.refs.tolist() == [1, 1, 1, 0, 0, 0]
+    assert m.k[:3, 0, 0, 0].tolist() == [3.0, 1.0, 5.0]

@@ -933,3 +933,31 @@ def test_copies_and_replaced_tensors_of_a_cache():
     o, _ = cache.attention(q, k1, v1)
     want, _ = g.tree_attention(q, k1, v1, cache.k_pages, cache.v_pages, cache.table, cache.lengths)
     assert torch.equal(o, want)
+
+
+@flags
+@pytest.mark.parametrize("pages", [40, 8192, 8193, 9000])
+def test_compact_clears_entries_that_name_free_pages(pages):
+    """Entries with a page that nothing counts, below and above the pages that stay, and numbers
+    outside the pool: each becomes -1 and is flagged, and no slot ends with a page of another."""
+    g = _g()
+    rng = np.random.default_rng(pages)
+    lengths = [64 * (pages // 5)] * 3 + [130, 64]
+    cache, model = cache_pair(rng, lengths, pages // 5 + 4, pages, Hkv=1, dh=32)
+    live = int((model.refs > 0).sum())
+    free = [p for p in range(pages) if model.refs[p] == 0]
+    low, high = [p for p in free if p < live], [p for p in free if p >= live]
+    bad = [(0, -1, low[0]), (1, -1, low[0]), (2, -2, low[-1]), (3, -1, high[0]), (4, 3, high[-1]), (4, 2, pages), (3, -2, -7),
+           (0, -2, model.table[1, 0])]  # the last is held: it moves like any other
+    for s, p, page in bad:
+        cache.table[s, p] = int(page)
+        model.table[s, p] = page
+    assert int(cache.compact()) == model.compact() == live
+    assert model.flagged and (model.table >= 0).sum() == live + 1
+    same_state(cache, model)
+    with pytest.raises(g.GCAError) as e:
+        cache.check()
+    assert e.value.status == g.GCA_ERR_DEVICE_INDEX
+    assert int(cache.compact()) == live  # nothing left to move or to clear
+    same_state(cache, model)
+    cache.check()
