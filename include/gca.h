@@ -25,7 +25,7 @@
  *   - `ws` is caller-owned device workspace of at least the size returned by the
  *     matching *_workspace_size function, 256-byte aligned.  Its first 256 bytes are a
  *     sticky device error word: zero it once after allocation; kernels only ever set
- *     bits in it; gca_check_error() reads and clears it.  Different concurrent calls
+ *     bits in it; gca_check_error() reports and clears them.  Different concurrent calls
  *     must use different workspaces.
  *   - Errors: argument problems are reported synchronously (nothing is launched).
  *     A bad retrieved index met by a kernel (outside [-1, nC)) is treated as an empty
@@ -556,7 +556,8 @@ GCA_API gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_new
                               size_t ws_bytes, void* scratch, size_t scratch_bytes, gca_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
- * gca_check_error - synchronise `stream`, read and clear the device error word of `ws`.
+ * gca_check_error - synchronise `stream`, read the device error word of `ws` and clear what
+ * is reported: one kind a call, in the order below, so that the next call reports the next.
  * Returns GCA_OK, GCA_ERR_TIMEOUT (a tensor-core completion wait gave up instead of
  * hanging; the results of that call are not valid), GCA_ERR_DEVICE_INDEX (with the
  * offending index in *bad_value when bad_value != NULL), GCA_ERR_CACHE_FULL or GCA_ERR_CUDA.

@@ -207,8 +207,9 @@ class Workspace:
         return self.buf
 
     def check(self):
-        """Synchronise the current stream and raise GCAError if a kernel flagged a bad
-        retrieved index since the last check (the flag is cleared)."""
+        """Synchronise the current stream and raise GCAError if a kernel flagged something (a
+        wait that ran out, a bad index, a full cache) since the last check.  One kind is
+        raised and cleared a call; the next call raises the next."""
         bad = ctypes.c_int(0)
         _check(LIB.gca_check_error(_ptr(self.buf), _stream(), ctypes.byref(bad)))
 

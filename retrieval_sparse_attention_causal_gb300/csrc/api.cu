@@ -888,19 +888,25 @@ extern "C" gca_status gca_check_error(void* ws, gca_stream_t stream, int* bad_va
   e = cudaMemcpy(&h, ws, sizeof h, cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "gca_check_error read");
   if (h.flags == 0) return GCA_OK;
-  const ErrWord zero{};
-  e = cudaMemcpy(ws, &zero, sizeof zero, cudaMemcpyHostToDevice);
+  // One kind a call, what makes results unusable first: it is cleared, the others stay for the next.
+  const int kind = h.flags & kErrTimeout ? kErrTimeout : h.flags & kErrIndex ? kErrIndex : h.flags;
+  ErrWord left = h;
+  left.flags &= ~kind;
+  if (kind == kErrTimeout) left.wait_sites = left.first[0] = left.first[1] = left.first[2] = left.first[3] = 0;
+  else left.bad_value = 0;
+  e = cudaMemcpy(ws, &left, sizeof left, cudaMemcpyHostToDevice);
   if (e != cudaSuccess) return cuda_fail(e, "gca_check_error clear");
-  if (h.flags & kErrTimeout)
+  const char* more = left.flags ? "; more is flagged: check again" : "";
+  if (kind == kErrTimeout)
     return fail(GCA_ERR_TIMEOUT,
                 "a bounded wait for tensor-core or copy completion ran out (wait sites 0x%x; first: site %d, "
-                "CTA %d, tile %d, slot %d)",
-                (unsigned)h.wait_sites, h.first[0] - 1, h.first[1], h.first[2], h.first[3]);
-  if (!(h.flags & kErrIndex))
+                "CTA %d, tile %d, slot %d)%s",
+                (unsigned)h.wait_sites, h.first[0] - 1, h.first[1], h.first[2], h.first[3], more);
+  if (kind != kErrIndex)
     return fail(GCA_ERR_CACHE_FULL, "a cache had too few free pages, or too narrow a table, for an append");
   if (bad_value) *bad_value = h.bad_value;
   return fail(GCA_ERR_DEVICE_INDEX, "a kernel met index %d out of range (a retrieved chunk outside [-1, nC), or a page, slot, "
-              "count or token)", h.bad_value);
+              "count or token)%s", h.bad_value, more);
 }
 
 // ==================================================================== wait self-test

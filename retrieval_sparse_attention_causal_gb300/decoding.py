@@ -175,6 +175,6 @@ class PagedCache:
 
     def check(self):
         """Synchronise the current stream and raise GCAError if a call flagged an entry since
-        the last check (the flag is cleared)."""
+        the last check (one kind a call: see Workspace.check)."""
         with torch.cuda.device(self.table.device):
             (self.ws or cache_workspace(self.table.device)).check()

@@ -961,3 +961,26 @@ def test_compact_clears_entries_that_name_free_pages(pages):
     assert int(cache.compact()) == live  # nothing left to move or to clear
     same_state(cache, model)
     cache.check()
+
+
+@flags
+def test_checks_report_one_kind_after_the_other():
+    """An append that names a bad slot and runs out of pages, behind a wait that ran out, in one error
+    word: each check reports one kind and leaves the others."""
+    g = _g()
+    for waited in (False, True):
+        cache, model = cache_pair(np.random.default_rng(6), [64, 0, 64], 4, 4)
+        cache.ws = g.Workspace()
+        if waited:
+            g.selftest_timeout(cache.ws, spins=64)
+        kn, vn = new_rows(6, 3, 128)
+        cache.append(dev(kn, "bf16"), dev(vn, "bf16"), ints([128, 1, 128]), slots=ints([0, 7, 2]))
+        model.append(kn, vn, [128, 1, 128], slots=[0, 7, 2])
+        assert model.flagged and model.full
+        same_state(cache, model)
+        for status in [g.GCA_ERR_TIMEOUT] * waited + [g.GCA_ERR_DEVICE_INDEX, g.GCA_ERR_CACHE_FULL]:
+            with pytest.raises(g.GCAError) as e:
+                cache.check()
+            assert e.value.status == status
+            assert ("index 7" in str(e.value)) == (status == g.GCA_ERR_DEVICE_INDEX)
+        cache.check()
