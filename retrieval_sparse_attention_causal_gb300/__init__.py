@@ -134,8 +134,24 @@ def _load_decoding():
     return mod
 
 
+class _NoDecoding:
+    """In the extension's place where it cannot be loaded: the rest of the library works, the
+    decoding operators raise."""
+
+    def __init__(self, why: ImportError):
+        self._why = str(why)
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        raise ImportError(f"the decoding operators need their extension, which could not be loaded: {self._why}")
+
+
 LIB = _load()
-EXT = _load_decoding()
+try:
+    EXT = _load_decoding()
+except ImportError as _e:
+    EXT = _NoDecoding(_e)
 EXPORTS = (
     "gca_status_string", "gca_last_error_detail", "gca_retrieve_workspace_size", "gca_retrieve_topk",
     "gca_retrieve_topk_dseed",

@@ -44,10 +44,27 @@ def _stale(obj, src):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir():
+    """Where torch's headers and libraries are, found without importing it."""
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
+def _binding_made_for():
+    """What the Python extension fits besides its source: this torch and this Python."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{_torch_dir()}\n{f.read()}\n{sys.version}\n"
+
+
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _binding(obj):
-    """Compile command of the Python extension, and its link command (torch's headers and
-    libraries, found without importing it)."""
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    """Compile command of the Python extension, and its link command."""
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
@@ -72,10 +89,10 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
     cuda_jobs = bool(jobs)
     bind_obj = os.path.join(BUILD, "binding.o")
+    bind_for = os.path.join(BUILD, "binding.txt")
     compile_binding, link_binding = _binding(bind_obj)
-    bind_job = _stale(bind_obj, os.path.join(CSRC, "binding.cpp"))
-    if bind_job:
-        jobs.append(compile_binding)
+    made_for = _binding_made_for()
+    bind_job = _stale(bind_obj, os.path.join(CSRC, "binding.cpp")) or _read(bind_for) != made_for
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -86,12 +103,17 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         return r
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bound = ex.submit(run, compile_binding) if bind_job else None
         list(ex.map(run, jobs))
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
     if cuda_jobs or not os.path.exists(LIB):
         run([nvcc, *ARCH, "-shared", "-o", LIB, *objs])
+    if bound:
+        bound.result()  # raised here: the C library is there without the extension too
     if bind_job or not os.path.exists(EXT):
         run(link_binding)
+        with open(bind_for, "w") as f:
+            f.write(made_for)
     return LIB
 
 

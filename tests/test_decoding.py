@@ -244,3 +244,71 @@ def test_oracle_compact_clears_entries_that_name_free_pages():
     assert m.compact() == 3  # pages 3 and 5 move to 0 and 2; the entry with 0 named a free page, 9 no page
     assert m.flagged and m.table.tolist() == [[2, 1, -1], [0, -1, -1]] and m.refs.tolist() == [1, 1, 1, 0, 0, 0]
     assert m.k[:3, 0, 0, 0].tolist() == [3.0, 1.0, 5.0]
+
+
+def test_the_extension_is_built_again_for_another_torch(gca, monkeypatch, tmp_path):
+    """An extension fits the torch and the Python that it was compiled for; where one of them changed,
+    build() compiles it again, and the C library is linked before a compiler's failure there is raised."""
+    import os
+    import subprocess
+    from retrieval_sparse_attention_causal_gb300 import build as b
+    out, torch_dir = tmp_path / "_build", tmp_path / "torch"
+    out.mkdir(), torch_dir.mkdir()
+    (torch_dir / "version.py").write_text("__version__ = '1'\n")
+    fake = lambda name: type("Spec", (), {"submodule_search_locations": [str(torch_dir)]})()  # noqa: E731
+    monkeypatch.setattr(b.importlib.util, "find_spec", fake)
+    for n, f in (("BUILD", out), ("LIB", out / "libgca.so"), ("EXT", out / "_gca_decoding.so")):
+        monkeypatch.setattr(b, n, str(f))
+    made, broken = [], []
+
+    def run(cmd, **kw):
+        target = os.path.basename(cmd[cmd.index("-o") + 1])
+        made.append(target)
+        if target in broken:
+            return subprocess.CompletedProcess(cmd, 1, "", "")
+        (out / target).write_text("")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(b.subprocess, "run", run)
+    b.build()
+    assert sorted(made) == sorted([s.replace(".cu", ".o") for s in b.SOURCES] + ["binding.o", "libgca.so", "_gca_decoding.so"])
+    made.clear()
+    b.build()
+    assert made == []
+    (torch_dir / "version.py").write_text("__version__ = '2'\n")
+    b.build()
+    assert made == ["binding.o", "_gca_decoding.so"]
+    made.clear()
+    (torch_dir / "version.py").write_text("__version__ = '3'\n")
+    (out / "libgca.so").unlink()
+    broken.append("binding.o")
+    with pytest.raises(RuntimeError):
+        b.build()
+    assert "libgca.so" in made and "_gca_decoding.so" not in made
+    broken.clear(), made.clear()
+    b.build()
+    assert made == ["binding.o", "_gca_decoding.so"]
+
+
+@pytest.mark.parametrize("broken", [False, True])
+def test_the_library_imports_without_the_extension(gca, broken, tmp_path):
+    """Without the extension (or with one that does not load) everything but the decoding operators is
+    there, and those say what is missing."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    src = os.path.dirname(gca.__file__)
+    pkg = tmp_path / os.path.basename(src)
+    shutil.copytree(src, pkg, ignore=shutil.ignore_patterns("_build", "csrc", "__pycache__"))
+    (pkg / "_build").mkdir()
+    (pkg / "_build" / "libgca.so").symlink_to(gca.LIB_PATH)
+    if broken:
+        (pkg / "_build" / "_gca_decoding.so").write_text("not a library")
+    code = ("import torch, %s as g\n"
+            "assert g.LIB.gca_forward_workspace_size() == 256 and g.gca_forward and g.retrieve_topk\n"
+            "assert g.rotary_frequencies(8, device='cpu').shape == (4,)\n"
+            "try:\n g.tree_plan(torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))\n"
+            "except ImportError as e:\n assert '_gca_decoding' in str(e)\n"
+            "else:\n raise SystemExit('no error')\n" % pkg.name)
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
