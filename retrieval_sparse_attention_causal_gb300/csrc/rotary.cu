@@ -6,9 +6,11 @@
 //
 // The angle.  w_i arrives as f_i = round(2^64 w_i / 2 pi), so the angle in turns is the
 // low 64 bits of p f_i: whole turns fall off as the integer overflows, and a position of
-// any size costs one multiplication.  The error is |p| 2^-65 turns from f_i (2^-34 at
-// p = 2^31), plus half a unit in the last place of the float that sincospif takes, at
-// most 2^-26 of a turn.  A float product p w_i would be off by a radian at 16M tokens.
+// any size costs one multiplication, which is exact.  What is off, in radians: f_i, computed in
+// double precision, by |p| 2^-49 at most (2^-25 at 16M tokens; at 2^31, 2^-18, which is the
+// largest term there); the cut to the top 32 bits by 2 pi 2^-32; half a unit in the last place of
+// the float that sincospif takes, pi 2^-25.  A float product p w_i would be off by a radian at
+// 16M tokens.
 //
 // Bound by memory: every element is read and written once, three operations each.  A CTA
 // takes some tokens of one sequence, computes their sines and cosines once into shared memory

@@ -312,3 +312,33 @@ def test_the_library_imports_without_the_extension(gca, broken, tmp_path):
             "else:\n raise SystemExit('no error')\n" % pkg.name)
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("rot,kw", [(64, {}), (128, dict(base=5e5)), (128, dict(scaling="linear", factor=16.0)),
+                                    (64, dict(scaling="ntk", factor=4.0)), (4, dict(scaling="ntk", factor=32.0, base=1e6)),
+                                    (128, dict(scaling="parts", factor=8.0, context=8192.0)),
+                                    (256, dict(scaling="parts", factor=32.0, context=2048.0, low=1.0, high=4.0))])
+def test_rotary_frequencies_against_many_digits(gca, rot, kw):
+    """Each speed is within 2^-49 radians a position of its value, as documented.  In units of 2^-53, with
+    x = 2i / rot and w = base^-x <= 1: the rounding of x in the power w x ln(base) <= 1/e, pow itself 2 w; of
+    an NTK base its own error (its power of factor: (ln factor e + 3)) times w x, at most 10 for what is below;
+    by parts c is off by (4 high + low) / (high - low) <= 6, of which 1 - 1 / factor counts, and three products
+    and a sum round; the division by 2 pi and its own rounding 3 w.  Together below 16.  The integer is off by a half, 2^-65
+    turns."""
+    mp = pytest.importorskip("mpmath")
+    with mp.workdps(60):
+        f = lambda x: mp.mpf(float(x))  # noqa: E731
+        base, factor = f(kw.get("base", 10000.0)), f(kw.get("factor", 1.0))
+        scaling = kw.get("scaling")
+        got = gca.rotary_frequencies(rot, device="cpu", **kw).tolist()
+        if scaling == "ntk":
+            base *= factor ** (mp.mpf(rot) / (rot - 2))
+        for i in range(rot // 2):
+            w = base ** (-2 * mp.mpf(i) / rot)
+            if scaling == "linear":
+                w /= factor
+            if scaling == "parts":
+                low, high = f(kw.get("low", 1.0)), f(kw.get("high", 32.0))
+                c = min(mp.mpf(1), max(mp.mpf(0), (f(kw["context"]) * w / (2 * mp.pi) - low) / (high - low)))
+                w = c * w + (1 - c) * w / factor
+            assert abs(mp.mpf(got[i]) * 2 * mp.pi / 2 ** 64 - w) <= mp.mpf(2) ** -49, (i, w)

@@ -984,3 +984,21 @@ def test_checks_report_one_kind_after_the_other():
             assert e.value.status == status
             assert ("index 7" in str(e.value)) == (status == g.GCA_ERR_DEVICE_INDEX)
         cache.check()
+
+
+def test_rotary_turns_by_whole_numbers_exactly():
+    """From the table on, positions cost no precision: the angle is p f mod 2^64 (whole numbers here, so that
+    the speeds' own rounding has no part in it), off by the cut to 32 bits, 2 pi 2^-32, and the float that
+    sincospif takes, pi 2^-25.  The rest as in rotary_bound."""
+    g = _g()
+    rot, H = 64, 2
+    pos = np.array([[0, 1, -1, -12345, 1 << 24, (1 << 31) - 1, -(1 << 31), (1 << 31) - 64]])
+    x = synth.normal(6, 0, (1, pos.shape[1], H, rot), 1.0, "f32")
+    freq = g.rotary_frequencies(rot)
+    turns = [[(p * f) % 2 ** 64 / 2.0 ** 64 for f in freq.tolist()] for p in pos[0].tolist()]
+    angle = 2 * np.pi * np.array(turns)[None, :, None, :]
+    got = host(g.rotary(dev(x, "f32"), None, freq, positions=ints(pos))[0])
+    a, b = x[..., :rot // 2], x[..., rot // 2:]
+    ref = np.concatenate([a * np.cos(angle) - b * np.sin(angle), a * np.sin(angle) + b * np.cos(angle)], -1)
+    lim = np.hypot(a, b) * np.sqrt(2) * (np.pi * (2.0 ** -25 + 2.0 ** -31) + 6 * U) + 1e-40
+    within(got, ref, np.concatenate([lim, lim], -1) + U * np.abs(ref), "rotary")
