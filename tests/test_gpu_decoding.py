@@ -1002,3 +1002,25 @@ def test_rotary_turns_by_whole_numbers_exactly():
     ref = np.concatenate([a * np.cos(angle) - b * np.sin(angle), a * np.sin(angle) + b * np.cos(angle)], -1)
     lim = np.hypot(a, b) * np.sqrt(2) * (np.pi * (2.0 ** -25 + 2.0 ** -31) + 6 * U) + 1e-40
     within(got, ref, np.concatenate([lim, lim], -1) + U * np.abs(ref), "rotary")
+
+
+SHARES = [  # lengths, T, H, Hkv, dh, kind: blocks and leads of a set of heads, and the limit
+    ([25000], 16, 4, 1, 64, "tree"),             # 396 of 400: shares of four blocks or more
+    ([25344], 16, 4, 1, 64, "wild"),             # 401 of 400: shares of eight or more
+    ([30000], 16, 4, 1, 64, "tree"),             # 474 of 400
+    ([30000], 40, 8, 2, 64, "tree"),             # two row groups of two key heads: too few shares for a limit
+    ([33333], 130, 1, 1, 64, "padded chain"),    # two row groups: 528 of 400
+    ([1, 78000, 100], 8, 8, 1, 128, "wild"),     # 1237 of 1200: one long among three
+    ([27000, 26000], 20, 4, 2, 64, "padded chain"),  # 839 of 800
+]
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,kind", SHARES)
+def test_tree_attention_over_many_blocks_of_few_heads(lengths, T, H, Hkv, dh, kind):
+    """Long contexts of one or two key heads, where a share's least length grows: the kernel and the
+    join must divide the work alike on both sides of the limit."""
+    g = _g()
+    g.profile_begin()
+    attend_and_check(np.random.default_rng(T + dh), lengths, T, H, Hkv, dh, "bf16", kind, seed=5)
+    names = g.profile_end()
+    assert "tree_tc" in names and "tree_join" in names
