@@ -269,7 +269,8 @@ PyObject* tree_plan(Args a) {
   need(parents.dim() == 2, "parents must be int32 [B, T]");
   const int64_t B = parents.size(0), T = parents.size(1);
   need_int32(parents, {B, T}, "parents");
-  need_int32(len, {B}, "lengths");
+  need(len.scalar_type() == at::kInt && len.dim() == 1 && len.size(0) >= B && len.is_contiguous(),
+       "lengths must be a contiguous int32 tensor of B entries or more");
   need(B <= INT32_MAX && T <= INT32_MAX, "a size is out of range");
   On on;
   for (const Tensor* t : {&parents, &len, ws}) on.add(t);
@@ -286,7 +287,7 @@ const int32_t* ints(const Tensor* t) { return t ? static_cast<const int32_t*>(t-
 const int32_t* entries(const Tensor* slots, int64_t n, const gca_cache& c) {
   need(n >= 1 && n <= INT32_MAX, "a call needs an entry");
   if (slots) need_int32(*slots, {n}, "slots");
-  else need(n == c.slots, "without `slots` the call has one entry for each slot");
+  else need(n <= c.slots, "without `slots` entry i is slot i: there are more entries than slots");
   return ints(slots);
 }
 // The cache's five, then: k_new, v_new, counts, path, slots, ws

@@ -76,7 +76,7 @@ def rotary_backward(dq: torch.Tensor, dk, freq: torch.Tensor, positions: torch.T
 def tree_plan(parents: torch.Tensor, lengths: torch.Tensor, ws: Workspace = None):
     """Mask and positions of a draft (gca_tree_plan), once for all layers of a step.
     parents int32 [B, T]: the earlier draft token that each follows, -1 for the cache's last
-    token, -2 for padding; lengths int32 [B].  Returns mask int64 [B, T, ceil(T/64)] (bit u
+    token, -2 for padding; lengths int32 [slots >= B].  Returns mask int64 [B, T, ceil(T/64)] (bit u
     of row t: t sees u) and positions int32 [B, T] (-1 for padding)."""
     return EXT.tree_plan(parents, lengths, _word(ws))
 
@@ -107,7 +107,9 @@ class PagedCache:
     The pool is also a K/V store for gca_forward: gca_forward(q, *cache.store(),
     cache.lookup(idx), scores, shift=0, kv_shared=True) attends to retrieved chunks where
     they lie.  Calls change the state in place, in stream order; no call waits for the
-    device.  What a call could not do is flagged in the error word (see check()).
+    device.  What a call could not do is flagged in the error word (see check()).  A page
+    operation takes up to MAX_CACHE_ENTRIES entries; where no slots are named, entry i is slot i
+    and a call may have fewer entries than there are slots.
 
     The five tensors are all there is: each call takes them as they are then, so that one of
     them may be replaced (a larger pool, a wider table) and a copy is a cache of its own."""

@@ -1024,3 +1024,31 @@ def test_tree_attention_over_many_blocks_of_few_heads(lengths, T, H, Hkv, dh, ki
     attend_and_check(np.random.default_rng(T + dh), lengths, T, H, Hkv, dh, "bf16", kind, seed=5)
     names = g.profile_end()
     assert "tree_tc" in names and "tree_join" in names
+
+
+def test_steps_over_the_first_slots_of_a_cache():
+    """A batch may be smaller than the cache: entry i is slot i where no slots are named, and the slots
+    behind keep their state."""
+    g = _g()
+    from retrieval_sparse_attention_causal_gb300 import pipeline
+    rng = np.random.default_rng(12)
+    cache, model = cache_pair(rng, [70, 0, 64, 130, 5], 6, 30)
+    freq = g.rotary_frequencies(32)
+    for B, T in ((2, 3), (1, 1), (3, 70)):
+        q, k, v = (dev(synth.normal(B, s, (B, T, n, 32), 1.0, "bf16"), "bf16") for s, n in ((22, 4), (23, 2), (24, 2)))
+        parents = ints([[t - 1 for t in range(T)]] * B)
+        step = pipeline.draft_step(q, k, v, parents, cache, freq, window=0)
+        mask, pos = g.tree_plan(parents, cache.lengths[:B].clone())
+        assert torch.equal(step["plan"][0], mask) and torch.equal(step["plan"][1], pos)
+        counts = [T, 1, T // 2][:B]
+        path = [list(range(T))] * B
+        begin = [64, 0, 0][:B]
+        pipeline.accept_draft(step, cache, ints(counts), ints(path), begin=ints(begin))
+        model.append(host(step["k"]), host(v), counts, np.array(path))
+        model.trim(begin=begin)
+        same_state(cache, model)
+    with pytest.raises(ValueError):
+        cache.trim(end=ints([1] * 6))  # more entries than slots
+    with pytest.raises(ValueError):
+        g.tree_plan(ints([[-1]] * 6), cache.lengths)
+    same_state(cache, model)
