@@ -530,7 +530,9 @@ GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, cons
  *   q [B][T][H][dh], k_new, v_new [B][T][heads][dh]: free strides, 16-byte aligned, strides
  *           multiples of 16 bytes (0 repeats a sequence or a head; in k_new, v_new not a token).  B <= cache->slots: sequence b is slot b.
  *   mask    [B][T][ceil(T/64)] uint64: bit u % 64 of word u / 64 of row t: t sees u.  NULL: t
- *           sees the tokens u <= t.  Tokens that no row sees are not used in any way.
+ *           sees the tokens u <= t.  Tokens of the cache or the draft that no row sees may hold
+ *           anything; an infinity or NaN that some row sees can reach the sequence's other rows
+ *           (a weight of 0 times it is NaN).
  *   positions [B][T] int32: -1 for padding (seen by none and seeing none), else the token's
  *           position, taken as lengths[b] where it is lower.  NULL: lengths[b] + t.
  *   window  0 (everything) or more.   scale > 0.   T 1..256.   dh 32, 64 or 128.

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
 #pragma unroll
       for (int c = 0; c < NC * CV; ++c) o[i][c] = 0.f;
     }
+    int near = INT32_MAX;  // the lowest position of a row
     for (int blk = blk0; blk < blk1; ++blk) {
       const bool ctx = blk < sb.np;
       int lo = 0, hi = 0, j0 = 0;       // keys lo .. hi - 1 of the block, of which j0 is the first's index
@@ -85,7 +86,6 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
         const int page = a.table[(int64_t)b * a.width + sb.p0 + blk];
         if (page >= 0 && page < a.pages) {
           hi = min(kChunk, sb.len - j0);
-          lo = a.window > 0 ? max(0, sb.len - a.window + 1 - j0) : 0;
           const int64_t at = ((int64_t)page * kChunk * a.Hkv + m) * DH;
           kb = reinterpret_cast<const T*>(a.kp) + at;
           vb = reinterpret_cast<const T*>(a.vp) + at;
@@ -101,6 +101,12 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
         vts = a.vn_ts;
       }
       __syncthreads();  // the last block's readers are done; row_pos is written
+      if (a.window > 0 && ctx) {
+        if (blk == blk0)
+          for (int r = 0; r < MT; ++r)
+            if (row_pos[r] >= 0) near = min(near, row_pos[r]);
+        lo = min(max(near - a.window + 1 - j0, 0), kChunk);
+      }
       // Which keys each row sees, one bit a key; of the draft's, those that any row sees.
       if (!ctx) {
         if (tid < 64) {
@@ -121,11 +127,9 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
           if (!ctx) {
             const int t = (rt * MT + tid) / a.g;
             see &= ((unsigned long long)real_s[1] << 32) | real_s[0];
-            see &= a.mask ? a.mask[((int64_t)b * a.T + t) * a.words + (j0 >> 6)]
-                          : (t - j0 >= 63 ? ~0ull : (t < j0 ? 0ull : (2ull << (t - j0)) - 1));
+            see &= draft_word(a, b, t, j0 >> 6);
             if (a.window > 0 && pos - a.window >= sb.len)  // the window ends inside the draft
-              for (int u = 0; u < kChunk; ++u)
-                if ((see >> u) & 1 && token_position(a, b, j0 + u, sb.len) <= (int64_t)pos - a.window) see &= ~(1ull << u);
+              see = draft_above(a.positions ? a.positions + (int64_t)b * a.T : nullptr, sb.len, j0, see, pos - a.window);
             atomicOr(&used_s, see);
           }
         }

@@ -187,4 +187,21 @@ __device__ __forceinline__ int64_t token_position(const TreeArgs& a, int b, int 
   return p < 0 ? -1 : max(p, len);
 }
 
+// Of the draft's tokens 64 w .. 64 w + 63, those in token t's mask (bit k: token 64 w + k).
+__device__ __forceinline__ uint64_t draft_word(const TreeArgs& a, int b, int t, int w) {
+  if (a.mask) return a.mask[((int64_t)b * a.T + t) * a.words + w];
+  const int past = t - 64 * w;
+  return past >= 63 ? ~0ull : (past < 0 ? 0ull : (2ull << past) - 1);
+}
+// Of the tokens `first` + k with bit k in `word` (all of them there), those at a position above `low`.
+// `at`: the sequence's positions, or null.
+__device__ __forceinline__ uint64_t draft_above(const int32_t* at, int len, int first, uint64_t word, int low) {
+  uint64_t left = 0;
+  for (; word; word &= word - 1) {
+    const int k = __ffsll((long long)word) - 1, u = first + k;
+    if ((at ? max(at[u], len) : len + u) > low) left |= 1ull << k;
+  }
+  return left;
+}
+
 }  // namespace gca

@@ -62,6 +62,20 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_
   return __all_sync(kAll, wait_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
 }
 
+// Masks of a draft whose windows end inside it: of the tokens `first` + k with bit k in `there`, those that
+// tokens x0, x0 + step, .. below x1 see.  Off the straight path too.
+__device__ __noinline__ uint64_t seen_in_windows(const uint64_t* mask, int words, const int32_t* where, int len, int window, int first,
+                                                 uint64_t there, int x0, int x1, int step) {
+  uint64_t seen = 0;
+  for (int x = x0; x < x1; x += step) {
+    const int p = where ? (where[x] < 0 ? -1 : max(where[x], len)) : len + x;
+    if (p < 0) continue;
+    const uint64_t d = there & (mask ? mask[x * words + first / kChunk] : (x - first >= 63 ? ~0ull : (x < first ? 0ull : (2ull << (x - first)) - 1)));
+    seen |= draft_above(where, len, first, d, p - window);
+  }
+  return seen;
+}
+
 template <int DH>
 struct Tc {
   static constexpr int SUB = DH / 64;               // 64-element parts of a head
@@ -268,10 +282,6 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       // What the segment asks of memory, all of it before the first use: Q, the row's position, the
       // page numbers, and of the draft's first block the mask and the positions.
       auto page_at = [&](int blk) { return a.table[(int64_t)b * a.width + sb.p0 + blk]; };
-      auto draft_word = [&](int x, int w) {  // of the draft's tokens 64 w .. 64 w + 63, those in token x's mask
-        if (a.mask) return a.mask[((int64_t)b * a.T + x) * a.words + w];
-        return (uint64_t)(x - 64 * w >= 63 ? ~0ull : (x < 64 * w ? 0ull : (2ull << (x - 64 * w)) - 1));
-      };
       const int32_t* where = a.positions ? a.positions + (int64_t)b * a.T : nullptr;
       if (on) row_of(a, r, m, t, h);
       uint4 w[DH / 8];
@@ -283,19 +293,24 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       int page = blk0 + lane < held ? page_at(blk0 + lane) : 0;
       const bool draft = blk1 > sb.np;
       const int x0 = rt * kRows / a.g + lane, x1 = min(a.T, ((rt + 1) * kRows - 1) / a.g + 1);  // tokens of the CTA's rows
+      // The lowest and the highest position of the CTA's rows.
+      int near = where ? INT32_MAX : sb.len + rt * kRows / a.g, most = where ? -1 : sb.len + x1 - 1;
       uint64_t own = 0, any = 0;  // of the first draft block: this row's mask, all rows' masks
       int real0 = 0, real1 = 0;   // positions of its tokens
-      if (draft) {
-        if (on) own = draft_word(t, 0);
+      if (draft && on) own = draft_word(a, b, t, 0);
+      if (draft || (where && a.window > 0))
         for (int x = x0; x < x1; x += 32) {
           const int p = where ? where[x] : 0;
-          const uint64_t d = draft_word(x, 0);
+          const uint64_t d = draft ? draft_word(a, b, x, 0) : 0;
           any |= p >= 0 ? d : 0;
+          if (where && p >= 0) {
+            near = min(near, p);
+            most = max(most, p);
+          }
         }
-        if (where) {
-          real0 = where[min(lane, a.T - 1)];
-          real1 = where[min(32 + lane, a.T - 1)];
-        }
+      if (draft && where) {
+        real0 = where[min(lane, a.T - 1)];
+        real1 = where[min(32 + lane, a.T - 1)];
       }
 #pragma unroll
       for (int u = 0; u < DH / 8; ++u) *reinterpret_cast<uint4*>(Qs + (u / 8) * 2 * kTile + swz<128>(tid, u % 8)) = w[u];
@@ -304,8 +319,15 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar_q);
       float mx = -CUDART_INF_F, l = 0.f;
+      int far = __reduce_max_sync(kAll, pos);
+      bool passes = false;  // a window ends inside the draft
+      if (a.window > 0) {
+        near = __reduce_min_sync(kAll, near);
+        near = near == INT32_MAX ? sb.len : max(near, sb.len);  // (where all rows are padding, what they see is of no account)
+        far = max(far, near);
+        passes = (int)__reduce_max_sync(kAll, most) - a.window >= sb.len;
+      }
       // Blocks in0 .. in1 - 1 are seen whole by every row of this warp, unless there are holes.
-      const int far = max(__reduce_max_sync(kAll, pos), sb.len);
       const int in0 = a.window > 0 && far >= a.window ? (far - a.window) / kChunk + 1 - sb.p0 : 0, in1 = sb.len / kChunk - sb.p0;
       bool hole = page < 0 || page >= a.pages;  // a page that is not held
       for (int blk = blk0 + 32 + lane; blk < held; blk += 32) {
@@ -386,7 +408,7 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
           const int j0 = ctx ? (sb.p0 + blk) * kChunk : (blk - sb.np) * kChunk;
           // Keys lo .. hi - 1 of the block exist.
           int lo = 0, hi = min(kChunk, (ctx ? sb.len : a.T) - j0);
-          if (ctx && a.window > 0) lo = max(0, sb.len - a.window + 1 - j0);
+          if (ctx && a.window > 0) lo = min(max(near - a.window + 1 - j0, 0), kChunk);
           if (ctx && holes) {
             const int page = page_at(blk);
             if (page < 0 || page >= a.pages) hi = 0;
@@ -400,24 +422,24 @@ tree_tc_kernel(TreeArgs a, const __grid_constant__ CUtensorMap tmK, const __grid
           if (!ctx) {
             uint64_t real = ~0ull;  // tokens that are not padding
             if (j0 > 0) {
-              own = on ? draft_word(t, j0 / kChunk) : 0;
+              own = on ? draft_word(a, b, t, j0 / kChunk) : 0;
               any = 0;
               for (int x = x0; x < x1; x += 32)
-                if (!where || where[x] >= 0) any |= draft_word(x, j0 / kChunk);
+                if (!where || where[x] >= 0) any |= draft_word(a, b, x, j0 / kChunk);
               if (where) {
                 real0 = where[min(j0 + lane, a.T - 1)];
                 real1 = where[min(j0 + 32 + lane, a.T - 1)];
               }
             }
             if (where) real = ((uint64_t)__ballot_sync(kAll, real1 >= 0) << 32) | __ballot_sync(kAll, real0 >= 0);
-            seen = real & (((uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32) | __reduce_or_sync(kAll, (uint32_t)any));
-            uint64_t word = 0;
-            if (pos >= 0) {
-              word = own & see & real;
-              if (a.window > 0 && pos - a.window >= sb.len)  // the window ends inside the draft
-                for (int u = 0; u < kChunk; ++u)
-                  if ((word >> u) & 1 && token_position(a, b, j0 + u, sb.len) <= (int64_t)pos - a.window) word &= ~(1ull << u);
+            real &= see;
+            uint64_t word = pos >= 0 ? own & real : 0;
+            if (__builtin_expect(passes, 0)) {
+              const uint64_t* mask = a.mask ? a.mask + (int64_t)b * a.T * a.words : nullptr;
+              any = seen_in_windows(mask, a.words, where, sb.len, a.window, j0, real, x0, x1, 32);
+              word = seen_in_windows(mask, a.words, where, sb.len, a.window, j0, word, t, pos >= 0 ? t + 1 : t, 1);
             }
+            seen = real & (((uint64_t)__reduce_or_sync(kAll, (uint32_t)(any >> 32)) << 32) | __reduce_or_sync(kAll, (uint32_t)any));
             see = word;
           }
           if (!ctx || lo > 0 || hi < kChunk) {

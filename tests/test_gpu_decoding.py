@@ -1052,3 +1052,64 @@ def test_steps_over_the_first_slots_of_a_cache():
     with pytest.raises(ValueError):
         g.tree_plan(ints([[-1]] * 6), cache.lengths)
     same_state(cache, model)
+
+
+UNSEEN = [  # lengths, T, H, Hkv, dh, dtype, kind, window, pages of the table behind the longest, kernel
+    ([300, 64, 1000, 90], 1, 8, 4, 64, "bf16", "late", 50, 1, None),
+    ([300, 64, 1000, 90] * 40, 1, 12, 12, 64, "bf16", "late", 130, 1, "tree_rows"),
+    ([300, 64, 1000, 90], 5, 4, 4, 32, "bf16", "late", 70, 1, "tree_rows"),
+    ([300, 64, 700, 90], 70, 4, 2, 64, "bf16", "late", 100, 1, "tree_tc"),
+    ([300, 64, 700, 90], 20, 24, 6, 128, "bf16", "late", 200, 1, "tree_tc"),
+    ([300, 64, 700], 150, 4, 2, 64, "bf16", "late", 33, 1, "tree_tc"),
+    ([300, 64, 700], 9, 4, 2, 32, "f32", "late", 70, 1, "tree_simt"),
+    ([300, 64, 700], 70, 4, 2, 64, "f32", "late", 100, 1, "tree_simt"),
+    ([100, 65, 0], 12, 4, 4, 32, "bf16", "far apart", 7, 1, "tree_rows"),
+    ([100, 65, 0], 40, 8, 2, 64, "bf16", "far apart", 9, 1, "tree_tc"),
+    ([100, 65, 0] * 30, 10, 16, 16, 64, "bf16", "far apart", 9, 1, "tree_rows"),
+    ([100, 65, 0], 100, 2, 1, 128, "bf16", "far apart", 60, 1, "tree_tc"),
+    ([100, 65, 0], 70, 2, 1, 32, "f32", "far apart", 30, 1, "tree_simt"),
+    ([100, 65, 3000], 40, 4, 2, 64, "bf16", "far apart", 0, 1000, "tree_tc"),
+]
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,dtype,kind,window,spare,kernel", UNSEEN)
+def test_tree_attention_does_not_use_what_no_row_sees(lengths, T, H, Hkv, dh, dtype, kind, window, spare, kernel):
+    """NaN and infinities in every token of the cache and of the draft that no row sees: behind lengths, in
+    padding, outside all masks, and passed by the window of every row, which is not only what the
+    length tells where positions lie behind it ('late') or a mask names tokens that the window has passed
+    ('far apart')."""
+    g = _g()
+    rng = np.random.default_rng(T + dh + len(lengths))
+    B = len(lengths)
+    k, v, table, _ = random_cache(rng, lengths, Hkv, dh, dtype, width_spare=spare)
+    q = synth.normal(1, 22, (B, T, H, dh), 1.0, dtype)
+    kn, vn = synth.normal(1, 23, (B, T, Hkv, dh), 1.0, dtype), synth.normal(1, 24, (B, T, Hkv, dh), 1.0, dtype)
+    n = np.array(lengths)[:, None]
+    if kind == "late":
+        pos = n + rng.integers(0, 60, (B, 1)) + np.arange(T)
+        see = rng.random((B, T, T)) < 0.5
+    else:
+        pos = n + rng.integers(0, 4 * max(window, 5), (B, T))
+        see = rng.random((B, T, T)) < 0.2
+    pos[:, 1::7] = -1
+    low = pos - window if window else np.full((B, T), -1)
+    for b in range(B):
+        rows = [t for t in range(T) if pos[b, t] >= 0]
+        first = min(low[b, t] for t in rows) + 1
+        for j in range(max(0, min(first, lengths[b]))):
+            k[table[b, j // 64], j % 64], v[table[b, j // 64], j % 64] = np.nan, (np.inf if j % 2 else np.nan)
+        for u in range(T):
+            if pos[b, u] < 0 or not any(see[b, t, u] and pos[b, u] > low[b, t] for t in rows):
+                kn[b, u], vn[b, u] = np.nan, (-np.inf if u % 2 else np.nan)
+    assert np.isnan(kn).any()
+    g.profile_begin()
+    o, lse = g.tree_attention(*(dev(x, dtype) for x in (q, kn, vn, k, v)), ints(table), ints(lengths),
+                              mask=torch.from_numpy(orc.pack_mask(see)).cuda(), positions=ints(pos), window=window)
+    names = g.profile_end()
+    assert kernel is None or kernel in names, names
+    ro, rl, mean_abs, dot_abs, keys = orc.tree_attention(q, kn, vn, k, v, table, lengths, see, pos, window)
+    ds = (2 * dh + 4) * U * dot_abs  # the bounds of attend_and_check
+    dw = 2 * ds + 4 * U * dot_abs + 8 * U + 1.2 * keys * U
+    within(host(lse), rl, ds + dw + np.where(np.isfinite(rl), 4 * U * (1 + np.abs(rl)), 0), "lse")
+    weight = HALF["bf16"] if dtype == "bf16" else 0.0
+    within(host(o), ro, (2 * dw + weight)[..., None] * mean_abs * (1 + 2 * HALF[dtype]) + 2 * HALF[dtype] * np.abs(ro) + 1e-38, "o")
