@@ -535,7 +535,8 @@ GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, cons
  *           (a weight of 0 times it is NaN).
  *   positions [B][T] int32: -1 for padding (seen by none and seeing none), else the token's
  *           position, taken as lengths[b] where it is lower.  NULL: lengths[b] + t.
- *   window  0 (everything) or more.   scale > 0.   T 1..256.   dh 32, 64 or 128.
+ *   window  0 (everything) or more.   scale > 0.   T 1..256.   dh 32, 64 or 128.   A table of
+ *           64 * width + 256 < 2^31.
  *   o       [B][T][H][dh] contiguous, 16-byte aligned.   lse [B][T][H] float32.
  *   ws      >= gca_forward_workspace_size() bytes (error word only).
  *   scratch >= gca_tree_attention_scratch_size() bytes, 256-byte aligned, any contents; one for

@@ -855,6 +855,8 @@ extern "C" gca_status gca_tree_attention(const gca_heads* q, const gca_heads* k_
   if (mask && (reinterpret_cast<uintptr_t>(mask) & 7)) return fail(GCA_ERR_INVALID_ARG, "mask must be 8-byte aligned");
   if ((T > 1 && k_new->token_stride == 0) || (T > 1 && v_new->token_stride == 0))
     return fail(GCA_ERR_UNSUPPORTED, "k_new and v_new may not repeat one token (token stride 0)");
+  if ((int64_t)cache->width * 64 + GCA_MAX_DRAFT > INT32_MAX)
+    return fail(GCA_ERR_UNSUPPORTED, "table too wide: positions behind 64 * width tokens must stay below 2^31");
   // All blocks of 64 keys are numbered in 32 bits.
   if ((double)B * cache->heads * ((double)cache->width + 16) > INT32_MAX)
     return fail(GCA_ERR_UNSUPPORTED, "B, H, T and the table's width are too large together");

@@ -342,3 +342,12 @@ def test_rotary_frequencies_against_many_digits(gca, rot, kw):
                 c = min(mp.mpf(1), max(mp.mpf(0), (f(kw["context"]) * w / (2 * mp.pi) - low) / (high - low)))
                 w = c * w + (1 - c) * w / factor
             assert abs(mp.mpf(got[i]) * 2 * mp.pi / 2 ** 64 - w) <= mp.mpf(2) ** -49, (i, w)
+
+
+def test_attention_refuses_tables_whose_positions_pass_31_bits(gca):
+    """A draft behind a full table of 2^25 - 1 pages would lie at positions above 2^31 - 1."""
+    def attend(width):
+        return gca.LIB.gca_tree_attention(heads(gca), heads(gca), heads(gca), pool(gca, width=width), 2, 5, 8, None, None, 0, 0.125,
+                                          FAKE, FAKE, FAKE, 256, FAKE, 0, None)  # no scratch: nothing is launched
+    assert attend((1 << 25) - 1) == gca.GCA_ERR_UNSUPPORTED and attend((1 << 25) - 4) == gca.GCA_ERR_UNSUPPORTED
+    assert attend((1 << 25) - 5) == gca.GCA_ERR_WORKSPACE
