@@ -220,11 +220,14 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeArgs a) {
 #pragma unroll
       for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (r >= rows) continue;
+      if (sum == 0.f)  // the row saw nothing: what was weighed by 0 goes nowhere
+#pragma unroll
+        for (int c = 0; c < NC * CV; ++c) o[i][c] = 0.f;
       if (whole) {
         int t, h;
         row_of(a, rt * MT + r, m, t, h);
         const int64_t at = ((int64_t)b * a.T + t) * a.H + h;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // sum is 0 where the row saw nothing
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (tx == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : mx[i] * kTreeLn2 + logf(sum);
 #pragma unroll
         for (int c = 0; c < NC * CV; ++c)

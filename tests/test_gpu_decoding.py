@@ -1113,3 +1113,28 @@ def test_tree_attention_does_not_use_what_no_row_sees(lengths, T, H, Hkv, dh, dt
     within(host(lse), rl, ds + dw + np.where(np.isfinite(rl), 4 * U * (1 + np.abs(rl)), 0), "lse")
     weight = HALF["bf16"] if dtype == "bf16" else 0.0
     within(host(o), ro, (2 * dw + weight)[..., None] * mean_abs * (1 + 2 * HALF[dtype]) + 2 * HALF[dtype] * np.abs(ro) + 1e-38, "o")
+
+
+@pytest.mark.parametrize("lengths,T,H,Hkv,dh,dtype,window", [
+    ([100, 0, 700], 1, 4, 2, 32, "f32", 0), ([700, 64], 1, 8, 1, 64, "f32", 0), ([300, 5000], 3, 2, 2, 128, "f32", 100),
+    ([100, 0, 700], 1, 4, 2, 32, "bf16", 0), ([100, 64, 5000], 1, 12, 12, 64, "bf16", 0), ([100, 700], 2, 4, 4, 128, "bf16", 50),
+    ([100, 0, 9000], 70, 4, 2, 64, "bf16", 0), ([100, 700], 200, 4, 2, 64, "bf16", 90)])
+def test_tree_attention_of_padding_alone(lengths, T, H, Hkv, dh, dtype, window):
+    """A sequence whose draft is padding sees nothing, whatever its cache holds: zeros and -inf, beside
+    sequences that are not changed by it."""
+    g = _g()
+    rng = np.random.default_rng(dh)
+    B = len(lengths)
+    k, v, table, _ = random_cache(rng, lengths, Hkv, dh, dtype)
+    q = synth.normal(1, 22, (B, T, H, dh), 1.0, dtype)
+    kn, vn = synth.normal(1, 23, (B, T, Hkv, dh), 1.0, dtype), synth.normal(1, 24, (B, T, Hkv, dh), 1.0, dtype)
+    pos = np.array(lengths)[:, None] + np.arange(T)
+    args = lambda: ([dev(x, dtype) for x in (q, kn, vn, k, v)] + [ints(table), ints(lengths)])  # noqa: E731
+    want, wlse = g.tree_attention(*args(), positions=ints(pos), window=window)
+    pos[-1] = -1
+    for p in table[-1][table[-1] >= 0]:
+        k[p], v[p] = np.nan, np.inf
+    q[-1], kn[-1], vn[-1] = np.inf, np.nan, np.nan
+    o, lse = g.tree_attention(*args(), positions=ints(pos), window=window)
+    assert torch.equal(o[:-1], want[:-1]) and torch.equal(lse[:-1], wlse[:-1])
+    assert not o[-1].any() and bool((lse[-1] == -float("inf")).all())
