@@ -102,6 +102,8 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"compiler failed: {' '.join(cmd)}")
         return r
 
+    if bind_job and os.path.exists(bind_for):
+        os.remove(bind_for)  # written again when the extension is linked
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         bound = ex.submit(run, compile_binding) if bind_job else None
         list(ex.map(run, jobs))

@@ -289,6 +289,33 @@ def test_the_extension_is_built_again_for_another_torch(gca, monkeypatch, tmp_pa
     assert made == ["binding.o", "_gca_decoding.so"]
 
 
+def test_a_link_that_failed_is_made_up_for(gca, monkeypatch, tmp_path):
+    """An extension whose source was compiled anew but not linked is not taken for a current one."""
+    import os
+    import subprocess
+    from retrieval_sparse_attention_causal_gb300 import build as b
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    for n in ("libgca.so", "_gca_decoding.so"):
+        monkeypatch.setattr(b, {"libgca.so": "LIB"}.get(n, "EXT"), str(tmp_path / n))
+    made, broken = [], []
+
+    def run(cmd, **kw):
+        target = os.path.basename(cmd[cmd.index("-o") + 1])
+        made.append(target)
+        if target not in broken:
+            (tmp_path / target).write_text("")
+        return subprocess.CompletedProcess(cmd, int(target in broken), "", "")
+    monkeypatch.setattr(b.subprocess, "run", run)
+    b.build()
+    os.utime(tmp_path / "binding.o", (0, 0))  # as after a change of the source
+    broken.append("_gca_decoding.so")
+    with pytest.raises(RuntimeError):
+        b.build()
+    broken.clear(), made.clear()
+    b.build()
+    assert "_gca_decoding.so" in made
+
+
 @pytest.mark.parametrize("broken", [False, True])
 def test_the_library_imports_without_the_extension(gca, broken, tmp_path):
     """Without the extension (or with one that does not load) everything but the decoding operators is
