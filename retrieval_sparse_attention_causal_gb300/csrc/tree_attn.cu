@@ -24,8 +24,8 @@ using bf16 = __nv_bfloat16;
 // The path of exact results: products, sums and weights in float32 (a tensor core would round
 // its operands).  Bound by the reads of shared memory: five of 16 bytes for 16 products a thread
 // where a thread has one row, eight for 64 where it has four; nothing hides a block's load but
-// the other CTAs of the SM (four; with two, 12 heads over 64K tokens take 320 us, not 207).
-// Measured: one token of 12 heads over 64K, 207 us (1.9 TB/s); 8 drafts of 16 over 4K, 128 us (10
+// the other CTAs of the SM (four; with two, 12 heads over 64K tokens took 320 us where four took 207).
+// Measured: one token of 12 heads over 64K, 192 us (2.1 TB/s); 8 drafts of 16 over 4K, 124 us (10
 // TFLOP/s); 64 drafted tokens of 16 and 4 heads over 16K, 143 us (30 TFLOP/s).
 constexpr int kSimtThreads = 128;
 template <int DH, int RT>

@@ -31,9 +31,9 @@
 // are seen whole run through one straight loop, everything else is rolled up and there once,
 // and a wait whose first probe fails goes on in a function of its own.  Against code that was
 // inlined and unrolled throughout: 2 x 256K tokens, 64 drafted, 16 query and 4 key heads of 64,
-// 200 -> 130 us (1074 MB from L2, half of that from DRAM; issue slots 51 %, tensor pipe 44 %, the
+// 200 -> 131 us (1074 MB from L2, half of that from DRAM; issue slots 53 %, tensor pipe 44 %, the
 // exponentials' pipe 44 %, DRAM 52 %: none alone bounds it); 64 of 12 heads over 2 x 128K, 137
-// -> 127 us (6.3 TB/s); 16 sequences of trees in a window of 512, 22.5 -> 18.9 us, and 13.0 with
+// -> 129 us (6.2 TB/s); 16 sequences of trees in a window of 512, 22.5 -> 18.9 us, and 13.0 with
 // whole tiles and no join (a launch, the chain of a first block: lengths, page numbers, tiles,
 // products, about 6 us, and 0.5 a block).
 #include "common.cuh"
