@@ -61,9 +61,9 @@ typedef enum {
   GCA_ERR_CACHE_FULL = 7    /* (gca_check_error) a cache had no room for an append       */
 } gca_status;
 
-typedef enum { GCA_F32 = 0, GCA_BF16 = 1 } gca_dtype;
+typedef enum { GCA_F32 = 0, GCA_BF16 = 1, GCA_E4M3 = 2 /* pages of a quantised cache only */ } gca_dtype;
 
-enum { GCA_CHUNK = 64, GCA_MAX_TOPK = 16, GCA_MAX_DRAFT = 256, GCA_MAX_CACHE_ENTRIES = 1024 };
+enum { GCA_CHUNK = 64, GCA_MAX_TOPK = 16, GCA_MAX_DRAFT = 256, GCA_MAX_CACHE_ENTRIES = 1024, GCA_MAX_SEQUENCES = 1024 };
 
 /* Human-readable name of a status. */
 GCA_API const char* gca_status_string(gca_status s);
@@ -449,6 +449,75 @@ GCA_API gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_
                       int64_t position_batch_stride, float gain, gca_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * gca_norm_rotary - RMS norm of every head of queries and keys, and their rotary positions, in one pass.
+ *
+ *     y = gain R(p) (x w / sqrt(mean(x^2) + eps))       for each token and head of q and of k
+ * with the mean over the head's dh elements, the weights w [dh] shared by the heads, and R(p), freq,
+ * rot, interleaved, positions and gain as in gca_rotary (elements rot .. dh-1 are not turned).
+ *
+ *   q, k, q_out, k_out, dtype and sizes: as in gca_rotary; outputs may be the inputs themselves.
+ *   q_weight, k_weight [dh] float32 device (k_weight may be NULL without k).   eps >= 0, finite.
+ *
+ * gca_norm_rotary_backward - its gradients.  q, k are its inputs, dq_out, dk_out the gradients of its
+ * outputs; written are dq, dk (they may be dq_out, dk_out themselves) and dq_weight, dk_weight [dh]
+ * float32, sums over all tokens and heads.  Deterministic (no atomics).
+ *   scratch >= gca_norm_rotary_backward_scratch_size(dh) bytes, 256-byte aligned, any contents; one for
+ *           each call that can overlap another.
+ * ------------------------------------------------------------------------------- */
+GCA_API gca_status gca_norm_rotary(const gca_heads* q, const gca_heads* k, const gca_heads* q_out, const gca_heads* k_out,
+                           gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot, int interleaved, float eps,
+                           const float* q_weight, const float* k_weight, const uint64_t* freq, const int32_t* positions,
+                           int64_t position_batch_stride, float gain, gca_stream_t stream);
+GCA_API size_t gca_norm_rotary_backward_scratch_size(int dh);
+GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads* k, const gca_heads* dq_out,
+                                    const gca_heads* dk_out, const gca_heads* dq, const gca_heads* dk, gca_dtype dtype, int B,
+                                    int L, int H, int Hkv, int dh, int rot, int interleaved, float eps, const float* q_weight,
+                                    const float* k_weight, const uint64_t* freq, const int32_t* positions,
+                                    int64_t position_batch_stride, float gain, float* dq_weight, float* dk_weight,
+                                    void* scratch, size_t scratch_bytes, gca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * gca_prompt_attention - causal attention over packed sequences, with shared key heads.
+ *
+ * The window sublayer and the lower layers on prompts or documents of any lengths, one behind the
+ * other in one tensor.  Sequence b is rows offsets[b] .. offsets[b+1]-1; query head h reads key head
+ * h / (H / Hkv).  Row t of a sequence sees its rows t - window + 1 .. t (window 0: 0 .. t):
+ *     s = scale <q, k>,   o = sum softmax(s) v,   lse = log sum exp(s)
+ *
+ *   q [N][H][dh], k, v [N][Hkv][dh]: token and head strides of gca_heads (batch_stride is not used),
+ *           16-byte aligned, strides multiples of 16 bytes (a head stride of 0 repeats a head; no
+ *           token stride of 0).
+ *   offsets [B+1] int32 device, 0 <= offsets[0] <= .. <= offsets[B] <= N; a sequence may be empty.  One
+ *           whose offsets are out of order or of range is left out and flagged (GCA_ERR_DEVICE_INDEX).
+ *   N 0 .. 2^30 rows.   B 1 .. 1024.   H a multiple of Hkv.   dh 32, 64 or 128.   window >= 0.   scale > 0.
+ *   o [N][H][dh] contiguous, 16-byte aligned.   lse [N][H] float32.   Rows of no sequence are left as
+ *           they were.
+ *   ws      >= gca_forward_workspace_size() bytes (error word only).
+ * No sequence sees another: rows of others, and behind the last, may hold anything.  An infinity or
+ * NaN of a sequence can reach all its own rows (a weight of 0 times it is NaN).  bf16: as in
+ * gca_tree_attention, products accumulate in float32 and softmax weights are rounded to bf16 for the
+ * product with v.
+ *
+ * gca_prompt_attention_backward - its gradients:
+ *     D = <dout, o>,  dS = P (<dout, v> - D) scale,  dq = sum dS k,  dk = sum dS q,  dv = sum P dout
+ * with P from lse; dk, dv sum over the query heads that share a key head.  Deterministic (no atomics).
+ * bf16: P and dS are rounded to bf16 for their products.
+ *   o, lse  from the forward call.   dout [N][H][dh]: like q.
+ *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap.
+ *   scratch >= gca_prompt_attention_backward_scratch_size() bytes, 256-byte aligned, any contents; one
+ *           for each call that can overlap another.
+ * ------------------------------------------------------------------------------- */
+GCA_API gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* k, const gca_heads* v, gca_dtype dtype, int N,
+                                int B, int H, int Hkv, int dh, const int32_t* offsets, int window, float scale, void* o,
+                                float* lse, void* ws, size_t ws_bytes, gca_stream_t stream);
+GCA_API size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H);
+GCA_API gca_status gca_prompt_attention_backward(const gca_heads* q, const gca_heads* k, const gca_heads* v, const void* o,
+                                         const gca_heads* dout, const float* lse, gca_dtype dtype, int N, int B, int H,
+                                         int Hkv, int dh, const int32_t* offsets, int window, float scale,
+                                         const gca_heads* dq, const gca_heads* dk, const gca_heads* dv, void* ws,
+                                         size_t ws_bytes, void* scratch, size_t scratch_bytes, gca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * A paged K/V cache.
  *
  * Pages are the method's chunks: 64 tokens of every key head, in the layout of the K/V
@@ -514,6 +583,40 @@ GCA_API gca_status gca_cache_compact(const gca_cache* cache, int32_t* live, void
  * -1 stays -1; outside [-1, width) or in a bad slot is flagged and gives -1. */
 GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, const int32_t* slot_ids, const int32_t* idx,
                             int32_t* pages_out, void* ws, size_t ws_bytes, gca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * A quantised cache: pages of dtype GCA_E4M3, half the bytes of bf16.
+ *
+ * A token's row in a page is heads * dh numbers in e4m3, then one byte a head, filled up with zeros to a
+ * multiple of 16 bytes: gca_cache_row_bytes().  A number is its e4m3 value times 2^(byte - 127).  The byte
+ * is the least exponent, -120 or more, by which the head's largest finite magnitude is 448 at most, so
+ * a number is off by 2^-4 of itself or 2^-10 times the scale at most, whichever is more.  Infinities and
+ * NaN become NaN.  gca_cache_fork, _trim, _compact and _lookup work on such pages as on others;
+ * gca_cache_append, gca_tree_attention and gca_forward do not read them.  dh 32, 64 or 128, heads * dh a
+ * multiple of 16.
+ *
+ * gca_cache_append_quantised - gca_cache_append of rows in `dtype` (GCA_BF16 or GCA_F32), quantised as they
+ * are written.  With offsets [n+1] int32 instead of counts, k_new and v_new are packed tensors of T rows
+ * (batch_stride is not used, path NULL) and entry i takes rows offsets[i] .. offsets[i+1]-1; offsets that
+ * are not in order within 0 .. T are flagged and nothing is appended.
+ *
+ * gca_cache_read - chunks of a quantised cache, widened to `dtype` (exactly).  Chunk idx[i][e] of entry i's
+ * slot goes to rows 64e .. 64e+63 of its outputs and idx_local[i][e] = e, so that gca_forward(q, k_out,
+ * v_out, kv_batch_stride = per * 64 * heads * dh, nC = per, idx_local, ...) attends to them.  Rows at or
+ * behind the slot's length are zeros.  A chunk of -1, or one whose page is not held, is zeros with
+ * idx_local -1; one outside [-1, width), or in a bad slot, is that and flagged (GCA_ERR_DEVICE_INDEX).
+ *   k_out, v_out [n][per * 64][heads][dh], 16-byte aligned.   idx, idx_local [n][per] int32 (idx_local may
+ *           be NULL).   per >= 1.
+ * ------------------------------------------------------------------------------- */
+GCA_API size_t gca_cache_row_bytes(gca_dtype dtype, int heads, int dh);
+GCA_API size_t gca_cache_append_quantised_scratch_size(int n, int T, int packed);
+GCA_API gca_status gca_cache_append_quantised(const gca_cache* cache, const gca_heads* k_new, const gca_heads* v_new,
+                                      gca_dtype dtype, int n, int T, const int32_t* slot_ids, const int32_t* counts,
+                                      const int32_t* path, const int32_t* offsets, void* ws, size_t ws_bytes, void* scratch,
+                                      size_t scratch_bytes, gca_stream_t stream);
+GCA_API gca_status gca_cache_read(const gca_cache* cache, int n, int per, const int32_t* slot_ids, const int32_t* idx,
+                          gca_dtype dtype, void* k_out, void* v_out, int32_t* idx_local, void* ws, size_t ws_bytes,
+                          gca_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
  * gca_tree_attention - attention of newly drafted tokens over a paged cache.

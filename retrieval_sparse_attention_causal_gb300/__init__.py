@@ -22,12 +22,13 @@ CHUNK = 64
 MAX_TOPK = 16
 MAX_DRAFT = 256           # tokens of a draft (tree_attention)
 MAX_CACHE_ENTRIES = 1024  # sequences of one page operation
+MAX_SEQUENCES = 1024      # packed sequences of a call (prompt_attention)
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libgca.so")
 
 (GCA_OK, GCA_ERR_INVALID_ARG, GCA_ERR_UNSUPPORTED, GCA_ERR_WORKSPACE, GCA_ERR_CUDA, GCA_ERR_DEVICE_INDEX,
  GCA_ERR_TIMEOUT, GCA_ERR_CACHE_FULL) = range(8)
-GCA_F32, GCA_BF16 = 0, 1
+GCA_F32, GCA_BF16, GCA_E4M3 = 0, 1, 2
 
 
 class GCAError(RuntimeError):
@@ -98,6 +99,16 @@ def _load():
         "gca_rotary_frequencies": (I, [I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                        ctypes.c_double, ctypes.POINTER(U64)]),
         "gca_rotary": (I, [HP, HP, HP, HP, I, I, I, I, I, I, I, I, I, P, P, I64, F, P]),
+        "gca_norm_rotary": (I, [HP, HP, HP, HP, I, I, I, I, I, I, I, I, F, P, P, P, P, I64, F, P]),
+        "gca_norm_rotary_backward_scratch_size": (SZ, [I]),
+        "gca_norm_rotary_backward": (I, [HP, HP, HP, HP, HP, HP, I, I, I, I, I, I, I, I, F, P, P, P, P, I64, F, P, P, P, SZ, P]),
+        "gca_prompt_attention": (I, [HP, HP, HP, I, I, I, I, I, I, P, I, F, P, P, P, SZ, P]),
+        "gca_prompt_attention_backward_scratch_size": (SZ, [I, I, I]),
+        "gca_prompt_attention_backward": (I, [HP, HP, HP, P, HP, P, I, I, I, I, I, I, P, I, F, HP, HP, HP, P, SZ, P, SZ, P]),
+        "gca_cache_row_bytes": (SZ, [I, I, I]),
+        "gca_cache_append_quantised_scratch_size": (SZ, [I, I, I]),
+        "gca_cache_append_quantised": (I, [CP, HP, HP, I, I, I, P, P, P, P, P, SZ, P, SZ, P]),
+        "gca_cache_read": (I, [CP, I, I, P, P, I, P, P, P, P, SZ, P]),
         "gca_cache_append_scratch_size": (SZ, [I, I]),
         "gca_cache_append": (I, [CP, HP, HP, I, I, P, P, P, P, SZ, P, SZ, P]),
         "gca_cache_fork": (I, [CP, I, P, P, P, SZ, P]),
@@ -169,6 +180,9 @@ EXPORTS = (
     "gca_cache_append_scratch_size", "gca_cache_append", "gca_cache_fork", "gca_cache_trim",
     "gca_cache_compact_scratch_size", "gca_cache_compact", "gca_cache_lookup",
     "gca_tree_plan", "gca_tree_attention_scratch_size", "gca_tree_attention",
+    "gca_norm_rotary", "gca_norm_rotary_backward_scratch_size", "gca_norm_rotary_backward",
+    "gca_prompt_attention", "gca_prompt_attention_backward_scratch_size", "gca_prompt_attention_backward",
+    "gca_cache_row_bytes", "gca_cache_append_quantised_scratch_size", "gca_cache_append_quantised", "gca_cache_read",
 )
 
 
@@ -560,6 +574,8 @@ def scores_backward(q_lmk, k_lmk, idx, dscores, ws: Workspace = None, dq_out=Non
 
 
 # --------------------------------------------------------------------------- rotary, paged cache, drafted tokens
+from .prompt import (QuantisedCache, norm_rotary, norm_rotary_backward, prompt_attention,  # noqa: E402,F401
+                     prompt_attention_backward)
 from .decoding import (PagedCache, cache_workspace, rotary, rotary_backward, rotary_frequencies,  # noqa: E402,F401
                        tree_attention, tree_plan)
 

@@ -621,10 +621,10 @@ static bool strides_overlap(const gca_heads& t, int64_t B, int64_t L, int64_t H,
   return false;
 }
 
-extern "C" gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_heads* q_out,
-                                 const gca_heads* k_out, gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot,
-                                 int interleaved, int backward, const uint64_t* freq, const int32_t* positions,
-                                 int64_t position_batch_stride, float gain, gca_stream_t stream) {
+// What gca_rotary and gca_norm_rotary ask of their tensors and sizes.
+static gca_status check_turned(const gca_heads* q, const gca_heads* k, const gca_heads* q_out, const gca_heads* k_out,
+                               gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot, const uint64_t* freq,
+                               int64_t position_batch_stride) {
   if (dtype != GCA_F32 && dtype != GCA_BF16) return fail(GCA_ERR_INVALID_ARG, "dtype must be GCA_F32 or GCA_BF16");
   if (!q || !q_out || !q->data || !q_out->data) return fail(GCA_ERR_INVALID_ARG, "q or q_out is NULL");
   if (!k != !k_out || (k && (!k->data || !k_out->data))) return fail(GCA_ERR_INVALID_ARG, "k and k_out must both be given");
@@ -644,6 +644,15 @@ extern "C" gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const g
   }
   if (strides_overlap(*q_out, B, L, H, dh) || (k && strides_overlap(*k_out, B, L, Hkv, dh)))
     return fail(GCA_ERR_INVALID_ARG, "output strides make elements overlap");
+  return GCA_OK;
+}
+
+extern "C" gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_heads* q_out,
+                                 const gca_heads* k_out, gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot,
+                                 int interleaved, int backward, const uint64_t* freq, const int32_t* positions,
+                                 int64_t position_batch_stride, float gain, gca_stream_t stream) {
+  gca_status st = check_turned(q, k, q_out, k_out, dtype, B, L, H, Hkv, dh, rot, freq, position_batch_stride);
+  if (st != GCA_OK) return st;
   auto same = [](const gca_heads* a, const gca_heads* b) {
     return a->data == b->data && a->batch_stride == b->batch_stride && a->token_stride == b->token_stride &&
            a->head_stride == b->head_stride;
@@ -665,19 +674,207 @@ extern "C" gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const g
   return GCA_OK;
 }
 
+// ==================================================================== norms with rotary positions
+namespace {
+gca_status check_weights(const gca_heads* k, float eps, const float* q_weight, const float* k_weight) {
+  if (!q_weight || (k && !k_weight)) return fail(GCA_ERR_INVALID_ARG, "a weight is NULL");
+  for (const float* w : {q_weight, k_weight})
+    if (reinterpret_cast<uintptr_t>(w) & 3) return fail(GCA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GCA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return GCA_OK;
+}
+NormSide norm_side(const gca_heads* in, const gca_heads* dy, const gca_heads* out) {
+  NormSide x{};
+  x.in = in->data; x.in_bs = in->batch_stride; x.in_ts = in->token_stride; x.in_hs = in->head_stride;
+  if (dy) { x.dy = dy->data; x.dy_bs = dy->batch_stride; x.dy_ts = dy->token_stride; x.dy_hs = dy->head_stride; }
+  x.out = out->data; x.out_bs = out->batch_stride; x.out_ts = out->token_stride; x.out_hs = out->head_stride;
+  return x;
+}
+}  // namespace
+
+extern "C" gca_status gca_norm_rotary(const gca_heads* q, const gca_heads* k, const gca_heads* q_out, const gca_heads* k_out,
+                                      gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot, int interleaved,
+                                      float eps, const float* q_weight, const float* k_weight, const uint64_t* freq,
+                                      const int32_t* positions, int64_t position_batch_stride, float gain,
+                                      gca_stream_t stream) {
+  gca_status st = check_turned(q, k, q_out, k_out, dtype, B, L, H, Hkv, dh, rot, freq, position_batch_stride);
+  if (st != GCA_OK) return st;
+  if ((st = check_weights(k, eps, q_weight, k_weight)) != GCA_OK) return st;
+  NormRotaryArgs a{};
+  a.q = norm_side(q, nullptr, q_out);
+  if (k) a.k = norm_side(k, nullptr, k_out);
+  a.bf16 = dtype == GCA_BF16; a.B = B; a.L = L; a.H = H; a.Hkv = Hkv; a.dh = dh; a.rot = rot; a.paired = interleaved ? 1 : 0;
+  a.qw = q_weight; a.kw = k_weight; a.freq = freq; a.pos = positions; a.pos_bs = position_batch_stride;
+  a.gain = gain; a.sgain = gain; a.eps = eps;
+  cudaError_t e = launch_norm_rotary(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_norm_rotary launch");
+  return GCA_OK;
+}
+
+extern "C" size_t gca_norm_rotary_backward_scratch_size(int dh) {
+  return dh < 2 || dh > 256 ? 256 : align256(norm_rotary_scratch_bytes(dh));
+}
+
+static gca_status check_scratch(const void* p, size_t have, size_t need) {
+  if (p == nullptr) return fail(GCA_ERR_WORKSPACE, "scratch pointer is NULL");
+  if (reinterpret_cast<uintptr_t>(p) & 255) return fail(GCA_ERR_WORKSPACE, "scratch is not 256-byte aligned");
+  if (have < need) return fail(GCA_ERR_WORKSPACE, "scratch has %zu bytes, needs %zu", have, need);
+  return GCA_OK;
+}
+
+extern "C" gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads* k, const gca_heads* dq_out,
+                                               const gca_heads* dk_out, const gca_heads* dq, const gca_heads* dk,
+                                               gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot,
+                                               int interleaved, float eps, const float* q_weight, const float* k_weight,
+                                               const uint64_t* freq, const int32_t* positions, int64_t position_batch_stride,
+                                               float gain, float* dq_weight, float* dk_weight, void* scratch,
+                                               size_t scratch_bytes, gca_stream_t stream) {
+  gca_status st = check_turned(q, k, dq, dk, dtype, B, L, H, Hkv, dh, rot, freq, position_batch_stride);
+  if (st != GCA_OK) return st;
+  if ((st = check_turned(dq_out, dk_out, dq, dk, dtype, B, L, H, Hkv, dh, rot, freq, position_batch_stride)) != GCA_OK) return st;
+  if ((st = check_weights(k, eps, q_weight, k_weight)) != GCA_OK) return st;
+  if (!dq_weight || (k && !dk_weight)) return fail(GCA_ERR_INVALID_ARG, "a weight's gradient is NULL");
+  for (const float* w : {dq_weight, dk_weight})
+    if (reinterpret_cast<uintptr_t>(w) & 3) return fail(GCA_ERR_INVALID_ARG, "weights' gradients must be 4-byte aligned");
+  if ((st = check_scratch(scratch, scratch_bytes, gca_norm_rotary_backward_scratch_size(dh))) != GCA_OK) return st;
+  NormRotaryArgs a{};
+  a.q = norm_side(q, dq_out, dq);
+  if (k) a.k = norm_side(k, dk_out, dk);
+  a.bf16 = dtype == GCA_BF16; a.backward = 1; a.B = B; a.L = L; a.H = H; a.Hkv = Hkv; a.dh = dh; a.rot = rot;
+  a.paired = interleaved ? 1 : 0;
+  a.qw = q_weight; a.kw = k_weight; a.freq = freq; a.pos = positions; a.pos_bs = position_batch_stride;
+  a.gain = gain; a.sgain = -gain; a.eps = eps;
+  a.partial = static_cast<float*>(scratch); a.dqw = dq_weight; a.dkw = dk_weight;
+  cudaError_t e = launch_norm_rotary(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_norm_rotary_backward launch");
+  return GCA_OK;
+}
+
+// ==================================================================== attention over prompts
+namespace {
+// A packed tensor whose rows are read (or written) in 16-byte units.
+gca_status check_packed(const gca_heads* t, int esize, int N, int heads, const char* what) {
+  if (!t || !t->data) return fail(GCA_ERR_INVALID_ARG, "%s is NULL", what);
+  if (!aligned16(t->data)) return fail(GCA_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+  if (N > 1 && t->token_stride <= 0) return fail(GCA_ERR_INVALID_ARG, "%s: the token stride must be > 0", what);
+  // (in a tensor map a stride has 40 bits of bytes)
+  for (int64_t s : {N > 1 ? t->token_stride : 0, heads > 1 ? t->head_stride : 0})
+    if (s < 0 || s * esize % 16 || s >= (int64_t)1 << 36)
+      return fail(GCA_ERR_INVALID_ARG, "%s: strides must be >= 0, multiples of 16 bytes and below 2^36", what);
+  return GCA_OK;
+}
+gca_status check_prompt(const gca_heads* q, const gca_heads* k, const gca_heads* v, gca_dtype dtype, int N, int B, int H,
+                        int Hkv, int dh, const int32_t* offsets, int window, float scale, const void* o, const float* lse) {
+  if (dtype != GCA_F32 && dtype != GCA_BF16) return fail(GCA_ERR_INVALID_ARG, "dtype must be GCA_F32 or GCA_BF16");
+  if (N < 0 || N > 1 << 30) return fail(GCA_ERR_INVALID_ARG, "N must be in 0..2^30 (got %d)", N);
+  if (B < 1 || B > GCA_MAX_SEQUENCES) return fail(GCA_ERR_INVALID_ARG, "B must be in 1..%d (got %d)", GCA_MAX_SEQUENCES, B);
+  if (Hkv < 1 || H < Hkv || H % Hkv || H > 65535) return fail(GCA_ERR_INVALID_ARG, "H must be a multiple of Hkv, at most 65535 (got %d, %d)", H, Hkv);
+  if (dh != 32 && dh != 64 && dh != 128) return fail(GCA_ERR_UNSUPPORTED, "head dim must be 32, 64 or 128 (got %d)", dh);
+  if (((int64_t)N / 64 + B) * H > INT32_MAX) return fail(GCA_ERR_UNSUPPORTED, "N, B and H are too large together");
+  if (window < 0) return fail(GCA_ERR_INVALID_ARG, "window must be >= 0");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(GCA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!offsets || (reinterpret_cast<uintptr_t>(offsets) & 3)) return fail(GCA_ERR_INVALID_ARG, "offsets must be 4-byte aligned and not NULL");
+  if (N == 0) return GCA_OK;  // no row: no address is used
+  gca_status st;
+  const int esize = dtype == GCA_BF16 ? 2 : 4;
+  if ((st = check_packed(q, esize, N, H, "q")) != GCA_OK) return st;
+  if ((st = check_packed(k, esize, N, Hkv, "k")) != GCA_OK) return st;
+  if ((st = check_packed(v, esize, N, Hkv, "v")) != GCA_OK) return st;
+  if (!o || !lse || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3))
+    return fail(GCA_ERR_INVALID_ARG, "o and lse must not be NULL, o 16-byte aligned");
+  return GCA_OK;
+}
+PromptArgs prompt_args(const gca_heads* q, const gca_heads* k, const gca_heads* v, gca_dtype dtype, int N, int B, int H, int Hkv,
+                       int dh, const int32_t* offsets, int window, float scale, const void* o, const float* lse, void* ws) {
+  PromptArgs a{};
+  auto ts = [&](const gca_heads* t) { return N > 1 ? t->token_stride : 0; };
+  a.q = q->data; a.q_ts = ts(q); a.q_hs = H > 1 ? q->head_stride : 0;
+  a.k = k->data; a.k_ts = ts(k); a.k_hs = Hkv > 1 ? k->head_stride : 0;
+  a.v = v->data; a.v_ts = ts(v); a.v_hs = Hkv > 1 ? v->head_stride : 0;
+  a.offsets = offsets; a.N = N; a.bf16 = dtype == GCA_BF16; a.B = B; a.H = H; a.Hkv = Hkv; a.g = H / Hkv; a.dh = dh;
+  a.window = window; a.scale = scale;
+  a.o = const_cast<void*>(o); a.lse = const_cast<float*>(lse);
+  a.err = reinterpret_cast<ErrWord*>(ws);
+  return a;
+}
+}  // namespace
+
+extern "C" gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* k, const gca_heads* v, gca_dtype dtype, int N,
+                                           int B, int H, int Hkv, int dh, const int32_t* offsets, int window, float scale,
+                                           void* o, float* lse, void* ws, size_t ws_bytes, gca_stream_t stream) {
+  gca_status st = check_prompt(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse);
+  if (st != GCA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  if (N == 0) return GCA_OK;
+  const PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
+  cudaError_t e = launch_prompt_forward(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_prompt_attention launch");
+  return GCA_OK;
+}
+
+extern "C" size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H) {
+  if (N < 1 || B < 1 || H < 1) return 256;
+  return 2 * align256((size_t)prompt_scratch_rows(N, B) * H * sizeof(float));
+}
+
+extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gca_heads* k, const gca_heads* v, const void* o,
+                                                    const gca_heads* dout, const float* lse, gca_dtype dtype, int N, int B,
+                                                    int H, int Hkv, int dh, const int32_t* offsets, int window, float scale,
+                                                    const gca_heads* dq, const gca_heads* dk, const gca_heads* dv, void* ws,
+                                                    size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                                    gca_stream_t stream) {
+  gca_status st = check_prompt(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse);
+  if (st != GCA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  if (N == 0) return GCA_OK;
+  const int esize = dtype == GCA_BF16 ? 2 : 4;
+  const struct { const gca_heads* t; int heads; const char* what; } all[] = {{dout, H, "dout"}, {dq, H, "dq"}, {dk, Hkv, "dk"}, {dv, Hkv, "dv"}};
+  for (auto& x : all)
+    if ((st = check_packed(x.t, esize, N, x.heads, x.what)) != GCA_OK) return st;
+  if (strides_overlap(*dq, 1, N, H, dh) || strides_overlap(*dk, 1, N, Hkv, dh) || strides_overlap(*dv, 1, N, Hkv, dh))
+    return fail(GCA_ERR_INVALID_ARG, "output strides make elements overlap");
+  if ((st = check_scratch(scratch, scratch_bytes, gca_prompt_attention_backward_scratch_size(N, B, H))) != GCA_OK) return st;
+  PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
+  a.dout = dout->data; a.do_ts = N > 1 ? dout->token_stride : 0; a.do_hs = H > 1 ? dout->head_stride : 0;
+  a.dq = dq->data; a.dq_ts = dq->token_stride; a.dq_hs = dq->head_stride;
+  a.dk = dk->data; a.dk_ts = dk->token_stride; a.dk_hs = dk->head_stride;
+  a.dv = dv->data; a.dv_ts = dv->token_stride; a.dv_hs = dv->head_stride;
+  a.np = prompt_scratch_rows(N, B);
+  a.lse2 = static_cast<float*>(scratch);
+  a.D = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + align256((size_t)a.np * H * sizeof(float)));
+  cudaError_t e = launch_prompt_backward(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_prompt_attention_backward launch");
+  return GCA_OK;
+}
+
 // ==================================================================== paged cache
 namespace {
-gca_status check_cache(const gca_cache* c, bool need_refs) {
+// Bytes of a token's row: a quantised one has a byte a head behind its numbers, up to a multiple of 16.
+int64_t row_bytes(gca_dtype dtype, int heads, int dh) {
+  const int64_t n = (int64_t)heads * dh;
+  return dtype == GCA_E4M3 ? n + ((int64_t)heads + 15) / 16 * 16 : n * (dtype == GCA_BF16 ? 2 : 4);
+}
+// The page operations take pages of any kind (`any`); what reads or writes numbers takes its own.
+gca_status check_cache(const gca_cache* c, bool need_refs, bool any = false) {
   if (!c) return fail(GCA_ERR_INVALID_ARG, "cache is NULL");
-  if (c->dtype != GCA_F32 && c->dtype != GCA_BF16) return fail(GCA_ERR_INVALID_ARG, "dtype must be GCA_F32 or GCA_BF16");
+  if (c->dtype != GCA_F32 && c->dtype != GCA_BF16 && !(any && c->dtype == GCA_E4M3))
+    return fail(GCA_ERR_INVALID_ARG, any ? "dtype must be GCA_F32, GCA_BF16 or GCA_E4M3" : "dtype must be GCA_F32 or GCA_BF16");
   if (!c->k_pages || !c->v_pages || !c->table || !c->lengths || (need_refs && !c->refs))
     return fail(GCA_ERR_INVALID_ARG, "a cache pointer is NULL");
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return fail(GCA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
   if (c->heads < 1 || c->heads > 65535 || c->dh < 1 || c->dh > 65535 || c->pages < 1 || c->slots < 1 || c->width < 1)
     return fail(GCA_ERR_INVALID_ARG, "heads, dh, pages, slots and width must be >= 1 (heads, dh <= 65535)");
   if ((int64_t)c->width * 64 > INT32_MAX) return fail(GCA_ERR_INVALID_ARG, "table too wide: 64 * width must be below 2^31");
-  if ((int64_t)c->heads * c->dh * (c->dtype == GCA_BF16 ? 2 : 4) % 16)
+  if (row_bytes(c->dtype, c->heads, c->dh) % 16)
     return fail(GCA_ERR_INVALID_ARG, "a token's row (heads * dh elements) must be a multiple of 16 bytes");
+  return GCA_OK;
+}
+gca_status check_quantised(const gca_cache* c, gca_dtype dtype) {
+  gca_status st = check_cache(c, false, true);
+  if (st != GCA_OK) return st;
+  if (c->dtype != GCA_E4M3) return fail(GCA_ERR_INVALID_ARG, "the cache must hold GCA_E4M3");
+  if (dtype != GCA_F32 && dtype != GCA_BF16) return fail(GCA_ERR_INVALID_ARG, "dtype must be GCA_F32 or GCA_BF16");
+  if (c->dh != 32 && c->dh != 64 && c->dh != 128) return fail(GCA_ERR_UNSUPPORTED, "head dim must be 32, 64 or 128 (got %d)", c->dh);
   return GCA_OK;
 }
 gca_status check_entries(const gca_cache* c, int n, bool listed) {
@@ -690,17 +887,11 @@ CacheArgs cache_args(const gca_cache* c, int n, const int32_t* slot, void* ws) {
   a.kp = static_cast<unsigned char*>(c->k_pages);
   a.vp = static_cast<unsigned char*>(c->v_pages);
   a.pages = c->pages;
-  a.token_bytes = (int64_t)c->heads * c->dh * (c->dtype == GCA_BF16 ? 2 : 4);
+  a.token_bytes = row_bytes(c->dtype, c->heads, c->dh);
   a.table = c->table; a.slots = c->slots; a.width = c->width; a.lengths = c->lengths; a.refs = c->refs;
   a.n = n; a.slot = slot;
   a.err = reinterpret_cast<ErrWord*>(ws);
   return a;
-}
-gca_status check_scratch(const void* p, size_t have, size_t need) {
-  if (p == nullptr) return fail(GCA_ERR_WORKSPACE, "scratch pointer is NULL");
-  if (reinterpret_cast<uintptr_t>(p) & 255) return fail(GCA_ERR_WORKSPACE, "scratch is not 256-byte aligned");
-  if (have < need) return fail(GCA_ERR_WORKSPACE, "scratch has %zu bytes, needs %zu", have, need);
-  return GCA_OK;
 }
 // A tensor whose rows are read in 16-byte units.
 gca_status check_vectors(const gca_heads* t, int esize, const char* what) {
@@ -748,10 +939,78 @@ extern "C" gca_status gca_cache_append(const gca_cache* cache, const gca_heads* 
   return GCA_OK;
 }
 
+extern "C" size_t gca_cache_row_bytes(gca_dtype dtype, int heads, int dh) {
+  return heads < 1 || dh < 1 ? 0 : (size_t)row_bytes(dtype, heads, dh);
+}
+
+// Pages that the entries of a quantised append can write to: those of n times T rows, or of T rows in all.
+static int64_t most_pages(int n, int T, bool packed) { return packed ? T / 64 + 2 * (int64_t)n : n * ((int64_t)T / 64 + 2); }
+
+extern "C" size_t gca_cache_append_quantised_scratch_size(int n, int T, int packed) {
+  if (n < 1 || T < 1) return 256;
+  return align256((size_t)n * kAppendRec * 4) + align256((size_t)n * 4) + align256((size_t)most_pages(n, T, packed != 0) * 4);
+}
+
+extern "C" gca_status gca_cache_append_quantised(const gca_cache* cache, const gca_heads* k_new, const gca_heads* v_new,
+                                                 gca_dtype dtype, int n, int T, const int32_t* slot_ids, const int32_t* counts,
+                                                 const int32_t* path, const int32_t* offsets, void* ws, size_t ws_bytes,
+                                                 void* scratch, size_t scratch_bytes, gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_quantised(cache, dtype)) != GCA_OK) return st;
+  if (!cache->refs) return fail(GCA_ERR_INVALID_ARG, "a cache pointer is NULL");
+  if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
+  if (T < 1 || T > INT32_MAX / 2) return fail(GCA_ERR_INVALID_ARG, "T must be in 1..2^30");
+  if (most_pages(n, T, offsets != nullptr) > INT32_MAX / 4) return fail(GCA_ERR_INVALID_ARG, "n and T are too large together");
+  if (!counts == !offsets) return fail(GCA_ERR_INVALID_ARG, "counts or offsets must be given, not both");
+  if (offsets && path) return fail(GCA_ERR_INVALID_ARG, "a packed append has no path");
+  const int esize = dtype == GCA_BF16 ? 2 : 4;
+  if ((st = check_vectors(k_new, esize, "k_new")) != GCA_OK) return st;
+  if ((st = check_vectors(v_new, esize, "v_new")) != GCA_OK) return st;
+  if (cache->heads > 1 && (k_new->head_stride != cache->dh || v_new->head_stride != cache->dh))
+    return fail(GCA_ERR_INVALID_ARG, "the heads of a new token must be contiguous (head stride dh)");
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  if ((st = check_scratch(scratch, scratch_bytes, gca_cache_append_quantised_scratch_size(n, T, offsets != nullptr))) != GCA_OK) return st;
+  AppendArgs a{};
+  a.c = cache_args(cache, n, slot_ids, ws);
+  a.kn = static_cast<const unsigned char*>(k_new->data);
+  a.kn_bs = offsets ? 0 : k_new->batch_stride * esize; a.kn_ts = k_new->token_stride * esize;
+  a.vn = static_cast<const unsigned char*>(v_new->data);
+  a.vn_bs = offsets ? 0 : v_new->batch_stride * esize; a.vn_ts = v_new->token_stride * esize;
+  a.counts = counts; a.path = path; a.T = T; a.offsets = offsets;
+  a.heads = cache->heads; a.dh = cache->dh; a.src_bf16 = dtype == GCA_BF16;
+  a.most_steps = most_pages(n, T, offsets != nullptr);
+  unsigned char* p = static_cast<unsigned char*>(scratch);
+  a.rec = reinterpret_cast<int32_t*>(p); p += align256((size_t)n * kAppendRec * 4);
+  a.steps = reinterpret_cast<int32_t*>(p); p += align256((size_t)n * 4);
+  a.fresh = reinterpret_cast<int32_t*>(p);
+  cudaError_t e = launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_append_quantised launch");
+  return GCA_OK;
+}
+
+extern "C" gca_status gca_cache_read(const gca_cache* cache, int n, int per, const int32_t* slot_ids, const int32_t* idx,
+                                     gca_dtype dtype, void* k_out, void* v_out, int32_t* idx_local, void* ws, size_t ws_bytes,
+                                     gca_stream_t stream) {
+  gca_status st;
+  if ((st = check_quantised(cache, dtype)) != GCA_OK) return st;
+  if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
+  if (per < 1 || per > INT32_MAX / 256) return fail(GCA_ERR_INVALID_ARG, "per must be in 1..2^23 (got %d)", per);
+  if (!idx || !k_out || !v_out) return fail(GCA_ERR_INVALID_ARG, "a pointer is NULL");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(GCA_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
+  ReadArgs a{};
+  a.c = cache_args(cache, n, slot_ids, ws);
+  a.idx = idx; a.per = per; a.heads = cache->heads; a.dh = cache->dh; a.bf16 = dtype == GCA_BF16;
+  a.k = k_out; a.v = v_out; a.local = idx_local;
+  cudaError_t e = launch_cache_read(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gca_cache_read launch");
+  return GCA_OK;
+}
+
 extern "C" gca_status gca_cache_fork(const gca_cache* cache, int n, const int32_t* src, const int32_t* dst, void* ws,
                                      size_t ws_bytes, gca_stream_t stream) {
   gca_status st;
-  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if ((st = check_cache(cache, true, true)) != GCA_OK) return st;
   if (!src || !dst) return fail(GCA_ERR_INVALID_ARG, "src or dst is NULL");
   if ((st = check_entries(cache, n, true)) != GCA_OK) return st;
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
@@ -763,7 +1022,7 @@ extern "C" gca_status gca_cache_fork(const gca_cache* cache, int n, const int32_
 extern "C" gca_status gca_cache_trim(const gca_cache* cache, int n, const int32_t* slot_ids, const int32_t* begin,
                                      const int32_t* end, int release, void* ws, size_t ws_bytes, gca_stream_t stream) {
   gca_status st;
-  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if ((st = check_cache(cache, true, true)) != GCA_OK) return st;
   if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
   cudaError_t e = launch_cache_trim(cache_args(cache, n, slot_ids, ws), begin, end, release ? 1 : 0,
@@ -780,7 +1039,7 @@ extern "C" size_t gca_cache_compact_scratch_size(int pages) {
 extern "C" gca_status gca_cache_compact(const gca_cache* cache, int32_t* live, void* ws, size_t ws_bytes,
                                         void* scratch, size_t scratch_bytes, gca_stream_t stream) {
   gca_status st;
-  if ((st = check_cache(cache, true)) != GCA_OK) return st;
+  if ((st = check_cache(cache, true, true)) != GCA_OK) return st;
   if (!live) return fail(GCA_ERR_INVALID_ARG, "live is NULL");
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
   if ((st = check_scratch(scratch, scratch_bytes, gca_cache_compact_scratch_size(cache->pages))) != GCA_OK) return st;
@@ -802,7 +1061,7 @@ extern "C" gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, c
                                        const int32_t* idx, int32_t* pages_out, void* ws, size_t ws_bytes,
                                        gca_stream_t stream) {
   gca_status st;
-  if ((st = check_cache(cache, false)) != GCA_OK) return st;
+  if ((st = check_cache(cache, false, true)) != GCA_OK) return st;
   if ((st = check_entries(cache, n, slot_ids != nullptr)) != GCA_OK) return st;
   if (per < 1) return fail(GCA_ERR_INVALID_ARG, "per must be >= 1");
   if (!idx || !pages_out) return fail(GCA_ERR_INVALID_ARG, "idx or pages_out is NULL");

@@ -71,11 +71,18 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a)
   const int i = threadIdx.x;
   all[i] = i < c.n ? given_slot(c, i) : -1;
   __syncthreads();
-  int slot = -1, old = 0, take = 0, hold = -1;
+  int slot = -1, old = 0, take = 0, hold = -1, span = 0;
+  if (a.offsets) {  // rows offsets[i] .. offsets[i + 1] - 1 of a packed tensor of T rows
+    const int from = i < c.n ? a.offsets[i] : 0, to = i < c.n ? a.offsets[i + 1] : 0;
+    const bool bad = from < 0 || to < from || to > a.T;
+    if (bad) flag_bad_index(c.err, from < 0 || from > a.T ? from : to);
+    // Out of order, they could ask for more rows than there are, and for more pages than the scratch holds.
+    span = __syncthreads_or(bad) ? 0 : to - from;
+  }
   if (i < c.n) {
     slot = checked_slot(c, all, i);
     if (slot >= 0) {
-      take = a.counts[i];
+      take = a.offsets ? span : a.counts[i];
       old = c.lengths[slot];
       if (take < 0 || take > a.T) {
         flag_bad_index(c.err, take);
@@ -151,6 +158,11 @@ __global__ void __launch_bounds__(kPlanThreads) append_plan_kernel(AppendArgs a)
   if (i < c.n) {
     int4* rec = reinterpret_cast<int4*>(a.rec) + i;
     *rec = make_int4(old, served ? take : 0, served && copy ? hold : -1, slot);
+  }
+  if (a.steps) {  // pages that the entries up to this one write to
+    int all_steps;
+    const int sum = block_scan(served ? (old + take - 1) / kChunk - old / kChunk + 1 : 0, red, all_steps);
+    if (i < c.n) a.steps[i] = sum;
   }
 }
 
@@ -435,6 +447,7 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s) {
   append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
   cudaError_t e = launch_end("cache_append_plan", s);
   if (e != cudaSuccess) return e;
+  if (a.steps) return launch_quantise_rows(a, s);
   const int steps = (a.T + kChunk - 1) / kChunk + 1;
   launch_begin("cache_append_rows", s);
   e = launch_after(append_rows_kernel, dim3(steps * kRowParts, a.c.n), dim3(256), s, a);

@@ -206,6 +206,48 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(RotaryArgs a, cudaStream_t s);
 
+// ---- norms of queries and keys with rotary positions (norm_rotary.cu)
+struct NormSide {
+  const void* in; int64_t in_bs, in_ts, in_hs;  // element strides: batch, token, head
+  const void* dy; int64_t dy_bs, dy_ts, dy_hs;  // backward: the gradient of the output
+  void* out; int64_t out_bs, out_ts, out_hs;    // the output, or the gradient of the input
+};
+struct NormRotaryArgs {
+  NormSide q, k;
+  int bf16, backward, B, L, H, Hkv, dh, rot, paired;
+  const float* qw; const float* kw;             // [dh]
+  const uint64_t* freq;                         // [rot / 2]
+  const int32_t* pos; int64_t pos_bs;           // null: token l is at position l
+  float gain, sgain, eps;
+  float* partial; float* dqw; float* dkw;       // backward: scratch [2][CTAs][dh], and [dh]
+  int tokens, group;                            // of a piece, lanes of a row (set by the launcher)
+};
+constexpr int kNormCtas = kSMs * 6;             // of the backward pass, at most
+size_t norm_rotary_scratch_bytes(int dh);
+cudaError_t launch_norm_rotary(NormRotaryArgs a, cudaStream_t s);
+
+// ---- causal attention over packed sequences (prompt_attn.cu; bf16: prompt_tc.cu, prompt_bwd_tc.cu)
+struct PromptArgs {
+  const void* q; int64_t q_ts, q_hs;                       // [N][H][dh], element strides
+  const void* k; int64_t k_ts, k_hs;                       // [N][Hkv][dh]
+  const void* v; int64_t v_ts, v_hs;
+  const int32_t* offsets;                                  // [B + 1]
+  int64_t N;
+  int bf16, B, H, Hkv, g, dh, window;
+  float scale;
+  void* o; float* lse;                                     // [N][H][dh], [N][H]
+  const void* dout; int64_t do_ts, do_hs;                  // backward
+  void* dq; int64_t dq_ts, dq_hs;
+  void* dk; int64_t dk_ts, dk_hs;
+  void* dv; int64_t dv_ts, dv_hs;
+  float* lse2; float* D; int64_t np;                       // scratch [H][np]
+  ErrWord* err;
+};
+constexpr int kPromptSequences = 1024;
+int64_t prompt_scratch_rows(int64_t N, int B);
+cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s);
+cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s);
+
 // ---- attention of drafted tokens over a paged cache (tree_attn.cu)
 struct TreeArgs {
   const void* q; int64_t q_bs, q_ts, q_hs;                 // [B][T][H][dh], element strides
@@ -255,12 +297,26 @@ struct AppendArgs {
   const int32_t* counts; const int32_t* path; int T;
   int32_t* rec;                                            // scratch: kAppendRec values an entry
   int32_t* fresh;                                          // scratch: free pages in order
+  // Rows that are quantised (quantised.cu): the head split of a row, the new rows' type, scratch for the pages that
+  // the entries up to each write to (null: rows are copied as they are), and how many that can be at most.
+  int heads, dh, src_bf16;
+  int32_t* steps; int64_t most_steps;
+  const int32_t* offsets;                                  // [n + 1]: entry i takes these rows of a packed tensor of T rows (null: counts)
 };
 constexpr int kAppendRec = 4;      // old length, tokens, source page of a copied last page (or -1), slot
 constexpr int kCacheEntries = 1024;
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_cache_fork(const CacheArgs& a, const int32_t* dst, cudaStream_t s);
 cudaError_t launch_cache_trim(const CacheArgs& a, const int32_t* begin, const int32_t* end, int release, cudaStream_t s);
+cudaError_t launch_quantise_rows(const AppendArgs& a, cudaStream_t s);
+// Chunks of a quantised cache, widened (quantised.cu).
+struct ReadArgs {
+  CacheArgs c;
+  const int32_t* idx; int per;                             // [n][per] chunk numbers
+  int heads, dh, bf16;                                     // of the outputs
+  void* k; void* v; int32_t* local;                        // [n][per * 64][heads][dh], [n][per] (may be null)
+};
+cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t s);
 struct CompactArgs {
   CacheArgs c;
   int32_t* live;                                           // out: pages in use

@@ -1,0 +1,69 @@
+// Packed sequences and their tiles: what the kernels of the attention over prompts share.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gca {
+
+// A tile of a packed sequence: rows first .. first + T - 1 of the sequence that starts at row `off` and
+// has `len` rows.
+struct PromptTile {
+  int b, tile, off, len;
+};
+
+// Rows of sequence b; one whose offsets are out of order or out of the tensor counts as empty (flagged).
+__device__ __forceinline__ int prompt_length(const PromptArgs& a, int b) {
+  const int s = a.offsets[b], e = a.offsets[b + 1];
+  if (s < 0 || e < s || e > a.N) {
+    if (blockIdx.x == 0) flag_bad_index(a.err, s < 0 || s > a.N ? s : e);
+    return 0;
+  }
+  return e - s;
+}
+
+// Tile number `rank` of the call: tiles of T rows in the order of their work, the most first, so that
+// those that start last are short.  Under the causal mask that is the order of their number in their
+// sequence, from the highest down (`back`: counted from the sequence's end, for the side of the keys),
+// sequences of equal tiles in order.  With S(i) the tiles numbered i or higher, tile `rank` has the number
+// i with S(i + 1) <= rank < S(i).  Called by a whole warp; false behind the last tile.
+template <int T>
+__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int rank, bool back, PromptTile& x) {
+  const int lane = threadIdx.x & 31;
+  auto tiles_of = [&](int b) { return b < a.B ? (prompt_length(a, b) + T - 1) / T : 0; };
+  const int mine = tiles_of(lane);  // the first 32 sequences stay in registers
+  int most = mine;
+  for (int b = lane + 32; b < a.B; b += 32) most = max(most, tiles_of(b));
+  auto from = [&](int i) {
+    int n = max(mine - i, 0);
+    for (int b = lane + 32; b < a.B; b += 32) n += max(tiles_of(b) - i, 0);
+    return (int)__reduce_add_sync(0xffffffffu, n);
+  };
+  int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, most);  // from(lo) > rank >= from(hi)
+  if (from(0) <= rank) return false;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (from(mid) > rank) lo = mid;
+    else hi = mid;
+  }
+  int left = rank - from(lo + 1);  // of the sequences with more than `lo` tiles, in order
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int n = b0 ? tiles_of(b0 + lane) : mine;
+    const uint32_t those = __ballot_sync(0xffffffffu, n > lo);
+    if (left < __popc(those)) {
+      const int at = __fns(those, 0, left + 1);
+      x.b = b0 + at;
+      x.tile = back ? __shfl_sync(0xffffffffu, n, at) - 1 - lo : lo;
+      x.off = a.offsets[x.b];
+      x.len = a.offsets[x.b + 1] - x.off;
+      return true;
+    }
+    left -= __popc(those);
+  }
+  return false;
+}
+
+// Where the rows of sequence b begin in the backward pass's scratch rows: on 16-byte boundaries.
+__device__ __forceinline__ int64_t prompt_pad(int off, int b) { return (int64_t)(off & ~3) + 4 * b; }
+
+}  // namespace gca

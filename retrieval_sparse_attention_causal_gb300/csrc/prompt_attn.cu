@@ -1,0 +1,400 @@
+// Causal attention over packed sequences with shared key heads, and its gradients: the launches, and
+// the kernels for float32 on CUDA cores.
+//
+// Row t of a sequence sees its rows max(0, t - window + 1) .. t (window 0: 0 .. t):
+//     s = scale <q, k>,   o = sum softmax(s) v,   lse = log sum exp(s)
+//     D = <do, o>,  dS = P (<do, v> - D) scale,   dq = sum dS k,  dk = sum dS q,  dv = sum P do
+// where dk and dv sum over the query heads of a key head.  Each gradient is summed by one CTA in a
+// fixed order: the queries' side walks a tile's keys, the keys' side its queries and the heads that
+// share it.  That costs a second product Q K^T and dO V^T, and needs no atomics.
+//
+// Float32 (prompt_tc.cu and prompt_bwd_tc.cu have bf16): tiles of 64 rows by 64 keys, operands in
+// shared memory with rows padded by four floats, 16 x 16 threads with 4 x 4 logits and 4 x dh / 16
+// outputs each.  Both products read two vectors of four floats for 16 multiplications, so the CUDA cores
+// and shared memory are busy at about the same rate.
+#include <algorithm>
+
+#include "prompt.cuh"
+
+namespace gca {
+namespace {
+
+constexpr int kT = 64;        // rows and keys of a tile
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int DH>
+struct Simt {
+  static constexpr int LD = DH + 4, LP = kT + 4;          // floats of a row in shared memory
+  static constexpr int TILE = kT * LD, SCORES = kT * LP;  // floats
+  static constexpr int CV = DH / 16;                      // columns of a thread's outputs
+};
+
+// Rows of a tile into shared memory; what lies behind the sequence counts as zeros.
+template <typename T, int DH>
+__device__ __forceinline__ void load_tile(float* to, const T* from, int64_t stride, int rows) {
+  constexpr int V = Elem<T>::kVec, U = DH / V;
+  for (int u = threadIdx.x; u < kT * U; u += kThreads) {
+    const int r = u / U, c = (u - r * U) * V;
+    float f[V];
+    if (r < rows) {
+      unpack16(*reinterpret_cast<const uint4*>(from + r * stride + c), f, (const T*)nullptr);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(to + r * Simt<DH>::LD + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  }
+}
+
+// s[i][j] = <A row ty + 16 i, B row tx + 16 j>.
+template <int DH>
+__device__ __forceinline__ void products(const float* A, const float* B, float (&s)[4][4]) {
+  constexpr int LD = Simt<DH>::LD;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DH; d += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * LD + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * LD + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] += x[i].x * y[j].x + x[i].y * y[j].y + x[i].z * y[j].z + x[i].w * y[j].w;
+  }
+}
+
+// The columns of a thread's outputs: runs of up to four, 64 apart.
+template <int DH> __device__ __forceinline__ int column(int c) {
+  constexpr int RUN = Simt<DH>::CV < 4 ? Simt<DH>::CV : 4;
+  return (c / RUN) * 64 + (threadIdx.x & 15) * RUN + c % RUN;
+}
+
+// o[i][c] += sum over k of P[row ty + 16 i][k] V[k][column c].
+template <int DH>
+__device__ __forceinline__ void weighted(const float* P, const float* V, float (&o)[4][Simt<DH>::CV]) {
+  constexpr int LD = Simt<DH>::LD, LP = Simt<DH>::LP, CV = Simt<DH>::CV, RUN = CV < 4 ? CV : 4;
+  const int ty = threadIdx.x >> 4;
+#pragma unroll 2
+  for (int k = 0; k < kT; k += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty + 16 * i) * LP + k);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      float v[CV];
+#pragma unroll
+      for (int c = 0; c < CV; c += RUN) {
+        const float* at = V + (k + x) * LD + column<DH>(c);
+        if constexpr (RUN == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(at);
+          v[c] = f.x; v[c + 1] = f.y; v[c + 2] = f.z; v[c + 3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(at);
+          v[c] = f.x; v[c + 1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+#pragma unroll
+        for (int c = 0; c < CV; ++c) o[i][c] += w * v[c];
+      }
+    }
+  }
+}
+
+// Of the 16 threads that share a row.
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The tile of this CTA and its head; false: there is none.
+__device__ __forceinline__ bool my_tile(const PromptArgs& a, int heads, bool back, PromptTile& x, int& h) {
+  h = blockIdx.x % heads;
+  return prompt_tile<kT>(a, blockIdx.x / heads, back, x);
+}
+__device__ __forceinline__ bool sees(const PromptArgs& a, int t, int k) { return k <= t && (a.window == 0 || k > t - a.window); }
+// The first tile of keys that rows t .. see, and behind the last tile of rows that see keys .. k.
+__device__ __forceinline__ int first_keys(const PromptArgs& a, int t) { return a.window ? max(0, t - a.window + 1) / kT : 0; }
+__device__ __forceinline__ int last_rows(const PromptArgs& a, int k, int len) {
+  const int most = a.window ? (int)min((int64_t)len - 1, (int64_t)k + a.window - 1) : len - 1;
+  return most / kT + 1;
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
+  using C = Simt<DH>;
+  extern __shared__ float sm[];
+  float *Q = sm, *K = Q + C::TILE, *V = K + C::TILE, *P = V + C::TILE;
+  PromptTile x;
+  int h;
+  if (!my_tile(a, a.H, false, x, h)) return;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, t0 = x.tile * kT, m = h / a.g;
+  load_tile<T, DH>(Q, reinterpret_cast<const T*>(a.q) + (int64_t)(x.off + t0) * a.q_ts + h * a.q_hs, a.q_ts, x.len - t0);
+  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
+  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
+  float o[4][C::CV] = {}, mx[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    mx[i] = -CUDART_INF_F;
+    l[i] = 0.f;
+  }
+  const float sl2 = a.scale * kLog2e;
+  for (int j = first_keys(a, t0); j <= x.tile; ++j) {
+    __syncthreads();
+    load_tile<T, DH>(K, k + (int64_t)j * kT * a.k_ts, a.k_ts, x.len - j * kT);
+    load_tile<T, DH>(V, v + (int64_t)j * kT * a.v_ts, a.v_ts, x.len - j * kT);
+    __syncthreads();
+    float s[4][4];
+    products<DH>(Q, K, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + ty + 16 * i;
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!sees(a, t, j * kT + tx + 16 * c)) s[i][c] = -CUDART_INF_F;
+        top = fmaxf(top, s[i][c]);
+      }
+      top = fmaxf(mx[i], row_max(top));
+      const float base = top == -CUDART_INF_F ? 0.f : top, f = exp2f((mx[i] - base) * sl2);
+      mx[i] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float p = exp2f((s[i][c] - base) * sl2);
+        sum += p;
+        P[(ty + 16 * i) * C::LP + tx + 16 * c] = p;
+      }
+      l[i] = l[i] * f + row_sum(sum);
+#pragma unroll
+      for (int c = 0; c < C::CV; ++c) o[i][c] *= f;
+    }
+    __syncthreads();
+    weighted<DH>(P, V, o);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + ty + 16 * i;
+    if (t >= x.len) continue;
+    const int64_t row = (int64_t)(x.off + t) * a.H + h;
+    const float inv = 1.f / l[i];
+#pragma unroll
+    for (int c = 0; c < C::CV; ++c) Elem<T>::st(reinterpret_cast<T*>(a.o) + row * DH + column<DH>(c), o[i][c] * inv);
+    if (tx == 0) a.lse[row] = mx[i] * a.scale + logf(l[i]);
+  }
+}
+
+// Row sums D = <do, o> and the log-sum-exps times log2(e), a head's rows side by side: [H][np] each.
+
+template <typename T>
+__global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
+  const int h = blockIdx.y;
+  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  // The sequence of the row: the last that starts at it or before (empty ones behind it start there too).
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.offsets[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  const int off = a.offsets[lo];
+  const bool on = row < a.N && row >= off && row - off < prompt_length(a, lo);
+  float d = 0.f;
+  constexpr int V = Elem<T>::kVec;
+  if (on) {
+    const T* o = reinterpret_cast<const T*>(a.o) + (row * a.H + h) * a.dh;
+    const T* g = reinterpret_cast<const T*>(a.dout) + row * a.do_ts + h * a.do_hs;
+    for (int c = 0; c < a.dh; c += V) {
+      float x[V], y[V];
+      unpack16(*reinterpret_cast<const uint4*>(o + c), x, (const T*)nullptr);
+      unpack16(*reinterpret_cast<const uint4*>(g + c), y, (const T*)nullptr);
+#pragma unroll
+      for (int i = 0; i < V; ++i) d += x[i] * y[i];
+    }
+    const int64_t to = h * a.np + prompt_pad(off, lo) + row - off;
+    a.D[to] = d;
+    a.lse2[to] = a.lse[row * a.H + h] * kLog2e;
+  }
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) {
+  using C = Simt<DH>;
+  extern __shared__ float sm[];
+  float *Q = sm, *G = Q + C::TILE, *K = G + C::TILE, *V = K + C::TILE, *S = V + C::TILE;
+  PromptTile x;
+  int h;
+  if (!my_tile(a, a.H, false, x, h)) return;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, t0 = x.tile * kT, m = h / a.g;
+  load_tile<T, DH>(Q, reinterpret_cast<const T*>(a.q) + (int64_t)(x.off + t0) * a.q_ts + h * a.q_hs, a.q_ts, x.len - t0);
+  load_tile<T, DH>(G, reinterpret_cast<const T*>(a.dout) + (int64_t)(x.off + t0) * a.do_ts + h * a.do_hs, a.do_ts, x.len - t0);
+  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
+  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
+  float dq[4][C::CV] = {}, lse[4], D[4];
+  const int64_t rows = h * a.np + prompt_pad(x.off, x.b) + t0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool on = t0 + ty + 16 * i < x.len;
+    lse[i] = on ? a.lse2[rows + ty + 16 * i] : CUDART_INF_F;  // rows that do not exist weigh nothing
+    D[i] = on ? a.D[rows + ty + 16 * i] : 0.f;
+  }
+  const float sl2 = a.scale * kLog2e;
+  for (int j = first_keys(a, t0); j <= x.tile; ++j) {
+    __syncthreads();
+    load_tile<T, DH>(K, k + (int64_t)j * kT * a.k_ts, a.k_ts, x.len - j * kT);
+    load_tile<T, DH>(V, v + (int64_t)j * kT * a.v_ts, a.v_ts, x.len - j * kT);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    products<DH>(Q, K, s);
+    products<DH>(G, V, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool on = sees(a, t0 + ty + 16 * i, j * kT + tx + 16 * c);
+        S[(ty + 16 * i) * C::LP + tx + 16 * c] = on ? exp2f(s[i][c] * sl2 - lse[i]) * (dp[i][c] - D[i]) : 0.f;
+      }
+    __syncthreads();
+    weighted<DH>(S, K, dq);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + ty + 16 * i;
+    if (t >= x.len) continue;
+    T* to = reinterpret_cast<T*>(a.dq) + (int64_t)(x.off + t) * a.dq_ts + h * a.dq_hs;
+#pragma unroll
+    for (int c = 0; c < C::CV; ++c) Elem<T>::st(to + column<DH>(c), dq[i][c] * a.scale);
+  }
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kThreads) prompt_dkv_simt_kernel(PromptArgs a) {
+  using C = Simt<DH>;
+  extern __shared__ float sm[];
+  float *K = sm, *V = K + C::TILE, *Q = V + C::TILE, *G = Q + C::TILE, *P = G + C::TILE, *S = P + C::SCORES;
+  PromptTile x;
+  int m;
+  if (!my_tile(a, a.Hkv, true, x, m)) return;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, k0 = x.tile * kT;
+  load_tile<T, DH>(K, reinterpret_cast<const T*>(a.k) + (int64_t)(x.off + k0) * a.k_ts + m * a.k_hs, a.k_ts, x.len - k0);
+  load_tile<T, DH>(V, reinterpret_cast<const T*>(a.v) + (int64_t)(x.off + k0) * a.v_ts + m * a.v_hs, a.v_ts, x.len - k0);
+  float dk[4][C::CV] = {}, dv[4][C::CV] = {};
+  const float sl2 = a.scale * kLog2e;
+  const int end = last_rows(a, min(k0 + kT, x.len) - 1, x.len);
+  for (int h = m * a.g; h < m * a.g + a.g; ++h) {
+    const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)x.off * a.q_ts + h * a.q_hs;
+    const T* g = reinterpret_cast<const T*>(a.dout) + (int64_t)x.off * a.do_ts + h * a.do_hs;
+    const int64_t rows = h * a.np + prompt_pad(x.off, x.b);
+    for (int i = x.tile; i < end; ++i) {
+      __syncthreads();
+      load_tile<T, DH>(Q, q + (int64_t)i * kT * a.q_ts, a.q_ts, x.len - i * kT);
+      load_tile<T, DH>(G, g + (int64_t)i * kT * a.do_ts, a.do_ts, x.len - i * kT);
+      __syncthreads();
+      float s[4][4], dp[4][4];
+      products<DH>(K, Q, s);
+      products<DH>(V, G, dp);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int t = i * kT + tx + 16 * c;
+        const bool row = t < x.len;
+        const float lse = row ? a.lse2[rows + t] : 0.f, D = row ? a.D[rows + t] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool on = row && sees(a, t, k0 + ty + 16 * e);
+          const float p = on ? exp2f(s[e][c] * sl2 - lse) : 0.f;
+          P[(ty + 16 * e) * C::LP + tx + 16 * c] = p;
+          S[(ty + 16 * e) * C::LP + tx + 16 * c] = on ? p * (dp[e][c] - D) : 0.f;
+        }
+      }
+      __syncthreads();
+      weighted<DH>(P, G, dv);
+      weighted<DH>(S, Q, dk);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int k = k0 + ty + 16 * e;
+    if (k >= x.len) continue;
+    T* kt = reinterpret_cast<T*>(a.dk) + (int64_t)(x.off + k) * a.dk_ts + m * a.dk_hs;
+    T* vt = reinterpret_cast<T*>(a.dv) + (int64_t)(x.off + k) * a.dv_ts + m * a.dv_hs;
+#pragma unroll
+    for (int c = 0; c < C::CV; ++c) {
+      Elem<T>::st(kt + column<DH>(c), dk[e][c] * a.scale);
+      Elem<T>::st(vt + column<DH>(c), dv[e][c]);
+    }
+  }
+}
+
+// CTAs for every tile that the sequences can have: as many as whole tiles, and one that is not full each.
+int64_t tiles_at_most(const PromptArgs& a) { return a.N / kT + std::min<int64_t>(a.B, a.N); }
+
+template <typename T, int DH>
+cudaError_t forward_simt(const PromptArgs& a, cudaStream_t s) {
+  using C = Simt<DH>;
+  constexpr int smem = (3 * C::TILE + C::SCORES) * 4;
+  cudaError_t e = allow_smem((const void*)prompt_simt_kernel<T, DH>, smem);
+  if (e != cudaSuccess) return e;
+  launch_begin("prompt_simt", s);
+  prompt_simt_kernel<T, DH><<<(unsigned)(tiles_at_most(a) * a.H), kThreads, smem, s>>>(a);
+  return launch_end("prompt_simt", s);
+}
+
+template <typename T, int DH>
+cudaError_t backward_simt(const PromptArgs& a, cudaStream_t s) {
+  using C = Simt<DH>;
+  constexpr int sq = (4 * C::TILE + C::SCORES) * 4, skv = (4 * C::TILE + 2 * C::SCORES) * 4;
+  cudaError_t e = allow_smem((const void*)prompt_dq_simt_kernel<T, DH>, sq);
+  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dkv_simt_kernel<T, DH>, skv);
+  if (e != cudaSuccess) return e;
+  launch_begin("prompt_dq_simt", s);
+  prompt_dq_simt_kernel<T, DH><<<(unsigned)(tiles_at_most(a) * a.H), kThreads, sq, s>>>(a);
+  e = launch_end("prompt_dq_simt", s);
+  if (e != cudaSuccess) return e;
+  launch_begin("prompt_dkv_simt", s);
+  prompt_dkv_simt_kernel<T, DH><<<(unsigned)(tiles_at_most(a) * a.Hkv), kThreads, skv, s>>>(a);
+  return launch_end("prompt_dkv_simt", s);
+}
+
+}  // namespace
+
+int64_t prompt_scratch_rows(int64_t N, int B) { return (N + 4 * (int64_t)B + 128 + 3) / 4 * 4; }
+
+cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
+  if (a.bf16) {
+    using T = __nv_bfloat16;
+    return a.dh == 32 ? forward_simt<T, 32>(a, s) : a.dh == 64 ? forward_simt<T, 64>(a, s) : forward_simt<T, 128>(a, s);
+  }
+  return a.dh == 32 ? forward_simt<float, 32>(a, s) : a.dh == 64 ? forward_simt<float, 64>(a, s) : forward_simt<float, 128>(a, s);
+}
+
+cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s) {
+  launch_begin("prompt_rows", s);
+  const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)a.H);
+  if (a.bf16) prompt_rows_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+  else prompt_rows_kernel<float><<<grid, 256, 0, s>>>(a);
+  cudaError_t e = launch_end("prompt_rows", s);
+  if (e != cudaSuccess) return e;
+  if (a.bf16) {
+    using T = __nv_bfloat16;
+    return a.dh == 32 ? backward_simt<T, 32>(a, s) : a.dh == 64 ? backward_simt<T, 64>(a, s) : backward_simt<T, 128>(a, s);
+  }
+  return a.dh == 32 ? backward_simt<float, 32>(a, s) : a.dh == 64 ? backward_simt<float, 64>(a, s) : backward_simt<float, 128>(a, s);
+}
+
+}  // namespace gca
