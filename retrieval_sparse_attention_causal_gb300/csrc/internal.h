@@ -60,6 +60,8 @@ cudaError_t make_lmk_tmap(CUtensorMap* out, const void* base, int64_t D, int64_t
 cudaError_t make_pages_tmap(CUtensorMap* out, const void* base, int dh, int heads, int64_t pages);
 cudaError_t make_draft_tmap(CUtensorMap* out, const void* base, int dh, int heads, int tokens, int batches,
                             int64_t head_stride, int64_t token_stride, int64_t batch_stride);
+// Rows [rows][heads][dh] bf16 of packed sequences with free strides as boxes of 64 elements of 128 rows.
+cudaError_t make_packed_tmap(CUtensorMap* out, const void* base, int dh, int heads, int64_t rows, int64_t head_stride, int64_t row_stride);
 // The same matrix as a TMA store target: 32 x 32 boxes, 64-byte swizzle (tmap.cu).
 cudaError_t make_store_tmap(CUtensorMap* out, const void* base, int64_t cols, int64_t rows);
 
@@ -247,6 +249,7 @@ constexpr int kPromptSequences = 1024;
 int64_t prompt_scratch_rows(int64_t N, int B);
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s);
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s);
 
 // ---- attention of drafted tokens over a paged cache (tree_attn.cu)
 struct TreeArgs {

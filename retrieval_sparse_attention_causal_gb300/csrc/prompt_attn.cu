@@ -376,10 +376,7 @@ cudaError_t backward_simt(const PromptArgs& a, cudaStream_t s) {
 int64_t prompt_scratch_rows(int64_t N, int B) { return (N + 4 * (int64_t)B + 128 + 3) / 4 * 4; }
 
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
-  if (a.bf16) {
-    using T = __nv_bfloat16;
-    return a.dh == 32 ? forward_simt<T, 32>(a, s) : a.dh == 64 ? forward_simt<T, 64>(a, s) : forward_simt<T, 128>(a, s);
-  }
+  if (a.bf16) return launch_prompt_tc(a, s);
   return a.dh == 32 ? forward_simt<float, 32>(a, s) : a.dh == 64 ? forward_simt<float, 64>(a, s) : forward_simt<float, 128>(a, s);
 }
 

@@ -1,0 +1,441 @@
+// Causal attention over packed sequences, bf16, on the 5th-generation tensor cores.
+//
+// With 128 rows and 128 keys a tile asks 4 * 128 * 128 * dh operations and 128 * 128 exponentials: at dh
+// 64 the tensor pipe and the exponentials' pipe take about 512 cycles each, at dh 128 the tensor pipe
+// takes twice as long.  Both have to work at once, so a CTA (one on an SM, persistent) holds two tiles of
+// rows that take turns: while one tile's softmax runs, the other's products do.  The two tiles are two
+// heads that share a key head where their number is even, else two neighbouring tiles of one head; either
+// way they read the same keys.
+//   * one warp loads: the rows' tiles, and blocks of 128 keys of K and V in turn through a ring, from the
+//     diagonal down (so a tile's first block is the one with the causal mask, which has to be weighed by
+//     its maximum anyway);
+//   * one warp issues the products: O += P(n) V(n) with P in the TMEM columns that S(n) lay in, behind
+//     it S(n + 1) = Q K(n + 1)^T into the same columns.  The tensor pipe runs one warp's products in
+//     order, so a thread that has seen S(n + 1) knows that P(n) V(n) is done;
+//   * four warps a tile do the softmax, a thread a row, as in tree_tc.cu: the weights are exp(s - r) by a
+//     reference r that need not stay the maximum; when the sum of a row's 128 weights passes 2^14 the
+//     block is weighed again by the new maximum, and the output and the sum so far are scaled to it.
+//     P is rounded to bf16, the type of the product's other operand, so each weight is off by half a
+//     step (2^-8 of it) at most, like the output itself; the sum is of the float32 weights.
+// Blocks that a sequence's end cuts may hold anything behind it: those rows of V become zeros in shared
+// memory, for a weight of 0 times what lies in them must stay 0.  dh 32 is read as 64 with zeros behind
+// it (the tensor map fills them in).
+#include <algorithm>
+
+#include "prompt.cuh"
+#include "tc.cuh"
+#include "tc_rows.cuh"
+#include "waits.cuh"
+
+namespace gca {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kT = 128;           // rows of a tile, keys of a block
+constexpr int kThreads = 320;     // warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: products, 9: loads
+constexpr int kTile = kT * 128;   // bytes of 128 rows x 64 elements
+constexpr uint32_t kCols = 512;   // of TMEM: two tiles' logits, then their outputs
+constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteQFree, kSiteS, kSiteP, kSiteO, kSiteOFree, kSiteV, kSiteRing };
+
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
+  return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
+}
+
+template <int DH>
+struct Tc {
+  static constexpr int SUB = DH / 64;              // 64-element parts of a head
+  static constexpr int BLOCK = kTile * SUB;        // a tile of Q, a block of K or of V
+  static constexpr int NS = DH == 64 ? 11 : 5;     // ring slots: what shared memory holds beside two tiles of Q
+  static constexpr int SMEM = 1024 + 2 * BLOCK + NS * BLOCK;
+};
+
+// A work item: up to two tiles of rows and the blocks of keys that they see, from hi down to lo.
+struct Item {
+  PromptTile x;
+  int head[2], tile[2];        // of each tile of rows
+  int hi[2], lo[2];            // its blocks; hi < lo: there is no such tile
+  int m;                       // the key head
+  __device__ __forceinline__ int top() const { return max(hi[0], hi[1]); }
+  __device__ __forceinline__ int low() const { return hi[1] < lo[1] ? lo[0] : min(lo[0], lo[1]); }
+};
+
+__device__ __forceinline__ bool item_of(const PromptArgs& a, int w, Item& it) {
+  const bool heads = a.g % 2 == 0;  // two heads of a tile, or two tiles of a head
+  const int per = heads ? a.H / 2 : a.H, h = w % per, rank = w / per;
+  if (heads) {
+    if (!prompt_tile<kT>(a, rank, false, it.x)) return false;
+    it.head[0] = 2 * h;
+    it.head[1] = 2 * h + 1;
+    it.tile[0] = it.tile[1] = it.x.tile;
+  } else {
+    if (!prompt_tile<2 * kT>(a, rank, false, it.x)) return false;
+    it.head[0] = it.head[1] = h;
+    it.tile[0] = 2 * it.x.tile;
+    it.tile[1] = 2 * it.x.tile + 1;
+  }
+  it.m = it.head[0] / a.g;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.hi[t] = it.tile[t] * kT < it.x.len ? it.tile[t] : -1;
+    it.lo[t] = a.window ? max(0, it.tile[t] * kT - a.window + 1) / kT : 0;
+  }
+  return true;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV) {
+  using C = Tc<DH>;
+  constexpr int SUB = C::SUB, NS = C::NS;
+  constexpr uint32_t kIdS = tc::idesc_bf16(kT, kT, false), kIdPV = tc::idesc_bf16(kT, 64, true);
+  extern __shared__ unsigned char dsm[];
+  unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  unsigned char* ring = Qs + 2 * C::BLOCK;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q[2], bar_qfree[2], bar_s[2], bar_p[2], bar_o[2], bar_ofree[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 288) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(&bar_full[i], 1);
+      tc::mbar_init(&bar_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(&bar_q[t], 1);
+      tc::mbar_init(&bar_qfree[t], 1);
+      tc::mbar_init(&bar_s[t], 1);
+      tc::mbar_init(&bar_p[t], 4);
+      tc::mbar_init(&bar_o[t], 1);
+      tc::mbar_init(&bar_ofree[t], 4);
+    }
+    abort_s = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 8) tc::tmem_alloc(&tmem_slot, kCols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+  auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
+    if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
+    return wait_on(bar, parity, &abort_s, a.err, site, blockIdx.x, at);
+  };
+  bool ok = true;
+  Item it;
+
+  if (warp == 9) {
+    // ---------------------------------------------------------------- loads
+    int id = 0, st = 0;      // slots so far, the next
+    uint32_t parity = 0;     // of its filling
+    int nq[2] = {0, 0};      // tiles of rows so far
+    for (int w = blockIdx.x; ok && item_of(a, w, it); w += gridDim.x) {
+      auto rows = [&](int t) {
+        if (it.hi[t] < it.lo[t]) return;
+        ok = ok && waited(&bar_qfree[t], (nq[t] & 1) ^ 1, kSiteQFree, w);
+        if (!ok) return;
+        tc::mbar_expect_tx_warp(&bar_q[t], C::BLOCK);
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+          tc::tma_load_4d_warp(Qs + t * C::BLOCK + s * kTile, &tmQ, 64 * s, a.q_hs ? it.head[t] : 0, it.x.off + it.tile[t] * kT, 0, &bar_q[t]);
+        ++nq[t];
+      };
+      const int top = it.top(), low = it.low();
+      for (int n = top; n >= low && ok; --n)
+#pragma unroll 1
+        for (int v = 0; v < 2 && ok; ++v) {
+          if (n == top) rows(v);
+          ok = ok && waited(&bar_empty[st], parity ^ 1, kSiteEmpty, n);
+          if (!ok) break;
+          tc::mbar_expect_tx_warp(&bar_full[st], C::BLOCK);
+#pragma unroll
+          for (int s = 0; s < SUB; ++s)
+            tc::tma_load_4d_warp(ring + st * C::BLOCK + s * kTile, v ? &tmV : &tmK, 64 * s, (v ? a.v_hs : a.k_hs) ? it.m : 0,
+                                 it.x.off + n * kT, 0, &bar_full[st]);
+          ++id;
+          if (++st == NS) {
+            st = 0;
+            parity ^= 1;
+          }
+        }
+    }
+    if (!ok) {  // let the copies in flight land before the CTA ends
+      for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&bar_full[i % NS], (i / NS) & 1, 1u << 16);
+      for (int t = 0; t < 2; ++t)
+        if (nq[t]) tc::mbar_wait(&bar_q[t], (nq[t] - 1) & 1, 1u << 16);
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- products
+    int ks = 0, vs = 1;               // the slots that K and V come from, and the parities they are filled at
+    uint32_t kp = 0, vp = 0;
+    auto pass = [](int& slot, uint32_t& parity) {
+      slot += 2;
+      if (slot >= NS) {
+        slot -= NS;
+        parity ^= 1;
+      }
+    };
+    int nq[2] = {0, 0}, nb[2] = {0, 0};  // tiles of rows and blocks so far
+    const uint64_t dQ = tc::desc_km(tc::su32(Qs));
+    for (int w = blockIdx.x; ok && item_of(a, w, it); w += gridDim.x) {
+      const int top = it.top(), low = it.low();
+      auto has = [&](int t, int n) { return n <= it.hi[t] && n >= it.lo[t]; };
+      // Step n: P V of block n + 1 (the one before), and the logits of block n, tile by tile.
+      for (int n = top; n >= low - 1 && ok; --n) {
+        const bool load_k = n >= low, load_v = n < top;
+        if (load_k) ok = waited(&bar_full[ks], kp, kSiteFull, n);
+        if (load_v) ok = ok && waited(&bar_full[vs], vp, kSiteFull, n);
+        if (!ok) break;
+        const uint32_t k = tc::su32(ring + ks * C::BLOCK), v = tc::su32(ring + vs * C::BLOCK);
+        tc::fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t tS = tmem + kT * t, tO = tmem + 2 * kT + DH * t;
+          if (load_v && has(t, n + 1)) {
+            const bool first = n + 1 == it.hi[t];
+            if (first) ok = ok && waited(&bar_ofree[t], nq[t] & 1, kSiteOFree, n);  // read by the tile before (nq counts this one)
+            ok = ok && waited(&bar_p[t], nb[t] & 1, kSiteP, n);
+            if (!ok) break;
+            ++nb[t];
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+              tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tS, tc::desc_mn(v + s * kTile), kIdPV, first ? 0u : 1u);
+              tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tS + 32, tc::desc_mn(v + s * kTile + kTile / 2), kIdPV, 1u);
+            }
+            if (n < it.lo[t]) tc::commit_warp(&bar_o[t]);  // the tile's last
+          }
+          if (load_k && has(t, n)) {
+            if (n == it.hi[t]) {
+              ok = ok && waited(&bar_q[t], nq[t] & 1, kSiteQ, n);
+              if (!ok) break;
+              ++nq[t];
+              tc::fence_after();
+            }
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+              tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tS, dQ + ((t * C::BLOCK + s * kTile) >> 4), tc::desc_km(k + s * kTile), kIdS, s ? 1u : 0u);
+            tc::commit_warp(&bar_s[t]);
+            if (n == it.lo[t]) tc::commit_warp(&bar_qfree[t]);
+          }
+        }
+        if (!ok) break;
+        if (load_k) {
+          tc::commit_warp(&bar_empty[ks]);
+          pass(ks, kp);
+        }
+        if (load_v) {
+          tc::commit_warp(&bar_empty[vs]);
+          pass(vs, vp);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2, r = tid & 127;  // the tile, the row of it
+    const float sl2 = a.scale * kLog2e;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + kT * t + lanes, tO = tmem + 2 * kT + DH * t + lanes;
+    int nb = 0, no = 0, slot = 0;            // blocks and tiles so far, ring slots before the item
+    for (int w = blockIdx.x; ok && item_of(a, w, it); w += gridDim.x) {
+      const int hi = it.hi[t], lo = it.lo[t], top = it.top();
+      const int pos = it.tile[t] * kT + r;
+      const bool on = pos < it.x.len;
+      const int first = a.window ? max(0, pos - a.window + 1) : 0;  // the first key that the row sees
+      const int whole = a.window ? (max(0, it.tile[t] * kT + kT - a.window) + kT - 1) / kT : 0;  // blocks from here to hi - 1 are seen whole
+      float mx = -CUDART_INF_F, l = 0.f;
+      const uint64_t k2 = tc::f2(sl2, sl2);
+      uint64_t sums[4], b2 = 0;
+      auto weigh = [&](const float (&s)[32], uint32_t* p) {  // by the row's reference
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x, y;
+          tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, b2), x, y);
+          x = tc::ex2(x);
+          y = tc::ex2(y);
+          sums[i & 3] = tc::add2(sums[i & 3], tc::f2(x, y));
+          p[i] = pack_bf16(x, y);
+        }
+      };
+      auto total = [&]() {
+        float x, y;
+        tc::uf2(tc::add2(tc::add2(sums[0], sums[1]), tc::add2(sums[2], sums[3])), x, y);
+        return x + y;
+      };
+      // A row that does not exist weighs nothing.
+      auto set_base = [&]() {
+        const float base = !on ? -CUDART_INF_F : mx == -CUDART_INF_F ? 0.f : -mx * sl2;
+        b2 = tc::f2(base, base);
+      };
+      for (int n = hi; n >= lo && ok; --n, ++nb) {
+        ok = waited(&bar_s[t], nb & 1, kSiteS, n);
+        if (!ok) break;
+        tc::fence_after();
+        const bool inner = n < hi && n >= whole;
+        bool done = false;
+        if (__builtin_expect(inner, 1)) {
+          // Seen whole, by references that hold: one straight run.
+          float s0[32], s1[32];
+          uint32_t p[64];
+          sums[0] = sums[1] = sums[2] = sums[3] = 0;
+          tc::ld32x32b_x32(tS, s0);
+          tc::ld_wait_row(s0);
+          tc::ld32x32b_x32(tS + 32, s1);  // on its way while the first quarter is weighed
+          weigh(s0, p);
+          tc::ld_wait_row(s1);
+          tc::ld32x32b_x32(tS + 64, s0);
+          weigh(s1, p + 16);
+          tc::ld_wait_row(s0);
+          tc::ld32x32b_x32(tS + 96, s1);
+          weigh(s0, p + 32);
+          tc::ld_wait_row(s1);
+          weigh(s1, p + 48);
+          const float sum = total();
+          if (__builtin_expect(!__any_sync(kAll, sum > kMost), 1)) {
+            l += sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t q[8] = {p[8 * i], p[8 * i + 1], p[8 * i + 2], p[8 * i + 3], p[8 * i + 4], p[8 * i + 5], p[8 * i + 6], p[8 * i + 7]};
+              tc::st32x32b_x8(tS + 8 * i, q);
+            }
+            done = true;
+          }
+        }
+        if (__builtin_expect(!done, 0)) {
+          // Keys c0 .. c1 - 1 of the block are seen.  The maximum with this block, and the weights by it.
+          const int c0 = max(first - n * kT, 0), c1 = on ? min(pos - n * kT + 1, kT) : 0;
+          if (n == hi && (n + 1) * kT > it.x.len) {
+            // Rows of V behind the sequence become zeros (by this tile's softmax where it is the tile that
+            // reaches them, or by both with the same zeros).
+            const int i = slot + 2 * (top - n) + 1;
+            ok = waited(&bar_full[i % NS], (i / NS) & 1, kSiteV, n);
+            if (!ok) break;
+            if (n * kT + r >= it.x.len)
+#pragma unroll
+              for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  *reinterpret_cast<uint4*>(ring + (i % NS) * C::BLOCK + s * kTile + r * 128 + u * 16) = make_uint4(0, 0, 0, 0);
+            tc::fence_async_smem();
+          }
+          float now = mx;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float s[32];
+            tc::ld32x32b_x32(tS + 32 * q, s);
+            tc::ld_wait_row(s);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int c = 32 * q + i;
+              if (c >= c0 && c < c1) now = fmaxf(now, s[i]);
+            }
+          }
+          const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
+          mx = now;
+          l *= f;
+          if (n < hi && __any_sync(kAll, f != 1.f)) {  // S(n) was seen, so the products before it are done
+#pragma unroll 1
+            for (int q = 0; q < DH / 32; ++q) {
+              float o[32];
+              tc::ld32x32b_x32(tO + 32 * q, o);
+              tc::ld_wait_row(o);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(o[8 * i + e] * f);
+                tc::st32x32b_x8(tO + 32 * q + 8 * i, x);
+              }
+            }
+          }
+          set_base();
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float s[32];
+            tc::ld32x32b_x32(tS + 32 * q, s);
+            tc::ld_wait_row(s);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int c = 32 * q + i;
+              if (c < c0 || c >= c1) s[i] = -CUDART_INF_F;
+            }
+            uint32_t p[16];
+            sums[0] = sums[1] = sums[2] = sums[3] = 0;
+            weigh(s, p);
+            l += total();
+            const uint32_t p0[8] = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]}, p1[8] = {p[8], p[9], p[10], p[11], p[12], p[13], p[14], p[15]};
+            tc::st32x32b_x8(tS + 16 * q, p0);  // over logits that have been read
+            tc::st32x32b_x8(tS + 16 * q + 8, p1);
+          }
+        }
+        tc::st_wait();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar_p[t]);
+      }
+      slot += 2 * (top - it.low() + 1);
+      if (!ok || hi < lo) continue;
+      ok = waited(&bar_o[t], no & 1, kSiteO, -1);
+      ++no;
+      if (!ok) break;
+      tc::fence_after();
+      const float inv = 1.f / l;
+      const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
+      bf16* row = reinterpret_cast<bf16*>(a.o) + to * a.dh;
+#pragma unroll
+      for (int q = 0; q < DH / 32; ++q) {
+        if (32 * q >= a.dh) break;
+        float o[32];
+        tc::ld32x32b_x32(tO + 32 * q, o);
+        tc::ld_wait_row(o);
+        if (!on) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(row + 32 * q + 8 * i) =
+              make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                         pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar_ofree[t]);
+      if (on) a.lse[to] = mx * a.scale + logf(l);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem_slot, kCols);
+  }
+}
+
+template <int DH>
+cudaError_t run_tc(const PromptArgs& a, cudaStream_t s) {
+  using C = Tc<DH>;
+  CUtensorMap q, k, v;
+  cudaError_t e = make_packed_tmap(&q, a.q, a.dh, a.H, a.N, a.q_hs, a.q_ts);
+  if (e == cudaSuccess) e = make_packed_tmap(&k, a.k, a.dh, a.Hkv, a.N, a.k_hs, a.k_ts);
+  if (e == cudaSuccess) e = make_packed_tmap(&v, a.v, a.dh, a.Hkv, a.N, a.v_hs, a.v_ts);
+  if (e == cudaSuccess) e = allow_smem((const void*)prompt_tc_kernel<DH>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // Items: whole tiles of rows, and at most one that is not whole a sequence.
+  const int rows = a.g % 2 == 0 ? kT : 2 * kT;
+  const int64_t items = (a.N / rows + std::min<int64_t>(a.B, a.N)) * (a.g % 2 == 0 ? a.H / 2 : a.H);
+  launch_begin("prompt_tc", s);
+  prompt_tc_kernel<DH><<<(unsigned)std::min<int64_t>(items, kSMs), kThreads, C::SMEM, s>>>(a, q, k, v);
+  return launch_end("prompt_tc", s);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s) { return a.dh <= 64 ? run_tc<64>(a, s) : run_tc<128>(a, s); }
+
+}  // namespace gca

@@ -128,6 +128,24 @@ cudaError_t make_draft_tmap(CUtensorMap* out, const void* base, int dh, int head
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_packed_tmap(CUtensorMap* out, const void* base, int dh, int heads, int64_t rows, int64_t head_stride, int64_t row_stride) {
+  std::call_once(g_once, load_encode);
+  if (g_encode_err != cudaSuccess) return g_encode_err;
+  // dims innermost first: element, head, row, and an axis of one.  The box is 64 elements of one head of 128
+  // rows; elements behind a head of 32, and rows past the end, read zeros.  A head stride of 0 repeats one
+  // head: an axis of one, read at coordinate 0.
+  const int64_t any = (int64_t)heads * dh;
+  const int64_t rs = row_stride ? row_stride : any;
+  cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)(head_stride ? heads : 1), (cuuint64_t)rows, 1};
+  cuuint64_t strides[3] = {(cuuint64_t)(head_stride ? head_stride : any) * 2, (cuuint64_t)rs * 2, (cuuint64_t)rs * 2};
+  cuuint32_t box[4] = {64, 1, 128, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_store_tmap(CUtensorMap* out, const void* base, int64_t cols, int64_t rows) {
   std::call_once(g_once, load_encode);
   if (g_encode_err != cudaSuccess) return g_encode_err;

@@ -1,0 +1,577 @@
+"""GPU parity of a prompt's operators (attention over packed sequences with its gradients, norms with
+rotary positions, the quantised cache) against the float64 oracle, and their use together.
+
+Tolerances count roundings.  u = 2^-24 is float32's half step, h the output type's (bf16 2^-8,
+float32 2^-24); bf16 operands of a product that were rounded for it (P and dS) are off by 2^-8 of
+themselves.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.decode_oracle as dorc
+import oracle.prompt_oracle as orc
+from retrieval_sparse_attention_causal_gb300 import pipeline, synth
+from tests.gpu_helpers import dev, host
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _g():
+    import retrieval_sparse_attention_causal_gb300 as g
+    return g
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word(request):
+    yield
+    if not getattr(request.function, "flags", False):
+        _g().cache_workspace("cuda").check()
+
+
+def flags(test):
+    """A test that sets the error word and reads it itself."""
+    test.flags = True
+    return test
+
+
+def ints(x):
+    return torch.as_tensor(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+
+def offsets_of(lengths, first=0):
+    return np.concatenate([[first], first + np.cumsum(lengths)]).astype(np.int64)
+
+
+def within(got, ref, lim, what):
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    there = ~np.isnan(ref)
+    assert not np.isnan(got[there]).any(), f"{what}: NaN"
+    over = np.abs(got[there] - ref[there]) - np.broadcast_to(lim, ref.shape)[there]
+    assert over.size == 0 or over.max() <= 0, f"{what}: {int((over > 0).sum())} of {over.size} beyond the bound by {over.max():.3g}"
+
+
+# ------------------------------------------------------------------ packed sequences
+def prompt_bounds(r, dtype, dh, longest, g, scale=None):
+    """What the outputs of a call may be off.  A logit: dh + 8 roundings of its products' sum, the scale
+    and the reference, all relative to scale sum |q||k| (s_abs).  An exponential: 2^-22 of itself from
+    the hardware's, and what its argument is off.  So p is off by c of itself: its own logit and the
+    sum's, the sum's n roundings.  Then o: bf16 rounds p for the product (2^-8), n + 16 roundings of the
+    sum, and the output's rounding; D = <do, o> takes o as it was rounded.  The gradients: c for p, dh
+    roundings of <do, v> and of D, bf16 rounds P or dS for the product, n g roundings of the sum (dq
+    and dk have the scale's too), and the output's rounding."""
+    h, p8 = HALF[dtype], 1.02 * (2.0 ** -8 if dtype == "bf16" else 0.0)
+    # (a bound for all rows: the largest logit's)
+    ds = (dh + 8) * U * np.nanmax(r["s_abs"]) + 8 * U
+    c = 2 * ds + (longest + 16) * U
+    lim = dict(lse=ds + (longest + 16) * U + 4 * U * np.abs(r["lse"]),
+               o=h * np.abs(r["o"]) + r["o_abs"] * (p8 + 1.02 * c))
+    if "dq" in r:
+        e = 2 * c + (longest * g + 4 * dh + 32) * U
+        for name, extra in (("dq", 1.02 * h), ("dk", 1.02 * h), ("dv", 0.0)):
+            lim[name] = h * np.abs(r[name]) + r[name + "_abs"] * (p8 + 1.02 * e + extra) + 1e-30
+    return lim
+
+
+CASES = [  # lengths, H, Hkv, dh, window, dtype
+    ((1,), 1, 1, 64, 0, "bf16"),
+    ((77,), 12, 12, 64, 0, "bf16"),
+    ((128,), 2, 1, 64, 0, "bf16"),
+    ((129, 0, 1, 64), 2, 2, 64, 0, "bf16"),
+    ((256, 255, 257), 3, 1, 64, 0, "bf16"),
+    ((300, 5, 0, 641), 4, 2, 128, 0, "bf16"),
+    ((130, 700), 3, 3, 128, 0, "bf16"),
+    ((60, 200), 8, 2, 32, 0, "bf16"),
+    ((900,), 5, 1, 32, 100, "bf16"),
+    ((1000, 30), 4, 4, 64, 1, "bf16"),
+    ((513, 640), 4, 1, 64, 128, "bf16"),
+    ((777,), 2, 2, 64, 129, "bf16"),
+    ((600, 600), 6, 3, 128, 300, "bf16"),
+    ((1500,), 2, 1, 64, 1000, "bf16"),
+    (tuple([3, 70] * 40), 2, 2, 64, 0, "bf16"),
+    (tuple([130, 0, 1, 260] * 17), 2, 1, 64, 50, "bf16"),
+    ((1,), 1, 1, 32, 0, "f32"),
+    ((64, 65, 0, 63), 2, 1, 64, 0, "f32"),
+    ((200, 3), 6, 2, 32, 0, "f32"),
+    ((150, 90), 3, 3, 128, 40, "f32"),
+    (tuple([5, 66] * 20), 2, 1, 64, 7, "f32"),
+]
+
+
+@pytest.mark.parametrize("lengths,H,Hkv,dh,window,dtype", CASES)
+def test_prompt_attention_against_oracle(lengths, H, Hkv, dh, window, dtype):
+    """Outputs, log-sum-exps and gradients; rows in front of the first sequence and behind the last, which
+    hold NaN, reach nothing and stay as they were."""
+    g = _g()
+    off = offsets_of(lengths, 3)
+    N = int(off[-1]) + 5
+    q, k, v, do = (synth.normal(21, s, (N, h, dh), 1.0, dtype) for s, h in ((0, H), (1, Hkv), (2, Hkv), (3, H)))
+    r = orc.prompt_attention(q, k, v, off, window, dout=do)
+    for x in (q, k, v, do):
+        x[:3] = x[off[-1]:] = np.nan
+    qd, kd, vd, dod = (dev(x, dtype) for x in (q, k, v, do))
+    o = torch.full((N, H, dh), 7.0, dtype=TORCH[dtype], device="cuda")
+    lse = torch.full((N, H), 7.0, device="cuda")
+    got = dict(zip(("o", "lse"), g.prompt_attention(qd, kd, vd, ints(off), window=window, out=o, lse=lse)))
+    grads = [torch.full_like(x, 7.0) for x in (qd, kd, vd)]
+    got.update(zip(("dq", "dk", "dv"), g.prompt_attention_backward(qd, kd, vd, o, dod, lse, ints(off), window=window,
+                                                                   dq=grads[0], dk=grads[1], dv=grads[2])))
+    lim = prompt_bounds(r, dtype, dh, max(lengths), H // Hkv)
+    for name, x in got.items():
+        x = host(x)
+        within(x, r[name], lim[name], name)
+        assert (x[:3] == 7).all() and (x[off[-1]:] == 7).all(), f"{name}: rows of no sequence were written"
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("bf16", 32), ("f32", 64)])
+def test_prompt_sequences_do_not_reach_each_other(dtype, dh):
+    """NaN and infinities in one sequence leave the others' results as they were, to the bit."""
+    g = _g()
+    lengths = (130, 60, 300, 1, 90)
+    off = offsets_of(lengths)
+    N, H = int(off[-1]), 2
+    x = [dev(synth.normal(22, s, (N, H, dh), 1.0, dtype), dtype) for s in range(4)]
+    run = lambda q, k, v, do: (lambda o, lse: (o, lse) + g.prompt_attention_backward(q, k, v, o, do, lse, ints(off)))(  # noqa: E731
+        *g.prompt_attention(q, k, v, ints(off)))
+    want = run(*x)
+    for b in (0, 2, 4):
+        bad = [t.clone() for t in x]
+        for t, value in zip(bad, (float("nan"), float("inf"), float("nan"), float("-inf"))):
+            t[off[b]:off[b + 1]] = value
+        for w, got in zip(want, run(*bad)):
+            rest = torch.ones(N, dtype=torch.bool)
+            rest[off[b]:off[b + 1]] = False
+            assert torch.equal(w[rest], got[rest])
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 32)])
+def test_prompt_large_logits(dtype, dh):
+    """Logits that grow by hundreds along a sequence, and fall again: references that are outgrown."""
+    g = _g()
+    n, H = 700, 2
+    q, k, v, do = (synth.normal(23, s, (n, H, dh), 1.0, dtype) for s in range(4))
+    k = k * np.concatenate([np.linspace(0.1, 12, n // 2), np.linspace(12, 0.01, n - n // 2)])[:, None, None]
+    k = host(dev(k, dtype))
+    q[:, :, 0] = 4.0
+    k[::-1, :, 0] += np.linspace(0, 60, n)[:, None] * (np.arange(n)[:, None] % 97 == 0)
+    k = host(dev(k, dtype))
+    off = offsets_of((n,))
+    r = orc.prompt_attention(q, k, v, off, 0, dout=do)
+    d = [dev(x, dtype) for x in (q, k, v, do)]
+    o, lse = g.prompt_attention(*d[:3], ints(off))
+    dq, dk, dv = g.prompt_attention_backward(*d[:3], o, d[3], lse, ints(off))
+    lim = prompt_bounds(r, dtype, dh, n, 1)
+    for name, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        within(host(x), r[name], lim[name], name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_views_scale_and_gradients_into_views(dtype):
+    """Views of a fused projection, heads-first storage, one key head repeated, a scale of its own, and
+    gradients into the views of one tensor give what contiguous tensors give."""
+    g = _g()
+    lengths = (140, 33)
+    off, H, Hkv, dh = offsets_of(lengths), 4, 2, 64
+    N = int(off[-1])
+    qkv = torch.randn(N, H + 2 * Hkv, dh, device="cuda").to(TORCH[dtype])
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    do = torch.randn(N, H, dh, device="cuda").to(TORCH[dtype])
+    c = [x.contiguous() for x in (q, k, v)]
+    want = g.prompt_attention(*c, ints(off), scale=0.3)
+    gwant = g.prompt_attention_backward(*c, want[0], do, want[1], ints(off), scale=0.3)
+    got = g.prompt_attention(q, k, v, ints(off), scale=0.3)
+    dqkv = torch.zeros_like(qkv)
+    g.prompt_attention_backward(q, k, v, got[0], do.transpose(0, 1).contiguous().transpose(0, 1), got[1], ints(off), scale=0.3,
+                                dq=dqkv[:, :H], dk=dqkv[:, H:H + Hkv], dv=dqkv[:, H + Hkv:])
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert torch.equal(dqkv, torch.cat(gwant, dim=1))
+    turned = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in c]
+    assert torch.equal(g.prompt_attention(*turned, ints(off), scale=0.3)[0], want[0])
+    one = [x[:, :1].expand(N, H, dh) for x in c[1:]]
+    a, _ = g.prompt_attention(c[0], *one, ints(off))
+    b, _ = g.prompt_attention(c[0], *(x.contiguous() for x in one), ints(off))
+    assert torch.equal(a, b)
+
+
+def test_prompt_calls_are_equal_and_follow_the_device():
+    """Equal calls give equal bits; on another stream too; and a captured pass follows offsets and inputs that
+    change behind it."""
+    g = _g()
+    H, Hkv, dh, N = 4, 2, 64, 900
+    q, k, v, do = (torch.randn(N, h, dh, device="cuda").bfloat16() for h in (H, Hkv, Hkv, H))
+    off = ints([0, 400, 400, 900])
+
+    def step():
+        o, lse = g.prompt_attention(q, k, v, off, window=200)
+        return (o, lse) + g.prompt_attention_backward(q, k, v, o, do, lse, off, window=200)
+    want = step()
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(want, step()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, other))
+    graphs = []
+    for _ in range(2):  # two graphs share no scratch
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    off.copy_(ints([0, 1, 877, 900]))
+    q.copy_(torch.randn_like(q))
+    want = step()
+    for graph, _ in graphs:
+        graph.replay()
+    for _, out in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_prompt_gradient_against_differences():
+    """(f(x + e d) - f(x - e d)) / 2e against <gradient, d>, f = <dout, o>, float32, e = 2^-6.  The difference's
+    truncation is e^2 / 6 of a third derivative of order |f|; rounding leaves 2^-24 n dh |f| / e.  Both are
+    far below 1e-2 of |f| here."""
+    g = _g()
+    off = ints([0, 30, 75])
+    x = [torch.from_numpy(synth.normal(24, s, (75, h, 32))).float().cuda() for s, h in ((0, 4), (1, 2), (2, 2))]
+    do = torch.from_numpy(synth.normal(24, 3, (75, 4, 32))).float().cuda()
+    o, lse = g.prompt_attention(*x, off, window=20)
+    grads = g.prompt_attention_backward(*x, o, do, lse, off, window=20)
+    f = lambda y: (g.prompt_attention(*y, off, window=20)[0].double() * do.double()).sum()  # noqa: E731
+    e = 2.0 ** -6
+    size = (o.double() * do.double()).abs().sum()
+    for i in range(3):
+        d = torch.from_numpy(synth.normal(25, i, x[i].shape)).float().cuda()
+        up, down = ([t + s * e * d if j == i else t for j, t in enumerate(x)] for s in (1, -1))
+        left, right = (f(up) - f(down)) / (2 * e), (grads[i].double() * d.double()).sum()
+        assert abs(float(left - right)) <= 1e-2 * float(size) * e + 1e-3 * abs(float(right)), (i, float(left), float(right))
+
+
+@flags
+def test_prompt_bad_offsets_are_flagged():
+    """A sequence whose offsets are out of order or of range is left out; the others are right."""
+    g = _g()
+    q, k, v = (torch.randn(300, 2, 64, device="cuda").bfloat16() for _ in range(3))
+    want, _ = g.prompt_attention(q, k, v, ints([100, 200]))
+    for off in ([0, -5, 100, 200], [100, 200, 301], [100, 200, 150], [100, 200, 2 ** 31 - 1]):
+        got, _ = g.prompt_attention(q, k, v, ints(off))
+        assert torch.equal(got[100:200], want[100:200]), off
+        with pytest.raises(g.GCAError) as e:
+            g.cache_workspace("cuda").check()
+        assert e.value.status == g.GCA_ERR_DEVICE_INDEX
+    g.cache_workspace("cuda").check()
+
+
+def test_prompt_nothing_to_do():
+    """No rows at all, and sequences that are all empty."""
+    g = _g()
+    q = torch.empty(0, 4, 64, device="cuda").bfloat16()
+    o, lse = g.prompt_attention(q, q[:, :2], q[:, :2], ints([0, 0, 0]))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert [x.shape[0] for x in g.prompt_attention_backward(q, q[:, :2], q[:, :2], o, q, lse, ints([0, 0]))] == [0, 0, 0]
+    x = torch.ones(7, 4, 64, device="cuda").bfloat16()
+    out, lse = torch.full_like(x, 3.0), torch.full((7, 4), 3.0, device="cuda")
+    g.prompt_attention(x, x, x, ints([2, 2, 2]), out=out, lse=lse)
+    assert (out == 3).all() and (lse == 3).all()
+    grads = [torch.full_like(x, 3.0) for _ in range(3)]
+    g.prompt_attention_backward(x, x, x, out, x, lse, ints([2, 2, 2]), dq=grads[0], dk=grads[1], dv=grads[2])
+    assert all((t == 3).all() for t in grads)
+
+
+def test_prompt_many_sequences_match_single_ones():
+    """1024 sequences (the most) give what each gives by itself."""
+    g = _g()
+    rng = np.random.default_rng(5)
+    lengths = rng.integers(0, 40, 1024)
+    off = offsets_of(lengths)
+    q, k, v = (torch.randn(int(off[-1]), h, 64, device="cuda").bfloat16() for h in (4, 2, 2))
+    o, lse = g.prompt_attention(q, k, v, ints(off))
+    for b in (0, 1, 31, 32, 511, 1022, 1023):
+        a, z = int(off[b]), int(off[b + 1])
+        if a == z:
+            continue
+        one, l1 = g.prompt_attention(q[a:z], k[a:z], v[a:z], ints([0, z - a]))
+        assert torch.equal(one, o[a:z]) and torch.equal(l1, lse[a:z])
+
+
+# ------------------------------------------------------------------ norms with rotary positions
+NORM = [  # B, L, H, Hkv, dh, rot, dtype, interleaved, eps
+    (1, 1, 1, 1, 2, 2, "f32", False, 1e-6),
+    (2, 5, 3, 1, 64, 64, "bf16", False, 1e-6),
+    (1, 33, 12, 12, 64, 32, "bf16", True, 1e-5),
+    (3, 17, 5, 1, 72, 40, "f32", False, 1e-6),
+    (2, 9, 4, 2, 40, 6, "bf16", True, 1e-6),
+    (1, 7, 2, 2, 50, 34, "bf16", False, 1e-6),
+    (2, 3, 6, 3, 256, 256, "f32", True, 1e-6),
+    (2, 3, 3, 1, 255, 2, "bf16", False, 1e-6),
+    (2, 3, 3, 1, 256, 8, "bf16", True, 1e-6),
+    (1, 700, 16, 4, 128, 96, "bf16", False, 0.0),
+    (4, 1, 12, 12, 64, 64, "bf16", True, 1e-6),
+    (2, 1500, 4, 2, 64, 64, "f32", False, 1e-6),
+]
+
+
+@pytest.mark.parametrize("B,L,H,Hkv,dh,rot,dtype,interleaved,eps", NORM)
+def test_norm_rotary_against_oracle(B, L, H, Hkv, dh, rot, dtype, interleaved, eps):
+    """The norm: dh + 8 roundings of the sum of squares halve through the root, its reciprocal 2 u, three
+    products: (dh / 2 + 12) u of each element.  The rotation as in rotary's own test, relative to the pair's
+    length r; bf16's rounding last.  Backward, mean(w u x r) sums dh terms more.  A weight's gradient sums
+    n = B L heads terms, each off by as much, with n roundings (of a tree and short runs) at most."""
+    g = _g()
+    q, k = synth.normal(1, 0, (B, L, H, dh), 1.0, dtype), synth.normal(1, 1, (B, L, Hkv, dh), 1.0, dtype)
+    dy = [synth.normal(1, 2 + i, x.shape, 1.0, dtype) for i, x in enumerate((q, k))]
+    wt = [synth.normal(1, 4 + i, (dh,), 0.3, "f32") + 1.0 for i in range(2)]
+    wt = [np.float32(x).astype(np.float64) for x in wt]
+    pos = np.random.default_rng(3).integers(0, 1 << 24, (B, L))
+    pos[0, 0] = (1 << 31) - 1
+    w, gain = dorc.speeds(rot), 1.25
+    args = (dev(wt[0], "f32"), dev(wt[1], "f32"), g.rotary_frequencies(rot))
+    how = dict(positions=ints(pos), interleaved=interleaved, gain=gain, eps=eps)
+    got = g.norm_rotary(dev(q, dtype), dev(k, dtype), *args, **how)
+    back = g.norm_rotary_backward(dev(q, dtype), dev(k, dtype), dev(dy[0], dtype), dev(dy[1], dtype), *args, **how)
+    i1 = np.arange(rot // 2) * 2 if interleaved else np.arange(rot // 2)
+    i2 = i1 + 1 if interleaved else i1 + rot // 2
+    ang = np.sqrt(2) * (np.pi * U / 2 + 6 * U + pos[:, :, None, None] * w * 2.0 ** -51)
+    h = HALF[dtype]
+    for i, (x, what) in enumerate(((q, "q"), (k, "k"))):
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + np.float64(np.float32(eps)))
+
+        def turned(y):  # what the rotation adds to an element's error, and its size
+            size, more = np.abs(y), np.zeros_like(y)
+            pair = np.hypot(y[..., i1], y[..., i2])
+            for at in (i1, i2):
+                more[..., at] = gain * pair * ang
+                size[..., at] = gain * pair
+            return size, more
+        ref = orc.norm_rotary(x, wt[i], pos, w, np.float64(np.float32(eps)), interleaved, gain)
+        size, more = turned(x * r * wt[i])
+        within(host(got[i]), ref, h * np.abs(ref) + (1 + h) * (more + 1.02 * (dh / 2 + 12) * U * size) + 1e-40, what)
+        dref, dw = orc.norm_rotary_backward(x, dy[i], wt[i], pos, w, np.float64(np.float32(eps)), interleaved, gain)
+        usize, umore = turned(dy[i])
+        terms = r * np.abs(wt[i]) * usize
+        dots = r * np.abs(x * r) * (np.abs(wt[i]) * usize * np.abs(x * r)).mean(-1, keepdims=True)
+        e = 1.02 * (2 * dh + 30) * U
+        extra = r * np.abs(wt[i]) * umore + r * np.abs(x * r) * (np.abs(wt[i]) * umore * np.abs(x * r)).mean(-1, keepdims=True)
+        within(host(back[i]), dref, h * np.abs(dref) + (1 + h) * (extra + e * (terms + dots)) + 1e-40, "d" + what)
+        n = B * L * x.shape[2]
+        lim = (np.abs(x * r) * (umore + usize * 1.02 * (dh / 2 + 16 + n) * U)).sum((0, 1, 2))
+        within(host(back[2 + i]), dw, lim + 1e-40, f"d{what}_weight")
+
+
+@pytest.mark.parametrize("dtype,offset", [("bf16", 0), ("bf16", 1), ("f32", 0), ("f32", 1)])
+def test_norm_rotary_views_and_in_place(dtype, offset):
+    """Views of a fused projection (also at odd addresses), a broadcast key head, default and shared
+    positions, no k, and the in-place forms give what contiguous tensors give; what lies around the views
+    stays as it was.  (At an odd address sums run in another order: an ulp of float32, so bf16 may differ by
+    one rounding and float32 by a few u.)"""
+    g = _g()
+    B, L, H, Hkv, dh, rot = 2, 11, 4, 2, 64, 48
+    n = (H + 2 * Hkv) * dh
+    raw = torch.randn(B * L * n + 8, device="cuda").to(TORCH[dtype])
+    qkv = raw[offset:offset + B * L * n].view(B, L, H + 2 * Hkv, dh)
+    q, k = qkv[:, :, :H], qkv[:, :, H:H + Hkv]
+    freq, wt = g.rotary_frequencies(rot), [1 + 0.1 * torch.randn(dh, device="cuda") for _ in range(2)]
+    same = lambda a, b: torch.allclose(a.float(), b.float(), rtol=2 * HALF[dtype] if offset == 1 else 0,  # noqa: E731
+                                       atol=64 * U if offset == 1 else 0)
+    want = g.norm_rotary(q.contiguous(), k.contiguous(), *wt, freq, positions=torch.arange(L, dtype=torch.int32, device="cuda"))
+    got = g.norm_rotary(q, k, *wt, freq)
+    assert same(got[0], want[0]) and same(got[1], want[1])
+    assert same(g.norm_rotary(q, None, wt[0], None, freq)[0], want[0])
+    one = k[:, :, :1].expand(B, L, 3, dh)
+    assert same(g.norm_rotary(q, one, *wt, freq)[1], want[1][:, :, :1].expand(B, L, 3, dh))
+    dy = [torch.randn_like(x) for x in want]
+    grads = g.norm_rotary_backward(q.contiguous(), k.contiguous(), *dy, *wt, freq)
+    mine = [x.clone() for x in dy]
+    again = g.norm_rotary_backward(q.contiguous(), k.contiguous(), *mine, *wt, freq, dq=mine[0], dk=mine[1])
+    assert all(torch.equal(a, b) for a, b in zip(grads, again)) and torch.equal(mine[0], grads[0])
+    alone = g.norm_rotary_backward(q.contiguous(), None, dy[0], None, wt[0], None, freq)
+    assert torch.equal(alone[0], grads[0]) and alone[1] is None and alone[3] is None
+    before = raw.clone()
+    g.norm_rotary(q, k, *wt, freq, q_out=q, k_out=k)
+    assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+    rest = qkv[:, :, H + Hkv:]
+    assert torch.equal(rest, before[offset:offset + B * L * n].view(B, L, -1, dh)[:, :, H + Hkv:])
+    assert torch.equal(raw[:offset], before[:offset]) and torch.equal(raw[offset + B * L * n:], before[offset + B * L * n:])
+
+
+def test_norm_rotary_zero_rows():
+    """A row of zeros: eps keeps it finite, and its gradient too."""
+    g = _g()
+    x = torch.zeros(1, 3, 2, 64, device="cuda").bfloat16()
+    wt, freq = torch.ones(64, device="cuda"), g.rotary_frequencies(64)
+    assert (g.norm_rotary(x, None, wt, None, freq)[0] == 0).all()
+    dq, _, dw, _ = g.norm_rotary_backward(x, None, torch.ones_like(x), None, wt, None, freq)
+    assert torch.isfinite(dq.float()).all() and (dw == 0).all()
+
+
+# ------------------------------------------------------------------ the quantised cache
+def numbers(cache):
+    """Values of the cache's pages in float64, from their bytes."""
+    k, v, ke, ve = cache.numbers()
+    return [x.double().cpu().numpy() * 2.0 ** (e.long().cpu().numpy()[..., None] - 127.0) for x, e in ((k, ke), (v, ve))]
+
+
+def expected(x):
+    y, e = orc.quantise(x)
+    return y * 2.0 ** e[..., None]
+
+
+@pytest.mark.parametrize("heads,dh,dtype", [(12, 64, "bf16"), (1, 32, "f32"), (3, 128, "bf16"), (17, 32, "bf16"), (4, 64, "f32")])
+def test_quantised_append_and_read(heads, dh, dtype):
+    """Appends in pieces, a fork whose shared last page is copied, an accepted path, and what is read back:
+    exactly the numbers of the definition."""
+    g = _g()
+    rng = np.random.default_rng(6)
+    cache = g.QuantisedCache.empty(40, 5, 6, heads, dh)
+    for p in (cache.k_pages, cache.v_pages):
+        p.fill_(0x7f)
+    rows = [[], [], [], [], []]
+    for step, T in enumerate((70, 5, 1, 64)):
+        k, v = (synth.normal(30 + step, s, (3, T, heads, dh), 1.0, dtype) * 2.0 ** rng.integers(-9, 9, (3, T, heads, 1)) for s in (0, 1))
+        k[0, 0, 0] = 0.0
+        counts = rng.integers(0, T + 1, 3)
+        counts[0] = T
+        path = np.stack([np.sort(rng.permutation(T)) for _ in range(3)]) if step == 1 else None
+        cache.append(dev(k, dtype), dev(v, dtype), ints(counts), path=None if path is None else ints(path))
+        for b in range(3):
+            at = list(range(T)) if path is None else path[b]
+            rows[b] += [(k[b, at[t]], v[b, at[t]]) for t in range(counts[b])]
+        if step == 0:
+            cache.fork(ints([0]), ints([3]))
+            rows[3] = list(rows[0])
+    one = synth.normal(40, 0, (1, 3, heads, dh), 1.0, dtype)
+    cache.append(dev(one, dtype), dev(one, dtype), ints([3]), slots=ints([3]))
+    rows[3] += [(one[0, t], one[0, t]) for t in range(3)]
+    cache.check()
+    assert cache.lengths.tolist() == [len(r) for r in rows]
+    pool, table = numbers(cache), cache.table.cpu().numpy()
+    for b, r in enumerate(rows):
+        for t, pair in enumerate(r):
+            for p, x in zip(pool, pair):
+                assert np.array_equal(p[table[b, t // 64], t % 64], expected(x)), (b, t)
+    idx = np.array([[0, 1, -1], [1, 0, 0], [0, 5, 0], [1, -1, 0], [0, 0, 0]])
+    for out in (torch.bfloat16, torch.float32):
+        k, v, local = cache.read(ints(idx), dtype=out)
+        for b in range(5):
+            for e in range(3):
+                held = idx[b, e] >= 0 and table[b, idx[b, e]] >= 0
+                assert int(local[b, e]) == (e if held else -1)
+                n = min(64, max(0, len(rows[b]) - 64 * idx[b, e])) if held else 0
+                for i, x in enumerate((k, v)):
+                    x = host(x[b, 64 * e:64 * e + 64])
+                    assert (x[n:] == 0).all()
+                    for t in range(n):
+                        assert np.array_equal(x[t], expected(rows[b][64 * idx[b, e] + t][i]))
+
+
+def test_quantised_numbers_at_the_edges():
+    """Ties, the largest and smallest numbers, subnormal ones, powers of two and their neighbours, infinities and
+    NaN, in both input types."""
+    g = _g()
+    dh = 64
+    x = np.zeros((8, dh))
+    x[0] = np.linspace(-448, 448, dh)
+    x[1, :8] = [448, 447.9, 432, 416, 208, 1.0625, 1.1875, 2.0 ** -10]
+    x[2, :6] = [449, 2.0 ** -9, 3 * 2.0 ** -10, 2.0 ** -8, 17.0, 19.0]
+    x[3, :4] = [2.0 ** 127, -(2.0 ** 127) * 1.9, 2.0 ** 110, 1.0]
+    x[4, :4] = [2.0 ** -126, 2.0 ** -120, -(2.0 ** -125), 2.0 ** -130]
+    x[5] = 2.0 ** np.linspace(-20, 20, dh)
+    x[6, :4] = [1.0, np.inf, -np.inf, np.nan]
+    for dtype in ("bf16", "f32"):
+        y = x.astype(np.float32)
+        t = torch.from_numpy(y).cuda().to(TORCH[dtype]).view(1, 8, 1, dh)
+        cache = g.QuantisedCache.empty(1, 1, 1, 1, dh)
+        cache.append(t, t, ints([8]))
+        ref = expected(host(t)[0])
+        k, v, _ = cache.read(ints([[0]]), dtype=torch.float32)
+        for out in (k, v, cache.read(ints([[0]]))[0]):
+            assert np.array_equal(host(out)[0, :8], ref, equal_nan=True)
+        assert (host(k)[0, 8:] == 0).all()
+
+
+def test_quantised_append_packed():
+    """Packed prompts into slots in another order: what entry by entry gives; rows around them are not read."""
+    g = _g()
+    lengths, heads, dh = (130, 0, 64, 1, 300), 3, 64
+    off = offsets_of(lengths, 2)
+    k, v = (torch.randn(int(off[-1]) + 3, heads, dh, device="cuda").bfloat16() for _ in range(2))
+    slots = [4, 1, 0, 3, 2]
+    a, b = (g.QuantisedCache.empty(12, 5, 5, heads, dh) for _ in range(2))
+    for c in (a, b):
+        c.k_pages.zero_()
+        c.v_pages.zero_()
+    a.append_packed(k, v, ints(off), slots=ints(slots))
+    for i, n in enumerate(lengths):
+        if n:
+            s = slice(int(off[i]), int(off[i + 1]))
+            b.append(k[None, s], v[None, s], ints([n]), slots=ints([slots[i]]))
+    for x, y in ((a.table, b.table), (a.lengths, b.lengths), (a.refs, b.refs), (a.k_pages, b.k_pages), (a.v_pages, b.v_pages)):
+        assert torch.equal(x, y)
+    a.append_packed(k[:0], v[:0], ints([0, 0]))
+    a.check()
+
+
+@flags
+def test_quantised_refusals_on_the_device():
+    """Offsets out of order, bad slots, chunks out of range and a pool without room are flagged, and nothing of
+    what is refused is written."""
+    g = _g()
+    cache = g.QuantisedCache.empty(4, 2, 3, 1, 64)
+    k = torch.randn(200, 1, 64, device="cuda").bfloat16()
+    state = lambda: [x.clone() for x in (cache.table, cache.lengths, cache.refs)]  # noqa: E731
+    before = state()
+    for off in ([0, 200, 100], [0, 201, 201], [-1, 5, 9], [100, 50, 200]):
+        cache.append_packed(k, k, ints(off))
+        with pytest.raises(g.GCAError) as e:
+            cache.check()
+        assert e.value.status == g.GCA_ERR_DEVICE_INDEX
+        assert all(torch.equal(x, y) for x, y in zip(before, state()))
+    cache.append_packed(k, k, ints([0, 190]), slots=ints([7]))
+    with pytest.raises(g.GCAError):
+        cache.check()
+    cache.append_packed(k, k, ints([0, 190, 200]))  # four pages for 200 tokens: 3 + 1
+    cache.check()
+    cache.append_packed(k, k, ints([0, 100]), slots=ints([1]))
+    with pytest.raises(g.GCAError) as e:
+        cache.check()
+    assert e.value.status == g.GCA_ERR_CACHE_FULL and cache.lengths.tolist() == [190, 10]
+    for idx in ([[0, 3]], [[-2, 0]]):
+        out, _, local = cache.read(ints(idx))
+        with pytest.raises(g.GCAError):
+            cache.check()
+        assert sorted(local[0].tolist()) == sorted([idx[0].index(0), -1])
+        bad = 1 - idx[0].index(0)
+        assert (out[0, 64 * bad:64 * bad + 64] == 0).all()
+    cache.table[0, 0] = 99
+    assert cache.read(ints([[0]]))[2].tolist() == [[-1]]
+    with pytest.raises(g.GCAError):
+        cache.check()
+
+
+def test_quantised_page_operations():
+    """fork, trim, compact and free move quantised rows as they are."""
+    g = _g()
+    cache = g.QuantisedCache.empty(30, 4, 8, 2, 32)
+    x = torch.randn(3, 200, 2, 32, device="cuda").bfloat16()
+    cache.append(x, -x, ints([200, 130, 64]))
+    cache.free(ints([0]))
+    cache.fork(ints([1]), ints([3]))
+    cache.append(x[:1, :10], x[:1, :10], ints([10]), slots=ints([3]))
+    idx = ints([[0, 1, 2], [0, 1, 2], [0, 0, 0], [0, 1, 2]])
+    want = cache.read(idx)
+    live = cache.compact()
+    cache.check()
+    assert int(live[0]) == int((cache.refs > 0).sum()) and int(cache.table.max()) < int(live[0])
+    assert all(torch.equal(a, b) for a, b in zip(want, cache.read(idx)))
+    cache.trim(begin=ints([0, 64, 0, 0]))
+    assert cache.read(ints([[0], [0], [0], [0]]))[2].tolist() == [[-1], [-1], [0], [0]]
+    with pytest.raises(TypeError):
+        cache.store()
+    with pytest.raises(TypeError):
+        cache.attention(None, None, None)
+    cache.check()
