@@ -23,7 +23,7 @@ EXT = os.path.join(BUILD, "_gca_decoding.so")
 SOURCES = ["api.cu", "retrieve.cu", "gca_fwd.cu", "gca_bwd.cu", "scores_bwd.cu", "noalloc.cu", "tmap.cu", "gca_bwd_tc.cu",
            "gather.cu", "block_attn.cu", "window_bwd.cu", "encoder.cu", "retrieve_tc.cu", "rotary.cu", "tree_attn.cu",
            "tree_rows.cu", "tree_tc.cu", "cache.cu", "quantised.cu", "norm_rotary.cu", "prompt_attn.cu",
-           "prompt_tc.cu"]
+           "prompt_tc.cu", "prompt_bwd_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

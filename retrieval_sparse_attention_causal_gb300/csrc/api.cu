@@ -840,8 +840,8 @@ extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gc
   a.dk = dk->data; a.dk_ts = dk->token_stride; a.dk_hs = dk->head_stride;
   a.dv = dv->data; a.dv_ts = dv->token_stride; a.dv_hs = dv->head_stride;
   a.np = prompt_scratch_rows(N, B);
-  a.lse2 = static_cast<float*>(scratch);
-  a.D = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + align256((size_t)a.np * H * sizeof(float)));
+  a.nlse = static_cast<float*>(scratch);
+  a.nD = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + align256((size_t)a.np * H * sizeof(float)));
   cudaError_t e = launch_prompt_backward(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gca_prompt_attention_backward launch");
   return GCA_OK;

@@ -242,7 +242,7 @@ struct PromptArgs {
   void* dq; int64_t dq_ts, dq_hs;
   void* dk; int64_t dk_ts, dk_hs;
   void* dv; int64_t dv_ts, dv_hs;
-  float* lse2; float* D; int64_t np;                       // scratch [H][np]
+  float* nlse; float* nD; int64_t np;                      // scratch [H][np]: -lse log2(e), -D
   ErrWord* err;
 };
 constexpr int kPromptSequences = 1024;
@@ -250,6 +250,7 @@ int64_t prompt_scratch_rows(int64_t N, int B);
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t s);
+cudaError_t launch_prompt_bwd_tc(const PromptArgs& a, cudaStream_t s);
 
 // ---- attention of drafted tokens over a paged cache (tree_attn.cu)
 struct TreeArgs {

@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
   }
 }
 
-// Row sums D = <do, o> and the log-sum-exps times log2(e), a head's rows side by side: [H][np] each.
+// What both sides of the backward pass need of a row, negative as they add it: D = <do, o>, and the
+// log-sum-exp times log2(e); a head's rows side by side, [H][np] each.
 
 template <typename T>
 __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
       for (int i = 0; i < V; ++i) d += x[i] * y[i];
     }
     const int64_t to = h * a.np + prompt_pad(off, lo) + row - off;
-    a.D[to] = d;
-    a.lse2[to] = a.lse[row * a.H + h] * kLog2e;
+    a.nD[to] = -d;
+    a.nlse[to] = -a.lse[row * a.H + h] * kLog2e;
   }
 }
 
@@ -246,13 +247,13 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) 
   load_tile<T, DH>(G, reinterpret_cast<const T*>(a.dout) + (int64_t)(x.off + t0) * a.do_ts + h * a.do_hs, a.do_ts, x.len - t0);
   const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
   const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
-  float dq[4][C::CV] = {}, lse[4], D[4];
+  float dq[4][C::CV] = {}, nl[4], nd[4];
   const int64_t rows = h * a.np + prompt_pad(x.off, x.b) + t0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool on = t0 + ty + 16 * i < x.len;
-    lse[i] = on ? a.lse2[rows + ty + 16 * i] : CUDART_INF_F;  // rows that do not exist weigh nothing
-    D[i] = on ? a.D[rows + ty + 16 * i] : 0.f;
+    nl[i] = on ? a.nlse[rows + ty + 16 * i] : -CUDART_INF_F;  // rows that do not exist weigh nothing
+    nd[i] = on ? a.nD[rows + ty + 16 * i] : 0.f;
   }
   const float sl2 = a.scale * kLog2e;
   for (int j = first_keys(a, t0); j <= x.tile; ++j) {
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) 
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const bool on = sees(a, t0 + ty + 16 * i, j * kT + tx + 16 * c);
-        S[(ty + 16 * i) * C::LP + tx + 16 * c] = on ? exp2f(s[i][c] * sl2 - lse[i]) * (dp[i][c] - D[i]) : 0.f;
+        S[(ty + 16 * i) * C::LP + tx + 16 * c] = on ? exp2f(s[i][c] * sl2 + nl[i]) * (dp[i][c] + nd[i]) : 0.f;
       }
     __syncthreads();
     weighted<DH>(S, K, dq);
@@ -313,13 +314,13 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_simt_kernel(PromptArgs a)
       for (int c = 0; c < 4; ++c) {
         const int t = i * kT + tx + 16 * c;
         const bool row = t < x.len;
-        const float lse = row ? a.lse2[rows + t] : 0.f, D = row ? a.D[rows + t] : 0.f;
+        const float nl = row ? a.nlse[rows + t] : 0.f, nd = row ? a.nD[rows + t] : 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const bool on = row && sees(a, t, k0 + ty + 16 * e);
-          const float p = on ? exp2f(s[e][c] * sl2 - lse) : 0.f;
+          const float p = on ? exp2f(s[e][c] * sl2 + nl) : 0.f;
           P[(ty + 16 * e) * C::LP + tx + 16 * c] = p;
-          S[(ty + 16 * e) * C::LP + tx + 16 * c] = on ? p * (dp[e][c] - D) : 0.f;
+          S[(ty + 16 * e) * C::LP + tx + 16 * c] = on ? p * (dp[e][c] + nd) : 0.f;
         }
       }
       __syncthreads();
@@ -387,10 +388,7 @@ cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s) {
   else prompt_rows_kernel<float><<<grid, 256, 0, s>>>(a);
   cudaError_t e = launch_end("prompt_rows", s);
   if (e != cudaSuccess) return e;
-  if (a.bf16) {
-    using T = __nv_bfloat16;
-    return a.dh == 32 ? backward_simt<T, 32>(a, s) : a.dh == 64 ? backward_simt<T, 64>(a, s) : backward_simt<T, 128>(a, s);
-  }
+  if (a.bf16) return launch_prompt_bwd_tc(a, s);
   return a.dh == 32 ? backward_simt<float, 32>(a, s) : a.dh == 64 ? backward_simt<float, 64>(a, s) : backward_simt<float, 128>(a, s);
 }
 
