@@ -63,6 +63,12 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int rank, bool 
   return false;
 }
 
+// The work item of a persistent CTA's turn n: every other turn the CTAs take theirs in the opposite order, so that
+// the same ones do not always get the larger (in order, 1024 items over 152 CTAs left a CTA 13 % over the mean).
+__device__ __forceinline__ int prompt_turn(int n) {
+  return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 // Where the rows of sequence b begin in the backward pass's scratch rows: on 16-byte boundaries.
 __device__ __forceinline__ int64_t prompt_pad(int off, int b) { return (int64_t)(off & ~3) + 4 * b; }
 

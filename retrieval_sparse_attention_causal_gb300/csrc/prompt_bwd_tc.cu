@@ -4,17 +4,21 @@
 // 128 rows sees, the keys' side (dK, dV) the rows that see a tile of 128 keys, of all heads that share it.
 // Each computes the logits and <dO, V> anew: 3 and 4 products of 128 x 128 x dh a pair of tiles, 7 where
 // the gradients themselves need 5.  Both are persistent, a CTA an SM: one warp loads, one issues the
-// products, eight warps do the arithmetic, a row (TMEM lane) and 64 columns a thread.
-//   * Queries' side: S = Q K^T and dP = dO V^T of the next block are issued as soon as this one's are in
-//     registers; dS goes to one of two buffers as the A operand of dQ += dS K.
-//   * Keys' side: S^T = K Q^T, dP^T = V dO^T; P^T and dS^T take the columns that they came from as the A
-//     operands of dV += P^T dO and dK += dS^T Q.  The products go in the order dV(x), S^T(x + 1), dK(x),
+// products, sixteen do the arithmetic, 32 columns of 32 rows (TMEM
+// lanes) each: with eight warps of 64 columns the chain of a block (loads from TMEM, exponentials, stores, a
+// barrier) was longer than its products.
+//   * Queries' side: S = Q K^T of the next block is issued as soon as this one's is in registers, and so
+//     is dP = dO V^T; dS goes to one of two buffers as the A operand of dQ += dS K.
+//   * Keys' side: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q, with P^T and dS^T as A operands
+//     in TMEM.  At dh 64 they have columns of their own, and S^T and dP^T run ahead as above.  At dh 128
+//     they take the columns that they came from: the products go in the order dV(x), S^T(x + 1), dK(x),
 //     dP^T(x + 1), so each follows only the one that read the columns it overwrites, and the weights of
 //     x + 1 are computed while dK(x) and dP^T(x + 1) run.
 // P and dS are rounded to bf16, the type of the products' other operands (half a step, 2^-8 of each).
 // Rows behind a sequence's end may hold anything: as operands that are summed over they become zeros in
 // shared memory, elsewhere their results are not used.
 #include <algorithm>
+#include <type_traits>
 
 #include "prompt.cuh"
 #include "tc.cuh"
@@ -26,13 +30,13 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kT = 128;             // rows, and keys, of a tile
-constexpr int kElem = 8;            // warps that do the arithmetic
+constexpr int kElem = 16;           // warps that do the arithmetic: four of each 32 rows, 32 columns a warp
 constexpr int kThreads = 32 * (kElem + 2);
 constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteP, kSiteTaken, kSiteDs, kSiteAcc, kSiteAccFree, kSiteRows };
+enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDv, kSiteAcc, kSiteAccFree, kSiteRows };
 
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
   return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
@@ -52,7 +56,10 @@ template <int DH>
 struct Shared {
   uint64_t full[Tc<DH>::NS], empty[Tc<DH>::NS];  // stages
   uint64_t tile[2], tile_free[2];                // the tile that stays
-  uint64_t s, dp, p, ds, acc, acc_free;
+  uint64_t s, dp;                                // products that are there: S and dP (or their transposes)
+  uint64_t s_taken, dp_taken;                    // ... that are in registers
+  uint64_t p, ds, dv;                            // P and dS in TMEM; P's product done
+  uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
 };
@@ -70,8 +77,11 @@ __device__ __forceinline__ void set_up(Shared<DH>& sh) {
     }
     tc::mbar_init(&sh.s, 1);
     tc::mbar_init(&sh.dp, 1);
+    tc::mbar_init(&sh.s_taken, kElem);
+    tc::mbar_init(&sh.dp_taken, kElem);
     tc::mbar_init(&sh.p, kElem);
     tc::mbar_init(&sh.ds, kElem);
+    tc::mbar_init(&sh.dv, 1);
     tc::mbar_init(&sh.acc, 1);
     tc::mbar_init(&sh.acc_free, kElem);
     sh.abort = 0;
@@ -100,24 +110,27 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b) {
   for (int s = 0; s < Tc<DH>::SUB; ++s)
     tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(d, tc::desc_km(a + s * kTile), tc::desc_km(b + s * kTile), tc::idesc_bf16(kT, kT, false), s ? 1u : 0u);
 }
-// D[128 x DH] (+)= A B with A [128 x 128] in TMEM (64 columns at a0, 64 at a1) and B [128 x DH] in shared memory.
-template <int DH>
-__device__ __forceinline__ void accumulate(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool add) {
+// D[128 x DH] (+)= A B with A [128 x 128] in TMEM and B [128 x DH] in shared memory.  A's columns lie side by side
+// (GAP 0), or each 16 of them in front of GAP others.
+template <int DH, int GAP>
+__device__ __forceinline__ void accumulate(uint32_t d, uint32_t at, uint32_t b, bool add) {
 #pragma unroll
   for (int s = 0; s < Tc<DH>::SUB; ++s) {
-    tc::mma4_ts<8, 16, 24, tc::kKStepMn>(d + 64 * s, a0, tc::desc_mn(b + s * kTile), tc::idesc_bf16(kT, 64, true), add ? 1u : 0u);
-    tc::mma4_ts<8, 16, 24, tc::kKStepMn>(d + 64 * s, a1, tc::desc_mn(b + s * kTile + kTile / 2), tc::idesc_bf16(kT, 64, true), 1u);
+    tc::mma4_ts<8, 16 + GAP, 24 + GAP, tc::kKStepMn>(d + 64 * s, at, tc::desc_mn(b + s * kTile), tc::idesc_bf16(kT, 64, true), add ? 1u : 0u);
+    tc::mma4_ts<8, 16 + GAP, 24 + GAP, tc::kKStepMn>(d + 64 * s, at + 32 + 2 * GAP, tc::desc_mn(b + s * kTile + kTile / 2), tc::idesc_bf16(kT, 64, true), 1u);
   }
 }
 
-// 32 columns of an accumulator's row, scaled, to global memory.
+// W columns of an accumulator's row, scaled, to global memory.
+template <int W>
 __device__ __forceinline__ void write_row(uint32_t at, bf16* to, float scale, bool on) {
-  float o[32];
-  tc::ld32x32b_x32(at, o);
+  float o[W];
+  if constexpr (W == 32) tc::ld32x32b_x32(at, o);
+  else tc::ld32x32b_x16(at, o);
   tc::ld_wait_row(o);
   if (!on) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < W / 8; ++i)
     *reinterpret_cast<uint4*>(to + 8 * i) =
         make_uint4(pack_bf16(o[8 * i] * scale, o[8 * i + 1] * scale), pack_bf16(o[8 * i + 2] * scale, o[8 * i + 3] * scale),
                    pack_bf16(o[8 * i + 4] * scale, o[8 * i + 5] * scale), pack_bf16(o[8 * i + 6] * scale, o[8 * i + 7] * scale));
@@ -162,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   if (warp == kElem + 1) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    for (int w = blockIdx.x; ok && q_item(a, w, it); w += gridDim.x, ++nt) {
+    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
       const int buf = nt % NB;
-      ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, w);
+      ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, nt);
       if (!ok) break;
       tc::mbar_expect_tx_warp(&sh.tile[buf], 2 * C::BLOCK);
 #pragma unroll
@@ -193,22 +206,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   } else if (warp == kElem) {
     // ---------------------------------------------------------------- products
     int id = 0, nt = 0;
-    for (int w = blockIdx.x; ok && q_item(a, w, it); w += gridDim.x, ++nt) {
+    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
       const int n = it.x.tile - it.lo + 1;
       const uint32_t q = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), g = q + C::BLOCK;
-      ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, w);
-      // Step x: S and dP of block x, and dQ of the block before.
+      ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
+      // Step x: S and dP of block x, each once that of the block before is in registers, and dQ of the block before.
       for (int x = 0; x <= n && ok; ++x) {
         if (x < n) {
           const int i = id + x, st = i % NS;
           ok = waited(&sh.full[st], (i / NS) & 1, kSiteFull, x);
-          if (i > 0) ok = ok && waited(&sh.p, (i - 1) & 1, kSiteTaken, x);  // the block before is in registers
+          if (i > 0) ok = ok && waited(&sh.s_taken, (i - 1) & 1, kSiteTaken, x);
           if (!ok) break;
           tc::fence_after();
           const uint32_t k = tc::su32(ring + st * 2 * C::BLOCK);
           product<DH>(tS, q, k);
-          product<DH>(tP, g, k + C::BLOCK);
           tc::commit_warp(&sh.s);
+          if (i > 0) ok = waited(&sh.dp_taken, (i - 1) & 1, kSiteTaken, x);
+          if (!ok) break;
+          tc::fence_after();
+          product<DH>(tP, g, k + C::BLOCK);
+          tc::commit_warp(&sh.dp);
           if (x == n - 1) tc::commit_warp(&sh.tile_free[nt % NB]);
         }
         if (x > 0) {
@@ -217,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
           ok = ok && waited(&sh.ds, i & 1, kSiteDs, x);
           if (!ok) break;
           tc::fence_after();
-          accumulate<DH>(tQ, tD + 64 * (i & 1), tD + 64 * (i & 1) + 32, tc::su32(ring + st * 2 * C::BLOCK), x > 1);
+          accumulate<DH, 0>(tQ, tD + 64 * (i & 1), tc::su32(ring + st * 2 * C::BLOCK), x > 1);
           tc::commit_warp(&sh.empty[st]);
         }
       }
@@ -227,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
     }
   } else {
     // ---------------------------------------------------------------- arithmetic
-    const int r = 32 * (warp & 3) + lane, half = warp >> 2;  // row of the tile; columns 64 half ..
+    const int r = 32 * (warp & 3) + lane, part = warp >> 2;  // row of the tile; columns 32 part ..
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
     int id = 0, nt = 0;
-    for (int w = blockIdx.x; ok && q_item(a, w, it); w += gridDim.x, ++nt) {
+    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
       const int pos = it.x.tile * kT + r;
       const bool on = pos < it.x.len;
       const int64_t row = it.h * a.np + prompt_pad(it.x.off, it.x.b) + pos;
@@ -244,70 +261,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
         ok = waited(&sh.s, id & 1, kSiteS, n);
         if (!ok) break;
         tc::fence_after();
-        float s[2][32], dp[2][32];
-        tc::ld32x32b_x32(tS + lanes + 64 * half, s[0]);
-        tc::ld32x32b_x32(tS + lanes + 64 * half + 32, s[1]);
-        tc::ld32x32b_x32(tP + lanes + 64 * half, dp[0]);
-        tc::ld32x32b_x32(tP + lanes + 64 * half + 32, dp[1]);
-        tc::ld_wait_row(s[0]);
-        tc::ld_wait_row(s[1]);
-        tc::ld_wait_row(dp[0]);
-        tc::ld_wait_row(dp[1]);
+        float s[32], dp[32];
+        tc::ld32x32b_x32(tS + lanes + 32 * part, s);
+        tc::ld_wait_row(s);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.p);
-        uint32_t d[32];
+        if (lane == 0) tc::mbar_arrive(&sh.s_taken);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int i = 0; i < 16; ++i) {
+          float x, y;
+          tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, nl2), x, y);
+          s[2 * i] = tc::ex2(x);
+          s[2 * i + 1] = tc::ex2(y);
+        }
+        ok = waited(&sh.dp, id & 1, kSiteDp, n);
+        if (!ok) break;
+        tc::fence_after();
+        tc::ld32x32b_x32(tP + lanes + 32 * part, dp);
+        tc::ld_wait_row(dp);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.dp_taken);
+        uint32_t d[16];
+        auto weigh = [&](auto edge, int c0, int c1) {  // at an edge: of the part's keys c0 .. c1 - 1 are seen
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x, y;
-            tc::uf2(tc::fma2(tc::f2(s[c][2 * i], s[c][2 * i + 1]), k2, nl2), x, y);
-            const uint64_t p = tc::f2(tc::ex2(x), tc::ex2(y));
-            tc::uf2(tc::mul2(p, tc::add2(tc::f2(dp[c][2 * i], dp[c][2 * i + 1]), nd2)), x, y);
-            s[c][2 * i] = x;
-            s[c][2 * i + 1] = y;
+            tc::uf2(tc::mul2(tc::f2(s[2 * i], s[2 * i + 1]), tc::add2(tc::f2(dp[2 * i], dp[2 * i + 1]), nd2)), x, y);
+            if constexpr (decltype(edge)::value) {
+              if (2 * i < c0 || 2 * i >= c1) x = 0.f;
+              if (2 * i + 1 < c0 || 2 * i + 1 >= c1) y = 0.f;
+            }
+            d[i] = pack_bf16(x, y);
           }
-        if (n == it.x.tile || n < whole) {  // keys that the row does not see, and rows that do not exist
-          const int c0 = first - n * kT - 64 * half, c1 = on ? pos - n * kT - 64 * half + 1 : 0;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i < c0 || 32 * c + i >= c1) s[c][i] = 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) d[16 * c + i] = pack_bf16(s[c][2 * i], s[c][2 * i + 1]);
+        };
+        if (n == it.x.tile || n < whole)  // keys that the row does not see, and rows that do not exist
+          weigh(std::true_type{}, first - n * kT - 32 * part, on ? pos - n * kT - 32 * part + 1 : 0);
+        else weigh(std::false_type{}, 0, 32);
         if ((n + 1) * kT > it.x.len) {  // rows of K behind the sequence
           ok = waited(&sh.full[id % NS], (id / NS) & 1, kSiteRows, n);
           if (!ok) break;
-          if (half == 0) blank<DH>(ring + (id % NS) * 2 * C::BLOCK, r, it.x.len - n * kT);
+          if (part == 0) blank<DH>(ring + (id % NS) * 2 * C::BLOCK, r, it.x.len - n * kT);
           tc::fence_async_smem();
         }
-        // The buffer's last reader, dQ of two blocks ago, was issued before S(n) and is done.
-        const uint32_t to = tD + lanes + 64 * (id & 1) + 32 * half;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x[8] = {d[8 * i], d[8 * i + 1], d[8 * i + 2], d[8 * i + 3], d[8 * i + 4], d[8 * i + 5], d[8 * i + 6], d[8 * i + 7]};
-          tc::st32x32b_x8(to + 8 * i, x);
-        }
+        // The buffer's last reader, dQ of two blocks ago, was issued before dP(n) and is done.
+        const uint32_t to = tD + lanes + 64 * (id & 1) + 16 * part;
+        const uint32_t d0[8] = {d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7]}, d1[8] = {d[8], d[9], d[10], d[11], d[12], d[13], d[14], d[15]};
+        tc::st32x32b_x8(to, d0);
+        tc::st32x32b_x8(to + 8, d1);
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.ds);
       }
       if (!ok) break;
-      ok = waited(&sh.acc, nt & 1, kSiteAcc, w);
+      ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
       if (!ok) break;
       tc::fence_after();
+      const int col = part * (DH / 4);
       bf16* to = reinterpret_cast<bf16*>(a.dq) + (int64_t)(it.x.off + pos) * a.dq_ts + it.h * a.dq_hs;
-#pragma unroll
-      for (int c = 0; c < DH / 64; ++c) {
-        const int col = half * (DH / 2) + 32 * c;
-        if (col < a.dh) write_row(tQ + lanes + col, to + col, a.scale, on);
-      }
+      if (col < a.dh) write_row<DH / 4>(tQ + lanes + col, to + col, a.scale, on);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.acc_free);
@@ -347,7 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   __shared__ __align__(8) Shared<DH> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   set_up<DH>(sh);
-  const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
+  // Where TMEM has room (dh 64), P^T and dS^T have columns of their own, and S^T and dP^T of the next block are issued
+  // once this one's are in registers; else they lie in S^T's and dP^T's columns.
+  constexpr bool OWN = DH == 64;
+  constexpr int GAP = OWN ? 0 : 16;
+  const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH, tPt = OWN ? tK + DH : tS, tDt = OWN ? tPt + 64 : tP;
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
@@ -358,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   if (warp == kElem + 1) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    for (int w = blockIdx.x; ok && kv_item(a, w, it); w += gridDim.x, ++nt) {
+    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
       const int buf = nt % NB;
-      ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, w);
+      ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, nt);
       if (!ok) break;
       tc::mbar_expect_tx_warp(&sh.tile[buf], 2 * C::BLOCK);
 #pragma unroll
@@ -396,37 +413,54 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   } else if (warp == kElem) {
     // ---------------------------------------------------------------- products
     int id = 0, nt = 0;
-    for (int w = blockIdx.x; ok && kv_item(a, w, it); w += gridDim.x, ++nt) {
+    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
       const int n = (it.end - it.x.tile) * a.g;
       const uint32_t k = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), v = k + C::BLOCK;
-      ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, w);
+      ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
       for (int x = -1; x < n && ok; ++x) {
         const int i = id + x, st = i % NS, next = (i + 1) % NS;
         const uint32_t q = tc::su32(ring + st * 2 * C::BLOCK), qn = tc::su32(ring + next * 2 * C::BLOCK);
-        if (x >= 0) {
-          if (x == 0) ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, x);
+        const bool more = x + 1 < n;
+        auto weights = [&]() {  // dV += P^T dO
+          if (x == 0) ok = ok && waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, x);
           ok = ok && waited(&sh.p, i & 1, kSiteP, x);
-          if (!ok) break;
+          if (!ok) return;
           tc::fence_after();
-          accumulate<DH>(tV, tS, tS + 64, q + C::BLOCK, x > 0);
-        }
-        if (x + 1 < n) {
-          ok = waited(&sh.full[next], ((i + 1) / NS) & 1, kSiteFull, x);
-          if (!ok) break;
+          accumulate<DH, GAP>(tV, tPt, q + C::BLOCK, x > 0);
+          if (OWN) tc::commit_warp(&sh.dv);
+        };
+        auto logits = [&]() {  // S^T of the next block
+          ok = ok && waited(&sh.full[next], ((i + 1) / NS) & 1, kSiteFull, x);
+          if (OWN && i >= 0) ok = ok && waited(&sh.s_taken, i & 1, kSiteTaken, x);
+          if (!ok) return;
           tc::fence_after();
           product<DH>(tS, k, qn);
           tc::commit_warp(&sh.s);
-        }
-        if (x >= 0) {
-          ok = waited(&sh.ds, i & 1, kSiteDs, x);
-          if (!ok) break;
+        };
+        auto gradients = [&]() {  // dK += dS^T Q
+          ok = ok && waited(&sh.ds, i & 1, kSiteDs, x);
+          if (!ok) return;
           tc::fence_after();
-          accumulate<DH>(tK, tP, tP + 64, q, x > 0);
+          accumulate<DH, GAP>(tK, tDt, q, x > 0);
           tc::commit_warp(&sh.empty[st]);
-        }
-        if (x + 1 < n) {
+        };
+        auto outputs = [&]() {  // dP^T of the next block
+          if (OWN && i >= 0) ok = ok && waited(&sh.dp_taken, i & 1, kSiteTaken, x);
+          if (!ok) return;
+          tc::fence_after();
           product<DH>(tP, v, qn + C::BLOCK);
           tc::commit_warp(&sh.dp);
+        };
+        if constexpr (OWN) {
+          if (more) logits();
+          if (x >= 0) weights();
+          if (more) outputs();
+          if (x >= 0) gradients();
+        } else {
+          if (x >= 0) weights();
+          if (more) logits();
+          if (x >= 0) gradients();
+          if (more) outputs();
         }
       }
       if (!ok) break;
@@ -436,120 +470,137 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
     }
   } else {
     // ---------------------------------------------------------------- arithmetic
-    const int r = 32 * (warp & 3) + lane, half = warp >> 2;  // key of the tile; rows 64 half .. of a block
+    // A warp's 32 keys (lanes) and 32 rows (columns 32 part ..) in fragments: of each 16 keys and 8 rows a thread has
+    // keys lane / 4 and lane / 4 + 8 and rows 2 (lane % 4) and the next.  So it needs eight rows' sums, not all 32:
+    // in whole rows a thread their loads from shared memory (four wavefronts a vector, broadcast or not) took longer
+    // than the operands of the products.
+    const int part = warp >> 2, group = lane >> 2, two = 2 * (lane & 3);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
     int id = 0, nt = 0;
-    for (int w = blockIdx.x; ok && kv_item(a, w, it); w += gridDim.x, ++nt) {
-      const int key = it.x.tile * kT + r;
+    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
+      const int key0 = it.x.tile * kT + 32 * (warp & 3) + group;  // keys key0 + 0, 8, 16, 24
       for (int h = 0; h < a.g && ok; ++h)
         for (int i = it.x.tile; i < it.end; ++i, ++id) {
-          const int st = id % NS, t0 = i * kT + 64 * half;
+          const int st = id % NS, t0 = i * kT + 32 * part + two;  // rows t0 + 8 n, and the next
           ok = waited(&sh.full[st], (id / NS) & 1, kSiteRows, i) && waited(&sh.s, id & 1, kSiteS, i);
           if (!ok) break;
           tc::fence_after();
-          // Rows c0 .. c1 - 1 of this half see the key; every row sees every key of blocks inside.
+          // Every row sees every key of blocks inside.
           const bool edge = i == it.x.tile || (i + 1) * kT > it.x.len || (a.window && i * kT + kT - a.window > it.x.tile * kT);
-          int c0 = 0, c1 = 64;
-          if (edge) {
-            c0 = key - t0;
-            c1 = it.x.len - t0;
-            if (a.window) c1 = (int)min((int64_t)c1, (int64_t)key + a.window - t0);
-          }
-          float p[2][32];
-          tc::ld32x32b_x32(tS + lanes + 64 * half, p[0]);
-          tc::ld32x32b_x32(tS + lanes + 64 * half + 32, p[1]);
-          if ((i + 1) * kT > it.x.len) {  // rows of Q and dO behind the sequence
-            blank<DH>(ring + st * 2 * C::BLOCK + half * C::BLOCK, r, it.x.len - i * kT);
+          auto seen = [&](int t, int key) { return t >= key && t < it.x.len && (a.window == 0 || t - key < a.window); };
+          float p[2][4][4];
+          tc::ld16x256_x4(tS + lanes + 32 * part, p[0]);
+          tc::ld16x256_x4(tS + lanes + (16u << 16) + 32 * part, p[1]);
+          if (part < 2 && (i + 1) * kT > it.x.len) {  // rows of Q and dO behind the sequence
+            blank<DH>(ring + st * 2 * C::BLOCK + part * C::BLOCK, 32 * (warp & 3) + lane, it.x.len - i * kT);
             tc::fence_async_smem();
           }
-          const float4* nl = reinterpret_cast<const float4*>(rows + st * 2 * kT + 64 * half);
-          const float4* nd = nl + kT / 4;
-          tc::ld_wait_row(p[0]);
-          tc::ld_wait_row(p[1]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 l = nl[8 * c + j];
-              float x, y, z, u;
-              tc::uf2(tc::fma2(tc::f2(p[c][4 * j], p[c][4 * j + 1]), k2, tc::f2(l.x, l.y)), x, y);
-              tc::uf2(tc::fma2(tc::f2(p[c][4 * j + 2], p[c][4 * j + 3]), k2, tc::f2(l.z, l.w)), z, u);
-              p[c][4 * j] = tc::ex2(x);
-              p[c][4 * j + 1] = tc::ex2(y);
-              p[c][4 * j + 2] = tc::ex2(z);
-              p[c][4 * j + 3] = tc::ex2(u);
-            }
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (32 * c + j < c0 || 32 * c + j >= c1) p[c][j] = 0.f;
+          const float* nl = rows + st * 2 * kT + 32 * part + two;
+          const float* nd = nl + kT;
+          tc::ld_wait(p[0]);
+          tc::ld_wait(p[1]);
+          if constexpr (OWN) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.s_taken);
           }
+          uint32_t x[2][8];
+          auto weigh = [&](auto at_edge) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+            for (int n = 0; n < 4; ++n) {
+              const uint64_t l = *reinterpret_cast<const uint64_t*>(nl + 8 * n);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t x[8];
+              for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = pack_bf16(p[c][16 * j + 2 * e], p[c][16 * j + 2 * e + 1]);
-              tc::st32x32b_x8(tS + lanes + 64 * half + 16 * c + 8 * j, x);
+                for (int u = 0; u < 2; ++u) {
+                  float e, f;
+                  tc::uf2(tc::fma2(tc::f2(p[k][n][2 * u], p[k][n][2 * u + 1]), k2, l), e, f);
+                  e = tc::ex2(e);
+                  f = tc::ex2(f);
+                  if constexpr (decltype(at_edge)::value) {
+                    const int key = key0 + 16 * k + 8 * u;
+                    if (!seen(t0 + 8 * n, key)) e = 0.f;
+                    if (!seen(t0 + 8 * n + 1, key)) f = 0.f;
+                  }
+                  p[k][n][2 * u] = e;
+                  p[k][n][2 * u + 1] = f;
+                  x[k][2 * n + u] = pack_bf16(e, f);
+                }
             }
+          };
+          if (edge) weigh(std::true_type{});
+          else weigh(std::false_type{});
+          if (OWN && id > 0) {  // P^T's columns have been read
+            ok = waited(&sh.dv, (id - 1) & 1, kSiteDv, i);
+            if (!ok) break;
+            tc::fence_after();
+          }
+          const uint32_t at = (16 + GAP) * part;  // of the A operand
+          tc::st16x128_x4(tPt + lanes + at, x[0]);
+          tc::st16x128_x4(tPt + lanes + (16u << 16) + at, x[1]);
           tc::st_wait();
           tc::fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh.p);
-          ok = waited(&sh.dp, id & 1, kSiteDs, i);
+          ok = waited(&sh.dp, id & 1, kSiteDp, i);
           if (!ok) break;
           tc::fence_after();
-          float d[2][32];
-          tc::ld32x32b_x32(tP + lanes + 64 * half, d[0]);
-          tc::ld_wait_row(d[0]);
-          tc::ld32x32b_x32(tP + lanes + 64 * half + 32, d[1]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c == 1) tc::ld_wait_row(d[1]);
-            uint32_t x[16];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 l = nd[8 * c + j];
-              float e0, e1, e2, e3;
-              tc::uf2(tc::mul2(tc::f2(p[c][4 * j], p[c][4 * j + 1]), tc::add2(tc::f2(d[c][4 * j], d[c][4 * j + 1]), tc::f2(l.x, l.y))), e0, e1);
-              tc::uf2(tc::mul2(tc::f2(p[c][4 * j + 2], p[c][4 * j + 3]), tc::add2(tc::f2(d[c][4 * j + 2], d[c][4 * j + 3]), tc::f2(l.z, l.w))), e2, e3);
-              if (edge) {  // (what is not seen may be anything, an infinity times 0 too)
-                const int at = 32 * c + 4 * j;
-                if (at < c0 || at >= c1) e0 = 0.f;
-                if (at + 1 < c0 || at + 1 >= c1) e1 = 0.f;
-                if (at + 2 < c0 || at + 2 >= c1) e2 = 0.f;
-                if (at + 3 < c0 || at + 3 >= c1) e3 = 0.f;
-              }
-              x[2 * j] = pack_bf16(e0, e1);
-              x[2 * j + 1] = pack_bf16(e2, e3);
-            }
-            const uint32_t x0[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, x1[8] = {x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]};
-            tc::st32x32b_x8(tP + lanes + 64 * half + 16 * c, x0);  // over columns that have been read
-            tc::st32x32b_x8(tP + lanes + 64 * half + 16 * c + 8, x1);
+          float d[2][4][4];
+          tc::ld16x256_x4(tP + lanes + 32 * part, d[0]);
+          tc::ld16x256_x4(tP + lanes + (16u << 16) + 32 * part, d[1]);
+          tc::ld_wait(d[0]);
+          tc::ld_wait(d[1]);
+          if constexpr (OWN) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.dp_taken);
           }
+          auto differ = [&](auto at_edge) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint64_t l = *reinterpret_cast<const uint64_t*>(nd + 8 * n);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  float e, f;
+                  tc::uf2(tc::mul2(tc::f2(p[k][n][2 * u], p[k][n][2 * u + 1]), tc::add2(tc::f2(d[k][n][2 * u], d[k][n][2 * u + 1]), l)), e, f);
+                  if constexpr (decltype(at_edge)::value) {  // (what is not seen may be anything, an infinity times 0 too)
+                    const int key = key0 + 16 * k + 8 * u;
+                    if (!seen(t0 + 8 * n, key)) e = 0.f;
+                    if (!seen(t0 + 8 * n + 1, key)) f = 0.f;
+                  }
+                  x[k][2 * n + u] = pack_bf16(e, f);
+                }
+            }
+          };
+          if (edge) differ(std::true_type{});
+          else differ(std::false_type{});
+          if (OWN && id > 0) {  // dS^T's columns have been read: the block before has given its stage back
+            ok = waited(&sh.empty[(id - 1) % NS], ((id - 1) / NS) & 1, kSiteDs, i);
+            if (!ok) break;
+            tc::fence_after();
+          }
+          tc::st16x128_x4(tDt + lanes + at, x[0]);
+          tc::st16x128_x4(tDt + lanes + (16u << 16) + at, x[1]);
           tc::st_wait();
           tc::fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh.ds);
         }
       if (!ok) break;
-      ok = waited(&sh.acc, nt & 1, kSiteAcc, w);
+      ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
       if (!ok) break;
       tc::fence_after();
+      const int key = it.x.tile * kT + 32 * (warp & 3) + lane, col = part * (DH / 4);
       const bool on = key < it.x.len;
       bf16* kt = reinterpret_cast<bf16*>(a.dk) + (int64_t)(it.x.off + key) * a.dk_ts + it.m * a.dk_hs;
       bf16* vt = reinterpret_cast<bf16*>(a.dv) + (int64_t)(it.x.off + key) * a.dv_ts + it.m * a.dv_hs;
-#pragma unroll
-      for (int c = 0; c < DH / 64; ++c) {
-        const int col = half * (DH / 2) + 32 * c;
-        if (col >= a.dh) break;
-        write_row(tV + lanes + col, vt + col, 1.f, on);
-        write_row(tK + lanes + col, kt + col, a.scale, on);
+      if (col < a.dh) {
+        write_row<DH / 4>(tV + lanes + col, vt + col, 1.f, on);
+        write_row<DH / 4>(tK + lanes + col, kt + col, a.scale, on);
       }
       tc::fence_before();
       __syncwarp();

@@ -137,10 +137,10 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
     int nq[2] = {0, 0};      // tiles of rows so far
-    for (int w = blockIdx.x; ok && item_of(a, w, it); w += gridDim.x) {
+    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
       auto rows = [&](int t) {
         if (it.hi[t] < it.lo[t]) return;
-        ok = ok && waited(&bar_qfree[t], (nq[t] & 1) ^ 1, kSiteQFree, w);
+        ok = ok && waited(&bar_qfree[t], (nq[t] & 1) ^ 1, kSiteQFree, turn);
         if (!ok) return;
         tc::mbar_expect_tx_warp(&bar_q[t], C::BLOCK);
 #pragma unroll
@@ -185,7 +185,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     };
     int nq[2] = {0, 0}, nb[2] = {0, 0};  // tiles of rows and blocks so far
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
-    for (int w = blockIdx.x; ok && item_of(a, w, it); w += gridDim.x) {
+    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
       const int top = it.top(), low = it.low();
       auto has = [&](int t, int n) { return n <= it.hi[t] && n >= it.lo[t]; };
       // Step n: P V of block n + 1 (the one before), and the logits of block n, tile by tile.
@@ -245,7 +245,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + kT * t + lanes, tO = tmem + 2 * kT + DH * t + lanes;
     int nb = 0, no = 0, slot = 0;            // blocks and tiles so far, ring slots before the item
-    for (int w = blockIdx.x; ok && item_of(a, w, it); w += gridDim.x) {
+    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
       const int hi = it.hi[t], lo = it.lo[t], top = it.top();
       const int pos = it.tile[t] * kT + r;
       const bool on = pos < it.x.len;
