@@ -3,17 +3,16 @@
 // Two passes without atomics, as in window_bwd.cu: the queries' side (dQ) walks the keys that a tile of
 // 128 rows sees, the keys' side (dK, dV) the rows that see a tile of 128 keys, of all heads that share it.
 // Each computes the logits and <dO, V> anew: 3 and 4 products of 128 x 128 x dh a pair of tiles, 7 where
-// the gradients themselves need 5.  Both are persistent, a CTA an SM: one warp loads, one issues the
-// products, sixteen do the arithmetic, 32 columns of 32 rows (TMEM
-// lanes) each: with eight warps of 64 columns the chain of a block (loads from TMEM, exponentials, stores, a
-// barrier) was longer than its products.
+// the gradients themselves need 5.  Both are persistent, a CTA an SM: one warp loads; one issues the
+// products that make the logits and <dO, V>, one those that sum the gradients (one warp for both took as
+// long as its instructions' way from the caches: 1.8 of a block's 1.8 thousand cycles); sixteen do the
+// arithmetic, 32 columns of 32 rows (TMEM lanes) each: with eight warps of 64 columns the chain of a block
+// (loads from TMEM, exponentials, stores, a barrier) was longer than its products.
 //   * Queries' side: S = Q K^T of the next block is issued as soon as this one's is in registers, and so
-//     is dP = dO V^T; dS goes to one of two buffers as the A operand of dQ += dS K.
+//     is dP = dO V^T; dS has columns of its own as the A operand of dQ += dS K.
 //   * Keys' side: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q, with P^T and dS^T as A operands
 //     in TMEM.  At dh 64 they have columns of their own, and S^T and dP^T run ahead as above.  At dh 128
-//     they take the columns that they came from: the products go in the order dV(x), S^T(x + 1), dK(x),
-//     dP^T(x + 1), so each follows only the one that read the columns it overwrites, and the weights of
-//     x + 1 are computed while dK(x) and dP^T(x + 1) run.
+//     they take the columns that they came from, so S^T(x + 1) waits for dV(x), and dP^T(x + 1) for dK(x).
 // P and dS are rounded to bf16, the type of the products' other operands (half a step, 2^-8 of each).
 // Rows behind a sequence's end may hold anything: as operands that are summed over they become zeros in
 // shared memory, elsewhere their results are not used.
@@ -31,7 +30,8 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kT = 128;             // rows, and keys, of a tile
 constexpr int kElem = 16;           // warps that do the arithmetic: four of each 32 rows, 32 columns a warp
-constexpr int kThreads = 32 * (kElem + 2);
+constexpr int kThreads = 32 * (kElem + 3);
+constexpr int kProducts = kElem, kSums = kElem + 1, kLoads = kElem + 2;  // the warps of the other roles
 constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -47,18 +47,20 @@ struct Tc {
   static constexpr int SUB = DH / 64;                   // 64-element parts of a head
   static constexpr int BLOCK = kTile * SUB;             // 128 rows of a head
   static constexpr int NB = DH == 64 ? 2 : 1;           // buffers of the tile that stays (Q and dO, or K and V)
-  static constexpr int NS = DH == 64 ? 4 : 2;           // stages of what is walked
-  static constexpr int SMEM = 1024 + NB * 2 * BLOCK + NS * (2 * BLOCK + 2 * kT * 4);  // a stage: two operands, the rows' two sums
+  static constexpr int NK = DH == 64 ? 8 : 5;           // queries' side: ring slots, a block of K or of V each
+  static constexpr int NS = DH == 64 ? 4 : 2;           // keys' side: stages, a tile of Q and of dO and the rows' two sums
+  static constexpr int SMEM_Q = 1024 + NB * 2 * BLOCK + NK * BLOCK;
+  static constexpr int SMEM_KV = 1024 + NB * 2 * BLOCK + NS * (2 * BLOCK + 2 * kT * 4);
 };
 
 // Shared memory and barriers of a CTA, the same for both passes.
 template <int DH>
 struct Shared {
-  uint64_t full[Tc<DH>::NS], empty[Tc<DH>::NS];  // stages
+  uint64_t full[Tc<DH>::NK], empty[Tc<DH>::NK];  // slots, or stages
   uint64_t tile[2], tile_free[2];                // the tile that stays
   uint64_t s, dp;                                // products that are there: S and dP (or their transposes)
   uint64_t s_taken, dp_taken;                    // ... that are in registers
-  uint64_t p, ds, dv;                            // P and dS in TMEM; P's product done
+  uint64_t p, ds, dv;                            // P and dS in TMEM; P's product done (queries' side: dS's)
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
@@ -67,7 +69,7 @@ struct Shared {
 template <int DH>
 __device__ __forceinline__ void set_up(Shared<DH>& sh) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Tc<DH>::NS; ++i) {
+    for (int i = 0; i < Tc<DH>::NK; ++i) {
       tc::mbar_init(&sh.full[i], 1);
       tc::mbar_init(&sh.empty[i], 1);
     }
@@ -87,7 +89,7 @@ __device__ __forceinline__ void set_up(Shared<DH>& sh) {
     sh.abort = 0;
     tc::fence_mbar_init();
   }
-  if (threadIdx.x / 32 == kElem) tc::tmem_alloc(&sh.tmem, kCols);
+  if (threadIdx.x / 32 == kProducts) tc::tmem_alloc(&sh.tmem, kCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -157,14 +159,14 @@ __device__ __forceinline__ bool q_item(const PromptArgs& a, int w, QItem& it) {
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
   using C = Tc<DH>;
-  constexpr int NS = C::NS, NB = C::NB, SUB = C::SUB;
+  constexpr int NK = C::NK, NB = C::NB, SUB = C::SUB;
   extern __shared__ unsigned char dsm[];
   unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = tiles + NB * 2 * C::BLOCK;
   __shared__ __align__(8) Shared<DH> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   set_up<DH>(sh);
-  const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 384;  // S, dP, two buffers of dS, dQ
+  const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320;  // S, dP, dS, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   };
   QItem it;
 
-  if (warp == kElem + 1) {
+  if (warp == kLoads) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
     for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
@@ -186,61 +188,62 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
         tc::tma_load_4d_warp(to, &tm.q, 64 * s, a.q_hs ? it.h : 0, it.x.off + it.x.tile * kT, 0, &sh.tile[buf]);
         tc::tma_load_4d_warp(to + C::BLOCK, &tm.g, 64 * s, a.do_hs ? it.h : 0, it.x.off + it.x.tile * kT, 0, &sh.tile[buf]);
       }
-      for (int n = it.lo; n <= it.x.tile; ++n, ++id) {
-        const int st = id % NS;
-        ok = waited(&sh.empty[st], ((id / NS) & 1) ^ 1, kSiteEmpty, n);
-        if (!ok) break;
-        tc::mbar_expect_tx_warp(&sh.full[st], 2 * C::BLOCK);
+      for (int n = it.lo; n <= it.x.tile && ok; ++n)
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v, ++id) {  // K, then V
+          const int st = id % NK;
+          ok = waited(&sh.empty[st], ((id / NK) & 1) ^ 1, kSiteEmpty, n);
+          if (!ok) break;
+          tc::mbar_expect_tx_warp(&sh.full[st], C::BLOCK);
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-          unsigned char* to = ring + st * 2 * C::BLOCK + s * kTile;
-          tc::tma_load_4d_warp(to, &tm.k, 64 * s, a.k_hs ? it.m : 0, it.x.off + n * kT, 0, &sh.full[st]);
-          tc::tma_load_4d_warp(to + C::BLOCK, &tm.v, 64 * s, a.v_hs ? it.m : 0, it.x.off + n * kT, 0, &sh.full[st]);
+          for (int s = 0; s < SUB; ++s)
+            tc::tma_load_4d_warp(ring + st * C::BLOCK + s * kTile, v ? &tm.v : &tm.k, 64 * s, (v ? a.v_hs : a.k_hs) ? it.m : 0, it.x.off + n * kT, 0,
+                                 &sh.full[st]);
         }
-      }
     }
     if (!ok) {  // let the copies in flight land before the CTA ends
-      for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&sh.full[i % NS], (i / NS) & 1, 1u << 16);
+      for (int i = max(0, id - NK); i < id; ++i) tc::mbar_wait(&sh.full[i % NK], (i / NK) & 1, 1u << 16);
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
-  } else if (warp == kElem) {
-    // ---------------------------------------------------------------- products
-    int id = 0, nt = 0;
+  } else if (warp == kProducts) {
+    // ---------------------------------------------------------------- S and dP, each once the block before is in registers
+    int id = 0, nt = 0;  // blocks, tiles so far
     for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
-      const int n = it.x.tile - it.lo + 1;
       const uint32_t q = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), g = q + C::BLOCK;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
-      // Step x: S and dP of block x, each once that of the block before is in registers, and dQ of the block before.
-      for (int x = 0; x <= n && ok; ++x) {
-        if (x < n) {
-          const int i = id + x, st = i % NS;
-          ok = waited(&sh.full[st], (i / NS) & 1, kSiteFull, x);
-          if (i > 0) ok = ok && waited(&sh.s_taken, (i - 1) & 1, kSiteTaken, x);
-          if (!ok) break;
-          tc::fence_after();
-          const uint32_t k = tc::su32(ring + st * 2 * C::BLOCK);
-          product<DH>(tS, q, k);
-          tc::commit_warp(&sh.s);
-          if (i > 0) ok = waited(&sh.dp_taken, (i - 1) & 1, kSiteTaken, x);
-          if (!ok) break;
-          tc::fence_after();
-          product<DH>(tP, g, k + C::BLOCK);
-          tc::commit_warp(&sh.dp);
-          if (x == n - 1) tc::commit_warp(&sh.tile_free[nt % NB]);
-        }
-        if (x > 0) {
-          const int i = id + x - 1, st = i % NS;
-          if (x == 1) ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, x);
-          ok = ok && waited(&sh.ds, i & 1, kSiteDs, x);
-          if (!ok) break;
-          tc::fence_after();
-          accumulate<DH, 0>(tQ, tD + 64 * (i & 1), tc::su32(ring + st * 2 * C::BLOCK), x > 1);
-          tc::commit_warp(&sh.empty[st]);
-        }
+      for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
+        const int ks = 2 * id % NK, vs = (2 * id + 1) % NK;
+        ok = waited(&sh.full[ks], (2 * id / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.s_taken, (id - 1) & 1, kSiteTaken, n));
+        if (!ok) break;
+        tc::fence_after();
+        product<DH>(tS, q, tc::su32(ring + ks * C::BLOCK));
+        tc::commit_warp(&sh.s);
+        ok = waited(&sh.full[vs], ((2 * id + 1) / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.dp_taken, (id - 1) & 1, kSiteTaken, n));
+        if (!ok) break;
+        tc::fence_after();
+        product<DH>(tP, g, tc::su32(ring + vs * C::BLOCK));
+        tc::commit_warp(&sh.dp);
+        tc::commit_warp(&sh.empty[vs]);
+      }
+      if (!ok) break;
+      tc::commit_warp(&sh.tile_free[nt % NB]);
+    }
+  } else if (warp == kSums) {
+    // ---------------------------------------------------------------- dQ += dS K
+    int id = 0, nt = 0;
+    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
+      ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
+      for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
+        const int ks = 2 * id % NK;
+        ok = waited(&sh.ds, id & 1, kSiteDs, n);
+        if (!ok) break;
+        tc::fence_after();
+        accumulate<DH, 0>(tQ, tD, tc::su32(ring + ks * C::BLOCK), n > it.lo);
+        tc::commit_warp(&sh.dv);
+        tc::commit_warp(&sh.empty[ks]);
       }
       if (!ok) break;
       tc::commit_warp(&sh.acc);
-      id += n;
     }
   } else {
     // ---------------------------------------------------------------- arithmetic
@@ -299,13 +302,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
           weigh(std::true_type{}, first - n * kT - 32 * part, on ? pos - n * kT - 32 * part + 1 : 0);
         else weigh(std::false_type{}, 0, 32);
         if ((n + 1) * kT > it.x.len) {  // rows of K behind the sequence
-          ok = waited(&sh.full[id % NS], (id / NS) & 1, kSiteRows, n);
+          ok = waited(&sh.full[2 * id % NK], (2 * id / NK) & 1, kSiteRows, n);
           if (!ok) break;
-          if (part == 0) blank<DH>(ring + (id % NS) * 2 * C::BLOCK, r, it.x.len - n * kT);
+          if (part == 0) blank<DH>(ring + (2 * id % NK) * C::BLOCK, r, it.x.len - n * kT);
           tc::fence_async_smem();
         }
-        // The buffer's last reader, dQ of two blocks ago, was issued before dP(n) and is done.
-        const uint32_t to = tD + lanes + 64 * (id & 1) + 16 * part;
+        if (id > 0) {  // dS's columns have been read
+          ok = waited(&sh.dv, (id - 1) & 1, kSiteDv, n);
+          if (!ok) break;
+          tc::fence_after();
+        }
+        const uint32_t to = tD + lanes + 16 * part;
         const uint32_t d0[8] = {d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7]}, d1[8] = {d[8], d[9], d[10], d[11], d[12], d[13], d[14], d[15]};
         tc::st32x32b_x8(to, d0);
         tc::st32x32b_x8(to + 8, d1);
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == kElem) {
+  if (warp == kProducts) {
     tc::fence_after();
     tc::tmem_dealloc(sh.tmem, kCols);
   }
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   };
   KvItem it;
 
-  if (warp == kElem + 1) {
+  if (warp == kLoads) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
     for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
@@ -410,63 +417,50 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
       for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&sh.full[i % NS], (i / NS) & 1, 1u << 16);
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
-  } else if (warp == kElem) {
-    // ---------------------------------------------------------------- products
-    int id = 0, nt = 0;
+  } else if (warp == kProducts) {
+    // ---------------------------------------------------------------- S^T and dP^T, each once its columns are free
+    int id = 0, nt = 0;  // blocks, tiles so far
     for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
-      const int n = (it.end - it.x.tile) * a.g;
       const uint32_t k = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), v = k + C::BLOCK;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
-      for (int x = -1; x < n && ok; ++x) {
-        const int i = id + x, st = i % NS, next = (i + 1) % NS;
-        const uint32_t q = tc::su32(ring + st * 2 * C::BLOCK), qn = tc::su32(ring + next * 2 * C::BLOCK);
-        const bool more = x + 1 < n;
-        auto weights = [&]() {  // dV += P^T dO
-          if (x == 0) ok = ok && waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, x);
-          ok = ok && waited(&sh.p, i & 1, kSiteP, x);
-          if (!ok) return;
-          tc::fence_after();
-          accumulate<DH, GAP>(tV, tPt, q + C::BLOCK, x > 0);
-          if (OWN) tc::commit_warp(&sh.dv);
-        };
-        auto logits = [&]() {  // S^T of the next block
-          ok = ok && waited(&sh.full[next], ((i + 1) / NS) & 1, kSiteFull, x);
-          if (OWN && i >= 0) ok = ok && waited(&sh.s_taken, i & 1, kSiteTaken, x);
-          if (!ok) return;
-          tc::fence_after();
-          product<DH>(tS, k, qn);
-          tc::commit_warp(&sh.s);
-        };
-        auto gradients = [&]() {  // dK += dS^T Q
-          ok = ok && waited(&sh.ds, i & 1, kSiteDs, x);
-          if (!ok) return;
-          tc::fence_after();
-          accumulate<DH, GAP>(tK, tDt, q, x > 0);
-          tc::commit_warp(&sh.empty[st]);
-        };
-        auto outputs = [&]() {  // dP^T of the next block
-          if (OWN && i >= 0) ok = ok && waited(&sh.dp_taken, i & 1, kSiteTaken, x);
-          if (!ok) return;
-          tc::fence_after();
-          product<DH>(tP, v, qn + C::BLOCK);
-          tc::commit_warp(&sh.dp);
-        };
-        if constexpr (OWN) {
-          if (more) logits();
-          if (x >= 0) weights();
-          if (more) outputs();
-          if (x >= 0) gradients();
-        } else {
-          if (x >= 0) weights();
-          if (more) logits();
-          if (x >= 0) gradients();
-          if (more) outputs();
-        }
+      for (int x = (it.end - it.x.tile) * a.g; x > 0 && ok; --x, ++id) {
+        const int st = id % NS, last = (id - 1) % NS;
+        ok = waited(&sh.full[st], (id / NS) & 1, kSiteFull, x) && (id == 0 || waited(OWN ? &sh.s_taken : &sh.dv, (id - 1) & 1, kSiteTaken, x));
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t q = tc::su32(ring + st * 2 * C::BLOCK);
+        product<DH>(tS, k, q);
+        tc::commit_warp(&sh.s);
+        ok = id == 0 || (OWN ? waited(&sh.dp_taken, (id - 1) & 1, kSiteTaken, x) : waited(&sh.empty[last], ((id - 1) / NS) & 1, kSiteTaken, x));
+        if (!ok) break;
+        tc::fence_after();
+        product<DH>(tP, v, q + C::BLOCK);
+        tc::commit_warp(&sh.dp);
       }
       if (!ok) break;
       tc::commit_warp(&sh.tile_free[nt % NB]);
+    }
+  } else if (warp == kSums) {
+    // ---------------------------------------------------------------- dV += P^T dO, dK += dS^T Q
+    int id = 0, nt = 0;
+    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
+      const int count = (it.end - it.x.tile) * a.g;
+      ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
+      for (int x = 0; x < count && ok; ++x, ++id) {
+        const uint32_t q = tc::su32(ring + (id % NS) * 2 * C::BLOCK);
+        ok = waited(&sh.p, id & 1, kSiteP, x);
+        if (!ok) break;
+        tc::fence_after();
+        accumulate<DH, GAP>(tV, tPt, q + C::BLOCK, x > 0);
+        tc::commit_warp(&sh.dv);
+        ok = waited(&sh.ds, id & 1, kSiteDs, x);
+        if (!ok) break;
+        tc::fence_after();
+        accumulate<DH, GAP>(tK, tDt, q, x > 0);
+        tc::commit_warp(&sh.empty[id % NS]);
+      }
+      if (!ok) break;
       tc::commit_warp(&sh.acc);
-      id += n;
     }
   } else {
     // ---------------------------------------------------------------- arithmetic
@@ -609,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == kElem) {
+  if (warp == kProducts) {
     tc::fence_after();
     tc::tmem_dealloc(sh.tmem, kCols);
   }
@@ -623,16 +617,16 @@ cudaError_t run_tc(const PromptArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = make_packed_tmap(&tm.k, a.k, a.dh, a.Hkv, a.N, a.k_hs, a.k_ts);
   if (e == cudaSuccess) e = make_packed_tmap(&tm.v, a.v, a.dh, a.Hkv, a.N, a.v_hs, a.v_ts);
   if (e == cudaSuccess) e = make_packed_tmap(&tm.g, a.dout, a.dh, a.H, a.N, a.do_hs, a.do_ts);
-  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dq_tc_kernel<DH>, C::SMEM);
-  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dkv_tc_kernel<DH>, C::SMEM);
+  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dq_tc_kernel<DH>, C::SMEM_Q);
+  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dkv_tc_kernel<DH>, C::SMEM_KV);
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.N / kT + std::min<int64_t>(a.B, a.N);
   launch_begin("prompt_dkv_tc", s);
-  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), kThreads, C::SMEM, s>>>(a, tm);
+  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), kThreads, C::SMEM_KV, s>>>(a, tm);
   e = launch_end("prompt_dkv_tc", s);
   if (e != cudaSuccess) return e;
   launch_begin("prompt_dq_tc", s);
-  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), kThreads, C::SMEM, s>>>(a, tm);
+  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), kThreads, C::SMEM_Q, s>>>(a, tm);
   return launch_end("prompt_dq_tc", s);
 }
 

@@ -9,9 +9,10 @@
 //   * one warp loads: the rows' tiles, and blocks of 128 keys of K and V in turn through a ring, from the
 //     diagonal down (so a tile's first block is the one with the causal mask, which has to be weighed by
 //     its maximum anyway);
-//   * one warp issues the products: O += P(n) V(n) with P in the TMEM columns that S(n) lay in, behind
-//     it S(n + 1) = Q K(n + 1)^T into the same columns.  The tensor pipe runs one warp's products in
-//     order, so a thread that has seen S(n + 1) knows that P(n) V(n) is done;
+//   * one warp issues the logits' products S = Q K^T, one the outputs' O += P V with P in the TMEM columns
+//     that S lay in.  S goes into the next of three buffers (two at dh 128) as soon as the product of the P that
+//     was there is done: with three, a softmax finds its next logits when it has stored its weights.  (One
+//     warp for both, and a buffer a tile: 1.4 thousand cycles a unit of 128 x 128 at dh 64, 1.75 at dh 128.)
 //   * four warps a tile do the softmax, a thread a row, as in tree_tc.cu: the weights are exp(s - r) by a
 //     reference r that need not stay the maximum; when the sum of a row's 128 weights passes 2^14 the
 //     block is weighed again by the new maximum, and the output and the sum so far are scaled to it.
@@ -32,13 +33,13 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kT = 128;           // rows of a tile, keys of a block
-constexpr int kThreads = 320;     // warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: products, 9: loads
+constexpr int kThreads = 352;     // warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: logits, 9: outputs, 10: loads
 constexpr int kTile = kT * 128;   // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;   // of TMEM: two tiles' logits, then their outputs
 constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteQFree, kSiteS, kSiteP, kSiteO, kSiteOFree, kSiteV, kSiteRing };
+enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteQFree, kSiteS, kSiteP, kSiteDone, kSiteO, kSiteOFree, kSiteV };
 
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
   return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
@@ -49,10 +50,12 @@ struct Tc {
   static constexpr int SUB = DH / 64;              // 64-element parts of a head
   static constexpr int BLOCK = kTile * SUB;        // a tile of Q, a block of K or of V
   static constexpr int NS = DH == 64 ? 11 : 5;     // ring slots: what shared memory holds beside two tiles of Q
+  static constexpr int NBUF = DH == 64 ? 3 : 2;    // buffers of logits: what TMEM holds beside two outputs
   static constexpr int SMEM = 1024 + 2 * BLOCK + NS * BLOCK;
 };
 
-// A work item: up to two tiles of rows and the blocks of keys that they see, from hi down to lo.
+// A work item: up to two tiles of rows and the blocks of keys that they see, from hi down to lo.  Its units
+// of work are (block, tile), block after block from the highest down, tile 0 before tile 1.
 struct Item {
   PromptTile x;
   int head[2], tile[2];        // of each tile of rows
@@ -60,6 +63,8 @@ struct Item {
   int m;                       // the key head
   __device__ __forceinline__ int top() const { return max(hi[0], hi[1]); }
   __device__ __forceinline__ int low() const { return hi[1] < lo[1] ? lo[0] : min(lo[0], lo[1]); }
+  __device__ __forceinline__ bool has(int t, int n) const { return t ? n <= hi[1] && n >= lo[1] : n <= hi[0] && n >= lo[0]; }
+  __device__ __forceinline__ int units() const { return max(0, hi[0] - lo[0] + 1) + max(0, hi[1] - lo[1] + 1); }
 };
 
 __device__ __forceinline__ bool item_of(const PromptArgs& a, int w, Item& it) {
@@ -90,16 +95,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV) {
   using C = Tc<DH>;
-  constexpr int SUB = C::SUB, NS = C::NS;
+  constexpr int SUB = C::SUB, NS = C::NS, NBUF = C::NBUF;
   constexpr uint32_t kIdS = tc::idesc_bf16(kT, kT, false), kIdPV = tc::idesc_bf16(kT, 64, true);
   extern __shared__ unsigned char dsm[];
   unsigned char* Qs = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = Qs + 2 * C::BLOCK;
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q[2], bar_qfree[2], bar_s[2], bar_p[2], bar_o[2], bar_ofree[2];
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q[2], bar_qfree[2], bar_s[2][NBUF], bar_p[NBUF], bar_done[NBUF],
+      bar_o[2], bar_ofree[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 288) {
+  if (tid == 320) {
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
@@ -112,10 +118,14 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(&bar_q[t], 1);
       tc::mbar_init(&bar_qfree[t], 1);
-      tc::mbar_init(&bar_s[t], 1);
-      tc::mbar_init(&bar_p[t], 4);
       tc::mbar_init(&bar_o[t], 1);
       tc::mbar_init(&bar_ofree[t], 4);
+    }
+    for (int i = 0; i < NBUF; ++i) {
+      tc::mbar_init(&bar_s[0][i], 1);
+      tc::mbar_init(&bar_s[1][i], 1);
+      tc::mbar_init(&bar_p[i], 4);
+      tc::mbar_init(&bar_done[i], 1);
     }
     abort_s = 0;
     tc::fence_mbar_init();
@@ -129,10 +139,12 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
     return wait_on(bar, parity, &abort_s, a.err, site, blockIdx.x, at);
   };
+  // A waiting warp has to see every phase of a barrier, or its parity says nothing: so the logits' barriers are each
+  // tile's own (a tile that an item lacks skips units), in turn for as many units as there are buffers.
   bool ok = true;
   Item it;
 
-  if (warp == 9) {
+  if (warp == 10) {
     // ---------------------------------------------------------------- loads
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
@@ -173,68 +185,83 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
         if (nq[t]) tc::mbar_wait(&bar_q[t], (nq[t] - 1) & 1, 1u << 16);
     }
   } else if (warp == 8) {
-    // ---------------------------------------------------------------- products
-    int ks = 0, vs = 1;               // the slots that K and V come from, and the parities they are filled at
-    uint32_t kp = 0, vp = 0;
-    auto pass = [](int& slot, uint32_t& parity) {
-      slot += 2;
-      if (slot >= NS) {
-        slot -= NS;
-        parity ^= 1;
-      }
-    };
-    int nq[2] = {0, 0}, nb[2] = {0, 0};  // tiles of rows and blocks so far
+    // ---------------------------------------------------------------- logits: S = Q K^T into the buffer of the unit
+    int ks = 0, buf = 0, nq[2] = {0, 0}, own[2] = {0, 0};  // K's slot, the buffer; tiles and units of each tile's warps so far
+    uint32_t kp = 0, bp = 1;              // the parities of K's filling, and of the buffer's last use
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
     for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
-      const int top = it.top(), low = it.low();
-      auto has = [&](int t, int n) { return n <= it.hi[t] && n >= it.lo[t]; };
-      // Step n: P V of block n + 1 (the one before), and the logits of block n, tile by tile.
-      for (int n = top; n >= low - 1 && ok; --n) {
-        const bool load_k = n >= low, load_v = n < top;
-        if (load_k) ok = waited(&bar_full[ks], kp, kSiteFull, n);
-        if (load_v) ok = ok && waited(&bar_full[vs], vp, kSiteFull, n);
-        if (!ok) break;
-        const uint32_t k = tc::su32(ring + ks * C::BLOCK), v = tc::su32(ring + vs * C::BLOCK);
-        tc::fence_after();
+      const int low = it.low();
+      for (int n = it.top(); n >= low && ok; --n) {
+        ok = waited(&bar_full[ks], kp, kSiteFull, n);
+        const uint32_t k = tc::su32(ring + ks * C::BLOCK);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t tS = tmem + kT * t, tO = tmem + 2 * kT + DH * t;
-          if (load_v && has(t, n + 1)) {
-            const bool first = n + 1 == it.hi[t];
-            if (first) ok = ok && waited(&bar_ofree[t], nq[t] & 1, kSiteOFree, n);  // read by the tile before (nq counts this one)
-            ok = ok && waited(&bar_p[t], nb[t] & 1, kSiteP, n);
-            if (!ok) break;
-            ++nb[t];
-            tc::fence_after();
-#pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-              tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tS, tc::desc_mn(v + s * kTile), kIdPV, first ? 0u : 1u);
-              tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tS + 32, tc::desc_mn(v + s * kTile + kTile / 2), kIdPV, 1u);
-            }
-            if (n < it.lo[t]) tc::commit_warp(&bar_o[t]);  // the tile's last
+          if (!it.has(t, n)) continue;
+          if (n == it.hi[t]) {
+            ok = ok && waited(&bar_q[t], nq[t] & 1, kSiteQ, n);
+            ++nq[t];
           }
-          if (load_k && has(t, n)) {
-            if (n == it.hi[t]) {
-              ok = ok && waited(&bar_q[t], nq[t] & 1, kSiteQ, n);
-              if (!ok) break;
-              ++nq[t];
-              tc::fence_after();
-            }
+          ok = ok && waited(&bar_done[buf], bp, kSiteDone, n);
+          if (!ok) break;
+          tc::fence_after();
 #pragma unroll
-            for (int s = 0; s < SUB; ++s)
-              tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tS, dQ + ((t * C::BLOCK + s * kTile) >> 4), tc::desc_km(k + s * kTile), kIdS, s ? 1u : 0u);
-            tc::commit_warp(&bar_s[t]);
-            if (n == it.lo[t]) tc::commit_warp(&bar_qfree[t]);
+          for (int s = 0; s < SUB; ++s)
+            tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + kT * buf, dQ + ((t * C::BLOCK + s * kTile) >> 4), tc::desc_km(k + s * kTile), kIdS, s ? 1u : 0u);
+          tc::commit_warp(&bar_s[t][own[t]]);
+          if (++own[t] == NBUF) own[t] = 0;
+          if (n == it.lo[t]) tc::commit_warp(&bar_qfree[t]);
+          if (++buf == NBUF) {
+            buf = 0;
+            bp ^= 1;
           }
         }
         if (!ok) break;
-        if (load_k) {
-          tc::commit_warp(&bar_empty[ks]);
-          pass(ks, kp);
+        tc::commit_warp(&bar_empty[ks]);
+        ks += 2;
+        if (ks >= NS) {
+          ks -= NS;
+          kp ^= 1;
         }
-        if (load_v) {
-          tc::commit_warp(&bar_empty[vs]);
-          pass(vs, vp);
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- outputs: O += P V
+    int vs = 1, buf = 0, no[2] = {0, 0};
+    uint32_t vp = 0, bp = 0;
+    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
+      const int low = it.low();
+      for (int n = it.top(); n >= low && ok; --n) {
+        ok = waited(&bar_full[vs], vp, kSiteFull, n);
+        const uint32_t v = tc::su32(ring + vs * C::BLOCK);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!it.has(t, n)) continue;
+          if (n == it.hi[t]) {
+            ok = ok && waited(&bar_ofree[t], (no[t] & 1) ^ 1, kSiteOFree, n);  // read by the tile before
+            ++no[t];
+          }
+          ok = ok && waited(&bar_p[buf], bp, kSiteP, n);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t tO = tmem + NBUF * kT + DH * t, tP = tmem + kT * buf;
+#pragma unroll
+          for (int s = 0; s < SUB; ++s) {
+            tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tP, tc::desc_mn(v + s * kTile), kIdPV, n < it.hi[t] ? 1u : 0u);
+            tc::mma4_ts<8, 16, 24, tc::kKStepMn>(tO + 64 * s, tP + 32, tc::desc_mn(v + s * kTile + kTile / 2), kIdPV, 1u);
+          }
+          tc::commit_warp(&bar_done[buf]);
+          if (n == it.lo[t]) tc::commit_warp(&bar_o[t]);
+          if (++buf == NBUF) {
+            buf = 0;
+            bp ^= 1;
+          }
+        }
+        if (!ok) break;
+        tc::commit_warp(&bar_empty[vs]);
+        vs += 2;
+        if (vs >= NS) {
+          vs -= NS;
+          vp ^= 1;
         }
       }
     }
@@ -243,9 +270,10 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     const int t = warp >> 2, r = tid & 127;  // the tile, the row of it
     const float sl2 = a.scale * kLog2e;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tS = tmem + kT * t + lanes, tO = tmem + 2 * kT + DH * t + lanes;
-    int nb = 0, no = 0, slot = 0;            // blocks and tiles so far, ring slots before the item
-    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
+    const uint32_t tO = tmem + NBUF * kT + DH * t + lanes;
+    int unit0 = 0, slot = 0, no = 0, own = 0;  // units of work and ring slots before the item, own tiles and own units so far
+    bool there = item_of(a, prompt_turn(0), it);
+    for (int turn = 1; ok && there; ++turn) {
       const int hi = it.hi[t], lo = it.lo[t], top = it.top();
       const int pos = it.tile[t] * kT + r;
       const bool on = pos < it.x.len;
@@ -275,8 +303,13 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
         const float base = !on ? -CUDART_INF_F : mx == -CUDART_INF_F ? 0.f : -mx * sl2;
         b2 = tc::f2(base, base);
       };
-      for (int n = hi; n >= lo && ok; --n, ++nb) {
-        ok = waited(&bar_s[t], nb & 1, kSiteS, n);
+      // The tile's first unit: those of the other tile's blocks before it.
+      int unit = unit0 + (t ? max(0, it.hi[0] - max(hi, it.lo[0]) + 1) : max(0, it.hi[1] - max(hi + 1, it.lo[1]) + 1)), last = unit;
+      for (int n = hi; n >= lo && ok; --n) {
+        const int buf = unit % NBUF;
+        const uint32_t tS = tmem + kT * buf + lanes;
+        ok = waited(&bar_s[t][own % NBUF], (own / NBUF) & 1, kSiteS, n);
+        ++own;
         if (!ok) break;
         tc::fence_after();
         const bool inner = n < hi && n >= whole;
@@ -341,7 +374,10 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
           const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
           mx = now;
           l *= f;
-          if (n < hi && __any_sync(kAll, f != 1.f)) {  // S(n) was seen, so the products before it are done
+          if (n < hi && __any_sync(kAll, f != 1.f)) {
+            ok = waited(&bar_done[last % NBUF], (last / NBUF) & 1, kSiteDone, n);  // (the products are issued in order: none behind this unit's)
+            if (!ok) break;
+            tc::fence_after();
 #pragma unroll 1
             for (int q = 0; q < DH / 32; ++q) {
               float o[32];
@@ -379,16 +415,20 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar_p[t]);
+        if (lane == 0) tc::mbar_arrive(&bar_p[buf]);
+        last = unit;
+        unit += 1 + it.has(1 - t, t ? n - 1 : n);
       }
+      unit0 += it.units();
       slot += 2 * (top - it.low() + 1);
+      const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
+      if (ok) there = item_of(a, prompt_turn(turn), it);  // the next item, while the last products run
       if (!ok || hi < lo) continue;
-      ok = waited(&bar_o[t], no & 1, kSiteO, -1);
+      ok = waited(&bar_o[t], no & 1, kSiteO, -1);  // (of its own: a buffer's could be two units further by now)
       ++no;
       if (!ok) break;
       tc::fence_after();
       const float inv = 1.f / l;
-      const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
       bf16* row = reinterpret_cast<bf16*>(a.o) + to * a.dh;
 #pragma unroll
       for (int q = 0; q < DH / 32; ++q) {
