@@ -3,16 +3,18 @@
 // Two passes without atomics, as in window_bwd.cu: the queries' side (dQ) walks the keys that a tile of
 // 128 rows sees, the keys' side (dK, dV) the rows that see a tile of 128 keys, of all heads that share it.
 // Each computes the logits and <dO, V> anew: 3 and 4 products of 128 x 128 x dh a pair of tiles, 7 where
-// the gradients themselves need 5.  Both are persistent, a CTA an SM: one warp loads; one issues the
-// products that make the logits and <dO, V>, one those that sum the gradients (one warp for both took as
-// long as its instructions' way from the caches: 1.8 of a block's 1.8 thousand cycles); sixteen do the
-// arithmetic, 32 columns of 32 rows (TMEM lanes) each: with eight warps of 64 columns the chain of a block
-// (loads from TMEM, exponentials, stores, a barrier) was longer than its products.
+// the gradients themselves need 5.  Both are persistent, a CTA an SM: one warp loads, one or two issue the
+// products, sixteen do the arithmetic, 32 columns of 32 rows (TMEM lanes) each.
 //   * Queries' side: S = Q K^T of the next block is issued as soon as this one's is in registers, and so
-//     is dP = dO V^T; dS has columns of its own as the A operand of dQ += dS K.
-//   * Keys' side: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q, with P^T and dS^T as A operands
-//     in TMEM.  At dh 64 they have columns of their own, and S^T and dP^T run ahead as above.  At dh 128
-//     they take the columns that they came from, so S^T(x + 1) waits for dV(x), and dP^T(x + 1) for dK(x).
+//     is dP = dO V^T; dS has columns of its own as the A operand of dQ += dS K, which another warp issues:
+//     one for all products took as long as its own instructions (waits, elections and commits, 80 to 140
+//     cycles each beside sixteen busy warps), 1.77 thousand cycles a block at dh 64; now 1.54.
+//   * Keys' side: S^T = K Q^T, dP^T = V dO^T; P^T and dS^T take the columns that they came from as the A
+//     operands of dV += P^T dO and dK += dS^T Q.  The products go in the order dV(x), S^T(x + 1), dK(x),
+//     dP^T(x + 1), so each follows only the one that read the columns it overwrites (the tensor pipe runs one
+//     warp's products in order).  At dh 64 the warps are two groups, each with half of a block's rows and with
+//     products, barriers and accumulators of its own (added at the end): one's exponentials run beside the
+//     other's sums.  2.14 thousand cycles a block, 2.24 without.  At dh 128 the accumulators fill TMEM.
 // P and dS are rounded to bf16, the type of the products' other operands (half a step, 2^-8 of each).
 // Rows behind a sequence's end may hold anything: as operands that are summed over they become zeros in
 // shared memory, elsewhere their results are not used.
@@ -36,7 +38,7 @@ constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDv, kSiteAcc, kSiteAccFree, kSiteRows };
+enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDone, kSiteAcc, kSiteAccFree, kSiteRows };
 
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
   return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
@@ -46,6 +48,7 @@ template <int DH>
 struct Tc {
   static constexpr int SUB = DH / 64;                   // 64-element parts of a head
   static constexpr int BLOCK = kTile * SUB;             // 128 rows of a head
+  static constexpr int G = DH == 64 ? 2 : 1;            // keys' side: groups of warps that take turns
   static constexpr int NB = DH == 64 ? 2 : 1;           // buffers of the tile that stays (Q and dO, or K and V)
   static constexpr int NK = DH == 64 ? 8 : 5;           // queries' side: ring slots, a block of K or of V each
   static constexpr int NS = DH == 64 ? 4 : 2;           // keys' side: stages, a tile of Q and of dO and the rows' two sums
@@ -58,33 +61,36 @@ template <int DH>
 struct Shared {
   uint64_t full[Tc<DH>::NK], empty[Tc<DH>::NK];  // slots, or stages
   uint64_t tile[2], tile_free[2];                // the tile that stays
-  uint64_t s, dp;                                // products that are there: S and dP (or their transposes)
-  uint64_t s_taken, dp_taken;                    // ... that are in registers
-  uint64_t p, ds, dv;                            // P and dS in TMEM; P's product done (queries' side: dS's)
+  // Of each group of warps:
+  uint64_t s[2], dp[2];                          // products that are there: S and dP (or their transposes)
+  uint64_t s_taken[2], dp_taken[2];              // ... that are in registers
+  uint64_t p[2], ds[2], done[2];                 // P and dS in TMEM; dS's product done
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
 };
 
-template <int DH>
+template <int DH, int G>
 __device__ __forceinline__ void set_up(Shared<DH>& sh) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < Tc<DH>::NK; ++i) {
       tc::mbar_init(&sh.full[i], 1);
-      tc::mbar_init(&sh.empty[i], 1);
+      tc::mbar_init(&sh.empty[i], G);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.tile[i], 1);
-      tc::mbar_init(&sh.tile_free[i], 1);
+      tc::mbar_init(&sh.tile_free[i], G);
     }
-    tc::mbar_init(&sh.s, 1);
-    tc::mbar_init(&sh.dp, 1);
-    tc::mbar_init(&sh.s_taken, kElem);
-    tc::mbar_init(&sh.dp_taken, kElem);
-    tc::mbar_init(&sh.p, kElem);
-    tc::mbar_init(&sh.ds, kElem);
-    tc::mbar_init(&sh.dv, 1);
-    tc::mbar_init(&sh.acc, 1);
+    for (int i = 0; i < G; ++i) {
+      tc::mbar_init(&sh.s[i], 1);
+      tc::mbar_init(&sh.dp[i], 1);
+      tc::mbar_init(&sh.s_taken[i], kElem / G);
+      tc::mbar_init(&sh.dp_taken[i], kElem / G);
+      tc::mbar_init(&sh.p[i], kElem / G);
+      tc::mbar_init(&sh.ds[i], kElem / G);
+      tc::mbar_init(&sh.done[i], 1);
+    }
+    tc::mbar_init(&sh.acc, G);
     tc::mbar_init(&sh.acc_free, kElem);
     sh.abort = 0;
     tc::fence_mbar_init();
@@ -95,41 +101,57 @@ __device__ __forceinline__ void set_up(Shared<DH>& sh) {
   tc::fence_after();
 }
 
-// Rows `have` .. 127 of a block in shared memory become zeros; called by 128 threads, r the thread's row.
-template <int DH>
-__device__ __forceinline__ void blank(unsigned char* block, int r, int have) {
+// Of group `grp`'s rows of a block in shared memory those from `have` on become zeros; called by 128 threads.
+template <int DH, int G>
+__device__ __forceinline__ void blank(unsigned char* block, int grp, int thread, int have) {
+  constexpr int U = 8 / G;  // 16-byte units of a row part a thread
+  const int r = grp * (kT / G) + thread / G, u0 = thread % G * U;
   if (r < have) return;
 #pragma unroll
   for (int s = 0; s < Tc<DH>::SUB; ++s)
 #pragma unroll
-    for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(block + s * kTile + r * 128 + u * 16) = make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(block + s * kTile + r * 128 + (u0 + u) * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// D[128 x 128] = A B^T of two K-major blocks.
-template <int DH>
-__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b) {
+// D = A B^T of two K-major blocks: group `grp`'s columns, 128 or 64 of them.
+template <int DH, int G>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, int grp) {
+  constexpr int N = kT / G;
 #pragma unroll
   for (int s = 0; s < Tc<DH>::SUB; ++s)
-    tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(d, tc::desc_km(a + s * kTile), tc::desc_km(b + s * kTile), tc::idesc_bf16(kT, kT, false), s ? 1u : 0u);
+    tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(d + N * grp, tc::desc_km(a + s * kTile), tc::desc_km(b + s * kTile + grp * N * 128),
+                                            tc::idesc_bf16(kT, N, false), s ? 1u : 0u);
 }
-// D[128 x DH] (+)= A B with A [128 x 128] in TMEM and B [128 x DH] in shared memory.  A's columns lie side by side
-// (GAP 0), or each 16 of them in front of GAP others.
-template <int DH, int GAP>
-__device__ __forceinline__ void accumulate(uint32_t d, uint32_t at, uint32_t b, bool add) {
+// D[128 x DH] (+)= A B with group `grp`'s columns of A [128 x 128] in TMEM and rows of B [128 x DH] in shared memory.  A's
+// columns lie side by side (GAP 0), or each 16 of them in front of GAP others.
+template <int DH, int G, int GAP>
+__device__ __forceinline__ void accumulate(uint32_t d, uint32_t at, uint32_t b, int grp, bool add) {
+  constexpr int H = 2 / G;  // runs of 64 rows
 #pragma unroll
-  for (int s = 0; s < Tc<DH>::SUB; ++s) {
-    tc::mma4_ts<8, 16 + GAP, 24 + GAP, tc::kKStepMn>(d + 64 * s, at, tc::desc_mn(b + s * kTile), tc::idesc_bf16(kT, 64, true), add ? 1u : 0u);
-    tc::mma4_ts<8, 16 + GAP, 24 + GAP, tc::kKStepMn>(d + 64 * s, at + 32 + 2 * GAP, tc::desc_mn(b + s * kTile + kTile / 2), tc::idesc_bf16(kT, 64, true), 1u);
-  }
+  for (int s = 0; s < Tc<DH>::SUB; ++s)
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      tc::mma4_ts<8, 16 + GAP, 24 + GAP, tc::kKStepMn>(d + 64 * s, at + (32 + 2 * GAP) * (H * grp + h),
+                                                       tc::desc_mn(b + s * kTile + kTile / 2 * (H * grp + h)), tc::idesc_bf16(kT, 64, true), add || h ? 1u : 0u);
 }
 
-// W columns of an accumulator's row, scaled, to global memory.
-template <int W>
-__device__ __forceinline__ void write_row(uint32_t at, bf16* to, float scale, bool on) {
-  float o[W];
-  if constexpr (W == 32) tc::ld32x32b_x32(at, o);
-  else tc::ld32x32b_x16(at, o);
+// W columns of a row of the groups' accumulators, `apart` columns from one to the next, summed and scaled, to
+// global memory.
+template <int W, int G>
+__device__ __forceinline__ void write_row(uint32_t at, int apart, bf16* to, float scale, bool on) {
+  float o[W], more[W];
+  auto load = [](uint32_t from, float (&x)[W]) {
+    if constexpr (W == 32) tc::ld32x32b_x32(from, x);
+    else tc::ld32x32b_x16(from, x);
+  };
+  load(at, o);
+  if constexpr (G == 2) load(at + apart, more);
   tc::ld_wait_row(o);
+  if constexpr (G == 2) {
+    tc::ld_wait_row(more);
+#pragma unroll
+    for (int i = 0; i < W; ++i) o[i] += more[i];
+  }
   if (!on) return;
 #pragma unroll
   for (int i = 0; i < W / 8; ++i)
@@ -165,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   unsigned char* ring = tiles + NB * 2 * C::BLOCK;
   __shared__ __align__(8) Shared<DH> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH>(sh);
+  set_up<DH, 1>(sh);
   const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320;  // S, dP, dS, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
@@ -213,16 +235,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
         const int ks = 2 * id % NK, vs = (2 * id + 1) % NK;
-        ok = waited(&sh.full[ks], (2 * id / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.s_taken, (id - 1) & 1, kSiteTaken, n));
+        ok = waited(&sh.full[ks], (2 * id / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.s_taken[0], (id - 1) & 1, kSiteTaken, n));
         if (!ok) break;
         tc::fence_after();
-        product<DH>(tS, q, tc::su32(ring + ks * C::BLOCK));
-        tc::commit_warp(&sh.s);
-        ok = waited(&sh.full[vs], ((2 * id + 1) / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.dp_taken, (id - 1) & 1, kSiteTaken, n));
+        product<DH, 1>(tS, q, tc::su32(ring + ks * C::BLOCK), 0);
+        tc::commit_warp(&sh.s[0]);
+        ok = waited(&sh.full[vs], ((2 * id + 1) / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.dp_taken[0], (id - 1) & 1, kSiteTaken, n));
         if (!ok) break;
         tc::fence_after();
-        product<DH>(tP, g, tc::su32(ring + vs * C::BLOCK));
-        tc::commit_warp(&sh.dp);
+        product<DH, 1>(tP, g, tc::su32(ring + vs * C::BLOCK), 0);
+        tc::commit_warp(&sh.dp[0]);
         tc::commit_warp(&sh.empty[vs]);
       }
       if (!ok) break;
@@ -235,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
       ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
         const int ks = 2 * id % NK;
-        ok = waited(&sh.ds, id & 1, kSiteDs, n);
+        ok = waited(&sh.ds[0], id & 1, kSiteDs, n);
         if (!ok) break;
         tc::fence_after();
-        accumulate<DH, 0>(tQ, tD, tc::su32(ring + ks * C::BLOCK), n > it.lo);
-        tc::commit_warp(&sh.dv);
+        accumulate<DH, 1, 0>(tQ, tD, tc::su32(ring + ks * C::BLOCK), 0, n > it.lo);
+        tc::commit_warp(&sh.done[0]);
         tc::commit_warp(&sh.empty[ks]);
       }
       if (!ok) break;
@@ -261,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
       const int first = a.window ? max(0, pos - a.window + 1) : 0;
       const int whole = a.window ? (max(0, it.x.tile * kT + kT - a.window) + kT - 1) / kT : 0;
       for (int n = it.lo; n <= it.x.tile; ++n, ++id) {
-        ok = waited(&sh.s, id & 1, kSiteS, n);
+        ok = waited(&sh.s[0], id & 1, kSiteS, n);
         if (!ok) break;
         tc::fence_after();
         float s[32], dp[32];
@@ -269,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
         tc::ld_wait_row(s);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.s_taken);
+        if (lane == 0) tc::mbar_arrive(&sh.s_taken[0]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float x, y;
@@ -277,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
           s[2 * i] = tc::ex2(x);
           s[2 * i + 1] = tc::ex2(y);
         }
-        ok = waited(&sh.dp, id & 1, kSiteDp, n);
+        ok = waited(&sh.dp[0], id & 1, kSiteDp, n);
         if (!ok) break;
         tc::fence_after();
         tc::ld32x32b_x32(tP + lanes + 32 * part, dp);
         tc::ld_wait_row(dp);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.dp_taken);
+        if (lane == 0) tc::mbar_arrive(&sh.dp_taken[0]);
         uint32_t d[16];
         auto weigh = [&](auto edge, int c0, int c1) {  // at an edge: of the part's keys c0 .. c1 - 1 are seen
 #pragma unroll
@@ -304,11 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
         if ((n + 1) * kT > it.x.len) {  // rows of K behind the sequence
           ok = waited(&sh.full[2 * id % NK], (2 * id / NK) & 1, kSiteRows, n);
           if (!ok) break;
-          if (part == 0) blank<DH>(ring + (2 * id % NK) * C::BLOCK, r, it.x.len - n * kT);
+          if (part == 0) blank<DH, 1>(ring + (2 * id % NK) * C::BLOCK, 0, r, it.x.len - n * kT);
           tc::fence_async_smem();
         }
         if (id > 0) {  // dS's columns have been read
-          ok = waited(&sh.dv, (id - 1) & 1, kSiteDv, n);
+          ok = waited(&sh.done[0], (id - 1) & 1, kSiteDone, n);
           if (!ok) break;
           tc::fence_after();
         }
@@ -319,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.ds);
+        if (lane == 0) tc::mbar_arrive(&sh.ds[0]);
       }
       if (!ok) break;
       ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
@@ -327,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
       tc::fence_after();
       const int col = part * (DH / 4);
       bf16* to = reinterpret_cast<bf16*>(a.dq) + (int64_t)(it.x.off + pos) * a.dq_ts + it.h * a.dq_hs;
-      if (col < a.dh) write_row<DH / 4>(tQ + lanes + col, to + col, a.scale, on);
+      if (col < a.dh) write_row<DH / 4, 1>(tQ + lanes + col, 0, to + col, a.scale, on);
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.acc_free);
@@ -359,19 +381,16 @@ __device__ __forceinline__ bool kv_item(const PromptArgs& a, int w, KvItem& it) 
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
   using C = Tc<DH>;
-  constexpr int NS = C::NS, NB = C::NB, SUB = C::SUB;
+  constexpr int NS = C::NS, NB = C::NB, SUB = C::SUB, G = C::G;
   extern __shared__ unsigned char dsm[];
   unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = tiles + NB * 2 * C::BLOCK;
   float* rows = reinterpret_cast<float*>(ring + NS * 2 * C::BLOCK);  // of each stage: -lse log2(e), -D
   __shared__ __align__(8) Shared<DH> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH>(sh);
-  // Where TMEM has room (dh 64), P^T and dS^T have columns of their own, and S^T and dP^T of the next block are issued
-  // once this one's are in registers; else they lie in S^T's and dP^T's columns.
-  constexpr bool OWN = DH == 64;
-  constexpr int GAP = OWN ? 0 : 16;
-  const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH, tPt = OWN ? tK + DH : tS, tDt = OWN ? tPt + 64 : tP;
+  set_up<DH, G>(sh);
+  // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
+  const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
@@ -417,50 +436,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
       for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&sh.full[i % NS], (i / NS) & 1, 1u << 16);
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
-  } else if (warp == kProducts) {
-    // ---------------------------------------------------------------- S^T and dP^T, each once its columns are free
+  } else if (warp >= kProducts + G) {
+  } else if (warp >= kProducts) {
+    // ---------------------------------------------------------------- products of a group
+    const int w = G == 1 ? 0 : warp - kProducts;
+    const uint32_t tVw = tV + 2 * DH * w, tKw = tVw + DH;
     int id = 0, nt = 0;  // blocks, tiles so far
     for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
       const uint32_t k = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), v = k + C::BLOCK;
+      const int count = (it.end - it.x.tile) * a.g;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
-      for (int x = (it.end - it.x.tile) * a.g; x > 0 && ok; --x, ++id) {
-        const int st = id % NS, last = (id - 1) % NS;
-        ok = waited(&sh.full[st], (id / NS) & 1, kSiteFull, x) && (id == 0 || waited(OWN ? &sh.s_taken : &sh.dv, (id - 1) & 1, kSiteTaken, x));
-        if (!ok) break;
-        tc::fence_after();
-        const uint32_t q = tc::su32(ring + st * 2 * C::BLOCK);
-        product<DH>(tS, k, q);
-        tc::commit_warp(&sh.s);
-        ok = id == 0 || (OWN ? waited(&sh.dp_taken, (id - 1) & 1, kSiteTaken, x) : waited(&sh.empty[last], ((id - 1) / NS) & 1, kSiteTaken, x));
-        if (!ok) break;
-        tc::fence_after();
-        product<DH>(tP, v, q + C::BLOCK);
-        tc::commit_warp(&sh.dp);
+      for (int x = -1; x < count && ok; ++x) {
+        const int i = id + x, st = i % NS, next = (i + 1) % NS;
+        const uint32_t q = tc::su32(ring + st * 2 * C::BLOCK), qn = tc::su32(ring + next * 2 * C::BLOCK);
+        if (x >= 0) {
+          ok = (x > 0 || waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt)) && waited(&sh.p[w], i & 1, kSiteP, x);
+          if (!ok) break;
+          tc::fence_after();
+          accumulate<DH, G, 16>(tVw, tS, q + C::BLOCK, w, x > 0);
+        }
+        if (x + 1 < count) {
+          ok = waited(&sh.full[next], ((i + 1) / NS) & 1, kSiteFull, x);
+          if (!ok) break;
+          tc::fence_after();
+          product<DH, G>(tS, k, qn, w);
+          tc::commit_warp(&sh.s[w]);
+        }
+        if (x >= 0) {
+          ok = waited(&sh.ds[w], i & 1, kSiteDs, x);
+          if (!ok) break;
+          tc::fence_after();
+          accumulate<DH, G, 16>(tKw, tP, q, w, x > 0);
+          tc::commit_warp(&sh.empty[st]);
+        }
+        if (x + 1 < count) {
+          product<DH, G>(tP, v, qn + C::BLOCK, w);
+          tc::commit_warp(&sh.dp[w]);
+        }
       }
       if (!ok) break;
       tc::commit_warp(&sh.tile_free[nt % NB]);
-    }
-  } else if (warp == kSums) {
-    // ---------------------------------------------------------------- dV += P^T dO, dK += dS^T Q
-    int id = 0, nt = 0;
-    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
-      const int count = (it.end - it.x.tile) * a.g;
-      ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
-      for (int x = 0; x < count && ok; ++x, ++id) {
-        const uint32_t q = tc::su32(ring + (id % NS) * 2 * C::BLOCK);
-        ok = waited(&sh.p, id & 1, kSiteP, x);
-        if (!ok) break;
-        tc::fence_after();
-        accumulate<DH, GAP>(tV, tPt, q + C::BLOCK, x > 0);
-        tc::commit_warp(&sh.dv);
-        ok = waited(&sh.ds, id & 1, kSiteDs, x);
-        if (!ok) break;
-        tc::fence_after();
-        accumulate<DH, GAP>(tK, tDt, q, x > 0);
-        tc::commit_warp(&sh.empty[id % NS]);
-      }
-      if (!ok) break;
       tc::commit_warp(&sh.acc);
+      id += count;
     }
   } else {
     // ---------------------------------------------------------------- arithmetic
@@ -468,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
     // keys lane / 4 and lane / 4 + 8 and rows 2 (lane % 4) and the next.  So it needs eight rows' sums, not all 32:
     // in whole rows a thread their loads from shared memory (four wavefronts a vector, broadcast or not) took longer
     // than the operands of the products.
-    const int part = warp >> 2, group = lane >> 2, two = 2 * (lane & 3);
+    const int part = warp >> 2, grp = G == 2 ? part >> 1 : 0, group = lane >> 2, two = 2 * (lane & 3);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
@@ -478,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
       for (int h = 0; h < a.g && ok; ++h)
         for (int i = it.x.tile; i < it.end; ++i, ++id) {
           const int st = id % NS, t0 = i * kT + 32 * part + two;  // rows t0 + 8 n, and the next
-          ok = waited(&sh.full[st], (id / NS) & 1, kSiteRows, i) && waited(&sh.s, id & 1, kSiteS, i);
+          ok = waited(&sh.full[st], (id / NS) & 1, kSiteRows, i) && waited(&sh.s[grp], id & 1, kSiteS, i);
           if (!ok) break;
           tc::fence_after();
           // Every row sees every key of blocks inside.
@@ -487,19 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
           float p[2][4][4];
           tc::ld16x256_x4(tS + lanes + 32 * part, p[0]);
           tc::ld16x256_x4(tS + lanes + (16u << 16) + 32 * part, p[1]);
-          if (part < 2 && (i + 1) * kT > it.x.len) {  // rows of Q and dO behind the sequence
-            blank<DH>(ring + st * 2 * C::BLOCK + part * C::BLOCK, 32 * (warp & 3) + lane, it.x.len - i * kT);
+          if ((G == 2 || part < 2) && (i + 1) * kT > it.x.len) {  // rows of Q and dO behind the sequence
+            blank<DH, G>(ring + st * 2 * C::BLOCK + part % 2 * C::BLOCK, grp, 32 * (warp & 3) + lane, it.x.len - i * kT);
             tc::fence_async_smem();
           }
           const float* nl = rows + st * 2 * kT + 32 * part + two;
           const float* nd = nl + kT;
           tc::ld_wait(p[0]);
           tc::ld_wait(p[1]);
-          if constexpr (OWN) {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.s_taken);
-          }
           uint32_t x[2][8];
           auto weigh = [&](auto at_edge) {
 #pragma unroll
@@ -526,19 +538,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
           };
           if (edge) weigh(std::true_type{});
           else weigh(std::false_type{});
-          if (OWN && id > 0) {  // P^T's columns have been read
-            ok = waited(&sh.dv, (id - 1) & 1, kSiteDv, i);
-            if (!ok) break;
-            tc::fence_after();
-          }
-          const uint32_t at = (16 + GAP) * part;  // of the A operand
-          tc::st16x128_x4(tPt + lanes + at, x[0]);
-          tc::st16x128_x4(tPt + lanes + (16u << 16) + at, x[1]);
+          // Over columns that have been read: an A operand's 16 of each 32.
+          tc::st16x128_x4(tS + lanes + 32 * part, x[0]);
+          tc::st16x128_x4(tS + lanes + (16u << 16) + 32 * part, x[1]);
           tc::st_wait();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sh.p);
-          ok = waited(&sh.dp, id & 1, kSiteDp, i);
+          if (lane == 0) tc::mbar_arrive(&sh.p[grp]);
+          ok = waited(&sh.dp[grp], id & 1, kSiteDp, i);
           if (!ok) break;
           tc::fence_after();
           float d[2][4][4];
@@ -546,11 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
           tc::ld16x256_x4(tP + lanes + (16u << 16) + 32 * part, d[1]);
           tc::ld_wait(d[0]);
           tc::ld_wait(d[1]);
-          if constexpr (OWN) {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.dp_taken);
-          }
           auto differ = [&](auto at_edge) {
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -572,17 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
           };
           if (edge) differ(std::true_type{});
           else differ(std::false_type{});
-          if (OWN && id > 0) {  // dS^T's columns have been read: the block before has given its stage back
-            ok = waited(&sh.empty[(id - 1) % NS], ((id - 1) / NS) & 1, kSiteDs, i);
-            if (!ok) break;
-            tc::fence_after();
-          }
-          tc::st16x128_x4(tDt + lanes + at, x[0]);
-          tc::st16x128_x4(tDt + lanes + (16u << 16) + at, x[1]);
+          tc::st16x128_x4(tP + lanes + 32 * part, x[0]);
+          tc::st16x128_x4(tP + lanes + (16u << 16) + 32 * part, x[1]);
           tc::st_wait();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sh.ds);
+          if (lane == 0) tc::mbar_arrive(&sh.ds[grp]);
         }
       if (!ok) break;
       ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
@@ -593,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
       bf16* kt = reinterpret_cast<bf16*>(a.dk) + (int64_t)(it.x.off + key) * a.dk_ts + it.m * a.dk_hs;
       bf16* vt = reinterpret_cast<bf16*>(a.dv) + (int64_t)(it.x.off + key) * a.dv_ts + it.m * a.dv_hs;
       if (col < a.dh) {
-        write_row<DH / 4>(tV + lanes + col, vt + col, 1.f, on);
-        write_row<DH / 4>(tK + lanes + col, kt + col, a.scale, on);
+        write_row<DH / 4, G>(tV + lanes + col, 2 * DH, vt + col, 1.f, on);
+        write_row<DH / 4, G>(tK + lanes + col, 2 * DH, kt + col, a.scale, on);
       }
       tc::fence_before();
       __syncwarp();

@@ -575,3 +575,39 @@ def test_quantised_page_operations():
     with pytest.raises(TypeError):
         cache.attention(None, None, None)
     cache.check()
+
+
+@pytest.mark.parametrize("H,Hkv,dh,window", [(12, 12, 64, 0), (10, 2, 128, 0), (24, 4, 64, 300), (12, 4, 32, 0), (8, 8, 128, 700)])
+def test_prompt_many_tiles_a_cta(H, Hkv, dh, window):
+    """Long sequences whose last tile has no neighbour among others that have, several work items a CTA: against
+    the formulas in float64 on the GPU."""
+    g = _g()
+    lengths = (1400, 2300, 130, 1153, 900, 385, 2049, 60)
+    off = offsets_of(lengths)
+    N, dev_ = int(off[-1]), "cuda"
+    gen = torch.Generator(device=dev_)
+    gen.manual_seed(3)
+    q, k, v, do = (torch.randn(N, h, dh, device=dev_, generator=gen).bfloat16() for h in (H, Hkv, Hkv, H))
+    o, lse = g.prompt_attention(q, k, v, ints(off), window=window)
+    grads = g.prompt_attention_backward(q, k, v, o, do, lse, ints(off), window=window)
+    for a, z in zip(off, off[1:]):
+        n, rep = int(z - a), H // Hkv
+        qs, ks, vs, ds_ = (x[a:z].double().transpose(0, 1) for x in (q, k, v, do))
+        ks, vs = ks.repeat_interleave(rep, 0), vs.repeat_interleave(rep, 0)
+        t = torch.arange(n, device=dev_)
+        see = (t[None] <= t[:, None]) & ((t[None] > t[:, None] - window) if window else True)
+        s = (qs @ ks.transpose(1, 2) * dh ** -0.5).masked_fill(~see, -float("inf"))
+        L = torch.logsumexp(s, 2)
+        p = torch.exp(s - L[..., None])
+        ref = p @ vs
+        dS = p * (ds_ @ vs.transpose(1, 2) - (ds_ * ref).sum(2, keepdim=True)) * dh ** -0.5
+        mag = p * (ds_.abs() @ vs.abs().transpose(1, 2) + (ds_.abs() * (p @ vs.abs())).sum(2, keepdim=True)) * dh ** -0.5
+        fold = lambda x: x.view(Hkv, rep, n, dh).sum(1)  # noqa: E731
+        # One rounding of the output, 2^-8 for the operand (P or dS), D's from the rounded output, and float32's sums.
+        e = 2.0 ** -8 * 1.05
+        for got, want, size in ((o, ref, p @ vs.abs()), (grads[0], dS @ ks, 2 * (mag @ ks.abs())),
+                                (grads[1], fold(dS.transpose(1, 2) @ qs), 2 * fold(mag.transpose(1, 2) @ qs.abs())),
+                                (grads[2], fold(p.transpose(1, 2) @ ds_), fold(p.transpose(1, 2) @ ds_.abs()))):
+            err = (got[a:z].double().transpose(0, 1) - want).abs()
+            assert bool((err <= 2.0 ** -8 * want.abs() + e * size + 1e-30).all()), (n, float((err - e * size).max()))
+        assert float((lse[a:z].double().transpose(0, 1) - L).abs().max()) <= 2e-5
