@@ -221,10 +221,10 @@ struct NormRotaryArgs {
   const uint64_t* freq;                         // [rot / 2]
   const int32_t* pos; int64_t pos_bs;           // null: token l is at position l
   float gain, sgain, eps;
-  float* partial; float* dqw; float* dkw;       // backward: scratch [2][CTAs][dh], and [dh]
-  int tokens, group;                            // of a piece, lanes of a row (set by the launcher)
+  float* partial; float* dqw; float* dkw;       // backward: scratch [CTAs][dh], and [dh]
+  int group, per, q_parts;                      // lanes of a token, heads of a CTA, CTAs of q's heads (set by the launcher)
 };
-constexpr int kNormCtas = kSMs * 6;             // of the backward pass, at most
+constexpr int kNormRows = kSMs * 6;             // CTAs of the backward pass at most, with a partial sum each: two rounds
 size_t norm_rotary_scratch_bytes(int dh);
 cudaError_t launch_norm_rotary(NormRotaryArgs a, cudaStream_t s);
 
