@@ -22,36 +22,56 @@ __device__ __forceinline__ int prompt_length(const PromptArgs& a, int b) {
   return e - s;
 }
 
+// Tiles of T rows of the sequences, for many lookups: the first kKeep in shared memory, a lane's own of the
+// first 32 in a register.  All threads of the CTA make it, with a barrier between `fill` and the first use.
+template <int T>
+struct PromptTiles {
+  static constexpr int kKeep = 256;
+  const int* kept;
+  int mine;
+  static __device__ __forceinline__ int of(const PromptArgs& a, int b) { return b < a.B ? (prompt_length(a, b) + T - 1) / T : 0; }
+  static __device__ __forceinline__ void fill(const PromptArgs& a, int* keep) {
+    for (int b = threadIdx.x; b < kKeep; b += blockDim.x) keep[b] = of(a, b);
+  }
+  __device__ __forceinline__ PromptTiles(const int* keep) : kept(keep), mine(keep[threadIdx.x & 31]) {}
+  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return b < kKeep ? kept[b] : of(a, b); }
+};
+
 // Tile number `rank` of the call: tiles of T rows in the order of their work, the most first, so that
 // those that start last are short.  Under the causal mask that is the order of their number in their
 // sequence, from the highest down (`back`: counted from the sequence's end, for the side of the keys),
 // sequences of equal tiles in order.  With S(i) the tiles numbered i or higher, tile `rank` has the number
 // i with S(i + 1) <= rank < S(i).  Called by a whole warp; false behind the last tile.
-template <int T>
-__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int rank, bool back, PromptTile& x) {
+template <typename Tiles>
+__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const Tiles& tiles, int rank, bool back, PromptTile& x) {
   const int lane = threadIdx.x & 31;
-  auto tiles_of = [&](int b) { return b < a.B ? (prompt_length(a, b) + T - 1) / T : 0; };
-  const int mine = tiles_of(lane);  // the first 32 sequences stay in registers
-  int most = mine;
-  for (int b = lane + 32; b < a.B; b += 32) most = max(most, tiles_of(b));
+  const int mine = tiles.mine;  // the first 32 sequences stay in registers
   auto from = [&](int i) {
     int n = max(mine - i, 0);
-    for (int b = lane + 32; b < a.B; b += 32) n += max(tiles_of(b) - i, 0);
+    for (int b = lane + 32; b < a.B; b += 32) n += max(tiles(a, b) - i, 0);
     return (int)__reduce_add_sync(0xffffffffu, n);
   };
-  int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, most);  // from(lo) > rank >= from(hi)
+  int most = mine;
+  for (int b = lane + 32; b < a.B; b += 32) most = max(most, tiles(a, b));
+  int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, most), below = 0;  // from(lo) > rank >= from(hi) = below
   if (from(0) <= rank) return false;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (from(mid) > rank) lo = mid;
-    else hi = mid;
+    const int mid = (lo + hi) >> 1, n = from(mid);
+    if (n > rank) {
+      lo = mid;
+    } else {
+      hi = mid;
+      below = n;
+    }
   }
-  int left = rank - from(lo + 1);  // of the sequences with more than `lo` tiles, in order
+  int left = rank - below;  // of the sequences with more than `lo` tiles, in order
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 ? tiles_of(b0 + lane) : mine;
+    const int n = b0 ? (b0 + lane < a.B ? tiles(a, b0 + lane) : 0) : mine;
     const uint32_t those = __ballot_sync(0xffffffffu, n > lo);
     if (left < __popc(those)) {
-      const int at = __fns(those, 0, left + 1);
+      // The lane of the bit that `left` others lie below.
+      const bool it = n > lo && __popc(those & ((1u << lane) - 1)) == left;
+      const int at = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
       x.b = b0 + at;
       x.tile = back ? __shfl_sync(0xffffffffu, n, at) - 1 - lo : lo;
       x.off = a.offsets[x.b];

@@ -68,10 +68,12 @@ struct Shared {
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
+  int keep[PromptTiles<kT>::kKeep];
 };
 
 template <int DH, int G>
-__device__ __forceinline__ void set_up(Shared<DH>& sh) {
+__device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh) {
+  PromptTiles<kT>::fill(a, sh.keep);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Tc<DH>::NK; ++i) {
       tc::mbar_init(&sh.full[i], 1);
@@ -169,10 +171,10 @@ struct QItem {
   PromptTile x;
   int h, m, lo;
 };
-__device__ __forceinline__ bool q_item(const PromptArgs& a, int w, QItem& it) {
+__device__ __forceinline__ bool q_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, QItem& it) {
   it.h = w % a.H;
   it.m = it.h / a.g;
-  if (!prompt_tile<kT>(a, w / a.H, false, it.x)) return false;
+  if (!prompt_tile(a, tiles, w / a.H, false, it.x)) return false;
   it.lo = a.window ? max(0, it.x.tile * kT - a.window + 1) / kT : 0;
   return true;
 }
@@ -187,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   unsigned char* ring = tiles + NB * 2 * C::BLOCK;
   __shared__ __align__(8) Shared<DH> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, 1>(sh);
+  set_up<DH, 1>(a, sh);
+  const PromptTiles<kT> counts(sh.keep);
   const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320;  // S, dP, dS, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   if (warp == kLoads) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
       const int buf = nt % NB;
       ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, nt);
       if (!ok) break;
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   } else if (warp == kProducts) {
     // ---------------------------------------------------------------- S and dP, each once the block before is in registers
     int id = 0, nt = 0;  // blocks, tiles so far
-    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
       const uint32_t q = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), g = q + C::BLOCK;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   } else if (warp == kSums) {
     // ---------------------------------------------------------------- dQ += dS K
     int id = 0, nt = 0;
-    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
       ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
         const int ks = 2 * id % NK;
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
     int id = 0, nt = 0;
-    for (; ok && q_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
       const int pos = it.x.tile * kT + r;
       const bool on = pos < it.x.len;
       const int64_t row = it.h * a.np + prompt_pad(it.x.off, it.x.b) + pos;
@@ -369,9 +372,9 @@ struct KvItem {
   PromptTile x;
   int m, end;
 };
-__device__ __forceinline__ bool kv_item(const PromptArgs& a, int w, KvItem& it) {
+__device__ __forceinline__ bool kv_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, KvItem& it) {
   it.m = w % a.Hkv;
-  if (!prompt_tile<kT>(a, w / a.Hkv, true, it.x)) return false;
+  if (!prompt_tile(a, tiles, w / a.Hkv, true, it.x)) return false;
   const int k = min(it.x.tile * kT + kT, it.x.len) - 1;  // the tile's last key
   it.end = (a.window ? (int)min((int64_t)it.x.len - 1, (int64_t)k + a.window - 1) : it.x.len - 1) / kT + 1;
   return true;
@@ -388,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   float* rows = reinterpret_cast<float*>(ring + NS * 2 * C::BLOCK);  // of each stage: -lse log2(e), -D
   __shared__ __align__(8) Shared<DH> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, G>(sh);
+  set_up<DH, G>(a, sh);
+  const PromptTiles<kT> counts(sh.keep);
   // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
   const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
   bool ok = true;
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   if (warp == kLoads) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
       const int buf = nt % NB;
       ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, nt);
       if (!ok) break;
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
     const int w = G == 1 ? 0 : warp - kProducts;
     const uint32_t tVw = tV + 2 * DH * w, tKw = tVw + DH;
     int id = 0, nt = 0;  // blocks, tiles so far
-    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
       const uint32_t k = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), v = k + C::BLOCK;
       const int count = (it.end - it.x.tile) * a.g;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
     int id = 0, nt = 0;
-    for (; ok && kv_item(a, prompt_turn(nt), it); ++nt) {
+    for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
       const int key0 = it.x.tile * kT + 32 * (warp & 3) + group;  // keys key0 + 0, 8, 16, 24
       for (int h = 0; h < a.g && ok; ++h)
         for (int i = it.x.tile; i < it.end; ++i, ++id) {

@@ -67,16 +67,25 @@ struct Item {
   __device__ __forceinline__ int units() const { return max(0, hi[0] - lo[0] + 1) + max(0, hi[1] - lo[1] + 1); }
 };
 
-__device__ __forceinline__ bool item_of(const PromptArgs& a, int w, Item& it) {
+// The sequences' tiles: of 128 rows where an item is two heads of a tile, of 256 where it is two tiles of a head.
+struct Counts {
+  const int* kept;
+  int mine;
+  static __device__ __forceinline__ int of(const PromptArgs& a, int b) {
+    return a.g % 2 == 0 ? PromptTiles<kT>::of(a, b) : PromptTiles<2 * kT>::of(a, b);
+  }
+  __device__ __forceinline__ Counts(const int* keep) : kept(keep), mine(keep[threadIdx.x & 31]) {}
+  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return b < PromptTiles<kT>::kKeep ? kept[b] : of(a, b); }
+};
+__device__ __forceinline__ bool item_of(const PromptArgs& a, const Counts& counts, int w, Item& it) {
   const bool heads = a.g % 2 == 0;  // two heads of a tile, or two tiles of a head
   const int per = heads ? a.H / 2 : a.H, h = w % per, rank = w / per;
+  if (!prompt_tile(a, counts, rank, false, it.x)) return false;
   if (heads) {
-    if (!prompt_tile<kT>(a, rank, false, it.x)) return false;
     it.head[0] = 2 * h;
     it.head[1] = 2 * h + 1;
     it.tile[0] = it.tile[1] = it.x.tile;
   } else {
-    if (!prompt_tile<2 * kT>(a, rank, false, it.x)) return false;
     it.head[0] = it.head[1] = h;
     it.tile[0] = 2 * it.x.tile;
     it.tile[1] = 2 * it.x.tile + 1;
@@ -103,7 +112,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q[2], bar_qfree[2], bar_s[2][NBUF], bar_p[NBUF], bar_done[NBUF],
       bar_o[2], bar_ofree[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_s;
+  __shared__ int abort_s, keep[PromptTiles<kT>::kKeep];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 320) {
     prefetch_tmap(&tmQ);
@@ -130,6 +139,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     abort_s = 0;
     tc::fence_mbar_init();
   }
+  for (int b = tid; b < PromptTiles<kT>::kKeep; b += kThreads) keep[b] = Counts::of(a, b);
   if (warp == 8) tc::tmem_alloc(&tmem_slot, kCols);
   tc::fence_before();
   __syncthreads();
@@ -142,6 +152,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
   // A waiting warp has to see every phase of a barrier, or its parity says nothing: so the logits' barriers are each
   // tile's own (a tile that an item lacks skips units), in turn for as many units as there are buffers.
   bool ok = true;
+  const Counts counts(keep);
   Item it;
 
   if (warp == 10) {
@@ -149,7 +160,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
     int nq[2] = {0, 0};      // tiles of rows so far
-    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
+    for (int turn = 0; ok && item_of(a, counts, prompt_turn(turn), it); ++turn) {
       auto rows = [&](int t) {
         if (it.hi[t] < it.lo[t]) return;
         ok = ok && waited(&bar_qfree[t], (nq[t] & 1) ^ 1, kSiteQFree, turn);
@@ -189,7 +200,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int ks = 0, buf = 0, nq[2] = {0, 0}, own[2] = {0, 0};  // K's slot, the buffer; tiles and units of each tile's warps so far
     uint32_t kp = 0, bp = 1;              // the parities of K's filling, and of the buffer's last use
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
-    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
+    for (int turn = 0; ok && item_of(a, counts, prompt_turn(turn), it); ++turn) {
       const int low = it.low();
       for (int n = it.top(); n >= low && ok; --n) {
         ok = waited(&bar_full[ks], kp, kSiteFull, n);
@@ -228,7 +239,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     // ---------------------------------------------------------------- outputs: O += P V
     int vs = 1, buf = 0, no[2] = {0, 0};
     uint32_t vp = 0, bp = 0;
-    for (int turn = 0; ok && item_of(a, prompt_turn(turn), it); ++turn) {
+    for (int turn = 0; ok && item_of(a, counts, prompt_turn(turn), it); ++turn) {
       const int low = it.low();
       for (int n = it.top(); n >= low && ok; --n) {
         ok = waited(&bar_full[vs], vp, kSiteFull, n);
@@ -272,7 +283,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + NBUF * kT + DH * t + lanes;
     int unit0 = 0, slot = 0, no = 0, own = 0;  // units of work and ring slots before the item, own tiles and own units so far
-    bool there = item_of(a, prompt_turn(0), it);
+    bool there = item_of(a, counts, prompt_turn(0), it);
     for (int turn = 1; ok && there; ++turn) {
       const int hi = it.hi[t], lo = it.lo[t], top = it.top();
       const int pos = it.tile[t] * kT + r;
@@ -343,8 +354,10 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
           }
         }
         if (__builtin_expect(!done, 0)) {
-          // Keys c0 .. c1 - 1 of the block are seen.  The maximum with this block, and the weights by it.
+          // Keys c0 .. c1 - 1 of the block are seen: by some row of the warp those of quarters q0 .. q1 - 1.  The maximum
+          // with this block, and the weights by it.
           const int c0 = max(first - n * kT, 0), c1 = on ? min(pos - n * kT + 1, kT) : 0;
+          const int q0 = min(__shfl_sync(kAll, c0, 0) / 32, 4), q1 = ((int)__reduce_max_sync(kAll, c1) + 31) / 32;
           if (n == hi && (n + 1) * kT > it.x.len) {
             // Rows of V behind the sequence become zeros (by this tile's softmax where it is the tile that
             // reaches them, or by both with the same zeros).
@@ -359,17 +372,24 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
                   *reinterpret_cast<uint4*>(ring + (i % NS) * C::BLOCK + s * kTile + r * 128 + u * 16) = make_uint4(0, 0, 0, 0);
             tc::fence_async_smem();
           }
-          float now = mx;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float s[32];
+          // A quarter's logits; what the row does not see becomes -inf.
+          auto logits = [&](int q, float (&s)[32]) {
             tc::ld32x32b_x32(tS + 32 * q, s);
             tc::ld_wait_row(s);
+            const int lo = min(max(c0 - 32 * q, 0), 32), n1 = min(max(c1 - 32 * q, 0), 32);
+            const uint32_t see = lo >= n1 ? 0u : (n1 == 32 ? ~0u : (1u << n1) - 1) & ~((1u << lo) - 1);
+            if (__all_sync(kAll, see == ~0u)) return;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c = 32 * q + i;
-              if (c >= c0 && c < c1) now = fmaxf(now, s[i]);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1)) s[i] = -CUDART_INF_F;
+          };
+          float now = mx;
+#pragma unroll 1
+          for (int q = q0; q < q1; ++q) {
+            float s[32];
+            logits(q, s);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) now = tc::max3(now, s[i], s[i + 1]);
           }
           const float f = now == -CUDART_INF_F ? 1.f : tc::ex2((mx - now) * sl2);
           mx = now;
@@ -395,18 +415,17 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
           set_base();
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            float s[32];
-            tc::ld32x32b_x32(tS + 32 * q, s);
-            tc::ld_wait_row(s);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c = 32 * q + i;
-              if (c < c0 || c >= c1) s[i] = -CUDART_INF_F;
-            }
             uint32_t p[16];
-            sums[0] = sums[1] = sums[2] = sums[3] = 0;
-            weigh(s, p);
-            l += total();
+            if (q < q0 || q >= q1) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) p[i] = 0;
+            } else {
+              float s[32];
+              logits(q, s);
+              sums[0] = sums[1] = sums[2] = sums[3] = 0;
+              weigh(s, p);
+              l += total();
+            }
             const uint32_t p0[8] = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]}, p1[8] = {p[8], p[9], p[10], p[11], p[12], p[13], p[14], p[15]};
             tc::st32x32b_x8(tS + 16 * q, p0);  // over logits that have been read
             tc::st32x32b_x8(tS + 16 * q + 8, p1);
@@ -422,7 +441,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       unit0 += it.units();
       slot += 2 * (top - it.low() + 1);
       const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
-      if (ok) there = item_of(a, prompt_turn(turn), it);  // the next item, while the last products run
+      if (ok) there = item_of(a, counts, prompt_turn(turn), it);  // the next item, while the last products run
       if (!ok || hi < lo) continue;
       ok = waited(&bar_o[t], no & 1, kSiteO, -1);  // (of its own: a buffer's could be two units further by now)
       ++no;
