@@ -204,12 +204,14 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
 }
 
 // What both sides of the backward pass need of a row, negative as they add it: D = <do, o>, and the
-// log-sum-exp times log2(e); a head's rows side by side, [H][np] each.
-
-template <typename T>
+// log-sum-exp times log2(e); a head's rows side by side, [H][np] each.  A warp takes a token, some of its heads
+// at a time.  Bound by memory.
+template <typename T, int DH>
 __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
-  const int h = blockIdx.y;
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  constexpr int V = Elem<T>::kVec, LANES = DH / V, SIDE = 32 / LANES, FLY = 3;  // lanes of a row, rows side by side
+  const int lane = threadIdx.x & 31, at = lane % LANES, h0 = lane / LANES;
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  if (row >= a.N) return;
   // The sequence of the row: the last that starts at it or before (empty ones behind it start there too).
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
@@ -218,22 +220,38 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
     else hi = mid;
   }
   const int off = a.offsets[lo];
-  const bool on = row < a.N && row >= off && row - off < prompt_length(a, lo);
-  float d = 0.f;
-  constexpr int V = Elem<T>::kVec;
-  if (on) {
-    const T* o = reinterpret_cast<const T*>(a.o) + (row * a.H + h) * a.dh;
-    const T* g = reinterpret_cast<const T*>(a.dout) + row * a.do_ts + h * a.do_hs;
-    for (int c = 0; c < a.dh; c += V) {
-      float x[V], y[V];
-      unpack16(*reinterpret_cast<const uint4*>(o + c), x, (const T*)nullptr);
-      unpack16(*reinterpret_cast<const uint4*>(g + c), y, (const T*)nullptr);
+  if (row < off || row - off >= prompt_length(a, lo)) return;
+  const T* o = reinterpret_cast<const T*>(a.o) + row * a.H * DH + at * V;
+  const T* g = reinterpret_cast<const T*>(a.dout) + row * a.do_ts + at * V;
+  const int64_t to = prompt_pad(off, lo) + row - off;
+  for (int h = h0; h - h0 < a.H; h += FLY * SIDE) {  // the same for the whole warp: shuffles need every lane
+    uint4 x[FLY], y[FLY];
+    float l[FLY];
 #pragma unroll
-      for (int i = 0; i < V; ++i) d += x[i] * y[i];
+    for (int f = 0; f < FLY; ++f) {
+      const int head = h + f * SIDE;
+      x[f] = y[f] = make_uint4(0, 0, 0, 0);
+      l[f] = 0.f;
+      if (head >= a.H) continue;
+      x[f] = *reinterpret_cast<const uint4*>(o + head * DH);
+      y[f] = *reinterpret_cast<const uint4*>(g + head * a.do_hs);
+      if (at == 0) l[f] = a.lse[row * a.H + head];
     }
-    const int64_t to = h * a.np + prompt_pad(off, lo) + row - off;
-    a.nD[to] = -d;
-    a.nlse[to] = -a.lse[row * a.H + h] * kLog2e;
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      float u[V], v[V], d = 0.f;
+      unpack16(x[f], u, (const T*)nullptr);
+      unpack16(y[f], v, (const T*)nullptr);
+#pragma unroll
+      for (int i = 0; i < V; ++i) d += u[i] * v[i];
+#pragma unroll
+      for (int m = LANES / 2; m >= 1; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+      const int head = h + f * SIDE;
+      if (at == 0 && head < a.H) {
+        a.nD[head * a.np + to] = -d;
+        a.nlse[head * a.np + to] = -l[f] * kLog2e;
+      }
+    }
   }
 }
 
@@ -386,9 +404,17 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
 
 cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s) {
   launch_begin("prompt_rows", s);
-  const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)a.H);
-  if (a.bf16) prompt_rows_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  else prompt_rows_kernel<float><<<grid, 256, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.N + 7) / 8));
+  if (a.bf16) {
+    using T = __nv_bfloat16;
+    if (a.dh == 32) prompt_rows_kernel<T, 32><<<grid, 256, 0, s>>>(a);
+    else if (a.dh == 64) prompt_rows_kernel<T, 64><<<grid, 256, 0, s>>>(a);
+    else prompt_rows_kernel<T, 128><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (a.dh == 32) prompt_rows_kernel<float, 32><<<grid, 256, 0, s>>>(a);
+    else if (a.dh == 64) prompt_rows_kernel<float, 64><<<grid, 256, 0, s>>>(a);
+    else prompt_rows_kernel<float, 128><<<grid, 256, 0, s>>>(a);
+  }
   cudaError_t e = launch_end("prompt_rows", s);
   if (e != cudaSuccess) return e;
   if (a.bf16) return launch_prompt_bwd_tc(a, s);

@@ -32,8 +32,10 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kT = 128;             // rows, and keys, of a tile
 constexpr int kElem = 16;           // warps that do the arithmetic: four of each 32 rows, 32 columns a warp
-constexpr int kThreads = 32 * (kElem + 3);
-constexpr int kProducts = kElem, kSums = kElem + 1, kLoads = kElem + 2;  // the warps of the other roles
+// The warps of the other roles: products; on the queries' side the sums', on the keys' side the second group's
+// products; loads.
+constexpr int kProducts = kElem, kSums = kElem + 1;
+constexpr int threads_of(int issuing) { return 32 * (kElem + issuing + 1); }
 constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -181,7 +183,7 @@ __device__ __forceinline__ bool q_item(const PromptArgs& a, const PromptTiles<kT
 
 // ------------------------------------------------------------------ the queries' side
 template <int DH>
-__global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
+__global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
   using C = Tc<DH>;
   constexpr int NK = C::NK, NB = C::NB, SUB = C::SUB;
   extern __shared__ unsigned char dsm[];
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dq_tc_kernel(PromptArgs a,
   };
   QItem it;
 
-  if (warp == kLoads) {
+  if (warp == kElem + 2) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
     for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
@@ -382,7 +384,7 @@ __device__ __forceinline__ bool kv_item(const PromptArgs& a, const PromptTiles<k
 
 // ------------------------------------------------------------------ the keys' side
 template <int DH>
-__global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
+__global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
   using C = Tc<DH>;
   constexpr int NS = C::NS, NB = C::NB, SUB = C::SUB, G = C::G;
   extern __shared__ unsigned char dsm[];
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
   };
   KvItem it;
 
-  if (warp == kLoads) {
+  if (warp == kElem + G) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
     for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
@@ -440,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_dkv_tc_kernel(PromptArgs a
       for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&sh.full[i % NS], (i / NS) & 1, 1u << 16);
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
-  } else if (warp >= kProducts + G) {
   } else if (warp >= kProducts) {
     // ---------------------------------------------------------------- products of a group
     const int w = G == 1 ? 0 : warp - kProducts;
@@ -623,11 +624,11 @@ cudaError_t run_tc(const PromptArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.N / kT + std::min<int64_t>(a.B, a.N);
   launch_begin("prompt_dkv_tc", s);
-  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), kThreads, C::SMEM_KV, s>>>(a, tm);
+  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), threads_of(C::G), C::SMEM_KV, s>>>(a, tm);
   e = launch_end("prompt_dkv_tc", s);
   if (e != cudaSuccess) return e;
   launch_begin("prompt_dq_tc", s);
-  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), kThreads, C::SMEM_Q, s>>>(a, tm);
+  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), threads_of(2), C::SMEM_Q, s>>>(a, tm);
   return launch_end("prompt_dq_tc", s);
 }
 
