@@ -11,6 +11,10 @@
                                         -> GCA forward over the retrieved chunks
   window sublayer, training:            rotary -> window attention -> its backward -> the
                                         gradient of rotary
+  packed prompts, training:             norms and rotary -> causal attention over the packed
+                                        sequences -> its backward -> the gradients of the norms
+  packed prompts, serving:              norms and rotary -> attention; keys and values go into
+                                        a quantised cache, whose retrieved chunks decode reads
   window sublayer, decoding a draft:    plan of the tree -> rotary at its positions ->
                                         attention over a paged cache; then the accepted
                                         path goes into the cache
@@ -24,8 +28,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (CHUNK, PagedCache, Workspace, default_workspace, gather_chunks, gca_backward, gca_forward, launch_count,
-               retrieve_topk, rotary, rotary_backward, scores_backward, tree_plan, window_backward, window_forward)
+from . import (CHUNK, PagedCache, QuantisedCache, Workspace, default_workspace, gather_chunks, gca_backward, gca_forward,
+               launch_count, norm_rotary, norm_rotary_backward, prompt_attention, prompt_attention_backward, retrieve_topk,
+               rotary, rotary_backward, scores_backward, tree_plan, window_backward, window_forward)
 
 
 def landmark_view(o: torch.Tensor) -> torch.Tensor:
@@ -114,6 +119,47 @@ def decode_paged(q_new, cache: PagedCache, q_lmk_new, k_lmk_store, topk=8, ws=No
     k, v = cache.store()
     o, lse = gca_forward(q_new, k, v, cache.lookup(idx), scores, shift=0, kv_shared=True, ws=ws)
     return dict(idx=idx, scores=scores, o=o, lse=lse)
+
+
+def decode_quantised(q_new, cache: QuantisedCache, q_lmk_new, k_lmk_store, topk=8, ws=None):
+    """decode_paged with the K/V store in the pages of a quantised cache: retrieval, the retrieved
+    chunks widened into a compact buffer, then the GCA forward on it.  Of a store of any length the
+    k retrieved chunks are read."""
+    ws = ws or default_workspace(q_new.device)
+    nC = k_lmk_store.shape[1]
+    idx, scores = retrieve_topk(q_lmk_new, k_lmk_store, topk, nC, False, ws=ws)
+    k, v, local = cache.read(idx, dtype=q_new.dtype)
+    o, lse = gca_forward(q_new, k, v, local, scores, shift=0, ws=ws)
+    return dict(idx=idx, scores=scores, o=o, lse=lse)
+
+
+def prompt_forward(q, k, v, offsets, q_weight, k_weight, freq, positions, window=0, interleaved=False, gain=1.0, eps=1e-6,
+                   cache: QuantisedCache = None, slots=None):
+    """Packed prompts through an attention sublayer: norms of queries and keys with rotary positions,
+    then causal attention (window > 0: over that many tokens).  q [N, H, dh], k, v [N, Hkv, dh]; offsets
+    int32 [B + 1]; positions int32 [N], each row's place in its sequence.  With a cache, the turned keys
+    and the values go behind the tokens of slots (default: sequence b is slot b).  Returns o, lse and
+    the turned q, k."""
+    qr, kr = norm_rotary(q[None], k[None], q_weight, k_weight, freq, positions, interleaved, gain, eps)
+    qr, kr = qr[0], kr[0]
+    o, lse = prompt_attention(qr, kr, v, offsets, window=window)
+    if cache is not None:
+        cache.append_packed(kr, v, offsets, slots=slots)
+    return dict(o=o, lse=lse, q=qr, k=kr)
+
+
+def prompt_step(q, k, v, dout, offsets, q_weight, k_weight, freq, positions, window=0, interleaved=False, gain=1.0, eps=1e-6):
+    """prompt_forward and its gradients (a training step's).  Returns o, lse, dq, dk, dv of q, k, v and the
+    norms' dq_weight, dk_weight (float32).  Rows of no sequence must hold finite numbers; their gradients are 0
+    (of v: not written)."""
+    r = prompt_forward(q, k, v, offsets, q_weight, k_weight, freq, positions, window, interleaved, gain, eps)
+    # The norms' weights sum over all rows, those of no sequence too.
+    grads = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
+    dq, dk, dv = prompt_attention_backward(r["q"], r["k"], v, r["o"], dout, r["lse"], offsets, window=window, dq=grads[0], dk=grads[1])
+    dq, dk = dq[None], dk[None]
+    dq, dk, dqw, dkw = norm_rotary_backward(q[None], k[None], dq, dk, q_weight, k_weight, freq, positions, interleaved, gain, eps,
+                                            dq=dq, dk=dk)
+    return dict(o=r["o"], lse=r["lse"], dq=dq[0], dk=dk[0], dv=dv, dq_weight=dqw, dk_weight=dkw)
 
 
 def window_step(q, k, v, dout, freq, window=512, positions=None, interleaved=False, gain=1.0, ws=None):

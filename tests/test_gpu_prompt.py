@@ -611,3 +611,73 @@ def test_prompt_many_tiles_a_cta(H, Hkv, dh, window):
             err = (got[a:z].double().transpose(0, 1) - want).abs()
             assert bool((err <= 2.0 ** -8 * want.abs() + e * size + 1e-30).all()), (n, float((err - e * size).max()))
         assert float((lse[a:z].double().transpose(0, 1) - L).abs().max()) <= 2e-5
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_step_against_oracle(dtype):
+    """A packed training step: norms with rotary, attention, and the gradients of all of it, against the oracle's
+    composition; in a captured graph too.  Tolerance: the repository's for its attention block, per element of
+    max(1, |x|), bf16 2e-2 and float32 1e-5 times what the norms' and sums' sizes are here (10)."""
+    g = _g()
+    lengths, H, Hkv, dh = (150, 0, 61, 200), 4, 2, 64
+    off = offsets_of(lengths)
+    N = int(off[-1])
+    q, k, v, do = (synth.normal(51, s, (N, h, dh), 1.0, dtype) for s, h in ((0, H), (1, Hkv), (2, Hkv), (3, H)))
+    wt = [np.float32(1 + 0.2 * synth.normal(51, 4 + i, (dh,))).astype(np.float64) for i in range(2)]
+    pos = np.concatenate([np.arange(n) for n in lengths])
+    w = dorc.speeds(dh)
+    args = [dev(x, dtype) for x in (q, k, v, do)] + [ints(off), dev(wt[0], "f32"), dev(wt[1], "f32"), g.rotary_frequencies(dh), ints(pos)]
+    r = pipeline.prompt_step(*args, window=100)
+    qr, kr = (orc.norm_rotary(x[None], y, pos[None], w, 1e-6)[0] for x, y in zip((q, k), wt))
+    ref = orc.prompt_attention(qr, kr, v, off, 100, dout=do)
+    dq, dqw = orc.norm_rotary_backward(q[None], ref["dq"][None], wt[0], pos[None], w, 1e-6)
+    dk, dkw = orc.norm_rotary_backward(k[None], ref["dk"][None], wt[1], pos[None], w, 1e-6)
+    tol = 2e-2 if dtype == "bf16" else 1e-4
+    for name, want in (("o", ref["o"]), ("lse", ref["lse"]), ("dq", dq[0]), ("dk", dk[0]), ("dv", ref["dv"])):
+        within(host(r[name]), want, 2 * tol * np.maximum(1, np.abs(want)), name)
+    for name, want, terms in (("dq_weight", dqw, ref["dq"]), ("dk_weight", dkw, ref["dk"])):
+        # a sum of N heads terms, each off by the rounding of the gradient that it takes: of random sign
+        lim = tol * np.sqrt((terms ** 2).sum((0, 1))).max() * 4
+        within(host(r[name]), want, lim, name)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pipeline.prompt_step(*args, window=100)
+    graph.replay()
+    assert all(torch.equal(out[n], r[n]) for n in r)
+
+
+def test_prompt_to_quantised_decode():
+    """Packed prompts into a quantised cache, then decoding over the chunks that retrieval names: the same as GCA's
+    forward over the pages' values."""
+    g = _g()
+    lengths, H, dh, D = (640, 1280, 900), 4, 64, 256
+    off = offsets_of(lengths)
+    N = int(off[-1])
+    q, k, v = (torch.randn(N, H, dh, device="cuda").bfloat16() for _ in range(3))
+    pos = ints(np.concatenate([np.arange(n) for n in lengths]))
+    wt, freq = torch.ones(dh, device="cuda"), g.rotary_frequencies(dh)
+    cache = g.QuantisedCache.empty(60, 3, 25, H, dh)
+    p = pipeline.prompt_forward(q, k, v, ints(off), wt, wt, freq, pos, cache=cache, slots=ints([2, 0, 1]))
+    cache.check()
+    assert cache.lengths.tolist() == [1280, 900, 640]
+    nC = 10  # full chunks of the shortest
+    lmk = torch.randn(3, nC, D, device="cuda").bfloat16()
+    q_new, q_lmk = torch.randn(3, 64, H, dh, device="cuda").bfloat16(), torch.randn(3, 1, D, device="cuda").bfloat16()
+    r = pipeline.decode_quantised(q_new, cache, q_lmk, lmk, topk=4)
+    kn, vn, ke, ve = cache.numbers()
+    wide = [x.float().mul(torch.exp2(e.float() - 127)[..., None]).bfloat16() for x, e in ((kn, ke), (vn, ve))]
+    pages = cache.lookup(r["idx"])
+    o, lse = g.gca_forward(q_new, wide[0].flatten(0, 1), wide[1].flatten(0, 1), pages, r["scores"], shift=0, kv_shared=True)
+    assert torch.equal(o, r["o"]) and torch.equal(lse, r["lse"])
+    # And the pages hold the prompt's keys, each within half a step of e4m3.
+    a, z = int(off[1]), int(off[2])
+    rows = wide[0][cache.table[0, :20].long()].flatten(0, 1)[:z - a].float()
+    turned = p["k"][a:z].float()
+    step = torch.exp2(torch.ceil(torch.log2(turned.abs().amax(-1, keepdim=True) / 448)) - 10)
+    assert bool(((rows - turned).abs() <= torch.maximum(turned.abs() * 2.0 ** -4, step)).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = pipeline.decode_quantised(q_new, cache, q_lmk, lmk, topk=4)
+    graph.replay()
+    assert torch.equal(again["o"], r["o"])
