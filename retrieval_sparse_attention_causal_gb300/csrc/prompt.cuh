@@ -3,6 +3,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace gca {
 
@@ -87,6 +88,43 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const Tiles& ti
 // the same ones do not always get the larger (in order, 1024 items over 152 CTAs left a CTA 13 % over the mean).
 __device__ __forceinline__ int prompt_turn(int n) {
   return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// Work items on their way from the warp that finds them to those that work on them.  Each warp finding its own took
+// two to three thousand cycles an item, most of it the way of code that is rarely run to the warp.
+template <typename I>
+struct PromptItems {
+  static constexpr int kSlots = 4;
+  uint64_t full[kSlots], empty[kSlots];
+  I item[kSlots];
+};
+template <typename I>
+__device__ __forceinline__ void init_items(PromptItems<I>& r, int readers) {  // one thread
+  for (int i = 0; i < r.kSlots; ++i) {
+    tc::mbar_init(&r.full[i], 1);
+    tc::mbar_init(&r.empty[i], readers);
+  }
+}
+// Item n, by a whole warp; `waited` as in the kernels.  False where a wait gave up.
+template <typename I, typename W>
+__device__ __forceinline__ bool put_item(PromptItems<I>& r, int n, const I& it, const W& waited, int site) {
+  const int s = n % r.kSlots;
+  if (!waited(&r.empty[s], ((n / r.kSlots) & 1) ^ 1, site, n)) return false;
+  if ((threadIdx.x & 31) == 0) {
+    r.item[s] = it;
+    tc::mbar_arrive(&r.full[s]);
+  }
+  __syncwarp();
+  return true;
+}
+template <typename I, typename W>
+__device__ __forceinline__ bool take_item(PromptItems<I>& r, int n, I& it, const W& waited, int site) {
+  const int s = n % r.kSlots;
+  if (!waited(&r.full[s], (n / r.kSlots) & 1, site, n)) return false;
+  it = r.item[s];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&r.empty[s]);
+  return true;
 }
 
 // Where the rows of sequence b begin in the backward pass's scratch rows: on 16-byte boundaries.

@@ -40,7 +40,7 @@ constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDone, kSiteAcc, kSiteAccFree, kSiteRows };
+enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDone, kSiteAcc, kSiteAccFree, kSiteRows, kSiteItem };
 
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
   return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
@@ -73,8 +73,8 @@ struct Shared {
   int keep[PromptTiles<kT>::kKeep];
 };
 
-template <int DH, int G>
-__device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh) {
+template <int DH, int G, typename I>
+__device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, PromptItems<I>& items, int readers) {
   PromptTiles<kT>::fill(a, sh.keep);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Tc<DH>::NK; ++i) {
@@ -96,6 +96,7 @@ __device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh) {
     }
     tc::mbar_init(&sh.acc, G);
     tc::mbar_init(&sh.acc_free, kElem);
+    init_items(items, readers);
     sh.abort = 0;
     tc::fence_mbar_init();
   }
@@ -171,7 +172,7 @@ struct Maps {
 // Work of the queries' side: a tile of rows of a head, and its blocks lo .. tile of keys.
 struct QItem {
   PromptTile x;
-  int h, m, lo;
+  int h, m, lo, more;  // more: 0 behind the last
 };
 __device__ __forceinline__ bool q_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, QItem& it) {
   it.h = w % a.H;
@@ -190,9 +191,9 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = tiles + NB * 2 * C::BLOCK;
   __shared__ __align__(8) Shared<DH> sh;
+  __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, 1>(a, sh);
-  const PromptTiles<kT> counts(sh.keep);
+  set_up<DH, 1>(a, sh, items, kElem + 2);
   const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320;  // S, dP, dS, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
@@ -200,11 +201,16 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
     return wait_on(bar, parity, &sh.abort, a.err, site, blockIdx.x, at);
   };
   QItem it;
+  auto take = [&](int n) { return (ok = ok && take_item(items, n, it, waited, kSiteItem)) && it.more; };
 
   if (warp == kElem + 2) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
+    const PromptTiles<kT> counts(sh.keep);
+    for (; ok; ++nt) {
+      it.more = q_item(a, counts, prompt_turn(nt), it);
+      ok = put_item(items, nt, it, waited, kSiteItem);
+      if (!ok || !it.more) break;
       const int buf = nt % NB;
       ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, nt);
       if (!ok) break;
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   } else if (warp == kProducts) {
     // ---------------------------------------------------------------- S and dP, each once the block before is in registers
     int id = 0, nt = 0;  // blocks, tiles so far
-    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
+    for (; take(nt); ++nt) {
       const uint32_t q = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), g = q + C::BLOCK;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   } else if (warp == kSums) {
     // ---------------------------------------------------------------- dQ += dS K
     int id = 0, nt = 0;
-    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
+    for (; take(nt); ++nt) {
       ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
         const int ks = 2 * id % NK;
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
     int id = 0, nt = 0;
-    for (; ok && q_item(a, counts, prompt_turn(nt), it); ++nt) {
+    for (; take(nt); ++nt) {
       const int pos = it.x.tile * kT + r;
       const bool on = pos < it.x.len;
       const int64_t row = it.h * a.np + prompt_pad(it.x.off, it.x.b) + pos;
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
 // tile .. end - 1 of rows.
 struct KvItem {
   PromptTile x;
-  int m, end;
+  int m, end, more;
 };
 __device__ __forceinline__ bool kv_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, KvItem& it) {
   it.m = w % a.Hkv;
@@ -392,9 +398,9 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
   unsigned char* ring = tiles + NB * 2 * C::BLOCK;
   float* rows = reinterpret_cast<float*>(ring + NS * 2 * C::BLOCK);  // of each stage: -lse log2(e), -D
   __shared__ __align__(8) Shared<DH> sh;
+  __shared__ __align__(8) PromptItems<KvItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, G>(a, sh);
-  const PromptTiles<kT> counts(sh.keep);
+  set_up<DH, G>(a, sh, items, kElem + G);
   // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
   const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
   bool ok = true;
@@ -403,11 +409,16 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
     return wait_on(bar, parity, &sh.abort, a.err, site, blockIdx.x, at);
   };
   KvItem it;
+  auto take = [&](int n) { return (ok = ok && take_item(items, n, it, waited, kSiteItem)) && it.more; };
 
   if (warp == kElem + G) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
+    const PromptTiles<kT> counts(sh.keep);
+    for (; ok; ++nt) {
+      it.more = kv_item(a, counts, prompt_turn(nt), it);
+      ok = put_item(items, nt, it, waited, kSiteItem);
+      if (!ok || !it.more) break;
       const int buf = nt % NB;
       ok = waited(&sh.tile_free[buf], ((nt / NB) & 1) ^ 1, kSiteTileFree, nt);
       if (!ok) break;
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
     const int w = G == 1 ? 0 : warp - kProducts;
     const uint32_t tVw = tV + 2 * DH * w, tKw = tVw + DH;
     int id = 0, nt = 0;  // blocks, tiles so far
-    for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
+    for (; take(nt); ++nt) {
       const uint32_t k = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), v = k + C::BLOCK;
       const int count = (it.end - it.x.tile) * a.g;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
@@ -495,7 +506,7 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
     int id = 0, nt = 0;
-    for (; ok && kv_item(a, counts, prompt_turn(nt), it); ++nt) {
+    for (; take(nt); ++nt) {
       const int key0 = it.x.tile * kT + 32 * (warp & 3) + group;  // keys key0 + 0, 8, 16, 24
       for (int h = 0; h < a.g && ok; ++h)
         for (int i = it.x.tile; i < it.end; ++i, ++id) {

@@ -22,6 +22,7 @@
 // memory, for a weight of 0 times what lies in them must stay 0.  dh 32 is read as 64 with zeros behind
 // it (the tensor map fills them in).
 #include <algorithm>
+#include <type_traits>
 
 #include "prompt.cuh"
 #include "tc.cuh"
@@ -39,7 +40,7 @@ constexpr uint32_t kCols = 512;   // of TMEM: two tiles' logits, then their outp
 constexpr float kMost = 16384.f;  // the largest sum of a row's weights over a block by an outgrown reference
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteQFree, kSiteS, kSiteP, kSiteDone, kSiteO, kSiteOFree, kSiteV };
+enum { kSiteFull = 1, kSiteEmpty, kSiteQ, kSiteQFree, kSiteS, kSiteP, kSiteDone, kSiteO, kSiteOFree, kSiteV, kSiteItem };
 
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
   return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
@@ -61,6 +62,7 @@ struct Item {
   int head[2], tile[2];        // of each tile of rows
   int hi[2], lo[2];            // its blocks; hi < lo: there is no such tile
   int m;                       // the key head
+  int more;                    // 0: there is none any more
   __device__ __forceinline__ int top() const { return max(hi[0], hi[1]); }
   __device__ __forceinline__ int low() const { return hi[1] < lo[1] ? lo[0] : min(lo[0], lo[1]); }
   __device__ __forceinline__ bool has(int t, int n) const { return t ? n <= hi[1] && n >= lo[1] : n <= hi[0] && n >= lo[0]; }
@@ -113,6 +115,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       bar_o[2], bar_ofree[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, keep[PromptTiles<kT>::kKeep];
+  __shared__ __align__(8) PromptItems<Item> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 320) {
     prefetch_tmap(&tmQ);
@@ -136,6 +139,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       tc::mbar_init(&bar_p[i], 4);
       tc::mbar_init(&bar_done[i], 1);
     }
+    init_items(items, kThreads / 32 - 1);
     abort_s = 0;
     tc::fence_mbar_init();
   }
@@ -152,15 +156,19 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
   // A waiting warp has to see every phase of a barrier, or its parity says nothing: so the logits' barriers are each
   // tile's own (a tile that an item lacks skips units), in turn for as many units as there are buffers.
   bool ok = true;
-  const Counts counts(keep);
   Item it;
+  auto take = [&](int n) { return (ok = ok && take_item(items, n, it, waited, kSiteItem)) && it.more; };
 
   if (warp == 10) {
     // ---------------------------------------------------------------- loads
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
     int nq[2] = {0, 0};      // tiles of rows so far
-    for (int turn = 0; ok && item_of(a, counts, prompt_turn(turn), it); ++turn) {
+    const Counts counts(keep);
+    for (int turn = 0; ok; ++turn) {
+      it.more = item_of(a, counts, prompt_turn(turn), it);
+      ok = put_item(items, turn, it, waited, kSiteItem);
+      if (!ok || !it.more) break;
       auto rows = [&](int t) {
         if (it.hi[t] < it.lo[t]) return;
         ok = ok && waited(&bar_qfree[t], (nq[t] & 1) ^ 1, kSiteQFree, turn);
@@ -200,7 +208,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int ks = 0, buf = 0, nq[2] = {0, 0}, own[2] = {0, 0};  // K's slot, the buffer; tiles and units of each tile's warps so far
     uint32_t kp = 0, bp = 1;              // the parities of K's filling, and of the buffer's last use
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
-    for (int turn = 0; ok && item_of(a, counts, prompt_turn(turn), it); ++turn) {
+    for (int turn = 0; take(turn); ++turn) {
       const int low = it.low();
       for (int n = it.top(); n >= low && ok; --n) {
         ok = waited(&bar_full[ks], kp, kSiteFull, n);
@@ -239,7 +247,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     // ---------------------------------------------------------------- outputs: O += P V
     int vs = 1, buf = 0, no[2] = {0, 0};
     uint32_t vp = 0, bp = 0;
-    for (int turn = 0; ok && item_of(a, counts, prompt_turn(turn), it); ++turn) {
+    for (int turn = 0; take(turn); ++turn) {
       const int low = it.low();
       for (int n = it.top(); n >= low && ok; --n) {
         ok = waited(&bar_full[vs], vp, kSiteFull, n);
@@ -283,8 +291,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + NBUF * kT + DH * t + lanes;
     int unit0 = 0, slot = 0, no = 0, own = 0;  // units of work and ring slots before the item, own tiles and own units so far
-    bool there = item_of(a, counts, prompt_turn(0), it);
-    for (int turn = 1; ok && there; ++turn) {
+    for (int turn = 0; take(turn); ++turn) {
       const int hi = it.hi[t], lo = it.lo[t], top = it.top();
       const int pos = it.tile[t] * kT + r;
       const bool on = pos < it.x.len;
@@ -323,25 +330,46 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
         ++own;
         if (!ok) break;
         tc::fence_after();
-        const bool inner = n < hi && n >= whole;
         bool done = false;
-        if (__builtin_expect(inner, 1)) {
-          // Seen whole, by references that hold: one straight run.
-          float s0[32], s1[32];
+        // Keys c0 .. c1 - 1 of the block are seen.
+        const int c0 = max(first - n * kT, 0), c1 = on ? min(pos - n * kT + 1, kT) : 0;
+        auto seen = [&](int q) {  // of quarter q, a bit a key
+          const int lo = min(max(c0 - 32 * q, 0), 32), n1 = min(max(c1 - 32 * q, 0), 32);
+          return lo >= n1 ? 0u : (n1 == 32 ? ~0u : (1u << n1) - 1) & ~((1u << lo) - 1);
+        };
+        if (__builtin_expect(n < hi, 1)) {
+          // By references that hold: one straight run.
           uint32_t p[64];
-          sums[0] = sums[1] = sums[2] = sums[3] = 0;
-          tc::ld32x32b_x32(tS, s0);
-          tc::ld_wait_row(s0);
-          tc::ld32x32b_x32(tS + 32, s1);  // on its way while the first quarter is weighed
-          weigh(s0, p);
-          tc::ld_wait_row(s1);
-          tc::ld32x32b_x32(tS + 64, s0);
-          weigh(s1, p + 16);
-          tc::ld_wait_row(s0);
-          tc::ld32x32b_x32(tS + 96, s1);
-          weigh(s0, p + 32);
-          tc::ld_wait_row(s1);
-          weigh(s1, p + 48);
+          auto run = [&](auto edge) {
+            float s0[32], s1[32];
+            auto hide = [&](int q, float (&s)[32]) {
+              if constexpr (decltype(edge)::value) {
+                const uint32_t see = seen(q);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((see >> i) & 1)) s[i] = -CUDART_INF_F;
+              }
+            };
+            sums[0] = sums[1] = sums[2] = sums[3] = 0;
+            tc::ld32x32b_x32(tS, s0);
+            tc::ld_wait_row(s0);
+            tc::ld32x32b_x32(tS + 32, s1);  // on its way while the first quarter is weighed
+            hide(0, s0);
+            weigh(s0, p);
+            tc::ld_wait_row(s1);
+            tc::ld32x32b_x32(tS + 64, s0);
+            hide(1, s1);
+            weigh(s1, p + 16);
+            tc::ld_wait_row(s0);
+            tc::ld32x32b_x32(tS + 96, s1);
+            hide(2, s0);
+            weigh(s0, p + 32);
+            tc::ld_wait_row(s1);
+            hide(3, s1);
+            weigh(s1, p + 48);
+          };
+          if (__builtin_expect(n >= whole, 1)) run(std::false_type{});
+          else run(std::true_type{});  // the window's edge
           const float sum = total();
           if (__builtin_expect(!__any_sync(kAll, sum > kMost), 1)) {
             l += sum;
@@ -354,9 +382,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
           }
         }
         if (__builtin_expect(!done, 0)) {
-          // Keys c0 .. c1 - 1 of the block are seen: by some row of the warp those of quarters q0 .. q1 - 1.  The maximum
-          // with this block, and the weights by it.
-          const int c0 = max(first - n * kT, 0), c1 = on ? min(pos - n * kT + 1, kT) : 0;
+          // Some row of the warp sees keys of quarters q0 .. q1 - 1.  The maximum with this block, and the weights by it.
           const int q0 = min(__shfl_sync(kAll, c0, 0) / 32, 4), q1 = ((int)__reduce_max_sync(kAll, c1) + 31) / 32;
           if (n == hi && (n + 1) * kT > it.x.len) {
             // Rows of V behind the sequence become zeros (by this tile's softmax where it is the tile that
@@ -376,8 +402,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
           auto logits = [&](int q, float (&s)[32]) {
             tc::ld32x32b_x32(tS + 32 * q, s);
             tc::ld_wait_row(s);
-            const int lo = min(max(c0 - 32 * q, 0), 32), n1 = min(max(c1 - 32 * q, 0), 32);
-            const uint32_t see = lo >= n1 ? 0u : (n1 == 32 ? ~0u : (1u << n1) - 1) & ~((1u << lo) - 1);
+            const uint32_t see = seen(q);
             if (__all_sync(kAll, see == ~0u)) return;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -441,7 +466,6 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       unit0 += it.units();
       slot += 2 * (top - it.low() + 1);
       const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
-      if (ok) there = item_of(a, counts, prompt_turn(turn), it);  // the next item, while the last products run
       if (!ok || hi < lo) continue;
       ok = waited(&bar_o[t], no & 1, kSiteO, -1);  // (of its own: a buffer's could be two units further by now)
       ++no;
