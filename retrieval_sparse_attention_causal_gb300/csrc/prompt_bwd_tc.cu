@@ -1,6 +1,6 @@
 // Gradients of the attention over packed sequences, bf16, on the 5th-generation tensor cores.
 //
-// Two passes without atomics, as in window_bwd.cu: the queries' side (dQ) walks the keys that a tile of
+// Two passes without atomics, as in window_bwd.cu: first the queries' side (dQ, and a better D) walks the keys that a tile of
 // 128 rows sees, the keys' side (dK, dV) the rows that see a tile of 128 keys, of all heads that share it.
 // Each computes the logits and <dO, V> anew: 3 and 4 products of 128 x 128 x dh a pair of tiles, 7 where
 // the gradients themselves need 5.  Both are persistent, a CTA an SM: one warp loads, one or two issue the
@@ -40,7 +40,7 @@ constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDone, kSiteAcc, kSiteAccFree, kSiteRows, kSiteItem };
+enum { kSiteFull = 1, kSiteEmpty, kSiteTile, kSiteTileFree, kSiteS, kSiteDp, kSiteP, kSiteTaken, kSiteDs, kSiteDone, kSiteAcc, kSiteAccFree, kSiteRows, kSiteRest, kSiteItem };
 
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort_flag, ErrWord* err, int site, int tile, int at) {
   return __all_sync(kAll, park_or_abort(bar, parity, abort_flag, err, site, tile, at)) != 0;
@@ -67,6 +67,7 @@ struct Shared {
   uint64_t s[2], dp[2];                          // products that are there: S and dP (or their transposes)
   uint64_t s_taken[2], dp_taken[2];              // ... that are in registers
   uint64_t p[2], ds[2], done[2];                 // P and dS in TMEM; dS's product done
+  uint64_t rest;                                 // queries' side: the rows' sums of dS in TMEM
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
@@ -94,6 +95,7 @@ __device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, Prom
       tc::mbar_init(&sh.ds[i], kElem / G);
       tc::mbar_init(&sh.done[i], 1);
     }
+    tc::mbar_init(&sh.rest, kElem);
     tc::mbar_init(&sh.acc, G);
     tc::mbar_init(&sh.acc_free, kElem);
     init_items(items, readers);
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   set_up<DH, 1>(a, sh, items, kElem + 2);
-  const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320;  // S, dP, dS, dQ
+  const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320, tR = tS + 448;  // S, dP, dS, dQ, sums of dS
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
@@ -291,6 +293,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       const int64_t row = it.h * a.np + prompt_pad(it.x.off, it.x.b) + pos;
       const float nl = on ? a.nlse[row] : -CUDART_INF_F, nd = on ? a.nD[row] : 0.f;  // a row that does not exist weighs nothing
       const uint64_t nl2 = tc::f2(nl, nl), nd2 = tc::f2(nd, nd);
+      uint64_t rest = 0;  // sum of dS
       const int first = a.window ? max(0, pos - a.window + 1) : 0;
       const int whole = a.window ? (max(0, it.x.tile * kT + kT - a.window) + kT - 1) / kT : 0;
       for (int n = it.lo; n <= it.x.tile; ++n, ++id) {
@@ -328,6 +331,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
               if (2 * i < c0 || 2 * i >= c1) x = 0.f;
               if (2 * i + 1 < c0 || 2 * i + 1 >= c1) y = 0.f;
             }
+            rest = tc::add2(rest, tc::f2(x, y));
             d[i] = pack_bf16(x, y);
           }
         };
@@ -361,6 +365,26 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       const int col = part * (DH / 4);
       bf16* to = reinterpret_cast<bf16*>(a.dq) + (int64_t)(it.x.off + pos) * a.dq_ts + it.h * a.dq_hs;
       if (col < a.dh) write_row<DH / 4, 1>(tQ + lanes + col, 0, to + col, a.scale, on);
+      // A row of dS sums to 0 by its D; what is left is how far D, of the rounded output, is off.  The keys' side takes
+      // the D that is right: in rows that see few keys the difference is as large as the roundings of dS.
+      // (The parts' sums meet in spare columns of TMEM; those of the item before last have been read, for each block
+      // since has needed the warps that read them.)
+      float x, y;
+      tc::uf2(rest, x, y);
+      const uint32_t spare = tR + lanes + 4 * (nt & 1);
+      tc::st32x32b_x1(spare + part, __float_as_uint(x + y));
+      tc::st_wait();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.rest);
+      if (part == 0) {
+        ok = waited(&sh.rest, nt & 1, kSiteRest, nt);
+        if (!ok) break;
+        tc::fence_after();
+        float part_of[4];
+        tc::ld32x32b_x4(spare, part_of);
+        if (on) a.nD[row] = nd - ((part_of[0] + part_of[1]) + (part_of[2] + part_of[3]));
+      }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.acc_free);
@@ -634,13 +658,13 @@ cudaError_t run_tc(const PromptArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = allow_smem((const void*)prompt_dkv_tc_kernel<DH>, C::SMEM_KV);
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.N / kT + std::min<int64_t>(a.B, a.N);
-  launch_begin("prompt_dkv_tc", s);
-  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), threads_of(C::G), C::SMEM_KV, s>>>(a, tm);
-  e = launch_end("prompt_dkv_tc", s);
-  if (e != cudaSuccess) return e;
   launch_begin("prompt_dq_tc", s);
   prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), threads_of(2), C::SMEM_Q, s>>>(a, tm);
-  return launch_end("prompt_dq_tc", s);
+  e = launch_end("prompt_dq_tc", s);
+  if (e != cudaSuccess) return e;
+  launch_begin("prompt_dkv_tc", s);
+  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), threads_of(C::G), C::SMEM_KV, s>>>(a, tm);
+  return launch_end("prompt_dkv_tc", s);
 }
 
 }  // namespace

@@ -330,59 +330,56 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
         ++own;
         if (!ok) break;
         tc::fence_after();
-        bool done = false;
-        // Keys c0 .. c1 - 1 of the block are seen.
-        const int c0 = max(first - n * kT, 0), c1 = on ? min(pos - n * kT + 1, kT) : 0;
-        auto seen = [&](int q) {  // of quarter q, a bit a key
-          const int lo = min(max(c0 - 32 * q, 0), 32), n1 = min(max(c1 - 32 * q, 0), 32);
+        // Of quarter q of the block, a bit a key that the row sees.
+        auto seen = [&](int q) {
+          const int lo = min(max(first - n * kT - 32 * q, 0), 32), n1 = on ? min(max(pos - n * kT + 1 - 32 * q, 0), 32) : 0;
           return lo >= n1 ? 0u : (n1 == 32 ? ~0u : (1u << n1) - 1) & ~((1u << lo) - 1);
         };
-        if (__builtin_expect(n < hi, 1)) {
-          // By references that hold: one straight run.
+        // The block's weights by references that hold, in one straight run; false where one is outgrown.
+        auto run = [&](auto edge) {
+          float s0[32], s1[32];
           uint32_t p[64];
-          auto run = [&](auto edge) {
-            float s0[32], s1[32];
-            auto hide = [&](int q, float (&s)[32]) {
-              if constexpr (decltype(edge)::value) {
-                const uint32_t see = seen(q);
+          auto hide = [&](int q, float (&s)[32]) {
+            if constexpr (decltype(edge)::value) {
+              const uint32_t see = seen(q);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((see >> i) & 1)) s[i] = -CUDART_INF_F;
-              }
-            };
-            sums[0] = sums[1] = sums[2] = sums[3] = 0;
-            tc::ld32x32b_x32(tS, s0);
-            tc::ld_wait_row(s0);
-            tc::ld32x32b_x32(tS + 32, s1);  // on its way while the first quarter is weighed
-            hide(0, s0);
-            weigh(s0, p);
-            tc::ld_wait_row(s1);
-            tc::ld32x32b_x32(tS + 64, s0);
-            hide(1, s1);
-            weigh(s1, p + 16);
-            tc::ld_wait_row(s0);
-            tc::ld32x32b_x32(tS + 96, s1);
-            hide(2, s0);
-            weigh(s0, p + 32);
-            tc::ld_wait_row(s1);
-            hide(3, s1);
-            weigh(s1, p + 48);
-          };
-          if (__builtin_expect(n >= whole, 1)) run(std::false_type{});
-          else run(std::true_type{});  // the window's edge
-          const float sum = total();
-          if (__builtin_expect(!__any_sync(kAll, sum > kMost), 1)) {
-            l += sum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t q[8] = {p[8 * i], p[8 * i + 1], p[8 * i + 2], p[8 * i + 3], p[8 * i + 4], p[8 * i + 5], p[8 * i + 6], p[8 * i + 7]};
-              tc::st32x32b_x8(tS + 8 * i, q);
+              for (int i = 0; i < 32; ++i)
+                if (!((see >> i) & 1)) s[i] = -CUDART_INF_F;
             }
-            done = true;
+          };
+          sums[0] = sums[1] = sums[2] = sums[3] = 0;
+          tc::ld32x32b_x32(tS, s0);
+          tc::ld_wait_row(s0);
+          tc::ld32x32b_x32(tS + 32, s1);  // on its way while the first quarter is weighed
+          hide(0, s0);
+          weigh(s0, p);
+          tc::ld_wait_row(s1);
+          tc::ld32x32b_x32(tS + 64, s0);
+          hide(1, s1);
+          weigh(s1, p + 16);
+          tc::ld_wait_row(s0);
+          tc::ld32x32b_x32(tS + 96, s1);
+          hide(2, s0);
+          weigh(s0, p + 32);
+          tc::ld_wait_row(s1);
+          hide(3, s1);
+          weigh(s1, p + 48);
+          const float sum = total();
+          if (__builtin_expect(__any_sync(kAll, sum > kMost), 0)) return false;
+          l += sum;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t q[8] = {p[8 * i], p[8 * i + 1], p[8 * i + 2], p[8 * i + 3], p[8 * i + 4], p[8 * i + 5], p[8 * i + 6], p[8 * i + 7]};
+            tc::st32x32b_x8(tS + 8 * i, q);
           }
-        }
+          return true;
+        };
+        bool done = false;
+        if (__builtin_expect(n < hi && n >= whole, 1)) done = run(std::false_type{});
+        else if (n < hi) done = run(std::true_type{});  // the window's edge
         if (__builtin_expect(!done, 0)) {
           // Some row of the warp sees keys of quarters q0 .. q1 - 1.  The maximum with this block, and the weights by it.
+          const int c0 = max(first - n * kT, 0), c1 = on ? min(pos - n * kT + 1, kT) : 0;  // keys c0 .. c1 - 1 are seen
           const int q0 = min(__shfl_sync(kAll, c0, 0) / 32, 4), q1 = ((int)__reduce_max_sync(kAll, c1) + 31) / 32;
           if (n == hi && (n + 1) * kT > it.x.len) {
             // Rows of V behind the sequence become zeros (by this tile's softmax where it is the tile that

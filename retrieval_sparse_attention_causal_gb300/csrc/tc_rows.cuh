@@ -56,6 +56,17 @@ __device__ __forceinline__ void st32x32b_x8(uint32_t taddr, const uint32_t (&v)[
                : "memory");
 }
 
+// One 32-bit column of the thread's lane, and four (with the wait).
+__device__ __forceinline__ void st32x32b_x1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void ld32x32b_x4(uint32_t taddr, float (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]));
+}
+
 // Announcement of `bytes`, and a 4-D TMA tile load, by one elected lane of a converged warp that
 // calls with the same operands (a one-lane branch around them costs about twice the issue time).
 __device__ __forceinline__ void mbar_expect_tx_warp(uint64_t* bar, uint32_t bytes) {
