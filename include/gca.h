@@ -510,7 +510,7 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
 GCA_API gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* k, const gca_heads* v, gca_dtype dtype, int N,
                                 int B, int H, int Hkv, int dh, const int32_t* offsets, int window, float scale, void* o,
                                 float* lse, void* ws, size_t ws_bytes, gca_stream_t stream);
-GCA_API size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H);
+GCA_API size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H, int Hkv, int dh, gca_dtype dtype);
 GCA_API gca_status gca_prompt_attention_backward(const gca_heads* q, const gca_heads* k, const gca_heads* v, const void* o,
                                          const gca_heads* dout, const float* lse, gca_dtype dtype, int N, int B, int H,
                                          int Hkv, int dh, const int32_t* offsets, int window, float scale,

@@ -103,7 +103,7 @@ def _load():
         "gca_norm_rotary_backward_scratch_size": (SZ, [I]),
         "gca_norm_rotary_backward": (I, [HP, HP, HP, HP, HP, HP, I, I, I, I, I, I, I, I, F, P, P, P, P, I64, F, P, P, P, SZ, P]),
         "gca_prompt_attention": (I, [HP, HP, HP, I, I, I, I, I, I, P, I, F, P, P, P, SZ, P]),
-        "gca_prompt_attention_backward_scratch_size": (SZ, [I, I, I]),
+        "gca_prompt_attention_backward_scratch_size": (SZ, [I, I, I, I, I, I]),
         "gca_prompt_attention_backward": (I, [HP, HP, HP, P, HP, P, I, I, I, I, I, I, P, I, F, HP, HP, HP, P, SZ, P, SZ, P]),
         "gca_cache_row_bytes": (SZ, [I, I, I]),
         "gca_cache_append_quantised_scratch_size": (SZ, [I, I, I]),

@@ -812,9 +812,9 @@ extern "C" gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* 
   return GCA_OK;
 }
 
-extern "C" size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H) {
-  if (N < 1 || B < 1 || H < 1) return 256;
-  return 2 * align256((size_t)prompt_scratch_rows(N, B) * H * sizeof(float));
+extern "C" size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H, int Hkv, int dh, gca_dtype dtype) {
+  if (N < 1 || B < 1 || H < 1 || Hkv < 1 || dh < 1) return 256;
+  return 2 * align256((size_t)prompt_scratch_rows(N, B) * H * sizeof(float)) + align256(prompt_parts_bytes(N, B, Hkv, dh, dtype == GCA_BF16));
 }
 
 extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gca_heads* k, const gca_heads* v, const void* o,
@@ -833,7 +833,7 @@ extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gc
     if ((st = check_packed(x.t, esize, N, x.heads, x.what)) != GCA_OK) return st;
   if (strides_overlap(*dq, 1, N, H, dh) || strides_overlap(*dk, 1, N, Hkv, dh) || strides_overlap(*dv, 1, N, Hkv, dh))
     return fail(GCA_ERR_INVALID_ARG, "output strides make elements overlap");
-  if ((st = check_scratch(scratch, scratch_bytes, gca_prompt_attention_backward_scratch_size(N, B, H))) != GCA_OK) return st;
+  if ((st = check_scratch(scratch, scratch_bytes, gca_prompt_attention_backward_scratch_size(N, B, H, Hkv, dh, dtype))) != GCA_OK) return st;
   PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
   a.dout = dout->data; a.do_ts = N > 1 ? dout->token_stride : 0; a.do_hs = H > 1 ? dout->head_stride : 0;
   a.dq = dq->data; a.dq_ts = dq->token_stride; a.dq_hs = dq->head_stride;
@@ -841,7 +841,9 @@ extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gc
   a.dv = dv->data; a.dv_ts = dv->token_stride; a.dv_hs = dv->head_stride;
   a.np = prompt_scratch_rows(N, B);
   a.nlse = static_cast<float*>(scratch);
-  a.nD = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + align256((size_t)a.np * H * sizeof(float)));
+  const size_t rows = align256((size_t)a.np * H * sizeof(float));
+  a.nD = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + rows);
+  a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + 2 * rows);
   cudaError_t e = launch_prompt_backward(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gca_prompt_attention_backward launch");
   return GCA_OK;

@@ -364,7 +364,7 @@ PyObject* prompt_attention_backward(Args a) {
   if (!dk) k_new = at::empty({x.N, x.Hkv, x.dh}, on.options(x.q.scalar_type()));
   if (!dv) v_new = at::empty({x.N, x.Hkv, x.dh}, on.options(x.q.scalar_type()));
   const Word w(ws, on);
-  const Scratch s(gca_prompt_attention_backward_scratch_size((int)x.N, (int)x.B, (int)x.H), on);
+  const Scratch s(gca_prompt_attention_backward_scratch_size((int)x.N, (int)x.B, (int)x.H, (int)x.Hkv, (int)x.dh, dtype_of(x.q)), on);
   const gca_heads q = rows(x.q), k = rows(x.k), v = rows(x.v), g = rows(dout), gq = rows(dq ? *dq : q_new), gk = rows(dk ? *dk : k_new),
                   gv = rows(dv ? *dv : v_new);
   check(gca_prompt_attention_backward(&q, &k, &v, o.data_ptr(), &g, static_cast<const float*>(lse.data_ptr()), dtype_of(x.q), (int)x.N, (int)x.B,
@@ -502,6 +502,12 @@ gca_cache quantised_of(Args a, PyObject* heads, PyObject* dh, On& on) {
   need(c.heads >= 1 && c.dh >= 1 && (int64_t)gca_cache_row_bytes(GCA_E4M3, c.heads, c.dh) == tensor(a[0], "k_pages").size(2),
        "a row of the pages must be gca_cache_row_bytes(GCA_E4M3, heads, dh) bytes");
   return c;
+}
+// The cache's five, heads, dh: refused where a call on them would be.
+PyObject* check_quantised(Args a) {
+  On on;
+  quantised_of(a, a[5], a[6], on);
+  Py_RETURN_NONE;
 }
 // The cache's five, then: heads, dh, k_new, v_new, counts, path, offsets, slots, ws (offsets: k_new, v_new are packed)
 PyObject* append_quantised(Args a) {
@@ -655,7 +661,7 @@ PyMethodDef g_methods[] = {
     method<compact, 6>("compact"), method<lookup, 8>("lookup"),
     method<norm_rotary, 11>("norm_rotary"), method<norm_rotary_backward, 13>("norm_rotary_backward"),
     method<prompt_attention, 9>("prompt_attention"), method<prompt_attention_backward, 13>("prompt_attention_backward"),
-    method<append_quantised, 14>("append_quantised"), method<read_quantised, 11>("read_quantised"),
+    method<check_quantised, 7>("check_quantised"), method<append_quantised, 14>("append_quantised"), method<read_quantised, 11>("read_quantised"),
     method<error_word_of, 1>("error_word"), method<set_error, 1>("set_error"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_gca_decoding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -11,7 +11,9 @@
 // Float32 (prompt_tc.cu and prompt_bwd_tc.cu have bf16): tiles of 64 rows by 64 keys, operands in
 // shared memory with rows padded by four floats, 16 x 16 threads with 4 x 4 logits and 4 x dh / 16
 // outputs each.  Both products read two vectors of four floats for 16 multiplications, so the CUDA cores
-// and shared memory are busy at about the same rate.
+// and shared memory are busy at about the same rate.  The next tile's loads run while this one is worked
+// on.  Where the keys' tiles are too few to fill the GPU, the rows that see one are divided among CTAs,
+// whose sums a last kernel adds in order.
 #include <algorithm>
 
 #include "prompt.cuh"
@@ -30,22 +32,32 @@ struct Simt {
   static constexpr int CV = DH / 16;                      // columns of a thread's outputs
 };
 
-// Rows of a tile into shared memory; what lies behind the sequence counts as zeros.
-template <typename T, int DH>
-__device__ __forceinline__ void load_tile(float* to, const T* from, int64_t stride, int rows) {
-  constexpr int V = Elem<T>::kVec, U = DH / V;
-  for (int u = threadIdx.x; u < kT * U; u += kThreads) {
-    const int r = u / U, c = (u - r * U) * V;
-    float f[V];
-    if (r < rows) {
-      unpack16(*reinterpret_cast<const uint4*>(from + r * stride + c), f, (const T*)nullptr);
-    } else {
+// Rows of a tile on their way: into registers, then into shared memory.  What lies behind the sequence counts
+// as zeros.
+template <int DH>
+struct Rows {
+  static constexpr int U = DH / 4, N = kT * U / kThreads;  // vectors of four floats of a row, and of a thread
+  float4 x[N];
+  __device__ __forceinline__ void fetch(const float* from, int64_t stride, int rows) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = 0.f;
+    for (int n = 0; n < N; ++n) {
+      const int u = threadIdx.x + n * kThreads, r = u / U, c = u % U * 4;
+      x[n] = r < rows ? *reinterpret_cast<const float4*>(from + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-#pragma unroll
-    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(to + r * Simt<DH>::LD + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
   }
+  __device__ __forceinline__ void put(float* to) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int u = threadIdx.x + n * kThreads, r = u / U, c = u % U * 4;
+      *reinterpret_cast<float4*>(to + r * Simt<DH>::LD + c) = x[n];
+    }
+  }
+};
+template <int DH>
+__device__ __forceinline__ void load_tile(float* to, const float* from, int64_t stride, int rows) {
+  Rows<DH> r;
+  r.fetch(from, stride, rows);
+  r.put(to);
 }
 
 // s[i][j] = <A row ty + 16 i, B row tx + 16 j>.
@@ -139,7 +151,7 @@ __device__ __forceinline__ int last_rows(const PromptArgs& a, int k, int len) {
   return most / kT + 1;
 }
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
   using C = Simt<DH>;
   extern __shared__ float sm[];
@@ -148,9 +160,9 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
   int h;
   if (!my_tile(a, a.H, false, x, h)) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, t0 = x.tile * kT, m = h / a.g;
-  load_tile<T, DH>(Q, reinterpret_cast<const T*>(a.q) + (int64_t)(x.off + t0) * a.q_ts + h * a.q_hs, a.q_ts, x.len - t0);
-  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
-  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
+  load_tile<DH>(Q, reinterpret_cast<const float*>(a.q) + (int64_t)(x.off + t0) * a.q_ts + h * a.q_hs, a.q_ts, x.len - t0);
+  const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
+  const float* v = reinterpret_cast<const float*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
   float o[4][C::CV] = {}, mx[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -158,11 +170,18 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     l[i] = 0.f;
   }
   const float sl2 = a.scale * kLog2e;
+  Rows<DH> kr, vr;
+  auto fetch = [&](int j) {
+    kr.fetch(k + (int64_t)j * kT * a.k_ts, a.k_ts, x.len - j * kT);
+    vr.fetch(v + (int64_t)j * kT * a.v_ts, a.v_ts, x.len - j * kT);
+  };
+  fetch(first_keys(a, t0));
   for (int j = first_keys(a, t0); j <= x.tile; ++j) {
     __syncthreads();
-    load_tile<T, DH>(K, k + (int64_t)j * kT * a.k_ts, a.k_ts, x.len - j * kT);
-    load_tile<T, DH>(V, v + (int64_t)j * kT * a.v_ts, a.v_ts, x.len - j * kT);
+    kr.put(K);
+    vr.put(V);
     __syncthreads();
+    if (j < x.tile) fetch(j + 1);
     float s[4][4];
     products<DH>(Q, K, s);
 #pragma unroll
@@ -198,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     const int64_t row = (int64_t)(x.off + t) * a.H + h;
     const float inv = 1.f / l[i];
 #pragma unroll
-    for (int c = 0; c < C::CV; ++c) Elem<T>::st(reinterpret_cast<T*>(a.o) + row * DH + column<DH>(c), o[i][c] * inv);
+    for (int c = 0; c < C::CV; ++c) reinterpret_cast<float*>(a.o)[row * DH + column<DH>(c)] = o[i][c] * inv;
     if (tx == 0) a.lse[row] = mx[i] * a.scale + logf(l[i]);
   }
 }
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
   }
 }
 
-template <typename T, int DH>
+template <int DH>
 __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) {
   using C = Simt<DH>;
   extern __shared__ float sm[];
@@ -264,10 +283,10 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) 
   int h;
   if (!my_tile(a, a.H, false, x, h)) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, t0 = x.tile * kT, m = h / a.g;
-  load_tile<T, DH>(Q, reinterpret_cast<const T*>(a.q) + (int64_t)(x.off + t0) * a.q_ts + h * a.q_hs, a.q_ts, x.len - t0);
-  load_tile<T, DH>(G, reinterpret_cast<const T*>(a.dout) + (int64_t)(x.off + t0) * a.do_ts + h * a.do_hs, a.do_ts, x.len - t0);
-  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
-  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
+  load_tile<DH>(Q, reinterpret_cast<const float*>(a.q) + (int64_t)(x.off + t0) * a.q_ts + h * a.q_hs, a.q_ts, x.len - t0);
+  load_tile<DH>(G, reinterpret_cast<const float*>(a.dout) + (int64_t)(x.off + t0) * a.do_ts + h * a.do_hs, a.do_ts, x.len - t0);
+  const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
+  const float* v = reinterpret_cast<const float*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
   float dq[4][C::CV] = {}, nl[4], nd[4];
   const int64_t rows = h * a.np + prompt_pad(x.off, x.b) + t0;
 #pragma unroll
@@ -277,11 +296,18 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) 
     nd[i] = on ? a.nD[rows + ty + 16 * i] : 0.f;
   }
   const float sl2 = a.scale * kLog2e;
+  Rows<DH> kr, vr;
+  auto fetch = [&](int j) {
+    kr.fetch(k + (int64_t)j * kT * a.k_ts, a.k_ts, x.len - j * kT);
+    vr.fetch(v + (int64_t)j * kT * a.v_ts, a.v_ts, x.len - j * kT);
+  };
+  fetch(first_keys(a, t0));
   for (int j = first_keys(a, t0); j <= x.tile; ++j) {
     __syncthreads();
-    load_tile<T, DH>(K, k + (int64_t)j * kT * a.k_ts, a.k_ts, x.len - j * kT);
-    load_tile<T, DH>(V, v + (int64_t)j * kT * a.v_ts, a.v_ts, x.len - j * kT);
+    kr.put(K);
+    vr.put(V);
     __syncthreads();
+    if (DH <= 64 && j < x.tile) fetch(j + 1);
     float s[4][4], dp[4][4];
     products<DH>(Q, K, s);
     products<DH>(G, V, dp);
@@ -294,18 +320,21 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) 
       }
     __syncthreads();
     weighted<DH>(S, K, dq);
+    if (DH > 64 && j < x.tile) fetch(j + 1);  // (no registers for it before)
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = t0 + ty + 16 * i;
     if (t >= x.len) continue;
-    T* to = reinterpret_cast<T*>(a.dq) + (int64_t)(x.off + t) * a.dq_ts + h * a.dq_hs;
+    float* to = reinterpret_cast<float*>(a.dq) + (int64_t)(x.off + t) * a.dq_ts + h * a.dq_hs;
 #pragma unroll
-    for (int c = 0; c < C::CV; ++c) Elem<T>::st(to + column<DH>(c), dq[i][c] * a.scale);
+    for (int c = 0; c < C::CV; ++c) to[column<DH>(c)] = dq[i][c] * a.scale;
   }
 }
 
-template <typename T, int DH>
+// Part blockIdx.y of gridDim.y of the rows that see a tile of keys: a run of (head, tile of rows), the tiles of the
+// first head first.
+template <int DH>
 __global__ void __launch_bounds__(kThreads) prompt_dkv_simt_kernel(PromptArgs a) {
   using C = Simt<DH>;
   extern __shared__ float sm[];
@@ -314,111 +343,165 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_simt_kernel(PromptArgs a)
   int m;
   if (!my_tile(a, a.Hkv, true, x, m)) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, k0 = x.tile * kT;
-  load_tile<T, DH>(K, reinterpret_cast<const T*>(a.k) + (int64_t)(x.off + k0) * a.k_ts + m * a.k_hs, a.k_ts, x.len - k0);
-  load_tile<T, DH>(V, reinterpret_cast<const T*>(a.v) + (int64_t)(x.off + k0) * a.v_ts + m * a.v_hs, a.v_ts, x.len - k0);
+  load_tile<DH>(K, reinterpret_cast<const float*>(a.k) + (int64_t)(x.off + k0) * a.k_ts + m * a.k_hs, a.k_ts, x.len - k0);
+  load_tile<DH>(V, reinterpret_cast<const float*>(a.v) + (int64_t)(x.off + k0) * a.v_ts + m * a.v_hs, a.v_ts, x.len - k0);
   float dk[4][C::CV] = {}, dv[4][C::CV] = {};
   const float sl2 = a.scale * kLog2e;
-  const int end = last_rows(a, min(k0 + kT, x.len) - 1, x.len);
-  for (int h = m * a.g; h < m * a.g + a.g; ++h) {
-    const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)x.off * a.q_ts + h * a.q_hs;
-    const T* g = reinterpret_cast<const T*>(a.dout) + (int64_t)x.off * a.do_ts + h * a.do_hs;
-    const int64_t rows = h * a.np + prompt_pad(x.off, x.b);
-    for (int i = x.tile; i < end; ++i) {
-      __syncthreads();
-      load_tile<T, DH>(Q, q + (int64_t)i * kT * a.q_ts, a.q_ts, x.len - i * kT);
-      load_tile<T, DH>(G, g + (int64_t)i * kT * a.do_ts, a.do_ts, x.len - i * kT);
-      __syncthreads();
-      float s[4][4], dp[4][4];
-      products<DH>(K, Q, s);
-      products<DH>(V, G, dp);
+  const int tiles = last_rows(a, min(k0 + kT, x.len) - 1, x.len) - x.tile, steps = a.g * tiles;
+  const int w0 = (int)((int64_t)steps * blockIdx.y / gridDim.y), w1 = (int)((int64_t)steps * (blockIdx.y + 1) / gridDim.y);
+  Rows<DH> qr, gr;
+  auto fetch = [&](int w) {
+    const int h = m * a.g + w / tiles, i = x.tile + w % tiles;
+    qr.fetch(reinterpret_cast<const float*>(a.q) + (int64_t)(x.off + i * kT) * a.q_ts + h * a.q_hs, a.q_ts, x.len - i * kT);
+    gr.fetch(reinterpret_cast<const float*>(a.dout) + (int64_t)(x.off + i * kT) * a.do_ts + h * a.do_hs, a.do_ts, x.len - i * kT);
+  };
+  if (w0 < w1) fetch(w0);
+  for (int w = w0; w < w1; ++w) {
+    const int i = x.tile + w % tiles;
+    const int64_t rows = (m * a.g + w / tiles) * a.np + prompt_pad(x.off, x.b);
+    __syncthreads();
+    qr.put(Q);
+    gr.put(G);
+    __syncthreads();
+    if (DH <= 64 && w + 1 < w1) fetch(w + 1);
+    float s[4][4], dp[4][4];
+    products<DH>(K, Q, s);
+    products<DH>(V, G, dp);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int t = i * kT + tx + 16 * c;
-        const bool row = t < x.len;
-        const float nl = row ? a.nlse[rows + t] : 0.f, nd = row ? a.nD[rows + t] : 0.f;
+    for (int c = 0; c < 4; ++c) {
+      const int t = i * kT + tx + 16 * c;
+      const bool row = t < x.len;
+      const float nl = row ? a.nlse[rows + t] : 0.f, nd = row ? a.nD[rows + t] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool on = row && sees(a, t, k0 + ty + 16 * e);
-          const float p = on ? exp2f(s[e][c] * sl2 + nl) : 0.f;
-          P[(ty + 16 * e) * C::LP + tx + 16 * c] = p;
-          S[(ty + 16 * e) * C::LP + tx + 16 * c] = on ? p * (dp[e][c] + nd) : 0.f;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const bool on = row && sees(a, t, k0 + ty + 16 * e);
+        const float p = on ? exp2f(s[e][c] * sl2 + nl) : 0.f;
+        P[(ty + 16 * e) * C::LP + tx + 16 * c] = p;
+        S[(ty + 16 * e) * C::LP + tx + 16 * c] = on ? p * (dp[e][c] + nd) : 0.f;
       }
-      __syncthreads();
-      weighted<DH>(P, G, dv);
-      weighted<DH>(S, Q, dk);
     }
+    __syncthreads();
+    weighted<DH>(P, G, dv);
+    weighted<DH>(S, Q, dk);
+    if (DH > 64 && w + 1 < w1) fetch(w + 1);  // (no registers for it before)
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int k = k0 + ty + 16 * e;
     if (k >= x.len) continue;
-    T* kt = reinterpret_cast<T*>(a.dk) + (int64_t)(x.off + k) * a.dk_ts + m * a.dk_hs;
-    T* vt = reinterpret_cast<T*>(a.dv) + (int64_t)(x.off + k) * a.dv_ts + m * a.dv_hs;
+    if (gridDim.y == 1) {
+      float* kt = reinterpret_cast<float*>(a.dk) + (int64_t)(x.off + k) * a.dk_ts + m * a.dk_hs;
+      float* vt = reinterpret_cast<float*>(a.dv) + (int64_t)(x.off + k) * a.dv_ts + m * a.dv_hs;
 #pragma unroll
-    for (int c = 0; c < C::CV; ++c) {
-      Elem<T>::st(kt + column<DH>(c), dk[e][c] * a.scale);
-      Elem<T>::st(vt + column<DH>(c), dv[e][c]);
+      for (int c = 0; c < C::CV; ++c) {
+        kt[column<DH>(c)] = dk[e][c] * a.scale;
+        vt[column<DH>(c)] = dv[e][c];
+      }
+    } else {
+      float* to = a.parts + (((int64_t)blockIdx.y * 2 * a.N + x.off + k) * a.Hkv + m) * DH;
+#pragma unroll
+      for (int c = 0; c < C::CV; ++c) {
+        to[column<DH>(c)] = dk[e][c];
+        to[a.N * a.Hkv * DH + column<DH>(c)] = dv[e][c];
+      }
     }
   }
 }
 
-// CTAs for every tile that the sequences can have: as many as whole tiles, and one that is not full each.
-int64_t tiles_at_most(const PromptArgs& a) { return a.N / kT + std::min<int64_t>(a.B, a.N); }
+// The parts' sums of a tile of keys, added in order.
+template <int DH>
+__global__ void __launch_bounds__(kThreads) prompt_join_simt_kernel(PromptArgs a, int parts) {
+  PromptTile x;
+  int m;
+  if (!my_tile(a, a.Hkv, true, x, m)) return;
+  const int64_t part = a.N * a.Hkv * DH;  // floats of dK's, or dV's, part
+  for (int u = threadIdx.x; u < kT * DH / 4; u += kThreads) {
+    const int k = x.tile * kT + u / (DH / 4), c = u % (DH / 4) * 4;
+    if (k >= x.len) break;
+    const float* from = a.parts + ((int64_t)(x.off + k) * a.Hkv + m) * DH + c;
+    float4 s[2] = {};
+    for (int p = 0; p < parts; ++p)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float4 f = *reinterpret_cast<const float4*>(from + (2 * p + v) * part);
+        s[v].x += f.x; s[v].y += f.y; s[v].z += f.z; s[v].w += f.w;
+      }
+    float* kt = reinterpret_cast<float*>(a.dk) + (int64_t)(x.off + k) * a.dk_ts + m * a.dk_hs + c;
+    float* vt = reinterpret_cast<float*>(a.dv) + (int64_t)(x.off + k) * a.dv_ts + m * a.dv_hs + c;
+    *reinterpret_cast<float4*>(kt) = make_float4(s[0].x * a.scale, s[0].y * a.scale, s[0].z * a.scale, s[0].w * a.scale);
+    *reinterpret_cast<float4*>(vt) = s[1];
+  }
+}
 
-template <typename T, int DH>
+// Tiles that the sequences can have: as many as whole tiles, and one that is not full each.
+int64_t tiles_at_most(int64_t N, int B) { return N / kT + std::min<int64_t>(B, N); }
+// Parts that the rows of a tile of keys are divided into: where all tiles give less than two CTAs an SM.
+int parts_of(int64_t N, int B, int Hkv) {
+  return (int)std::min<int64_t>(8, std::max<int64_t>(1, 2 * kSMs / std::max<int64_t>(1, tiles_at_most(N, B) * Hkv)));
+}
+
+template <int DH>
 cudaError_t forward_simt(const PromptArgs& a, cudaStream_t s) {
   using C = Simt<DH>;
   constexpr int smem = (3 * C::TILE + C::SCORES) * 4;
-  cudaError_t e = allow_smem((const void*)prompt_simt_kernel<T, DH>, smem);
+  cudaError_t e = allow_smem((const void*)prompt_simt_kernel<DH>, smem);
   if (e != cudaSuccess) return e;
   launch_begin("prompt_simt", s);
-  prompt_simt_kernel<T, DH><<<(unsigned)(tiles_at_most(a) * a.H), kThreads, smem, s>>>(a);
+  prompt_simt_kernel<DH><<<(unsigned)(tiles_at_most(a.N, a.B) * a.H), kThreads, smem, s>>>(a);
   return launch_end("prompt_simt", s);
 }
 
-template <typename T, int DH>
+template <int DH>
 cudaError_t backward_simt(const PromptArgs& a, cudaStream_t s) {
   using C = Simt<DH>;
   constexpr int sq = (4 * C::TILE + C::SCORES) * 4, skv = (4 * C::TILE + 2 * C::SCORES) * 4;
-  cudaError_t e = allow_smem((const void*)prompt_dq_simt_kernel<T, DH>, sq);
-  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dkv_simt_kernel<T, DH>, skv);
+  cudaError_t e = allow_smem((const void*)prompt_dq_simt_kernel<DH>, sq);
+  if (e == cudaSuccess) e = allow_smem((const void*)prompt_dkv_simt_kernel<DH>, skv);
   if (e != cudaSuccess) return e;
+  const int64_t tiles = tiles_at_most(a.N, a.B);
+  const int parts = parts_of(a.N, a.B, a.Hkv);
   launch_begin("prompt_dq_simt", s);
-  prompt_dq_simt_kernel<T, DH><<<(unsigned)(tiles_at_most(a) * a.H), kThreads, sq, s>>>(a);
+  prompt_dq_simt_kernel<DH><<<(unsigned)(tiles * a.H), kThreads, sq, s>>>(a);
   e = launch_end("prompt_dq_simt", s);
   if (e != cudaSuccess) return e;
   launch_begin("prompt_dkv_simt", s);
-  prompt_dkv_simt_kernel<T, DH><<<(unsigned)(tiles_at_most(a) * a.Hkv), kThreads, skv, s>>>(a);
-  return launch_end("prompt_dkv_simt", s);
+  prompt_dkv_simt_kernel<DH><<<dim3((unsigned)(tiles * a.Hkv), (unsigned)parts), kThreads, skv, s>>>(a);
+  e = launch_end("prompt_dkv_simt", s);
+  if (e != cudaSuccess || parts == 1) return e;
+  launch_begin("prompt_join_simt", s);
+  prompt_join_simt_kernel<DH><<<(unsigned)(tiles * a.Hkv), kThreads, 0, s>>>(a, parts);
+  return launch_end("prompt_join_simt", s);
+}
+
+template <typename T>
+void rows(const PromptArgs& a, cudaStream_t s) {
+  const unsigned grid = (unsigned)((a.N + 7) / 8);
+  if (a.dh == 32) prompt_rows_kernel<T, 32><<<grid, 256, 0, s>>>(a);
+  else if (a.dh == 64) prompt_rows_kernel<T, 64><<<grid, 256, 0, s>>>(a);
+  else prompt_rows_kernel<T, 128><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace
 
 int64_t prompt_scratch_rows(int64_t N, int B) { return (N + 4 * (int64_t)B + 128 + 3) / 4 * 4; }
+size_t prompt_parts_bytes(int64_t N, int B, int Hkv, int dh, int bf16) {
+  const int parts = bf16 ? 1 : parts_of(N, B, Hkv);
+  return parts == 1 ? 0 : (size_t)parts * 2 * N * Hkv * dh * sizeof(float);
+}
 
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   if (a.bf16) return launch_prompt_tc(a, s);
-  return a.dh == 32 ? forward_simt<float, 32>(a, s) : a.dh == 64 ? forward_simt<float, 64>(a, s) : forward_simt<float, 128>(a, s);
+  return a.dh == 32 ? forward_simt<32>(a, s) : a.dh == 64 ? forward_simt<64>(a, s) : forward_simt<128>(a, s);
 }
 
 cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s) {
   launch_begin("prompt_rows", s);
-  const dim3 grid((unsigned)((a.N + 7) / 8));
-  if (a.bf16) {
-    using T = __nv_bfloat16;
-    if (a.dh == 32) prompt_rows_kernel<T, 32><<<grid, 256, 0, s>>>(a);
-    else if (a.dh == 64) prompt_rows_kernel<T, 64><<<grid, 256, 0, s>>>(a);
-    else prompt_rows_kernel<T, 128><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (a.dh == 32) prompt_rows_kernel<float, 32><<<grid, 256, 0, s>>>(a);
-    else if (a.dh == 64) prompt_rows_kernel<float, 64><<<grid, 256, 0, s>>>(a);
-    else prompt_rows_kernel<float, 128><<<grid, 256, 0, s>>>(a);
-  }
+  if (a.bf16) rows<__nv_bfloat16>(a, s);
+  else rows<float>(a, s);
   cudaError_t e = launch_end("prompt_rows", s);
   if (e != cudaSuccess) return e;
   if (a.bf16) return launch_prompt_bwd_tc(a, s);
-  return a.dh == 32 ? backward_simt<float, 32>(a, s) : a.dh == 64 ? backward_simt<float, 64>(a, s) : backward_simt<float, 128>(a, s);
+  return a.dh == 32 ? backward_simt<32>(a, s) : a.dh == 64 ? backward_simt<64>(a, s) : backward_simt<128>(a, s);
 }
 
 }  // namespace gca

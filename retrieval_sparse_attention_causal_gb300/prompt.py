@@ -72,10 +72,9 @@ class QuantisedCache(PagedCache):
     __slots__ = ("heads", "dh")
 
     def __init__(self, k_pages, v_pages, table, lengths, refs, heads: int, dh: int, ws: Workspace = None):
-        super().__init__(k_pages, v_pages, table, lengths, refs, ws)
-        _need(k_pages.dtype == torch.uint8 and k_pages.shape[2] == self.row_bytes(heads, dh),
-              "pages must be uint8 [pages, 64, row_bytes(heads, dh)]")
-        self.heads, self.dh = heads, dh
+        EXT.check_quantised(k_pages, v_pages, table, lengths, refs, heads, dh)
+        self.k_pages, self.v_pages, self.table, self.lengths, self.refs = k_pages, v_pages, table, lengths, refs
+        self.heads, self.dh, self.ws = heads, dh, ws
 
     @staticmethod
     def row_bytes(heads: int, dh: int) -> int:
@@ -93,26 +92,26 @@ class QuantisedCache(PagedCache):
                    torch.zeros(slots, dtype=torch.int32, device=device),
                    torch.zeros(pages, dtype=torch.int32, device=device), heads, dh, ws)
 
-    def _state(self):
-        return self.k_pages, self.v_pages, self.table, self.lengths, self.refs, self.heads, self.dh
-
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: torch.Tensor, path: torch.Tensor = None,
                slots: torch.Tensor = None):
         """PagedCache.append of rows in bfloat16 or float32, quantised as they are written
         (gca_cache_append_quantised)."""
-        EXT.append_quantised(*self._state(), k_new, v_new, counts, path, None, slots, _word(self.ws))
+        EXT.append_quantised(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, self.heads, self.dh, k_new,
+                             v_new, counts, path, None, slots, _word(self.ws))
 
     def append_packed(self, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, slots: torch.Tensor = None):
         """Rows offsets[i] .. offsets[i+1]-1 (int32 [n + 1]) of k, v [N, heads, dh] go behind the last token
         of slots[i] (default: entry i is slot i): the packed prompts of prompt_attention."""
-        EXT.append_quantised(*self._state(), k, v, None, None, offsets, slots, _word(self.ws))
+        EXT.append_quantised(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, self.heads, self.dh, k, v,
+                             None, None, offsets, slots, _word(self.ws))
 
     def read(self, idx: torch.Tensor, slots: torch.Tensor = None, dtype=torch.bfloat16):
         """Chunks idx int32 [n, ...] of slots[i] (default: entry i is slot i), -1: none, widened to
         bfloat16 or float32 (gca_cache_read; exactly).  Returns k, v [n, per * 64, heads, dh] and idx_local
         like idx, so that gca_forward(q, k, v, idx_local, scores, shift=0) attends to them."""
         _need(dtype in (torch.bfloat16, torch.float32), "dtype must be bfloat16 or float32")
-        return EXT.read_quantised(*self._state(), idx, slots, dtype == torch.float32, _word(self.ws))
+        return EXT.read_quantised(self.k_pages, self.v_pages, self.table, self.lengths, self.refs, self.heads, self.dh, idx,
+                                  slots, dtype == torch.float32, _word(self.ws))
 
     def numbers(self):
         """Views of the pages: k, v float8_e4m3fn [pages, 64, heads, dh], and their exponents uint8 [pages, 64,

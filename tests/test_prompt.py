@@ -44,8 +44,9 @@ def test_prompt_attention_refusals(gca):
 
 def test_prompt_attention_backward_refusals(gca):
     L = gca.LIB
-    need = L.gca_prompt_attention_backward_scratch_size(100, 3, 12)
+    need = L.gca_prompt_attention_backward_scratch_size(100, 3, 12, 12, 64, gca.GCA_BF16)
     assert need >= 2 * 100 * 12 * 4
+    assert L.gca_prompt_attention_backward_scratch_size(100, 3, 12, 12, 64, gca.GCA_F32) > need  # parts of few tiles
 
     def call(dt=gca.GCA_BF16, N=100, B=3, H=12, Hkv=12, dh=64, o=FAKE, dout=None, lse=FAKE, dq=None, dk=None, dv=None, scratch=FAKE,
              size=need):
