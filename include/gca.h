@@ -453,7 +453,8 @@ GCA_API gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_
  *
  *     y = gain R(p) (x w / sqrt(mean(x^2) + eps))       for each token and head of q and of k
  * with the mean over the head's dh elements, the weights w [dh] shared by the heads, and R(p), freq,
- * rot, interleaved, positions and gain as in gca_rotary (elements rot .. dh-1 are not turned).
+ * rot, interleaved, positions and gain as in gca_rotary: elements rot .. dh-1 are normed, but neither
+ * turned nor multiplied by gain.
  *
  *   q, k, q_out, k_out, dtype and sizes: as in gca_rotary; outputs may be the inputs themselves.
  *   q_weight, k_weight [dh] float32 device (k_weight may be NULL without k).   eps >= 0, finite.
@@ -488,10 +489,11 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  *           16-byte aligned, strides multiples of 16 bytes (a head stride of 0 repeats a head; no
  *           token stride of 0).
  *   offsets [B+1] int32 device, 0 <= offsets[0] <= .. <= offsets[B] <= N; a sequence may be empty.  One
- *           whose offsets are out of order or of range is left out and flagged (GCA_ERR_DEVICE_INDEX).
+ *           whose offsets are out of order or of range is left out and flagged (GCA_ERR_DEVICE_INDEX);
+ *           rows that two others then share get any values.
  *   N 0 .. 2^30 rows.   B 1 .. 1024.   H a multiple of Hkv.   dh 32, 64 or 128.   window >= 0.   scale > 0.
- *   o [N][H][dh] contiguous, 16-byte aligned.   lse [N][H] float32.   Rows of no sequence are left as
- *           they were.
+ *   o [N][H][dh] contiguous, 16-byte aligned, not an input.   lse [N][H] float32.   Rows of no
+ *           sequence are left as they were.
  *   ws      >= gca_forward_workspace_size() bytes (error word only).
  * No sequence sees another: rows of others, and behind the last, may hold anything.  An infinity or
  * NaN of a sequence can reach all its own rows (a weight of 0 times it is NaN).  bf16: as in
@@ -503,7 +505,8 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  * with P from lse; dk, dv sum over the query heads that share a key head.  Deterministic (no atomics).
  * bf16: P and dS are rounded to bf16 for their products.
  *   o, lse  from the forward call.   dout [N][H][dh]: like q.
- *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap.
+ *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap,
+ *           with each other or with an input either.
  *   scratch >= gca_prompt_attention_backward_scratch_size() bytes, 256-byte aligned, any contents; one
  *           for each call that can overlap another.
  * ------------------------------------------------------------------------------- */
@@ -591,7 +594,7 @@ GCA_API gca_status gca_cache_lookup(const gca_cache* cache, int n, int per, cons
  * multiple of 16 bytes: gca_cache_row_bytes().  A number is its e4m3 value times 2^(byte - 127).  The byte
  * is the least exponent, -120 or more, by which the head's largest finite magnitude is 448 at most, so
  * a number is off by 2^-4 of itself or 2^-10 times the scale at most, whichever is more.  Infinities and
- * NaN become NaN.  gca_cache_fork, _trim, _compact and _lookup work on such pages as on others;
+ * NaN become NaN; what rounds to 2^128 reads as an infinity.  gca_cache_fork, _trim, _compact and _lookup work on such pages as on others;
  * gca_cache_append, gca_tree_attention and gca_forward do not read them.  dh 32, 64 or 128, heads * dh a
  * multiple of 16.
  *

@@ -806,6 +806,8 @@ extern "C" gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* 
   if (st != GCA_OK) return st;
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
   if (N == 0) return GCA_OK;
+  for (const gca_heads* in : {q, k, v})
+    if (o == in->data) return fail(GCA_ERR_INVALID_ARG, "o must not be an input");
   const PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
   cudaError_t e = launch_prompt_forward(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gca_prompt_attention launch");
@@ -834,6 +836,14 @@ extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gc
   if (strides_overlap(*dq, 1, N, H, dh) || strides_overlap(*dk, 1, N, Hkv, dh) || strides_overlap(*dv, 1, N, Hkv, dh))
     return fail(GCA_ERR_INVALID_ARG, "output strides make elements overlap");
   if ((st = check_scratch(scratch, scratch_bytes, gca_prompt_attention_backward_scratch_size(N, B, H, Hkv, dh, dtype))) != GCA_OK) return st;
+  // Each gradient is written before the last input is read.
+  const void* in[] = {q->data, k->data, v->data, o, dout->data};
+  const void* out[] = {dq->data, dk->data, dv->data};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* x : in)
+      if (out[i] == x) return fail(GCA_ERR_INVALID_ARG, "a gradient must not be an input");
+    if (out[i] == out[(i + 1) % 3]) return fail(GCA_ERR_INVALID_ARG, "two gradients are one tensor");
+  }
   PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
   a.dout = dout->data; a.do_ts = N > 1 ? dout->token_stride : 0; a.do_hs = H > 1 ? dout->head_stride : 0;
   a.dq = dq->data; a.dq_ts = dq->token_stride; a.dq_hs = dq->head_stride;

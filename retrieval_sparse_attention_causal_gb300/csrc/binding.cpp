@@ -399,7 +399,7 @@ gca_cache pool_of(Args a, On& on, bool any = false) {
 // k_pages, v_pages, table, lengths, refs: refused where a call on them would be.
 PyObject* check_pool(Args a) {
   On on;
-  pool_of(a, on, true);
+  pool_of(a, on);
   Py_RETURN_NONE;
 }
 

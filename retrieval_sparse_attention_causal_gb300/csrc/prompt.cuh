@@ -73,6 +73,7 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const Tiles& ti
       // The lane of the bit that `left` others lie below.
       const bool it = n > lo && __popc(those & ((1u << lane) - 1)) == left;
       const int at = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+      if (at < 0) return false;  // (offsets out of order can make more tiles than an int counts)
       x.b = b0 + at;
       x.tile = back ? __shfl_sync(0xffffffffu, n, at) - 1 - lo : lo;
       x.off = a.offsets[x.b];

@@ -199,41 +199,24 @@ __global__ void __launch_bounds__(kThreads) read_chunks_kernel(ReadArgs a) {
     }
     I::pack(y, out);
   };
-  constexpr int kFly = 1;
-  for (int u0 = part * per * units + threadIdx.x; u0 < (part + 1) * per * units; u0 += kFly * kThreads) {
-    uint4 kq[kFly], vq[kFly];
-    int ke[kFly], ve[kFly];
-    bool on[kFly], there[kFly];
+  for (int u = part * per * units + threadIdx.x; u < (part + 1) * per * units; u += kThreads) {
+    uint4 ko[I::kVecs], vo[I::kVecs];
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      const int u = u0 + f * kThreads;
-      on[f] = u < (part + 1) * per * units;
-      const int r = u / units, x = u - r * units;
-      there[f] = on[f] && r < have;
-      if (!there[f]) continue;
+    for (int n = 0; n < I::kVecs; ++n) ko[n] = vo[n] = make_uint4(0, 0, 0, 0);
+    const int r = u / units, x = u - r * units;
+    if (r < have) {
       const int64_t at = (int64_t)r * c.token_bytes;
-      kq[f] = *reinterpret_cast<const uint4*>(kp + at + x * kPer);
-      vq[f] = *reinterpret_cast<const uint4*>(vp + at + x * kPer);
-      ke[f] = kp[at + a.heads * a.dh + x / lanes];
-      ve[f] = vp[at + a.heads * a.dh + x / lanes];
+      const uint4 kq = *reinterpret_cast<const uint4*>(kp + at + x * kPer), vq = *reinterpret_cast<const uint4*>(vp + at + x * kPer);
+      const int ke = kp[at + a.heads * a.dh + x / lanes], ve = vp[at + a.heads * a.dh + x / lanes];
+      widen(kq, ke, ko);
+      widen(vq, ve, vo);
     }
+    uint4* k = reinterpret_cast<uint4*>(a.k) + (to + u) * I::kVecs;
+    uint4* v = reinterpret_cast<uint4*>(a.v) + (to + u) * I::kVecs;
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      if (!on[f]) continue;
-      uint4 ko[I::kVecs], vo[I::kVecs];
-#pragma unroll
-      for (int n = 0; n < I::kVecs; ++n) ko[n] = vo[n] = make_uint4(0, 0, 0, 0);
-      if (there[f]) {
-        widen(kq[f], ke[f], ko);
-        widen(vq[f], ve[f], vo);
-      }
-      uint4* k = reinterpret_cast<uint4*>(a.k) + (to + u0 + f * kThreads) * I::kVecs;
-      uint4* v = reinterpret_cast<uint4*>(a.v) + (to + u0 + f * kThreads) * I::kVecs;
-#pragma unroll
-      for (int n = 0; n < I::kVecs; ++n) {
-        k[n] = ko[n];
-        v[n] = vo[n];
-      }
+    for (int n = 0; n < I::kVecs; ++n) {
+      k[n] = ko[n];
+      v[n] = vo[n];
     }
   }
 }

@@ -19,7 +19,7 @@ def norm_rotary(q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, freq: torc
                 interleaved: bool = False, gain: float = 1.0, eps: float = 1e-6, q_out: torch.Tensor = None,
                 k_out: torch.Tensor = None):
     """RMS norm of every head of q and k, and their rotary positions, in one pass (gca_norm_rotary):
-    gain R(p) (x w / sqrt(mean(x^2) + eps)).
+    gain R(p) (x w / sqrt(mean(x^2) + eps)); elements that do not turn are normed alone.
 
     q [B, L, H, dh], k [B, L, Hkv, dh] or None, with any strides but the last; q_weight, k_weight
     float32 [dh]; freq, positions, interleaved and gain as in rotary().  Pass q_out=q, k_out=k to
@@ -54,7 +54,8 @@ def prompt_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                               dq: torch.Tensor = None, dk: torch.Tensor = None, dv: torch.Tensor = None,
                               ws: Workspace = None):
     """Gradients of prompt_attention() (gca_prompt_attention_backward): o, lse as it returned them, dout
-    [N, H, dh] the gradient of o.  Returns (dq, dk, dv); dq=, dk=, dv= may be views of one tensor.
+    [N, H, dh] the gradient of o.  Returns (dq, dk, dv); dq=, dk=, dv= may be views of one tensor, but not
+    of an input.
     Rows that no sequence has are not written."""
     return EXT.prompt_attention_backward(q, k, v, o, dout, lse, offsets, window, scale, dq, dk, dv, _word(ws))
 

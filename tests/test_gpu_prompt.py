@@ -613,6 +613,93 @@ def test_prompt_many_tiles_a_cta(H, Hkv, dh, window):
         assert float((lse[a:z].double().transpose(0, 1) - L).abs().max()) <= 2e-5
 
 
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_prompt_widest_window_and_repeated_heads(dtype, dh):
+    """A window as wide as an int is none; heads and gradients that repeat one (a stride of 0) are as their copies."""
+    g = _g()
+    off, N, H, Hkv = ints([0, 300, 301, 700]), 700, 4, 2
+    q, k, v, do = (torch.randn(N, h, dh, device="cuda").to(TORCH[dtype]) for h in (H, Hkv, Hkv, H))
+
+    def step(q, k, v, do, window=0):
+        o, lse = g.prompt_attention(q, k, v, off, window=window)
+        return (o, lse) + g.prompt_attention_backward(q, k, v, o, do, lse, off, window=window)
+    assert all(torch.equal(a, b) for a, b in zip(step(q, k, v, do), step(q, k, v, do, 2 ** 31 - 1)))
+    one = [x[:, :1].expand(N, x.shape[1], dh) for x in (q, k, v, do)]
+    assert all(torch.equal(a, b) for a, b in zip(step(*one), step(*(x.contiguous() for x in one))))
+
+
+def test_calls_at_once_share_the_error_word_alone():
+    """Steps on two streams that overlap, with scratch of their own, give what they give one after another."""
+    g = _g()
+    off, N = ints([0, 900, 2000]), 2000
+    sets = [[torch.randn(N, h, 64, device="cuda").bfloat16() for h in (8, 2, 2, 8)] for _ in range(2)]
+    wt, freq = torch.rand(64, device="cuda"), g.rotary_frequencies(64)
+    caches = [g.QuantisedCache.empty(40, 2, 20, 2, 64) for _ in range(4)]
+
+    def step(x, cache):
+        q, k = g.norm_rotary(x[0][None], x[1][None], wt, wt, freq)
+        o, lse = g.prompt_attention(q[0], k[0], x[2], off)
+        grads = g.prompt_attention_backward(q[0], k[0], x[2], o, x[3], lse, off)
+        dq, dk, dwq, dwk = g.norm_rotary_backward(x[0][None], x[1][None], grads[0][None], grads[1][None], wt, wt, freq)
+        cache.append_packed(k[0], x[2], off)
+        return [o, lse, dq, dk, grads[2], dwq, dwk] + list(cache.read(ints([[0, 13], [3, -1]])))
+    want = [step(x, c) for x, c in zip(sets, caches)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(3):
+        for c in caches[2:]:
+            c.trim(end=ints([0, 0]))
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = step(sets[i], caches[2 + i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, r in zip(want, got) for a, b in zip(w, r))
+
+
+def test_norms_and_cache_in_a_graph():
+    """A captured norm with its gradients, append and read follow the inputs, positions and state that change
+    behind them."""
+    g = _g()
+    q, k, v = (torch.randn(3, 70, h, 64, device="cuda").bfloat16() for h in (4, 2, 2))
+    wt, freq, pos, counts = torch.rand(64, device="cuda"), g.rotary_frequencies(64), ints([range(70)] * 3), ints([70, 1, 0])
+    caches = [g.QuantisedCache.empty(20, 3, 6, 2, 64) for _ in range(2)]
+    idx = ints([[0, 1, 2], [0, 1, -1], [0, 0, 0]])
+
+    def step(cache):
+        a, b = g.norm_rotary(q, k, wt, wt, freq, positions=pos)
+        grads = g.norm_rotary_backward(q, k, a, b, wt, wt, freq, positions=pos)
+        cache.append(b, v, counts)
+        return [a, b] + list(grads) + list(cache.read(idx))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(caches[0])
+    for turn in range(3):
+        q.copy_(torch.randn_like(q))
+        v.copy_(torch.randn_like(v))
+        pos.copy_(pos + 70)
+        counts.copy_(ints([[70, 1, 0], [0, 64, 3], [35, 0, 61]][turn]))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, step(caches[1])))
+    caches[0].check()
+    assert caches[0].lengths.tolist() == [105, 65, 64]
+
+
+def test_quantised_chunks_and_slots_named_twice():
+    """read() takes a chunk, and a slot, as often as it is named."""
+    g = _g()
+    cache = g.QuantisedCache.empty(8, 3, 4, 2, 64)
+    x = torch.randn(2, 130, 2, 64, device="cuda").bfloat16()
+    cache.append(x, -x, ints([130, 100]), slots=ints([2, 1]))
+    one = cache.read(ints([[0, 1, 2]]), slots=ints([2]))
+    two = cache.read(ints([[2, 2, 0], [1, 0, 1], [1, 1, -1]]), slots=ints([2, 2, 1]))
+    split = lambda t: t.unflatten(1, (3, 64))  # noqa: E731
+    for a, b in zip(one[:2], two[:2]):
+        a, b = split(a)[0], split(b)
+        assert torch.equal(b[0], a[[2, 2, 0]]) and torch.equal(b[1], a[[1, 0, 1]]) and torch.equal(b[2, 0], b[2, 1]) and (b[2, 2] == 0).all()
+    assert two[2].tolist() == [[0, 1, 2], [0, 1, 2], [0, 1, -1]]
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_step_against_oracle(dtype):

@@ -140,6 +140,21 @@ def test_python_refusals(gca):
         gca.PagedCache(torch.zeros(5, 64, 80, dtype=torch.uint8), torch.zeros(5, 64, 80), *state)
 
 
+def test_outputs_that_are_inputs_and_bytes_as_a_plain_cache_are_refused(gca):
+    L, h = gca.LIB, heads(gca)
+    other = lambda n: heads(gca, FAKE + n * 0x1000000)  # noqa: E731
+    assert L.gca_prompt_attention(h, h, h, gca.GCA_BF16, 100, 3, 12, 12, 64, FAKE, 0, 0.125, FAKE, FAKE, FAKE, 256, None) == gca.GCA_ERR_INVALID_ARG
+    assert b"input" in L.gca_last_error_detail()
+    for dq, dk, dv, what in ((h, other(1), other(2), b"input"), (other(1), other(2), h, b"input"), (other(1), other(2), other(2), b"one tensor"),
+                             (other(1), other(2), other(1), b"one tensor")):
+        st = L.gca_prompt_attention_backward(h, h, h, FAKE, h, FAKE, gca.GCA_BF16, 100, 3, 12, 12, 64, FAKE, 0, 0.125, dq, dk, dv, FAKE, 256,
+                                             FAKE, 1 << 30, None)
+        assert st == gca.GCA_ERR_INVALID_ARG and what in L.gca_last_error_detail()
+    pages = torch.zeros(5, 64, 80, dtype=torch.uint8)
+    with pytest.raises((ValueError, TypeError), match="k_pages"):
+        gca.PagedCache(pages, pages, torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(5, dtype=torch.int32))
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_attention_is_softmax_attention():
     """Against torch's own attention in float64 on one dense sequence, and packed sequences against each by itself."""
