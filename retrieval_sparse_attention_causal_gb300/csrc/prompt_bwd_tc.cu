@@ -63,9 +63,9 @@ template <int DH>
 struct Shared {
   uint64_t full[Tc<DH>::NK], empty[Tc<DH>::NK];  // slots, or stages
   uint64_t tile[2], tile_free[2];                // the tile that stays
-  // Of each group of warps:
+  // Of each group of warps (on the queries' side dp, ds and done are of each of two buffers):
   uint64_t s[2], dp[2];                          // products that are there: S and dP (or their transposes)
-  uint64_t s_taken[2], dp_taken[2];              // ... that are in registers
+  uint64_t s_taken;                              // queries' side: S is in registers
   uint64_t p[2], ds[2], done[2];                 // P and dS in TMEM; dS's product done
   uint64_t rest;                                 // queries' side: the rows' sums of dS in TMEM
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
@@ -88,13 +88,14 @@ __device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, Prom
     }
     for (int i = 0; i < G; ++i) {
       tc::mbar_init(&sh.s[i], 1);
-      tc::mbar_init(&sh.dp[i], 1);
-      tc::mbar_init(&sh.s_taken[i], kElem / G);
-      tc::mbar_init(&sh.dp_taken[i], kElem / G);
       tc::mbar_init(&sh.p[i], kElem / G);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh.dp[i], 1);
       tc::mbar_init(&sh.ds[i], kElem / G);
       tc::mbar_init(&sh.done[i], 1);
     }
+    tc::mbar_init(&sh.s_taken, kElem);
     tc::mbar_init(&sh.rest, kElem);
     tc::mbar_init(&sh.acc, G);
     tc::mbar_init(&sh.acc_free, kElem);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   set_up<DH, 1>(a, sh, items, kElem + 2);
-  const uint32_t tS = sh.tmem, tP = tS + 128, tD = tS + 256, tQ = tS + 320, tR = tS + 448;  // S, dP, dS, dQ, sums of dS
+  const uint32_t tS = sh.tmem, tP = tS + 128, tQ = tS + 384;  // S, two of dP, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
     if (__builtin_expect(__all_sync(kAll, tc::mbar_try(bar, parity)), 1)) return true;
@@ -241,23 +242,23 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
   } else if (warp == kProducts) {
-    // ---------------------------------------------------------------- S and dP, each once the block before is in registers
+    // ---------------------------------------------------------------- S once the last is in registers, dP two blocks ahead
     int id = 0, nt = 0;  // blocks, tiles so far
     for (; take(nt); ++nt) {
       const uint32_t q = tc::su32(tiles + (nt % NB) * 2 * C::BLOCK), g = q + C::BLOCK;
       ok = waited(&sh.tile[nt % NB], (nt / NB) & 1, kSiteTile, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
         const int ks = 2 * id % NK, vs = (2 * id + 1) % NK;
-        ok = waited(&sh.full[ks], (2 * id / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.s_taken[0], (id - 1) & 1, kSiteTaken, n));
+        ok = waited(&sh.full[ks], (2 * id / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.s_taken, (id - 1) & 1, kSiteTaken, n));
         if (!ok) break;
         tc::fence_after();
         product<DH, 1>(tS, q, tc::su32(ring + ks * C::BLOCK), 0);
         tc::commit_warp(&sh.s[0]);
-        ok = waited(&sh.full[vs], ((2 * id + 1) / NK) & 1, kSiteFull, n) && (id == 0 || waited(&sh.dp_taken[0], (id - 1) & 1, kSiteTaken, n));
+        ok = waited(&sh.full[vs], ((2 * id + 1) / NK) & 1, kSiteFull, n) && (id < 2 || waited(&sh.done[id & 1], ((id >> 1) - 1) & 1, kSiteDone, n));
         if (!ok) break;
         tc::fence_after();
-        product<DH, 1>(tP, g, tc::su32(ring + vs * C::BLOCK), 0);
-        tc::commit_warp(&sh.dp[0]);
+        product<DH, 1>(tP + 128 * (id & 1), g, tc::su32(ring + vs * C::BLOCK), 0);
+        tc::commit_warp(&sh.dp[id & 1]);
         tc::commit_warp(&sh.empty[vs]);
       }
       if (!ok) break;
@@ -270,11 +271,11 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       ok = waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt);
       for (int n = it.lo; n <= it.x.tile && ok; ++n, ++id) {
         const int ks = 2 * id % NK;
-        ok = waited(&sh.ds[0], id & 1, kSiteDs, n);
+        ok = waited(&sh.ds[id & 1], (id >> 1) & 1, kSiteDs, n);
         if (!ok) break;
         tc::fence_after();
-        accumulate<DH, 1, 0>(tQ, tD, tc::su32(ring + ks * C::BLOCK), 0, n > it.lo);
-        tc::commit_warp(&sh.done[0]);
+        accumulate<DH, 1, 16>(tQ, tP + 128 * (id & 1), tc::su32(ring + ks * C::BLOCK), 0, n > it.lo);
+        tc::commit_warp(&sh.done[id & 1]);
         tc::commit_warp(&sh.empty[ks]);
       }
       if (!ok) break;
@@ -305,7 +306,12 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
         tc::ld_wait_row(s);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.s_taken[0]);
+        if (lane == 0) tc::mbar_arrive(&sh.s_taken);
+        ok = waited(&sh.dp[id & 1], (id >> 1) & 1, kSiteDp, n);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t to = tP + 128 * (id & 1) + lanes + 32 * part;
+        tc::ld32x32b_x32(to, dp);  // on its way while the logits are weighed
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float x, y;
@@ -313,14 +319,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
           s[2 * i] = tc::ex2(x);
           s[2 * i + 1] = tc::ex2(y);
         }
-        ok = waited(&sh.dp[0], id & 1, kSiteDp, n);
-        if (!ok) break;
-        tc::fence_after();
-        tc::ld32x32b_x32(tP + lanes + 32 * part, dp);
         tc::ld_wait_row(dp);
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.dp_taken[0]);
         uint32_t d[16];
         auto weigh = [&](auto edge, int c0, int c1) {  // at an edge: of the part's keys c0 .. c1 - 1 are seen
 #pragma unroll
@@ -344,19 +343,14 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
           if (part == 0) blank<DH, 1>(ring + (2 * id % NK) * C::BLOCK, 0, r, it.x.len - n * kT);
           tc::fence_async_smem();
         }
-        if (id > 0) {  // dS's columns have been read
-          ok = waited(&sh.done[0], (id - 1) & 1, kSiteDone, n);
-          if (!ok) break;
-          tc::fence_after();
-        }
-        const uint32_t to = tD + lanes + 16 * part;
+        // Over columns that have been read: an A operand's 16 of each 32.
         const uint32_t d0[8] = {d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7]}, d1[8] = {d[8], d[9], d[10], d[11], d[12], d[13], d[14], d[15]};
         tc::st32x32b_x8(to, d0);
         tc::st32x32b_x8(to + 8, d1);
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.ds[0]);
+        if (lane == 0) tc::mbar_arrive(&sh.ds[id & 1]);  // (a warp is never two blocks ahead of another: dP of the second waits for all)
       }
       if (!ok) break;
       ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
@@ -367,12 +361,10 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       if (col < a.dh) write_row<DH / 4, 1>(tQ + lanes + col, 0, to + col, a.scale, on);
       // A row of dS sums to 0 by its D; what is left is how far D, of the rounded output, is off.  The keys' side takes
       // the D that is right: in rows that see few keys the difference is as large as the roundings of dS.
-      // (The parts' sums meet in spare columns of TMEM; those of the item before last have been read, for each block
-      // since has needed the warps that read them.)
+      // (The parts' sums meet in columns of dQ that the part has read.)
       float x, y;
       tc::uf2(rest, x, y);
-      const uint32_t spare = tR + lanes + 4 * (nt & 1);
-      tc::st32x32b_x1(spare + part, __float_as_uint(x + y));
+      tc::st32x32b_x1(tQ + lanes + col, __float_as_uint(x + y));
       tc::st_wait();
       tc::fence_before();
       __syncwarp();
@@ -382,7 +374,9 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
         if (!ok) break;
         tc::fence_after();
         float part_of[4];
-        tc::ld32x32b_x4(spare, part_of);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) tc::ld32x32b_x1(tQ + lanes + p * (DH / 4), part_of[p]);
+        tc::ld_wait_row(part_of);
         if (on) a.nD[row] = nd - ((part_of[0] + part_of[1]) + (part_of[2] + part_of[3]));
       }
       tc::fence_before();

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 16;      // numbers of a thread: 16 bytes of a row
-constexpr int kParts = 4;      // CTAs of a page that is written
+constexpr int kParts = 2;      // CTAs of a page that is written
 constexpr int kReadParts = 8;  // ... that is read: few chunks are read at a time
 constexpr int kLowest = -120, kBias = 127;
 
@@ -101,28 +101,17 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(AppendArgs a) {
   const int4 rec = reinterpret_cast<const int4*>(a.rec)[i];
   const int old = rec.x, now = old + rec.y, slot = rec.w;
   const int p = old / kChunk + step - (i ? a.steps[i - 1] : 0);
-  const int64_t page = c.table[(int64_t)slot * c.width + p];
   constexpr int per = kChunk / kParts;
   const int r0 = part * per, lanes = a.dh / kPer, units = a.heads * lanes;
-  unsigned char *kto = c.kp + page * kChunk * c.token_bytes, *vto = c.vp + page * kChunk * c.token_bytes;
   const int held = old - p * kChunk;  // rows of the page that were there before
-  if (rec.z >= 0 && held > r0) {      // a shared last page: its rows move to this one
-    const int words = (int)(c.token_bytes / 16), end = min(r0 + per, held) * words;
-    const uint4* kfrom = reinterpret_cast<const uint4*>(c.kp + (int64_t)rec.z * kChunk * c.token_bytes);
-    const uint4* vfrom = reinterpret_cast<const uint4*>(c.vp + (int64_t)rec.z * kChunk * c.token_bytes);
-    for (int u = r0 * words + threadIdx.x; u < end; u += kThreads) {
-      const uint4 x = kfrom[u], y = vfrom[u];
-      reinterpret_cast<uint4*>(kto)[u] = x;
-      reinterpret_cast<uint4*>(vto)[u] = y;
-    }
-  }
   const int first = max(r0, held), end = min(r0 + per, now - p * kChunk);
   const int64_t start = a.offsets ? a.offsets[i] : 0;
-  // Whole warps go round together, for the heads' maxima.  (With two units of a thread on their way it was no faster.)
-  for (int u0 = first * units; u0 < end * units; u0 += kThreads) {
-    const int u = u0 + threadIdx.x;
-    bool on = u < end * units;
-    const int r = on ? u / units : first, x = on ? u - r * units : 0, h = x / lanes, t = r - held;
+  // A thread's unit on its way: the first is fetched before the page is known, the next before one is written.
+  uint4 kin[I::kVecs], vin[I::kVecs];
+  bool on;
+  auto fetch = [&](int u) {
+    on = u < end * units;
+    const int r = u / units, x = u - r * units, t = r - held;
     int64_t row = t;
     if (a.path && on) {
       row = a.path[(int64_t)i * a.T + t];
@@ -131,7 +120,6 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(AppendArgs a) {
         on = false;
       }
     }
-    uint4 kin[I::kVecs], vin[I::kVecs];
     const uint4* k = reinterpret_cast<const uint4*>(a.kn + i * a.kn_bs + (start + row) * a.kn_ts) + x * I::kVecs;
     const uint4* v = reinterpret_cast<const uint4*>(a.vn + i * a.vn_bs + (start + row) * a.vn_ts) + x * I::kVecs;
 #pragma unroll
@@ -139,13 +127,33 @@ __global__ void __launch_bounds__(kThreads) quantise_rows_kernel(AppendArgs a) {
       kin[n] = on ? k[n] : make_uint4(0, 0, 0, 0);
       vin[n] = on ? v[n] : make_uint4(0, 0, 0, 0);
     }
-    float f[kPer];
+  };
+  fetch(first * units + threadIdx.x);
+  const int64_t page = c.table[(int64_t)slot * c.width + p];
+  unsigned char *kto = c.kp + page * kChunk * c.token_bytes, *vto = c.vp + page * kChunk * c.token_bytes;
+  if (rec.z >= 0 && held > r0) {      // a shared last page: its rows move to this one
+    const int words = (int)(c.token_bytes / 16), to = min(r0 + per, held) * words;
+    const uint4* kfrom = reinterpret_cast<const uint4*>(c.kp + (int64_t)rec.z * kChunk * c.token_bytes);
+    const uint4* vfrom = reinterpret_cast<const uint4*>(c.vp + (int64_t)rec.z * kChunk * c.token_bytes);
+    for (int u = r0 * words + threadIdx.x; u < to; u += kThreads) {
+      const uint4 x = kfrom[u], y = vfrom[u];
+      reinterpret_cast<uint4*>(kto)[u] = x;
+      reinterpret_cast<uint4*>(vto)[u] = y;
+    }
+  }
+  // Whole warps go round together, for the heads' maxima.
+  for (int u0 = first * units; u0 < end * units; u0 += kThreads) {
+    const int u = u0 + threadIdx.x;
+    const bool mine = on;
+    float f[kPer], g[kPer];
     int ke, ve;
     I::unpack(kin, f);
+    I::unpack(vin, g);
+    if (u0 + kThreads < end * units) fetch(u + kThreads);
     const uint4 kq = quantise(f, lanes, ke);
-    I::unpack(vin, f);
-    const uint4 vq = quantise(f, lanes, ve);
-    if (!on) continue;
+    const uint4 vq = quantise(g, lanes, ve);
+    if (!mine) continue;
+    const int r = u / units, x = u - r * units, h = x / lanes;
     const int64_t at = (int64_t)r * c.token_bytes;
     *reinterpret_cast<uint4*>(kto + at + x * kPer) = kq;
     *reinterpret_cast<uint4*>(vto + at + x * kPer) = vq;
