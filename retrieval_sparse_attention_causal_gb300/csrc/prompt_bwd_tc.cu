@@ -31,11 +31,11 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kT = 128;             // rows, and keys, of a tile
-constexpr int kElem = 16;           // warps that do the arithmetic: four of each 32 rows, 32 columns a warp
-// The warps of the other roles: products; on the queries' side the sums', on the keys' side the second group's
-// products; loads.
-constexpr int kProducts = kElem, kSums = kElem + 1;
-constexpr int threads_of(int issuing) { return 32 * (kElem + issuing + 1); }
+// Warps that do the arithmetic: of each 32 rows, two with 64 columns each on the queries' side, four with 32 on the
+// keys' side.  The warps of the other roles come behind them: products; on the queries' side the sums', on the
+// keys' side the second group's products; loads.
+constexpr int kElemQ = 8, kElemKv = 16;
+constexpr int threads_of(int elem, int issuing) { return 32 * (elem + issuing + 1); }
 constexpr int kTile = kT * 128;     // bytes of 128 rows x 64 elements
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -74,7 +74,7 @@ struct Shared {
   int keep[PromptTiles<kT>::kKeep];
 };
 
-template <int DH, int G, typename I>
+template <int DH, int G, int E, typename I>
 __device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, PromptItems<I>& items, int readers) {
   PromptTiles<kT>::fill(a, sh.keep);
   if (threadIdx.x == 0) {
@@ -88,22 +88,22 @@ __device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, Prom
     }
     for (int i = 0; i < G; ++i) {
       tc::mbar_init(&sh.s[i], 1);
-      tc::mbar_init(&sh.p[i], kElem / G);
+      tc::mbar_init(&sh.p[i], E / G);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.dp[i], 1);
-      tc::mbar_init(&sh.ds[i], kElem / G);
+      tc::mbar_init(&sh.ds[i], E / G);
       tc::mbar_init(&sh.done[i], 1);
     }
-    tc::mbar_init(&sh.s_taken, kElem);
-    tc::mbar_init(&sh.rest, kElem);
+    tc::mbar_init(&sh.s_taken, E);
+    tc::mbar_init(&sh.rest, E);
     tc::mbar_init(&sh.acc, G);
-    tc::mbar_init(&sh.acc_free, kElem);
+    tc::mbar_init(&sh.acc_free, E);
     init_items(items, readers);
     sh.abort = 0;
     tc::fence_mbar_init();
   }
-  if (threadIdx.x / 32 == kProducts) tc::tmem_alloc(&sh.tmem, kCols);
+  if (threadIdx.x / 32 == E) tc::tmem_alloc(&sh.tmem, kCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -187,7 +187,7 @@ __device__ __forceinline__ bool q_item(const PromptArgs& a, const PromptTiles<kT
 
 // ------------------------------------------------------------------ the queries' side
 template <int DH>
-__global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
+__global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
   using C = Tc<DH>;
   constexpr int NK = C::NK, NB = C::NB, SUB = C::SUB;
   extern __shared__ unsigned char dsm[];
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   __shared__ __align__(8) Shared<DH> sh;
   __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, 1>(a, sh, items, kElem + 2);
+  set_up<DH, 1, kElemQ>(a, sh, items, kElemQ + 2);
   const uint32_t tS = sh.tmem, tP = tS + 128, tQ = tS + 384;  // S, two of dP, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   QItem it;
   auto take = [&](int n) { return (ok = ok && take_item(items, n, it, waited, kSiteItem)) && it.more; };
 
-  if (warp == kElem + 2) {
+  if (warp == kElemQ + 2) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
     const PromptTiles<kT> counts(sh.keep);
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       for (int i = max(0, id - NK); i < id; ++i) tc::mbar_wait(&sh.full[i % NK], (i / NK) & 1, 1u << 16);
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
-  } else if (warp == kProducts) {
+  } else if (warp == kElemQ) {
     // ---------------------------------------------------------------- S once the last is in registers, dP two blocks ahead
     int id = 0, nt = 0;  // blocks, tiles so far
     for (; take(nt); ++nt) {
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       if (!ok) break;
       tc::commit_warp(&sh.tile_free[nt % NB]);
     }
-  } else if (warp == kSums) {
+  } else if (warp == kElemQ + 1) {
     // ---------------------------------------------------------------- dQ += dS K
     int id = 0, nt = 0;
     for (; take(nt); ++nt) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
     }
   } else {
     // ---------------------------------------------------------------- arithmetic
-    const int r = 32 * (warp & 3) + lane, part = warp >> 2;  // row of the tile; columns 32 part ..
+    const int r = 32 * (warp & 3) + lane, part = warp >> 2;  // row of the tile; columns 64 part ..
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
@@ -301,27 +301,30 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
         ok = waited(&sh.s[0], id & 1, kSiteS, n);
         if (!ok) break;
         tc::fence_after();
-        float s[32], dp[32];
-        tc::ld32x32b_x32(tS + lanes + 32 * part, s);
-        tc::ld_wait_row(s);
+        float s[2][32], dp[32];
+        tc::ld32x32b_x32(tS + lanes + 64 * part, s[0]);
+        tc::ld32x32b_x32(tS + lanes + 64 * part + 32, s[1]);
+        tc::ld_wait_row(s[0]);
+        tc::ld_wait_row(s[1]);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.s_taken);
         ok = waited(&sh.dp[id & 1], (id >> 1) & 1, kSiteDp, n);
         if (!ok) break;
         tc::fence_after();
-        const uint32_t to = tP + 128 * (id & 1) + lanes + 32 * part;
+        const uint32_t to = tP + 128 * (id & 1) + lanes + 64 * part;
         tc::ld32x32b_x32(to, dp);  // on its way while the logits are weighed
+        uint32_t d[2][16];
+        auto probabilities = [&](float (&s)[32]) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x, y;
-          tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, nl2), x, y);
-          s[2 * i] = tc::ex2(x);
-          s[2 * i + 1] = tc::ex2(y);
-        }
-        tc::ld_wait_row(dp);
-        uint32_t d[16];
-        auto weigh = [&](auto edge, int c0, int c1) {  // at an edge: of the part's keys c0 .. c1 - 1 are seen
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            tc::uf2(tc::fma2(tc::f2(s[2 * i], s[2 * i + 1]), k2, nl2), x, y);
+            s[2 * i] = tc::ex2(x);
+            s[2 * i + 1] = tc::ex2(y);
+          }
+        };
+        auto weigh = [&](auto edge, const float (&s)[32], uint32_t (&d)[16], int c0, int c1) {  // at an edge: keys c0 .. c1 - 1 are seen
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x, y;
@@ -334,9 +337,18 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
             d[i] = pack_bf16(x, y);
           }
         };
-        if (n == it.x.tile || n < whole)  // keys that the row does not see, and rows that do not exist
-          weigh(std::true_type{}, first - n * kT - 32 * part, on ? pos - n * kT - 32 * part + 1 : 0);
-        else weigh(std::false_type{}, 0, 32);
+        auto both = [&](auto edge) {
+          const int c0 = first - n * kT - 64 * part, c1 = on ? pos - n * kT - 64 * part + 1 : 0;
+          probabilities(s[0]);
+          tc::ld_wait_row(dp);
+          weigh(edge, s[0], d[0], c0, c1);
+          tc::ld32x32b_x32(to + 32, dp);
+          probabilities(s[1]);
+          tc::ld_wait_row(dp);
+          weigh(edge, s[1], d[1], c0 - 32, c1 - 32);
+        };
+        if (n == it.x.tile || n < whole) both(std::true_type{});  // keys that the row does not see, and rows that do not exist
+        else both(std::false_type{});
         if ((n + 1) * kT > it.x.len) {  // rows of K behind the sequence
           ok = waited(&sh.full[2 * id % NK], (2 * id / NK) & 1, kSiteRows, n);
           if (!ok) break;
@@ -344,9 +356,13 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
           tc::fence_async_smem();
         }
         // Over columns that have been read: an A operand's 16 of each 32.
-        const uint32_t d0[8] = {d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7]}, d1[8] = {d[8], d[9], d[10], d[11], d[12], d[13], d[14], d[15]};
-        tc::st32x32b_x8(to, d0);
-        tc::st32x32b_x8(to + 8, d1);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t d0[8] = {d[c][0], d[c][1], d[c][2], d[c][3], d[c][4], d[c][5], d[c][6], d[c][7]};
+          const uint32_t d1[8] = {d[c][8], d[c][9], d[c][10], d[c][11], d[c][12], d[c][13], d[c][14], d[c][15]};
+          tc::st32x32b_x8(to + 32 * c, d0);
+          tc::st32x32b_x8(to + 32 * c + 8, d1);
+        }
         tc::st_wait();
         tc::fence_before();
         __syncwarp();
@@ -356,9 +372,11 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
       ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
       if (!ok) break;
       tc::fence_after();
-      const int col = part * (DH / 4);
+      const int col = part * (DH / 2);
       bf16* to = reinterpret_cast<bf16*>(a.dq) + (int64_t)(it.x.off + pos) * a.dq_ts + it.h * a.dq_hs;
-      if (col < a.dh) write_row<DH / 4, 1>(tQ + lanes + col, 0, to + col, a.scale, on);
+#pragma unroll
+      for (int c = col; c < col + DH / 2; c += 32)
+        if (c < a.dh) write_row<32, 1>(tQ + lanes + c, 0, to + c, a.scale, on);
       // A row of dS sums to 0 by its D; what is left is how far D, of the rounded output, is off.  The keys' side takes
       // the D that is right: in rows that see few keys the difference is as large as the roundings of dS.
       // (The parts' sums meet in columns of dQ that the part has read.)
@@ -373,11 +391,10 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
         ok = waited(&sh.rest, nt & 1, kSiteRest, nt);
         if (!ok) break;
         tc::fence_after();
-        float part_of[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) tc::ld32x32b_x1(tQ + lanes + p * (DH / 4), part_of[p]);
-        tc::ld_wait_row(part_of);
-        if (on) a.nD[row] = nd - ((part_of[0] + part_of[1]) + (part_of[2] + part_of[3]));
+        float other[1];
+        tc::ld32x32b_x1(tQ + lanes + DH / 2, other[0]);
+        tc::ld_wait_row(other);
+        if (on) a.nD[row] = nd - ((x + y) + other[0]);
       }
       tc::fence_before();
       __syncwarp();
@@ -386,7 +403,7 @@ __global__ void __launch_bounds__(threads_of(2), 1) prompt_dq_tc_kernel(PromptAr
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == kProducts) {
+  if (warp == kElemQ) {
     tc::fence_after();
     tc::tmem_dealloc(sh.tmem, kCols);
   }
@@ -408,7 +425,7 @@ __device__ __forceinline__ bool kv_item(const PromptArgs& a, const PromptTiles<k
 
 // ------------------------------------------------------------------ the keys' side
 template <int DH>
-__global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
+__global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_tc_kernel(PromptArgs a, const __grid_constant__ Maps tm) {
   using C = Tc<DH>;
   constexpr int NS = C::NS, NB = C::NB, SUB = C::SUB, G = C::G;
   extern __shared__ unsigned char dsm[];
@@ -418,7 +435,7 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
   __shared__ __align__(8) Shared<DH> sh;
   __shared__ __align__(8) PromptItems<KvItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, G>(a, sh, items, kElem + G);
+  set_up<DH, G, kElemKv>(a, sh, items, kElemKv + G);
   // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
   const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
   bool ok = true;
@@ -429,7 +446,7 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
   KvItem it;
   auto take = [&](int n) { return (ok = ok && take_item(items, n, it, waited, kSiteItem)) && it.more; };
 
-  if (warp == kElem + G) {
+  if (warp == kElemKv + G) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
     const PromptTiles<kT> counts(sh.keep);
@@ -471,9 +488,9 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
       for (int i = max(0, id - NS); i < id; ++i) tc::mbar_wait(&sh.full[i % NS], (i / NS) & 1, 1u << 16);
       for (int i = max(0, nt + 1 - NB); i <= nt; ++i) tc::mbar_wait(&sh.tile[i % NB], (i / NB) & 1, 1u << 16);
     }
-  } else if (warp >= kProducts) {
+  } else if (warp >= kElemKv) {
     // ---------------------------------------------------------------- products of a group
-    const int w = G == 1 ? 0 : warp - kProducts;
+    const int w = G == 1 ? 0 : warp - kElemKv;
     const uint32_t tVw = tV + 2 * DH * w, tKw = tVw + DH;
     int id = 0, nt = 0;  // blocks, tiles so far
     for (; take(nt); ++nt) {
@@ -634,7 +651,7 @@ __global__ void __launch_bounds__(threads_of(Tc<DH>::G), 1) prompt_dkv_tc_kernel
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == kProducts) {
+  if (warp == kElemKv) {
     tc::fence_after();
     tc::tmem_dealloc(sh.tmem, kCols);
   }
@@ -653,11 +670,11 @@ cudaError_t run_tc(const PromptArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.N / kT + std::min<int64_t>(a.B, a.N);
   launch_begin("prompt_dq_tc", s);
-  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), threads_of(2), C::SMEM_Q, s>>>(a, tm);
+  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), threads_of(kElemQ, 2), C::SMEM_Q, s>>>(a, tm);
   e = launch_end("prompt_dq_tc", s);
   if (e != cudaSuccess) return e;
   launch_begin("prompt_dkv_tc", s);
-  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), threads_of(C::G), C::SMEM_KV, s>>>(a, tm);
+  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), threads_of(kElemKv, C::G), C::SMEM_KV, s>>>(a, tm);
   return launch_end("prompt_dkv_tc", s);
 }
 

@@ -56,16 +56,14 @@ __device__ __forceinline__ void st32x32b_x8(uint32_t taddr, const uint32_t (&v)[
                : "memory");
 }
 
-// One 32-bit column of the thread's lane; loads are waited for four at a time.
+// One 32-bit column of the thread's lane.
 __device__ __forceinline__ void st32x32b_x1(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void ld32x32b_x1(uint32_t taddr, float& v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
 }
-__device__ __forceinline__ void ld_wait_row(float (&v)[4]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]));
-}
+__device__ __forceinline__ void ld_wait_row(float (&v)[1]) { asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0])); }
 
 // Announcement of `bytes`, and a 4-D TMA tile load, by one elected lane of a converged warp that
 // calls with the same operands (a one-lane branch around them costs about twice the issue time).
