@@ -10,8 +10,8 @@
 //
 // The pages, their table and counts are those of cache.cu, whose operations move rows as bytes.
 // Bound by memory: each row is read and written once.  Measured, 12 heads of 64 in bf16: eight prompts of 67
-// thousand tokens in all, 66 us with the plan of their pages (4.7 TB/s; 57 without it); 80 tokens of 32
-// sequences 6.6; 16 x 8 chunks read 9.3, 16 x 128 chunks 104 (5.9 TB/s).
+// thousand tokens in all, 59 us with the plan of their pages (5.2 TB/s); 80 tokens of 32 sequences 6.4; 16 x 8 chunks
+// read 9.2, 16 x 128 chunks 103 (5.9 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 16;      // numbers of a thread: 16 bytes of a row
-constexpr int kParts = 2;      // CTAs of a page that is written
+constexpr int kParts = 2;      // CTAs of a page that is written (with 4 the prompts take 61 us, with 8 75)
 constexpr int kReadParts = 8;  // ... that is read: few chunks are read at a time
 constexpr int kLowest = -120, kBias = 127;
 
