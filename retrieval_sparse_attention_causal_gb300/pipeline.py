@@ -150,12 +150,12 @@ def prompt_forward(q, k, v, offsets, q_weight, k_weight, freq, positions, window
 
 def prompt_step(q, k, v, dout, offsets, q_weight, k_weight, freq, positions, window=0, interleaved=False, gain=1.0, eps=1e-6):
     """prompt_forward and its gradients (a training step's).  Returns o, lse, dq, dk, dv of q, k, v and the
-    norms' dq_weight, dk_weight (float32).  Rows of no sequence must hold finite numbers; their gradients are 0
-    (of v: not written)."""
+    norms' dq_weight, dk_weight (float32).  Rows of no sequence must hold finite numbers; their gradients are 0,
+    their o and lse are not written."""
     r = prompt_forward(q, k, v, offsets, q_weight, k_weight, freq, positions, window, interleaved, gain, eps)
     # The norms' weights sum over all rows, those of no sequence too.
-    grads = [torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
-    dq, dk, dv = prompt_attention_backward(r["q"], r["k"], v, r["o"], dout, r["lse"], offsets, window=window, dq=grads[0], dk=grads[1])
+    dq, dk, dv = (torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
+    prompt_attention_backward(r["q"], r["k"], v, r["o"], dout, r["lse"], offsets, window=window, dq=dq, dk=dk, dv=dv)
     dq, dk = dq[None], dk[None]
     dq, dk, dqw, dkw = norm_rotary_backward(q[None], k[None], dq, dk, q_weight, k_weight, freq, positions, interleaved, gain, eps,
                                             dq=dq, dk=dk)

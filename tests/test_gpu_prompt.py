@@ -734,6 +734,25 @@ def test_prompt_step_against_oracle(dtype):
     assert all(torch.equal(out[n], r[n]) for n in r)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_step_of_a_padded_batch(dtype):
+    """Rows in front of the first sequence and behind the last change nothing, and have gradients of 0."""
+    g = _g()
+    off, H, Hkv, dh, lo, hi, N = [5, 140, 140, 333], 4, 2, 64, 5, 333, 400
+    q, k, v, do = (torch.randn(N, h, dh, device="cuda").to(TORCH[dtype]) for h in (H, Hkv, Hkv, H))
+    wt, freq, pos = torch.rand(dh, device="cuda"), g.rotary_frequencies(dh), torch.arange(N, dtype=torch.int32, device="cuda")
+    r = pipeline.prompt_step(q, k, v, do, ints(off), wt, wt, freq, pos)
+    cut = [x[lo:hi].contiguous() for x in (q, k, v, do)]
+    want = pipeline.prompt_step(*cut, ints([0, 135, 135, 328]), wt, wt, freq, pos[lo:hi].contiguous())
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        assert torch.equal(r[n][lo:hi], want[n]), n
+    for n in ("dq", "dk", "dv"):
+        assert (r[n][:lo] == 0).all() and (r[n][hi:] == 0).all(), n
+    for n in ("dq_weight", "dk_weight"):
+        # The same terms in another order, of N heads: a few roundings of sums of random sign.
+        assert torch.allclose(r[n], want[n], rtol=0, atol=float(N * H * U * want[n].abs().max())), n
+
+
 def test_prompt_to_quantised_decode():
     """Packed prompts into a quantised cache, then decoding over the chunks that retrieval names: the same as GCA's
     forward over the pages' values."""
