@@ -241,8 +241,18 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
     if (a.offsets[mid] <= row) lo = mid;
     else hi = mid;
   }
-  const int off = a.offsets[lo];
-  if (row < off || row - off >= prompt_length(a, lo)) return;
+  int off = a.offsets[lo];
+  if (row < off || row - off >= prompt_length(a, lo)) {
+    // A row of no sequence; or offsets are out of order, and one that the search passed over has it.
+    lo = a.B;
+    for (int b = lane; b < a.B && lo == a.B; b += 32) {
+      const int s = a.offsets[b], n = prompt_length(a, b);
+      if (row >= s && row - s < n) lo = b;
+    }
+    lo = (int)__reduce_min_sync(0xffffffffu, (unsigned)lo);
+    if (lo == a.B) return;
+    off = a.offsets[lo];
+  }
   const T* o = reinterpret_cast<const T*>(a.o) + row * a.H * DH + at * V;
   const T* g = reinterpret_cast<const T*>(a.dout) + row * a.do_ts + at * V;
   const int64_t to = prompt_pad(off, lo) + row - off;

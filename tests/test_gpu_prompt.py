@@ -267,6 +267,29 @@ def test_prompt_bad_offsets_are_flagged():
     g.cache_workspace("cuda").check()
 
 
+@flags
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_gradients_beside_bad_offsets(dtype):
+    """Sequences beside those that are left out have their gradients, wherever the bad offsets lie."""
+    g = _g()
+    q, k, v, do = (torch.randn(300, 2, 64, device="cuda").to(TORCH[dtype]) for _ in range(4))
+
+    def step(off):
+        o, lse = torch.zeros_like(q), torch.zeros(300, 2, device="cuda")
+        g.prompt_attention(q, k, v, ints(off), out=o, lse=lse)
+        grads = [torch.zeros_like(q) for _ in range(3)]
+        g.prompt_attention_backward(q, k, v, o, do, lse, ints(off), dq=grads[0], dk=grads[1], dv=grads[2])
+        return [o, lse] + grads
+    for off, there in (([0, 100, 400, 200, 300], [[0, 100], [200, 300]]), ([0, 70, -1, 50, 70, 300], [[70, 300]]),
+                       ([250, 300, 0, 120, 120, 200], [[250, 300], [0, 120], [120, 200]])):
+        got = step(off)
+        with pytest.raises(g.GCAError):
+            g.cache_workspace("cuda").check()
+        for a, z in there:
+            assert all(torch.equal(x[a:z], y[a:z]) for x, y in zip(got, step([a, z]))), (off, a, z)
+    g.cache_workspace("cuda").check()
+
+
 def test_prompt_nothing_to_do():
     """No rows at all, and sequences that are all empty."""
     g = _g()
