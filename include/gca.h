@@ -503,7 +503,8 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  * gca_prompt_attention_backward - its gradients:
  *     D = <dout, o>,  dS = P (<dout, v> - D) scale,  dq = sum dS k,  dk = sum dS q,  dv = sum P dout
  * with P from lse; dk, dv sum over the query heads that share a key head.  Deterministic (no atomics).
- * bf16: P and dS are rounded to bf16 for their products.
+ * bf16: P and dS are rounded to bf16 for their products, and D, of the rounded o, is corrected by the
+ * sums of dS, which ought to be 0.
  *   o, lse  from the forward call.   dout [N][H][dh]: like q.
  *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap,
  *           with each other or with an input either.

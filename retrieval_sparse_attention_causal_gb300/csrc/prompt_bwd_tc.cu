@@ -17,12 +17,12 @@
 //     products, barriers and accumulators of its own (added at the end): one's exponentials run beside the
 //     other's sums.  2.14 thousand cycles a block, 2.24 without.  At dh 128 the accumulators fill TMEM.
 // P and dS are rounded to bf16, the type of the products' other operands (half a step, 2^-8 of each).
-// With that, and with a D of the rounded output, dQ and dK are off by 1.4 to 1.8 times their own rounding.
+// With that dQ and dK are off by 1.4 times their own rounding.
 // Rows behind a sequence's end may hold anything: as operands that are summed over they become zeros in
 // shared memory, elsewhere their results are not used.
 // Measured, bf16, in a graph, with the rows' sums of prompt_attn.cu: four documents of 46 thousand tokens in all, 12
-// heads of 64, 2.60 ms (860 TFLOP/s of five products; queries' side 1.09, keys' side 1.53, rows 0.04); one prompt of
-// 32768 tokens, 16 heads of 128 and 4 key heads, 9.6 ms (1.14 PFLOP/s); 54 thousand tokens, 16 and 4 heads of 64, in
+// heads of 64, 2.62 ms (855 TFLOP/s of five products; queries' side 1.11, keys' side 1.53, rows 0.04); one prompt of
+// 32768 tokens, 16 heads of 128 and 4 key heads, 9.7 ms (1.13 PFLOP/s); 54 thousand tokens, 16 and 4 heads of 64, in
 // a window of 512 0.65 ms.
 #include <algorithm>
 #include <type_traits>
@@ -293,16 +293,61 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const float sl2 = a.scale * kLog2e;
     const uint64_t k2 = tc::f2(sl2, sl2);
-    int id = 0, nt = 0;
+    int id = 0, nt = 0, met = 0;
+    // The sum over a row's two warps.  They meet in columns of dQ that each has read (or that hold nothing yet), in
+    // another one every other time: until then both have read.
+    auto meet = [&](float own) {
+      float both[1];
+      const uint32_t at = tQ + lanes + (met & 1);
+      tc::st32x32b_x1(at + part * (DH / 2), __float_as_uint(own));
+      tc::st_wait();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.rest);
+      ok = waited(&sh.rest, met & 1, kSiteRest, nt);
+      ++met;
+      if (!ok) return 0.f;
+      tc::fence_after();
+      tc::ld32x32b_x1(at + (part ^ 1) * (DH / 2), both[0]);
+      tc::ld_wait_row(both);
+      return own + both[0];
+    };
     for (; take(nt); ++nt) {
       const int pos = it.x.tile * kT + r;
       const bool on = pos < it.x.len;
       const int64_t row = it.h * a.np + prompt_pad(it.x.off, it.x.b) + pos;
-      const float nl = on ? a.nlse[row] : -CUDART_INF_F, nd = on ? a.nD[row] : 0.f;  // a row that does not exist weighs nothing
-      const uint64_t nl2 = tc::f2(nl, nl), nd2 = tc::f2(nd, nd);
+      const float nl = on ? a.nlse[row] : -CUDART_INF_F;  // a row that does not exist weighs nothing
+      float nd = on ? a.nD[row] : 0.f;
+      const uint64_t nl2 = tc::f2(nl, nl);
       uint64_t rest = 0;  // sum of dS
       const int first = a.window ? max(0, pos - a.window + 1) : 0;
       const int whole = a.window ? (max(0, it.x.tile * kT + kT - a.window) + kT - 1) / kT : 0;
+      if (it.lo == it.x.tile) {
+        // One block alone, so rows that see few keys: what the rounding of o puts into D is largest there.  dS is summed
+        // once beforehand, for a D that is right when it is rounded.  (Without that dQ of sequences of two tokens is off
+        // by 4.0e-3 of its size, of 17 by 2.9e-3, now by 2.4e-3; of single tokens, whose gradient is 0, it is 0.  It
+        // costs short prompts' gradients 7 us of 92.)
+        ok = waited(&sh.s[0], id & 1, kSiteS, nt) && waited(&sh.dp[id & 1], (id >> 1) & 1, kSiteDp, nt);
+        if (!ok) break;
+        tc::fence_after();
+        float sum = 0.f;
+#pragma unroll 1
+        for (int c = 64 * part; c < 64 * part + 64; c += 32) {
+          float s[32], dp[32];
+          tc::ld32x32b_x32(tS + lanes + c, s);
+          tc::ld32x32b_x32(tP + 128 * (id & 1) + lanes + c, dp);
+          tc::ld_wait_row(s);
+          tc::ld_wait_row(dp);
+          const int k0 = it.x.tile * kT + c;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (on && k0 + i <= pos && k0 + i >= first) sum += tc::ex2(fmaf(s[i], sl2, nl)) * (dp[i] + nd);
+        }
+        sum = meet(sum);
+        if (!ok) break;
+        nd -= sum;
+      }
+      const uint64_t nd2 = tc::f2(nd, nd);
       for (int n = it.lo; n <= it.x.tile; ++n, ++id) {
         ok = waited(&sh.s[0], id & 1, kSiteS, n);
         if (!ok) break;
@@ -385,23 +430,11 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
         if (c < a.dh) write_row<32, 1>(tQ + lanes + c, 0, to + c, a.scale, on);
       // A row of dS sums to 0 by its D; what is left is how far D, of the rounded output, is off.  The keys' side takes
       // the D that is right: in rows that see few keys the difference is as large as the roundings of dS.
-      // (The parts' sums meet in columns of dQ that the part has read.)
       float x, y;
       tc::uf2(rest, x, y);
-      tc::st32x32b_x1(tQ + lanes + col, __float_as_uint(x + y));
-      tc::st_wait();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sh.rest);
-      if (part == 0) {
-        ok = waited(&sh.rest, nt & 1, kSiteRest, nt);
-        if (!ok) break;
-        tc::fence_after();
-        float other[1];
-        tc::ld32x32b_x1(tQ + lanes + DH / 2, other[0]);
-        tc::ld_wait_row(other);
-        if (on) a.nD[row] = nd - ((x + y) + other[0]);
-      }
+      const float left = meet(x + y);
+      if (!ok) break;
+      if (part == 0 && on) a.nD[row] = nd - left;
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.acc_free);

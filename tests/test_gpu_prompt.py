@@ -168,6 +168,21 @@ def test_prompt_large_logits(dtype, dh):
         within(host(x), r[name], lim[name], name)
 
 
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_prompt_single_tokens_have_no_gradient(dtype, dh):
+    """A row that sees itself alone has dS = 0.  What is left: P = 1 to a logit's roundings, 2 (dh + 8) u |s| <= 5e-4
+    for |s| <= 30, times <do, v> - D with D of the rounded output, 2^-8 dh |do v| <= 4, times scale |k| <= 1 / 2."""
+    g = _g()
+    N, H = 70, 3
+    q, k, v, do = (torch.randn(N, H, dh, device="cuda").to(TORCH[dtype]) for _ in range(4))
+    off = ints(np.arange(N + 1))
+    o, lse = g.prompt_attention(q, k, v, off)
+    assert torch.equal(o, v)
+    dq, dk, dv = g.prompt_attention_backward(q, k, v, o, do, lse, off)
+    assert float(dq.abs().max()) <= 1e-3 and float(dk.abs().max()) <= 1e-3
+    assert float((dv.float() - do.float()).abs().max()) <= 2 * HALF[dtype] * float(do.abs().max()) + 1e-6
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_views_scale_and_gradients_into_views(dtype):
     """Views of a fused projection, heads-first storage, one key head repeated, a scale of its own, and
