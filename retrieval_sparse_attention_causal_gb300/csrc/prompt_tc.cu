@@ -5,7 +5,7 @@
 // takes twice as long.  Both have to work at once, so a CTA (one on an SM, persistent) holds two tiles of
 // rows that take turns: while one tile's softmax runs, the other's products do.  The two tiles are two
 // heads that share a key head where their number is even, else two neighbouring tiles of one head; either
-// way they read the same keys.
+// way they read the same keys.  (A last tile without a neighbour: see item_of.)
 //   * one warp loads: the rows' tiles, and blocks of 128 keys of K and V in turn through a ring, from the
 //     diagonal down (so a tile's first block is the one with the causal mask, which has to be weighed by
 //     its maximum anyway);
@@ -24,8 +24,8 @@
 // it (the tensor map fills them in).
 // Measured, bf16, in a graph: one prompt of 32768 tokens, 16 heads of 128 and 4 key heads, 2.5 ms (1.75 PFLOP/s, the
 // tensor pipe), with dh 64 1.64 ms (1.34; exponentials and issue); four documents of 46 thousand tokens in all,
-// 12 heads of 64, 0.73 ms (1.23); 54 thousand tokens, 16 and 4 heads, in a window of 512 200 us; 48 prompts of up
-// to 300 tokens 35 us, five work items a CTA of some 5 thousand cycles each: load, masked block, store.
+// 12 heads of 64, 0.73 ms (1.23); 54 thousand tokens, 16 and 4 heads, in a window of 512 197 us; 48 prompts of up
+// to 300 tokens 29 us, three or four work items a CTA of some 5 thousand cycles each: load, masked block, store.
 #include <algorithm>
 #include <type_traits>
 
@@ -66,7 +66,8 @@ struct Item {
   PromptTile x;
   int head[2], tile[2];        // of each tile of rows
   int hi[2], lo[2];            // its blocks; hi < lo: there is no such tile
-  int m;                       // the key head
+  int m[2];                    // their key heads
+  int own;                     // 1: each tile has blocks of its own, of its key head (they see the same ones)
   int more;                    // 0: there is none any more
   __device__ __forceinline__ int top() const { return max(hi[0], hi[1]); }
   __device__ __forceinline__ int low() const { return hi[1] < lo[1] ? lo[0] : min(lo[0], lo[1]); }
@@ -74,33 +75,56 @@ struct Item {
   __device__ __forceinline__ int units() const { return max(0, hi[0] - lo[0] + 1) + max(0, hi[1] - lo[1] + 1); }
 };
 
-// The sequences' tiles: of 128 rows where an item is two heads of a tile, of 256 where it is two tiles of a head.
+// Of the sequences' tiles of 128 rows: all, those in pairs (COUNT 2), or the last one where it is alone (COUNT 1).
+template <int COUNT>
 struct Counts {
-  const int* kept;
+  PromptTiles<kT> tiles;
   int mine;
-  static __device__ __forceinline__ int of(const PromptArgs& a, int b) {
-    return a.g % 2 == 0 ? PromptTiles<kT>::of(a, b) : PromptTiles<2 * kT>::of(a, b);
-  }
-  __device__ __forceinline__ Counts(const int* keep) : kept(keep), mine(keep[threadIdx.x & 31]) {}
-  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return b < PromptTiles<kT>::kKeep ? kept[b] : of(a, b); }
+  static __device__ __forceinline__ int of(int n) { return COUNT == 2 ? n >> 1 : COUNT == 1 ? n & 1 : n; }
+  __device__ __forceinline__ Counts(const int* keep) : tiles(keep), mine(of(tiles.mine)) {}
+  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return of(tiles(a, b)); }
 };
-__device__ __forceinline__ bool item_of(const PromptArgs& a, const Counts& counts, int w, Item& it) {
-  const bool heads = a.g % 2 == 0;  // two heads of a tile, or two tiles of a head
-  const int per = heads ? a.H / 2 : a.H, h = w % per, rank = w / per;
-  if (!prompt_tile(a, counts, rank, false, it.x)) return false;
-  if (heads) {
-    it.head[0] = 2 * h;
-    it.head[1] = 2 * h + 1;
+// Work item w.  Two heads that share a key head have the same tile, where their number is even.  Else an item is two
+// neighbouring tiles of a head, and the last tile of a sequence that has none beside it goes with the next head's, each
+// with its own keys: 48 prompts of up to 300 tokens 32 us alone, 29 together, 64 of 100 tokens 29 and 21.  (These
+// come first: there may be long ones among them.)  Where there are CTAs for all of them they stay alone, for a tile by
+// itself is done sooner.
+__device__ __forceinline__ bool item_of(const PromptArgs& a, const int* keep, int w, Item& it) {
+  it.own = 0;
+  bool second = true;
+  if (a.g % 2 == 0) {
+    const int h = 2 * (w % (a.H / 2));
+    if (!prompt_tile(a, Counts<0>(keep), w / (a.H / 2), false, it.x)) return false;
+    it.head[0] = h;
+    it.head[1] = h + 1;
     it.tile[0] = it.tile[1] = it.x.tile;
   } else {
-    it.head[0] = it.head[1] = h;
-    it.tile[0] = 2 * it.x.tile;
-    it.tile[1] = 2 * it.x.tile + 1;
+    const Counts<1> alone(keep);
+    int n = 0;
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) n += b < 32 ? alone.mine : alone(a, b);
+    n = (int)__reduce_add_sync(kAll, n);
+    it.own = (int64_t)n * a.H > gridDim.x;
+    const int per = it.own ? (a.H + 1) / 2 : a.H, h = w % per;
+    if (w < n * per) {
+      if (!prompt_tile(a, alone, w / per, false, it.x)) return false;
+      it.head[0] = it.own ? 2 * h : h;
+      it.head[1] = it.head[0] + 1;
+      it.tile[0] = it.tile[1] = (it.x.len - 1) / kT;
+      second = it.own && it.head[1] < a.H;
+    } else {
+      it.own = 0;
+      w -= n * per;
+      if (!prompt_tile(a, Counts<2>(keep), w / a.H, false, it.x)) return false;
+      it.head[0] = it.head[1] = w % a.H;
+      it.tile[0] = 2 * it.x.tile;
+      it.tile[1] = 2 * it.x.tile + 1;
+    }
   }
-  it.m = it.head[0] / a.g;
+  it.own = it.own && second;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    it.hi[t] = it.tile[t] * kT < it.x.len ? it.tile[t] : -1;
+    it.m[t] = it.head[t] / a.g;
+    it.hi[t] = t == 0 || second ? it.tile[t] : -1;
     it.lo[t] = a.window ? max(0, it.tile[t] * kT - a.window + 1) / kT : 0;
   }
   return true;
@@ -148,7 +172,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     abort_s = 0;
     tc::fence_mbar_init();
   }
-  for (int b = tid; b < PromptTiles<kT>::kKeep; b += kThreads) keep[b] = Counts::of(a, b);
+  PromptTiles<kT>::fill(a, keep);
   if (warp == 8) tc::tmem_alloc(&tmem_slot, kCols);
   tc::fence_before();
   __syncthreads();
@@ -169,9 +193,8 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
     int nq[2] = {0, 0};      // tiles of rows so far
-    const Counts counts(keep);
     for (int turn = 0; ok; ++turn) {
-      it.more = item_of(a, counts, prompt_turn(turn), it);
+      it.more = item_of(a, keep, prompt_turn(turn), it);
       ok = put_item(items, turn, it, waited, kSiteItem);
       if (!ok || !it.more) break;
       auto rows = [&](int t) {
@@ -187,14 +210,15 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       const int top = it.top(), low = it.low();
       for (int n = top; n >= low && ok; --n)
 #pragma unroll 1
-        for (int v = 0; v < 2 && ok; ++v) {
-          if (n == top) rows(v);
+        for (int u = 0; u < 2 + 2 * it.own && ok; ++u) {  // K, then V; of both tiles' key heads where they have their own
+          const int v = u & 1, m = u < 2 ? it.m[0] : it.m[1];
+          if (n == top && u < 2) rows(u);
           ok = ok && waited(&bar_empty[st], parity ^ 1, kSiteEmpty, n);
           if (!ok) break;
           tc::mbar_expect_tx_warp(&bar_full[st], C::BLOCK);
 #pragma unroll
           for (int s = 0; s < SUB; ++s)
-            tc::tma_load_4d_warp(ring + st * C::BLOCK + s * kTile, v ? &tmV : &tmK, 64 * s, (v ? a.v_hs : a.k_hs) ? it.m : 0,
+            tc::tma_load_4d_warp(ring + st * C::BLOCK + s * kTile, v ? &tmV : &tmK, 64 * s, (v ? a.v_hs : a.k_hs) ? m : 0,
                                  it.x.off + n * kT, 0, &bar_full[st]);
           ++id;
           if (++st == NS) {
@@ -210,63 +234,83 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- logits: S = Q K^T into the buffer of the unit
-    int ks = 0, buf = 0, nq[2] = {0, 0}, own[2] = {0, 0};  // K's slot, the buffer; tiles and units of each tile's warps so far
+    int ks = 0, buf = 0, nq[2] = {0, 0}, own_units[2] = {0, 0};  // K's slot, the buffer; tiles and units of each tile's warps so far
     uint32_t kp = 0, bp = 1;              // the parities of K's filling, and of the buffer's last use
     const uint64_t dQ = tc::desc_km(tc::su32(Qs));
-    for (int turn = 0; take(turn); ++turn) {
+    auto blocks = [&](auto own) {
       const int low = it.low();
       for (int n = it.top(); n >= low && ok; --n) {
-        ok = waited(&bar_full[ks], kp, kSiteFull, n);
-        const uint32_t k = tc::su32(ring + ks * C::BLOCK);
+        auto fetched = [&]() { return ok = waited(&bar_full[ks], kp, kSiteFull, n); };
+        auto read = [&]() {
+          tc::commit_warp(&bar_empty[ks]);
+          ks += 2;
+          if (ks >= NS) {
+            ks -= NS;
+            kp ^= 1;
+          }
+        };
+        if (!fetched()) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!it.has(t, n)) continue;
+          if (decltype(own)::value && t == 1 && !fetched()) break;
           if (n == it.hi[t]) {
-            ok = ok && waited(&bar_q[t], nq[t] & 1, kSiteQ, n);
+            ok = waited(&bar_q[t], nq[t] & 1, kSiteQ, n);
             ++nq[t];
           }
           ok = ok && waited(&bar_done[buf], bp, kSiteDone, n);
           if (!ok) break;
           tc::fence_after();
+          const uint32_t k = tc::su32(ring + ks * C::BLOCK);
 #pragma unroll
           for (int s = 0; s < SUB; ++s)
             tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(tmem + kT * buf, dQ + ((t * C::BLOCK + s * kTile) >> 4), tc::desc_km(k + s * kTile), kIdS, s ? 1u : 0u);
-          tc::commit_warp(&bar_s[t][own[t]]);
-          if (++own[t] == NBUF) own[t] = 0;
+          tc::commit_warp(&bar_s[t][own_units[t]]);
+          if (++own_units[t] == NBUF) own_units[t] = 0;
           if (n == it.lo[t]) tc::commit_warp(&bar_qfree[t]);
           if (++buf == NBUF) {
             buf = 0;
             bp ^= 1;
           }
+          if (decltype(own)::value && t == 0) read();
         }
         if (!ok) break;
-        tc::commit_warp(&bar_empty[ks]);
-        ks += 2;
-        if (ks >= NS) {
-          ks -= NS;
-          kp ^= 1;
-        }
+        read();
       }
+    };
+    for (int turn = 0; take(turn); ++turn) {
+      if (it.own) blocks(std::true_type{});
+      else blocks(std::false_type{});
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- outputs: O += P V
     int vs = 1, buf = 0, no[2] = {0, 0};
     uint32_t vp = 0, bp = 0;
-    for (int turn = 0; take(turn); ++turn) {
+    auto blocks = [&](auto own) {
       const int low = it.low();
       for (int n = it.top(); n >= low && ok; --n) {
-        ok = waited(&bar_full[vs], vp, kSiteFull, n);
-        const uint32_t v = tc::su32(ring + vs * C::BLOCK);
+        auto fetched = [&]() { return ok = waited(&bar_full[vs], vp, kSiteFull, n); };
+        auto read = [&]() {
+          tc::commit_warp(&bar_empty[vs]);
+          vs += 2;
+          if (vs >= NS) {
+            vs -= NS;
+            vp ^= 1;
+          }
+        };
+        if (!fetched()) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!it.has(t, n)) continue;
+          if (decltype(own)::value && t == 1 && !fetched()) break;
           if (n == it.hi[t]) {
-            ok = ok && waited(&bar_ofree[t], (no[t] & 1) ^ 1, kSiteOFree, n);  // read by the tile before
+            ok = waited(&bar_ofree[t], (no[t] & 1) ^ 1, kSiteOFree, n);  // read by the tile before
             ++no[t];
           }
           ok = ok && waited(&bar_p[buf], bp, kSiteP, n);
           if (!ok) break;
           tc::fence_after();
+          const uint32_t v = tc::su32(ring + vs * C::BLOCK);
           const uint32_t tO = tmem + NBUF * kT + DH * t, tP = tmem + kT * buf;
 #pragma unroll
           for (int s = 0; s < SUB; ++s) {
@@ -279,15 +323,15 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
             buf = 0;
             bp ^= 1;
           }
+          if (decltype(own)::value && t == 0) read();
         }
         if (!ok) break;
-        tc::commit_warp(&bar_empty[vs]);
-        vs += 2;
-        if (vs >= NS) {
-          vs -= NS;
-          vp ^= 1;
-        }
+        read();
       }
+    };
+    for (int turn = 0; take(turn); ++turn) {
+      if (it.own) blocks(std::true_type{});
+      else blocks(std::false_type{});
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -389,7 +433,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
           if (n == hi && (n + 1) * kT > it.x.len) {
             // Rows of V behind the sequence become zeros (by this tile's softmax where it is the tile that
             // reaches them, or by both with the same zeros).
-            const int i = slot + 2 * (top - n) + 1;
+            const int i = slot + (2 + 2 * it.own) * (top - n) + 1 + 2 * t * it.own;
             ok = waited(&bar_full[i % NS], (i / NS) & 1, kSiteV, n);
             if (!ok) break;
             if (n * kT + r >= it.x.len)
@@ -466,7 +510,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
         unit += 1 + it.has(1 - t, t ? n - 1 : n);
       }
       unit0 += it.units();
-      slot += 2 * (top - it.low() + 1);
+      slot += (2 + 2 * it.own) * (top - it.low() + 1);
       const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
       if (!ok || hi < lo) continue;
       ok = waited(&bar_o[t], no & 1, kSiteO, -1);  // (of its own: a buffer's could be two units further by now)

@@ -93,6 +93,9 @@ CASES = [  # lengths, H, Hkv, dh, window, dtype
     ((1500,), 2, 1, 64, 1000, "bf16"),
     (tuple([3, 70] * 40), 2, 2, 64, 0, "bf16"),
     (tuple([130, 0, 1, 260] * 17), 2, 1, 64, 50, "bf16"),
+    (tuple([100, 300, 20] * 20), 5, 5, 64, 0, "bf16"),
+    (tuple([300, 40] * 40), 3, 1, 128, 60, "bf16"),
+    (tuple([400, 128] * 30), 7, 7, 32, 200, "bf16"),
     ((1,), 1, 1, 32, 0, "f32"),
     ((64, 65, 0, 63), 2, 1, 64, 0, "f32"),
     ((200, 3), 6, 2, 32, 0, "f32"),
@@ -736,6 +739,33 @@ def test_quantised_chunks_and_slots_named_twice():
         a, b = split(a)[0], split(b)
         assert torch.equal(b[0], a[[2, 2, 0]]) and torch.equal(b[1], a[[1, 0, 1]]) and torch.equal(b[2, 0], b[2, 1]) and (b[2, 2] == 0).all()
     assert two[2].tolist() == [[0, 1, 2], [0, 1, 2], [0, 1, -1]]
+
+
+def test_more_elements_than_an_int_counts():
+    """Tensors of more than 2^31 elements: the last rows are what they are in small tensors."""
+    g = _g()
+    n, L, H, dh = 530, 1000, 64, 64  # 2.17e9 elements
+    N, last = n * L, (n - 1) * L
+    q, k, v = (torch.randn(N, h, dh, device="cuda", dtype=torch.bfloat16) for h in (H, 1, 1))
+    off, one = ints(np.arange(n + 1) * L), ints([0, L])
+    o, lse = g.prompt_attention(q, k, v, off)
+    grads = g.prompt_attention_backward(q, k, v, o, q, lse, off)
+    s = [x[last:].contiguous() for x in (q, k, v)]
+    o1, l1 = g.prompt_attention(*s, one)
+    assert torch.equal(o[last:], o1) and torch.equal(lse[last:], l1)
+    for x, y in zip(grads, g.prompt_attention_backward(*s, o1, s[0], l1, one)):
+        assert torch.equal(x[last:], y)
+    del o, grads
+    wt, freq, pos = torch.rand(dh, device="cuda"), g.rotary_frequencies(dh), ints(np.arange(last, N))
+    assert torch.equal(g.norm_rotary(q[None], None, wt, None, freq)[0][0, last:], g.norm_rotary(s[0][None], None, wt, None, freq, positions=pos)[0][0])
+    dx = g.norm_rotary_backward(q[None], None, q[None], None, wt, None, freq)[0]
+    assert torch.equal(dx[0, last:], g.norm_rotary_backward(s[0][None], None, s[0][None], None, wt, None, freq, positions=pos)[0][0])
+    del dx
+    pages, tail = -(-N // 64), N - N // 64 * 64
+    cache, small = (g.QuantisedCache.empty(p, 1, p, H, dh) for p in (pages, 1))
+    cache.append_packed(q, q, ints([0, N]))
+    small.append_packed(q[N - tail:], q[N - tail:], ints([0, tail]))
+    assert all(torch.equal(x, y) for x, y in zip(cache.read(ints([[pages - 1]]))[:2], small.read(ints([[0]]))[:2]))
 
 
 # ------------------------------------------------------------------ together
