@@ -150,28 +150,27 @@ __device__ __forceinline__ void accumulate(uint32_t d, uint32_t at, uint32_t b, 
 }
 
 // W columns of a row of the groups' accumulators, `apart` columns from one to the next, summed and scaled, to
-// global memory.
+// global memory: `to` is the first of them in row 0, with `have` columns there, `pos` the lane's row of `len`.
 template <int W, int G>
-__device__ __forceinline__ void write_row(uint32_t at, int apart, bf16* to, float scale, bool on) {
-  float o[W], more[W];
-  auto load = [](uint32_t from, float (&x)[W]) {
-    if constexpr (W == 32) tc::ld32x32b_x32(from, x);
-    else tc::ld32x32b_x16(from, x);
-  };
-  load(at, o);
-  if constexpr (G == 2) load(at + apart, more);
-  tc::ld_wait_row(o);
-  if constexpr (G == 2) {
-    tc::ld_wait_row(more);
+__device__ __forceinline__ void write_rows(uint32_t at, int apart, bf16* to, int64_t stride, int pos, int len, float scale, int have) {
+  uint4 x[W / 8];
 #pragma unroll
-    for (int i = 0; i < W; ++i) o[i] += more[i];
+  for (int c = 0; c < W; c += 32) {
+    float o[32], more[32];
+    tc::ld32x32b_x32(at + c, o);
+    if constexpr (G == 2) tc::ld32x32b_x32(at + apart + c, more);
+    tc::ld_wait_row(o);
+    if constexpr (G == 2) {
+      tc::ld_wait_row(more);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] += more[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[c / 8 + i] = make_uint4(pack_bf16(o[8 * i] * scale, o[8 * i + 1] * scale), pack_bf16(o[8 * i + 2] * scale, o[8 * i + 3] * scale),
+                                pack_bf16(o[8 * i + 4] * scale, o[8 * i + 5] * scale), pack_bf16(o[8 * i + 6] * scale, o[8 * i + 7] * scale));
   }
-  if (!on) return;
-#pragma unroll
-  for (int i = 0; i < W / 8; ++i)
-    *reinterpret_cast<uint4*>(to + 8 * i) =
-        make_uint4(pack_bf16(o[8 * i] * scale, o[8 * i + 1] * scale), pack_bf16(o[8 * i + 2] * scale, o[8 * i + 3] * scale),
-                   pack_bf16(o[8 * i + 4] * scale, o[8 * i + 5] * scale), pack_bf16(o[8 * i + 6] * scale, o[8 * i + 7] * scale));
+  tc::store_rows(x, reinterpret_cast<uint4*>(to), stride / 8, pos, len, have / 8);
 }
 
 struct Maps {
@@ -424,10 +423,8 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
       if (!ok) break;
       tc::fence_after();
       const int col = part * (DH / 2);
-      bf16* to = reinterpret_cast<bf16*>(a.dq) + (int64_t)(it.x.off + pos) * a.dq_ts + it.h * a.dq_hs;
-#pragma unroll
-      for (int c = col; c < col + DH / 2; c += 32)
-        if (c < a.dh) write_row<32, 1>(tQ + lanes + c, 0, to + c, a.scale, on);
+      bf16* to = reinterpret_cast<bf16*>(a.dq) + (int64_t)it.x.off * a.dq_ts + it.h * a.dq_hs + col;
+      if (col < a.dh) write_rows<DH / 2, 1>(tQ + lanes + col, 0, to, a.dq_ts, pos, it.x.len, a.scale, a.dh - col);
       // A row of dS sums to 0 by its D; what is left is how far D, of the rounded output, is off.  The keys' side takes
       // the D that is right: in rows that see few keys the difference is as large as the roundings of dS.
       float x, y;
@@ -675,13 +672,15 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
       ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
       if (!ok) break;
       tc::fence_after();
-      const int key = it.x.tile * kT + 32 * (warp & 3) + lane, col = part * (DH / 4);
-      const bool on = key < it.x.len;
-      bf16* kt = reinterpret_cast<bf16*>(a.dk) + (int64_t)(it.x.off + key) * a.dk_ts + it.m * a.dk_hs;
-      bf16* vt = reinterpret_cast<bf16*>(a.dv) + (int64_t)(it.x.off + key) * a.dv_ts + it.m * a.dv_hs;
+      // Half a row of dV, or of dK, a warp.
+      const int key = it.x.tile * kT + 32 * (warp & 3) + lane, col = (part & 1) * (DH / 2);
       if (col < a.dh) {
-        write_row<DH / 4, G>(tV + lanes + col, 2 * DH, vt + col, 1.f, on);
-        write_row<DH / 4, G>(tK + lanes + col, 2 * DH, kt + col, a.scale, on);
+        if (part < 2)
+          write_rows<DH / 2, G>(tV + lanes + col, 2 * DH, reinterpret_cast<bf16*>(a.dv) + (int64_t)it.x.off * a.dv_ts + it.m * a.dv_hs + col,
+                                a.dv_ts, key, it.x.len, 1.f, a.dh - col);
+        else
+          write_rows<DH / 2, G>(tK + lanes + col, 2 * DH, reinterpret_cast<bf16*>(a.dk) + (int64_t)it.x.off * a.dk_ts + it.m * a.dk_hs + col,
+                                a.dk_ts, key, it.x.len, a.scale, a.dh - col);
       }
       tc::fence_before();
       __syncwarp();

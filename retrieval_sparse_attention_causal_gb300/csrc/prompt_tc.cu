@@ -518,19 +518,21 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       if (!ok) break;
       tc::fence_after();
       const float inv = 1.f / l;
-      bf16* row = reinterpret_cast<bf16*>(a.o) + to * a.dh;
+      uint4* rows = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + ((int64_t)it.x.off * a.H + it.head[t]) * a.dh);
 #pragma unroll
-      for (int q = 0; q < DH / 32; ++q) {
-        if (32 * q >= a.dh) break;
-        float o[32];
-        tc::ld32x32b_x32(tO + 32 * q, o);
-        tc::ld_wait_row(o);
-        if (!on) continue;
+      for (int half = 0; half < DH / 64; ++half) {
+        uint4 x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(row + 32 * q + 8 * i) =
-              make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                         pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        for (int q = 0; q < 2; ++q) {
+          float o[32];
+          tc::ld32x32b_x32(tO + 64 * half + 32 * q, o);
+          tc::ld_wait_row(o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[4 * q + i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                      pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        }
+        tc::store_rows(x, rows + 8 * half, (int64_t)a.H * (a.dh / 8), pos, it.x.len, a.dh / 8);
       }
       tc::fence_before();
       __syncwarp();
