@@ -21,9 +21,9 @@
 // Rows behind a sequence's end may hold anything: as operands that are summed over they become zeros in
 // shared memory, elsewhere their results are not used.
 // Measured, bf16, in a graph, with the rows' sums of prompt_attn.cu: four documents of 46 thousand tokens in all, 12
-// heads of 64, 2.62 ms (855 TFLOP/s of five products; queries' side 1.11, keys' side 1.53, rows 0.04); one prompt of
+// heads of 64, 2.59 ms (866 TFLOP/s of five products; queries' side 1.09, keys' side 1.51, rows 0.04); one prompt of
 // 32768 tokens, 16 heads of 128 and 4 key heads, 9.7 ms (1.13 PFLOP/s); 54 thousand tokens, 16 and 4 heads of 64, in
-// a window of 512 0.65 ms.
+// a window of 512 0.64 ms.
 #include <algorithm>
 #include <type_traits>
 
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
         // One block alone, so rows that see few keys: what the rounding of o puts into D is largest there.  dS is summed
         // once beforehand, for a D that is right when it is rounded.  (Without that dQ of sequences of two tokens is off
         // by 4.0e-3 of its size, of 17 by 2.9e-3, now by 2.4e-3; of single tokens, whose gradient is 0, it is 0.  It
-        // costs short prompts' gradients some 5 us of 80.)
+        // costs short prompts' gradients some 5 us of 78.)
         ok = waited(&sh.s[0], id & 1, kSiteS, nt) && waited(&sh.dp[id & 1], (id >> 1) & 1, kSiteDp, nt);
         if (!ok) break;
         tc::fence_after();
