@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
     return wait_on(bar, parity, &sh.abort, a.err, site, blockIdx.x, at);
   };
   QItem it;
-  auto take = [&](int n) { return (ok = ok && take_item(items, n, it, waited, kSiteItem)) && it.more; };
+  auto take_into = [&](int n, QItem& x) { return (ok = ok && take_item(items, n, x, waited, kSiteItem)) && x.more; };
+  auto take = [&](int n) { return take_into(n, it); };
 
   if (warp == kElemQ + 2) {
     // ---------------------------------------------------------------- loads
@@ -311,12 +312,17 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
       tc::ld_wait_row(both);
       return own + both[0];
     };
-    for (; take(nt); ++nt) {
+    // -lse log2(e) and -D of the item's row; a row that does not exist weighs nothing.
+    auto row_of = [&](const QItem& x) { return x.h * a.np + prompt_pad(x.x.off, x.x.b) + x.x.tile * kT + r; };
+    float nl = -CUDART_INF_F, nd = 0.f;
+    bool more = take(0);
+    if (more && it.x.tile * kT + r < it.x.len) {
+      nl = a.nlse[row_of(it)];
+      nd = a.nD[row_of(it)];
+    }
+    for (; more; ++nt) {
       const int pos = it.x.tile * kT + r;
       const bool on = pos < it.x.len;
-      const int64_t row = it.h * a.np + prompt_pad(it.x.off, it.x.b) + pos;
-      const float nl = on ? a.nlse[row] : -CUDART_INF_F;  // a row that does not exist weighs nothing
-      float nd = on ? a.nD[row] : 0.f;
       const uint64_t nl2 = tc::f2(nl, nl);
       uint64_t rest = 0;  // sum of dS
       const int first = a.window ? max(0, pos - a.window + 1) : 0;
@@ -419,6 +425,15 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
         if (lane == 0) tc::mbar_arrive(&sh.ds[id & 1]);  // (a warp is never two blocks ahead of another: dP of the second waits for all)
       }
       if (!ok) break;
+      // The next row's sums are on their way while this one's gradients are written.
+      QItem next;
+      more = take_into(nt + 1, next);
+      if (!ok) break;
+      float next_nl = -CUDART_INF_F, next_nd = 0.f;
+      if (more && next.x.tile * kT + r < next.x.len) {
+        next_nl = a.nlse[row_of(next)];
+        next_nd = a.nD[row_of(next)];
+      }
       ok = waited(&sh.acc, nt & 1, kSiteAcc, nt);
       if (!ok) break;
       tc::fence_after();
@@ -431,10 +446,13 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
       tc::uf2(rest, x, y);
       const float left = meet(x + y);
       if (!ok) break;
-      if (part == 0 && on) a.nD[row] = nd - left;
+      if (part == 0 && on) a.nD[row_of(it)] = nd - left;
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.acc_free);
+      it = next;
+      nl = next_nl;
+      nd = next_nd;
     }
   }
   tc::fence_before();
