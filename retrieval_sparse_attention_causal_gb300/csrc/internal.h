@@ -20,10 +20,11 @@ cudaError_t launch_end(const char* name, cudaStream_t s);
 // Launches a kernel that may start before the previous one of the stream has ended (it waits
 // for it with after_previous()): its launch and its first steps overlap that one's end.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+cudaError_t launch_after_smem(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c{};
   c.gridDim = grid;
   c.blockDim = block;
+  c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -31,6 +32,10 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream
   c.attrs = &at;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  return launch_after_smem(kernel, grid, block, 0, s, args...);
 }
 
 // Records `msg` as the calling thread's error detail and returns `s`.

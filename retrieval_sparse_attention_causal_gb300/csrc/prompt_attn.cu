@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
 // way 50, with four 53: fewer warps fit).
 template <typename T, int DH>
 __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
+  let_next();  // (in bf16.  float32's kernels, several CTAs an SM, are placed worse if they start early: 114 us for 86.)
   constexpr int V = Elem<T>::kVec, LANES = DH / V, SIDE = 32 / LANES, FLY = 2;  // lanes of a row, rows side by side
   const int lane = threadIdx.x & 31, at = lane % LANES, h0 = lane / LANES;
   const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;

@@ -23,7 +23,8 @@
 // Measured, bf16, in a graph, with the rows' sums of prompt_attn.cu: four documents of 46 thousand tokens in all, 12
 // heads of 64, 2.59 ms (866 TFLOP/s of five products; queries' side 1.09, keys' side 1.51, rows 0.04); one prompt of
 // 32768 tokens, 16 heads of 128 and 4 key heads, 9.7 ms (1.13 PFLOP/s); 54 thousand tokens, 16 and 4 heads of 64, in
-// a window of 512 0.64 ms.
+// a window of 512 0.62 ms; one prompt of 77 tokens 14 us, where each of the two starts while what is ahead of it
+// ends (17 without).
 #include <algorithm>
 #include <type_traits>
 
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
   __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   set_up<DH, 1, kElemQ>(a, sh, items, kElemQ + 2);
+  let_next();
   const uint32_t tS = sh.tmem, tP = tS + 128, tQ = tS + 384;  // S, two of dP, dQ
   bool ok = true;
   auto waited = [&](uint64_t* bar, uint32_t parity, int site, int at) {
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
     auto row_of = [&](const QItem& x) { return x.h * a.np + prompt_pad(x.x.off, x.x.b) + x.x.tile * kT + r; };
     float nl = -CUDART_INF_F, nd = 0.f;
     bool more = take(0);
+    after_previous();  // the rows' sums
     if (more && it.x.tile * kT + r < it.x.len) {
       nl = a.nlse[row_of(it)];
       nd = a.nD[row_of(it)];
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
         // One block alone, so rows that see few keys: what the rounding of o puts into D is largest there.  dS is summed
         // once beforehand, for a D that is right when it is rounded.  (Without that dQ of sequences of two tokens is off
         // by 4.0e-3 of its size, of 17 by 2.9e-3, now by 2.4e-3; of single tokens, whose gradient is 0, it is 0.  It
-        // costs short prompts' gradients some 5 us of 78.)
+        // costs short prompts' gradients some 5 us of 73.)
         ok = waited(&sh.s[0], id & 1, kSiteS, nt) && waited(&sh.dp[id & 1], (id >> 1) & 1, kSiteDp, nt);
         if (!ok) break;
         tc::fence_after();
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
   __shared__ __align__(8) PromptItems<KvItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   set_up<DH, G, kElemKv>(a, sh, items, kElemKv + G);
+  if (warp != kElemKv + G) after_previous();  // (before any wait with a limit: the queries' side may take long)
   // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
   const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
   bool ok = true;
@@ -518,6 +522,7 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
         tc::tma_load_4d_warp(to, &tm.k, 64 * s, a.k_hs ? it.m : 0, it.x.off + it.x.tile * kT, 0, &sh.tile[buf]);
         tc::tma_load_4d_warp(to + C::BLOCK, &tm.v, 64 * s, a.v_hs ? it.m : 0, it.x.off + it.x.tile * kT, 0, &sh.tile[buf]);
       }
+      if (nt == 0) after_previous();  // the rows' sums, as the queries' side left them
       for (int h = it.m * a.g; h < it.m * a.g + a.g && ok; ++h)
         for (int i = it.x.tile; i < it.end; ++i, ++id) {
           const int st = id % NS;
@@ -726,12 +731,14 @@ cudaError_t run_tc(const PromptArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.N / kT + std::min<int64_t>(a.B, a.N);
   launch_begin("prompt_dq_tc", s);
-  prompt_dq_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.H, kSMs), threads_of(kElemQ, 2), C::SMEM_Q, s>>>(a, tm);
-  e = launch_end("prompt_dq_tc", s);
+  e = launch_after_smem(prompt_dq_tc_kernel<DH>, dim3((unsigned)std::min<int64_t>(tiles * a.H, kSMs)), dim3(threads_of(kElemQ, 2)), C::SMEM_Q, s, a, tm);
+  cudaError_t last = launch_end("prompt_dq_tc", s);
+  if (e == cudaSuccess) e = last;
   if (e != cudaSuccess) return e;
   launch_begin("prompt_dkv_tc", s);
-  prompt_dkv_tc_kernel<DH><<<(unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs), threads_of(kElemKv, C::G), C::SMEM_KV, s>>>(a, tm);
-  return launch_end("prompt_dkv_tc", s);
+  e = launch_after_smem(prompt_dkv_tc_kernel<DH>, dim3((unsigned)std::min<int64_t>(tiles * a.Hkv, kSMs)), dim3(threads_of(kElemKv, C::G)), C::SMEM_KV, s, a, tm);
+  last = launch_end("prompt_dkv_tc", s);
+  return e != cudaSuccess ? e : last;
 }
 
 }  // namespace
