@@ -137,17 +137,17 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b, int 
     tc::mma4_ss<tc::kKStepKm, tc::kKStepKm>(d + N * grp, tc::desc_km(a + s * kTile), tc::desc_km(b + s * kTile + grp * N * 128),
                                             tc::idesc_bf16(kT, N, false), s ? 1u : 0u);
 }
-// D[128 x DH] (+)= A B with group `grp`'s columns of A [128 x 128] in TMEM and rows of B [128 x DH] in shared memory.  A's
-// columns lie side by side (GAP 0), or each 16 of them in front of GAP others.
-template <int DH, int G, int GAP>
+// D[128 x DH] (+)= A B with group `grp`'s columns of A [128 x 128] in TMEM, each 16 of them in front of 16 others, and rows
+// of B [128 x DH] in shared memory.
+template <int DH, int G>
 __device__ __forceinline__ void accumulate(uint32_t d, uint32_t at, uint32_t b, int grp, bool add) {
   constexpr int H = 2 / G;  // runs of 64 rows
 #pragma unroll
   for (int s = 0; s < Tc<DH>::SUB; ++s)
 #pragma unroll
     for (int h = 0; h < H; ++h)
-      tc::mma4_ts<8, 16 + GAP, 24 + GAP, tc::kKStepMn>(d + 64 * s, at + (32 + 2 * GAP) * (H * grp + h),
-                                                       tc::desc_mn(b + s * kTile + kTile / 2 * (H * grp + h)), tc::idesc_bf16(kT, 64, true), add || h ? 1u : 0u);
+      tc::mma4_ts<8, 32, 40, tc::kKStepMn>(d + 64 * s, at + 64 * (H * grp + h),
+                                         tc::desc_mn(b + s * kTile + kTile / 2 * (H * grp + h)), tc::idesc_bf16(kT, 64, true), add || h ? 1u : 0u);
 }
 
 // W columns of a row of the groups' accumulators, `apart` columns from one to the next, summed and scaled, to
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
         ok = waited(&sh.ds[id & 1], (id >> 1) & 1, kSiteDs, n);
         if (!ok) break;
         tc::fence_after();
-        accumulate<DH, 1, 16>(tQ, tP + 128 * (id & 1), tc::su32(ring + ks * C::BLOCK), 0, n > it.lo);
+        accumulate<DH, 1>(tQ, tP + 128 * (id & 1), tc::su32(ring + ks * C::BLOCK), 0, n > it.lo);
         tc::commit_warp(&sh.done[id & 1]);
         tc::commit_warp(&sh.empty[ks]);
       }
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
           ok = (x > 0 || waited(&sh.acc_free, (nt & 1) ^ 1, kSiteAccFree, nt)) && waited(&sh.p[w], i & 1, kSiteP, x);
           if (!ok) break;
           tc::fence_after();
-          accumulate<DH, G, 16>(tVw, tS, q + C::BLOCK, w, x > 0);
+          accumulate<DH, G>(tVw, tS, q + C::BLOCK, w, x > 0);
         }
         if (x + 1 < count) {
           ok = waited(&sh.full[next], ((i + 1) / NS) & 1, kSiteFull, x);
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
           ok = waited(&sh.ds[w], i & 1, kSiteDs, x);
           if (!ok) break;
           tc::fence_after();
-          accumulate<DH, G, 16>(tKw, tP, q, w, x > 0);
+          accumulate<DH, G>(tKw, tP, q, w, x > 0);
           tc::commit_warp(&sh.empty[st]);
         }
         if (x + 1 < count) {
