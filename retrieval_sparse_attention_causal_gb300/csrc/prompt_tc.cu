@@ -197,7 +197,8 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       it.more = item_of(a, keep, prompt_turn(turn), it);
       ok = put_item(items, turn, it, waited, kSiteItem);
       if (!ok || !it.more) break;
-      auto rows = [&](int t) {
+      auto rows = [&](auto tile) {
+        constexpr int t = decltype(tile)::value;
         if (it.hi[t] < it.lo[t]) return;
         ok = ok && waited(&bar_qfree[t], (nq[t] & 1) ^ 1, kSiteQFree, turn);
         if (!ok) return;
@@ -212,7 +213,8 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
 #pragma unroll 1
         for (int u = 0; u < 2 + 2 * it.own && ok; ++u) {  // K, then V; of both tiles' key heads where they have their own
           const int v = u & 1, m = u < 2 ? it.m[0] : it.m[1];
-          if (n == top && u < 2) rows(u);
+          if (n == top && u == 0) rows(std::integral_constant<int, 0>{});
+          if (n == top && u == 1) rows(std::integral_constant<int, 1>{});
           ok = ok && waited(&bar_empty[st], parity ^ 1, kSiteEmpty, n);
           if (!ok) break;
           tc::mbar_expect_tx_warp(&bar_full[st], C::BLOCK);
@@ -341,11 +343,13 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     const uint32_t tO = tmem + NBUF * kT + DH * t + lanes;
     int unit0 = 0, slot = 0, no = 0, own = 0;  // units of work and ring slots before the item, own tiles and own units so far
     for (int turn = 0; take(turn); ++turn) {
-      const int hi = it.hi[t], lo = it.lo[t], top = it.top();
-      const int pos = it.tile[t] * kT + r;
+      // (Chosen, not indexed by t: the item stays in registers.)
+      const int hi = t ? it.hi[1] : it.hi[0], lo = t ? it.lo[1] : it.lo[0], top = it.top();
+      const int tile = t ? it.tile[1] : it.tile[0], head = t ? it.head[1] : it.head[0];
+      const int pos = tile * kT + r;
       const bool on = pos < it.x.len;
       const int first = a.window ? max(0, pos - a.window + 1) : 0;  // the first key that the row sees
-      const int whole = a.window ? (max(0, it.tile[t] * kT + kT - a.window) + kT - 1) / kT : 0;  // blocks from here to hi - 1 are seen whole
+      const int whole = a.window ? (max(0, tile * kT + kT - a.window) + kT - 1) / kT : 0;  // blocks from here to hi - 1 are seen whole
       float mx = -CUDART_INF_F, l = 0.f;
       const uint64_t k2 = tc::f2(sl2, sl2);
       uint64_t sums[4], b2 = 0;
@@ -511,14 +515,14 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       }
       unit0 += it.units();
       slot += (2 + 2 * it.own) * (top - it.low() + 1);
-      const int64_t to = (int64_t)(it.x.off + pos) * a.H + it.head[t];
+      const int64_t to = (int64_t)(it.x.off + pos) * a.H + head;
       if (!ok || hi < lo) continue;
       ok = waited(&bar_o[t], no & 1, kSiteO, -1);  // (of its own: a buffer's could be two units further by now)
       ++no;
       if (!ok) break;
       tc::fence_after();
       const float inv = 1.f / l;
-      uint4* rows = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + ((int64_t)it.x.off * a.H + it.head[t]) * a.dh);
+      uint4* rows = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.o) + ((int64_t)it.x.off * a.H + head) * a.dh);
 #pragma unroll
       for (int half = 0; half < DH / 64; ++half) {
         uint4 x[8];
