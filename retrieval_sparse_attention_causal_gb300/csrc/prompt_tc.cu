@@ -24,7 +24,7 @@
 // it (the tensor map fills them in).
 // Measured, bf16, in a graph: one prompt of 32768 tokens, 16 heads of 128 and 4 key heads, 2.5 ms (1.75 PFLOP/s, the
 // tensor pipe), with dh 64 1.61 ms (1.37; exponentials and issue); four documents of 46 thousand tokens in all,
-// 12 heads of 64, 0.70 ms (1.27); 54 thousand tokens, 16 and 4 heads, in a window of 512 183 us; 48 prompts of up
+// 12 heads of 64, 0.70 ms (1.27); 54 thousand tokens, 16 and 4 heads, in a window of 512 181 us; 48 prompts of up
 // to 300 tokens 29 us, three or four work items a CTA of some 5 thousand cycles each: load, masked block, store.
 #include <algorithm>
 #include <type_traits>
