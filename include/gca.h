@@ -490,7 +490,8 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  *           token stride of 0).
  *   offsets [B+1] int32 device, 0 <= offsets[0] <= .. <= offsets[B] <= N; a sequence may be empty.  One
  *           whose offsets are out of order or of range is left out and flagged (GCA_ERR_DEVICE_INDEX);
- *           rows that two others then share get any values.
+ *           others that then share rows get any values (o and lse in the rows that they share, dq, dk and
+ *           dv in all of theirs), those that share none are as ever.
  *   N 0 .. 2^30 rows.   B 1 .. 1024.   H a multiple of Hkv.   dh 32, 64 or 128.   window >= 0.   scale > 0.
  *   o [N][H][dh] contiguous, 16-byte aligned, not an input.   lse [N][H] float32.   Rows of no
  *           sequence are left as they were.

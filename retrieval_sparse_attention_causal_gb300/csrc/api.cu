@@ -816,7 +816,7 @@ extern "C" gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* 
 
 extern "C" size_t gca_prompt_attention_backward_scratch_size(int N, int B, int H, int Hkv, int dh, gca_dtype dtype) {
   if (N < 1 || B < 1 || H < 1 || Hkv < 1 || dh < 1) return 256;
-  return 2 * align256((size_t)prompt_scratch_rows(N, B) * H * sizeof(float)) + align256(prompt_parts_bytes(N, B, Hkv, dh, dtype == GCA_BF16));
+  return 2 * align256((size_t)prompt_scratch_rows(N) * 2 * H * sizeof(float)) + align256(prompt_parts_bytes(N, B, Hkv, dh, dtype == GCA_BF16));
 }
 
 extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gca_heads* k, const gca_heads* v, const void* o,
@@ -849,9 +849,9 @@ extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gc
   a.dq = dq->data; a.dq_ts = dq->token_stride; a.dq_hs = dq->head_stride;
   a.dk = dk->data; a.dk_ts = dk->token_stride; a.dk_hs = dk->head_stride;
   a.dv = dv->data; a.dv_ts = dv->token_stride; a.dv_hs = dv->head_stride;
-  a.np = prompt_scratch_rows(N, B);
+  a.np = prompt_scratch_rows(N);
   a.nlse = static_cast<float*>(scratch);
-  const size_t rows = align256((size_t)a.np * H * sizeof(float));
+  const size_t rows = align256((size_t)a.np * 2 * H * sizeof(float));
   a.nD = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + rows);
   a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + 2 * rows);
   cudaError_t e = launch_prompt_backward(a, reinterpret_cast<cudaStream_t>(stream));

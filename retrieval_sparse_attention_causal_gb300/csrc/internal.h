@@ -247,11 +247,11 @@ struct PromptArgs {
   void* dq; int64_t dq_ts, dq_hs;
   void* dk; int64_t dk_ts, dk_hs;
   void* dv; int64_t dv_ts, dv_hs;
-  float* nlse; float* nD; int64_t np;                      // scratch [H][np]: -lse log2(e), -D
+  float* nlse; float* nD; int64_t np;                      // scratch [2][H][np]: -lse log2(e), -D
   float* parts;                                            // scratch (float32): [parts][2][N][Hkv][dh], of dK and of dV
   ErrWord* err;
 };
-int64_t prompt_scratch_rows(int64_t N, int B);
+int64_t prompt_scratch_rows(int64_t N);
 size_t prompt_parts_bytes(int64_t N, int B, int Hkv, int dh, int bf16);
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_backward(const PromptArgs& a, cudaStream_t s);

@@ -128,7 +128,14 @@ __device__ __forceinline__ bool take_item(PromptItems<I>& r, int n, I& it, const
   return true;
 }
 
-// Where the rows of sequence b begin in the backward pass's scratch rows: on 16-byte boundaries.
-__device__ __forceinline__ int64_t prompt_pad(int off, int b) { return (int64_t)(off & ~3) + 4 * b; }
+// The backward pass's scratch rows, two sums of each row of a head: row off + t of a sequence that starts at `off` is
+// number prompt_sums(a, off, h) + t.  There is a set for sequences that start at even rows and one for odd rows, in
+// which a row has its own number, less one in the odd set.  So rows that differ never share a number, in whatever order
+// the offsets are, and a sequence starts at an even one: what is read two rows at a time is aligned, and a copy of 16-byte
+// units (kSumsOfTile rows for a tile) starts off & 2 rows before it.
+__device__ __forceinline__ int64_t prompt_sums(const PromptArgs& a, int off, int h) {
+  return ((off & 1) * (int64_t)a.H + h) * a.np + (off & ~1);
+}
+constexpr int kSumsOfTile = 128 + 4;
 
 }  // namespace gca

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
 }
 
 // What both sides of the backward pass need of a row, negative as they add it: D = <do, o>, and the
-// log-sum-exp times log2(e); a head's rows side by side, [H][np] each.  A warp takes a token, some of its heads
+// log-sum-exp times log2(e); a head's rows side by side, [2][H][np] each (prompt_sums).  A warp takes a token, some of its heads
 // at a time.  Bound by memory: 54 thousand tokens of 16 heads of 64 44 us (5.1 TB/s; with three heads of a lane on their
 // way 50, with four 53: fewer warps fit).
 template <typename T, int DH>
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
   }
   const T* o = reinterpret_cast<const T*>(a.o) + row * a.H * DH + at * V;
   const T* g = reinterpret_cast<const T*>(a.dout) + row * a.do_ts + at * V;
-  const int64_t to = prompt_pad(off, lo) + row - off;
+  const int64_t to = prompt_sums(a, off, 0) + row - off;
   for (int h = h0; h - h0 < a.H; h += FLY * SIDE) {  // the same for the whole warp: shuffles need every lane
     uint4 x[FLY], y[FLY];
     float l[FLY];
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dq_simt_kernel(PromptArgs a) 
   const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)x.off * a.k_ts + m * a.k_hs;
   const float* v = reinterpret_cast<const float*>(a.v) + (int64_t)x.off * a.v_ts + m * a.v_hs;
   float dq[4][C::CV] = {}, nl[4], nd[4];
-  const int64_t rows = h * a.np + prompt_pad(x.off, x.b) + t0;
+  const int64_t rows = prompt_sums(a, x.off, h) + t0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool on = t0 + ty + 16 * i < x.len;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) prompt_dkv_simt_kernel(PromptArgs a)
   if (w0 < w1) fetch(w0);
   for (int w = w0; w < w1; ++w) {
     const int i = x.tile + w % tiles;
-    const int64_t rows = (m * a.g + w / tiles) * a.np + prompt_pad(x.off, x.b);
+    const int64_t rows = prompt_sums(a, x.off, m * a.g + w / tiles);
     __syncthreads();
     qr.put(Q);
     gr.put(G);
@@ -501,7 +501,7 @@ void rows(const PromptArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int64_t prompt_scratch_rows(int64_t N, int B) { return (N + 4 * (int64_t)B + 128 + 3) / 4 * 4; }
+int64_t prompt_scratch_rows(int64_t N) { return (N + kSumsOfTile + 3) / 4 * 4; }
 size_t prompt_parts_bytes(int64_t N, int B, int Hkv, int dh, int bf16) {
   const int parts = bf16 ? 1 : parts_of(N, B, Hkv);
   return parts == 1 ? 0 : (size_t)parts * 2 * N * Hkv * dh * sizeof(float);

@@ -62,7 +62,7 @@ struct Tc {
   static constexpr int NK = DH == 64 ? 8 : 5;           // queries' side: ring slots, a block of K or of V each
   static constexpr int NS = DH == 64 ? 4 : 2;           // keys' side: stages, a tile of Q and of dO and the rows' two sums
   static constexpr int SMEM_Q = 1024 + NB * 2 * BLOCK + NK * BLOCK;
-  static constexpr int SMEM_KV = 1024 + NB * 2 * BLOCK + NS * (2 * BLOCK + 2 * kT * 4);
+  static constexpr int SMEM_KV = 1024 + NB * 2 * BLOCK + NS * (2 * BLOCK + 2 * kSumsOfTile * 4);
 };
 
 // Shared memory and barriers of a CTA, the same for both passes.
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
       return own + both[0];
     };
     // -lse log2(e) and -D of the item's row; a row that does not exist weighs nothing.
-    auto row_of = [&](const QItem& x) { return x.h * a.np + prompt_pad(x.x.off, x.x.b) + x.x.tile * kT + r; };
+    auto row_of = [&](const QItem& x) { return prompt_sums(a, x.x.off, x.h) + x.x.tile * kT + r; };
     float nl = -CUDART_INF_F, nd = 0.f;
     bool more = take(0);
     after_previous();  // the rows' sums
@@ -528,17 +528,17 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
           const int st = id % NS;
           ok = waited(&sh.empty[st], ((id / NS) & 1) ^ 1, kSiteEmpty, i);
           if (!ok) break;
-          tc::mbar_expect_tx_warp(&sh.full[st], 2 * C::BLOCK + 2 * kT * 4);
+          tc::mbar_expect_tx_warp(&sh.full[st], 2 * C::BLOCK + 2 * kSumsOfTile * 4);
 #pragma unroll
           for (int s = 0; s < SUB; ++s) {
             unsigned char* to = ring + st * 2 * C::BLOCK + s * kTile;
             tc::tma_load_4d_warp(to, &tm.q, 64 * s, a.q_hs ? h : 0, it.x.off + i * kT, 0, &sh.full[st]);
             tc::tma_load_4d_warp(to + C::BLOCK, &tm.g, 64 * s, a.do_hs ? h : 0, it.x.off + i * kT, 0, &sh.full[st]);
           }
-          const int64_t row = h * a.np + prompt_pad(it.x.off, it.x.b) + i * kT;
+          const int64_t row = prompt_sums(a, it.x.off, h) + i * kT - (it.x.off & 2);
           if (lane == 0) {
-            tc::bulk_load(rows + st * 2 * kT, a.nlse + row, kT * 4, &sh.full[st]);
-            tc::bulk_load(rows + st * 2 * kT + kT, a.nD + row, kT * 4, &sh.full[st]);
+            tc::bulk_load(rows + st * 2 * kSumsOfTile, a.nlse + row, kSumsOfTile * 4, &sh.full[st]);
+            tc::bulk_load(rows + (st * 2 + 1) * kSumsOfTile, a.nD + row, kSumsOfTile * 4, &sh.full[st]);
           }
           __syncwarp();
         }
@@ -618,8 +618,8 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
             blank<DH, G>(ring + st * 2 * C::BLOCK + part % 2 * C::BLOCK, grp, 32 * (warp & 3) + lane, it.x.len - i * kT);
             tc::fence_async_smem();
           }
-          const float* nl = rows + st * 2 * kT + 32 * part + two;
-          const float* nd = nl + kT;
+          const float* nl = rows + st * 2 * kSumsOfTile + (it.x.off & 2) + 32 * part + two;
+          const float* nd = nl + kSumsOfTile;
           tc::ld_wait(p[0]);
           tc::ld_wait(p[1]);
           uint32_t x[2][8];

@@ -308,6 +308,36 @@ def test_prompt_gradients_beside_bad_offsets(dtype):
     g.cache_workspace("cuda").check()
 
 
+@flags
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_prompt_gradients_of_sequences_out_of_order(dtype, dh):
+    """Where offsets fall, the sequences on either side of the fall are right if they share no row, although
+    those behind it start before the others: short and long ones, at even and odd rows."""
+    g = _g()
+    N, H = 700, 2
+    q, k, v, do = (torch.randn(N, H, dh, device="cuda").to(TORCH[dtype]) for _ in range(4))
+
+    def step(off):
+        o, lse = torch.zeros_like(q), torch.zeros(N, H, device="cuda")
+        g.prompt_attention(q, k, v, ints(off), out=o, lse=lse)
+        grads = [torch.zeros_like(q) for _ in range(3)]
+        g.prompt_attention_backward(q, k, v, o, do, lse, ints(off), dq=grads[0], dk=grads[1], dv=grads[2])
+        return [o, lse] + grads
+    for off in ([8, 12, 0, 4], [40, 60, 0, 0, 0, 20, 40], [9, 12, 5, 8, 1, 4], [401, 700, 2, 200, 203, 401], [403, 404, 400, 403, 130, 399],
+                [600, 601, 300, 597, 1, 2, 300]):
+        there = [(a, z) for a, z in zip(off, off[1:]) if a < z]
+        for _ in range(2):
+            got = step(off)
+            with pytest.raises(g.GCAError):
+                g.cache_workspace("cuda").check()
+            rest = torch.ones(N, dtype=torch.bool, device="cuda")
+            for a, z in there:
+                rest[a:z] = False
+                assert all(torch.equal(x[a:z], y[a:z]) for x, y in zip(got, step([a, z]))), (off, a, z)
+            assert all((x[rest] == 0).all() for x in got), off
+    g.cache_workspace("cuda").check()
+
+
 def test_prompt_nothing_to_do():
     """No rows at all, and sequences that are all empty."""
     g = _g()
