@@ -493,8 +493,8 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  *           others that then share rows get any values (o and lse in the rows that they share, dq, dk and
  *           dv in all of theirs), those that share none are as ever.
  *   N 0 .. 2^30 rows.   B 1 .. 1024.   H a multiple of Hkv.   dh 32, 64 or 128.   window >= 0.   scale > 0.
- *   o [N][H][dh] contiguous, 16-byte aligned, not an input.   lse [N][H] float32.   Rows of no
- *           sequence are left as they were.
+ *   o [N][H][dh] contiguous, 16-byte aligned.   lse [N][H] float32.   Neither may share a byte with an
+ *           input or the other.  Rows of no sequence are left as they were.
  *   ws      >= gca_forward_workspace_size() bytes (error word only).
  * No sequence sees another: rows of others, and behind the last, may hold anything.  An infinity or
  * NaN of a sequence can reach all its own rows (a weight of 0 times it is NaN).  bf16: as in
@@ -507,8 +507,8 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  * bf16: P and dS are rounded to bf16 for their products, and D, of the rounded o, is corrected by the
  * sums of dS, which ought to be 0.
  *   o, lse  from the forward call.   dout [N][H][dh]: like q.
- *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap,
- *           with each other or with an input either.
+ *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap;
+ *           no byte of one may be another's or an input's (views of one tensor that lie between each other may).
  *   scratch >= gca_prompt_attention_backward_scratch_size() bytes, 256-byte aligned, any contents; one
  *           for each call that can overlap another.
  * ------------------------------------------------------------------------------- */

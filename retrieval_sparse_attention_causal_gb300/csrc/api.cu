@@ -621,6 +621,59 @@ static bool strides_overlap(const gca_heads& t, int64_t B, int64_t L, int64_t H,
   return false;
 }
 
+// Runs of bytes that a tensor has: `run` at p + s[0] i + s[1] j + s[2] k, for i < n[0] and so on.
+struct Runs {
+  const void* p;
+  int64_t run, n[3], s[3];
+};
+static Runs runs_of(const gca_heads& t, int64_t B, int64_t L, int64_t H, int64_t dh, int esize) {
+  return Runs{t.data, dh * esize, {B, L, H}, {t.batch_stride * esize, t.token_stride * esize, t.head_stride * esize}};
+}
+static Runs runs_of(const void* p, int64_t bytes) { return Runs{p, bytes, {1, 1, 1}, {0, 0, 0}}; }
+
+// Whether two tensors share a byte.  Their runs do where the distance of two of them, a sum of multiples of both
+// tensors' strides, lies in (-b.run, a.run).  Looked for from the largest stride down, with the multiples by which
+// the rest can still reach that range: one to three where the strides nest, as those of views of one tensor do.
+// (Strides of two tensors that do not nest could take long: after a million steps they count as sharing.)
+static bool share_bytes(const Runs& a, const Runs& b) {
+  using Wide = __int128;
+  struct Term { Wide s, lo, hi; };  // s x, lo <= x <= hi
+  Term t[6];
+  int m = 0;
+  auto add = [&](Wide s, Wide lo, Wide hi) {
+    if (s == 0 || lo == hi) return;
+    for (int i = 0; i < m; ++i)
+      if (t[i].s == s) {
+        t[i].lo += lo;
+        t[i].hi += hi;
+        return;
+      }
+    t[m++] = Term{s, lo, hi};
+  };
+  for (int i = 0; i < 3; ++i) {
+    add(b.s[i], 0, b.n[i] - 1);
+    add(a.s[i], 1 - a.n[i], 0);
+  }
+  std::sort(t, t + m, [](const Term& x, const Term& y) { return x.s > y.s; });
+  Wide lo[7], hi[7];  // what the terms from i on can add
+  lo[m] = hi[m] = 0;
+  for (int i = m - 1; i >= 0; --i) {
+    lo[i] = lo[i + 1] + t[i].s * t[i].lo;
+    hi[i] = hi[i + 1] + t[i].s * t[i].hi;
+  }
+  auto floored = [](Wide x, Wide y) { return x / y - (x % y < 0); };  // y > 0
+  int steps = 1 << 20;
+  auto reach = [&](auto& self, int i, Wide d) -> bool {
+    if (d + hi[i] <= -b.run || d + lo[i] >= a.run) return false;
+    if (i == m || --steps < 0) return true;
+    const Wide from = -floored(d + hi[i + 1] + b.run - 1, t[i].s), to = floored(a.run - 1 - lo[i + 1] - d, t[i].s);
+    for (Wide x = std::max(from, t[i].lo); x <= std::min(to, t[i].hi); ++x)
+      if (self(self, i + 1, d + x * t[i].s)) return true;
+    return false;
+  };
+  return reach(reach, 0, (Wide)reinterpret_cast<intptr_t>(b.p) - (Wide)reinterpret_cast<intptr_t>(a.p));
+}
+
 // What gca_rotary and gca_norm_rotary ask of their tensors and sizes.
 static gca_status check_turned(const gca_heads* q, const gca_heads* k, const gca_heads* q_out, const gca_heads* k_out,
                                gca_dtype dtype, int B, int L, int H, int Hkv, int dh, int rot, const uint64_t* freq,
@@ -806,8 +859,15 @@ extern "C" gca_status gca_prompt_attention(const gca_heads* q, const gca_heads* 
   if (st != GCA_OK) return st;
   if ((st = check_ws(ws, ws_bytes, kErrBytes)) != GCA_OK) return st;
   if (N == 0) return GCA_OK;
-  for (const gca_heads* in : {q, k, v})
-    if (o == in->data) return fail(GCA_ERR_INVALID_ARG, "o must not be an input");
+  // Rows are written before others are read.
+  const int esize = dtype == GCA_BF16 ? 2 : 4;
+  const Runs out[] = {runs_of(o, (int64_t)N * H * dh * esize), runs_of(lse, (int64_t)N * H * 4)};
+  const Runs in[] = {runs_of(*q, 1, N, H, dh, esize), runs_of(*k, 1, N, Hkv, dh, esize), runs_of(*v, 1, N, Hkv, dh, esize),
+                     runs_of(offsets, ((int64_t)B + 1) * 4)};
+  for (const Runs& x : out)
+    for (const Runs& y : in)
+      if (share_bytes(x, y)) return fail(GCA_ERR_INVALID_ARG, "o and lse must not overlap an input");
+  if (share_bytes(out[0], out[1])) return fail(GCA_ERR_INVALID_ARG, "o and lse overlap");
   const PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
   cudaError_t e = launch_prompt_forward(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gca_prompt_attention launch");
@@ -837,12 +897,14 @@ extern "C" gca_status gca_prompt_attention_backward(const gca_heads* q, const gc
     return fail(GCA_ERR_INVALID_ARG, "output strides make elements overlap");
   if ((st = check_scratch(scratch, scratch_bytes, gca_prompt_attention_backward_scratch_size(N, B, H, Hkv, dh, dtype))) != GCA_OK) return st;
   // Each gradient is written before the last input is read.
-  const void* in[] = {q->data, k->data, v->data, o, dout->data};
-  const void* out[] = {dq->data, dk->data, dv->data};
+  const Runs in[] = {runs_of(*q, 1, N, H, dh, esize), runs_of(*k, 1, N, Hkv, dh, esize), runs_of(*v, 1, N, Hkv, dh, esize),
+                     runs_of(o, (int64_t)N * H * dh * esize), runs_of(*dout, 1, N, H, dh, esize), runs_of(lse, (int64_t)N * H * 4),
+                     runs_of(offsets, ((int64_t)B + 1) * 4)};
+  const Runs out[] = {runs_of(*dq, 1, N, H, dh, esize), runs_of(*dk, 1, N, Hkv, dh, esize), runs_of(*dv, 1, N, Hkv, dh, esize)};
   for (int i = 0; i < 3; ++i) {
-    for (const void* x : in)
-      if (out[i] == x) return fail(GCA_ERR_INVALID_ARG, "a gradient must not be an input");
-    if (out[i] == out[(i + 1) % 3]) return fail(GCA_ERR_INVALID_ARG, "two gradients are one tensor");
+    for (const Runs& x : in)
+      if (share_bytes(out[i], x)) return fail(GCA_ERR_INVALID_ARG, "a gradient must not overlap an input");
+    if (share_bytes(out[i], out[(i + 1) % 3])) return fail(GCA_ERR_INVALID_ARG, "two gradients are one tensor, or overlap");
   }
   PromptArgs a = prompt_args(q, k, v, dtype, N, B, H, Hkv, dh, offsets, window, scale, o, lse, ws);
   a.dout = dout->data; a.do_ts = N > 1 ? dout->token_stride : 0; a.do_hs = H > 1 ? dout->head_stride : 0;

@@ -45,7 +45,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets:
 
     q [N, H, dh], k, v [N, Hkv, dh] (H a multiple of Hkv; views of a fused projection work), offsets
     int32 [B + 1], read on the device.  Returns O like q (contiguous) and LSE float32 [N, H]; rows that
-    no sequence has are not written."""
+    no sequence has are not written.  out= and lse= may share no memory with an input or each other."""
     return EXT.prompt_attention(q, k, v, offsets, window, scale, out, lse, _word(ws))
 
 
@@ -54,9 +54,8 @@ def prompt_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                               dq: torch.Tensor = None, dk: torch.Tensor = None, dv: torch.Tensor = None,
                               ws: Workspace = None):
     """Gradients of prompt_attention() (gca_prompt_attention_backward): o, lse as it returned them, dout
-    [N, H, dh] the gradient of o.  Returns (dq, dk, dv); dq=, dk=, dv= may be views of one tensor, but not
-    of an input.
-    Rows that no sequence has are not written."""
+    [N, H, dh] the gradient of o.  Returns (dq, dk, dv); dq=, dk=, dv= may be views of one tensor, but
+    share no memory with each other or an input.  Rows that no sequence has are not written."""
     return EXT.prompt_attention_backward(q, k, v, o, dout, lse, offsets, window, scale, dq, dk, dv, _word(ws))
 
 

@@ -215,6 +215,45 @@ def test_prompt_views_scale_and_gradients_into_views(dtype):
     assert torch.equal(a, b)
 
 
+def test_prompt_outputs_between_and_over_others():
+    """Outputs in the gaps of a tensor's rows are taken, those that share an element with an input or with another
+    output are refused, and nothing of such a call is written."""
+    g = _g()
+    N, H, Hkv, dh = 70, 4, 2, 64
+    off = ints([0, 30, 70])
+    room = torch.randn(N, H + 2 * Hkv + H + 2 * Hkv, dh, device="cuda").bfloat16()  # inputs and gradients in turn, token by token
+    at = np.cumsum([0, H, Hkv, Hkv, H, Hkv, Hkv])
+    q, k, v, dq, dk, dv = (room[:, a:z] for a, z in zip(at, at[1:]))
+    do = torch.randn(N, H, dh, device="cuda").bfloat16()
+    c = [x.clone() for x in (q, k, v)]
+    o, lse = g.prompt_attention(*c, off)
+    want = g.prompt_attention_backward(*c, o, do, lse, off)
+    got = g.prompt_attention_backward(q, k, v, o, do, lse, off, dq=dq, dk=dk, dv=dv)
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and all(torch.equal(a, b) for a, b in zip(c, (q, k, v)))
+    first = torch.randn(H + 2 * Hkv, N, dh, device="cuda").bfloat16().transpose(0, 1)  # heads first: each tensor a block
+    for x, y in zip((first[:, :H], first[:, H:H + Hkv], first[:, H + Hkv:]), want):
+        x.copy_(y + 1)
+    grads = (first[:, :H], first[:, H:H + Hkv], first[:, H + Hkv:])
+    assert all(torch.equal(a, b) for a, b in zip(want, g.prompt_attention_backward(*c, o, do, lse, off, dq=grads[0], dk=grads[1], dv=grads[2])))
+    line = torch.randn(3 * N * H * dh, device="cuda").bfloat16()
+    piece = lambda e, h=H: line[e:e + N * h * dh].view(N, h, dh)  # noqa: E731
+    n = N * H * dh
+    assert torch.equal(g.prompt_attention(piece(0), *c[1:], off, out=piece(n))[0], g.prompt_attention(piece(0).clone(), *c[1:], off)[0])
+    before = line.clone(), room.clone(), o.clone(), lse.clone()
+    for call in (lambda: g.prompt_attention(piece(0), *c[1:], off, out=piece(64)), lambda: g.prompt_attention(piece(n), *c[1:], off, out=piece(8)),
+                 lambda: g.prompt_attention(c[0], piece(n - 8, Hkv), c[2], off, out=piece(0)),
+                 lambda: g.prompt_attention(*c, off, out=piece(0), lse=line[n - 2:n - 2 + 2 * N * H].view(torch.float32).view(N, H)),
+                 lambda: g.prompt_attention_backward(*c, o, do, lse, off, dq=piece(0), dk=piece(n - 64, Hkv)),
+                 lambda: g.prompt_attention_backward(*c, o, do, lse, off, dq=room[:, :H], dv=room[:, H - 1:H - 1 + Hkv]),
+                 lambda: g.prompt_attention_backward(q, k, v, o, do, lse, off, dk=room[:, 1:1 + Hkv]),
+                 lambda: g.prompt_attention_backward(*c, piece(0), do, lse, off, dv=piece(n - 8, Hkv)),
+                 lambda: g.prompt_attention_backward(*c, o, do, lse, off, dk=do[:, 1:1 + Hkv])):
+        with pytest.raises(g.GCAError) as e:
+            call()
+        assert e.value.status == g.GCA_ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(before, (line, room, o, lse)))
+
+
 def test_prompt_calls_are_equal_and_follow_the_device():
     """Equal calls give equal bits; on another stream too; and a captured pass follows offsets and inputs that
     change behind it."""

@@ -155,6 +155,45 @@ def test_outputs_that_are_inputs_and_bytes_as_a_plain_cache_are_refused(gca):
         gca.PagedCache(pages, pages, torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(5, dtype=torch.int32))
 
 
+def test_outputs_that_overlap_are_refused(gca):
+    """At whatever addresses: shifted, inside, one in rows of the other, interleaved with too little room."""
+    L = gca.LIB
+    n = 100 * 12 * 64  # elements of q
+    at = lambda e, **kw: heads(gca, FAKE + 2 * e, **kw)  # noqa: E731
+    far = 1 << 30
+
+    def forward(q, k, v, o, lse=FAKE + 8 * far, off=FAKE + 10 * far):
+        st = L.gca_prompt_attention(q, k, v, gca.GCA_BF16, 100, 3, 12, 12, 64, off, 0, 0.125, o, lse, FAKE, 256, None)
+        return st, L.gca_last_error_detail()
+    q, k, v = at(0), at(far), at(2 * far)
+    for o in (FAKE + 16, FAKE + 2 * n - 16, FAKE + 2 * far + 2048):
+        assert forward(q, k, v, o) == (gca.GCA_ERR_INVALID_ARG, b"o and lse must not overlap an input"), o
+    wide = at(0, ts=36 * 64)  # the queries of a fused projection: o lies in the first of them, or over several tokens
+    assert forward(wide, k, v, FAKE + 2 * 36 * 64 * 50)[0] == gca.GCA_ERR_INVALID_ARG
+    assert forward(wide, k, v, FAKE + 2 * 12 * 64)[0] == gca.GCA_ERR_INVALID_ARG
+    turned = at(0, ts=64, hs=100 * 64)  # heads first
+    assert forward(turned, k, v, FAKE + 2 * 11 * 100 * 64)[0] == gca.GCA_ERR_INVALID_ARG
+    o = FAKE + 6 * far
+    for kw in (dict(lse=o + 2 * n - 4), dict(lse=FAKE + 4), dict(off=o + 16), dict(off=FAKE + 8 * far + 4)):
+        assert forward(q, k, v, o, **kw)[0] == gca.GCA_ERR_INVALID_ARG, kw
+
+    def backward(dq, dk, dv, q=q, Hkv=12):
+        st = L.gca_prompt_attention_backward(q, k, v, o, at(7 * far), FAKE + 8 * far, gca.GCA_BF16, 100, 3, 12, Hkv, 64, FAKE + 10 * far, 0, 0.125,
+                                             dq, dk, dv, FAKE, 256, FAKE, 1 << 30, None)
+        return st, L.gca_last_error_detail()
+    a, b, c = at(11 * far), at(12 * far), at(13 * far)
+    for x in (at(8), at(far + n - 8), at(2 * far + 64), at(3 * far + 8), at(7 * far - 8 + n), at(4 * far), at(5 * far)):
+        for g in ((x, b, c), (a, x, c), (a, b, x)):
+            assert backward(*g) == (gca.GCA_ERR_INVALID_ARG, b"a gradient must not overlap an input")
+    for g in ((a, at(11 * far + n - 8), c), (a, b, at(11 * far + 8)), (a, b, at(12 * far + 64 * 3))):
+        assert backward(*g)[0] == gca.GCA_ERR_INVALID_ARG and b"two gradients" in L.gca_last_error_detail()
+    # Views of one tensor [N, 12 + 2 + 2, 64]: the values' gradients begin a head, or half a one, too soon.
+    view = lambda h: at(11 * far + h * 64, ts=16 * 64)  # noqa: E731
+    for first in (13, 13.5):
+        assert backward(view(0), view(12), at(11 * far + int(first * 64), ts=16 * 64), Hkv=2)[0] == gca.GCA_ERR_INVALID_ARG
+        assert b"two gradients" in L.gca_last_error_detail()
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_attention_is_softmax_attention():
     """Against torch's own attention in float64 on one dense sequence, and packed sequences against each by itself."""
