@@ -456,11 +456,12 @@ GCA_API gca_status gca_rotary(const gca_heads* q, const gca_heads* k, const gca_
  * rot, interleaved, positions and gain as in gca_rotary: elements rot .. dh-1 are normed, but neither
  * turned nor multiplied by gain.
  *
- *   q, k, q_out, k_out, dtype and sizes: as in gca_rotary; outputs may be the inputs themselves.
+ *   q, k, q_out, k_out, dtype and sizes: as in gca_rotary; q_out may be q itself and k_out k (same
+ *           pointer and strides), but no output may share a byte with an input or an output otherwise.
  *   q_weight, k_weight [dh] float32 device (k_weight may be NULL without k).   eps >= 0, finite.
  *
  * gca_norm_rotary_backward - its gradients.  q, k are its inputs, dq_out, dk_out the gradients of its
- * outputs; written are dq, dk (they may be dq_out, dk_out themselves) and dq_weight, dk_weight [dh]
+ * outputs; written are dq, dk (they may be dq_out, dk_out or q, k themselves) and dq_weight, dk_weight [dh]
  * float32, sums over all tokens and heads.  Deterministic (no atomics).
  *   scratch >= gca_norm_rotary_backward_scratch_size(dh) bytes, 256-byte aligned, any contents; one for
  *           each call that can overlap another.

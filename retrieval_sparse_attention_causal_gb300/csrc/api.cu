@@ -637,6 +637,13 @@ static Runs runs_of(const void* p, int64_t bytes) { return Runs{p, bytes, {1, 1,
 // (Strides of two tensors that do not nest could take long: after a million steps they count as sharing.)
 static bool share_bytes(const Runs& a, const Runs& b) {
   using Wide = __int128;
+  auto span = [](const Runs& x) {
+    Wide n = x.run;
+    for (int i = 0; i < 3; ++i) n += (Wide)x.s[i] * (x.n[i] - 1);
+    return n;
+  };
+  const Wide apart = (Wide)reinterpret_cast<intptr_t>(b.p) - (Wide)reinterpret_cast<intptr_t>(a.p);
+  if (apart >= span(a) || -apart >= span(b)) return false;
   struct Term { Wide s, lo, hi; };  // s x, lo <= x <= hi
   Term t[6];
   int m = 0;
@@ -661,7 +668,10 @@ static bool share_bytes(const Runs& a, const Runs& b) {
     lo[i] = lo[i + 1] + t[i].s * t[i].lo;
     hi[i] = hi[i + 1] + t[i].s * t[i].hi;
   }
-  auto floored = [](Wide x, Wide y) { return x / y - (x % y < 0); };  // y > 0
+  auto floored = [](Wide x, Wide y) -> Wide {  // y > 0
+    if (x == (int64_t)x && y == (int64_t)y) return (int64_t)x / (int64_t)y - ((int64_t)x % (int64_t)y < 0);  // (the wide division is slow)
+    return x / y - (x % y < 0);
+  };
   int steps = 1 << 20;
   auto reach = [&](auto& self, int i, Wide d) -> bool {
     if (d + hi[i] <= -b.run || d + lo[i] >= a.run) return false;
@@ -671,7 +681,7 @@ static bool share_bytes(const Runs& a, const Runs& b) {
       if (self(self, i + 1, d + x * t[i].s)) return true;
     return false;
   };
-  return reach(reach, 0, (Wide)reinterpret_cast<intptr_t>(b.p) - (Wide)reinterpret_cast<intptr_t>(a.p));
+  return reach(reach, 0, apart);
 }
 
 // What gca_rotary and gca_norm_rotary ask of their tensors and sizes.
@@ -736,6 +746,37 @@ gca_status check_weights(const gca_heads* k, float eps, const float* q_weight, c
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GCA_ERR_INVALID_ARG, "eps must be finite and >= 0");
   return GCA_OK;
 }
+// Written tensors share no byte with each other, nor with a read one, but that a lane may write each element where it
+// read it: of the tensors read in `own`, one may be the written one itself (same pointer and strides).
+struct Written {
+  const gca_heads* t;
+  int heads;
+  const gca_heads* own[2];
+};
+gca_status check_written(std::initializer_list<Written> written, std::initializer_list<Runs> read, int B, int L, int dh, int esize) {
+  auto runs = [&](const gca_heads* t, int heads) { return runs_of(*t, B, L, heads, dh, esize); };
+  auto itself = [&](const gca_heads* a, const gca_heads* b, int heads) {
+    return a->data == b->data && (B == 1 || a->batch_stride == b->batch_stride) && (L == 1 || a->token_stride == b->token_stride) &&
+           (heads == 1 || a->head_stride == b->head_stride);
+  };
+  for (const Written& x : written) {
+    if (!x.t) continue;
+    const Runs out = runs(x.t, x.heads);
+    for (const Runs& y : read)
+      if (y.p && share_bytes(out, y)) return fail(GCA_ERR_INVALID_ARG, "an output must not overlap an input");
+    for (const Written& y : written) {
+      if (!y.t) continue;
+      if (&y != &x && share_bytes(out, runs(y.t, y.heads))) return fail(GCA_ERR_INVALID_ARG, "two outputs overlap");
+      for (const gca_heads* in : y.own)
+        if (in && !(&y == &x && itself(x.t, in, x.heads)) && share_bytes(out, runs(in, y.heads)))
+          return fail(GCA_ERR_INVALID_ARG, "an output must be its input itself or not overlap it");
+    }
+  }
+  return GCA_OK;
+}
+Runs runs_of_positions(const int32_t* positions, int B, int L, int64_t batch_stride) {
+  return Runs{positions, (int64_t)L * 4, {B, 1, 1}, {batch_stride * 4, 0, 0}};
+}
 NormSide norm_side(const gca_heads* in, const gca_heads* dy, const gca_heads* out) {
   NormSide x{};
   x.in = in->data; x.in_bs = in->batch_stride; x.in_ts = in->token_stride; x.in_hs = in->head_stride;
@@ -753,6 +794,10 @@ extern "C" gca_status gca_norm_rotary(const gca_heads* q, const gca_heads* k, co
   gca_status st = check_turned(q, k, q_out, k_out, dtype, B, L, H, Hkv, dh, rot, freq, position_batch_stride);
   if (st != GCA_OK) return st;
   if ((st = check_weights(k, eps, q_weight, k_weight)) != GCA_OK) return st;
+  st = check_written({{q_out, H, {q, nullptr}}, {k_out, Hkv, {k, nullptr}}},
+                     {runs_of(q_weight, dh * 4), runs_of(k_weight, dh * 4), runs_of(freq, rot * 4), runs_of_positions(positions, B, L, position_batch_stride)},
+                     B, L, dh, dtype == GCA_BF16 ? 2 : 4);
+  if (st != GCA_OK) return st;
   NormRotaryArgs a{};
   a.q = norm_side(q, nullptr, q_out);
   if (k) a.k = norm_side(k, nullptr, k_out);
@@ -790,6 +835,13 @@ extern "C" gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_hea
   for (const float* w : {dq_weight, dk_weight})
     if (reinterpret_cast<uintptr_t>(w) & 3) return fail(GCA_ERR_INVALID_ARG, "weights' gradients must be 4-byte aligned");
   if ((st = check_scratch(scratch, scratch_bytes, gca_norm_rotary_backward_scratch_size(dh))) != GCA_OK) return st;
+  st = check_written({{dq, H, {q, dq_out}}, {dk, Hkv, {k, dk_out}}},
+                     {runs_of(q_weight, dh * 4), runs_of(k_weight, dh * 4), runs_of(freq, rot * 4), runs_of_positions(positions, B, L, position_batch_stride),
+                      runs_of(dq_weight, dh * 4), runs_of(dk_weight, dh * 4)},
+                     B, L, dh, dtype == GCA_BF16 ? 2 : 4);
+  if (st != GCA_OK) return st;
+  if (dk_weight && share_bytes(runs_of(dq_weight, dh * 4), runs_of(dk_weight, dh * 4)))
+    return fail(GCA_ERR_INVALID_ARG, "the weights' gradients overlap");
   NormRotaryArgs a{};
   a.q = norm_side(q, dq_out, dq);
   if (k) a.k = norm_side(k, dk_out, dk);

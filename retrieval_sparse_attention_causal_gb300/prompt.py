@@ -23,8 +23,8 @@ def norm_rotary(q: torch.Tensor, k, q_weight: torch.Tensor, k_weight, freq: torc
 
     q [B, L, H, dh], k [B, L, Hkv, dh] or None, with any strides but the last; q_weight, k_weight
     float32 [dh]; freq, positions, interleaved and gain as in rotary().  Pass q_out=q, k_out=k to
-    work in place (not where the gradients are needed: they take q and k as they were).  Returns
-    (q_out, k_out)."""
+    work in place (not where the gradients are needed: they take q and k as they were); outputs
+    share no memory with inputs or each other otherwise.  Returns (q_out, k_out)."""
     return EXT.norm_rotary(q, k, q_weight, k_weight, freq, positions, interleaved, gain, eps, q_out, k_out)
 
 

@@ -509,6 +509,37 @@ def test_norm_rotary_views_and_in_place(dtype, offset):
     assert torch.equal(raw[:offset], before[:offset]) and torch.equal(raw[offset + B * L * n:], before[offset + B * L * n:])
 
 
+def test_norm_rotary_outputs_between_and_over_others():
+    """Outputs in the gaps of the inputs' rows and in place of the inputs (in the backward pass of either) are taken; each
+    other's places, and shifted ones, are refused, and nothing is written."""
+    g = _g()
+    B, L, H, dh = 2, 9, 3, 64
+    wt, freq = [torch.rand(dh, device="cuda") for _ in range(2)], g.rotary_frequencies(dh)
+    room = torch.randn(B, L, 4 * H, dh, device="cuda").bfloat16()
+    q, k, qo, ko = (room[:, :, i * H:(i + 1) * H] for i in range(4))
+    c, dy = [q.clone(), k.clone()], [torch.randn(B, L, H, dh, device="cuda").bfloat16() for _ in range(2)]
+    want, back = g.norm_rotary(*c, *wt, freq), g.norm_rotary_backward(*c, *dy, *wt, freq)
+    assert all(torch.equal(a, b) for a, b in zip(want, g.norm_rotary(q, k, *wt, freq, q_out=qo, k_out=ko)))
+    assert all(torch.equal(a, b) for a, b in zip(back, g.norm_rotary_backward(q, k, *dy, *wt, freq, dq=qo, dk=ko)))
+    assert all(torch.equal(a, b) for a, b in zip(c, (q, k)))
+    for i in range(2):  # in place of q and k, or of the gradients
+        own = [x.clone() for x in c + dy]
+        assert all(torch.equal(a, b) for a, b in zip(back, g.norm_rotary_backward(*own, *wt, freq, dq=own[2 * i], dk=own[2 * i + 1])))
+    line = torch.randn(3 * B * L * H * dh, device="cuda").bfloat16()
+    piece = lambda e: line[e:e + B * L * H * dh].view(B, L, H, dh)  # noqa: E731
+    before = line.clone(), room.clone()
+    for call in (lambda: g.norm_rotary(q, k, *wt, freq, q_out=k, k_out=q), lambda: g.norm_rotary(q, k, *wt, freq, k_out=q),
+                 lambda: g.norm_rotary(piece(0), k, *wt, freq, q_out=piece(64)), lambda: g.norm_rotary(piece(64), None, wt[0], None, freq, q_out=piece(0)),
+                 lambda: g.norm_rotary(q, k, *wt, freq, q_out=piece(0), k_out=piece(64)),
+                 lambda: g.norm_rotary(q, k, *wt, freq, q_out=room[:, :, 1:1 + H]),
+                 lambda: g.norm_rotary_backward(q, k, *dy, *wt, freq, dq=dy[1]), lambda: g.norm_rotary_backward(q, k, *dy, *wt, freq, dk=q),
+                 lambda: g.norm_rotary_backward(q, k, piece(0), dy[1], *wt, freq, dq=piece(8))):
+        with pytest.raises(g.GCAError) as e:
+            call()
+        assert e.value.status == g.GCA_ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(before, (line, room)))
+
+
 def test_norm_rotary_zero_rows():
     """A row of zeros: eps keeps it finite, and its gradient too."""
     g = _g()

@@ -194,6 +194,35 @@ def test_outputs_that_overlap_are_refused(gca):
         assert b"two gradients" in L.gca_last_error_detail()
 
 
+def test_norm_outputs_that_overlap_are_refused(gca):
+    """Shifted, in another order, inside the other side's, or the other side's itself; each output."""
+    L, far = gca.LIB, 1 << 30
+    at = lambda e, **kw: heads(gca, FAKE + 2 * e, **kw)  # noqa: E731
+    n = 2 * 64 * 12 * 64
+    w = FAKE + 40 * far
+
+    def forward(q, k, qo, ko, pos=None):
+        st = L.gca_norm_rotary(q, k, qo, ko, gca.GCA_BF16, 2, 64, 12, 12, 64, 64, 0, 1e-6, w, w + 4096, w + 8192, pos, 64, 1.0, None)
+        return st, L.gca_last_error_detail()
+    q, k, a, b = at(0), at(far), at(2 * far), at(3 * far)
+    for qo, ko, what in ((at(64), b, b"itself"), (a, at(far + n - 64), b"itself"), (k, b, b"itself"), (a, q, b"itself"), (k, q, b"itself"),
+                         (a, at(2 * far + n - 64), b"two outputs"), (at(0, ts=64, hs=64 * 64), b, b"itself")):
+        st, detail = forward(q, k, qo, ko)
+        assert st == gca.GCA_ERR_INVALID_ARG and what in detail
+    assert forward(q, k, at(20 * far), b)[1] == b"an output must not overlap an input"  # the weights
+    assert forward(q, k, a, b, pos=FAKE + 4 * far)[0] == gca.GCA_ERR_INVALID_ARG
+
+    def backward(dq, dk, dqw=w + 16384, dkw=w + 20480):
+        size = L.gca_norm_rotary_backward_scratch_size(64)
+        st = L.gca_norm_rotary_backward(q, k, at(4 * far), at(5 * far), dq, dk, gca.GCA_BF16, 2, 64, 12, 12, 64, 64, 0, 1e-6, w, w + 4096, w + 8192,
+                                        None, 0, 1.0, dqw, dkw, FAKE + 60 * far, size, None)
+        return st, L.gca_last_error_detail()
+    for x in ((at(4 * far + 64), b), (at(5 * far), b), (k, b), (a, q), (a, at(4 * far)), (a, at(5 * far + 8)), (a, at(2 * far + 64)), (at(64), b)):
+        assert backward(*x)[0] == gca.GCA_ERR_INVALID_ARG
+    for kw in (dict(dqw=FAKE + 4 * far + 4), dict(dkw=w + 16384 + 252)):
+        assert backward(a, b, **kw)[0] == gca.GCA_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_attention_is_softmax_attention():
     """Against torch's own attention in float64 on one dense sequence, and packed sequences against each by itself."""
