@@ -505,8 +505,10 @@ GCA_API gca_status gca_norm_rotary_backward(const gca_heads* q, const gca_heads*
  * gca_prompt_attention_backward - its gradients:
  *     D = <dout, o>,  dS = P (<dout, v> - D) scale,  dq = sum dS k,  dk = sum dS q,  dv = sum P dout
  * with P from lse; dk, dv sum over the query heads that share a key head.  Deterministic (no atomics).
- * bf16: P and dS are rounded to bf16 for their products, and D, of the rounded o, is corrected by the
- * sums of dS, which ought to be 0.
+ * bf16: P and dS are rounded to bf16 for their products.  D, of the rounded o, is corrected by the sums
+ * of dS, which ought to be 0, for dk everywhere and for dq in a sequence's first 128 rows; under a window
+ * of 16 or less it is summed from the keys, for both.  (In wider windows dq of later rows is off by 2.5e-3 of its size
+ * at most, elsewhere dq and dk by 2.4e-3: normal inputs.)
  *   o, lse  from the forward call.   dout [N][H][dh]: like q.
  *   dq [N][H][dh], dk, dv [N][Hkv][dh]: written, strides like q's but none may make elements overlap;
  *           no byte of one may be another's or an input's (views of one tensor that lie between each other may).

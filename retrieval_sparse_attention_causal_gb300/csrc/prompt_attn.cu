@@ -225,6 +225,30 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
   }
 }
 
+// The first row of a row's sequence; false where it has none.  By a whole warp.
+__device__ __forceinline__ bool sequence_of(const PromptArgs& a, int64_t row, int& off) {
+  // The last that starts at the row or before (empty ones behind it start there too).
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.offsets[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  off = a.offsets[lo];
+  if (row < off || row - off >= prompt_length(a, lo)) {
+    // A row of no sequence; or offsets are out of order, and one that the search passed over has it.
+    lo = a.B;
+    for (int x = threadIdx.x & 31; x < a.B && lo == a.B; x += 32) {
+      const int s = a.offsets[x], n = prompt_length(a, x);
+      if (row >= s && row - s < n) lo = x;
+    }
+    lo = (int)__reduce_min_sync(0xffffffffu, (unsigned)lo);
+    if (lo == a.B) return false;
+    off = a.offsets[lo];
+  }
+  return true;
+}
+
 // What both sides of the backward pass need of a row, negative as they add it: D = <do, o>, and the
 // log-sum-exp times log2(e); a head's rows side by side, [2][H][np] each (prompt_sums).  A warp takes a token, some of its heads
 // at a time.  Bound by memory: 54 thousand tokens of 16 heads of 64 44 us (5.1 TB/s; with three heads of a lane on their
@@ -236,25 +260,8 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
   const int lane = threadIdx.x & 31, at = lane % LANES, h0 = lane / LANES;
   const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   if (row >= a.N) return;
-  // The sequence of the row: the last that starts at it or before (empty ones behind it start there too).
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.offsets[mid] <= row) lo = mid;
-    else hi = mid;
-  }
-  int off = a.offsets[lo];
-  if (row < off || row - off >= prompt_length(a, lo)) {
-    // A row of no sequence; or offsets are out of order, and one that the search passed over has it.
-    lo = a.B;
-    for (int b = lane; b < a.B && lo == a.B; b += 32) {
-      const int s = a.offsets[b], n = prompt_length(a, b);
-      if (row >= s && row - s < n) lo = b;
-    }
-    lo = (int)__reduce_min_sync(0xffffffffu, (unsigned)lo);
-    if (lo == a.B) return;
-    off = a.offsets[lo];
-  }
+  int off;
+  if (!sequence_of(a, row, off)) return;
   const T* o = reinterpret_cast<const T*>(a.o) + row * a.H * DH + at * V;
   const T* g = reinterpret_cast<const T*>(a.dout) + row * a.do_ts + at * V;
   const int64_t to = prompt_sums(a, off, 0) + row - off;
@@ -285,6 +292,83 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(PromptArgs a) {
         a.nD[head * a.np + to] = -d;
         a.nlse[head * a.np + to] = -l[f] * kLog2e;
       }
+    }
+  }
+}
+
+// The same in bf16 where a window leaves a row few keys.  There D from the rounded output is off by as much as dS's own
+// rounding, so it is made anew: the sum of P <do, v> over the row's keys, P from the log-sum-exp, in float32.  A warp takes a
+// token, DH / 8 lanes a head.  (In a sequence's first 128 rows the queries' side finds D's error by itself, from dS of their
+// one block; everywhere it does so for the keys' side.)
+// Off by, dQ of rows behind the first 128, before and with this: a window of 2 3.7e-3 and 2.34e-3, of 4 3.0 and 2.34, of 8
+// 2.7 and 2.35, of 16 2.54 and 2.36; of 24 2.49 without, of 64 2.43.  Bound by issue: all gradients of 46 thousand tokens of 12
+// heads of 64 take 320 us by the rounded output, with this 349 in a window of 2, 400 of 8, 477 of 16; so wider ones go
+// without.  (With four keys on their way, three CTAs an SM, 364, 407 and 482; with one 354, 410 and 494.)
+constexpr int kFewKeys = 16;
+template <int DH>
+__global__ void __launch_bounds__(256, 4) prompt_few_rows_kernel(PromptArgs a) {
+  let_next();
+  using T = __nv_bfloat16;
+  constexpr int V = 8, LANES = DH / V, SIDE = 32 / LANES, FLY = 2;  // keys on their way
+  const int at = threadIdx.x % LANES, h0 = (threadIdx.x & 31) / LANES;
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  if (row >= a.N) return;
+  int off;
+  if (!sequence_of(a, row, off)) return;
+  const int keys = (int)min(row - off + 1, (int64_t)a.window);
+  const int64_t first = row - keys + 1, to = prompt_sums(a, off, 0) + row - off;
+  const float sl2 = a.scale * kLog2e;
+  auto pairs = [](const uint4& u, uint64_t (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = tc::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  };
+  auto product = [&](const uint64_t (&x)[4], const uint4& u) {
+    uint64_t y[4];
+    pairs(u, y);
+    uint64_t s = tc::mul2(x[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = tc::fma2(x[i], y[i], s);
+    float lo, hi;
+    tc::uf2(s, lo, hi);
+    return lo + hi;
+  };
+  for (int h = h0; h - h0 < a.H; h += SIDE) {  // the same for the whole warp: shuffles need every lane
+    const bool on = h < a.H;
+    const int head = on ? h : 0;
+    const T* k = reinterpret_cast<const T*>(a.k) + first * a.k_ts + head / a.g * a.k_hs + at * V;
+    const T* v = reinterpret_cast<const T*>(a.v) + first * a.v_ts + head / a.g * a.v_hs + at * V;
+    uint4 x[FLY], y[FLY];
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) {
+        const int n = min(j + f, keys - 1);
+        x[f] = *reinterpret_cast<const uint4*>(k + n * a.k_ts);
+        y[f] = *reinterpret_cast<const uint4*>(v + n * a.v_ts);
+      }
+    };
+    fetch(0);
+    uint64_t q[4], g[4];
+    pairs(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + row * a.q_ts + head * a.q_hs + at * V), q);
+    pairs(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.dout) + row * a.do_ts + head * a.do_hs + at * V), g);
+    const float nl = -a.lse[row * a.H + head] * kLog2e;
+    float d = 0.f;
+    for (int j = 0; j < keys; j += FLY) {
+      if (j) fetch(j);
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) {
+        if (j + f >= keys) break;  // (the same for the whole warp)
+        float s = product(q, x[f]);
+#pragma unroll
+        for (int m = LANES / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        d += tc::ex2(s * sl2 + nl) * product(g, y[f]);  // (a lane's share of <do, v>)
+      }
+    }
+#pragma unroll
+    for (int m = LANES / 2; m >= 1; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+    if (at == 0 && on) {
+      a.nD[head * a.np + to] = -d;
+      a.nlse[head * a.np + to] = nl;
     }
   }
 }
@@ -494,6 +578,12 @@ cudaError_t backward_simt(const PromptArgs& a, cudaStream_t s) {
 template <typename T>
 void rows(const PromptArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)((a.N + 7) / 8);
+  if (a.bf16 && a.window > 0 && a.window <= kFewKeys) {
+    if (a.dh == 32) prompt_few_rows_kernel<32><<<grid, 256, 0, s>>>(a);
+    else if (a.dh == 64) prompt_few_rows_kernel<64><<<grid, 256, 0, s>>>(a);
+    else prompt_few_rows_kernel<128><<<grid, 256, 0, s>>>(a);
+    return;
+  }
   if (a.dh == 32) prompt_rows_kernel<T, 32><<<grid, 256, 0, s>>>(a);
   else if (a.dh == 64) prompt_rows_kernel<T, 64><<<grid, 256, 0, s>>>(a);
   else prompt_rows_kernel<T, 128><<<grid, 256, 0, s>>>(a);

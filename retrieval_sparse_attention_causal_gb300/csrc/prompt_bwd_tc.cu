@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
         // One block alone, so rows that see few keys: what the rounding of o puts into D is largest there.  dS is summed
         // once beforehand, for a D that is right when it is rounded.  (Without that dQ of sequences of two tokens is off
         // by 4.0e-3 of its size, of 17 by 2.9e-3, now by 2.4e-3; of single tokens, whose gradient is 0, it is 0.  It
-        // costs short prompts' gradients some 5 us of 73.)
+        // costs short prompts' gradients some 5 us of 73.  Later rows see few keys only in small windows, where D comes
+        // right: prompt_few_rows_kernel.)
         ok = waited(&sh.s[0], id & 1, kSiteS, nt) && waited(&sh.dp[id & 1], (id >> 1) & 1, kSiteDp, nt);
         if (!ok) break;
         tc::fence_after();

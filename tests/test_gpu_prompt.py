@@ -377,6 +377,48 @@ def test_prompt_gradients_of_sequences_out_of_order(dtype, dh):
     g.cache_workspace("cuda").check()
 
 
+@pytest.mark.parametrize("lengths,window,H,Hkv,dh", [
+    ((2,) * 200, 0, 4, 4, 64), ((3, 5) * 60, 0, 4, 2, 64), ((17,) * 40, 0, 6, 2, 128), ((40, 90), 0, 8, 8, 32),
+    ((700,), 2, 4, 4, 64), ((520, 300), 3, 6, 2, 128), ((700,), 4, 4, 1, 64), ((900,), 8, 4, 4, 64), ((640, 260), 16, 8, 2, 32)])
+def test_prompt_gradients_of_rows_that_see_few_keys(lengths, window, H, Hkv, dh):
+    """dS is rounded for its products and dq, dk as outputs, which leaves a relative error e; D from the rounded output
+    instead of the right one makes it r (2.5 and 4.0e-3 with two keys, 2.36 and 2.50e-3 with sixteen).  Both by the formula
+    in float64 with these roundings, on the same inputs; what the kernels add in float32 is 1e-5 of them, so they
+    lie nearer to e than to r, over all rows and over those behind the first 128 of a sequence."""
+    g = _g()
+    off = offsets_of(lengths)
+    N, rep, scale = int(off[-1]), H // Hkv, dh ** -0.5
+    x = [dev(synth.normal(27, s, (N, h, dh), 1.0, "bf16"), "bf16") for s, h in ((0, H), (1, Hkv), (2, Hkv), (3, H))]
+    o, lse = g.prompt_attention(*x[:3], ints(off), window=window)
+    dq, dk, _ = g.prompt_attention_backward(*x[:3], o, x[3], lse, ints(off), window=window)
+    b16 = lambda t: t.bfloat16().double()  # noqa: E731
+    fold = lambda t, n: t.view(Hkv, rep, n, dh).sum(1)  # noqa: E731
+    found = {}  # what: [got, right, raw], each with squares of (error, reference)
+    for a, z in zip(off, off[1:]):
+        n = int(z - a)
+        q, k, v, do = (t[a:z].double().cpu().transpose(0, 1) for t in x)
+        k, v = k.repeat_interleave(rep, 0), v.repeat_interleave(rep, 0)
+        t = torch.arange(n)
+        see = (t[None] <= t[:, None]) & ((t[None] > t[:, None] - window) if window else True)
+        p = torch.softmax((q @ k.transpose(1, 2) * scale).masked_fill(~see, -float("inf")), 2)
+        out, dp = p @ v, do @ v.transpose(1, 2)
+        D = [(do * y).sum(2, keepdim=True) for y in (out, b16(out))]
+        dS = [p * (dp - d) * scale for d in D]
+        want = dS[0] @ k, fold(dS[0].transpose(1, 2) @ q, n)
+        sides = [[(s[a:z].double().cpu().transpose(0, 1)) for s in (dq, dk)]]
+        sides += [[b16(b16(s) @ k), b16(fold(b16(s).transpose(1, 2) @ q, n))] for s in dS]
+        for name, i, first in (("dq", 0, 0), ("dk", 1, 0), ("dq behind", 0, 128), ("dk behind", 1, 128)):
+            if n <= first:
+                continue
+            sums = found.setdefault(name, [[0.0, 0.0] for _ in range(3)])
+            for s, side in zip(sums, sides):
+                s[0] += float(((side[i] - want[i])[:, first:] ** 2).sum())
+                s[1] += float((want[i][:, first:] ** 2).sum())
+    for name, sums in found.items():
+        got, right, raw = ((s / t) ** 0.5 for s, t in sums)
+        assert got <= (right + raw) / 2, f"{name}: {got:.3e}, {right:.3e} with the right D, {raw:.3e} with the rounded output's"
+
+
 def test_prompt_nothing_to_do():
     """No rows at all, and sequences that are all empty."""
     g = _g()
