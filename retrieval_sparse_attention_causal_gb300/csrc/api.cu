@@ -988,7 +988,8 @@ gca_status check_cache(const gca_cache* c, bool need_refs, bool any = false) {
   if (!c->k_pages || !c->v_pages || !c->table || !c->lengths || (need_refs && !c->refs))
     return fail(GCA_ERR_INVALID_ARG, "a cache pointer is NULL");
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return fail(GCA_ERR_INVALID_ARG, "pages must be 16-byte aligned");
-  if (c->heads < 1 || c->heads > 65535 || c->dh < 1 || c->dh > 65535 || c->pages < 1 || c->slots < 1 || c->width < 1)
+  // (The page operations may be given a quantised row as one head of what is left beside its exponents.)
+  if (c->heads < 1 || c->heads > 65535 || c->dh < 1 || (c->dh > 65535 && c->dtype != GCA_E4M3) || c->pages < 1 || c->slots < 1 || c->width < 1)
     return fail(GCA_ERR_INVALID_ARG, "heads, dh, pages, slots and width must be >= 1 (heads, dh <= 65535)");
   if ((int64_t)c->width * 64 > INT32_MAX) return fail(GCA_ERR_INVALID_ARG, "table too wide: 64 * width must be below 2^31");
   if (row_bytes(c->dtype, c->heads, c->dh) % 16)

@@ -760,6 +760,25 @@ def test_quantised_page_operations():
     cache.check()
 
 
+def test_quantised_page_operations_on_wide_rows():
+    """Rows of more than 65536 bytes: appended, forked, trimmed, compacted, looked up and read like others."""
+    g = _g()
+    heads, dh = 520, 128
+    cache = g.QuantisedCache.empty(8, 3, 3, heads, dh)
+    x = torch.randn(2, 70, heads, dh, device="cuda").bfloat16()
+    cache.append(x, -x, ints([70, 64]))
+    want = cache.read(ints([[0, 1]]))
+    cache.fork(ints([0]), ints([2]))
+    cache.append(x[:1, :3], x[:1, :3], ints([3]), slots=ints([2]))
+    cache.trim(end=ints([70, 0, 73]))
+    assert int(cache.compact()[0]) == 3 and cache.lengths.tolist() == [70, 0, 73]
+    assert cache.lookup(ints([[0, 1, 2]])).flatten().tolist() == cache.table[0].tolist()
+    assert all(torch.equal(a, b) for a, b in zip(want, cache.read(ints([[0, 1]]))))
+    tail = cache.read(ints([[1]]), slots=ints([2]))[0][0]
+    assert torch.equal(tail[:6], want[0][0, 64:70]) and torch.equal(tail[6:9], want[0][0, :3])
+    cache.check()
+
+
 @pytest.mark.parametrize("H,Hkv,dh,window", [(12, 12, 64, 0), (10, 2, 128, 0), (24, 4, 64, 300), (12, 4, 32, 0), (8, 8, 128, 700)])
 def test_prompt_many_tiles_a_cta(H, Hkv, dh, window):
     """Long sequences whose last tile has no neighbour among others that have, several work items a CTA: against

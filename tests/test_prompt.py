@@ -119,6 +119,16 @@ def test_quantised_cache_refusals(gca):
     assert L.gca_cache_fork(pool(dtype=3), 1, FAKE, FAKE, FAKE, 256, None) == gca.GCA_ERR_INVALID_ARG
 
 
+def test_quantised_rows_of_any_width_have_page_operations(gca):
+    """A row as one head of what is left beside its exponents, as the Python cache gives it: not refused for its width."""
+    row = gca.LIB.gca_cache_row_bytes(gca.GCA_E4M3, 520, 128)
+    pool = ctypes.byref(gca.Cache(k_pages=FAKE, v_pages=FAKE, dtype=gca.GCA_E4M3, heads=1, dh=row - 16, pages=100, table=FAKE, slots=8, width=10,
+                                  lengths=FAKE, refs=FAKE))
+    assert row == 520 * 128 + 528 and gca.LIB.gca_cache_row_bytes(gca.GCA_E4M3, 1, row - 16) == row
+    assert gca.LIB.gca_cache_fork(pool, 0, FAKE, FAKE, FAKE, 256, None) == gca.GCA_ERR_INVALID_ARG
+    assert b"n must be in" in gca.LIB.gca_last_error_detail()  # what is refused is the call without an entry
+
+
 def test_python_refusals(gca):
     """Tensors that a call cannot take are refused before a device is looked for."""
     x = torch.zeros(10, 4, 64, dtype=torch.bfloat16)
