@@ -23,37 +23,63 @@ __device__ __forceinline__ int prompt_length(const PromptArgs& a, int b) {
   return e - s;
 }
 
-// Tiles of T rows of the sequences, for many lookups: the first kKeep in shared memory, a lane's own of the
-// first 32 in a register.  All threads of the CTA make it, with a barrier between `fill` and the first use.
+// Tiles of T rows of the sequences, for many lookups by a warp: lane l has those of sequences l, l + 32 and so on in
+// registers.  (Read anew from the offsets for each work item, beyond the first 256 sequences, they took time that grew with
+// the square of the sequences: 1024 prompts of 64 tokens, 12 heads, forward 864 us and gradients 2020, now 192 and 672; 256 67
+// and 197, now 56 and 185.)  It is made before the CTA's first barrier, beside what the other warps prepare: a
+// prompt's gradients take 2 us longer otherwise.
 template <int T>
 struct PromptTiles {
-  static constexpr int kKeep = 256;
-  const int* kept;
-  int mine;
-  static __device__ __forceinline__ int of(const PromptArgs& a, int b) { return b < a.B ? (prompt_length(a, b) + T - 1) / T : 0; }
-  static __device__ __forceinline__ void fill(const PromptArgs& a, int* keep) {
-    for (int b = threadIdx.x; b < kKeep; b += blockDim.x) keep[b] = of(a, b);
+  static constexpr int kEach = GCA_MAX_SEQUENCES / 32;
+  int n[kEach];
+  __device__ __forceinline__ PromptTiles() {}  // (of the warps that find no items)
+  __device__ __forceinline__ explicit PromptTiles(const PromptArgs& a) {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) n[j] = 0;
+    any(a, [&](int j) {
+      const int b = 32 * j + (threadIdx.x & 31);
+      if (b < a.B) n[j] = (prompt_length(a, b) + T - 1) / T;
+      return false;
+    });
   }
-  __device__ __forceinline__ PromptTiles(const int* keep) : kept(keep), mine(keep[threadIdx.x & 31]) {}
-  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return b < kKeep ? kept[b] : of(a, b); }
+  // Whether f(j) holds for one of the n's that hold sequences, asked in order up to the first; few sequences ask few.
+  template <typename F>
+  static __device__ __forceinline__ bool any(const PromptArgs& a, const F& f) {
+    if (f(0)) return true;
+    if (a.B <= 32) return false;
+#pragma unroll
+    for (int j = 1; j < 4; ++j)
+      if (f(j)) return true;
+    if (a.B <= 128) return false;
+#pragma unroll
+    for (int j = 4; j < kEach; ++j)
+      if (f(j)) return true;
+    return false;
+  }
 };
 
 // Tile number `rank` of the call: tiles of T rows in the order of their work, the most first, so that
 // those that start last are short.  Under the causal mask that is the order of their number in their
 // sequence, from the highest down (`back`: counted from the sequence's end, for the side of the keys),
 // sequences of equal tiles in order.  With S(i) the tiles numbered i or higher, tile `rank` has the number
-// i with S(i + 1) <= rank < S(i).  Called by a whole warp; false behind the last tile.
-template <typename Tiles>
-__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const Tiles& tiles, int rank, bool back, PromptTile& x) {
+// i with S(i + 1) <= rank < S(i).  `of` says how many of a sequence's tiles count.  Called by a whole warp; false
+// behind the last tile.
+template <int T, typename Of>
+__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const PromptTiles<T>& tiles, const Of& of, int rank, bool back, PromptTile& x) {
   const int lane = threadIdx.x & 31;
-  const int mine = tiles.mine;  // the first 32 sequences stay in registers
   auto from = [&](int i) {
-    int n = max(mine - i, 0);
-    for (int b = lane + 32; b < a.B; b += 32) n += max(tiles(a, b) - i, 0);
+    int n = 0;
+    tiles.any(a, [&](int j) {
+      n += max(of(tiles.n[j]) - i, 0);
+      return false;
+    });
     return (int)__reduce_add_sync(0xffffffffu, n);
   };
-  int most = mine;
-  for (int b = lane + 32; b < a.B; b += 32) most = max(most, tiles(a, b));
+  int most = 0;
+  tiles.any(a, [&](int j) {
+    most = max(most, of(tiles.n[j]));
+    return false;
+  });
   int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, most), below = 0;  // from(lo) > rank >= from(hi) = below
   if (from(0) <= rank) return false;
   while (hi - lo > 1) {
@@ -66,24 +92,27 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const Tiles& ti
     }
   }
   int left = rank - below;  // of the sequences with more than `lo` tiles, in order
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 ? (b0 + lane < a.B ? tiles(a, b0 + lane) : 0) : mine;
-    const uint32_t those = __ballot_sync(0xffffffffu, n > lo);
-    if (left < __popc(those)) {
-      // The lane of the bit that `left` others lie below.
-      const bool it = n > lo && __popc(those & ((1u << lane) - 1)) == left;
-      const int at = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
-      if (at < 0) return false;  // (offsets out of order can make more tiles than an int counts)
-      x.b = b0 + at;
-      x.tile = back ? __shfl_sync(0xffffffffu, n, at) - 1 - lo : lo;
-      x.off = a.offsets[x.b];
-      x.len = a.offsets[x.b + 1] - x.off;
-      return true;
-    }
+  int first = 0, count = 0;
+  uint32_t those = 0;
+  const bool found = tiles.any(a, [&](int j) {
+    first = 32 * j;
+    count = of(tiles.n[j]);
+    those = __ballot_sync(0xffffffffu, count > lo);
+    if (left < __popc(those)) return true;
     left -= __popc(those);
-  }
-  return false;
+    return false;
+  });
+  // The lane of the bit that `left` others lie below.
+  const bool it = found && count > lo && __popc(those & ((1u << lane) - 1)) == left;
+  const int at = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+  if (at < 0) return false;  // (offsets out of order can make more tiles than an int counts)
+  x.b = first + at;
+  x.tile = back ? __shfl_sync(0xffffffffu, count, at) - 1 - lo : lo;
+  x.off = a.offsets[x.b];
+  x.len = a.offsets[x.b + 1] - x.off;
+  return true;
 }
+__device__ __forceinline__ int all_tiles(int n) { return n; }
 
 // The work item of a persistent CTA's turn n: every other turn the CTAs take theirs in the opposite order, so that
 // the same ones do not always get the larger (in order, 1024 items over 152 CTAs left a CTA 13 % over the mean).

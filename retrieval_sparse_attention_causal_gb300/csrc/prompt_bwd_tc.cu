@@ -78,12 +78,10 @@ struct Shared {
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
-  int keep[PromptTiles<kT>::kKeep];
 };
 
 template <int DH, int G, int E, typename I>
-__device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, PromptItems<I>& items, int readers) {
-  PromptTiles<kT>::fill(a, sh.keep);
+__device__ __forceinline__ void set_up(Shared<DH>& sh, PromptItems<I>& items, int readers) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < Tc<DH>::NK; ++i) {
       tc::mbar_init(&sh.full[i], 1);
@@ -186,7 +184,7 @@ struct QItem {
 __device__ __forceinline__ bool q_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, QItem& it) {
   it.h = w % a.H;
   it.m = it.h / a.g;
-  if (!prompt_tile(a, tiles, w / a.H, false, it.x)) return false;
+  if (!prompt_tile(a, tiles, all_tiles, w / a.H, false, it.x)) return false;
   it.lo = a.window ? max(0, it.x.tile * kT - a.window + 1) / kT : 0;
   return true;
 }
@@ -202,7 +200,9 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
   __shared__ __align__(8) Shared<DH> sh;
   __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, 1, kElemQ>(a, sh, items, kElemQ + 2);
+  PromptTiles<kT> counts;
+  if (warp == kElemQ + 2) counts = PromptTiles<kT>(a);
+  set_up<DH, 1, kElemQ>(sh, items, kElemQ + 2);
   let_next();
   const uint32_t tS = sh.tmem, tP = tS + 128, tQ = tS + 384;  // S, two of dP, dQ
   bool ok = true;
@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
   if (warp == kElemQ + 2) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    const PromptTiles<kT> counts(sh.keep);
     for (; ok; ++nt) {
       it.more = q_item(a, counts, prompt_turn(nt), it);
       ok = put_item(items, nt, it, waited, kSiteItem);
@@ -475,7 +474,7 @@ struct KvItem {
 };
 __device__ __forceinline__ bool kv_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, KvItem& it) {
   it.m = w % a.Hkv;
-  if (!prompt_tile(a, tiles, w / a.Hkv, true, it.x)) return false;
+  if (!prompt_tile(a, tiles, all_tiles, w / a.Hkv, true, it.x)) return false;
   const int k = min(it.x.tile * kT + kT, it.x.len) - 1;  // the tile's last key
   it.end = (a.window ? (int)min((int64_t)it.x.len - 1, (int64_t)k + a.window - 1) : it.x.len - 1) / kT + 1;
   return true;
@@ -493,7 +492,9 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
   __shared__ __align__(8) Shared<DH> sh;
   __shared__ __align__(8) PromptItems<KvItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  set_up<DH, G, kElemKv>(a, sh, items, kElemKv + G);
+  PromptTiles<kT> counts;
+  if (warp == kElemKv + G) counts = PromptTiles<kT>(a);
+  set_up<DH, G, kElemKv>(sh, items, kElemKv + G);
   if (warp != kElemKv + G) after_previous();  // (before any wait with a limit: the queries' side may take long)
   // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
   const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
@@ -508,7 +509,6 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
   if (warp == kElemKv + G) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
-    const PromptTiles<kT> counts(sh.keep);
     for (; ok; ++nt) {
       it.more = kv_item(a, counts, prompt_turn(nt), it);
       ok = put_item(items, nt, it, waited, kSiteItem);

@@ -75,46 +75,45 @@ struct Item {
   __device__ __forceinline__ int units() const { return max(0, hi[0] - lo[0] + 1) + max(0, hi[1] - lo[1] + 1); }
 };
 
-// Of the sequences' tiles of 128 rows: all, those in pairs (COUNT 2), or the last one where it is alone (COUNT 1).
-template <int COUNT>
-struct Counts {
-  PromptTiles<kT> tiles;
-  int mine;
-  static __device__ __forceinline__ int of(int n) { return COUNT == 2 ? n >> 1 : COUNT == 1 ? n & 1 : n; }
-  __device__ __forceinline__ Counts(const int* keep) : tiles(keep), mine(of(tiles.mine)) {}
-  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return of(tiles(a, b)); }
-};
+// Of a sequence's tiles of 128 rows: those in pairs, and the last one where it is alone.
+__device__ __forceinline__ int pairs_of(int n) { return n >> 1; }
+__device__ __forceinline__ int alone_of(int n) { return n & 1; }
+// The last tiles that are alone, of all sequences.
+__device__ __forceinline__ int count_alone(const PromptArgs& a, const PromptTiles<kT>& tiles) {
+  int n = 0;
+  tiles.any(a, [&](int j) {
+    n += alone_of(tiles.n[j]);
+    return false;
+  });
+  return (int)__reduce_add_sync(kAll, n);
+}
 // Work item w.  Two heads that share a key head have the same tile, where their number is even.  Else an item is two
 // neighbouring tiles of a head, and the last tile of a sequence that has none beside it goes with the next head's, each
 // with its own keys: 48 prompts of up to 300 tokens 32 us alone, 29 together, 64 of 100 tokens 29 and 21.  (These
 // come first: there may be long ones among them.)  Where there are CTAs for all of them they stay alone, for a tile by
 // itself is done sooner.
-__device__ __forceinline__ bool item_of(const PromptArgs& a, const int* keep, int w, Item& it) {
+__device__ __forceinline__ bool item_of(const PromptArgs& a, const PromptTiles<kT>& tiles, int alone, int w, Item& it) {
   it.own = 0;
   bool second = true;
   if (a.g % 2 == 0) {
     const int h = 2 * (w % (a.H / 2));
-    if (!prompt_tile(a, Counts<0>(keep), w / (a.H / 2), false, it.x)) return false;
+    if (!prompt_tile(a, tiles, all_tiles, w / (a.H / 2), false, it.x)) return false;
     it.head[0] = h;
     it.head[1] = h + 1;
     it.tile[0] = it.tile[1] = it.x.tile;
   } else {
-    const Counts<1> alone(keep);
-    int n = 0;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) n += b < 32 ? alone.mine : alone(a, b);
-    n = (int)__reduce_add_sync(kAll, n);
-    it.own = (int64_t)n * a.H > gridDim.x;
+    it.own = (int64_t)alone * a.H > gridDim.x;
     const int per = it.own ? (a.H + 1) / 2 : a.H, h = w % per;
-    if (w < n * per) {
-      if (!prompt_tile(a, alone, w / per, false, it.x)) return false;
+    if (w < alone * per) {
+      if (!prompt_tile(a, tiles, alone_of, w / per, false, it.x)) return false;
       it.head[0] = it.own ? 2 * h : h;
       it.head[1] = it.head[0] + 1;
       it.tile[0] = it.tile[1] = (it.x.len - 1) / kT;
       second = it.own && it.head[1] < a.H;
     } else {
       it.own = 0;
-      w -= n * per;
-      if (!prompt_tile(a, Counts<2>(keep), w / a.H, false, it.x)) return false;
+      w -= alone * per;
+      if (!prompt_tile(a, tiles, pairs_of, w / a.H, false, it.x)) return false;
       it.head[0] = it.head[1] = w % a.H;
       it.tile[0] = 2 * it.x.tile;
       it.tile[1] = 2 * it.x.tile + 1;
@@ -143,7 +142,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
   __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_q[2], bar_qfree[2], bar_s[2][NBUF], bar_p[NBUF], bar_done[NBUF],
       bar_o[2], bar_ofree[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_s, keep[PromptTiles<kT>::kKeep];
+  __shared__ int abort_s;
   __shared__ __align__(8) PromptItems<Item> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 320) {
@@ -172,7 +171,8 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     abort_s = 0;
     tc::fence_mbar_init();
   }
-  PromptTiles<kT>::fill(a, keep);
+  PromptTiles<kT> tiles;
+  if (warp == 10) tiles = PromptTiles<kT>(a);
   if (warp == 8) tc::tmem_alloc(&tmem_slot, kCols);
   tc::fence_before();
   __syncthreads();
@@ -193,8 +193,9 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
     int nq[2] = {0, 0};      // tiles of rows so far
+    const int alone = count_alone(a, tiles);
     for (int turn = 0; ok; ++turn) {
-      it.more = item_of(a, keep, prompt_turn(turn), it);
+      it.more = item_of(a, tiles, alone, prompt_turn(turn), it);
       ok = put_item(items, turn, it, waited, kSiteItem);
       if (!ok || !it.more) break;
       auto rows = [&](auto tile) {

@@ -451,6 +451,31 @@ def test_prompt_many_sequences_match_single_ones():
         assert torch.equal(one, o[a:z]) and torch.equal(l1, lse[a:z])
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 128, 129, 1024])
+@pytest.mark.parametrize("H,Hkv,dh,dtype", [(3, 1, 64, "bf16"), (5, 5, 128, "bf16"), (4, 2, 32, "bf16"), (2, 1, 64, "f32")])
+def test_prompt_gradients_of_many_sequences_match_single_ones(B, H, Hkv, dh, dtype):
+    """As many sequences as a warp's lanes hold, one more, and so on up to the most: outputs and gradients of each
+    are those that it has by itself; a few are longer than a tile and some are empty.  (Float32's dk and dv are
+    sums of parts whose number goes by the call's size: they are left to the tests against the oracle.)"""
+    g = _g()
+    lengths = np.random.default_rng(B).integers(0, 60, B)
+    lengths[::9] *= 7
+    off = offsets_of(lengths)
+    N = int(off[-1])
+    q, k, v, do = (torch.randn(N, h, dh, device="cuda").to(TORCH[dtype]) for h in (H, Hkv, Hkv, H))
+
+    def step(q, k, v, do, off):
+        o, lse = g.prompt_attention(q, k, v, off)
+        return (o, lse) + g.prompt_attention_backward(q, k, v, o, do, lse, off)[:3 if dtype == "bf16" else 1]
+    got = step(q, k, v, do, ints(off))
+    for b in sorted({0, 1, 9, 27, 30, 31, 32, 33, 63, 64, 127, 128, B // 2, B - 2, B - 1}):
+        if b >= B or lengths[b] == 0:
+            continue
+        a, z = int(off[b]), int(off[b + 1])
+        for x, y in zip(got, step(q[a:z], k[a:z], v[a:z], do[a:z], ints([0, z - a]))):
+            assert torch.equal(x[a:z], y), (b, z - a)
+
+
 # ------------------------------------------------------------------ norms with rotary positions
 NORM = [  # B, L, H, Hkv, dh, rot, dtype, interleaved, eps
     (1, 1, 1, 1, 2, 2, "f32", False, 1e-6),
