@@ -23,38 +23,44 @@ __device__ __forceinline__ int prompt_length(const PromptArgs& a, int b) {
   return e - s;
 }
 
-// Tiles of T rows of the sequences, for many lookups by a warp: lane l has those of sequences l, l + 32 and so on in
-// registers.  (Read anew from the offsets for each work item, beyond the first 256 sequences, they took time that grew with
-// the square of the sequences: 1024 prompts of 64 tokens, 12 heads, forward 864 us and gradients 2020, now 192 and 672; 256 67
-// and 197, now 56 and 185.)  It is made before the CTA's first barrier, beside what the other warps prepare: a
-// prompt's gradients take 2 us longer otherwise.
+// What every search needs of the counts of tiles (PromptTiles, or what is made of them): made once, by each warp that
+// searches.
+template <typename Tiles>
+__device__ __forceinline__ void prompt_totals(const PromptArgs& a, Tiles& tiles) {
+  const int lane = threadIdx.x & 31;
+  int n = tiles(a, lane), most = n, total = n;
+  tiles.mine = n;
+  for (int b = lane + 32; b < a.B; b += 32) {
+    n = tiles(a, b);
+    most = max(most, n);
+    total += n;
+  }
+  tiles.most = (int)__reduce_max_sync(0xffffffffu, most);
+  tiles.total = (int)__reduce_add_sync(0xffffffffu, total);
+  tiles.lo = tiles.below = tiles.above = 0;
+}
+
+// Tiles of T rows of the sequences, for many lookups: in shared memory, a byte each (kMore: as many or more, to be
+// looked up), and a lane's own of the first 32 in a register.  All threads of the CTA make it, with a barrier between `fill`
+// and the first use.
+// With 256 of them kept, and sums over all sequences made for each work item, the time of many short prompts grew with the
+// square of their number: 1024 of 64 tokens, 12 heads of 64, forward 847 us and gradients 2016, now 230 and 753; 256 67 and
+// 191, now 50 to 53 and 170; 48 of up to 300 27.8 and 72.9, now 26.7 and 70.  (All counts in the lanes' registers, searched
+// in unrolled code: 190 and 668 for the 1024, but one prompt's gradients 14.8 us for 13.8 and windows 2 % slower.)
 template <int T>
 struct PromptTiles {
-  static constexpr int kEach = GCA_MAX_SEQUENCES / 32;
-  int n[kEach];
-  __device__ __forceinline__ PromptTiles() {}  // (of the warps that find no items)
-  __device__ __forceinline__ explicit PromptTiles(const PromptArgs& a) {
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) n[j] = 0;
-    any(a, [&](int j) {
-      const int b = 32 * j + (threadIdx.x & 31);
-      if (b < a.B) n[j] = (prompt_length(a, b) + T - 1) / T;
-      return false;
-    });
+  static constexpr int kKeep = GCA_MAX_SEQUENCES, kMore = 255;
+  const uint8_t* kept;
+  int mine, most, total;  // the lane's of the first 32 sequences; the most of a sequence, of all together
+  int lo, below, above;   // of the last search: the tile's number i, S(i + 1) and S(i)
+  static __device__ __forceinline__ int of(const PromptArgs& a, int b) { return b < a.B ? (prompt_length(a, b) + T - 1) / T : 0; }
+  static __device__ __forceinline__ void fill(const PromptArgs& a, uint8_t* keep) {
+    for (int b = threadIdx.x; b < max(a.B, 32); b += blockDim.x) keep[b] = (uint8_t)min(of(a, b), kMore);
   }
-  // Whether f(j) holds for one of the n's that hold sequences, asked in order up to the first; few sequences ask few.
-  template <typename F>
-  static __device__ __forceinline__ bool any(const PromptArgs& a, const F& f) {
-    if (f(0)) return true;
-    if (a.B <= 32) return false;
-#pragma unroll
-    for (int j = 1; j < 4; ++j)
-      if (f(j)) return true;
-    if (a.B <= 128) return false;
-#pragma unroll
-    for (int j = 4; j < kEach; ++j)
-      if (f(j)) return true;
-    return false;
+  __device__ __forceinline__ PromptTiles(const PromptArgs& a, const uint8_t* keep) : kept(keep) { prompt_totals(a, *this); }
+  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const {
+    const int n = kept[b];
+    return n < kMore ? n : of(a, b);
   }
 };
 
@@ -62,57 +68,54 @@ struct PromptTiles {
 // those that start last are short.  Under the causal mask that is the order of their number in their
 // sequence, from the highest down (`back`: counted from the sequence's end, for the side of the keys),
 // sequences of equal tiles in order.  With S(i) the tiles numbered i or higher, tile `rank` has the number
-// i with S(i + 1) <= rank < S(i).  `of` says how many of a sequence's tiles count.  Called by a whole warp; false
-// behind the last tile.
-template <int T, typename Of>
-__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, const PromptTiles<T>& tiles, const Of& of, int rank, bool back, PromptTile& x) {
+// i with S(i + 1) <= rank < S(i).  Called by a whole warp, with ranks that do not fall, so that most have the number of
+// the last; false behind the last tile.
+template <typename Tiles>
+__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, Tiles& tiles, int rank, bool back, PromptTile& x) {
   const int lane = threadIdx.x & 31;
+  const int mine = tiles.mine;  // the first 32 sequences stay in registers
   auto from = [&](int i) {
-    int n = 0;
-    tiles.any(a, [&](int j) {
-      n += max(of(tiles.n[j]) - i, 0);
-      return false;
-    });
+    int n = max(mine - i, 0);
+    for (int b = lane + 32; b < a.B; b += 32) n += max(tiles(a, b) - i, 0);
     return (int)__reduce_add_sync(0xffffffffu, n);
   };
-  int most = 0;
-  tiles.any(a, [&](int j) {
-    most = max(most, of(tiles.n[j]));
-    return false;
-  });
-  int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, most), below = 0;  // from(lo) > rank >= from(hi) = below
-  if (from(0) <= rank) return false;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1, n = from(mid);
-    if (n > rank) {
-      lo = mid;
-    } else {
-      hi = mid;
-      below = n;
+  if (tiles.total <= rank) return false;
+  if (rank >= tiles.above) {
+    int lo = 0, hi = tiles.most, below = 0, above = tiles.total;  // above = from(lo) > rank >= from(hi) = below
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1, n = from(mid);
+      if (n > rank) {
+        lo = mid;
+        above = n;
+      } else {
+        hi = mid;
+        below = n;
+      }
     }
+    tiles.lo = lo;
+    tiles.below = below;
+    tiles.above = above;
   }
-  int left = rank - below;  // of the sequences with more than `lo` tiles, in order
-  int first = 0, count = 0;
-  uint32_t those = 0;
-  const bool found = tiles.any(a, [&](int j) {
-    first = 32 * j;
-    count = of(tiles.n[j]);
-    those = __ballot_sync(0xffffffffu, count > lo);
-    if (left < __popc(those)) return true;
+  const int lo = tiles.lo;
+  int left = rank - tiles.below;  // of the sequences with more than `lo` tiles, in order
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int n = b0 ? (b0 + lane < a.B ? tiles(a, b0 + lane) : 0) : mine;
+    const uint32_t those = __ballot_sync(0xffffffffu, n > lo);
+    if (left < __popc(those)) {
+      // The lane of the bit that `left` others lie below.
+      const bool it = n > lo && __popc(those & ((1u << lane) - 1)) == left;
+      const int at = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+      if (at < 0) return false;  // (offsets out of order can make more tiles than an int counts)
+      x.b = b0 + at;
+      x.tile = back ? __shfl_sync(0xffffffffu, n, at) - 1 - lo : lo;
+      x.off = a.offsets[x.b];
+      x.len = a.offsets[x.b + 1] - x.off;
+      return true;
+    }
     left -= __popc(those);
-    return false;
-  });
-  // The lane of the bit that `left` others lie below.
-  const bool it = found && count > lo && __popc(those & ((1u << lane) - 1)) == left;
-  const int at = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
-  if (at < 0) return false;  // (offsets out of order can make more tiles than an int counts)
-  x.b = first + at;
-  x.tile = back ? __shfl_sync(0xffffffffu, count, at) - 1 - lo : lo;
-  x.off = a.offsets[x.b];
-  x.len = a.offsets[x.b + 1] - x.off;
-  return true;
+  }
+  return false;
 }
-__device__ __forceinline__ int all_tiles(int n) { return n; }
 
 // The work item of a persistent CTA's turn n: every other turn the CTAs take theirs in the opposite order, so that
 // the same ones do not always get the larger (in order, 1024 items over 152 CTAs left a CTA 13 % over the mean).

@@ -140,8 +140,12 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // The tile of this CTA and its head; false: there is none.
 __device__ __forceinline__ bool my_tile(const PromptArgs& a, int heads, bool back, PromptTile& x, int& h) {
+  __shared__ uint8_t keep[PromptTiles<kT>::kKeep];
+  PromptTiles<kT>::fill(a, keep);
+  __syncthreads();
   h = blockIdx.x % heads;
-  return prompt_tile(a, PromptTiles<kT>(a), all_tiles, blockIdx.x / heads, back, x);
+  PromptTiles<kT> tiles(a, keep);
+  return prompt_tile(a, tiles, blockIdx.x / heads, back, x);
 }
 __device__ __forceinline__ bool sees(const PromptArgs& a, int t, int k) { return k <= t && (a.window == 0 || k > t - a.window); }
 // The first tile of keys that rows t .. see, and behind the last tile of rows that see keys .. k.

@@ -23,8 +23,8 @@
 // Measured, bf16, in a graph, with the rows' sums of prompt_attn.cu: four documents of 46 thousand tokens in all, 12
 // heads of 64, 2.59 ms (866 TFLOP/s of five products; queries' side 1.09, keys' side 1.51, rows 0.04); one prompt of
 // 32768 tokens, 16 heads of 128 and 4 key heads, 9.7 ms (1.13 PFLOP/s); 54 thousand tokens, 16 and 4 heads of 64, in
-// a window of 512 0.62 ms; one prompt of 77 tokens 14 us, where each of the two starts while what is ahead of it
-// ends (17 without).
+// a window of 512 0.62 ms; 1024 prompts of 64 tokens, 12 heads of 64, 0.75; one prompt of 77 tokens 14 us, where each of
+// the two starts while what is ahead of it ends (17 without).
 #include <algorithm>
 #include <type_traits>
 
@@ -78,10 +78,12 @@ struct Shared {
   uint64_t acc, acc_free;                        // the tile's gradients: complete, read
   uint32_t tmem;
   int abort;
+  uint8_t keep[PromptTiles<kT>::kKeep];
 };
 
 template <int DH, int G, int E, typename I>
-__device__ __forceinline__ void set_up(Shared<DH>& sh, PromptItems<I>& items, int readers) {
+__device__ __forceinline__ void set_up(const PromptArgs& a, Shared<DH>& sh, PromptItems<I>& items, int readers) {
+  PromptTiles<kT>::fill(a, sh.keep);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Tc<DH>::NK; ++i) {
       tc::mbar_init(&sh.full[i], 1);
@@ -181,10 +183,10 @@ struct QItem {
   PromptTile x;
   int h, m, lo, more;  // more: 0 behind the last
 };
-__device__ __forceinline__ bool q_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, QItem& it) {
+__device__ __forceinline__ bool q_item(const PromptArgs& a, PromptTiles<kT>& tiles, int w, QItem& it) {
   it.h = w % a.H;
   it.m = it.h / a.g;
-  if (!prompt_tile(a, tiles, all_tiles, w / a.H, false, it.x)) return false;
+  if (!prompt_tile(a, tiles, w / a.H, false, it.x)) return false;
   it.lo = a.window ? max(0, it.x.tile * kT - a.window + 1) / kT : 0;
   return true;
 }
@@ -200,9 +202,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
   __shared__ __align__(8) Shared<DH> sh;
   __shared__ __align__(8) PromptItems<QItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  PromptTiles<kT> counts;
-  if (warp == kElemQ + 2) counts = PromptTiles<kT>(a);
-  set_up<DH, 1, kElemQ>(sh, items, kElemQ + 2);
+  set_up<DH, 1, kElemQ>(a, sh, items, kElemQ + 2);
   let_next();
   const uint32_t tS = sh.tmem, tP = tS + 128, tQ = tS + 384;  // S, two of dP, dQ
   bool ok = true;
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(threads_of(kElemQ, 2), 1) prompt_dq_tc_kernel(
   if (warp == kElemQ + 2) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
+    PromptTiles<kT> counts(a, sh.keep);
     for (; ok; ++nt) {
       it.more = q_item(a, counts, prompt_turn(nt), it);
       ok = put_item(items, nt, it, waited, kSiteItem);
@@ -472,9 +473,9 @@ struct KvItem {
   PromptTile x;
   int m, end, more;
 };
-__device__ __forceinline__ bool kv_item(const PromptArgs& a, const PromptTiles<kT>& tiles, int w, KvItem& it) {
+__device__ __forceinline__ bool kv_item(const PromptArgs& a, PromptTiles<kT>& tiles, int w, KvItem& it) {
   it.m = w % a.Hkv;
-  if (!prompt_tile(a, tiles, all_tiles, w / a.Hkv, true, it.x)) return false;
+  if (!prompt_tile(a, tiles, w / a.Hkv, true, it.x)) return false;
   const int k = min(it.x.tile * kT + kT, it.x.len) - 1;  // the tile's last key
   it.end = (a.window ? (int)min((int64_t)it.x.len - 1, (int64_t)k + a.window - 1) : it.x.len - 1) / kT + 1;
   return true;
@@ -492,9 +493,7 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
   __shared__ __align__(8) Shared<DH> sh;
   __shared__ __align__(8) PromptItems<KvItem> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  PromptTiles<kT> counts;
-  if (warp == kElemKv + G) counts = PromptTiles<kT>(a);
-  set_up<DH, G, kElemKv>(sh, items, kElemKv + G);
+  set_up<DH, G, kElemKv>(a, sh, items, kElemKv + G);
   if (warp != kElemKv + G) after_previous();  // (before any wait with a limit: the queries' side may take long)
   // P^T and dS^T lie in the columns that S^T and dP^T came in; behind those dV and dK, of each group its own.
   const uint32_t tS = sh.tmem, tP = tS + 128, tV = tS + 256, tK = tV + DH;
@@ -509,6 +508,7 @@ __global__ void __launch_bounds__(threads_of(kElemKv, Tc<DH>::G), 1) prompt_dkv_
   if (warp == kElemKv + G) {
     // ---------------------------------------------------------------- loads
     int id = 0, nt = 0;
+    PromptTiles<kT> counts(a, sh.keep);
     for (; ok; ++nt) {
       it.more = kv_item(a, counts, prompt_turn(nt), it);
       ok = put_item(items, nt, it, waited, kSiteItem);

@@ -23,9 +23,10 @@
 // memory, for a weight of 0 times what lies in them must stay 0.  dh 32 is read as 64 with zeros behind
 // it (the tensor map fills them in).
 // Measured, bf16, in a graph: one prompt of 32768 tokens, 16 heads of 128 and 4 key heads, 2.5 ms (1.75 PFLOP/s, the
-// tensor pipe), with dh 64 1.61 ms (1.37; exponentials and issue); four documents of 46 thousand tokens in all,
-// 12 heads of 64, 0.70 ms (1.27); 54 thousand tokens, 16 and 4 heads, in a window of 512 181 us; 48 prompts of up
-// to 300 tokens 29 us, three or four work items a CTA of some 5 thousand cycles each: load, masked block, store.
+// tensor pipe), with dh 64 1.61 ms (1.37; exponentials and products each busy for 0.57 of it, the rest waits); four documents
+// of 46 thousand tokens in all, 12 heads of 64, 0.70 ms (1.27), of 32, which take as long, 0.70; 54 thousand tokens, 16 and 4
+// heads, in a window of 512 176 us; 48 prompts of up to 300 tokens 26.7 us, three or four work items a CTA of some 5 thousand
+// cycles each: load, masked block, store; 1024 prompts of 64 tokens, 12 heads, 230 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -75,45 +76,42 @@ struct Item {
   __device__ __forceinline__ int units() const { return max(0, hi[0] - lo[0] + 1) + max(0, hi[1] - lo[1] + 1); }
 };
 
-// Of a sequence's tiles of 128 rows: those in pairs, and the last one where it is alone.
-__device__ __forceinline__ int pairs_of(int n) { return n >> 1; }
-__device__ __forceinline__ int alone_of(int n) { return n & 1; }
-// The last tiles that are alone, of all sequences.
-__device__ __forceinline__ int count_alone(const PromptArgs& a, const PromptTiles<kT>& tiles) {
-  int n = 0;
-  tiles.any(a, [&](int j) {
-    n += alone_of(tiles.n[j]);
-    return false;
-  });
-  return (int)__reduce_add_sync(kAll, n);
-}
+// Of the sequences' tiles of 128 rows: all, those in pairs (COUNT 2), or the last one where it is alone (COUNT 1).
+template <int COUNT>
+struct Counts {
+  const PromptTiles<kT>& tiles;
+  int mine, most, total, lo, below, above;
+  static __device__ __forceinline__ int of(int n) { return COUNT == 2 ? n >> 1 : COUNT == 1 ? n & 1 : n; }
+  __device__ __forceinline__ Counts(const PromptArgs& a, const PromptTiles<kT>& all) : tiles(all) { prompt_totals(a, *this); }
+  __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return of(tiles(a, b)); }
+};
 // Work item w.  Two heads that share a key head have the same tile, where their number is even.  Else an item is two
 // neighbouring tiles of a head, and the last tile of a sequence that has none beside it goes with the next head's, each
 // with its own keys: 48 prompts of up to 300 tokens 32 us alone, 29 together, 64 of 100 tokens 29 and 21.  (These
 // come first: there may be long ones among them.)  Where there are CTAs for all of them they stay alone, for a tile by
 // itself is done sooner.
-__device__ __forceinline__ bool item_of(const PromptArgs& a, const PromptTiles<kT>& tiles, int alone, int w, Item& it) {
+__device__ __forceinline__ bool item_of(const PromptArgs& a, PromptTiles<kT>& tiles, Counts<1>& alone, Counts<2>& pairs, int w, Item& it) {
   it.own = 0;
   bool second = true;
   if (a.g % 2 == 0) {
     const int h = 2 * (w % (a.H / 2));
-    if (!prompt_tile(a, tiles, all_tiles, w / (a.H / 2), false, it.x)) return false;
+    if (!prompt_tile(a, tiles, w / (a.H / 2), false, it.x)) return false;
     it.head[0] = h;
     it.head[1] = h + 1;
     it.tile[0] = it.tile[1] = it.x.tile;
   } else {
-    it.own = (int64_t)alone * a.H > gridDim.x;
+    it.own = (int64_t)alone.total * a.H > gridDim.x;
     const int per = it.own ? (a.H + 1) / 2 : a.H, h = w % per;
-    if (w < alone * per) {
-      if (!prompt_tile(a, tiles, alone_of, w / per, false, it.x)) return false;
+    if (w < alone.total * per) {
+      if (!prompt_tile(a, alone, w / per, false, it.x)) return false;
       it.head[0] = it.own ? 2 * h : h;
       it.head[1] = it.head[0] + 1;
       it.tile[0] = it.tile[1] = (it.x.len - 1) / kT;
       second = it.own && it.head[1] < a.H;
     } else {
       it.own = 0;
-      w -= alone * per;
-      if (!prompt_tile(a, tiles, pairs_of, w / a.H, false, it.x)) return false;
+      w -= alone.total * per;
+      if (!prompt_tile(a, pairs, w / a.H, false, it.x)) return false;
       it.head[0] = it.head[1] = w % a.H;
       it.tile[0] = 2 * it.x.tile;
       it.tile[1] = 2 * it.x.tile + 1;
@@ -143,6 +141,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
       bar_o[2], bar_ofree[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
+  __shared__ uint8_t keep[PromptTiles<kT>::kKeep];
   __shared__ __align__(8) PromptItems<Item> items;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 320) {
@@ -171,8 +170,7 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     abort_s = 0;
     tc::fence_mbar_init();
   }
-  PromptTiles<kT> tiles;
-  if (warp == 10) tiles = PromptTiles<kT>(a);
+  PromptTiles<kT>::fill(a, keep);
   if (warp == 8) tc::tmem_alloc(&tmem_slot, kCols);
   tc::fence_before();
   __syncthreads();
@@ -193,9 +191,11 @@ prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmQ, const __
     int id = 0, st = 0;      // slots so far, the next
     uint32_t parity = 0;     // of its filling
     int nq[2] = {0, 0};      // tiles of rows so far
-    const int alone = count_alone(a, tiles);
+    PromptTiles<kT> counts(a, keep);
+    Counts<1> alone(a, counts);
+    Counts<2> pairs(a, counts);
     for (int turn = 0; ok; ++turn) {
-      it.more = item_of(a, tiles, alone, prompt_turn(turn), it);
+      it.more = item_of(a, counts, alone, pairs, prompt_turn(turn), it);
       ok = put_item(items, turn, it, waited, kSiteItem);
       if (!ok || !it.more) break;
       auto rows = [&](auto tile) {

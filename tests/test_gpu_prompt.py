@@ -454,7 +454,7 @@ def test_prompt_many_sequences_match_single_ones():
 @pytest.mark.parametrize("B", [31, 32, 33, 128, 129, 1024])
 @pytest.mark.parametrize("H,Hkv,dh,dtype", [(3, 1, 64, "bf16"), (5, 5, 128, "bf16"), (4, 2, 32, "bf16"), (2, 1, 64, "f32")])
 def test_prompt_gradients_of_many_sequences_match_single_ones(B, H, Hkv, dh, dtype):
-    """As many sequences as a warp's lanes hold, one more, and so on up to the most: outputs and gradients of each
+    """As many sequences as a warp has lanes, one more, and so on up to the most: outputs and gradients of each
     are those that it has by itself; a few are longer than a tile and some are empty.  (Float32's dk and dv are
     sums of parts whose number goes by the call's size: they are left to the tests against the oracle.)"""
     g = _g()
@@ -474,6 +474,25 @@ def test_prompt_gradients_of_many_sequences_match_single_ones(B, H, Hkv, dh, dty
         a, z = int(off[b]), int(off[b + 1])
         for x, y in zip(got, step(q[a:z], k[a:z], v[a:z], do[a:z], ints([0, z - a]))):
             assert torch.equal(x[a:z], y), (b, z - a)
+
+
+@pytest.mark.parametrize("H,Hkv,dtype,long", [(2, 2, "bf16", 33000), (2, 1, "bf16", 32640), (1, 1, "f32", 16400)])
+def test_prompt_long_sequences_among_many(H, Hkv, dtype, long):
+    """Sequences of 255 tiles and more behind the first 32, which a byte does not count, are what they are alone."""
+    g = _g()
+    lengths = np.full(70, 5)
+    lengths[[34, 69]] = long, long - 200
+    off = offsets_of(lengths)
+    q, k, v, do = (torch.randn(int(off[-1]), h, 64, device="cuda").to(TORCH[dtype]) for h in (H, Hkv, Hkv, H))
+
+    def step(q, k, v, do, off):
+        o, lse = g.prompt_attention(q, k, v, off)
+        return (o, lse) + g.prompt_attention_backward(q, k, v, o, do, lse, off)[:3 if dtype == "bf16" else 1]
+    got = step(q, k, v, do, ints(off))
+    for b in (0, 33, 34, 35, 68, 69):
+        a, z = int(off[b]), int(off[b + 1])
+        for x, y in zip(got, step(q[a:z], k[a:z], v[a:z], do[a:z], ints([0, z - a]))):
+            assert torch.equal(x[a:z], y), b
 
 
 # ------------------------------------------------------------------ norms with rotary positions
