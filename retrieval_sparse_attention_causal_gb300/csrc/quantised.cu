@@ -11,7 +11,7 @@
 // The pages, their table and counts are those of cache.cu, whose operations move rows as bytes.
 // Bound by memory: each row is read and written once.  Measured, 12 heads of 64 in bf16: eight prompts of 67
 // thousand tokens in all, 59 us with the plan of their pages (5.2 TB/s); 80 tokens of 32 sequences 6.4; 16 x 8 chunks
-// read 9.2, 16 x 128 chunks 103 (5.9 TB/s).
+// read 9.2, 16 x 128 chunks 103 (5.9 TB/s).  In float32: 79 thousand tokens 102 us (5.9 TB/s), chunks 16.4 and 206 (4.9).
 #include <algorithm>
 
 #include "common.cuh"

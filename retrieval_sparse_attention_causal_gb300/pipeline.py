@@ -150,8 +150,8 @@ def prompt_forward(q, k, v, offsets, q_weight, k_weight, freq, positions, window
 
 def prompt_step(q, k, v, dout, offsets, q_weight, k_weight, freq, positions, window=0, interleaved=False, gain=1.0, eps=1e-6):
     """prompt_forward and its gradients (a training step's).  Returns o, lse, dq, dk, dv of q, k, v and the
-    norms' dq_weight, dk_weight (float32).  Rows of no sequence must hold finite numbers; their gradients are 0,
-    their o and lse are not written."""
+    norms' dq_weight, dk_weight (float32).  Rows of no sequence must hold finite numbers (with
+    eps 0 not zeros alone); their gradients are 0, their o and lse are not written."""
     r = prompt_forward(q, k, v, offsets, q_weight, k_weight, freq, positions, window, interleaved, gain, eps)
     # The norms' weights sum over all rows, those of no sequence too.
     dq, dk, dv = (torch.zeros(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
