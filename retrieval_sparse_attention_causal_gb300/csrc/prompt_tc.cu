@@ -76,12 +76,12 @@ struct Item {
   __device__ __forceinline__ int units() const { return max(0, hi[0] - lo[0] + 1) + max(0, hi[1] - lo[1] + 1); }
 };
 
-// Of the sequences' tiles of 128 rows: all, those in pairs (COUNT 2), or the last one where it is alone (COUNT 1).
+// Of the sequences' tiles of 128 rows those in pairs (COUNT 2), or the last one where it is alone (COUNT 1).
 template <int COUNT>
 struct Counts {
   const PromptTiles<kT>& tiles;
   int mine, most, total, lo, below, above;
-  static __device__ __forceinline__ int of(int n) { return COUNT == 2 ? n >> 1 : COUNT == 1 ? n & 1 : n; }
+  static __device__ __forceinline__ int of(int n) { return COUNT == 2 ? n >> 1 : n & 1; }
   __device__ __forceinline__ Counts(const PromptArgs& a, const PromptTiles<kT>& all) : tiles(all) { prompt_totals(a, *this); }
   __device__ __forceinline__ int operator()(const PromptArgs& a, int b) const { return of(tiles(a, b)); }
 };
